@@ -3,19 +3,14 @@
 // synchronizes; every device call is enqueued on the caller's stream.
 #include <cstdint>
 
+#include "api_util.h"
 #include "common.h"
 #include "kernels.h"
 #include "qlora.h"
 
 using namespace qlora;
 
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-qlora_status hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP; }
-
-qlora_status check_weight(const qlora_nf4_weight* w) {
+qlora_status qlora::check_weight(const qlora_nf4_weight* w) {
   if (w == nullptr) return QLORA_ERR_INVALID_ARG;
   if (w->n < 1 || w->k < 1 || (w->k % QLORA_BLOCK) != 0) return QLORA_ERR_SHAPE;
   // code8 NULL: no double quantization (s2 holds one fp32 scale per block,
@@ -27,23 +22,11 @@ qlora_status check_weight(const qlora_nf4_weight* w) {
   return QLORA_OK;
 }
 
-Nf4View view_of(const qlora_nf4_weight* w) {
+Nf4View qlora::view_of(const qlora_nf4_weight* w) {
   return Nf4View{w->n, w->k, w->codes, w->code8, w->s2, w->mean, w->codebook, w->scale_bf16 == 1};
 }
 
-// Bump allocator over the caller's workspace (256-byte aligned regions).
-struct Carver {
-  char* base;
-  size_t used = 0;
-  explicit Carver(void* p) : base(static_cast<char*>(p)) {}
-  template <typename T>
-  T* take(size_t bytes) {
-    if (bytes == 0) return nullptr;
-    T* p = reinterpret_cast<T*>(base ? base + used : nullptr);
-    used += align256(bytes);
-    return p;
-  }
-};
+namespace {
 
 bool small_m(int64_t M) { return M <= 16; }
 
@@ -147,20 +130,18 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, bool have_tsaved, Carver& 
   return cv.used;
 }
 
-// Zeros for the adapter gradients of an empty batch (a kernel, not a memset,
-// so the call stays capturable in a graph).
 __global__ __launch_bounds__(256) void zero_f32_kernel(float* __restrict__ p, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i < n) p[i] = 0.0f;
 }
 
-hipError_t zero_f32(float* p, int64_t n, hipStream_t st) {
+}  // namespace
+
+hipError_t qlora::zero_f32(float* p, int64_t n, hipStream_t st) {
   if (n <= 0) return hipSuccess;
   zero_f32_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(p, n);
   return hipGetLastError();
 }
-
-}  // namespace
 
 extern "C" {
 

@@ -1,0 +1,224 @@
+// Host side of the 8-bit layer's C ABI: argument checks, workspace carving
+// and composition of its kernels.
+#include <cmath>
+
+#include "api_util.h"
+#include "fp8.h"
+#include "kernels.h"
+#include "qlora.h"
+
+using namespace qlora;
+
+namespace {
+
+qlora_status check_fp8(const qlora_fp8_weight* w) {
+  if (w == nullptr) return QLORA_ERR_INVALID_ARG;
+  if (w->n < 1 || w->k < 1 || w->k % QLORA_BLOCK != 0 || w->n > kMaxDim || w->k > kMaxDim) return QLORA_ERR_SHAPE;
+  if (!good(w->codes) || !good(w->scale)) return QLORA_ERR_INVALID_ARG;
+  return QLORA_OK;
+}
+
+Fp8View view8(const qlora_fp8_weight* w) { return Fp8View{w->n, w->k, w->codes, w->scale}; }
+
+bool dims_ok(int64_t M, int64_t n, int64_t k, int r) {
+  return M >= 0 && M <= kMaxDim && n >= 1 && n <= kMaxDim && k >= QLORA_BLOCK && k <= kMaxDim && k % QLORA_BLOCK == 0 &&
+         r >= 0 && r <= QLORA_MAX_RANK;
+}
+
+bool fwd_fits(int64_t M, int64_t n, int64_t k, int r) {
+  return M <= 16 ? 32 * f8_pad(k) < ((int64_t)1 << 31) : gemm_fp8_offsets_fit(M, k, lora_extra_cols(r), n);
+}
+
+struct FwdWs {
+  void* gv = nullptr;      // M <= 16: activations in the GEMV's operand order
+  float* T = nullptr;      // M <= 16 without T_save
+  uint8_t* xq = nullptr;   // M > 16: activation codes and scale words
+  uint8_t* xs = nullptr;
+  uint16_t* TS = nullptr;  // low-rank operand columns
+  uint16_t* Bx = nullptr;
+  void* proj = nullptr;
+  float* part = nullptr;
+};
+
+size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
+  if (r > 0) o.proj = cv.take<char>(rowdot_ws_bytes(M, k, r));
+  if (M <= 16) {
+    if (r > 0) o.T = cv.take<float>((size_t)M * r * 4);
+    o.gv = cv.take<char>(fp8_gemv_ws_bytes(k));
+    return cv.used;
+  }
+  o.xq = cv.take<uint8_t>((size_t)M * f8_pad(k));
+  o.xs = cv.take<uint8_t>(fp8_rows_scale_bytes(M, k));
+  if (r > 0) {
+    o.TS = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
+    o.Bx = cv.take<uint16_t>((size_t)n * lora_extra_cols(r) * 2);
+  }
+  o.part = cv.take<float>(gemm_fp8_ws_bytes(M, k, n));
+  return cv.used;
+}
+
+struct BwdWs {
+  uint8_t* yq = nullptr;   // dY's codes and scale words
+  uint8_t* ys = nullptr;
+  uint8_t* wt = nullptr;   // the weight's codes as [k, n]
+  uint16_t* US = nullptr;
+  uint16_t* Ax = nullptr;
+  float* U = nullptr;
+  float* T = nullptr;
+  void* proj = nullptr;
+  void* grad = nullptr;
+  float* part = nullptr;
+};
+
+size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
+  o.yq = cv.take<uint8_t>((size_t)M * f8_pad(n));
+  o.ys = cv.take<uint8_t>(fp8_rows_scale_bytes(M, n));
+  o.wt = cv.take<uint8_t>((size_t)k * f8_pad(n));
+  if (r > 0) {
+    o.US = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
+    o.Ax = cv.take<uint16_t>((size_t)k * lora_extra_cols(r) * 2);
+    o.U = cv.take<float>((size_t)M * r * 4);
+    o.T = cv.take<float>((size_t)M * r * 4);
+    const size_t p1 = rowdot_ws_bytes(M, n, r), p2 = rowdot_ws_bytes(M, k, r);
+    o.proj = cv.take<char>(p1 > p2 ? p1 : p2);
+    const size_t g1 = coldot_ws_bytes(M, k, r), g2 = coldot_ws_bytes(M, n, r);
+    o.grad = cv.take<char>(g1 > g2 ? g1 : g2);
+  }
+  o.part = cv.take<float>(gemm_fp8_ws_bytes(M, n, k));
+  return cv.used;
+}
+
+bool is16(int dtype) { return dtype == QLORA_DT_BF16 || dtype == QLORA_DT_FP16; }
+
+}  // namespace
+
+extern "C" {
+
+size_t qlora_fp8_storage_bytes(int64_t n, int64_t k) {
+  if (n < 1 || k < 1 || k % QLORA_BLOCK) return 0;
+  return (size_t)(n * f8_pad(k) + (f8_pad(n) / kF8Block) * (f8_pad(k) / kF8Block));
+}
+
+qlora_status qlora_quantize_fp8(const void* W, int w_dtype, const qlora_fp8_weight* out, void* stream) {
+  const qlora_status s = check_fp8(out);
+  if (s != QLORA_OK) return s;
+  if (w_dtype != QLORA_DT_FP32 && !is16(w_dtype)) return QLORA_ERR_INVALID_ARG;
+  if (!good(W)) return QLORA_ERR_INVALID_ARG;
+  return hip_status(
+      launch_fp8_encode(W, w_dtype, out->n, out->k, out->codes, out->scale, static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_dequant_fp8(const qlora_fp8_weight* w, void* out, void* stream) {
+  const qlora_status s = check_fp8(w);
+  if (s != QLORA_OK) return s;
+  if (!good(out)) return QLORA_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_decode(view8(w), static_cast<uint16_t*>(out), static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_fp8_linear_workspace_bytes(int64_t M, int64_t n, int64_t k, int r, int is_bwd) {
+  if (M < 1 || !dims_ok(M, n, k, r) || (is_bwd != 0 && is_bwd != 1)) return 0;
+  Carver cv(nullptr);
+  if (is_bwd) {
+    BwdWs o;
+    return bwd_ws(M, n, k, r, cv, o);
+  }
+  FwdWs o;
+  return fwd_ws(M, n, k, r, cv, o);
+}
+
+qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int64_t M, int dtype, const void* A,
+                                  const void* B, int r, float scale, void* Y, float* T_save, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  const qlora_status s = check_fp8(w);
+  if (s != QLORA_OK) return s;
+  const int64_t n = w->n, k = w->k;
+  if (!is16(dtype)) return QLORA_ERR_INVALID_ARG;
+  if (!dims_ok(M, n, k, r) || !fwd_fits(M, n, k, r)) return QLORA_ERR_SHAPE;
+  if (M == 0) return QLORA_OK;
+  if (!good(X) || !good(Y) || (r > 0 && (!good(A) || !good(B))) || (T_save && !aligned16(T_save)))
+    return QLORA_ERR_INVALID_ARG;
+  if (!good(ws) || ws_bytes < qlora_fp8_linear_workspace_bytes(M, n, k, r, 0)) return QLORA_ERR_WORKSPACE;
+  Carver cv(ws);
+  FwdWs o;
+  fwd_ws(M, n, k, r, cv, o);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool f16 = dtype == QLORA_DT_FP16;
+  const uint16_t *x = static_cast<const uint16_t*>(X), *a = static_cast<const uint16_t*>(A),
+                 *b = static_cast<const uint16_t*>(B);
+  float* const proj = static_cast<float*>(o.proj);
+  hipError_t e = hipSuccess;
+  if (M <= 16) {
+    float* const T = T_save ? T_save : o.T;
+    if (r > 0) e = launch_rowdot(x, M, k, a, 0, r, T, nullptr, scale, proj, st, nullptr, f16);
+    if (e == hipSuccess)
+      e = launch_fp8_gemv(view8(w), x, M, T, b, r, scale, static_cast<uint16_t*>(Y), o.gv, st, f16);
+    return hip_status(e);
+  }
+  const int64_t nb = f8_pad(k) / kF8Block;
+  if (r > 0) {
+    e = launch_rowdot(x, M, k, a, 0, r, T_save, o.TS, scale, proj, st, nullptr, f16);
+    if (e == hipSuccess) e = launch_lowrank_rows(b, n, r, o.Bx, st);
+  }
+  if (e == hipSuccess) e = launch_fp8_rows(x, M, k, o.xq, o.xs, st, f16);
+  if (e == hipSuccess)
+    e = launch_gemm_fp8(o.xq, o.xs, M, k, o.TS, lora_extra_cols(r), w->codes, w->scale, nb, 1,
+                        (f8_pad(n) / kF8Block) * nb, o.Bx, n, static_cast<uint16_t*>(Y), o.part, st, f16);
+  return hip_status(e);
+}
+
+qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, const float* T_saved, const void* dY,
+                                  int64_t M, int dtype, const void* A, const void* B, int r, float scale, void* dX,
+                                  float* dA, float* dB, int accumulate, void* ws, size_t ws_bytes, void* stream) {
+  const qlora_status s = check_fp8(w);
+  if (s != QLORA_OK) return s;
+  const int64_t n = w->n, k = w->k;
+  if (!is16(dtype) || (accumulate != 0 && accumulate != 1)) return QLORA_ERR_INVALID_ARG;
+  if (!dims_ok(M, n, k, r) || (M > 0 && dX && !gemm_fp8_offsets_fit(M, n, lora_extra_cols(r), k)))
+    return QLORA_ERR_SHAPE;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (r == 0) {
+    dA = nullptr;
+    dB = nullptr;
+  }
+  if ((dX && !aligned16(dX)) || (dA && !aligned16(dA)) || (dB && !aligned16(dB))) return QLORA_ERR_INVALID_ARG;
+  hipError_t e = hipSuccess;
+  if (M == 0) {
+    if (accumulate) return QLORA_OK;
+    if (dA) e = zero_f32(dA, (int64_t)r * k, st);
+    if (e == hipSuccess && dB) e = zero_f32(dB, n * (int64_t)r, st);
+    return hip_status(e);
+  }
+  const bool need_x = dA != nullptr || (dB != nullptr && T_saved == nullptr);
+  if (!good(dY) || (need_x && !good(X)) || (r > 0 && (!good(A) || !good(B))) || (T_saved && !aligned16(T_saved)))
+    return QLORA_ERR_INVALID_ARG;
+  if (!good(ws) || ws_bytes < qlora_fp8_linear_workspace_bytes(M, n, k, r, 1)) return QLORA_ERR_WORKSPACE;
+  Carver cv(ws);
+  BwdWs o;
+  bwd_ws(M, n, k, r, cv, o);
+  const bool f16 = dtype == QLORA_DT_FP16;
+  const uint16_t *x = static_cast<const uint16_t*>(X), *dy = static_cast<const uint16_t*>(dY),
+                 *a = static_cast<const uint16_t*>(A), *b = static_cast<const uint16_t*>(B);
+  float *const proj = static_cast<float*>(o.proj), *const grad = static_cast<float*>(o.grad);
+  if (r > 0 && (dX || dA)) e = launch_rowdot(dy, M, n, b, 1, r, o.U, dX ? o.US : nullptr, scale, proj, st, nullptr, f16);
+  if (dX) {
+    if (e == hipSuccess && r > 0) e = launch_lowrank_rows_t(a, r, k, o.Ax, st);
+    if (e == hipSuccess) e = launch_fp8_rows(dy, M, n, o.yq, o.ys, st, f16);
+    if (e == hipSuccess) e = launch_fp8_transpose(view8(w), o.wt, st);
+    const int64_t kb = f8_pad(k) / kF8Block;
+    if (e == hipSuccess)
+      e = launch_gemm_fp8(o.yq, o.ys, M, n, o.US, lora_extra_cols(r), o.wt, w->scale, 1, kb, (f8_pad(n) / kF8Block) * kb,
+                          o.Ax, k, static_cast<uint16_t*>(dX), o.part, st, f16);
+  }
+  if (e == hipSuccess && dA) e = launch_coldot(x, M, k, o.U, r, scale, dA, 1, k, accumulate, grad, st, nullptr, f16);
+  if (e == hipSuccess && dB) {
+    const float* T = T_saved;
+    if (T == nullptr) {
+      e = launch_rowdot(x, M, k, a, 0, r, o.T, nullptr, scale, proj, st, nullptr, f16);
+      T = o.T;
+    }
+    if (e == hipSuccess) e = launch_coldot(dy, M, n, T, r, scale, dB, r, 1, accumulate, grad, st, nullptr, f16);
+  }
+  return hip_status(e);
+}
+
+}  // extern "C"

@@ -206,7 +206,33 @@ __global__ __launch_bounds__(256) void lowrank_cols_kernel(const uint16_t* __res
   out[q] = v;
 }
 
+// [k, xc] rows of A^T: row c = [A[0..r-1, c] | the same | 0]. One thread per
+// (row, 8 columns): neighbouring threads take neighbouring c, so each A row
+// is read in runs.
+__global__ __launch_bounds__(256) void lowrank_rows_t_kernel(const uint16_t* __restrict__ A, int r, int xc, int64_t k,
+                                                             u32x4* __restrict__ out) {
+  const int cpr = xc / 8;
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int j0 = (int)blockIdx.y * 8;
+  if (c >= k) return;
+  uint32_t h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int j = j0 + e;
+    h[e] = j < 2 * r ? (uint32_t)A[(int64_t)(j % r) * k + c] : 0u;
+  }
+  out[c * cpr + blockIdx.y] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+}
+
 }  // namespace
+
+hipError_t launch_lowrank_rows_t(const uint16_t* A, int r, int64_t k, uint16_t* out, hipStream_t stream) {
+  const int xc = lora_extra_cols(r);
+  if (xc == 0 || k == 0) return hipSuccess;
+  lowrank_rows_t_kernel<<<dim3((unsigned)cdiv(k, (int64_t)256), (unsigned)(xc / 8)), 256, 0, stream>>>(
+      A, r, xc, k, reinterpret_cast<u32x4*>(out));
+  return hipGetLastError();
+}
 
 hipError_t launch_lowrank_cols(const uint16_t* A, int r, int64_t k, uint16_t* out, hipStream_t stream) {
   const int xc = lora_extra_cols(r);

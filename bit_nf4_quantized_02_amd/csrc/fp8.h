@@ -1,0 +1,49 @@
+// The 8-bit layer's storage and operand layouts (internal; include/qlora.h
+// states the public ones).
+//
+// Values are OCP E4M3 with a power-of-two scale 2^(b - 127) held as the
+// exponent byte b, one per 128 consecutive contraction elements: of one row
+// for activations, of 128 rows together for weights. b is the smallest byte
+// whose scale brings the block's largest finite magnitude to at most 448, so
+// nothing saturates, scaling is exact, and one rounding (to nearest, ties to
+// even) is all that encoding does. gfx950's scaled MFMA multiplies by such
+// scales inside the instruction: the product needs no vector work per block.
+#pragma once
+
+#include "common.h"
+
+namespace qlora {
+
+constexpr int kF8Block = 128;
+
+__host__ __device__ __forceinline__ int64_t f8_pad(int64_t c) { return (c + kF8Block - 1) / kF8Block * kF8Block; }
+
+// Exponent byte for a block whose largest finite |x| has the fp32 bits
+// `abits`: amax = 1.m 2^e needs 2^(e - 8) while 1.m <= 1.75 (448 = 1.75 2^8),
+// else 2^(e - 7); bytes below 0 clamp (blocks under 2^-119), 0 takes scale 1.
+__device__ __forceinline__ uint32_t f8_scale_byte(uint32_t abits) {
+  const int e = (int)(abits >> 23) + ((abits & 0x7FFFFFu) > 0x600000u ? 1 : 0) - 8;
+  return abits == 0 ? 127u : (uint32_t)(e < 0 ? 0 : e);
+}
+
+// 2^-(b - 127), exact for every byte f8_scale_byte gives (0 .. 247)
+__device__ __forceinline__ float f8_inv_scale(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+
+// |x| as fp32 bits for the block maximum: 0 where x is not finite
+__device__ __forceinline__ uint32_t f8_finite_abs(float x) {
+  const uint32_t a = __float_as_uint(x) & 0x7FFFFFFFu;
+  return a >= 0x7F800000u ? 0u : a;
+}
+
+// Four values times inv -> four E4M3 bytes; an infinity is stored as NaN (the
+// format has none), so it stays visible in every product it enters.
+__device__ __forceinline__ uint32_t f8_pack4(const float* x, float inv) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = isinf(x[i]) ? __uint_as_float(0x7FC00000u) : x[i] * inv;
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
+  return (uint32_t)w;
+}
+
+}  // namespace qlora

@@ -560,42 +560,12 @@ __global__ __launch_bounds__(kThreads) void gemm_bf16_kernel(BfArgs a) {
     return;
   }
 
-  // Epilogue: each wave writes its 128 x 64 bf16 block (16 KB) into its own
-  // LDS region (all copies have landed and all fragment reads are done: the
-  // step loop ends with a barrier after waiting for both), then stores
-  // 16-byte row segments.
-  {
-    char* const bufs0 = wave < 4 ? (wave < 2 ? As0 : As1) : (wave < 6 ? Bs0 : Bs1);
-    uint16_t* reg = reinterpret_cast<uint16_t*>(bufs0 + (wave & 1) * 16384);
-#pragma unroll
-    for (int i = 0; i < kTM; ++i)
-#pragma unroll
-      for (int j = 0; j < kTN; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int rr = i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-          reg[rr * 64 + j * 32 + (lane & 31)] = to16<kF16>(acc[i][j][v]);
-        }
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<63>());  // this wave's LDS writes are done
-    // 128 rows x 8 chunks of 16 B
-#pragma unroll 4
-    for (int q = lane; q < 128 * 8; q += 64) {
-      const int rr = q >> 3, cc = q & 7;
-      const int64_t m = m0 + wm0 + rr, n = n0 + wn0 + cc * 8;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(reg + rr * 64 + cc * 8);
-      if (m < a.M) {
-        if (n + 8 <= a.nout && (a.nout & 7) == 0) {
-          *reinterpret_cast<u32x4*>(a.out + m * a.nout + n) = v;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t h = (v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-            if (n + e < a.nout) a.out[m * a.nout + n + e] = (uint16_t)h;
-          }
-        }
-      }
-    }
-  }
+  // Epilogue: all copies have landed and all fragment reads are done (the step
+  // loop ends with a barrier after waiting for both), so each wave stages its
+  // 128 x 64 block in its own 16 KB of the tile buffers.
+  char* const bufs0 = wave < 4 ? (wave < 2 ? As0 : As1) : (wave < 6 ? Bs0 : Bs1);
+  store_staged<kF16>(acc, reinterpret_cast<uint16_t*>(bufs0 + (wave & 1) * 16384), a.out, a.M, a.nout, m0 + wm0,
+                     n0 + wn0, lane);
 }
 
 // Tail tiles: out = RN_bf16(part[0] + part[1] + ... + part[S-1]), added in
@@ -636,11 +606,6 @@ __global__ __launch_bounds__(256) void gemm_bf16_reduce_kernel(const float* __re
   }
 }
 
-struct SplitPlan {
-  int64_t full, tail;
-  int splits;
-};
-
 // One 256 x 256 workgroup fits a CU at a time (128 KB of LDS), so the 256
 // CUs of an MI355X take the tiles in waves of 256. When the last wave holds
 // at most 128 tiles, those tiles are split along the contraction: the
@@ -649,11 +614,16 @@ struct SplitPlan {
 // than 129 tiles in all, every tile is a tail tile).
 constexpr int64_t kWaveTiles = 256;
 
-SplitPlan split_plan(int64_t M, int64_t kc, int kx, int64_t nout) {
+GemmSplit split_plan(int64_t M, int64_t kc, int kx, int64_t nout) {
+  return gemm_split_plan(M, nout, cdiv(kc, (int64_t)kBK) + kx / kBK);
+}
+
+}  // namespace
+
+GemmSplit gemm_split_plan(int64_t M, int64_t nout, int64_t nk) {
   const int64_t tiles = cdiv(M, (int64_t)kBM) * cdiv(nout, (int64_t)kBN);
-  const int64_t nk = cdiv(kc, (int64_t)kBK) + kx / kBK;
   const int64_t rem = tiles % kWaveTiles;
-  SplitPlan p{tiles, 0, 1};
+  GemmSplit p{tiles, 0, 1};
   if (rem == 0 || rem > kWaveTiles / 2) return p;
   int s = 1;
   while (s < 8 && rem * s * 2 <= kWaveTiles && nk >= (int64_t)16 * s) s *= 2;
@@ -665,12 +635,20 @@ SplitPlan split_plan(int64_t M, int64_t kc, int kx, int64_t nout) {
   return p;
 }
 
-}  // namespace
+hipError_t launch_gemm_reduce(const float* part, const GemmSplit& sp, int64_t M, int64_t nout, uint16_t* out,
+                              hipStream_t stream, bool f16) {
+  const unsigned grid = (unsigned)cdiv(sp.tail * (kBM * kBN / 4), (int64_t)256);
+  if (f16)
+    gemm_bf16_reduce_kernel<true><<<grid, 256, 0, stream>>>(part, sp.full, sp.tail, sp.splits, M, nout, out);
+  else
+    gemm_bf16_reduce_kernel<false><<<grid, 256, 0, stream>>>(part, sp.full, sp.tail, sp.splits, M, nout, out);
+  return hipGetLastError();
+}
 
 int gemm_bf16_splits(int64_t M, int64_t kc, int kx, int64_t nout) { return split_plan(M, kc, kx, nout).splits; }
 
 size_t gemm_bf16_ws_bytes(int64_t M, int64_t kc, int kx, int64_t nout) {
-  const SplitPlan p = split_plan(M, kc, kx, nout);
+  const GemmSplit p = split_plan(M, kc, kx, nout);
   return p.splits > 1 ? align256((size_t)p.splits * (size_t)p.tail * kBM * kBN * 4) : 0;
 }
 
@@ -697,7 +675,7 @@ hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, cons
   a.f = f; a.ldf = ldf; a.nout = nout;
   a.fx = kx > 0 ? fx : f; a.ldx = kx > 0 ? ldx : ldf;
   a.out = out;
-  const SplitPlan sp = split_plan(M, kc, kx, nout);
+  const GemmSplit sp = split_plan(M, kc, kx, nout);
   a.full = sp.full; a.tail = sp.tail; a.splits = sp.splits;
   a.part = part;
   if (a.splits > 1 && part == nullptr) return hipErrorInvalidValue;
@@ -722,15 +700,7 @@ hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, cons
     else
       gemm_bf16_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
   }
-  if (a.splits > 1) {
-    const int64_t groups = a.tail * (kBM * kBN / 4);
-    if (f16)
-      gemm_bf16_reduce_kernel<true><<<dim3((unsigned)cdiv(groups, (int64_t)256)), 256, 0, stream>>>(
-          part, a.full, a.tail, a.splits, M, nout, out);
-    else
-      gemm_bf16_reduce_kernel<false><<<dim3((unsigned)cdiv(groups, (int64_t)256)), 256, 0, stream>>>(
-          part, a.full, a.tail, a.splits, M, nout, out);
-  }
+  if (a.splits > 1) launch_gemm_reduce(part, sp, M, nout, out, stream, f16);
   return hipGetLastError();
 }
 

@@ -114,6 +114,16 @@ hipError_t launch_lowrank_rows(const uint16_t* B, int64_t n, int r, uint16_t* ou
 bool gemm_bf16_offsets_fit(int64_t M, int64_t kc, int kx, int64_t nout);
 int gemm_bf16_splits(int64_t M, int64_t kc, int kx, int64_t nout);
 size_t gemm_bf16_ws_bytes(int64_t M, int64_t kc, int kx, int64_t nout);
+// How a 256 x 256-tile GEMM of nk steps spreads its tiles: the first `full`
+// whole, the `tail` after them split `splits` ways along the contraction.
+struct GemmSplit {
+  int64_t full, tail;
+  int splits;
+};
+GemmSplit gemm_split_plan(int64_t M, int64_t nout, int64_t nk);
+// Tail tiles' partials [splits][tail][256 x 256], added in split order and rounded once.
+hipError_t launch_gemm_reduce(const float* part, const GemmSplit& sp, int64_t M, int64_t nout, uint16_t* out,
+                              hipStream_t stream, bool f16);
 // mask (uint8 [M, nout], may be NULL): dropout on the low-rank term, which is
 // multiplied by keep_scale where mask is set and dropped where it is not,
 // before the main contraction is added (one rounding of the whole sum).
@@ -133,6 +143,9 @@ hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, cons
                                 const uint16_t* f, int64_t ldf, const uint16_t* fx, int64_t ldx, int64_t nout,
                                 uint16_t* out, float* part, hipStream_t stream, const uint8_t* mask = nullptr,
                                 float keep_scale = 1.0f, bool f16 = false, bool nn = false);
+
+// [k, lora_extra_cols(r)] rows of A^T: row c = [A[:, c] | A[:, c] | 0].
+hipError_t launch_lowrank_rows_t(const uint16_t* A, int r, int64_t k, uint16_t* out, hipStream_t stream);
 
 // [lora_extra_cols(r), k] rows [A ; A ; 0] (bf16), the low-rank operand of the
 // nn GEMM (dX over a bf16 base).
@@ -169,6 +182,33 @@ size_t gemv_dx_ws_bytes(int64_t n, int64_t k);
 hipError_t launch_gemv_dx(const Nf4View& w, const uint16_t* dY, int64_t M, const float* U, const uint16_t* A, int r,
                           float scale, uint16_t* dX, void* ws, hipStream_t stream, const uint8_t* mask = nullptr,
                           float keep = 1.0f);
+
+// ---- the 8-bit layer (formats and layouts: fp8.h)
+struct Fp8View {
+  int64_t n, k;
+  const uint8_t* codes;  // [n, k up to a multiple of 128]
+  const uint8_t* scale;  // [ceil(n / 128), ceil(k / 128)]
+};
+hipError_t launch_fp8_encode(const void* W, int dt, int64_t n, int64_t k, uint8_t* codes, uint8_t* scale,
+                             hipStream_t stream);
+hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream);
+// Activations [M, C] -> codes [M, C up to 128] + scale words of the GEMM.
+size_t fp8_rows_scale_bytes(int64_t M, int64_t C);
+hipError_t launch_fp8_rows(const uint16_t* X, int64_t M, int64_t C, uint8_t* codes, uint8_t* scale, hipStream_t stream,
+                           bool f16);
+// The weight's codes as [k, n up to 128] rows for dX.
+hipError_t launch_fp8_transpose(const Fp8View& w, uint8_t* out, hipStream_t stream);
+// out = RN16([act | split] [f | fx]^T); f's scale byte of (output block,
+// contraction block) at ob * fs_o + cb * fs_c. part: gemm_fp8_ws_bytes().
+bool gemm_fp8_offsets_fit(int64_t M, int64_t kc, int kx, int64_t nout);
+size_t gemm_fp8_ws_bytes(int64_t M, int64_t kc, int64_t nout);
+hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int64_t kc, const uint16_t* split, int kx,
+                           const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
+                           const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16);
+// M <= 16: activations in the GEMV's operand order, then Y = RN16(X8 W8^T + scale T B^T).
+size_t fp8_gemv_ws_bytes(int64_t k);
+hipError_t launch_fp8_gemv(const Fp8View& w, const uint16_t* X, int64_t M, const float* T, const uint16_t* B, int r,
+                           float scale, uint16_t* Y, void* ws, hipStream_t stream, bool f16);
 
 hipError_t launch_silu_fwd(const uint16_t* G, const uint16_t* U, uint16_t* H, int64_t count,
                            hipStream_t stream);

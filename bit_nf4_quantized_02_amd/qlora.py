@@ -11,6 +11,7 @@ Names follow the C ABI in include/qlora.h.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -28,7 +29,8 @@ BLOCK = 64
 DQ_BLOCK = 256
 MAX_RANK = 128
 SCRATCH_BYTES = 64 << 20   # QLORA_SCRATCH_BYTES: the library's own device scratch per device
-DT_BF16, DT_FP32 = 0, 1
+DT_BF16, DT_FP32, DT_FP16 = 0, 1, 2
+FP8_BLOCK = 128    # contraction elements per scale of the 8-bit layer
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -42,10 +44,15 @@ class _Weight(ctypes.Structure):
                 ("codebook", _vp), ("scale_bf16", ctypes.c_int32)]
 
 
+class _Weight8(ctypes.Structure):
+    _fields_ = [("n", _i64), ("k", _i64), ("codes", _vp), ("scale", _vp)]
+
+
 SCALE_FP32, SCALE_DQ, SCALE_BF16 = 0, 1, 2
 
 
 _W = ctypes.POINTER(_Weight)
+_W8 = ctypes.POINTER(_Weight8)
 
 _SIGS = {
     "qlora_status_string": (ctypes.c_char_p, [_int]),
@@ -94,6 +101,13 @@ _SIGS = {
     "qlora_adapter_merge": (_int, [_W, _vp, _vp, _int, _f, _vp, _int, _vp]),
     "qlora_adapter_unmerge": (_int, [_vp, _i64, _i64, _vp, _vp, _int, _f, _vp, _vp]),
     "qlora_adamw_step": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _f, _f, _f, _f, _f, _vp]),
+    "qlora_fp8_storage_bytes": (_sz, [_i64, _i64]),
+    "qlora_quantize_fp8": (_int, [_vp, _int, _W8, _vp]),
+    "qlora_dequant_fp8": (_int, [_W8, _vp, _vp]),
+    "qlora_fp8_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int]),
+    "qlora_fp8_linear_fwd": (_int, [_W8, _vp, _i64, _int, _vp, _vp, _int, _f, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_fp8_linear_bwd": (_int, [_W8, _vp, _vp, _vp, _i64, _int, _vp, _vp, _int, _f, _vp, _vp, _vp, _int, _vp, _sz,
+                                     _vp]),
     "qlora_calib_mfma": (_int, [_int, _int, _vp, _vp]),
     "qlora_calib_stream_read": (_int, [_vp, _i64, _vp, _vp]),
 }
@@ -468,6 +482,148 @@ def lora_linear_bwd(W: torch.Tensor, X: torch.Tensor | None, T: torch.Tensor | N
     _check(_lib.qlora_lora_linear_bwd(_ptr(W), n, k, _ptr(X), _ptr(T), _ptr(dY), M, _ptr(A), _ptr(B), r, float(scale),
                                       _ptr(dX), _ptr(dA), _ptr(dB), int(bool(accumulate)), _ptr(ws),
                                       0 if ws is None else ws.numel(), _stream(stream)), "qlora_lora_linear_bwd")
+    return dX, dA, dB
+
+
+# --------------------------------------------------------------------------- 8-bit layer
+
+_DT = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32, torch.float16: DT_FP16}
+
+
+def _on(stream, device):
+    """Context of a call: the tensors' device is current, and what the call
+    allocates belongs to the stream that it runs on."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _given(t: torch.Tensor | None, dtype, shape, name, device) -> None:
+    """_need for an operand that may be left out, on the call's device."""
+    if t is None:
+        return
+    _need(t, dtype, shape, name)
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _out(t: torch.Tensor | None, want: bool, dtype, shape, name, device, zeros: bool = False) -> torch.Tensor | None:
+    """An output: the caller's, checked, or a new one where it is wanted."""
+    if t is None and want:
+        return (torch.zeros if zeros else torch.empty)(shape, dtype=dtype, device=device)
+    _given(t, dtype, shape, name, device)
+    return t
+
+
+@dataclass
+class FP8Weight:
+    """Device buffers of one 8-bit [n, k] weight (owned by these tensors)."""
+    n: int
+    k: int
+    codes: torch.Tensor      # uint8 E4M3 patterns [n, k up to a multiple of 128]
+    scale: torch.Tensor      # uint8 exponent bytes [ceil(n / 128), ceil(k / 128)]
+
+    @staticmethod
+    def empty(n: int, k: int, device="cuda") -> "FP8Weight":
+        kb = -(-k // FP8_BLOCK)
+        return FP8Weight(n, k, torch.empty((n, kb * FP8_BLOCK), dtype=torch.uint8, device=device),
+                         torch.empty((-(-n // FP8_BLOCK), kb), dtype=torch.uint8, device=device))
+
+    def struct(self) -> _Weight8:
+        kb = -(-self.k // FP8_BLOCK)
+        _need(self.codes, torch.uint8, (self.n, kb * FP8_BLOCK), "codes")
+        _given(self.scale, torch.uint8, (-(-self.n // FP8_BLOCK), kb), "scale", self.codes.device)
+        return _Weight8(self.n, self.k, self.codes.data_ptr(), self.scale.data_ptr())
+
+    def nbytes(self) -> int:
+        return int(_lib.qlora_fp8_storage_bytes(self.n, self.k))
+
+
+def quantize_fp8(W: torch.Tensor, out: FP8Weight | None = None, stream=None) -> FP8Weight:
+    """Encode W ([n, k] bf16, fp16 or fp32, on the GPU) as E4M3 values with one
+    power-of-two scale per 128 x 128 tile (qlora_quantize_fp8)."""
+    if W.dim() != 2 or W.dtype not in _DT:
+        raise ValueError("W must be [n, k] in bf16, fp16 or fp32")
+    n, k = W.shape
+    _need(W, W.dtype, (n, k), "W")
+    with _on(stream, W.device):
+        if out is None:
+            out = FP8Weight.empty(n, k, device=W.device)
+        elif (out.n, out.k) != (n, k):
+            raise ValueError(f"out: [{out.n}, {out.k}], expected [{n}, {k}]")
+        st = out.struct()
+        _check(_lib.qlora_quantize_fp8(_ptr(W), _DT[W.dtype], ctypes.byref(st), _stream(stream)), "qlora_quantize_fp8")
+    return out
+
+
+def dequant_fp8(w: FP8Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of an 8-bit weight, [n, k] bf16 (qlora_dequant_fp8)."""
+    dev = w.codes.device
+    st = w.struct()
+    with _on(stream, dev):
+        out = _out(out, True, torch.bfloat16, (w.n, w.k), "out", dev)
+        _check(_lib.qlora_dequant_fp8(ctypes.byref(st), _ptr(out), _stream(stream)), "qlora_dequant_fp8")
+    return out
+
+
+def fp8_linear_workspace_bytes(M: int, n: int, k: int, r: int, is_bwd: bool) -> int:
+    return int(_lib.qlora_fp8_linear_workspace_bytes(M, n, k, r, int(bool(is_bwd))))
+
+
+def fp8_linear_fwd(w: FP8Weight, X: torch.Tensor, A: torch.Tensor | None, B: torch.Tensor | None, scale: float,
+                   Y: torch.Tensor | None = None, T: torch.Tensor | None = None, save_T: bool = True,
+                   ws: torch.Tensor | None = None, stream=None):
+    """Y = X8 W8^T + scale (X A^T) B^T with X encoded in the call
+    (qlora_fp8_linear_fwd); bf16 or fp16, as X.  Returns (Y, T)."""
+    st = w.struct()
+    M, dt, dev = X.shape[0], X.dtype, w.codes.device
+    r = 0 if A is None else A.shape[0]
+    _is_f16(dt)
+    _given(X, dt, (M, w.k), "X", dev)
+    if r:
+        _given(A, dt, (r, w.k), "A", dev)
+        _need(B, dt, (w.n, r), "B")
+    with _on(stream, dev):
+        Y = _out(Y, True, dt, (M, w.n), "Y", dev)
+        T = _out(T, save_T and r > 0, torch.float32, (M, r), "T", dev)
+        if ws is None:
+            ws = _bytes(fp8_linear_workspace_bytes(M, w.n, w.k, r, False), dev)
+        _check(_lib.qlora_fp8_linear_fwd(ctypes.byref(st), _ptr(X), M, _DT[dt], _ptr(A), _ptr(B), r, float(scale),
+                                         _ptr(Y), _ptr(T), _ptr(ws), 0 if ws is None else ws.nbytes, _stream(stream)),
+               "qlora_fp8_linear_fwd")
+    return Y, T
+
+
+def fp8_linear_bwd(w: FP8Weight, X: torch.Tensor | None, T: torch.Tensor | None, dY: torch.Tensor,
+                   A: torch.Tensor | None, B: torch.Tensor | None, scale: float, need_dX: bool = True,
+                   need_dA: bool = True, need_dB: bool = True, dX: torch.Tensor | None = None,
+                   dA: torch.Tensor | None = None, dB: torch.Tensor | None = None, accumulate: bool = False,
+                   ws: torch.Tensor | None = None, stream=None):
+    """dX = dY8 W8 + s (dY B) A;  dA = s (dY B)^T X;  dB = s dY^T T
+    (qlora_fp8_linear_bwd).  Returns (dX, dA, dB)."""
+    st = w.struct()
+    M, dt, dev = dY.shape[0], dY.dtype, w.codes.device
+    r = 0 if A is None else A.shape[0]
+    _is_f16(dt)
+    _given(dY, dt, (M, w.n), "dY", dev)
+    _given(X, dt, (M, w.k), "X", dev)
+    if r:
+        _given(A, dt, (r, w.k), "A", dev)
+        _need(B, dt, (w.n, r), "B")
+        _given(T, torch.float32, (M, r), "T", dev)
+    with _on(stream, dev):
+        dX = _out(dX, need_dX, dt, (M, w.k), "dX", dev)
+        dA = _out(dA, r > 0 and need_dA, torch.float32, (r, w.k), "dA", dev, zeros=accumulate)
+        dB = _out(dB, r > 0 and need_dB, torch.float32, (w.n, r), "dB", dev, zeros=accumulate)
+        if ws is None:
+            ws = _bytes(fp8_linear_workspace_bytes(M, w.n, w.k, r, True), dev)
+        _check(_lib.qlora_fp8_linear_bwd(ctypes.byref(st), _ptr(X), _ptr(T), _ptr(dY), M, _DT[dt], _ptr(A), _ptr(B), r,
+                                         float(scale), _ptr(dX), _ptr(dA), _ptr(dB), int(bool(accumulate)), _ptr(ws),
+                                         0 if ws is None else ws.nbytes, _stream(stream)), "qlora_fp8_linear_bwd")
     return dX, dA, dB
 
 

@@ -71,7 +71,7 @@ typedef enum {
   QLORA_ERR_SCRATCH = -6      /* the call needs more than QLORA_SCRATCH_BYTES of library scratch */
 } qlora_status;
 
-typedef enum { QLORA_DT_BF16 = 0, QLORA_DT_FP32 = 1 } qlora_dtype;
+typedef enum { QLORA_DT_BF16 = 0, QLORA_DT_FP32 = 1, QLORA_DT_FP16 = 2 } qlora_dtype;
 
 /*
  * One encoded weight W [n, k]. All pointers are (device), owned by the caller.
@@ -307,6 +307,85 @@ qlora_status qlora_linear_bwd_f16(const qlora_nf4_weight *w, const void *X, cons
                                   const void *dY, int64_t M, const void *A, const void *B, int r,
                                   float scale, void *dX, float *dA, float *dB, int accumulate,
                                   void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The layer over a frozen base kept and multiplied in 8 bits.
+ *
+ * Values are OCP E4M3 with one power-of-two scale per block of 128, stored as
+ * its exponent byte b (scale 2^(b - 127)): for the weight one byte per tile of
+ * 128 rows x 128 columns, for an activation one per 128 consecutive values of
+ * a row. b is the smallest byte whose scale brings the block's largest finite
+ * magnitude to at most 448 (127 for a block of zeros, 0 where even the
+ * smallest scale, 2^-127, is more than that asks for), so nothing saturates
+ * and a value is rounded once, to the nearest E4M3 value, ties to even. NaN
+ * and the infinities, for which the format has one pattern only, are stored as
+ * NaN; finite blocks and other elements of the block do not change with them.
+ *
+ *   codes  [n, kp] bytes, kp = k rounded up to a multiple of 128, the columns
+ *          from k on zero
+ *   scale  [ceil(n / 128), kp / 128] bytes
+ * Both (device), owned by the caller.
+ */
+typedef struct {
+  int64_t n;
+  int64_t k;
+  uint8_t *codes;
+  uint8_t *scale;
+} qlora_fp8_weight;
+
+/* Bytes of an 8-bit weight, codes + scale (0 if k % 64 != 0 or a size is not positive). */
+size_t qlora_fp8_storage_bytes(int64_t n, int64_t k);
+
+/*
+ * Encode W (device, [n, k] row-major, bf16, fp16 or fp32 per w_dtype) into the
+ * buffers of *out; the padding columns are written too.
+ * Errors: INVALID_ARG (NULL / misaligned pointers, bad dtype), SHAPE (k % 64,
+ * sizes below 1 or above 2^22), HIP.
+ */
+qlora_status qlora_quantize_fp8(const void *W, int w_dtype, const qlora_fp8_weight *out, void *stream);
+
+/*
+ * The values a weight stands for, in bf16: out (device, [n, k] bf16). Exact
+ * wherever bf16 holds value * scale; rounded to nearest even below its range.
+ * Errors: INVALID_ARG, SHAPE, HIP.
+ */
+qlora_status qlora_dequant_fp8(const qlora_fp8_weight *w, void *out, void *stream);
+
+/* Workspace bytes of qlora_fp8_linear_fwd (is_bwd = 0) or _bwd (1); 0 on bad
+ * arguments. */
+size_t qlora_fp8_linear_workspace_bytes(int64_t M, int64_t n, int64_t k, int r, int is_bwd);
+
+/*
+ * Forward: T = X A^T (fp32, to T_save if not NULL),
+ *   Y = RN16( X8 W8^T + scale * T B^T ), accumulated in fp32,
+ * with X8 the values X is encoded to (per 128 columns of a row, inside the
+ * call); the adapter sees X itself. X (device) [M, k], A [r, k], B [n, r] and
+ * Y [M, n] in bf16 or fp16 per dtype. For M <= 16 one pass over the codes;
+ * above, an MFMA GEMM that applies the block scales in the instruction.
+ * ws (device) holds qlora_fp8_linear_workspace_bytes(M, n, k, r, 0) bytes.
+ * Errors: INVALID_ARG (also dtype fp32), SHAPE (as qlora_quantize_fp8, rank,
+ * or for M > 16 an operand of 4 GiB: M kp, n kp, or 2 M or 2 n times
+ * qlora_lowrank_split_cols(r)), WORKSPACE, HIP.
+ */
+qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight *w, const void *X, int64_t M, int dtype, const void *A,
+                                  const void *B, int r, float scale, void *Y, float *T_save, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/*
+ * Backward, with U = dY B (fp32):
+ *   dX = RN16( dY8 W8 + scale * U A )   if dX != NULL
+ *   dA = scale * U^T X, dB = scale * dY^T T   (fp32, if not NULL)
+ * dY8: the values dY is encoded to, per 128 columns of a row (inside the
+ * call); U, dA and dB use dY itself. The straight-through gradient of the
+ * forward: rounding X to X8 is passed through. T_saved, accumulate, M = 0 and
+ * r = 0 as in qlora_linear_bwd. Reruns are bit-identical.
+ * ws (device) holds qlora_fp8_linear_workspace_bytes(M, n, k, r, 1) bytes.
+ * Errors: as the forward (operands of dX: M np, k np with np = n rounded up
+ * to a multiple of 128).
+ */
+qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight *w, const void *X, const float *T_saved, const void *dY,
+                                  int64_t M, int dtype, const void *A, const void *B, int r, float scale, void *dX,
+                                  float *dA, float *dB, int accumulate, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Building blocks. qlora_linear_fwd and qlora_linear_bwd are compositions of

@@ -23,10 +23,12 @@ Modules
 ``oracle.adamw``   the AdamW step on the adapter and its learning-rate schedule.
 ``oracle.mlp``     the gated-MLP join silu(G) * U and its gradients, which chains
                    the MLP linears of the 7B block and the 65B-class stack.
+``oracle.fp8``     the 8-bit layer: E4M3 values with a power-of-two scale per
+                   block of 128, the encoding, and the layer over its values.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against facts that do
 not come from this code (values the pages print, closed forms, brute force,
 library routines for special cases). No function here is "parity unpinned".
 """
 
-from . import nf4, linear, merge, adamw, mlp  # noqa: F401
+from . import nf4, linear, merge, adamw, mlp, fp8  # noqa: F401
