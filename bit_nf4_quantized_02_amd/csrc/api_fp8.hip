@@ -209,14 +209,14 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
       e = launch_gemm_fp8(o.yq, o.ys, M, n, o.US, lora_extra_cols(r), o.wt, w->scale, 1, kb, (f8_pad(n) / kF8Block) * kb,
                           o.Ax, k, static_cast<uint16_t*>(dX), o.part, st, f16);
   }
-  if (e == hipSuccess && dA) e = launch_coldot(x, M, k, o.U, r, scale, dA, 1, k, accumulate, grad, st, nullptr, f16);
+  if (e == hipSuccess && dA) e = launch_coldot(x, M, k, o.U, r, scale, dA, 1, k, accumulate, grad, st, nullptr, f16, /*fine=*/true);
   if (e == hipSuccess && dB) {
     const float* T = T_saved;
     if (T == nullptr) {
       e = launch_rowdot(x, M, k, a, 0, r, o.T, nullptr, scale, proj, st, nullptr, f16);
       T = o.T;
     }
-    if (e == hipSuccess) e = launch_coldot(dy, M, n, T, r, scale, dB, r, 1, accumulate, grad, st, nullptr, f16);
+    if (e == hipSuccess) e = launch_coldot(dy, M, n, T, r, scale, dB, r, 1, accumulate, grad, st, nullptr, f16, /*fine=*/true);
   }
   return hip_status(e);
 }

@@ -153,6 +153,11 @@ __device__ __forceinline__ u32x4 dequant8(uint32_t word, const float* lut, float
   return out;
 }
 
+// silu(g) = g sigma(g); e^-g overflows to infinity for large negative g, where
+// sigma is then 0 and silu -0, as they should be.
+__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
+
 __host__ __device__ __forceinline__ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <bool kF16>

@@ -1,0 +1,605 @@
+// Kernels of the gated feed-forward block around its two GEMMs (gemm_bf16.hip)
+// and its few-token form (gemv_nf4.hip):
+//
+//   G = X Wg'^T + s (X Ag^T) Bg^T,  U = X Wu'^T + s (X Au^T) Bu^T,  H = silu(G) U
+//   dG = dH U sg (1 + G (1 - sg)),  dU = dH G sg,  sg = sigma(G)
+//   dX = dG Wg' + dU Wu' + s (Pg Ag + Pu Au),  Pg = dG Bg, Pu = dU Bu
+//   dAg = s Pg^T X,  dBg = s dG^T Tg,  and the same for u
+//
+// dG and dU enter dX's GEMM in 16 bits (its output has no more). The adapter
+// gradients are fp32, so their products take the unrounded fp32 dG and dU in
+// parts: three bf16 parts hold all 24 bits, two fp16 parts 22. Neither G and U
+// nor dG and dU are kept in fp32: the two kernels that need them compute them
+// again from the 16-bit G, U and dH, which is fewer bytes than reading parts.
+#include "common.h"
+#include "kernels.h"
+
+namespace qlora {
+
+namespace {
+
+// ---------------------------------------------------------------- expansion
+
+struct PairView {
+  const uint32_t* codes;
+  const uint8_t* code8;
+  const float* s2;
+  const float* mean;
+  const float* codebook;
+  const uint16_t* lr;  // B (forward) or A (dX)
+};
+
+constexpr int kRows = 8;  // weight rows per workgroup, as the plain row expansion
+
+// One 16-byte output chunk column of 8 rows per thread; blockIdx.z picks the
+// weight. kDx: rows stacked (weight z at rows z np .., zero rows from n to np)
+// with pitch k; else interleaved in groups of 32 with the low-rank columns of
+// the block's forward at the end of each row. Workgroups past the code chunks
+// (blockIdx.y) write the low-rank columns, or for kDx (z == 2) the low-rank rows.
+template <bool kDx, bool kF16>
+__global__ __launch_bounds__(256) void gated_expand_kernel(PairView wg, PairView wu, bool s2_bf16, int64_t n, int64_t np,
+                                                           int64_t k, int r, int xc, u32x4* __restrict__ out) {
+  const int t = threadIdx.x, z = blockIdx.z;
+  const int64_t kw = k / 8;
+  const int64_t r0 = (int64_t)blockIdx.x * kRows;
+  const int64_t c = (int64_t)blockIdx.y * 256 + t;
+  if (kDx && z == 2) {
+    // rows [Ag ; Ag ; Au ; Au ; 0] after the weights
+    if (c >= kw) return;
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t x = r0 + i;
+      if (x >= xc) return;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (x < 4 * r) v = *reinterpret_cast<const u32x4*>((x < 2 * r ? wg.lr : wu.lr) + (x % r) * k + 8 * c);
+      out[(2 * np + x) * kw + c] = v;
+    }
+    return;
+  }
+  const PairView w = z == 0 ? wg : wu;
+  auto row_of = [&](int64_t i) -> int64_t { return kDx ? z * np + i : (i >> 5) * 64 + 32 * z + (i & 31); };
+  const int64_t ldc = kDx ? kw : (k + xc) / 8;
+  if (!kDx && (int64_t)blockIdx.y * 256 >= kw) {
+    // columns [B | B] of this weight at 2r z, zero elsewhere
+    const int cpr = xc / 8;
+    for (int q = t; q < kRows * cpr; q += 256) {
+      const int64_t i = r0 + q / cpr;
+      if (i >= n) return;
+      const int j0 = (q % cpr) * 8;
+      uint32_t h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = j0 + e - 2 * r * z;
+        h[e] = j >= 0 && j < 2 * r ? (uint32_t)w.lr[i * r + (j < r ? j : j - r)] : 0u;
+      }
+      out[row_of(i) * ldc + kw + q % cpr] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
+                                                  h[6] | (h[7] << 16)};
+    }
+    return;
+  }
+  __shared__ float lut[16];
+  if (t < 16) lut[t] = w.codebook[t];
+  __syncthreads();
+  if (c >= kw) return;
+  const float mean = weight_mean(w.code8, w.mean);
+  uint32_t word[kRows], c8[kRows];
+  float s2v[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t wi = (r0 + i < n ? r0 + i : n - 1) * kw + c;
+    word[i] = w.codes[wi];
+    scale_fields(w.code8, w.s2, s2_bf16, wi >> 3, c8[i], s2v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = r0 + i;
+    if (row < n)
+      out[row_of(row) * ldc + c] = dequant8<kF16>(word[i], lut, decode_block_scale(c8[i], s2v[i], mean));
+    else if (kDx && row < np)
+      out[row_of(row) * ldc + c] = u32x4{0u, 0u, 0u, 0u};
+  }
+}
+
+// ------------------------------------------------------------------ the join
+
+// sigma(g) to about 1 ulp without expf's range handling: e^-g as 2^t with the
+// rounding error of t = -g log2 e put back. Beyond |t| = 126 the correction is
+// dropped (2^t there is 0 or leaves sigma 0).
+__device__ __forceinline__ float fast_sigmoid(float g) {
+  const float t = -g * 1.44269504f;
+  const float lo = fmaf(-g, 1.44269504f, -t) + -g * 1.92596303e-8f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float d = 1.0f + (fabsf(t) < 126.0f ? fmaf(e, lo * 0.693147182f, e) : e);
+  float y = __builtin_amdgcn_rcpf(d);
+  return d < 8.0e37f ? fmaf(fmaf(-d, y, 1.0f), y, y) : y;
+}
+
+__device__ __forceinline__ void join_bwd(float g, float u, float dh, float& dg, float& du) {
+  const float sg = fast_sigmoid(g);
+  dg = dh * u * (sg * (1.0f + g * (1.0f - sg)));
+  du = dh * (g * sg);
+}
+
+// Eight 16-bit values at (row, c) of a [*, n] matrix, zero past n.
+template <bool kVec>
+__device__ __forceinline__ u32x4 load8h(const uint16_t* __restrict__ row, int64_t c, int64_t n) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if constexpr (kVec) {
+    if (c < n) v = *reinterpret_cast<const u32x4*>(row + c);
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = c + i < n ? (uint32_t)row[c + i] : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = e[2 * i] | (e[2 * i + 1] << 16);
+  }
+  return v;
+}
+
+// Eight fp32 values -> kParts 16-bit parts whose sum holds 24 (bf16, three)
+// or 22 (fp16, two) bits of each.
+template <bool kF16>
+constexpr int parts_of() { return kF16 ? 2 : 3; }
+
+template <bool kF16>
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&p)[parts_of<kF16>()]) {
+  float rem[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) rem[e] = x[e];
+#pragma unroll
+  for (int q = 0; q < parts_of<kF16>(); ++q)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      p[q][w] = pack2<kF16>(rem[2 * w], rem[2 * w + 1]);
+      rem[2 * w] -= from16<kF16>(p[q][w] & 0xFFFFu);
+      rem[2 * w + 1] -= from16<kF16>(p[q][w] >> 16);
+    }
+}
+
+// dG and dU of eight adjacent elements.
+template <bool kF16>
+__device__ __forceinline__ void join8(const u32x4& g, const u32x4& u, const u32x4& dh, float (&dg)[8], float (&du)[8]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      join_bwd(from16<kF16>((g[w] >> (16 * h)) & 0xFFFFu), from16<kF16>((u[w] >> (16 * h)) & 0xFFFFu),
+               from16<kF16>((dh[w] >> (16 * h)) & 0xFFFFu), dg[2 * w + h], du[2 * w + h]);
+}
+
+// B [n, r] -> Bt [rp, np]: rank-major rows for the join's operand (zero past r and n).
+__global__ __launch_bounds__(256) void gated_bt_kernel(const uint16_t* __restrict__ Bg, const uint16_t* __restrict__ Bu,
+                                                       int64_t n, int64_t np, int r, int rp, uint16_t* __restrict__ out) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int j = blockIdx.y;
+  if (c >= np) return;
+  const uint16_t* const B = blockIdx.z == 0 ? Bg : Bu;
+  out[((int64_t)blockIdx.z * rp + j) * np + c] = j < r && c < n ? B[c * r + j] : (uint16_t)0;
+}
+
+constexpr int kJoinMR = 2;     // 16-row tiles per wave
+constexpr int kJoinWaves = 4;  // each with rows of its own: the four share B's lines in L1
+constexpr int kJoinRows = 16 * kJoinMR * kJoinWaves;
+
+// A wave holds 32 rows and walks its workgroup's columns 32 at a time in the
+// A-operand layout of v_mfma_f32_16x16x32 (lane: row lane % 16, 8 columns from
+// 8 (lane / 16)): G, U and dH are loaded in it, dG and dU formed in it, written
+// rounded to D, and multiplied in parts with Bt's rows. kRP: ranks padded to
+// a multiple of 16 (0: no adapters, D only).
+template <int kRP, bool kF16, bool kVec>
+__global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
+    const uint16_t* __restrict__ G, const uint16_t* __restrict__ U, const uint16_t* __restrict__ dH, int64_t M, int64_t n,
+    int64_t np, const uint16_t* __restrict__ Bt, int r, int64_t cchunk, uint16_t* __restrict__ D,
+    float* __restrict__ part) {
+  constexpr int kTiles = kRP / 16;
+  constexpr int kP = parts_of<kF16>();
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m0 = (int64_t)blockIdx.x * kJoinRows + wave * 16 * kJoinMR;
+  if (m0 >= M) return;
+  const int64_t cbeg = (int64_t)blockIdx.y * cchunk;
+  const int64_t cend = cbeg + cchunk < np ? cbeg + cchunk : np;
+  const int64_t co = 8 * (lane >> 4);
+  int64_t off[kJoinMR];  // row offsets (rows past M repeat the last one; not stored)
+#pragma unroll
+  for (int i = 0; i < kJoinMR; ++i) {
+    const int64_t m = m0 + 16 * i + (lane & 15);
+    off[i] = (m < M ? m : M - 1) * n;
+  }
+  f32x4 acc[2][kJoinMR][kTiles > 0 ? kTiles : 1];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int i = 0; i < kJoinMR; ++i)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) acc[w][i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Stage {
+    u32x4 g[kJoinMR], u[kJoinMR], d[kJoinMR];
+  };
+  auto load = [&](int64_t c, Stage& s) {
+#pragma unroll
+    for (int i = 0; i < kJoinMR; ++i) {
+      s.g[i] = load8h<kVec>(G + off[i], c + co, n);
+      s.u[i] = load8h<kVec>(U + off[i], c + co, n);
+      s.d[i] = load8h<kVec>(dH + off[i], c + co, n);
+    }
+  };
+  Stage cur, nxt;
+  load(cbeg, cur);
+  for (int64_t c = cbeg; c < cend; c += 32) {
+    load(c + 32 < cend ? c + 32 : c, nxt);
+    u32x4 b[2][kTiles > 0 ? kTiles : 1];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+        b[w][t] = *reinterpret_cast<const u32x4*>(Bt + ((int64_t)w * kRP + 16 * t + (lane & 15)) * np + c + co);
+#pragma unroll
+    for (int i = 0; i < kJoinMR; ++i) {
+      float dg[8], du[8];
+      join8<kF16>(cur.g[i], cur.u[i], cur.d[i], dg, du);
+      u32x4 p[2][kP];
+      split8<kF16>(dg, p[0]);
+      split8<kF16>(du, p[1]);
+      const int64_t m = m0 + 16 * i + (lane & 15);
+      if (D != nullptr && m < M) {
+        *reinterpret_cast<u32x4*>(D + m * 2 * np + c + co) = p[0][0];
+        *reinterpret_cast<u32x4*>(D + m * 2 * np + np + c + co) = p[1][0];
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int q = kP - 1; q >= 0; --q)
+            acc[w][i][t] = mfma16<kF16>(__builtin_bit_cast(bf16x8, p[w][q]), __builtin_bit_cast(bf16x8, b[w][t]),
+                                        acc[w][i][t]);
+    }
+    cur = nxt;
+  }
+  // partials [split][w][M][r]; D layout: lane -> rank lane % 16, rows 4 (lane / 16) + v
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int i = 0; i < kJoinMR; ++i)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t m = m0 + 16 * i + 4 * (lane >> 4) + v;
+          const int j = 16 * t + (lane & 15);
+          if (m < M && j < r) part[(((int64_t)blockIdx.y * 2 + w) * M + m) * r + j] = acc[w][i][t][v];
+        }
+}
+
+// P = the partials added in split order; split row m = [hi_g | lo_g | hi_u |
+// lo_u | 0] of scale P. One thread per (m, w, j), and for the padding columns.
+template <bool kF16>
+__global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ part, int splits, int64_t M, int r,
+                                                      int xc, float scale, float* __restrict__ P,
+                                                      uint16_t* __restrict__ split) {
+#pragma clang fp contract(off)
+  const int per = xc - 2 * r;  // 2r products and xc - 4r zero columns
+  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (q >= M * per) return;
+  const int64_t m = q / per;
+  const int x = (int)(q % per);
+  if (x >= 2 * r) {
+    if (split) split[m * xc + 2 * r + x] = 0;
+    return;
+  }
+  const int w = x >= r ? 1 : 0, j = x - w * r;
+  float s = part[(w * M + m) * r + j];
+  for (int p = 1; p < splits; ++p) s += part[(((int64_t)p * 2 + w) * M + m) * r + j];
+  P[(w * M + m) * r + j] = s;
+  if (split) {
+    const float v = scale * s;
+    const uint16_t hi = to16<kF16>(v);
+    split[m * xc + w * 2 * r + j] = hi;
+    split[m * xc + w * 2 * r + r + j] = to16<kF16>(v - from16<kF16>(hi));
+  }
+}
+
+// ------------------------------------------------------ adapter gradients dB
+
+// T [2][M][r] -> Tt [part][w][rp][Mp]: rank-major rows of parts, zero past M and r.
+template <bool kF16>
+__global__ __launch_bounds__(256) void gated_tt_kernel(const float* __restrict__ T, int64_t M, int64_t Mp, int r, int rp,
+                                                       uint16_t* __restrict__ out) {
+  const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int j = blockIdx.y, w = blockIdx.z;
+  if (m >= Mp) return;
+  float x = m < M && j < r ? T[(w * M + m) * r + j] : 0.0f;
+#pragma unroll
+  for (int p = 0; p < parts_of<kF16>(); ++p) {
+    const uint16_t h = to16<kF16>(x);
+    out[(((int64_t)p * 2 + w) * rp + j) * Mp + m] = h;
+    x -= from16<kF16>(h);
+  }
+}
+
+constexpr int kDbCols = 64;                    // columns per workgroup
+constexpr int kDbPitch = kDbCols * 2 + 16;     // bytes per staged row
+
+// Partial of dB over tokens [m0, m1): rows = ranks, columns = block columns.
+// Each 32-token step every thread forms dG and dU of one row's 8 columns and
+// stages their parts as [token][column] tiles in LDS (two sets, one barrier
+// per step); the B operand (8 tokens of one column per lane) comes back through
+// the transposing read, the A operand (8 tokens of one rank) straight from Tt.
+// The four waves split the ranks first and then the columns, so that no rank
+// row is loaded twice where there are at least 64. Products of parts whose
+// order is below the last bit kept are left out (mid * lo and lo * lo).
+template <int kRP, bool kF16, bool kVec>
+__global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restrict__ G, const uint16_t* __restrict__ U,
+                                                       const uint16_t* __restrict__ dH, int64_t M, int64_t n,
+                                                       const uint16_t* __restrict__ Tt, int64_t Mp, int r,
+                                                       int64_t mchunk, float* __restrict__ part) {
+  constexpr int kP = parts_of<kF16>();
+  constexpr int kJTall = kRP / 16;
+  constexpr int kWJ = kJTall >= 4 ? 4 : kJTall;     // waves along ranks
+  constexpr int kWC = 4 / kWJ;                      // waves along columns
+  constexpr int kJT = kJTall / kWJ;                 // rank tiles per wave
+  constexpr int kCT = kDbCols / 16 / kWC;           // column tiles per wave
+  __shared__ __attribute__((aligned(16))) char sm[2][2][kP][32 * kDbPitch];  // [set][w][part]
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wj = wave % kWJ, wc = wave / kWJ;
+  const int64_t c0 = (int64_t)blockIdx.x * kDbCols;
+  const int64_t m0 = (int64_t)blockIdx.y * mchunk;
+  const int64_t m1 = m0 + mchunk < M ? m0 + mchunk : M;
+  const int64_t pc = c0 + 8 * (t & 7);
+  const int prow = t >> 3;
+  struct Stage {
+    u32x4 g, u, d;
+  };
+  auto load = [&](int64_t mb, Stage& s) {
+    const int64_t m = mb + prow;
+    const int64_t o = (m < m1 ? m : m1 - 1) * n;
+    s.g = load8h<kVec>(G + o, pc, n);
+    s.u = load8h<kVec>(U + o, pc, n);
+    s.d = load8h<kVec>(dH + o, pc, n);
+    if (m >= m1) s.d = u32x4{0u, 0u, 0u, 0u};
+    if (m >= m1) s.g = s.u = s.d;  // rows past the range add nothing, whatever the last row holds
+  };
+  auto stage = [&](int set, const Stage& s) {
+    float dg[8], du[8];
+    join8<kF16>(s.g, s.u, s.d, dg, du);
+    u32x4 p[kP];
+    char* const at = sm[0][0][0] + set * (2 * kP * 32 * kDbPitch) + prow * kDbPitch + (t & 7) * 16;
+    split8<kF16>(dg, p);
+#pragma unroll
+    for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(at + q * 32 * kDbPitch) = p[q];
+    split8<kF16>(du, p);
+#pragma unroll
+    for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(at + (kP + q) * 32 * kDbPitch) = p[q];
+  };
+  f32x4 acc[2][kJT][kCT];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int a = 0; a < kJT; ++a)
+#pragma unroll
+      for (int b = 0; b < kCT; ++b) acc[w][a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  Stage st;
+  if (m0 < m1) {
+    load(m0, st);
+    stage(0, st);
+    load(m0 + 32 < m1 ? m0 + 32 : m0, st);
+  }
+  __syncthreads();
+  int set = 0;
+  for (int64_t mb = m0; mb < m1; mb += 32, set ^= 1) {
+    u32x4 ta[2][kP][kJT];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int q = 0; q < kP; ++q)
+#pragma unroll
+        for (int a = 0; a < kJT; ++a)
+          ta[w][q][a] = *reinterpret_cast<const u32x4*>(
+              Tt + (((int64_t)q * 2 + w) * kRP + 16 * (wj * kJT + a) + (lane & 15)) * Mp + mb + 8 * (lane >> 4));
+    if (mb + 32 < m1) stage(set ^ 1, st);
+    load(mb + 64 < m1 ? mb + 64 : m0, st);
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int b = 0; b < kCT; ++b) {
+        bf16x8 pb[kP];
+#pragma unroll
+        for (int q = 0; q < kP; ++q)
+          pb[q] = tr_rows8(sm[0][0][0] + ((set * 2 + w) * kP + q) * 32 * kDbPitch, kDbPitch, 16 * (wc * kCT + b), lane);
+#pragma unroll
+        for (int a = 0; a < kJT; ++a)
+#pragma unroll
+          for (int order = kP - 1; order >= 0; --order)
+#pragma unroll
+            for (int q = 0; q <= order; ++q)
+              acc[w][a][b] = mfma16<kF16>(__builtin_bit_cast(bf16x8, ta[w][order - q][a]), pb[q], acc[w][a][b]);
+      }
+    __syncthreads();
+  }
+  // D[j][c]: lane -> c = lane % 16, j = 4 (lane / 16) + v; partials [split][w][r][n]
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int a = 0; a < kJT; ++a)
+#pragma unroll
+      for (int b = 0; b < kCT; ++b) {
+        const int64_t c = c0 + 16 * (wc * kCT + b) + (lane & 15);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int j = 16 * (wj * kJT + a) + 4 * (lane >> 4) + v;
+          if (c < n && j < r) part[(((int64_t)blockIdx.y * 2 + w) * r + j) * n + c] = acc[w][a][b][v];
+        }
+      }
+}
+
+// dB[c, j] (+)= scale * (partials added in split order)
+__global__ __launch_bounds__(256) void gated_db_reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
+                                                              int r, float scale, float* __restrict__ dBg,
+                                                              float* __restrict__ dBu, int accumulate) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int w = blockIdx.y;
+  float* const dB = w == 0 ? dBg : dBu;
+  if (i >= n * r || dB == nullptr) return;
+  const int64_t j = i / n, c = i % n;
+  float s = part[((int64_t)w * r + j) * n + c];
+  for (int p = 1; p < splits; ++p) s += part[(((int64_t)p * 2 + w) * r + j) * n + c];
+  float* const o = dB + c * r + j;
+  *o = accumulate ? *o + scale * s : scale * s;
+}
+
+int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+
+// Column ranges of the join: about 1024 workgroups (each a multiple of 32
+// columns, at least 256).
+struct JoinPlan {
+  int64_t cchunk;
+  int splits;
+};
+
+JoinPlan join_plan(int64_t M, int64_t n) {
+  const int64_t np = gated_pad(n);
+  int64_t s = cdiv((int64_t)1024, cdiv(M, (int64_t)kJoinRows));
+  if (s > cdiv(np, (int64_t)256)) s = cdiv(np, (int64_t)256);
+  if (s > 32) s = 32;
+  const int64_t cchunk = cdiv(cdiv(np, s), (int64_t)32) * 32;
+  return {cchunk, (int)cdiv(np, cchunk)};
+}
+
+// Token ranges of dB: about 1024 workgroups, each at least 128 tokens.
+struct DbPlan {
+  int64_t mchunk;
+  int splits;
+};
+
+DbPlan db_plan(int64_t M, int64_t n) {
+  int64_t s = cdiv((int64_t)1024, cdiv(n, (int64_t)kDbCols));
+  if (s > cdiv(M, (int64_t)128)) s = cdiv(M, (int64_t)128);
+  if (s > 16) s = 16;
+  const int64_t mchunk = cdiv(cdiv(M, s), (int64_t)32) * 32;
+  return {mchunk, (int)cdiv(M, mchunk)};
+}
+
+PairView pair_view(const Nf4View& w, const uint16_t* lr) {
+  return PairView{reinterpret_cast<const uint32_t*>(w.codes), w.code8, w.s2, w.mean, w.codebook, lr};
+}
+
+}  // namespace
+
+size_t gated_fwd_operand_bytes(int64_t n, int64_t k, int r) {
+  return align256((size_t)gated_rows(n) * (size_t)(k + gated_extra_cols(r)) * 2);
+}
+
+hipError_t launch_gated_expand_fwd(const Nf4View& g, const Nf4View& u, const uint16_t* Bg, const uint16_t* Bu, int r,
+                                   uint16_t* out, hipStream_t stream, bool f16) {
+  const int xc = gated_extra_cols(r);
+  const dim3 grid((unsigned)cdiv(g.n, (int64_t)kRows), (unsigned)(cdiv(g.k / 8, (int64_t)256) + (xc > 0 ? 1 : 0)), 2);
+  u32x4* const o = reinterpret_cast<u32x4*>(out);
+  const PairView a = pair_view(g, Bg), b = pair_view(u, Bu);
+  if (f16)
+    gated_expand_kernel<false, true><<<grid, 256, 0, stream>>>(a, b, g.s2_bf16, g.n, g.n, g.k, r, xc, o);
+  else
+    gated_expand_kernel<false, false><<<grid, 256, 0, stream>>>(a, b, g.s2_bf16, g.n, g.n, g.k, r, xc, o);
+  return hipGetLastError();
+}
+
+size_t gated_dx_operand_bytes(int64_t n, int64_t k, int r) {
+  return align256((size_t)(2 * gated_pad(n) + gated_extra_cols(r)) * (size_t)k * 2);
+}
+
+hipError_t launch_gated_expand_dx(const Nf4View& g, const Nf4View& u, const uint16_t* Ag, const uint16_t* Au, int r,
+                                  uint16_t* out, hipStream_t stream, bool f16) {
+  const int xc = gated_extra_cols(r);
+  const int64_t np = gated_pad(g.n);
+  const int64_t rows = np > xc ? np : xc;
+  const dim3 grid((unsigned)cdiv(rows, (int64_t)kRows), (unsigned)cdiv(g.k / 8, (int64_t)256), xc > 0 ? 3 : 2);
+  u32x4* const o = reinterpret_cast<u32x4*>(out);
+  const PairView a = pair_view(g, Ag), b = pair_view(u, Au);
+  if (f16)
+    gated_expand_kernel<true, true><<<grid, 256, 0, stream>>>(a, b, g.s2_bf16, g.n, np, g.k, r, xc, o);
+  else
+    gated_expand_kernel<true, false><<<grid, 256, 0, stream>>>(a, b, g.s2_bf16, g.n, np, g.k, r, xc, o);
+  return hipGetLastError();
+}
+
+size_t gated_join_ws_bytes(int64_t M, int64_t n, int r) {
+  if (r == 0) return 0;
+  return align256((size_t)2 * rank_pad(r) * (size_t)gated_pad(n) * 2) +
+         align256((size_t)join_plan(M, n).splits * 2 * (size_t)M * r * 4);
+}
+
+hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
+                             const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* D, float* P,
+                             uint16_t* split, void* ws, hipStream_t stream, bool f16) {
+  const JoinPlan pl = join_plan(M, n);
+  const int64_t np = gated_pad(n);
+  const int rp = rank_pad(r);
+  uint16_t* const Bt = static_cast<uint16_t*>(ws);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)2 * rp * (size_t)np * 2));
+  if (r > 0)
+    gated_bt_kernel<<<dim3((unsigned)cdiv(np, (int64_t)256), (unsigned)rp, 2), 256, 0, stream>>>(Bg, Bu, n, np, r, rp, Bt);
+  const dim3 grid((unsigned)cdiv(M, (int64_t)kJoinRows), (unsigned)pl.splits);
+#define QLORA_JOIN2(RP, H, V) \
+  gated_join_kernel<RP, H, V><<<grid, 64 * kJoinWaves, 0, stream>>>(G, U, dH, M, n, np, Bt, r, pl.cchunk, D, part)
+#define QLORA_JOIN(RP)                                                              \
+  {                                                                                 \
+    if (n % 8 == 0) { if (f16) QLORA_JOIN2(RP, true, true); else QLORA_JOIN2(RP, false, true); } \
+    else { if (f16) QLORA_JOIN2(RP, true, false); else QLORA_JOIN2(RP, false, false); }          \
+  }
+  if (r == 0) QLORA_JOIN(0)
+  else if (rp == 16) QLORA_JOIN(16)
+  else if (rp == 32) QLORA_JOIN(32)
+  else if (rp == 64) QLORA_JOIN(64)
+  else QLORA_JOIN(128)
+#undef QLORA_JOIN
+#undef QLORA_JOIN2
+  if (r > 0) {
+    const int xc = gated_extra_cols(r);
+    const unsigned pg = (unsigned)cdiv(M * (xc - 2 * r), (int64_t)256);
+    if (f16)
+      gated_p_kernel<true><<<pg, 256, 0, stream>>>(part, pl.splits, M, r, xc, scale, P, split);
+    else
+      gated_p_kernel<false><<<pg, 256, 0, stream>>>(part, pl.splits, M, r, xc, scale, P, split);
+  }
+  return hipGetLastError();
+}
+
+size_t gated_db_ws_bytes(int64_t M, int64_t n, int r) {
+  if (r == 0) return 0;
+  return align256((size_t)3 * 2 * rank_pad(r) * (size_t)(cdiv(M, (int64_t)32) * 32) * 2) +
+         align256((size_t)db_plan(M, n).splits * 2 * r * (size_t)n * 4);
+}
+
+hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
+                           const float* T, int r, float scale, float* dBg, float* dBu, int accumulate, void* ws,
+                           hipStream_t stream, bool f16) {
+  const DbPlan pl = db_plan(M, n);
+  const int64_t Mp = cdiv(M, (int64_t)32) * 32;
+  const int rp = rank_pad(r);
+  uint16_t* const Tt = static_cast<uint16_t*>(ws);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)3 * 2 * rp * (size_t)Mp * 2));
+  const dim3 tg((unsigned)cdiv(Mp, (int64_t)256), (unsigned)rp, 2);
+  if (f16)
+    gated_tt_kernel<true><<<tg, 256, 0, stream>>>(T, M, Mp, r, rp, Tt);
+  else
+    gated_tt_kernel<false><<<tg, 256, 0, stream>>>(T, M, Mp, r, rp, Tt);
+  const dim3 grid((unsigned)cdiv(n, (int64_t)kDbCols), (unsigned)pl.splits);
+#define QLORA_DB2(RP, H, V) \
+  gated_db_kernel<RP, H, V><<<grid, 256, 0, stream>>>(G, U, dH, M, n, Tt, Mp, r, pl.mchunk, part)
+#define QLORA_DB(RP)                                                                         \
+  {                                                                                          \
+    if (n % 8 == 0) { if (f16) QLORA_DB2(RP, true, true); else QLORA_DB2(RP, false, true); }  \
+    else { if (f16) QLORA_DB2(RP, true, false); else QLORA_DB2(RP, false, false); }           \
+  }
+  if (rp == 16) QLORA_DB(16)
+  else if (rp == 32) QLORA_DB(32)
+  else if (rp == 64) QLORA_DB(64)
+  else QLORA_DB(128)
+#undef QLORA_DB
+#undef QLORA_DB2
+  gated_db_reduce_kernel<<<dim3((unsigned)cdiv(n * r, (int64_t)256), 2), 256, 0, stream>>>(part, pl.splits, n, r, scale,
+                                                                                          dBg, dBu, accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

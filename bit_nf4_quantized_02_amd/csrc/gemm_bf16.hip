@@ -60,6 +60,11 @@ struct BfArgs {
   // dropout on the low-rank term (the masked kernel only): uint8 [M, nout]
   const uint8_t* mask;
   float keep_scale;
+  // gated block (kGate only; out is H): saved pre-activations, nullable, and
+  // the block's width (H, G, U are [M, hn])
+  uint16_t* g_out;
+  uint16_t* u_out;
+  int64_t hn;
 };
 
 constexpr int kCopies = 32 / kWaves;  // 1 KB copies per wave per operand tile
@@ -424,7 +429,11 @@ __device__ __forceinline__ void mask_acc_lds(f32x16 (&acc)[kTM][kTN], const char
 // from there, then runs its main steps as usual.
 // kF16: fp16 operands and output (the compute-type ablation), else bf16.
 // kA3: the mirrored ring (bf16_step_a3; plain bf16 only).
-template <bool kMask, bool kF16, bool kNN = false, bool kA3 = false>
+// kGate: the gated feed-forward block's forward. The weight operand holds 32
+// gate rows, then the same 32 up rows, so a wave's two 32-column blocks are G
+// and U of the same outputs, lane by lane, and the epilogue forms H = silu(G) U
+// from the unrounded fp32 sums: G and U need not reach memory.
+template <bool kMask, bool kF16, bool kNN = false, bool kA3 = false, bool kGate = false>
 __global__ __launch_bounds__(kThreads) void gemm_bf16_kernel(BfArgs a) {
   // four separate arrays so the compiler can tell the buffer being filled by
   // direct copies from the one being read
@@ -564,8 +573,16 @@ __global__ __launch_bounds__(kThreads) void gemm_bf16_kernel(BfArgs a) {
   // loop ends with a barrier after waiting for both), so each wave stages its
   // 128 x 64 block in its own 16 KB of the tile buffers.
   char* const bufs0 = wave < 4 ? (wave < 2 ? As0 : As1) : (wave < 6 ? Bs0 : Bs1);
-  store_staged<kF16>(acc, reinterpret_cast<uint16_t*>(bufs0 + (wave & 1) * 16384), a.out, a.M, a.nout, m0 + wm0,
-                     n0 + wn0, lane);
+  uint16_t* const reg = reinterpret_cast<uint16_t*>(bufs0 + (wave & 1) * 16384);
+  if constexpr (kGate) {
+    const int64_t h0 = (n0 + wn0) / 2;
+    if (a.g_out) store_half<kF16>(reg, a.g_out, a.M, a.hn, m0 + wm0, h0, lane, [&](int i, int v) { return acc[i][0][v]; });
+    if (a.u_out) store_half<kF16>(reg, a.u_out, a.M, a.hn, m0 + wm0, h0, lane, [&](int i, int v) { return acc[i][1][v]; });
+    store_half<kF16>(reg, a.out, a.M, a.hn, m0 + wm0, h0, lane,
+                     [&](int i, int v) { return silu(acc[i][0][v]) * acc[i][1][v]; });
+  } else {
+    store_staged<kF16>(acc, reg, a.out, a.M, a.nout, m0 + wm0, n0 + wn0, lane);
+  }
 }
 
 // Tail tiles: out = RN_bf16(part[0] + part[1] + ... + part[S-1]), added in
@@ -603,6 +620,41 @@ __global__ __launch_bounds__(256) void gemm_bf16_reduce_kernel(const float* __re
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (n + i < nout) o[i] = to16<kF16>(e[i]);
+  }
+}
+
+// The same for the gated block: a tile's column groups of 64 are 32 of G and
+// the same 32 of U. Four adjacent outputs of one row per thread.
+template <bool kF16>
+__global__ __launch_bounds__(256) void gemm_gated_reduce_kernel(const float* __restrict__ part, int64_t full,
+                                                                int64_t tail, int splits, int64_t M, int64_t nout,
+                                                                int64_t hn, uint16_t* __restrict__ H,
+                                                                uint16_t* __restrict__ G, uint16_t* __restrict__ U) {
+#pragma clang fp contract(off)
+  constexpr int kTile = kBM * kBN;
+  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;  // group of 4 outputs
+  const int64_t ti = q / (kTile / 8);
+  if (ti >= tail) return;
+  const int loc = (int)(q % (kTile / 8));
+  const int rr = loc / (kBN / 8), hc = (loc % (kBN / 8)) * 4;
+  const int64_t mt = cdiv(M, (int64_t)kBM), nt = cdiv(nout, (int64_t)kBN);
+  int64_t tm, tn;
+  tile_of(tm, tn, mt, nt, full + ti);
+  const int64_t m = tm * kBM + rr, n = tn * (kBN / 2) + hc;
+  if (m >= M || n >= hn) return;
+  const float* const p0 = part + ti * kTile + rr * kBN + (hc >> 5) * 64 + (hc & 31);
+  f32x4 g = *reinterpret_cast<const f32x4*>(p0), u = *reinterpret_cast<const f32x4*>(p0 + 32);
+  for (int p = 1; p < splits; ++p) {
+    const float* const pp = p0 + (int64_t)p * tail * kTile;
+    g += *reinterpret_cast<const f32x4*>(pp);
+    u += *reinterpret_cast<const f32x4*>(pp + 32);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i >= hn) break;
+    H[m * hn + n + i] = to16<kF16>(silu(g[i]) * u[i]);
+    if (G) G[m * hn + n + i] = to16<kF16>(g[i]);
+    if (U) U[m * hn + n + i] = to16<kF16>(u[i]);
   }
 }
 
@@ -682,8 +734,10 @@ hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, cons
   const dim3 grid((unsigned)(a.full + a.tail * a.splits));
   if (nn) {
     // the weight operand stored [contraction][output] (bf16 base, dX)
-    if (mask != nullptr || f16) return hipErrorInvalidValue;
-    if (M * kc * 2 > kActStreamBytes)
+    if (mask != nullptr) return hipErrorInvalidValue;
+    if (f16)
+      gemm_bf16_kernel<false, true, true><<<grid, kThreads, 0, stream>>>(a);
+    else if (M * kc * 2 > kActStreamBytes)
       gemm_bf16_kernel<false, false, true, true><<<grid, kThreads, 0, stream>>>(a);
     else
       gemm_bf16_kernel<false, false, true><<<grid, kThreads, 0, stream>>>(a);
@@ -700,7 +754,7 @@ hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, cons
     else
       gemm_bf16_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
   }
-  if (a.splits > 1) launch_gemm_reduce(part, sp, M, nout, out, stream, f16);
+  if (a.splits > 1) return launch_gemm_reduce(part, sp, M, nout, out, stream, f16);
   return hipGetLastError();
 }
 
@@ -713,6 +767,36 @@ hipError_t launch_gemm_bf16(const uint16_t* act, int64_t M, int64_t kc, const ui
   const int64_t ldf = kcp + kx;
   return launch_gemm_bf16_ext(act, M, kc, split, kx, f, ldf, f + kcp, ldf, nout, out, part, stream, mask, keep_scale,
                               f16, false);
+}
+
+hipError_t launch_gemm_gated(const uint16_t* act, int64_t M, int64_t k, const uint16_t* split, int kx,
+                             const uint16_t* f, int64_t n, uint16_t* H, uint16_t* G, uint16_t* U, float* part,
+                             hipStream_t stream, bool f16) {
+  BfArgs a{};
+  a.act = act; a.M = M; a.kc = k;
+  a.act_x = split; a.kx = kx;
+  a.f = f; a.ldf = k + kx; a.nout = gated_rows(n);
+  a.fx = f + k; a.ldx = k + kx;
+  a.out = H; a.g_out = G; a.u_out = U; a.hn = n;
+  const GemmSplit sp = split_plan(M, k, kx, a.nout);
+  a.full = sp.full; a.tail = sp.tail; a.splits = sp.splits;
+  a.part = part;
+  if (a.splits > 1 && part == nullptr) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)(a.full + a.tail * a.splits));
+  if (f16)
+    gemm_bf16_kernel<false, true, false, false, true><<<grid, kThreads, 0, stream>>>(a);
+  else if (M * k * 2 > kActStreamBytes)
+    gemm_bf16_kernel<false, false, false, true, true><<<grid, kThreads, 0, stream>>>(a);
+  else
+    gemm_bf16_kernel<false, false, false, false, true><<<grid, kThreads, 0, stream>>>(a);
+  if (a.splits > 1) {
+    const unsigned rg = (unsigned)cdiv(sp.tail * (kBM * kBN / 8), (int64_t)256);
+    if (f16)
+      gemm_gated_reduce_kernel<true><<<rg, 256, 0, stream>>>(part, sp.full, sp.tail, sp.splits, M, a.nout, n, H, G, U);
+    else
+      gemm_gated_reduce_kernel<false><<<rg, 256, 0, stream>>>(part, sp.full, sp.tail, sp.splits, M, a.nout, n, H, G, U);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace qlora

@@ -321,7 +321,7 @@ hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int
     gemm_fp8_kernel<true><<<grid, kThreads, 0, stream>>>(a);
   else
     gemm_fp8_kernel<false><<<grid, kThreads, 0, stream>>>(a);
-  if (a.splits > 1) launch_gemm_reduce(part, sp, M, nout, out, stream, f16);
+  if (a.splits > 1) return launch_gemm_reduce(part, sp, M, nout, out, stream, f16);
   return hipGetLastError();
 }
 

@@ -154,6 +154,39 @@ __device__ __forceinline__ void store_staged(const f32x16 (&acc)[kTM][kTN], uint
   }
 }
 
+// A wave's 128 x 32 block of 16-bit outputs at (m0, n0), value(i, v) being
+// register v of 32-row block i, staged and stored as above.
+template <bool kF16, typename F>
+__device__ __forceinline__ void store_half(uint16_t* reg, uint16_t* out, int64_t M, int64_t N, int64_t m0, int64_t n0,
+                                           int lane, F value) {
+#pragma unroll
+  for (int i = 0; i < kTM; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int rr = i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+      reg[rr * 32 + (lane & 31)] = to16<kF16>(value(i, v));
+    }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<63>());  // this wave's LDS writes are done
+  // 128 rows x 4 chunks of 16 B
+#pragma unroll 4
+  for (int q = lane; q < 128 * 4; q += 64) {
+    const int rr = q >> 2, cc = q & 3;
+    const int64_t m = m0 + rr, n = n0 + cc * 8;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(reg + rr * 32 + cc * 8);
+    if (m < M) {
+      if (n + 8 <= N && (N & 7) == 0) {
+        *reinterpret_cast<u32x4*>(out + m * N + n) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t h = (v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+          if (n + e < N) out[m * N + n + e] = (uint16_t)h;
+        }
+      }
+    }
+  }
+}
+
 // Dropout on the low-rank term of a tile: while the accumulators hold only
 // that term (its contraction steps run first), each output (m, n) is
 // multiplied by keep_scale where mask[m, n] is set and cleared where it is

@@ -31,6 +31,11 @@
 #include "common.h"
 #include "kernels.h"
 
+// The gated feed-forward block's few-token form is the same kernel with the
+// gate weight's rows as one tile and the up weight's as the other (kPair): X
+// is read and the launch paid once for both, and H = silu(G) U is formed from
+// the unrounded fp32 sums in the epilogue.
+
 #ifndef QLORA_GEMV_XP_MIN_M
 #define QLORA_GEMV_XP_MIN_M 5
 #endif
@@ -104,12 +109,27 @@ struct GvStage {
   u32x4 xa[8];
 };
 
+// The up weight of the gated block (kPair), its low-rank factors and the
+// block's outputs (the kernel's own weight is the gate; Y receives H; G and U
+// may be NULL).
+struct GvSecond {
+  const uint8_t* codes;
+  const uint8_t* code8;
+  const float* s2;
+  const float* mean;
+  const float* codebook;
+  const float* T;
+  const uint16_t* B;
+  uint16_t* G;
+  uint16_t* U;
+};
+
 // kT: 16-row tiles per workgroup (each wave covers all of them over its
 // share of the contraction); kW: waves. kXp: activations from the
 // operand-ordered copy Xp (else read in place from X). kF16: fp16
 // activations, weights, B and output (the compute-type ablation). kForm: the
 // block-scale form (scale_fields_of).
-template <int kT, int kW, bool kXp, bool kF16, int kForm>
+template <int kT, int kW, bool kXp, bool kF16, int kForm, bool kPair = false>
 __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ code8,
                                                        const float* __restrict__ s2,
@@ -119,13 +139,14 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
                                                        const u32x4* __restrict__ Xp, int64_t M,
                                                        const float* __restrict__ T,
                                                        const uint16_t* __restrict__ B, int r, float scale,
-                                                       uint16_t* __restrict__ Y) {
-  constexpr int NT = 16 * kT;
+                                                       uint16_t* __restrict__ Y, GvSecond up = {}) {
+  static_assert(!kPair || kT == 2, "a pair is one tile of each weight");
+  constexpr int NT = kPair ? 16 : 16 * kT;  // output columns per workgroup
   constexpr int kSlot = kT * 2048;  // one wave's codes of one chunk: kT tiles x 16 rows x 128 bytes
   // three separate ring arrays, so the compiler can tell the one being read
   // from the ones being filled by direct copies (and waits only for the copy
   // of the chunk it reads)
-  constexpr int kLutCopies = lut_copies<kW>();
+  constexpr int kLutCopies = kPair ? 16 : lut_copies<kW>();
   __shared__ __attribute__((aligned(16))) char lut[256 * kLutCopies * 8];
   __shared__ __attribute__((aligned(16))) char ring0[kW * kSlot];
   __shared__ __attribute__((aligned(16))) char ring1[kW * kSlot];
@@ -136,12 +157,23 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
   // table fill below reads LDS, not 16 rounds of global loads per thread
   float* const levels = reinterpret_cast<float*>(ring0);
   if (t < 16) levels[t] = codebook[t];
-  __syncthreads();
-  for (int i = t; i < 256 * kLutCopies; i += 64 * kW) {
-    const int e = i / kLutCopies;
-    reinterpret_cast<float2*>(lut)[i] = float2{levels[e & 15], levels[e >> 4]};
+  if constexpr (kPair) {
+    if (t < 16) levels[16 + t] = up.codebook[t];
   }
-  const float mean = weight_mean(code8, mean_p);
+  __syncthreads();
+  // kPair: where the two weights' levels are equal (the usual case) both read
+  // one table of 16 copies; else each has its own of 8 copies in its half.
+  bool same = true;
+  if constexpr (kPair)
+    same = __ballot(__float_as_uint(levels[lane & 15]) != __float_as_uint(levels[16 + (lane & 15)])) == 0;
+  for (int i = t; i < 256 * kLutCopies; i += 64 * kW) {
+    const int e = same ? i / kLutCopies : (i >> 3) & 255;
+    const float* const lv = same || i < 2048 ? levels : levels + 16;
+    reinterpret_cast<float2*>(lut)[i] = float2{lv[e & 15], lv[e >> 4]};
+  }
+  float mean[kPair ? 2 : 1];
+  mean[0] = weight_mean(code8, mean_p);
+  if constexpr (kPair) mean[1] = weight_mean(up.code8, up.mean);
   const int64_t n0 = (int64_t)blockIdx.x * NT;
   // this wave's contiguous range of 256-column chunks (a multiple-of-64 tail
   // in the last one)
@@ -159,7 +191,9 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
   // N lie past the end of the codes and read as zero (their outputs are not
   // stored); columns past K in the last chunk read the next row's codes and
   // meet zero activations.
-  const i32x4 crs = make_rsrc(codes, N * (K / 2));
+  i32x4 crs[kPair ? 2 : 1];
+  crs[0] = make_rsrc(codes, N * (K / 2));
+  if constexpr (kPair) crs[1] = make_rsrc(up.codes, N * (K / 2));
   uint32_t cvoff[kT][2];
 #pragma unroll
   for (int i = 0; i < kT; ++i)
@@ -167,16 +201,18 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
     for (int h = 0; h < 2; ++h) {
       const int rr = 8 * h + (lane >> 3);
       const int g = (lane & 7) ^ code_swz(rr);
-      cvoff[i][h] = (uint32_t)((n0 + 16 * i + rr) * (K / 2) + 16 * g);
+      cvoff[i][h] = (uint32_t)((n0 + (kPair ? 0 : 16 * i) + rr) * (K / 2) + 16 * g);
     }
   // reads: row col, logical segments 2 grp and 2 grp + 1 (64 codes)
   const uint32_t rd0 = (uint32_t)(col * 128 + 16 * ((2 * grp) ^ code_swz(col)));
-  const uint32_t lane_off = (uint32_t)(lane % kLutCopies) * 8;
+  const uint32_t lane_off = same ? (uint32_t)(lane % kLutCopies) * 8 : (uint32_t)(lane % 8) * 8;
+  const uint32_t up_off = same ? lane_off : lane_off + 16384;  // kPair: the up weight's table
+  const int lut_shift = same ? 7 : 6;                          // kPair: log2 bytes per entry
   // scale rows (clamped: rows past N are computed and dropped)
   uint32_t bbase[kT];  // (blocks < 2^27: the codes stay under 4 GiB)
 #pragma unroll
   for (int i = 0; i < kT; ++i) {
-    const int64_t n = n0 + 16 * i + col;
+    const int64_t n = n0 + (kPair ? 0 : 16 * i) + col;
     bbase[i] = (uint32_t)((n < N ? n : N - 1) * kblocks);
   }
   // activations: Xp[q][s][lane] (operand order), or X[col][256 q + 64 grp +
@@ -186,8 +222,14 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
 
   // scale arrays (blocks < 2^30: 32-bit byte offsets)
   const int64_t nblk = N * kblocks;
-  const i32x4 c8rs = make_rsrc(code8, kForm == 0 ? nblk : 0);
-  const i32x4 s2rs = make_rsrc(s2, kForm == 0 ? cdiv(nblk, (int64_t)kDqBlock) * 4 : nblk * (kForm == 1 ? 4 : 2));
+  const int64_t s2_bytes = kForm == 0 ? cdiv(nblk, (int64_t)kDqBlock) * 4 : nblk * (kForm == 1 ? 4 : 2);
+  i32x4 c8rs[kPair ? 2 : 1], s2rs[kPair ? 2 : 1];
+  c8rs[0] = make_rsrc(code8, kForm == 0 ? nblk : 0);
+  s2rs[0] = make_rsrc(s2, s2_bytes);
+  if constexpr (kPair) {
+    c8rs[1] = make_rsrc(up.code8, kForm == 0 ? nblk : 0);
+    s2rs[1] = make_rsrc(up.s2, s2_bytes);
+  }
 
   auto issue = [&](int j, char* R, GvStage<kT>& st) {
     const int q = wave + kW * (j < cnt ? j : cnt - 1);  // past the range: the last chunk again
@@ -195,11 +237,12 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
 #pragma unroll
     for (int i = 0; i < kT; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) copy16(crs, cvoff[i][h], q * 128, dst + i * 2048 + h * 1024);
+      for (int h = 0; h < 2; ++h) copy16(crs[kPair ? i : 0], cvoff[i][h], q * 128, dst + i * 2048 + h * 1024);
     const int kc = q * 256 + 64 * grp;
     const uint32_t bq = (uint32_t)(kc < K ? kc / kBlock : kblocks - 1);
 #pragma unroll
-    for (int i = 0; i < kT; ++i) scale_fields_of<kForm>(c8rs, s2rs, bbase[i] + bq, st.c8[i], st.s2v[i]);
+    for (int i = 0; i < kT; ++i)
+      scale_fields_of<kForm>(c8rs[kPair ? i : 0], s2rs[kPair ? i : 0], bbase[i] + bq, st.c8[i], st.s2v[i]);
     if constexpr (kXp) {
 #pragma unroll
       for (int s = 0; s < 8; ++s) st.xa[s] = raw_buffer_load_b128(xrs, (int)xvoff, q * 8192 + s * 1024, 0);
@@ -236,7 +279,7 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
         cw[i][e] = c0[e];
         cw[i][4 + e] = c1[e];
       }
-      cp[i] = decode_block_scale(st.c8[i], st.s2v[i], mean);
+      cp[i] = decode_block_scale(st.c8[i], st.s2v[i], mean[kPair ? i : 0]);
     }
     float2 lv[2][4 * kGw];
     auto gather = [&](int g, float2 (&out)[4 * kGw]) {
@@ -246,7 +289,9 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           uint32_t addr;
-          if constexpr (kLutCopies == 32) {
+          if constexpr (kPair) {
+            addr = (((cw[i][s0 + w] >> (8 * p)) & 0xFFu) << lut_shift) | (i == 0 ? lane_off : up_off);
+          } else if constexpr (kLutCopies == 32) {
             // bytes of the result: lane_off (byte 0 of the second operand),
             // code byte p (byte p of the first), zero, zero
             addr = __builtin_amdgcn_perm(cw[i][s0 + w], lane_off, 0x0C0C0400u + ((uint32_t)p << 8));
@@ -335,11 +380,13 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
     for (int i = wave; i < kT; i += kW) {
       f32x4 l = f32x4{0.f, 0.f, 0.f, 0.f};
       const int m = lane & 15;
-      const int64_t n = n0 + i * 16 + (lane & 15);
+      const int64_t n = n0 + (kPair ? 0 : i * 16) + (lane & 15);
+      const float* const Ti = kPair && i == 1 ? up.T : T;
+      const uint16_t* const Bi = kPair && i == 1 ? up.B : B;
       for (int j0 = 0; j0 < r; j0 += 4) {
         const int j = j0 + (lane >> 4);
-        const float a = (m < M && j < r) ? T[m * r + j] : 0.0f;
-        const float b = (n < N && j < r) ? from16<kF16>(B[n * r + j]) : 0.0f;
+        const float a = (m < M && j < r) ? Ti[m * r + j] : 0.0f;
+        const float b = (n < N && j < r) ? from16<kF16>(Bi[n * r + j]) : 0.0f;
         l = __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, l, 0, 0, 0);
       }
 #pragma unroll
@@ -352,11 +399,21 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
     const int64_t n = n0 + nl;
     if (m >= M || n >= N) continue;
     const int i = nl >> 4, nc = nl & 15;
-    float y = red[0][i][m][nc];
+    auto sum = [&](int i) {
+      float y = red[0][i][m][nc];
 #pragma unroll
-    for (int w2 = 1; w2 < kW; ++w2) y += red[w2][i][m][nc];  // in wave order
-    if (r > 0) y = fmaf(scale, lred[i][m][nc], y);
-    Y[m * N + n] = to16<kF16>(y);
+      for (int w2 = 1; w2 < kW; ++w2) y += red[w2][i][m][nc];  // in wave order
+      return r > 0 ? fmaf(scale, lred[i][m][nc], y) : y;
+    };
+    const float y = sum(i);
+    if constexpr (kPair) {
+      const float u = sum(1);
+      Y[m * N + n] = to16<kF16>(silu(y) * u);
+      if (up.G) up.G[m * N + n] = to16<kF16>(y);
+      if (up.U) up.U[m * N + n] = to16<kF16>(u);
+    } else {
+      Y[m * N + n] = to16<kF16>(y);
+    }
   }
 }
 
@@ -414,6 +471,41 @@ hipError_t launch_gemv(const Nf4View& w, const uint16_t* X, int64_t M, const flo
 #undef QLORA_GEMV2
 #undef QLORA_GEMV3
 #undef QLORA_GEMV4
+  return hipGetLastError();
+}
+
+hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const float* T,
+                            const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* H, uint16_t* G,
+                            uint16_t* U, void* ws, hipStream_t stream, bool f16) {
+  if (!gemv_fits(g.n, g.k)) return hipErrorInvalidValue;
+  u32x4* Xp = static_cast<u32x4*>(ws);
+  const bool xp = M >= kXpMinM && g.n >= kXpMinN;
+  if (xp) {
+    const int64_t entries = cdiv(g.k, (int64_t)256) * 512;
+    gemv_xperm_kernel<<<(unsigned)cdiv(entries, (int64_t)256), 256, 0, stream>>>(X, M, g.k, Xp, entries);
+  }
+  const GvSecond up{u.codes, u.code8, u.s2, u.mean, u.codebook, T ? T + M * r : nullptr, Bu, G, U};
+  // four waves (two workgroups per CU) where there are at least two per CU, else eight
+  const int64_t wgs = cdiv(g.n, (int64_t)16);
+  const int form = g.code8 ? 0 : (g.s2_bf16 ? 2 : 1);
+#define QLORA_GVP3(W, XP, H16, F)                                                                               \
+  gemv_nf4_kernel<2, W, XP, H16, F, true><<<dim3((unsigned)wgs), 64 * W, 0, stream>>>(                           \
+      g.codes, g.code8, g.s2, g.mean, g.codebook, g.s2_bf16, g.n, g.k, X, Xp, M, T, Bg, r, scale, H, up)
+#define QLORA_GVP2(W, XP, H16)                   \
+  {                                              \
+    if (form == 0) QLORA_GVP3(W, XP, H16, 0);    \
+    else if (form == 1) QLORA_GVP3(W, XP, H16, 1); \
+    else QLORA_GVP3(W, XP, H16, 2);              \
+  }
+#define QLORA_GVP1(W, XP) \
+  { if (f16) QLORA_GVP2(W, XP, true) else QLORA_GVP2(W, XP, false) }
+#define QLORA_GVP(W) \
+  { if (xp) QLORA_GVP1(W, true) else QLORA_GVP1(W, false) }
+  if (wgs >= 512) QLORA_GVP(4) else QLORA_GVP(8)
+#undef QLORA_GVP
+#undef QLORA_GVP1
+#undef QLORA_GVP2
+#undef QLORA_GVP3
   return hipGetLastError();
 }
 

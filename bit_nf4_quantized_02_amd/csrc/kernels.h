@@ -48,21 +48,24 @@ inline int lora_extra_cols(int r) { return r > 0 ? ((2 * r + 63) / 64) * 64 : 0;
 // out[m, j] = sum_c P[m, c] Q(c, j), P bf16 [M, C]; Q bf16 [r, C] (q_layout
 // 0) or [C, r] (q_layout 1); fp32 out [M, r] (nullable). If split != NULL it
 // also receives rows [bf16(scale*out) | bf16(scale*out - hi) | 0 ...] of
-// lora_extra_cols(r) elements. part: workspace of rowdot_ws_bytes (may be 0).
+// lora_extra_cols(r) elements; with split_cols >= 2r the rows are zero-padded
+// to split_cols elements instead and lie split_ld elements apart. part:
+// workspace of rowdot_ws_bytes (may be 0).
 size_t rowdot_ws_bytes(int64_t M, int64_t C, int r);
 // pmask (uint8 [M, C], q_layout 0 and C % 8 == 0 only; NULL: none): P's
 // elements whose byte is 0 read as zero (dropout on the adapter's input).
 hipError_t launch_rowdot(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int q_layout, int r,
                          float* out, uint16_t* split, float scale, float* part, hipStream_t stream,
-                         const uint8_t* pmask = nullptr, bool f16 = false);
+                         const uint8_t* pmask = nullptr, bool f16 = false, int split_cols = 0, int split_ld = 0);
 
 // Column reduction over M in fixed order, for the adapter gradients:
 //   G[c, j] (+)= scale * sum_m P[m, c] * Q[m, j]    P bf16 [M, C], Q fp32 [M, r]
 // written at G[c * g_sc + j * g_sj]. partial (fp32, [splits, C, r]) is workspace.
+// fine (bf16, no mask): Q in three bf16 parts (24 bits) instead of two.
 size_t coldot_ws_bytes(int64_t M, int64_t C, int r);
 hipError_t launch_coldot(const uint16_t* P, int64_t M, int64_t C, const float* Q, int r, float scale,
                          float* G, int64_t g_sc, int64_t g_sj, int accumulate, float* partial,
-                         hipStream_t stream, const uint8_t* pmask = nullptr, bool f16 = false);
+                         hipStream_t stream, const uint8_t* pmask = nullptr, bool f16 = false, bool fine = false);
 // dA and dB of one layer in one launch (both with a single token split, no
 // mask): products (P0, C0, Q0 -> G0 with strides g_sc0, g_sj0) and (P1, ...),
 // the same arithmetic as two launch_coldot calls. coldot_pairable tells when
@@ -182,6 +185,44 @@ size_t gemv_dx_ws_bytes(int64_t n, int64_t k);
 hipError_t launch_gemv_dx(const Nf4View& w, const uint16_t* dY, int64_t M, const float* U, const uint16_t* A, int r,
                           float scale, uint16_t* dX, void* ws, hipStream_t stream, const uint8_t* mask = nullptr,
                           float keep = 1.0f);
+
+// ---- the gated feed-forward block H = silu(G) U over two NF4 weights
+// Both T = X Ag^T, X Au^T as [2][M][r]. G and U may be NULL. ws: gemv_ws_bytes(k).
+hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const float* T,
+                            const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* H, uint16_t* G,
+                            uint16_t* U, void* ws, hipStream_t stream, bool f16);
+// Low-rank columns of the block's GEMMs, [hi_g | lo_g | hi_u | lo_u | 0].
+inline int gated_extra_cols(int r) { return r > 0 ? ((4 * r + 63) / 64) * 64 : 0; }
+// Both weights expanded for the forward: rows in groups of 64, 32 gate rows
+// then the same 32 up rows, [W' | low-rank columns], pitch k + extra.
+inline int64_t gated_rows(int64_t n) { return (n + 31) / 32 * 64; }
+size_t gated_fwd_operand_bytes(int64_t n, int64_t k, int r);
+hipError_t launch_gated_expand_fwd(const Nf4View& g, const Nf4View& u, const uint16_t* Bg, const uint16_t* Bu, int r,
+                                   uint16_t* out, hipStream_t stream, bool f16);
+// The forward GEMM over it with the join in its epilogue (part as the plain
+// GEMM's for gated_rows(n) outputs).
+hipError_t launch_gemm_gated(const uint16_t* act, int64_t M, int64_t k, const uint16_t* split, int kx,
+                             const uint16_t* f, int64_t n, uint16_t* H, uint16_t* G, uint16_t* U, float* part,
+                             hipStream_t stream, bool f16);
+// Both weights contraction-major for dX: [Wg ; 0 ; Wu ; 0 ; Ag ; Ag ; Au ; Au
+// ; 0], each weight's rows padded to a multiple of 64, pitch k.
+inline int64_t gated_pad(int64_t n) { return (n + 63) / 64 * 64; }
+size_t gated_dx_operand_bytes(int64_t n, int64_t k, int r);
+hipError_t launch_gated_expand_dx(const Nf4View& g, const Nf4View& u, const uint16_t* Ag, const uint16_t* Au, int r,
+                                  uint16_t* out, hipStream_t stream, bool f16);
+// D [M, 2 gated_pad(n)] = [dG | 0 | dU | 0] in 16 bits (D NULL: not written),
+// and (r > 0) P = [dG Bg ; dU Bu] as fp32 [2][M][r] from the unrounded dG, dU,
+// with its scaled hi / lo columns in split (NULL: not written).
+size_t gated_join_ws_bytes(int64_t M, int64_t n, int r);
+hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
+                             const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* D, float* P,
+                             uint16_t* split, void* ws, hipStream_t stream, bool f16);
+// dBg = scale dG^T T[0], dBu = scale dU^T T[1] (either may be NULL), dG and dU
+// unrounded.
+size_t gated_db_ws_bytes(int64_t M, int64_t n, int r);
+hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
+                           const float* T, int r, float scale, float* dBg, float* dBu, int accumulate, void* ws,
+                           hipStream_t stream, bool f16);
 
 // ---- the 8-bit layer (formats and layouts: fp8.h)
 struct Fp8View {

@@ -10,8 +10,6 @@ namespace qlora {
 
 namespace {
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
-
 __device__ __forceinline__ void unpack8(const u32x4 v, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -101,6 +101,11 @@ _SIGS = {
     "qlora_adapter_merge": (_int, [_W, _vp, _vp, _int, _f, _vp, _int, _vp]),
     "qlora_adapter_unmerge": (_int, [_vp, _i64, _i64, _vp, _vp, _int, _f, _vp, _vp]),
     "qlora_adamw_step": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _f, _f, _f, _f, _f, _vp]),
+    "qlora_gated_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int]),
+    "qlora_gated_fwd": (_int, [_W, _W, _vp, _i64, _int, _vp, _vp, _vp, _vp, _int, _f, _vp, _vp, _vp, _vp, _vp, _sz,
+                               _vp]),
+    "qlora_gated_bwd": (_int, [_W, _W, _vp, _vp, _vp, _vp, _vp, _i64, _int, _vp, _vp, _vp, _vp, _int, _f, _vp, _vp, _vp,
+                               _vp, _vp, _int, _vp, _sz, _vp]),
     "qlora_fp8_storage_bytes": (_sz, [_i64, _i64]),
     "qlora_quantize_fp8": (_int, [_vp, _int, _W8, _vp]),
     "qlora_dequant_fp8": (_int, [_W8, _vp, _vp]),
@@ -485,7 +490,7 @@ def lora_linear_bwd(W: torch.Tensor, X: torch.Tensor | None, T: torch.Tensor | N
     return dX, dA, dB
 
 
-# --------------------------------------------------------------------------- 8-bit layer
+# --------------------------------------------------------------------------- feed-forward operators
 
 _DT = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32, torch.float16: DT_FP16}
 
@@ -518,6 +523,91 @@ def _out(t: torch.Tensor | None, want: bool, dtype, shape, name, device, zeros: 
     _given(t, dtype, shape, name, device)
     return t
 
+
+# --------------------------------------------------------------------------- gated feed-forward block
+
+def gated_workspace_bytes(M: int, n: int, k: int, r: int, is_bwd: bool) -> int:
+    return int(_lib.qlora_gated_workspace_bytes(M, n, k, r, int(bool(is_bwd))))
+
+
+def _adapters(n, k, A_gate, B_gate, A_up, B_up, dt, dev) -> int:
+    """The block's rank; both adapters or neither, of one rank."""
+    r = 0 if A_gate is None else A_gate.shape[0]
+    if (A_gate is None) != (A_up is None):
+        raise ValueError("both adapters or neither")
+    if r:
+        for t, shape, name in ((A_gate, (r, k), "A_gate"), (A_up, (r, k), "A_up"), (B_gate, (n, r), "B_gate"),
+                               (B_up, (n, r), "B_up")):
+            if t is None:
+                raise ValueError(f"{name}: missing")
+            _given(t, dt, shape, name, dev)
+    return r
+
+
+def gated_fwd(w_gate: NF4Weight, w_up: NF4Weight, X: torch.Tensor, A_gate: torch.Tensor | None,
+              B_gate: torch.Tensor | None, A_up: torch.Tensor | None, B_up: torch.Tensor | None, scale: float,
+              H: torch.Tensor | None = None, G: torch.Tensor | None = None, U: torch.Tensor | None = None,
+              T: torch.Tensor | None = None, save: bool = True, ws: torch.Tensor | None = None, stream=None):
+    """H = silu(G) U with G and U the two layers' outputs, in bf16 or fp16 as X
+    (qlora_gated_fwd).  Returns (H, G, U, T): with save, G, U ([M, n]) and T
+    ([2, M, r] fp32) for gated_bwd; else those given, or None."""
+    M, dt, dev, n, k = X.shape[0], X.dtype, w_gate.codes.device, w_gate.n, w_gate.k
+    _is_f16(dt)
+    _given(X, dt, (M, k), "X", dev)
+    if w_up.codes.device != dev:
+        raise ValueError(f"w_up: on {w_up.codes.device}, expected {dev}")
+    r = _adapters(n, k, A_gate, B_gate, A_up, B_up, dt, dev)
+    sg, su = w_gate.struct(), w_up.struct()
+    with _on(stream, dev):
+        H = _out(H, True, dt, (M, n), "H", dev)
+        G = _out(G, save, dt, (M, n), "G", dev)
+        U = _out(U, save, dt, (M, n), "U", dev)
+        T = _out(T, save and r > 0, torch.float32, (2, M, r), "T", dev)
+        if ws is None:
+            ws = _bytes(gated_workspace_bytes(M, n, k, r, False), dev)
+        _check(_lib.qlora_gated_fwd(ctypes.byref(sg), ctypes.byref(su), _ptr(X), M, _DT[dt], _ptr(A_gate), _ptr(B_gate),
+                                    _ptr(A_up), _ptr(B_up), r, float(scale), _ptr(H), _ptr(G), _ptr(U), _ptr(T),
+                                    _ptr(ws), 0 if ws is None else ws.nbytes, _stream(stream)), "qlora_gated_fwd")
+    return H, G, U, T
+
+
+def gated_bwd(w_gate: NF4Weight, w_up: NF4Weight, X: torch.Tensor | None, T: torch.Tensor | None, G: torch.Tensor,
+              U: torch.Tensor, dH: torch.Tensor, A_gate: torch.Tensor | None, B_gate: torch.Tensor | None,
+              A_up: torch.Tensor | None, B_up: torch.Tensor | None, scale: float, need_dX: bool = True,
+              need_dA: bool = True, need_dB: bool = True, dX: torch.Tensor | None = None,
+              dA_gate: torch.Tensor | None = None, dB_gate: torch.Tensor | None = None,
+              dA_up: torch.Tensor | None = None, dB_up: torch.Tensor | None = None, accumulate: bool = False,
+              ws: torch.Tensor | None = None, stream=None):
+    """The gradients of gated_fwd from its saved G, U, T (qlora_gated_bwd).
+    Returns (dX, dA_gate, dB_gate, dA_up, dB_up)."""
+    M, dt, dev, n, k = dH.shape[0], dH.dtype, w_gate.codes.device, w_gate.n, w_gate.k
+    _is_f16(dt)
+    for t, shape, name in ((dH, (M, n), "dH"), (G, (M, n), "G"), (U, (M, n), "U"), (X, (M, k), "X")):
+        _given(t, dt, shape, name, dev)
+    if w_up.codes.device != dev:
+        raise ValueError(f"w_up: on {w_up.codes.device}, expected {dev}")
+    r = _adapters(n, k, A_gate, B_gate, A_up, B_up, dt, dev)
+    if r:
+        _given(T, torch.float32, (2, M, r), "T", dev)
+    sg, su = w_gate.struct(), w_up.struct()
+    f32, a, b = torch.float32, r > 0 and need_dA, r > 0 and need_dB
+    with _on(stream, dev):
+        dX = _out(dX, need_dX, dt, (M, k), "dX", dev)
+        dA_gate = _out(dA_gate, a, f32, (r, k), "dA_gate", dev, zeros=accumulate)
+        dB_gate = _out(dB_gate, b, f32, (n, r), "dB_gate", dev, zeros=accumulate)
+        dA_up = _out(dA_up, a, f32, (r, k), "dA_up", dev, zeros=accumulate)
+        dB_up = _out(dB_up, b, f32, (n, r), "dB_up", dev, zeros=accumulate)
+        if ws is None:
+            ws = _bytes(gated_workspace_bytes(M, n, k, r, True), dev)
+        _check(_lib.qlora_gated_bwd(ctypes.byref(sg), ctypes.byref(su), _ptr(X), _ptr(T), _ptr(G), _ptr(U), _ptr(dH), M,
+                                    _DT[dt], _ptr(A_gate), _ptr(B_gate), _ptr(A_up), _ptr(B_up), r, float(scale),
+                                    _ptr(dX), _ptr(dA_gate), _ptr(dB_gate), _ptr(dA_up), _ptr(dB_up),
+                                    int(bool(accumulate)), _ptr(ws), 0 if ws is None else ws.nbytes, _stream(stream)),
+               "qlora_gated_bwd")
+    return dX, dA_gate, dB_gate, dA_up, dB_up
+
+
+# --------------------------------------------------------------------------- 8-bit layer
 
 @dataclass
 class FP8Weight:

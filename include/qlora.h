@@ -309,6 +309,50 @@ qlora_status qlora_linear_bwd_f16(const qlora_nf4_weight *w, const void *X, cons
                                   void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * The gated feed-forward block over two NF4 weights with their adapters:
+ *   G = X Wg'^T + scale * Tg Bg^T,   Tg = X Ag^T     (fp32 sums)
+ *   U = X Wu'^T + scale * Tu Bu^T,   Tu = X Au^T
+ *   H = RN16( silu(G) * U ),  silu(g) = g / (1 + e^-g)
+ * in one kernel: H is formed from the unrounded fp32 G and U, which reach
+ * memory only if they are asked for. It replaces two qlora_linear_fwd and
+ * qlora_silu_mul_fwd (which round G and U first).
+ * Both weights (device) [n, k], in one storage form (each may have levels of
+ * its own). X [M, k], A_* [r, k], B_* [n, r], H and, if not NULL, G_save =
+ * RN16(G) and U_save = RN16(U), all [M, n], in bf16 or fp16 per dtype (w' in
+ * the same type). T_save (nullable): [2, M, r] fp32, Tg then Tu. For M <= 16
+ * one pass over both weights' codes; above, both are expanded into ws and
+ * multiplied by one GEMM whose epilogue is the join.
+ * ws (device) holds qlora_gated_workspace_bytes(M, n, k, r, 0) bytes.
+ * Errors: INVALID_ARG (also dtype fp32, and weights of different storage
+ * forms), SHAPE (weights of different shapes, k % 64, a size above 2^22, the
+ * rank, or an operand of the GEMM of 4 GiB), WORKSPACE, HIP.
+ */
+size_t qlora_gated_workspace_bytes(int64_t M, int64_t n, int64_t k, int r, int is_bwd);
+qlora_status qlora_gated_fwd(const qlora_nf4_weight *w_gate, const qlora_nf4_weight *w_up, const void *X, int64_t M,
+                             int dtype, const void *A_gate, const void *B_gate, const void *A_up, const void *B_up,
+                             int r, float scale, void *H, void *G_save, void *U_save, float *T_save, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/*
+ * Its backward, from the saved G and U (16 bits) and dH [M, n]:
+ *   dG = dH * U * silu'(G),  dU = dH * silu(G)         (fp32)
+ *   Pg = dG Bg,  Pu = dU Bu                            (fp32)
+ *   dX = RN16( RN16(dG) Wg' + RN16(dU) Wu' + scale (Pg Ag + Pu Au) )
+ *   dA_gate = scale Pg^T X,  dB_gate = scale dG^T Tg, and the same for up
+ * Each output may be NULL; the two halves of dX are one product with one
+ * rounding. The adapter gradients (fp32) come from the unrounded dG and dU.
+ * T_saved ([2, M, r], nullable: recomputed from X), accumulate, M = 0 and r =
+ * 0 as in qlora_linear_bwd; X is needed as there. Reruns are bit-identical.
+ * ws (device) holds qlora_gated_workspace_bytes(M, n, k, r, 1) bytes.
+ * Errors: as the forward.
+ */
+qlora_status qlora_gated_bwd(const qlora_nf4_weight *w_gate, const qlora_nf4_weight *w_up, const void *X,
+                             const float *T_saved, const void *G, const void *U, const void *dH, int64_t M, int dtype,
+                             const void *A_gate, const void *B_gate, const void *A_up, const void *B_up, int r,
+                             float scale, void *dX, float *dA_gate, float *dB_gate, float *dA_up, float *dB_up,
+                             int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * The layer over a frozen base kept and multiplied in 8 bits.
  *
  * Values are OCP E4M3 with one power-of-two scale per block of 128, stored as

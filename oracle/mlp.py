@@ -51,3 +51,29 @@ def bf16_step(ref) -> np.ndarray:
     _, e = np.frexp(a)                     # a = m 2^e, 0.5 <= m < 1
     step = np.ldexp(np.ones_like(a), e - 8)
     return np.maximum(step, 2.0 ** -133)
+
+
+def gated_fwd(X, Wg, Wu, Ag, Bg, Au, Bu, s):
+    """(H, G, U, Tg, Tu) of the gated block over the expanded weights Wg, Wu
+    with their adapters (None: none): G = X Wg^T + s Tg Bg^T, Tg = X Ag^T, U
+    likewise, H = silu(G) U from the unrounded G and U."""
+    f = lambda t: np.asarray(t, dtype=np.float64)  # noqa: E731
+    X = f(X)
+    G, U, Tg, Tu = X @ f(Wg).T, X @ f(Wu).T, None, None
+    if Ag is not None:
+        Tg, Tu = X @ f(Ag).T, X @ f(Au).T
+        G, U = G + s * (Tg @ f(Bg).T), U + s * (Tu @ f(Bu).T)
+    return silu_mul_fwd(G, U), G, U, Tg, Tu
+
+
+def gated_bwd(X, Wg, Wu, G, U, dH, Ag, Bg, Au, Bu, s):
+    """(dX, dAg, dBg, dAu, dBu) for dH arriving at H, from the saved G and U."""
+    f = lambda t: np.asarray(t, dtype=np.float64)  # noqa: E731
+    dG, dU = silu_mul_bwd(G, U, dH)
+    dX = dG @ f(Wg) + dU @ f(Wu)
+    if Ag is None:
+        return dX, None, None, None, None
+    X, Ag, Bg, Au, Bu = (f(t) for t in (X, Ag, Bg, Au, Bu))
+    Pg, Pu = dG @ Bg, dU @ Bu
+    dX = dX + s * (Pg @ Ag + Pu @ Au)
+    return dX, s * (Pg.T @ X), s * (dG.T @ (X @ Ag.T)), s * (Pu.T @ X), s * (dU.T @ (X @ Au.T))
