@@ -144,7 +144,13 @@ template <bool kF16>
 __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&p)[parts_of<kF16>()]) {
   float rem[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) rem[e] = x[e];
+  for (int e = 0; e < 8; ++e) {
+    rem[e] = x[e];
+    // one fp32 value from here on: folded into the operation that made x, the
+    // fp16 conversion stored and the one subtracted were rounded from
+    // different values and a step apart for one element in 10^5
+    asm("" : "+v"(rem[e]));
+  }
 #pragma unroll
   for (int q = 0; q < parts_of<kF16>(); ++q)
 #pragma unroll
@@ -292,7 +298,8 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
   for (int p = 1; p < splits; ++p) s += part[(((int64_t)p * 2 + w) * M + m) * r + j];
   P[(w * M + m) * r + j] = s;
   if (split) {
-    const float v = scale * s;
+    float v = scale * s;
+    asm("" : "+v"(v));  // one value for both conversions (split8)
     const uint16_t hi = to16<kF16>(v);
     split[m * xc + w * 2 * r + j] = hi;
     split[m * xc + w * 2 * r + r + j] = to16<kF16>(v - from16<kF16>(hi));

@@ -142,6 +142,24 @@ def test_levels_of_each_weight(q, m, n):
     _check_fwd(q, block, X, s, q.gated_fwd(*block[:2], X, *block[2:], s), BF)
 
 
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_adapter_gradients_hold_fp32(q, dt):
+    """The adapter gradients keep the unrounded dG and dU: 24 bits (22 in fp16)
+    of each and of T and P, a few fp32 operations each and sums over at most
+    1088 terms, so an element misses by a few 2^-22 of its terms, and one lost
+    low part (2^-12 of one dG, 5e-6 of the norm here) shows."""
+    m, n, k, r, s = 300, 1030, 1088, 12, 0.5
+    b = _block(q, n, k, r, dt, seed=5)
+    X = _normal((m, k), 1.0, dt, 50, 0)
+    G, U, dH = (_normal((m, n), 1.0, dt, 50, 1 + i) for i in range(3))
+    T = torch.stack([X.float() @ b[2].float().T, X.float() @ b[4].float().T])
+    out = q.gated_bwd(*b[:2], X, T, G, U, dH, *b[2:], s, need_dX=False)
+    W = np.zeros((n, k))
+    ref = omlp.gated_bwd(_f64(X), W, W, _f64(G), _f64(U), _f64(dH), *(_f64(t) for t in b[2:]), s)
+    for name, got, want in zip(("dAg", "dBg", "dAu", "dBu"), out[1:], ref[1:]):
+        assert report(name, f32(got), want, floor=False) <= 2.0 ** -20
+
+
 def test_streamed_activations(q):
     """Activations above 128 MB (the mirrored buffer rotation), forward and dX,
     against fp32 on the GPU on sampled rows."""
