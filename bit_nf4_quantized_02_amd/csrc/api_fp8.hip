@@ -30,21 +30,26 @@ bool fwd_fits(int64_t M, int64_t n, int64_t k, int r) {
 }
 
 struct FwdWs {
-  void* gv = nullptr;      // M <= 16: activations in the GEMV's operand order
-  float* T = nullptr;      // M <= 16 without T_save
-  uint8_t* xq = nullptr;   // M > 16: activation codes and scale words
+  uint8_t* xq = nullptr;   // activation codes and scales
   uint8_t* xs = nullptr;
+  float* proj = nullptr;   // partials of T
+  float* T = nullptr;      // M <= 16: T where its partials are too many for the GEMV to add
   uint16_t* TS = nullptr;  // low-rank operand columns
   uint16_t* Bx = nullptr;
-  void* proj = nullptr;
   float* part = nullptr;
 };
 
+// Few tokens: the GEMV adds T's partials itself while each of its workgroups
+// reads at most 16 KB of them (1 - 2 us in the shadow of its first loads); a
+// small kernel adds them before it otherwise (a launch, about 4 us).
+bool gemv_adds(int64_t M, int64_t k, int r) { return (int64_t)fp8_prep_plan(M, k, M <= 16).splits * M * r * 4 <= 16384; }
+
 size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
-  if (r > 0) o.proj = cv.take<char>(rowdot_ws_bytes(M, k, r));
+  o.proj = cv.take<float>((size_t)fp8_prep_plan(M, k, M <= 16).splits * M * r * 4);
   if (M <= 16) {
-    if (r > 0) o.T = cv.take<float>((size_t)M * r * 4);
-    o.gv = cv.take<char>(fp8_gemv_ws_bytes(k));
+    o.xq = cv.take<uint8_t>(fp8_gemv_codes_bytes(k));
+    o.xs = cv.take<uint8_t>(fp8_gemv_scale_bytes(k));
+    o.T = cv.take<float>((size_t)M * r * 4);
     return cv.used;
   }
   o.xq = cv.take<uint8_t>((size_t)M * f8_pad(k));
@@ -63,9 +68,10 @@ struct BwdWs {
   uint8_t* wt = nullptr;   // the weight's codes as [k, n]
   uint16_t* US = nullptr;
   uint16_t* Ax = nullptr;
+  uint16_t* Bt = nullptr;  // B rank-major
   float* U = nullptr;
   float* T = nullptr;
-  void* proj = nullptr;
+  float* proj = nullptr;
   void* grad = nullptr;
   float* part = nullptr;
 };
@@ -77,10 +83,11 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
   if (r > 0) {
     o.US = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
     o.Ax = cv.take<uint16_t>((size_t)k * lora_extra_cols(r) * 2);
+    o.Bt = cv.take<uint16_t>((size_t)r * f8_pad(n) * 2);
     o.U = cv.take<float>((size_t)M * r * 4);
     o.T = cv.take<float>((size_t)M * r * 4);
-    const size_t p1 = rowdot_ws_bytes(M, n, r), p2 = rowdot_ws_bytes(M, k, r);
-    o.proj = cv.take<char>(p1 > p2 ? p1 : p2);
+    const size_t p1 = (size_t)fp8_prep_plan(M, n, false).splits * M * r * 4, p2 = rowdot_ws_bytes(M, k, r);
+    o.proj = cv.take<float>(p1 > p2 ? p1 : p2);
     const size_t g1 = coldot_ws_bytes(M, k, r), g2 = coldot_ws_bytes(M, n, r);
     o.grad = cv.take<char>(g1 > g2 ? g1 : g2);
   }
@@ -145,21 +152,25 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int6
   const bool f16 = dtype == QLORA_DT_FP16;
   const uint16_t *x = static_cast<const uint16_t*>(X), *a = static_cast<const uint16_t*>(A),
                  *b = static_cast<const uint16_t*>(B);
-  float* const proj = static_cast<float*>(o.proj);
-  hipError_t e = hipSuccess;
-  if (M <= 16) {
-    float* const T = T_save ? T_save : o.T;
-    if (r > 0) e = launch_rowdot(x, M, k, a, 0, r, T, nullptr, scale, proj, st, nullptr, f16);
-    if (e == hipSuccess)
-      e = launch_fp8_gemv(view8(w), x, M, T, b, r, scale, static_cast<uint16_t*>(Y), o.gv, st, f16);
+  const bool few = M <= 16;
+  const int parts = fp8_prep_plan(M, k, few).splits;
+  hipError_t e = launch_fp8_prep(x, M, k, a, k, r, o.xq, o.xs, o.proj, few, st, f16);
+  if (few) {
+    if (r > 0 && !gemv_adds(M, k, r)) {
+      float* const T = T_save ? T_save : o.T;
+      if (e == hipSuccess) e = launch_rowdot_finalize(o.proj, parts, M, r, T, nullptr, scale, st, f16);
+      if (e == hipSuccess)
+        e = launch_fp8_gemv(view8(w), o.xq, o.xs, M, T, 1, b, r, scale, static_cast<uint16_t*>(Y), nullptr, st, f16);
+    } else if (e == hipSuccess) {
+      e = launch_fp8_gemv(view8(w), o.xq, o.xs, M, o.proj, parts, b, r, scale, static_cast<uint16_t*>(Y), T_save, st, f16);
+    }
     return hip_status(e);
   }
   const int64_t nb = f8_pad(k) / kF8Block;
   if (r > 0) {
-    e = launch_rowdot(x, M, k, a, 0, r, T_save, o.TS, scale, proj, st, nullptr, f16);
+    if (e == hipSuccess) e = launch_rowdot_finalize(o.proj, parts, M, r, T_save, o.TS, scale, st, f16);
     if (e == hipSuccess) e = launch_lowrank_rows(b, n, r, o.Bx, st);
   }
-  if (e == hipSuccess) e = launch_fp8_rows(x, M, k, o.xq, o.xs, st, f16);
   if (e == hipSuccess)
     e = launch_gemm_fp8(o.xq, o.xs, M, k, o.TS, lora_extra_cols(r), w->codes, w->scale, nb, 1,
                         (f8_pad(n) / kF8Block) * nb, o.Bx, n, static_cast<uint16_t*>(Y), o.part, st, f16);
@@ -198,11 +209,18 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
   const bool f16 = dtype == QLORA_DT_FP16;
   const uint16_t *x = static_cast<const uint16_t*>(X), *dy = static_cast<const uint16_t*>(dY),
                  *a = static_cast<const uint16_t*>(A), *b = static_cast<const uint16_t*>(B);
-  float *const proj = static_cast<float*>(o.proj), *const grad = static_cast<float*>(o.grad);
-  if (r > 0 && (dX || dA)) e = launch_rowdot(dy, M, n, b, 1, r, o.U, dX ? o.US : nullptr, scale, proj, st, nullptr, f16);
+  float* const grad = static_cast<float*>(o.grad);
+  if (dX || dA) {
+    const int64_t np = f8_pad(n);
+    if (r > 0) e = launch_rank_major(b, nullptr, n, r, np, o.Bt, st);
+    if (e == hipSuccess)
+      e = launch_fp8_prep(dy, M, n, o.Bt, np, r, dX ? o.yq : nullptr, o.ys, o.proj, false, st, f16);
+    if (e == hipSuccess && r > 0)
+      e = launch_rowdot_finalize(o.proj, fp8_prep_plan(M, n, false).splits, M, r, o.U, dX ? o.US : nullptr, scale, st,
+                                 f16);
+  }
   if (dX) {
     if (e == hipSuccess && r > 0) e = launch_lowrank_rows_t(a, r, k, o.Ax, st);
-    if (e == hipSuccess) e = launch_fp8_rows(dy, M, n, o.yq, o.ys, st, f16);
     if (e == hipSuccess) e = launch_fp8_transpose(view8(w), o.wt, st);
     const int64_t kb = f8_pad(k) / kF8Block;
     if (e == hipSuccess)
@@ -213,7 +231,7 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
   if (e == hipSuccess && dB) {
     const float* T = T_saved;
     if (T == nullptr) {
-      e = launch_rowdot(x, M, k, a, 0, r, o.T, nullptr, scale, proj, st, nullptr, f16);
+      e = launch_rowdot(x, M, k, a, 0, r, o.T, nullptr, scale, o.proj, st, nullptr, f16);
       T = o.T;
     }
     if (e == hipSuccess) e = launch_coldot(dy, M, n, T, r, scale, dB, r, 1, accumulate, grad, st, nullptr, f16, /*fine=*/true);

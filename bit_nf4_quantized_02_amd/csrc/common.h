@@ -192,6 +192,28 @@ __device__ __forceinline__ u32x4 apply_mask8(u32x4 v, uint2 mk) {
   return o;
 }
 
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+
+// Eight 16-bit values at (row, c) of a [*, n] matrix, zero past n. kVec: rows
+// of a multiple of 8 elements; else a load of any alignment inside the row and
+// single elements at its end.
+template <bool kVec>
+__device__ __forceinline__ u32x4 load8h(const uint16_t* __restrict__ row, int64_t c, int64_t n) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if constexpr (kVec) {
+    if (c < n) v = *reinterpret_cast<const u32x4*>(row + c);
+  } else if (c + 8 <= n) {
+    v = *reinterpret_cast<const u32x4_any*>(row + c);
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = c + i < n ? (uint32_t)row[c + i] : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = e[2 * i] | (e[2 * i + 1] << 16);
+  }
+  return v;
+}
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 

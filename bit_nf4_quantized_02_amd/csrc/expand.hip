@@ -224,7 +224,34 @@ __global__ __launch_bounds__(256) void lowrank_rows_t_kernel(const uint16_t* __r
   out[c * cpr + blockIdx.y] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
 }
 
+// B [n, r] -> rank-major rows [r, ld], zero from n on: 64 x 64 tiles turned
+// through LDS, so that both sides move in runs.
+__global__ __launch_bounds__(256) void rank_major_kernel(const uint16_t* __restrict__ B0, const uint16_t* __restrict__ B1,
+                                                         int64_t n, int r, int64_t ld, uint16_t* __restrict__ out) {
+  const uint16_t* const B = blockIdx.z == 0 ? B0 : B1;
+  out += blockIdx.z * r * ld;
+  __shared__ uint16_t tile[64][65];
+  const int64_t c0 = (int64_t)blockIdx.x * 64;
+  const int j0 = (int)blockIdx.y * 64;
+  const int nj = r - j0 < 64 ? r - j0 : 64;
+  for (int i = threadIdx.x; i < 64 * nj; i += 256) {
+    const int c = i / nj, j = i % nj;
+    tile[c][j] = c0 + c < n ? B[(c0 + c) * r + j0 + j] : (uint16_t)0;
+  }
+  __syncthreads();
+  const int c = threadIdx.x & 63;
+  if (c0 + c >= ld) return;
+  for (int j = threadIdx.x >> 6; j < nj; j += 4) out[(int64_t)(j0 + j) * ld + c0 + c] = tile[c][j];
+}
+
 }  // namespace
+
+hipError_t launch_rank_major(const uint16_t* B, const uint16_t* B1, int64_t n, int r, int64_t ld, uint16_t* out,
+                             hipStream_t stream) {
+  const dim3 grid((unsigned)cdiv(ld, (int64_t)64), (unsigned)cdiv(r, 64), B1 ? 2 : 1);
+  rank_major_kernel<<<grid, 256, 0, stream>>>(B, B1, n, r, ld, out);
+  return hipGetLastError();
+}
 
 hipError_t launch_lowrank_rows_t(const uint16_t* A, int r, int64_t k, uint16_t* out, hipStream_t stream) {
   const int xc = lora_extra_cols(r);

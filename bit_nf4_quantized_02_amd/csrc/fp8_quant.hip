@@ -1,12 +1,16 @@
 // Encoding into the 8-bit format and back (fp8.h): weights in 128 x 128
-// tiles, activations in runs of 128 along a row. All four kernels here are
-// bound by HBM: one pass, every value read once and written once.
+// tiles, activations in runs of 128 along a row. The kernels here are bound by
+// HBM: one pass, every value read once and written once.
+#include <type_traits>
+
 #include "fp8.h"
 #include "kernels.h"
 
 namespace qlora {
 
 namespace {
+
+constexpr int kPrepRows = 128;  // activation rows per workgroup of fp8_prep_kernel
 
 // 8 consecutive elements of a row as fp32, zero from element `lim` on.
 // kDt: 0 bf16, 1 fp32, 2 fp16. kVec: 16-byte aligned rows.
@@ -98,32 +102,154 @@ __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restri
   p[1] = o[1];
 }
 
-// Activations X [M, C] -> codes [M, Cp] (zero past C) and scales for the GEMM:
-// one 32-bit word per (128-column block, 128-row tile, row % 32) holding the
-// bytes of rows +0, +32, +64, +96, so that a wave of the GEMM gets the scales
-// of its four 32-row operand blocks with one load and picks each by the
-// instruction's byte select. 16 threads per block of 128.
-template <bool kF16, bool kVec>
-__global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t C, int64_t Cp,
-                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scale) {
-  const int64_t u = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // (row, block)
-  const int64_t nb = Cp / kF8Block;
-  const int64_t m = u / nb, kb = u % nb;
-  if (m >= M) return;
-  const int64_t c = kb * kF8Block + (threadIdx.x & 15) * 8;
-  float f[8];
-  load8f<kF16 ? 2 : 0, kVec>(X, m * C, c, C, f);
-  uint32_t a = 0;
+// Activations: one pass over P [M, C] that encodes it and forms its low-rank
+// projection P Q^T (Q rank-major [r, ldq], kRP ranks at most; 0: none) --
+// X with A in the forward, dY with B^T in the backward. A lane holds 32
+// consecutive columns of one row of a 128-column block (lane: row lane % 16,
+// columns 32 (lane / 16) ..): a block's maximum is four lanes' maximum, its
+// codes leave in 32-byte pieces, and its four groups of 8 columns are the A
+// operands of v_mfma_f32_16x16x32 over a permuted contraction that Q's
+// operands, loaded the same way, share.
+//   kFew = false: codes [M, Cp] (zero past C) and the GEMM's scale words, one
+// per (128-column block, 128-row tile, row % 32) with the bytes of rows +0,
+// +32, +64, +96, so that a wave of the GEMM gets the scales of its four
+// 32-row operand blocks with one load. A wave holds 32 rows; the workgroup's
+// four share Q's lines in L1 and walk the blocks of one column range.
+//   kFew = true (M <= 16): codes in the GEMV's operand order [block][lane][32
+// bytes] (zeros past M), scales [block][16]; the four waves take the range's
+// blocks in turn and their projections are added in wave order.
+// Partials of the projection go to part [range][M][r]; codes NULL: only those.
+template <int kRP, bool kF16, bool kVec, bool kFew>
+__global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restrict__ P, int64_t M, int64_t C, int64_t Cp,
+                                                       const uint16_t* __restrict__ Q, int64_t ldq, int r, int bchunk,
+                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scale,
+                                                       float* __restrict__ part) {
+  constexpr int kTiles = kRP / 16, kTA = kTiles > 0 ? kTiles : 1;
+  constexpr int kMR = kFew ? 1 : 2;
+  typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 15, co = 32 * (lane >> 4);
+  const int64_t m0 = kFew ? 0 : (int64_t)blockIdx.x * kPrepRows + wave * 16 * kMR;
+  if (!kFew && m0 >= M) return;
+  const int nb = (int)(Cp / kF8Block);
+  const int b0 = (int)blockIdx.y * bchunk, b1 = b0 + bchunk < nb ? b0 + bchunk : nb;
+  constexpr int kStep = kFew ? 4 : 1;
+  const int64_t mt = cdiv(M, (int64_t)kF8Block);
+  const uint16_t* prow[kMR];
+  const uint16_t* qrow[kTA];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a = max(a, f8_finite_abs(f[e]));
+  for (int i = 0; i < kMR; ++i) prow[i] = P + (m0 + 16 * i + row < M ? m0 + 16 * i + row : M - 1) * C;
 #pragma unroll
-  for (int d = 1; d < 16; d *= 2) a = max(a, (uint32_t)__shfl_xor((int)a, d));
-  const uint32_t b = f8_scale_byte(a);
-  const float inv = f8_inv_scale(b);
-  *reinterpret_cast<u32x2*>(codes + m * Cp + c) = u32x2{f8_pack4(f, inv), f8_pack4(f + 4, inv)};
-  if ((threadIdx.x & 15) == 0) {
-    const int64_t mt = cdiv(M, (int64_t)kF8Block);
-    scale[((kb * mt + m / kF8Block) * 32 + (m & 31)) * 4 + ((m >> 5) & 3)] = (uint8_t)b;
+  for (int t = 0; t < kTiles; ++t) qrow[t] = Q + (int64_t)(16 * t + row < r ? 16 * t + row : r - 1) * ldq;
+  f32x4 acc[kMR][kTA];
+#pragma unroll
+  for (int i = 0; i < kMR; ++i)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto load = [&](int kb, u32x4 (&x)[kMR][4]) {
+    const int64_t c = (int64_t)kb * kF8Block + co;
+    if ((int64_t)(kb + 1) * kF8Block <= C) {  // (uniform: no load behind a test of its own)
+#pragma unroll
+      for (int i = 0; i < kMR; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[i][s] = *reinterpret_cast<const Vec*>(prow[i] + c + 8 * s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMR; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[i][s] = load8h<kVec>(prow[i], c + 8 * s, C);
+    }
+  };
+  u32x4 x[kMR][4], nx[kMR][4];
+  const int kb0 = kFew ? b0 + wave : b0;
+  if (kb0 < b1) load(kb0, x);
+  for (int kb = kb0; kb < b1; kb += kStep) {
+    u32x4 q[kTA][4];
+    const int64_t c = (int64_t)kb * kF8Block + co;
+    if ((int64_t)(kb + 1) * kF8Block <= ldq) {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) q[t][s] = *reinterpret_cast<const u32x4*>(qrow[t] + c + 8 * s);
+    } else {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) q[t][s] = load8h<true>(qrow[t], c + 8 * s, ldq);
+    }
+    load(kb + kStep < b1 ? kb + kStep : kb, nx);
+#pragma unroll
+    for (int i = 0; i < kMR; ++i) {
+      if (kFew && row >= M) x[i][0] = x[i][1] = x[i][2] = x[i][3] = u32x4{0u, 0u, 0u, 0u};
+      if (codes != nullptr) {
+        float f[32];
+        uint32_t a = 0;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[8 * s + 2 * e] = from16<kF16>(x[i][s][e] & 0xFFFFu);
+            f[8 * s + 2 * e + 1] = from16<kF16>(x[i][s][e] >> 16);
+          }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) a = max(a, f8_finite_abs(f[e]));
+        a = max(a, (uint32_t)__shfl_xor((int)a, 16));
+        a = max(a, (uint32_t)__shfl_xor((int)a, 32));
+        const uint32_t b = f8_scale_byte(a);
+        const float inv = f8_inv_scale(b);
+        u32x4 o[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][e] = f8_pack4(f + 16 * h + 4 * e, inv);
+        const int64_t m = m0 + 16 * i + row;
+        if constexpr (kFew) {
+          u32x4* const d = reinterpret_cast<u32x4*>(codes) + ((int64_t)kb * 64 + lane) * 2;
+          d[0] = o[0];
+          d[1] = o[1];
+          if (lane < 16) scale[kb * 16 + lane] = (uint8_t)b;
+        } else if (m < M) {
+          u32x4* const d = reinterpret_cast<u32x4*>(codes + m * Cp + c);
+          d[0] = o[0];
+          d[1] = o[1];
+          if (lane < 16) scale[((kb * mt + m / kF8Block) * 32 + (m & 31)) * 4 + ((m >> 5) & 3)] = (uint8_t)b;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+          acc[i][t] = mfma16<kF16>(__builtin_bit_cast(bf16x8, x[i][s]), __builtin_bit_cast(bf16x8, q[t][s]), acc[i][t]);
+    }
+#pragma unroll
+    for (int i = 0; i < kMR; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) x[i][s] = nx[i][s];
+  }
+  // D layout: lane -> rank lane % 16, rows 4 (lane / 16) + v
+  if constexpr (kRP > 0 && kFew) {
+    __shared__ float red[4][16][kRP];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red[wave][4 * (lane >> 4) + v][16 * t + row] = acc[0][t][v];
+    __syncthreads();
+    for (int o = threadIdx.x; o < (int)M * r; o += 256) {
+      const int m = o / r, j = o % r;
+      part[((int64_t)blockIdx.y * M + m) * r + j] = red[0][m][j] + red[1][m][j] + red[2][m][j] + red[3][m][j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kMR; ++i)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t m = m0 + 16 * i + 4 * (lane >> 4) + v;
+          const int j = 16 * t + row;
+          if (m < M && j < r) part[((int64_t)blockIdx.y * M + m) * r + j] = acc[i][t][v];
+        }
   }
 }
 
@@ -177,17 +303,40 @@ size_t fp8_rows_scale_bytes(int64_t M, int64_t C) {
   return (size_t)(f8_pad(C) / kF8Block) * (size_t)f8_pad(M);
 }
 
-hipError_t launch_fp8_rows(const uint16_t* X, int64_t M, int64_t C, uint8_t* codes, uint8_t* scale, hipStream_t stream,
-                           bool f16) {
+// Column ranges: about 1024 workgroups; few rows: about 32 (their projections'
+// partials are added by every workgroup of the GEMV).
+Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few) {
+  const int64_t nb = f8_pad(C) / kF8Block;
+  int64_t s = few ? cdiv(nb, (int64_t)4) : cdiv((int64_t)1024, cdiv(M, (int64_t)kPrepRows));
+  if (s > nb) s = nb;
+  if (s > 32) s = 32;
+  const int64_t chunk = cdiv(nb, s);
+  return Fp8Prep{(int)chunk, (int)cdiv(nb, chunk)};
+}
+
+hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int64_t ldq, int r,
+                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16) {
+  const Fp8Prep pl = fp8_prep_plan(M, C, few);
   const int64_t Cp = f8_pad(C);
-  const unsigned grid = (unsigned)cdiv(M * (Cp / kF8Block), (int64_t)16);
-#define QLORA_F8R(H, V) fp8_rows_kernel<H, V><<<grid, 256, 0, stream>>>(X, M, C, Cp, codes, scale)
-  if (C % 8 == 0) {
-    if (f16) QLORA_F8R(true, true); else QLORA_F8R(false, true);
-  } else {
-    if (f16) QLORA_F8R(true, false); else QLORA_F8R(false, false);
+  if (few && (C % 8 != 0 || M > 16)) return hipErrorInvalidValue;
+  const dim3 grid(few ? 1u : (unsigned)cdiv(M, (int64_t)kPrepRows), (unsigned)pl.splits);
+#define QLORA_PREP3(RP, H, V, F) \
+  fp8_prep_kernel<RP, H, V, F><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, ldq, r, pl.chunk, codes, scale, part)
+#define QLORA_PREP2(RP, H)                                                                             \
+  {                                                                                                    \
+    if (few) QLORA_PREP3(RP, H, true, true);                                                           \
+    else if (C % 8 == 0) QLORA_PREP3(RP, H, true, false);                                              \
+    else QLORA_PREP3(RP, H, false, false);                                                             \
   }
-#undef QLORA_F8R
+#define QLORA_PREP(RP) { if (f16) QLORA_PREP2(RP, true) else QLORA_PREP2(RP, false) }
+  if (r == 0) QLORA_PREP(0)
+  else if (r <= 16) QLORA_PREP(16)
+  else if (r <= 32) QLORA_PREP(32)
+  else if (r <= 64) QLORA_PREP(64)
+  else QLORA_PREP(128)
+#undef QLORA_PREP
+#undef QLORA_PREP2
+#undef QLORA_PREP3
   return hipGetLastError();
 }
 

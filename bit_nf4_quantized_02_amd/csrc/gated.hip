@@ -11,6 +11,8 @@
 // parts: three bf16 parts hold all 24 bits, two fp16 parts 22. Neither G and U
 // nor dG and dU are kept in fp32: the two kernels that need them compute them
 // again from the 16-bit G, U and dH, which is fewer bytes than reading parts.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -101,38 +103,20 @@ __global__ __launch_bounds__(256) void gated_expand_kernel(PairView wg, PairView
 
 // ------------------------------------------------------------------ the join
 
-// sigma(g) to about 1 ulp without expf's range handling: e^-g as 2^t with the
-// rounding error of t = -g log2 e put back. Beyond |t| = 126 the correction is
-// dropped (2^t there is 0 or leaves sigma 0).
+// sigma(g) from the hardware's 2^x and reciprocal (1 ulp each): the product -g
+// log2 e carries half an ulp of itself into the exponent, 2^-24 |g| of sigma's
+// tail, where sigma is small (13 instructions with both errors taken out
+// against 4; the gradients' 2e-7 does not change). e^-g overflows to infinity
+// for large negative g, where sigma is then 0, as it should be.
 __device__ __forceinline__ float fast_sigmoid(float g) {
-  const float t = -g * 1.44269504f;
-  const float lo = fmaf(-g, 1.44269504f, -t) + -g * 1.92596303e-8f;
-  const float e = __builtin_amdgcn_exp2f(t);
-  const float d = 1.0f + (fabsf(t) < 126.0f ? fmaf(e, lo * 0.693147182f, e) : e);
-  float y = __builtin_amdgcn_rcpf(d);
-  return d < 8.0e37f ? fmaf(fmaf(-d, y, 1.0f), y, y) : y;
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
 }
 
+// dg = dh u (sg + silu (1 - sg)), du = dh silu, silu = g sg
 __device__ __forceinline__ void join_bwd(float g, float u, float dh, float& dg, float& du) {
-  const float sg = fast_sigmoid(g);
-  dg = dh * u * (sg * (1.0f + g * (1.0f - sg)));
-  du = dh * (g * sg);
-}
-
-// Eight 16-bit values at (row, c) of a [*, n] matrix, zero past n.
-template <bool kVec>
-__device__ __forceinline__ u32x4 load8h(const uint16_t* __restrict__ row, int64_t c, int64_t n) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if constexpr (kVec) {
-    if (c < n) v = *reinterpret_cast<const u32x4*>(row + c);
-  } else {
-    uint32_t e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = c + i < n ? (uint32_t)row[c + i] : 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = e[2 * i] | (e[2 * i + 1] << 16);
-  }
-  return v;
+  const float sg = fast_sigmoid(g), si = g * sg;
+  dg = dh * u * fmaf(si, 1.0f - sg, sg);
+  du = dh * si;
 }
 
 // Eight fp32 values -> kParts 16-bit parts whose sum holds 24 (bf16, three)
@@ -172,16 +156,6 @@ __device__ __forceinline__ void join8(const u32x4& g, const u32x4& u, const u32x
                from16<kF16>((dh[w] >> (16 * h)) & 0xFFFFu), dg[2 * w + h], du[2 * w + h]);
 }
 
-// B [n, r] -> Bt [rp, np]: rank-major rows for the join's operand (zero past r and n).
-__global__ __launch_bounds__(256) void gated_bt_kernel(const uint16_t* __restrict__ Bg, const uint16_t* __restrict__ Bu,
-                                                       int64_t n, int64_t np, int r, int rp, uint16_t* __restrict__ out) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int j = blockIdx.y;
-  if (c >= np) return;
-  const uint16_t* const B = blockIdx.z == 0 ? Bg : Bu;
-  out[((int64_t)blockIdx.z * rp + j) * np + c] = j < r && c < n ? B[c * r + j] : (uint16_t)0;
-}
-
 constexpr int kJoinMR = 2;     // 16-row tiles per wave
 constexpr int kJoinWaves = 4;  // each with rows of its own: the four share B's lines in L1
 constexpr int kJoinRows = 16 * kJoinMR * kJoinWaves;
@@ -198,6 +172,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
     float* __restrict__ part) {
   constexpr int kTiles = kRP / 16;
   constexpr int kP = parts_of<kF16>();
+  typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t m0 = (int64_t)blockIdx.x * kJoinRows + wave * 16 * kJoinMR;
@@ -211,6 +186,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
     const int64_t m = m0 + 16 * i + (lane & 15);
     off[i] = (m < M ? m : M - 1) * n;
   }
+  const uint16_t* brow[kTiles > 0 ? kTiles : 1];  // (ranks past r repeat the last one; not stored)
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int j = 16 * t + (lane & 15);
+    brow[t] = Bt + (int64_t)(j < r ? j : r - 1) * np + co;
+  }
   f32x4 acc[2][kJoinMR][kTiles > 0 ? kTiles : 1];
 #pragma unroll
   for (int w = 0; w < 2; ++w)
@@ -221,24 +202,37 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
   struct Stage {
     u32x4 g[kJoinMR], u[kJoinMR], d[kJoinMR];
   };
+  // whole steps load without a test per lane (a test would put each load behind
+  // a branch that waits for it)
   auto load = [&](int64_t c, Stage& s) {
+    if (c + 32 <= n) {
 #pragma unroll
-    for (int i = 0; i < kJoinMR; ++i) {
-      s.g[i] = load8h<kVec>(G + off[i], c + co, n);
-      s.u[i] = load8h<kVec>(U + off[i], c + co, n);
-      s.d[i] = load8h<kVec>(dH + off[i], c + co, n);
+      for (int i = 0; i < kJoinMR; ++i) {
+        s.g[i] = *reinterpret_cast<const Vec*>(G + off[i] + c + co);
+        s.u[i] = *reinterpret_cast<const Vec*>(U + off[i] + c + co);
+        s.d[i] = *reinterpret_cast<const Vec*>(dH + off[i] + c + co);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kJoinMR; ++i) {
+        s.g[i] = load8h<kVec>(G + off[i], c + co, n);
+        s.u[i] = load8h<kVec>(U + off[i], c + co, n);
+        s.d[i] = load8h<kVec>(dH + off[i], c + co, n);
+      }
     }
   };
   Stage cur, nxt;
   load(cbeg, cur);
   for (int64_t c = cbeg; c < cend; c += 32) {
-    load(c + 32 < cend ? c + 32 : c, nxt);
+    // B's rows first: waiting for them must not wait for the next step's loads
     u32x4 b[2][kTiles > 0 ? kTiles : 1];
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
-        b[w][t] = *reinterpret_cast<const u32x4*>(Bt + ((int64_t)w * kRP + 16 * t + (lane & 15)) * np + c + co);
+        b[w][t] = *reinterpret_cast<const u32x4*>(brow[t] + w * r * np + c);
+    load(c + 32 < cend ? c + 32 : c, nxt);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < kJoinMR; ++i) {
       float dg[8], du[8];
@@ -341,6 +335,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
                                                        const uint16_t* __restrict__ Tt, int64_t Mp, int r,
                                                        int64_t mchunk, float* __restrict__ part) {
   constexpr int kP = parts_of<kF16>();
+  typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
   constexpr int kJTall = kRP / 16;
   constexpr int kWJ = kJTall >= 4 ? 4 : kJTall;     // waves along ranks
   constexpr int kWC = 4 / kWJ;                      // waves along columns
@@ -358,16 +353,23 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
   struct Stage {
     u32x4 g, u, d;
   };
+  const bool inside = c0 + kDbCols <= n;
   auto load = [&](int64_t mb, Stage& s) {
     const int64_t m = mb + prow;
     const int64_t o = (m < m1 ? m : m1 - 1) * n;
-    s.g = load8h<kVec>(G + o, pc, n);
-    s.u = load8h<kVec>(U + o, pc, n);
-    s.d = load8h<kVec>(dH + o, pc, n);
-    if (m >= m1) s.d = u32x4{0u, 0u, 0u, 0u};
-    if (m >= m1) s.g = s.u = s.d;  // rows past the range add nothing, whatever the last row holds
+    if (inside) {
+      s.g = *reinterpret_cast<const Vec*>(G + o + pc);
+      s.u = *reinterpret_cast<const Vec*>(U + o + pc);
+      s.d = *reinterpret_cast<const Vec*>(dH + o + pc);
+    } else {
+      s.g = load8h<kVec>(G + o, pc, n);
+      s.u = load8h<kVec>(U + o, pc, n);
+      s.d = load8h<kVec>(dH + o, pc, n);
+    }
   };
-  auto stage = [&](int set, const Stage& s) {
+  // (rows past the range add nothing, whatever the row read in their place holds)
+  auto stage = [&](int set, int64_t mb, Stage& s) {
+    if (mb + 32 > m1 && mb + prow >= m1) s.g = s.u = s.d = u32x4{0u, 0u, 0u, 0u};
     float dg[8], du[8];
     join8<kF16>(s.g, s.u, s.d, dg, du);
     u32x4 p[kP];
@@ -389,7 +391,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
   Stage st;
   if (m0 < m1) {
     load(m0, st);
-    stage(0, st);
+    stage(0, m0, st);
     load(m0 + 32 < m1 ? m0 + 32 : m0, st);
   }
   __syncthreads();
@@ -404,7 +406,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
         for (int a = 0; a < kJT; ++a)
           ta[w][q][a] = *reinterpret_cast<const u32x4*>(
               Tt + (((int64_t)q * 2 + w) * kRP + 16 * (wj * kJT + a) + (lane & 15)) * Mp + mb + 8 * (lane >> 4));
-    if (mb + 32 < m1) stage(set ^ 1, st);
+    if (mb + 32 < m1) stage(set ^ 1, mb + 32, st);
     load(mb + 64 < m1 ? mb + 64 : m0, st);
 #pragma unroll
     for (int w = 0; w < 2; ++w)
@@ -458,7 +460,7 @@ __global__ __launch_bounds__(256) void gated_db_reduce_kernel(const float* __res
 int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
 // Column ranges of the join: about 1024 workgroups (each a multiple of 32
-// columns, at least 256).
+// columns, at least 64; at most 32 ranges, whose partials are added later).
 struct JoinPlan {
   int64_t cchunk;
   int splits;
@@ -467,7 +469,7 @@ struct JoinPlan {
 JoinPlan join_plan(int64_t M, int64_t n) {
   const int64_t np = gated_pad(n);
   int64_t s = cdiv((int64_t)1024, cdiv(M, (int64_t)kJoinRows));
-  if (s > cdiv(np, (int64_t)256)) s = cdiv(np, (int64_t)256);
+  if (s > np / 64) s = np / 64;
   if (s > 32) s = 32;
   const int64_t cchunk = cdiv(cdiv(np, s), (int64_t)32) * 32;
   return {cchunk, (int)cdiv(np, cchunk)};
@@ -531,7 +533,7 @@ hipError_t launch_gated_expand_dx(const Nf4View& g, const Nf4View& u, const uint
 
 size_t gated_join_ws_bytes(int64_t M, int64_t n, int r) {
   if (r == 0) return 0;
-  return align256((size_t)2 * rank_pad(r) * (size_t)gated_pad(n) * 2) +
+  return align256((size_t)2 * r * (size_t)gated_pad(n) * 2) +
          align256((size_t)join_plan(M, n).splits * 2 * (size_t)M * r * 4);
 }
 
@@ -542,9 +544,11 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
   const int64_t np = gated_pad(n);
   const int rp = rank_pad(r);
   uint16_t* const Bt = static_cast<uint16_t*>(ws);
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)2 * rp * (size_t)np * 2));
-  if (r > 0)
-    gated_bt_kernel<<<dim3((unsigned)cdiv(np, (int64_t)256), (unsigned)rp, 2), 256, 0, stream>>>(Bg, Bu, n, np, r, rp, Bt);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)2 * r * (size_t)np * 2));
+  if (r > 0) {
+    const hipError_t e = launch_rank_major(Bg, Bu, n, r, np, Bt, stream);
+    if (e != hipSuccess) return e;
+  }
   const dim3 grid((unsigned)cdiv(M, (int64_t)kJoinRows), (unsigned)pl.splits);
 #define QLORA_JOIN2(RP, H, V) \
   gated_join_kernel<RP, H, V><<<grid, 64 * kJoinWaves, 0, stream>>>(G, U, dH, M, n, np, Bt, r, pl.cchunk, D, part)

@@ -1,11 +1,12 @@
 // 8-bit layer for few tokens (M <= 16): one pass over the weight's codes.
 //
-//   Y = RN16( X8 W8^T + s T B^T ),   T = X A^T precomputed (fp32)
+//   Y = RN16( X8 W8^T + s T B^T )
 //
-// Bound by HBM: every code byte serves at most 16 tokens. A first small
-// kernel encodes X into the operand order of
-// v_mfma_scale_f32_16x16x128_f8f6f4 (per 128-column block and lane: 32 bytes
-// of one token row, zeros past M), so that the GEMV reads it in runs of 1 KB.
+// Bound by HBM: every code byte serves at most 16 tokens. fp8_prep_kernel has
+// encoded X into the operand order of v_mfma_scale_f32_16x16x128_f8f6f4 (per
+// 128-column block and lane: 32 bytes of one token row, zeros past M), so that
+// X is read in runs of 1 KB, and left T = X A^T in a few partials, which each
+// workgroup adds while its first codes are on the way (a launch less).
 // A workgroup owns 16 kT weight rows; its 8 waves take the 128-column blocks
 // in turn, so neighbouring waves read neighbouring lines of the same rows.
 // Codes go from memory to registers in operand order (a lane holds 32
@@ -23,41 +24,8 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kGvWaves = 8;
-constexpr int kU = 2;  // 128-column blocks per batch
-
-// One wave per 128-column block: lane (row lane % 16, columns 32 (lane / 16) ..)
-template <bool kF16>
-__global__ __launch_bounds__(256) void fp8_gemv_rows_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t C,
-                                                            int64_t nb, u32x4* __restrict__ Xq,
-                                                            uint8_t* __restrict__ Xs) {
-  const int lane = threadIdx.x & 63;
-  const int64_t kb = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (kb >= nb) return;
-  const int64_t m = lane & 15, c = kb * kF8Block + 32 * (lane >> 4);
-  float f[32];
-  uint32_t a = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (m < M && c < C) v = *reinterpret_cast<const u32x4*>(X + m * C + c + 8 * i);  // C % 64 == 0
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[8 * i + 2 * e] = from16<kF16>(v[e] & 0xFFFFu);
-      f[8 * i + 2 * e + 1] = from16<kF16>(v[e] >> 16);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 32; ++e) a = max(a, f8_finite_abs(f[e]));
-  a = max(a, (uint32_t)__shfl_xor((int)a, 16));
-  a = max(a, (uint32_t)__shfl_xor((int)a, 32));
-  const uint32_t b = f8_scale_byte(a);
-  const float inv = f8_inv_scale(b);
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    Xq[(kb * 64 + lane) * 2 + h] = u32x4{f8_pack4(f + 16 * h, inv), f8_pack4(f + 16 * h + 4, inv),
-                                         f8_pack4(f + 16 * h + 8, inv), f8_pack4(f + 16 * h + 12, inv)};
-  if (lane < 16) Xs[kb * 16 + lane] = (uint8_t)b;
-}
+constexpr int kU = 2;      // 128-column blocks per batch
+constexpr int kMaxR = 128;  // largest rank
 
 template <int kT>
 struct Batch {
@@ -74,12 +42,13 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
                                                                  const uint8_t* __restrict__ wscale, int64_t N,
                                                                  int64_t kp, const u32x4* __restrict__ Xq,
                                                                  const uint8_t* __restrict__ Xs, int64_t M,
-                                                                 const float* __restrict__ T,
+                                                                 const float* __restrict__ T, int parts,
                                                                  const uint16_t* __restrict__ B, int r, float scale,
-                                                                 uint16_t* __restrict__ Y) {
+                                                                 uint16_t* __restrict__ Y, float* __restrict__ T_save) {
   constexpr int NT = 16 * kT;
   __shared__ float red[kGvWaves][kT][16][16];
   __shared__ float lred[kT][16][16];
+  __shared__ float Ts[16 * kMaxR];  // T [M][r]
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * NT;
@@ -125,6 +94,12 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
   const int cnt = (nb + kGvWaves * kU - 1) / (kGvWaves * kU);  // batches
   Batch<kT> b0, b1;
   load(0, b0);
+  for (int o = t; o < (int)M * r; o += 64 * kGvWaves) {
+    float s = T[o];
+    for (int p = 1; p < parts; ++p) s += T[(int64_t)p * M * r + o];
+    Ts[o] = s;
+    if (T_save != nullptr && blockIdx.x == 0) T_save[o] = s;
+  }
   for (int j = 0; j < cnt; j += 2) {
     load(j + 1, b1);
     __builtin_amdgcn_sched_barrier(0);
@@ -139,6 +114,7 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
   for (int i = 0; i < kT; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v) red[wave][i][4 * (lane >> 4) + v][lane & 15] = acc[i][v];
+  __syncthreads();  // T
   if (r > 0 && wave < kT) {
     // L[m][n] = sum_j T[m][j] B[n][j], 4 ranks per fp32 MFMA (T and B exact)
     const int i = wave;
@@ -147,7 +123,7 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
     const int64_t n = n0 + i * 16 + (lane & 15);
     for (int j0 = 0; j0 < r; j0 += 4) {
       const int j = j0 + (lane >> 4);
-      const float a = (m < M && j < r) ? T[m * r + j] : 0.0f;
+      const float a = (m < M && j < r) ? Ts[m * r + j] : 0.0f;
       const float b = (n < N && j < r) ? from16<kF16>(B[n * r + j]) : 0.0f;
       l = __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, l, 0, 0, 0);
     }
@@ -170,24 +146,15 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
 
 }  // namespace
 
-size_t fp8_gemv_ws_bytes(int64_t k) {
-  const int64_t nb = f8_pad(k) / kF8Block;
-  return align256((size_t)nb * 2048) + align256((size_t)nb * 16);
-}
+size_t fp8_gemv_codes_bytes(int64_t k) { return (size_t)(f8_pad(k) / kF8Block) * 2048; }
+size_t fp8_gemv_scale_bytes(int64_t k) { return (size_t)(f8_pad(k) / kF8Block) * 16; }
 
-hipError_t launch_fp8_gemv(const Fp8View& w, const uint16_t* X, int64_t M, const float* T, const uint16_t* B, int r,
-                           float scale, uint16_t* Y, void* ws, hipStream_t stream, bool f16) {
-  const int64_t kp = f8_pad(w.k), nb = kp / kF8Block;
-  u32x4* const Xq = static_cast<u32x4*>(ws);
-  uint8_t* const Xs = static_cast<uint8_t*>(ws) + align256((size_t)nb * 2048);
-  const unsigned g0 = (unsigned)cdiv(nb, (int64_t)4);
-  if (f16)
-    fp8_gemv_rows_kernel<true><<<g0, 256, 0, stream>>>(X, M, w.k, nb, Xq, Xs);
-  else
-    fp8_gemv_rows_kernel<false><<<g0, 256, 0, stream>>>(X, M, w.k, nb, Xq, Xs);
+hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* xs, int64_t M, const float* T, int parts,
+                           const uint16_t* B, int r, float scale, uint16_t* Y, float* T_save, hipStream_t stream,
+                           bool f16) {
 #define QLORA_GV8(KT, H)                                                                                          \
   gemv_fp8_kernel<KT, H><<<(unsigned)cdiv(w.n, (int64_t)(16 * KT)), 64 * kGvWaves, 0, stream>>>(                   \
-      w.codes, w.scale, w.n, kp, Xq, Xs, M, T, B, r, scale, Y)
+      w.codes, w.scale, w.n, f8_pad(w.k), reinterpret_cast<const u32x4*>(xq), xs, M, T, parts, B, r, scale, Y, T_save)
   if (w.n >= 8192) {
     if (f16) QLORA_GV8(2, true); else QLORA_GV8(2, false);
   } else {

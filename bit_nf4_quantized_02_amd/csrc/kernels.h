@@ -58,6 +58,10 @@ hipError_t launch_rowdot(const uint16_t* P, int64_t M, int64_t C, const uint16_t
                          float* out, uint16_t* split, float scale, float* part, hipStream_t stream,
                          const uint8_t* pmask = nullptr, bool f16 = false, int split_cols = 0, int split_ld = 0);
 
+// out / split (as launch_rowdot's) from partials [ns][M][r], added in order.
+hipError_t launch_rowdot_finalize(const float* part, int ns, int64_t M, int r, float* out, uint16_t* split, float scale,
+                                  hipStream_t stream, bool f16);
+
 // Column reduction over M in fixed order, for the adapter gradients:
 //   G[c, j] (+)= scale * sum_m P[m, c] * Q[m, j]    P bf16 [M, C], Q fp32 [M, r]
 // written at G[c * g_sc + j * g_sj]. partial (fp32, [splits, C, r]) is workspace.
@@ -233,10 +237,20 @@ struct Fp8View {
 hipError_t launch_fp8_encode(const void* W, int dt, int64_t n, int64_t k, uint8_t* codes, uint8_t* scale,
                              hipStream_t stream);
 hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream);
-// Activations [M, C] -> codes [M, C up to 128] + scale words of the GEMM.
+// Activations P [M, C] -> codes and scales ([M, C up to 128] and the GEMM's
+// scale words; few, M <= 16: the GEMV's operand order, fp8_gemv_*_bytes),
+// and for r > 0 the partials [splits][M][r] of P Q^T, Q [r, ldq] rank-major
+// (ldq % 8 == 0; columns past C are not read or zero).
+struct Fp8Prep {
+  int chunk, splits;
+};
+Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few);
 size_t fp8_rows_scale_bytes(int64_t M, int64_t C);
-hipError_t launch_fp8_rows(const uint16_t* X, int64_t M, int64_t C, uint8_t* codes, uint8_t* scale, hipStream_t stream,
-                           bool f16);
+hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int64_t ldq, int r,
+                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16);
+// B [n, r] -> rank-major rows [r, ld], zero past n; B1's (not NULL) after them.
+hipError_t launch_rank_major(const uint16_t* B, const uint16_t* B1, int64_t n, int r, int64_t ld, uint16_t* out,
+                             hipStream_t stream);
 // The weight's codes as [k, n up to 128] rows for dX.
 hipError_t launch_fp8_transpose(const Fp8View& w, uint8_t* out, hipStream_t stream);
 // out = RN16([act | split] [f | fx]^T); f's scale byte of (output block,
@@ -246,10 +260,14 @@ size_t gemm_fp8_ws_bytes(int64_t M, int64_t kc, int64_t nout);
 hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int64_t kc, const uint16_t* split, int kx,
                            const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
                            const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16);
-// M <= 16: activations in the GEMV's operand order, then Y = RN16(X8 W8^T + scale T B^T).
-size_t fp8_gemv_ws_bytes(int64_t k);
-hipError_t launch_fp8_gemv(const Fp8View& w, const uint16_t* X, int64_t M, const float* T, const uint16_t* B, int r,
-                           float scale, uint16_t* Y, void* ws, hipStream_t stream, bool f16);
+// M <= 16: Y = RN16(X8 W8^T + scale T B^T) from launch_fp8_prep's operands; T
+// as `parts` partials [parts][M][r] that the kernel adds in order, written to
+// T_save if it is not NULL.
+size_t fp8_gemv_codes_bytes(int64_t k);
+size_t fp8_gemv_scale_bytes(int64_t k);
+hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* xs, int64_t M, const float* T, int parts,
+                           const uint16_t* B, int r, float scale, uint16_t* Y, float* T_save, hipStream_t stream,
+                           bool f16);
 
 hipError_t launch_silu_fwd(const uint16_t* G, const uint16_t* U, uint16_t* H, int64_t count,
                            hipStream_t stream);

@@ -542,6 +542,16 @@ hipError_t launch_rq(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q,
 
 }  // namespace
 
+hipError_t launch_rowdot_finalize(const float* part, int ns, int64_t M, int r, float* out, uint16_t* split, float scale,
+                                  hipStream_t stream, bool f16) {
+  const int xc = lora_extra_cols(r);
+  if (f16)
+    rowdot_finalize_kernel<true><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, xc, scale);
+  else
+    rowdot_finalize_kernel<false><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, xc, scale);
+  return hipGetLastError();
+}
+
 size_t rowdot_ws_bytes(int64_t M, int64_t C, int r) {
   const int ns = rowdot_plan(M, C, r).ns;
   return ns > 1 ? align256((size_t)ns * (size_t)M * (size_t)r * 4) : 0;

@@ -142,9 +142,9 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:  # the current stream of the current device (without building its Stream object: 3 us)
+        return _vp(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return _vp(stream.cuda_stream)
 
 
 def _need(t: torch.Tensor, dtype, shape, name):
