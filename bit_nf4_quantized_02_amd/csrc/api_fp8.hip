@@ -36,6 +36,7 @@ struct FwdWs {
   float* T = nullptr;      // M <= 16: T where its partials are too many for the GEMV to add
   uint16_t* TS = nullptr;  // low-rank operand columns
   uint16_t* Bx = nullptr;
+  uint16_t* Ao = nullptr;  // A in operand order
   float* part = nullptr;
 };
 
@@ -57,6 +58,7 @@ size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
   if (r > 0) {
     o.TS = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
     o.Bx = cv.take<uint16_t>((size_t)n * lora_extra_cols(r) * 2);
+    o.Ao = cv.take<uint16_t>(operand_order_bytes(f8_pad(k), r));
   }
   o.part = cv.take<float>(gemm_fp8_ws_bytes(M, k, n));
   return cv.used;
@@ -68,7 +70,7 @@ struct BwdWs {
   uint8_t* wt = nullptr;   // the weight's codes as [k, n]
   uint16_t* US = nullptr;
   uint16_t* Ax = nullptr;
-  uint16_t* Bt = nullptr;  // B rank-major
+  uint16_t* Bo = nullptr;  // B in operand order
   float* U = nullptr;
   float* T = nullptr;
   float* proj = nullptr;
@@ -83,7 +85,7 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
   if (r > 0) {
     o.US = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
     o.Ax = cv.take<uint16_t>((size_t)k * lora_extra_cols(r) * 2);
-    o.Bt = cv.take<uint16_t>((size_t)r * f8_pad(n) * 2);
+    o.Bo = cv.take<uint16_t>(operand_order_bytes(f8_pad(n), r));
     o.U = cv.take<float>((size_t)M * r * 4);
     o.T = cv.take<float>((size_t)M * r * 4);
     const size_t p1 = (size_t)fp8_prep_plan(M, n, false).splits * M * r * 4, p2 = rowdot_ws_bytes(M, k, r);
@@ -154,7 +156,9 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int6
                  *b = static_cast<const uint16_t*>(B);
   const bool few = M <= 16;
   const int parts = fp8_prep_plan(M, k, few).splits;
-  hipError_t e = launch_fp8_prep(x, M, k, a, k, r, o.xq, o.xs, o.proj, few, st, f16);
+  hipError_t e = hipSuccess;
+  if (r > 0 && !few) e = launch_operand_order(a, nullptr, 0, k, f8_pad(k), r, o.Ao, st);
+  if (e == hipSuccess) e = launch_fp8_prep(x, M, k, few ? a : o.Ao, r, o.xq, o.xs, o.proj, few, st, f16);
   if (few) {
     if (r > 0 && !gemv_adds(M, k, r)) {
       float* const T = T_save ? T_save : o.T;
@@ -211,10 +215,9 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
                  *a = static_cast<const uint16_t*>(A), *b = static_cast<const uint16_t*>(B);
   float* const grad = static_cast<float*>(o.grad);
   if (dX || dA) {
-    const int64_t np = f8_pad(n);
-    if (r > 0) e = launch_rank_major(b, nullptr, n, r, np, o.Bt, st);
+    if (r > 0) e = launch_operand_order(b, nullptr, 1, n, f8_pad(n), r, o.Bo, st);
     if (e == hipSuccess)
-      e = launch_fp8_prep(dy, M, n, o.Bt, np, r, dX ? o.yq : nullptr, o.ys, o.proj, false, st, f16);
+      e = launch_fp8_prep(dy, M, n, o.Bo, r, dX ? o.yq : nullptr, o.ys, o.proj, false, st, f16);
     if (e == hipSuccess && r > 0)
       e = launch_rowdot_finalize(o.proj, fp8_prep_plan(M, n, false).splits, M, r, o.U, dX ? o.US : nullptr, scale, st,
                                  f16);

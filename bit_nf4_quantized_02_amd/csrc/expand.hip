@@ -224,32 +224,47 @@ __global__ __launch_bounds__(256) void lowrank_rows_t_kernel(const uint16_t* __r
   out[c * cpr + blockIdx.y] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
 }
 
-// B [n, r] -> rank-major rows [r, ld], zero from n on: 64 x 64 tiles turned
-// through LDS, so that both sides move in runs.
-__global__ __launch_bounds__(256) void rank_major_kernel(const uint16_t* __restrict__ B0, const uint16_t* __restrict__ B1,
-                                                         int64_t n, int r, int64_t ld, uint16_t* __restrict__ out) {
-  const uint16_t* const B = blockIdx.z == 0 ? B0 : B1;
-  out += blockIdx.z * r * ld;
-  __shared__ uint16_t tile[64][65];
-  const int64_t c0 = (int64_t)blockIdx.x * 64;
-  const int j0 = (int)blockIdx.y * 64;
-  const int nj = r - j0 < 64 ? r - j0 : 64;
-  for (int i = threadIdx.x; i < 64 * nj; i += 256) {
-    const int c = i / nj, j = i % nj;
-    tile[c][j] = c0 + c < n ? B[(c0 + c) * r + j0 + j] : (uint16_t)0;
+// A low-rank factor in the operand order of v_mfma_f32_16x16x32: for 32
+// contraction columns c0 .. and rank tile t, lane l's 16 bytes are rank 16 t +
+// l % 16, columns c0 + 8 (l / 16) .. +7 (zero past r and C). Kernels that walk
+// the columns then read it in runs of 1 KB; read in place, a wave's 16 rank
+// rows are 16 lines for the four lanes that share one. One workgroup per 32
+// columns and factor; layout 0: Q [r, C], 1: Q [C, r].
+template <int kLayout>
+__global__ __launch_bounds__(256) void operand_order_kernel(const uint16_t* __restrict__ Q0,
+                                                            const uint16_t* __restrict__ Q1, int64_t C, int r, int tiles,
+                                                            u32x4* __restrict__ out) {
+  __shared__ uint16_t tile[32][130];  // [column][rank]
+  const uint16_t* const Q = blockIdx.y == 0 ? Q0 : Q1;
+  const int64_t c0 = (int64_t)blockIdx.x * 32;
+  out += ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * tiles * 64;
+  for (int i = threadIdx.x; i < 32 * r; i += 256) {
+    const int c = kLayout == 0 ? i & 31 : i / r, j = kLayout == 0 ? i >> 5 : i % r;
+    tile[c][j] = c0 + c < C ? (kLayout == 0 ? Q[j * C + c0 + c] : Q[(c0 + c) * r + j]) : (uint16_t)0;
   }
   __syncthreads();
-  const int c = threadIdx.x & 63;
-  if (c0 + c >= ld) return;
-  for (int j = threadIdx.x >> 6; j < nj; j += 4) out[(int64_t)(j0 + j) * ld + c0 + c] = tile[c][j];
+  for (int i = threadIdx.x; i < tiles * 64; i += 256) {
+    const int j = 16 * (i >> 6) + (i & 15), c = 8 * ((i >> 4) & 3);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (j < r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = tile[c + 2 * e][j] | ((uint32_t)tile[c + 2 * e + 1][j] << 16);
+    out[i] = v;
+  }
 }
 
 }  // namespace
 
-hipError_t launch_rank_major(const uint16_t* B, const uint16_t* B1, int64_t n, int r, int64_t ld, uint16_t* out,
-                             hipStream_t stream) {
-  const dim3 grid((unsigned)cdiv(ld, (int64_t)64), (unsigned)cdiv(r, 64), B1 ? 2 : 1);
-  rank_major_kernel<<<grid, 256, 0, stream>>>(B, B1, n, r, ld, out);
+size_t operand_order_bytes(int64_t Cp, int r) { return (size_t)(Cp / 32) * (rank_pad(r) / 16) * 1024; }
+
+hipError_t launch_operand_order(const uint16_t* Q, const uint16_t* Q1, int layout, int64_t C, int64_t Cp, int r,
+                                uint16_t* out, hipStream_t stream) {
+  const dim3 grid((unsigned)(Cp / 32), Q1 ? 2 : 1);
+  u32x4* const o = reinterpret_cast<u32x4*>(out);
+  if (layout == 0)
+    operand_order_kernel<0><<<grid, 256, 0, stream>>>(Q, Q1, C, r, rank_pad(r) / 16, o);
+  else
+    operand_order_kernel<1><<<grid, 256, 0, stream>>>(Q, Q1, C, r, rank_pad(r) / 16, o);
   return hipGetLastError();
 }
 

@@ -103,62 +103,72 @@ __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restri
 }
 
 // Activations: one pass over P [M, C] that encodes it and forms its low-rank
-// projection P Q^T (Q rank-major [r, ldq], kRP ranks at most; 0: none) --
-// X with A in the forward, dY with B^T in the backward. A lane holds 32
-// consecutive columns of one row of a 128-column block (lane: row lane % 16,
-// columns 32 (lane / 16) ..): a block's maximum is four lanes' maximum, its
-// codes leave in 32-byte pieces, and its four groups of 8 columns are the A
-// operands of v_mfma_f32_16x16x32 over a permuted contraction that Q's
-// operands, loaded the same way, share.
+// projection P Q^T (kRP ranks at most; 0: none) -- X with A in the forward, dY
+// with B^T in the backward. A wave takes 128-column blocks of 16 rows: 16
+// neighbouring lanes load one row's 256 bytes (8 columns each), find its
+// maximum, and store its 128 code bytes; the values then pass through the
+// wave's own LDS into the A operand of v_mfma_f32_16x16x32 (lane: row lane %
+// 16, columns 8 (lane / 16) ..). Loaded in that layout straight from memory,
+// neighbouring lanes lie in different rows and each of the 64 pieces is a
+// cache access of its own, which was the kernel's bound (4096 x 22016, r = 64:
+// 126 us).
 //   kFew = false: codes [M, Cp] (zero past C) and the GEMM's scale words, one
 // per (128-column block, 128-row tile, row % 32) with the bytes of rows +0,
 // +32, +64, +96, so that a wave of the GEMM gets the scales of its four
-// 32-row operand blocks with one load. A wave holds 32 rows; the workgroup's
-// four share Q's lines in L1 and walk the blocks of one column range.
+// 32-row operand blocks with one load. Q in operand order. A wave holds 32
+// rows; the workgroup's four walk the blocks of one column range.
 //   kFew = true (M <= 16): codes in the GEMV's operand order [block][lane][32
-// bytes] (zeros past M), scales [block][16]; the four waves take the range's
-// blocks in turn and their projections are added in wave order.
+// bytes] (lane: row lane % 16, bytes 32 (lane / 16) ..; zeros past M), scales
+// [block][16]; Q [r, C] as it is. The four waves take the range's blocks in
+// turn and their projections are added in wave order.
 // Partials of the projection go to part [range][M][r]; codes NULL: only those.
 template <int kRP, bool kF16, bool kVec, bool kFew>
 __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restrict__ P, int64_t M, int64_t C, int64_t Cp,
-                                                       const uint16_t* __restrict__ Q, int64_t ldq, int r, int bchunk,
+                                                       const uint16_t* __restrict__ Q, int r, int bchunk,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scale,
                                                        float* __restrict__ part) {
   constexpr int kTiles = kRP / 16, kTA = kTiles > 0 ? kTiles : 1;
   constexpr int kMR = kFew ? 1 : 2;
+  constexpr int kPitch = 256 + 16;  // bytes per staged row (16 rows on distinct banks)
   typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
+  __shared__ __attribute__((aligned(16))) char turn[4][kTiles > 0 ? 16 * kPitch : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = lane & 15, co = 32 * (lane >> 4);
   const int64_t m0 = kFew ? 0 : (int64_t)blockIdx.x * kPrepRows + wave * 16 * kMR;
   if (!kFew && m0 >= M) return;
   const int nb = (int)(Cp / kF8Block);
   const int b0 = (int)blockIdx.y * bchunk, b1 = b0 + bchunk < nb ? b0 + bchunk : nb;
   constexpr int kStep = kFew ? 4 : 1;
   const int64_t mt = cdiv(M, (int64_t)kF8Block);
-  const uint16_t* prow[kMR];
-  const uint16_t* qrow[kTA];
+  const int lr = lane >> 4, lc = 8 * (lane & 15);  // loads: row 4 u + lr, columns lc ..
+  const uint16_t* prow[kMR][4];
 #pragma unroll
-  for (int i = 0; i < kMR; ++i) prow[i] = P + (m0 + 16 * i + row < M ? m0 + 16 * i + row : M - 1) * C;
+  for (int i = 0; i < kMR; ++i)
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) qrow[t] = Q + (int64_t)(16 * t + row < r ? 16 * t + row : r - 1) * ldq;
+    for (int u = 0; u < 4; ++u) {
+      const int64_t m = m0 + 16 * i + 4 * u + lr;
+      prow[i][u] = P + (m < M ? m : M - 1) * C;
+    }
+  const uint16_t* qrow[kTA];  // kFew: this lane's rank rows
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) qrow[t] = Q + (kFew ? (int64_t)(16 * t + (lane & 15) < r ? 16 * t + (lane & 15) : r - 1) * C : 0);
   f32x4 acc[kMR][kTA];
 #pragma unroll
   for (int i = 0; i < kMR; ++i)
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto load = [&](int kb, u32x4 (&x)[kMR][4]) {
-    const int64_t c = (int64_t)kb * kF8Block + co;
+    const int64_t c = (int64_t)kb * kF8Block + lc;
     if ((int64_t)(kb + 1) * kF8Block <= C) {  // (uniform: no load behind a test of its own)
 #pragma unroll
       for (int i = 0; i < kMR; ++i)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) x[i][s] = *reinterpret_cast<const Vec*>(prow[i] + c + 8 * s);
+        for (int u = 0; u < 4; ++u) x[i][u] = *reinterpret_cast<const Vec*>(prow[i][u] + c);
     } else {
 #pragma unroll
       for (int i = 0; i < kMR; ++i)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) x[i][s] = load8h<kVec>(prow[i], c + 8 * s, C);
+        for (int u = 0; u < 4; ++u) x[i][u] = load8h<kVec>(prow[i][u], c, C);
     }
   };
   u32x4 x[kMR][4], nx[kMR][4];
@@ -166,66 +176,66 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
   if (kb0 < b1) load(kb0, x);
   for (int kb = kb0; kb < b1; kb += kStep) {
     u32x4 q[kTA][4];
-    const int64_t c = (int64_t)kb * kF8Block + co;
-    if ((int64_t)(kb + 1) * kF8Block <= ldq) {
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) q[t][s] = *reinterpret_cast<const u32x4*>(qrow[t] + c + 8 * s);
-    } else {
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) q[t][s] = load8h<true>(qrow[t], c + 8 * s, ldq);
-    }
-    load(kb + kStep < b1 ? kb + kStep : kb, nx);
-#pragma unroll
-    for (int i = 0; i < kMR; ++i) {
-      if (kFew && row >= M) x[i][0] = x[i][1] = x[i][2] = x[i][3] = u32x4{0u, 0u, 0u, 0u};
-      if (codes != nullptr) {
-        float f[32];
-        uint32_t a = 0;
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[8 * s + 2 * e] = from16<kF16>(x[i][s][e] & 0xFFFFu);
-            f[8 * s + 2 * e + 1] = from16<kF16>(x[i][s][e] >> 16);
-          }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) a = max(a, f8_finite_abs(f[e]));
-        a = max(a, (uint32_t)__shfl_xor((int)a, 16));
-        a = max(a, (uint32_t)__shfl_xor((int)a, 32));
-        const uint32_t b = f8_scale_byte(a);
-        const float inv = f8_inv_scale(b);
-        u32x4 o[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[h][e] = f8_pack4(f + 16 * h + 4 * e, inv);
-        const int64_t m = m0 + 16 * i + row;
+      for (int s = 0; s < 4; ++s) {
         if constexpr (kFew) {
-          u32x4* const d = reinterpret_cast<u32x4*>(codes) + ((int64_t)kb * 64 + lane) * 2;
-          d[0] = o[0];
-          d[1] = o[1];
-          if (lane < 16) scale[kb * 16 + lane] = (uint8_t)b;
-        } else if (m < M) {
-          u32x4* const d = reinterpret_cast<u32x4*>(codes + m * Cp + c);
-          d[0] = o[0];
-          d[1] = o[1];
-          if (lane < 16) scale[((kb * mt + m / kF8Block) * 32 + (m & 31)) * 4 + ((m >> 5) & 3)] = (uint8_t)b;
+          q[t][s] = load8h<true>(qrow[t], (int64_t)kb * kF8Block + 32 * s + 8 * (lane >> 4), C);
+        } else {
+          q[t][s] = reinterpret_cast<const u32x4*>(Q)[((int64_t)(kb * 4 + s) * kTiles + t) * 64 + lane];
         }
       }
+    load(kb + kStep < b1 ? kb + kStep : kb, nx);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+    for (int i = 0; i < kMR; ++i) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-          acc[i][t] = mfma16<kF16>(__builtin_bit_cast(bf16x8, x[i][s]), __builtin_bit_cast(bf16x8, q[t][s]), acc[i][t]);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t m = m0 + 16 * i + 4 * u + lr;
+        if (kFew && m >= M) x[i][u] = u32x4{0u, 0u, 0u, 0u};
+        if constexpr (kTiles > 0)
+          *reinterpret_cast<u32x4*>(turn[wave] + (4 * u + lr) * kPitch + 2 * lc) = x[i][u];
+        if (codes != nullptr) {
+          float f[8];
+          uint32_t a = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = from16<kF16>(x[i][u][e] & 0xFFFFu);
+            f[2 * e + 1] = from16<kF16>(x[i][u][e] >> 16);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a = max(a, f8_finite_abs(f[e]));
+#pragma unroll
+          for (int d = 1; d < 16; d *= 2) a = max(a, (uint32_t)__shfl_xor((int)a, d));
+          const uint32_t b = f8_scale_byte(a);
+          const float inv = f8_inv_scale(b);
+          const u32x2 o = {f8_pack4(f, inv), f8_pack4(f + 4, inv)};
+          if constexpr (kFew) {
+            // columns lc .. of row m: lane m + 16 (lc / 32), its bytes lc % 32 ..
+            *reinterpret_cast<u32x2*>(codes + ((int64_t)kb * 64 + 16 * (lc >> 5) + 4 * u + lr) * 32 + (lc & 31)) = o;
+            if ((lane & 15) == 0) scale[kb * 16 + 4 * u + lr] = (uint8_t)b;
+          } else if (m < M) {
+            *reinterpret_cast<u32x2*>(codes + m * Cp + (int64_t)kb * kF8Block + lc) = o;
+            if ((lane & 15) == 0) scale[((kb * mt + m / kF8Block) * 32 + (m & 31)) * 4 + ((m >> 5) & 3)] = (uint8_t)b;
+          }
+        }
+      }
+      // lanes read what others wrote: the LDS keeps a wave's order, the
+      // compiler must too
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int s = 0; s < (kTiles > 0 ? 4 : 0); ++s) {
+        const bf16x8 pa = *reinterpret_cast<const bf16x8*>(turn[wave] + (lane & 15) * kPitch + 64 * s + 16 * (lane >> 4));
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) acc[i][t] = mfma16<kF16>(pa, __builtin_bit_cast(bf16x8, q[t][s]), acc[i][t]);
+      }
+      asm volatile("" ::: "memory");
     }
 #pragma unroll
     for (int i = 0; i < kMR; ++i)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) x[i][s] = nx[i][s];
+      for (int u = 0; u < 4; ++u) x[i][u] = nx[i][u];
   }
   // D layout: lane -> rank lane % 16, rows 4 (lane / 16) + v
   if constexpr (kRP > 0 && kFew) {
@@ -233,7 +243,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) red[wave][4 * (lane >> 4) + v][16 * t + row] = acc[0][t][v];
+      for (int v = 0; v < 4; ++v) red[wave][4 * (lane >> 4) + v][16 * t + (lane & 15)] = acc[0][t][v];
     __syncthreads();
     for (int o = threadIdx.x; o < (int)M * r; o += 256) {
       const int m = o / r, j = o % r;
@@ -247,7 +257,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int64_t m = m0 + 16 * i + 4 * (lane >> 4) + v;
-          const int j = 16 * t + row;
+          const int j = 16 * t + (lane & 15);
           if (m < M && j < r) part[((int64_t)blockIdx.y * M + m) * r + j] = acc[i][t][v];
         }
   }
@@ -314,14 +324,14 @@ Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few) {
   return Fp8Prep{(int)chunk, (int)cdiv(nb, chunk)};
 }
 
-hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int64_t ldq, int r,
+hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r,
                            uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16) {
   const Fp8Prep pl = fp8_prep_plan(M, C, few);
   const int64_t Cp = f8_pad(C);
   if (few && (C % 8 != 0 || M > 16)) return hipErrorInvalidValue;
   const dim3 grid(few ? 1u : (unsigned)cdiv(M, (int64_t)kPrepRows), (unsigned)pl.splits);
 #define QLORA_PREP3(RP, H, V, F) \
-  fp8_prep_kernel<RP, H, V, F><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, ldq, r, pl.chunk, codes, scale, part)
+  fp8_prep_kernel<RP, H, V, F><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, r, pl.chunk, codes, scale, part)
 #define QLORA_PREP2(RP, H)                                                                             \
   {                                                                                                    \
     if (few) QLORA_PREP3(RP, H, true, true);                                                           \

@@ -31,6 +31,7 @@ struct PairView {
   const uint16_t* lr;  // B (forward) or A (dX)
 };
 
+constexpr int kMaxRank = 128;
 constexpr int kRows = 8;  // weight rows per workgroup, as the plain row expansion
 
 // One 16-byte output chunk column of 8 rows per thread; blockIdx.z picks the
@@ -157,40 +158,40 @@ __device__ __forceinline__ void join8(const u32x4& g, const u32x4& u, const u32x
 }
 
 constexpr int kJoinMR = 2;     // 16-row tiles per wave
-constexpr int kJoinWaves = 4;  // each with rows of its own: the four share B's lines in L1
+constexpr int kJoinWaves = 4;  // each with rows of its own
 constexpr int kJoinRows = 16 * kJoinMR * kJoinWaves;
 
-// A wave holds 32 rows and walks its workgroup's columns 32 at a time in the
-// A-operand layout of v_mfma_f32_16x16x32 (lane: row lane % 16, 8 columns from
-// 8 (lane / 16)): G, U and dH are loaded in it, dG and dU formed in it, written
-// rounded to D, and multiplied in parts with Bt's rows. kRP: ranks padded to
-// a multiple of 16 (0: no adapters, D only).
+// A wave holds 32 rows and walks its workgroup's columns 32 at a time: four
+// neighbouring lanes load 64 bytes of a row, dG and dU are formed in that
+// layout and written rounded to D, and their parts pass through the wave's own
+// LDS into the A operand of v_mfma_f32_16x16x32 (lane: row lane % 16, columns
+// 8 (lane / 16) ..) against the factors in operand order. (Loaded in operand
+// layout, neighbouring lanes lie in different rows: 55 cache accesses per load,
+// 340 us at 4096 x 22016, r = 64.) kRP: ranks padded (0: no adapters, D only).
 template <int kRP, bool kF16, bool kVec>
 __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
     const uint16_t* __restrict__ G, const uint16_t* __restrict__ U, const uint16_t* __restrict__ dH, int64_t M, int64_t n,
-    int64_t np, const uint16_t* __restrict__ Bt, int r, int64_t cchunk, uint16_t* __restrict__ D,
+    int64_t np, const u32x4* __restrict__ Bo, int r, int64_t cchunk, uint16_t* __restrict__ D,
     float* __restrict__ part) {
   constexpr int kTiles = kRP / 16;
   constexpr int kP = parts_of<kF16>();
   typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
+  // [wave][w][part][16 rows x 64 bytes], 16-byte piece p of row i at p ^ (i / 4 % 4)
+  __shared__ __attribute__((aligned(16))) char turn[kJoinWaves][kTiles > 0 ? 2 * kP * 1024 : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t m0 = (int64_t)blockIdx.x * kJoinRows + wave * 16 * kJoinMR;
   if (m0 >= M) return;
   const int64_t cbeg = (int64_t)blockIdx.y * cchunk;
   const int64_t cend = cbeg + cchunk < np ? cbeg + cchunk : np;
-  const int64_t co = 8 * (lane >> 4);
+  const int lr = lane >> 2, co = 8 * (lane & 3);  // loads: row lr, columns co ..
+  char* const wr = turn[wave] + lr * 64 + (((lane & 3) ^ ((lr >> 2) & 3)) << 4);
+  const char* const rd = turn[wave] + (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 2) & 3)) << 4);
   int64_t off[kJoinMR];  // row offsets (rows past M repeat the last one; not stored)
 #pragma unroll
   for (int i = 0; i < kJoinMR; ++i) {
-    const int64_t m = m0 + 16 * i + (lane & 15);
+    const int64_t m = m0 + 16 * i + lr;
     off[i] = (m < M ? m : M - 1) * n;
-  }
-  const uint16_t* brow[kTiles > 0 ? kTiles : 1];  // (ranks past r repeat the last one; not stored)
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int j = 16 * t + (lane & 15);
-    brow[t] = Bt + (int64_t)(j < r ? j : r - 1) * np + co;
   }
   f32x4 acc[2][kJoinMR][kTiles > 0 ? kTiles : 1];
 #pragma unroll
@@ -221,16 +222,17 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
       }
     }
   };
+  const u32x4* const bo1 = Bo + (np / 32) * kTiles * 64;  // the up factor
   Stage cur, nxt;
   load(cbeg, cur);
   for (int64_t c = cbeg; c < cend; c += 32) {
-    // B's rows first: waiting for them must not wait for the next step's loads
+    // the factors first: waiting for them must not wait for the next step's loads
     u32x4 b[2][kTiles > 0 ? kTiles : 1];
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-        b[w][t] = *reinterpret_cast<const u32x4*>(brow[t] + w * r * np + c);
+    for (int t = 0; t < kTiles; ++t) {
+      b[0][t] = Bo[((c >> 5) * kTiles + t) * 64 + lane];
+      b[1][t] = bo1[((c >> 5) * kTiles + t) * 64 + lane];
+    }
     load(c + 32 < cend ? c + 32 : c, nxt);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -240,19 +242,30 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
       u32x4 p[2][kP];
       split8<kF16>(dg, p[0]);
       split8<kF16>(du, p[1]);
-      const int64_t m = m0 + 16 * i + (lane & 15);
+      const int64_t m = m0 + 16 * i + lr;
       if (D != nullptr && m < M) {
         *reinterpret_cast<u32x4*>(D + m * 2 * np + c + co) = p[0][0];
         *reinterpret_cast<u32x4*>(D + m * 2 * np + np + c + co) = p[1][0];
       }
+      if constexpr (kTiles > 0) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+          for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(wr + (w * kP + q) * 1024) = p[w][q];
+        // lanes read what others wrote: the LDS keeps a wave's order, the
+        // compiler must too
+        asm volatile("" ::: "memory");
 #pragma unroll
-          for (int q = kP - 1; q >= 0; --q)
-            acc[w][i][t] = mfma16<kF16>(__builtin_bit_cast(bf16x8, p[w][q]), __builtin_bit_cast(bf16x8, b[w][t]),
-                                        acc[w][i][t]);
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int q = kP - 1; q >= 0; --q) {
+            const bf16x8 a = *reinterpret_cast<const bf16x8*>(rd + (w * kP + q) * 1024);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+              acc[w][i][t] = mfma16<kF16>(a, __builtin_bit_cast(bf16x8, b[w][t]), acc[w][i][t]);
+          }
+        asm volatile("" ::: "memory");
+      }
     }
     cur = nxt;
   }
@@ -302,38 +315,65 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
 
 // ------------------------------------------------------ adapter gradients dB
 
-// T [2][M][r] -> Tt [part][w][rp][Mp]: rank-major rows of parts, zero past M and r.
+// T [2][M][r] -> Tt [32-token step][part][w][rank tile][lane][16 bytes], the A
+// operand of dB's products: lane l holds rank 16 t + l % 16, tokens 8 (l / 16)
+// .. +7 of the step, zero past M and r.
 template <bool kF16>
-__global__ __launch_bounds__(256) void gated_tt_kernel(const float* __restrict__ T, int64_t M, int64_t Mp, int r, int rp,
-                                                       uint16_t* __restrict__ out) {
-  const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int j = blockIdx.y, w = blockIdx.z;
-  if (m >= Mp) return;
-  float x = m < M && j < r ? T[(w * M + m) * r + j] : 0.0f;
+__global__ __launch_bounds__(256) void gated_tt_kernel(const float* __restrict__ T, int64_t M, int r, int tiles,
+                                                       u32x4* __restrict__ out) {
+  __shared__ float tile[32][kMaxRank + 1];
+  const int w = blockIdx.y;
+  const int64_t m0 = (int64_t)blockIdx.x * 32;
+  for (int i = threadIdx.x; i < 32 * r; i += 256) {
+    const int64_t m = m0 + i / r;
+    tile[i / r][i % r] = m < M ? T[(w * M + m) * r + i % r] : 0.0f;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tiles * 64; i += 256) {
+    const int j = 16 * (i >> 6) + (i & 15);
+    float x[8];
 #pragma unroll
-  for (int p = 0; p < parts_of<kF16>(); ++p) {
-    const uint16_t h = to16<kF16>(x);
-    out[(((int64_t)p * 2 + w) * rp + j) * Mp + m] = h;
-    x -= from16<kF16>(h);
+    for (int e = 0; e < 8; ++e) x[e] = j < r ? tile[8 * ((i >> 4) & 3) + e][j] : 0.0f;
+    u32x4 p[parts_of<kF16>()];
+    split8<kF16>(x, p);
+#pragma unroll
+    for (int q = 0; q < parts_of<kF16>(); ++q)
+      out[(((int64_t)blockIdx.x * parts_of<kF16>() + q) * 2 + w) * tiles * 64 + i] = p[q];
   }
 }
 
-constexpr int kDbCols = 64;                    // columns per workgroup
-constexpr int kDbPitch = kDbCols * 2 + 16;     // bytes per staged row
+constexpr int kDbCols = 64;             // columns per workgroup
+constexpr int kDbTile = 32 * kDbCols * 2;  // bytes of one staged part
+
+// Staged tile [32 tokens][64 columns]: the 32-byte segment s of row i is kept
+// at s ^ f(i), f(i) = bit 1 of i + 2 (bit 3 of i), so that the eight rows that
+// one cycle of a transposing read touches lie on distinct banks.
+__device__ __forceinline__ int db_seg(int row, int s) { return row * 128 + ((s ^ (((row >> 1) & 1) | ((row >> 2) & 2))) << 5); }
+
+// B operand (8 tokens of one column per lane) of column tile s from such a tile
+__device__ __forceinline__ bf16x8 db_operand(const char* tile, int s, int lane) {
+  const int row = 8 * (lane >> 4) + ((lane & 15) >> 2);
+  const char* const p = tile + db_seg(row, s) + 8 * (lane & 3);
+  const char* const p4 = tile + db_seg(row + 4, s) + 8 * (lane & 3);
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p4));
+  const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
 
 // Partial of dB over tokens [m0, m1): rows = ranks, columns = block columns.
 // Each 32-token step every thread forms dG and dU of one row's 8 columns and
 // stages their parts as [token][column] tiles in LDS (two sets, one barrier
 // per step); the B operand (8 tokens of one column per lane) comes back through
-// the transposing read, the A operand (8 tokens of one rank) straight from Tt.
+// the transposing read, the A operand (8 tokens of one rank) from Tt in runs.
 // The four waves split the ranks first and then the columns, so that no rank
 // row is loaded twice where there are at least 64. Products of parts whose
 // order is below the last bit kept are left out (mid * lo and lo * lo).
 template <int kRP, bool kF16, bool kVec>
 __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restrict__ G, const uint16_t* __restrict__ U,
                                                        const uint16_t* __restrict__ dH, int64_t M, int64_t n,
-                                                       const uint16_t* __restrict__ Tt, int64_t Mp, int r,
-                                                       int64_t mchunk, float* __restrict__ part) {
+                                                       const u32x4* __restrict__ Tt, int r, int64_t mchunk,
+                                                       float* __restrict__ part) {
   constexpr int kP = parts_of<kF16>();
   typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
   constexpr int kJTall = kRP / 16;
@@ -341,7 +381,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
   constexpr int kWC = 4 / kWJ;                      // waves along columns
   constexpr int kJT = kJTall / kWJ;                 // rank tiles per wave
   constexpr int kCT = kDbCols / 16 / kWC;           // column tiles per wave
-  __shared__ __attribute__((aligned(16))) char sm[2][2][kP][32 * kDbPitch];  // [set][w][part]
+  __shared__ __attribute__((aligned(16))) char sm[2 * 2 * kP * kDbTile];  // [set][w][part]
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wj = wave % kWJ, wc = wave / kWJ;
@@ -373,13 +413,13 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
     float dg[8], du[8];
     join8<kF16>(s.g, s.u, s.d, dg, du);
     u32x4 p[kP];
-    char* const at = sm[0][0][0] + set * (2 * kP * 32 * kDbPitch) + prow * kDbPitch + (t & 7) * 16;
+    char* const at = sm + set * (2 * kP * kDbTile) + db_seg(prow, (t & 7) >> 1) + (t & 1) * 16;
     split8<kF16>(dg, p);
 #pragma unroll
-    for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(at + q * 32 * kDbPitch) = p[q];
+    for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(at + q * kDbTile) = p[q];
     split8<kF16>(du, p);
 #pragma unroll
-    for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(at + (kP + q) * 32 * kDbPitch) = p[q];
+    for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(at + (kP + q) * kDbTile) = p[q];
   };
   f32x4 acc[2][kJT][kCT];
 #pragma unroll
@@ -404,8 +444,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
       for (int q = 0; q < kP; ++q)
 #pragma unroll
         for (int a = 0; a < kJT; ++a)
-          ta[w][q][a] = *reinterpret_cast<const u32x4*>(
-              Tt + (((int64_t)q * 2 + w) * kRP + 16 * (wj * kJT + a) + (lane & 15)) * Mp + mb + 8 * (lane >> 4));
+          ta[w][q][a] = Tt[((((mb >> 5) * kP + q) * 2 + w) * kJTall + wj * kJT + a) * 64 + lane];
     if (mb + 32 < m1) stage(set ^ 1, mb + 32, st);
     load(mb + 64 < m1 ? mb + 64 : m0, st);
 #pragma unroll
@@ -415,7 +454,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
         bf16x8 pb[kP];
 #pragma unroll
         for (int q = 0; q < kP; ++q)
-          pb[q] = tr_rows8(sm[0][0][0] + ((set * 2 + w) * kP + q) * 32 * kDbPitch, kDbPitch, 16 * (wc * kCT + b), lane);
+          pb[q] = db_operand(sm + ((set * 2 + w) * kP + q) * kDbTile, wc * kCT + b, lane);
 #pragma unroll
         for (int a = 0; a < kJT; ++a)
 #pragma unroll
@@ -426,7 +465,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
       }
     __syncthreads();
   }
-  // D[j][c]: lane -> c = lane % 16, j = 4 (lane / 16) + v; partials [split][w][r][n]
+  // D[j][c]: lane -> c = lane % 16, j = 4 (lane / 16) + v; partials [split][w][n][r], as dB
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -434,30 +473,30 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
 #pragma unroll
       for (int b = 0; b < kCT; ++b) {
         const int64_t c = c0 + 16 * (wc * kCT + b) + (lane & 15);
+        const int j = 16 * (wj * kJT + a) + 4 * (lane >> 4);
+        float* const o = part + (((int64_t)blockIdx.y * 2 + w) * n + c) * r + j;
+        if (c < n && (r & 3) == 0 && j < r) {
+          *reinterpret_cast<f32x4*>(o) = acc[w][a][b];
+        } else if (c < n) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int j = 16 * (wj * kJT + a) + 4 * (lane >> 4) + v;
-          if (c < n && j < r) part[(((int64_t)blockIdx.y * 2 + w) * r + j) * n + c] = acc[w][a][b][v];
+          for (int v = 0; v < 4; ++v)
+            if (j + v < r) o[v] = acc[w][a][b][v];
         }
       }
 }
 
-// dB[c, j] (+)= scale * (partials added in split order)
-__global__ __launch_bounds__(256) void gated_db_reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
-                                                              int r, float scale, float* __restrict__ dBg,
+// dB (+)= scale * (partials added in split order)
+__global__ __launch_bounds__(256) void gated_db_reduce_kernel(const float* __restrict__ part, int splits, int64_t count,
+                                                              float scale, float* __restrict__ dBg,
                                                               float* __restrict__ dBu, int accumulate) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int w = blockIdx.y;
   float* const dB = w == 0 ? dBg : dBu;
-  if (i >= n * r || dB == nullptr) return;
-  const int64_t j = i / n, c = i % n;
-  float s = part[((int64_t)w * r + j) * n + c];
-  for (int p = 1; p < splits; ++p) s += part[(((int64_t)p * 2 + w) * r + j) * n + c];
-  float* const o = dB + c * r + j;
-  *o = accumulate ? *o + scale * s : scale * s;
+  if (i >= count || dB == nullptr) return;
+  float s = part[w * count + i];
+  for (int p = 1; p < splits; ++p) s += part[(p * 2 + w) * count + i];
+  dB[i] = accumulate ? dB[i] + scale * s : scale * s;
 }
-
-int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
 // Column ranges of the join: about 1024 workgroups (each a multiple of 32
 // columns, at least 64; at most 32 ranges, whose partials are added later).
@@ -488,6 +527,9 @@ DbPlan db_plan(int64_t M, int64_t n) {
   const int64_t mchunk = cdiv(cdiv(M, s), (int64_t)32) * 32;
   return {mchunk, (int)cdiv(M, mchunk)};
 }
+
+// T's parts in operand order (three at most).
+size_t db_t_bytes(int64_t M, int r) { return (size_t)cdiv(M, (int64_t)32) * 3 * 2 * rank_pad(r) * 64; }
 
 PairView pair_view(const Nf4View& w, const uint16_t* lr) {
   return PairView{reinterpret_cast<const uint32_t*>(w.codes), w.code8, w.s2, w.mean, w.codebook, lr};
@@ -533,7 +575,7 @@ hipError_t launch_gated_expand_dx(const Nf4View& g, const Nf4View& u, const uint
 
 size_t gated_join_ws_bytes(int64_t M, int64_t n, int r) {
   if (r == 0) return 0;
-  return align256((size_t)2 * r * (size_t)gated_pad(n) * 2) +
+  return align256(2 * operand_order_bytes(gated_pad(n), r)) +
          align256((size_t)join_plan(M, n).splits * 2 * (size_t)M * r * 4);
 }
 
@@ -543,15 +585,15 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
   const JoinPlan pl = join_plan(M, n);
   const int64_t np = gated_pad(n);
   const int rp = rank_pad(r);
-  uint16_t* const Bt = static_cast<uint16_t*>(ws);
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)2 * r * (size_t)np * 2));
+  uint16_t* const Bo = static_cast<uint16_t*>(ws);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(2 * operand_order_bytes(np, r)));
   if (r > 0) {
-    const hipError_t e = launch_rank_major(Bg, Bu, n, r, np, Bt, stream);
+    const hipError_t e = launch_operand_order(Bg, Bu, 1, n, np, r, Bo, stream);
     if (e != hipSuccess) return e;
   }
   const dim3 grid((unsigned)cdiv(M, (int64_t)kJoinRows), (unsigned)pl.splits);
 #define QLORA_JOIN2(RP, H, V) \
-  gated_join_kernel<RP, H, V><<<grid, 64 * kJoinWaves, 0, stream>>>(G, U, dH, M, n, np, Bt, r, pl.cchunk, D, part)
+  gated_join_kernel<RP, H, V><<<grid, 64 * kJoinWaves, 0, stream>>>(G, U, dH, M, n, np, reinterpret_cast<const u32x4*>(Bo), r, pl.cchunk, D, part)
 #define QLORA_JOIN(RP)                                                              \
   {                                                                                 \
     if (n % 8 == 0) { if (f16) QLORA_JOIN2(RP, true, true); else QLORA_JOIN2(RP, false, true); } \
@@ -577,26 +619,24 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
 
 size_t gated_db_ws_bytes(int64_t M, int64_t n, int r) {
   if (r == 0) return 0;
-  return align256((size_t)3 * 2 * rank_pad(r) * (size_t)(cdiv(M, (int64_t)32) * 32) * 2) +
-         align256((size_t)db_plan(M, n).splits * 2 * r * (size_t)n * 4);
+  return align256(db_t_bytes(M, r)) + align256((size_t)db_plan(M, n).splits * 2 * r * (size_t)n * 4);
 }
 
 hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
                            const float* T, int r, float scale, float* dBg, float* dBu, int accumulate, void* ws,
                            hipStream_t stream, bool f16) {
   const DbPlan pl = db_plan(M, n);
-  const int64_t Mp = cdiv(M, (int64_t)32) * 32;
   const int rp = rank_pad(r);
-  uint16_t* const Tt = static_cast<uint16_t*>(ws);
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)3 * 2 * rp * (size_t)Mp * 2));
-  const dim3 tg((unsigned)cdiv(Mp, (int64_t)256), (unsigned)rp, 2);
+  u32x4* const Tt = static_cast<u32x4*>(ws);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(db_t_bytes(M, r)));
+  const dim3 tg((unsigned)cdiv(M, (int64_t)32), 2);
   if (f16)
-    gated_tt_kernel<true><<<tg, 256, 0, stream>>>(T, M, Mp, r, rp, Tt);
+    gated_tt_kernel<true><<<tg, 256, 0, stream>>>(T, M, r, rp / 16, Tt);
   else
-    gated_tt_kernel<false><<<tg, 256, 0, stream>>>(T, M, Mp, r, rp, Tt);
+    gated_tt_kernel<false><<<tg, 256, 0, stream>>>(T, M, r, rp / 16, Tt);
   const dim3 grid((unsigned)cdiv(n, (int64_t)kDbCols), (unsigned)pl.splits);
 #define QLORA_DB2(RP, H, V) \
-  gated_db_kernel<RP, H, V><<<grid, 256, 0, stream>>>(G, U, dH, M, n, Tt, Mp, r, pl.mchunk, part)
+  gated_db_kernel<RP, H, V><<<grid, 256, 0, stream>>>(G, U, dH, M, n, Tt, r, pl.mchunk, part)
 #define QLORA_DB(RP)                                                                         \
   {                                                                                          \
     if (n % 8 == 0) { if (f16) QLORA_DB2(RP, true, true); else QLORA_DB2(RP, false, true); }  \
@@ -608,7 +648,7 @@ hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t*
   else QLORA_DB(128)
 #undef QLORA_DB
 #undef QLORA_DB2
-  gated_db_reduce_kernel<<<dim3((unsigned)cdiv(n * r, (int64_t)256), 2), 256, 0, stream>>>(part, pl.splits, n, r, scale,
+  gated_db_reduce_kernel<<<dim3((unsigned)cdiv(n * r, (int64_t)256), 2), 256, 0, stream>>>(part, pl.splits, n * r, scale,
                                                                                           dBg, dBu, accumulate);
   return hipGetLastError();
 }

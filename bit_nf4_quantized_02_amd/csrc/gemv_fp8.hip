@@ -9,9 +9,11 @@
 // workgroup adds while its first codes are on the way (a launch less).
 // A workgroup owns 16 kT weight rows; its 8 waves take the 128-column blocks
 // in turn, so neighbouring waves read neighbouring lines of the same rows.
-// Codes go from memory to registers in operand order (a lane holds 32
-// consecutive bytes of one row, four lanes one 128-byte line), two batches of
-// kU blocks rotating so that the next is in flight while one is multiplied.
+// Codes go from memory straight into LDS, eight neighbouring lanes a 128-byte
+// line, into a ring of three blocks per wave (one multiplied, two in flight), and
+// from there in operand order (a lane takes 32 consecutive bytes of one row).
+// Loaded in operand order they cost a cache access per lane: 52 us for 8192 x
+// 28672 at one token.
 // Partial sums of the waves are added in wave order through LDS, the low-rank
 // term is added in fp32, and Y is rounded once.
 #include "fp8.h"
@@ -24,18 +26,20 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kGvWaves = 8;
-constexpr int kU = 2;      // 128-column blocks per batch
 constexpr int kMaxR = 128;  // largest rank
-
-template <int kT>
-struct Batch {
-  u32x4 x[kU][2], w[kU][kT][2];
-  uint32_t xs[kU], ws[kU];
-};
 
 __device__ __forceinline__ i32x8 join(const u32x4& lo, const u32x4& hi) {
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
+
+// Row r of a tile keeps its 16-byte segment s at s ^ swz(r): the 16 rows that
+// one cycle reads lie on distinct banks.
+__device__ __forceinline__ int row_swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+struct Block {
+  u32x4 x[2];
+  uint32_t xs, ws;
+};
 
 template <int kT, bool kF16>
 __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* __restrict__ codes,
@@ -46,7 +50,12 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
                                                                  const uint16_t* __restrict__ B, int r, float scale,
                                                                  uint16_t* __restrict__ Y, float* __restrict__ T_save) {
   constexpr int NT = 16 * kT;
-  __shared__ float red[kGvWaves][kT][16][16];
+  constexpr int kSlot = kT * 2048;  // one wave's codes of one block
+  // three arrays, so that the compiler can tell the one being read from those
+  // being filled
+  __shared__ __attribute__((aligned(16))) char ring0[kGvWaves * kSlot];
+  __shared__ __attribute__((aligned(16))) char ring1[kGvWaves * kSlot];
+  __shared__ __attribute__((aligned(16))) char ring2[kGvWaves * kSlot];
   __shared__ float lred[kT][16][16];
   __shared__ float Ts[16 * kMaxR];  // T [M][r]
   const int t = threadIdx.x, lane = t & 63;
@@ -57,64 +66,88 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
   // this workgroup's rows (those past N read as zero and are not stored)
   const i32x4 wr = make_rsrc(codes + n0 * kp, rows * kp);
   const i32x4 sr = make_rsrc(wscale + (n0 / kF8Block) * nb, nb);
-  // blocks past the end read as zero activations
   const i32x4 xr = make_rsrc(Xq, (int64_t)nb * 2048);
   const i32x4 xsr = make_rsrc(Xs, (int64_t)nb * 16);
-  uint32_t woff[kT];
+  // copy h of tile i: lane l fills row 8 h + l / 8, position l % 8
+  uint32_t woff[kT][2];
 #pragma unroll
-  for (int i = 0; i < kT; ++i) woff[i] = (uint32_t)((16 * i + (lane & 15)) * kp + 32 * (lane >> 4));
-
-  auto load = [&](int j, Batch<kT>& b) {
+  for (int i = 0; i < kT; ++i)
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int kb = wave + kGvWaves * (j * kU + u);
-      const int wb = kb < nb ? kb : nb - 1;
-#pragma unroll
-      for (int i = 0; i < kT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) b.w[u][i][h] = raw_buffer_load_b128(wr, (int)(woff[i] + 16 * h), wb * kF8Block, 0);
-      b.ws[u] = raw_buffer_load_u8(sr, 0, wb, 0);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) b.x[u][h] = raw_buffer_load_b128(xr, lane * 32 + 16 * h, kb * 2048, 0);
-      b.xs[u] = raw_buffer_load_u8(xsr, lane & 15, kb * 16, 0);
+    for (int h = 0; h < 2; ++h) {
+      const int row = 8 * h + (lane >> 3);
+      woff[i][h] = (uint32_t)((16 * i + row) * kp + 16 * ((lane & 7) ^ row_swz(row)));
     }
+  const int rd = (lane & 15) * 128 + 16 * ((2 * (lane >> 4)) ^ row_swz(lane & 15));
+
+  const int cnt = wave < nb ? (nb - 1 - wave) / kGvWaves + 1 : 0;
+  auto issue = [&](int j, char* R, Block& b) {
+    const int kb = wave + kGvWaves * (j < cnt ? j : cnt - 1);  // past the range: the last block again
+    char* const dst = R + wave * kSlot;
+#pragma unroll
+    for (int i = 0; i < kT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) copy16(wr, woff[i][h], kb * kF8Block, dst + i * 2048 + h * 1024);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) b.x[h] = raw_buffer_load_b128(xr, lane * 32 + 16 * h, kb * 2048, 0);
+    b.xs = raw_buffer_load_u8(xsr, lane & 15, kb * 16, 0);
+    b.ws = raw_buffer_load_u8(sr, 0, kb, 0);
   };
   f32x4 acc[kT];
 #pragma unroll
   for (int i = 0; i < kT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](const Batch<kT>& b) {
+  auto compute = [&](const char* R, const Block& b) {
+    const char* const src = R + wave * kSlot + rd;
+    const char* const src2 = R + wave * kSlot + (rd ^ 16);
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int i = 0; i < kT; ++i)
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(b.x[u][0], b.x[u][1]),
-                                                                  join(b.w[u][i][0], b.w[u][i][1]), acc[i], 0, 0, 0,
-                                                                  (int)b.xs[u], 0, (int)b.ws[u]);
+    for (int i = 0; i < kT; ++i)
+      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          join(b.x[0], b.x[1]),
+          join(*reinterpret_cast<const u32x4*>(src + i * 2048), *reinterpret_cast<const u32x4*>(src2 + i * 2048)), acc[i],
+          0, 0, 0, (int)b.xs, 0, (int)b.ws);
   };
-  const int cnt = (nb + kGvWaves * kU - 1) / (kGvWaves * kU);  // batches
-  Batch<kT> b0, b1;
-  load(0, b0);
+  Block s0, s1, s2;
+  if (cnt > 0) {
+    issue(0, ring0, s0);
+    issue(1, ring1, s1);
+  }
   for (int o = t; o < (int)M * r; o += 64 * kGvWaves) {
     float s = T[o];
     for (int p = 1; p < parts; ++p) s += T[(int64_t)p * M * r + o];
     Ts[o] = s;
     if (T_save != nullptr && blockIdx.x == 0) T_save[o] = s;
   }
-  for (int j = 0; j < cnt; j += 2) {
-    load(j + 1, b1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(b0);
-    load(j + 2, b0);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(b1);
+  if (cnt > 0) {
+    // whole groups of three with no exit inside (an exit leaves a path on which
+    // the compiler waits for every load in flight)
+    int j = 0;
+    for (; j + 3 <= cnt; j += 3) {
+      issue(j + 2, ring2, s2);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(ring0, s0);
+      __builtin_amdgcn_sched_barrier(0);
+      issue(j + 3, ring0, s0);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(ring1, s1);
+      __builtin_amdgcn_sched_barrier(0);
+      issue(j + 4, ring1, s1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(ring2, s2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (j < cnt) compute(ring0, s0);
+    if (j + 1 < cnt) compute(ring1, s1);
   }
+  // copies past the range may still be landing: done before the ring is reused
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  float(*const red)[kT][16][16] = reinterpret_cast<float(*)[kT][16][16]>(ring0);  // [wave]
+  static_assert(sizeof(float) * kGvWaves * kT * 256 <= kGvWaves * kSlot, "partials fit the ring");
 
   // D[m][n]: lane -> n = lane % 16, m = 4 (lane / 16) + v
 #pragma unroll
   for (int i = 0; i < kT; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v) red[wave][i][4 * (lane >> 4) + v][lane & 15] = acc[i][v];
-  __syncthreads();  // T
   if (r > 0 && wave < kT) {
     // L[m][n] = sum_j T[m][j] B[n][j], 4 ranks per fp32 MFMA (T and B exact)
     const int i = wave;

@@ -151,6 +151,15 @@ hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, cons
                                 uint16_t* out, float* part, hipStream_t stream, const uint8_t* mask = nullptr,
                                 float keep_scale = 1.0f, bool f16 = false, bool nn = false);
 
+// Ranks padded to what the kernels that take factors in operand order are built for.
+inline int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+// A factor (layout 0: [r, C], 1: [C, r]) in operand order [Cp / 32][rank_pad(r)
+// / 16][64 lanes][16 bytes], zero past C (Cp: a multiple of 32); Q1's (not NULL)
+// after it.
+size_t operand_order_bytes(int64_t Cp, int r);
+hipError_t launch_operand_order(const uint16_t* Q, const uint16_t* Q1, int layout, int64_t C, int64_t Cp, int r,
+                                uint16_t* out, hipStream_t stream);
+
 // [k, lora_extra_cols(r)] rows of A^T: row c = [A[:, c] | A[:, c] | 0].
 hipError_t launch_lowrank_rows_t(const uint16_t* A, int r, int64_t k, uint16_t* out, hipStream_t stream);
 
@@ -239,18 +248,15 @@ hipError_t launch_fp8_encode(const void* W, int dt, int64_t n, int64_t k, uint8_
 hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream);
 // Activations P [M, C] -> codes and scales ([M, C up to 128] and the GEMM's
 // scale words; few, M <= 16: the GEMV's operand order, fp8_gemv_*_bytes),
-// and for r > 0 the partials [splits][M][r] of P Q^T, Q [r, ldq] rank-major
-// (ldq % 8 == 0; columns past C are not read or zero).
+// and for r > 0 the partials [splits][M][r] of P Q^T; Q in operand order, for
+// few as it is, [r, C].
 struct Fp8Prep {
   int chunk, splits;
 };
 Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few);
 size_t fp8_rows_scale_bytes(int64_t M, int64_t C);
-hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int64_t ldq, int r,
+hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r,
                            uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16);
-// B [n, r] -> rank-major rows [r, ld], zero past n; B1's (not NULL) after them.
-hipError_t launch_rank_major(const uint16_t* B, const uint16_t* B1, int64_t n, int r, int64_t ld, uint16_t* out,
-                             hipStream_t stream);
 // The weight's codes as [k, n up to 128] rows for dX.
 hipError_t launch_fp8_transpose(const Fp8View& w, uint8_t* out, hipStream_t stream);
 // out = RN16([act | split] [f | fx]^T); f's scale byte of (output block,
