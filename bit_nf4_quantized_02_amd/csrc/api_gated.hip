@@ -38,8 +38,7 @@ bool dx_fits(int64_t M, int64_t n, int64_t k, int r) {
 }
 
 struct FwdWs {
-  float* T = nullptr;
-  void* xp = nullptr;      // few tokens: activations in the GEMV's operand order
+  void* few = nullptr;     // few tokens: the GEMV's operands
   void* proj = nullptr;
   uint16_t* TS = nullptr;  // low-rank columns of the GEMM
   uint16_t* F = nullptr;   // both weights expanded
@@ -47,13 +46,12 @@ struct FwdWs {
 };
 
 size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
-  if (r > 0) o.proj = cv.take<char>(rowdot_ws_bytes(M, k, r));
   if (few_tokens(M, n, k)) {
-    if (r > 0) o.T = cv.take<float>((size_t)2 * M * r * 4);
-    o.xp = cv.take<char>(gemv_ws_bytes(k));
+    o.few = cv.take<char>(gemv_pair_ws_bytes(M, k, r));
     return cv.used;
   }
   const int xc = gated_extra_cols(r);
+  if (r > 0) o.proj = cv.take<char>(rowdot_ws_bytes(M, k, r));
   if (r > 0) o.TS = cv.take<uint16_t>((size_t)M * xc * 2);
   o.F = cv.take<uint16_t>(gated_fwd_operand_bytes(n, k, r));
   o.part = cv.take<float>(gemm_bf16_ws_bytes(M, k, xc, gated_rows(n)));
@@ -132,19 +130,11 @@ qlora_status qlora_gated_fwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
   const uint16_t* const x = u16(X);
   uint16_t *const h = static_cast<uint16_t*>(H), *const gs = static_cast<uint16_t*>(G_save),
            *const us = static_cast<uint16_t*>(U_save);
+  if (few_tokens(M, n, k))
+    return hip_status(launch_gemv_pair(g, u, x, M, u16(A_gate), u16(B_gate), u16(A_up), u16(B_up), r, scale, h, gs, us,
+                                       T_save, o.few, st, f16));
   float* const proj = static_cast<float*>(o.proj);
   hipError_t e = hipSuccess;
-  if (few_tokens(M, n, k)) {
-    float* const T = T_save ? T_save : o.T;
-    if (r > 0) {
-      e = launch_rowdot(x, M, k, u16(A_gate), 0, r, T, nullptr, scale, proj, st, nullptr, f16);
-      if (e == hipSuccess)
-        e = launch_rowdot(x, M, k, u16(A_up), 0, r, T + M * r, nullptr, scale, proj, st, nullptr, f16);
-    }
-    if (e == hipSuccess)
-      e = launch_gemv_pair(g, u, x, M, T, u16(B_gate), u16(B_up), r, scale, h, gs, us, o.xp, st, f16);
-    return hip_status(e);
-  }
   const int xc = gated_extra_cols(r);
   if (r > 0) {
     e = launch_rowdot(x, M, k, u16(A_gate), 0, r, T_save, o.TS, scale, proj, st, nullptr, f16, 2 * r, xc);

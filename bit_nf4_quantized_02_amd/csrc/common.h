@@ -205,9 +205,13 @@ __device__ __forceinline__ u32x4 load8h(const uint16_t* __restrict__ row, int64_
   } else if (c + 8 <= n) {
     v = *reinterpret_cast<const u32x4_any*>(row + c);
   } else {
+    // eight loads from inside the row, whatever is past its end cleared after
+    // them (a load behind a test of its own waits for the one before it)
     uint32_t e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = c + i < n ? (uint32_t)row[c + i] : 0u;
+    for (int i = 0; i < 8; ++i) e[i] = row[c + i < n ? c + i : n - 1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = c + i < n ? e[i] : 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = e[2 * i] | (e[2 * i + 1] << 16);
   }

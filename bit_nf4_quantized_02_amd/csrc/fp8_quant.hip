@@ -181,7 +181,9 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         if constexpr (kFew) {
-          q[t][s] = load8h<true>(qrow[t], (int64_t)kb * kF8Block + 32 * s + 8 * (lane >> 4), C);
+          const int64_t c = (int64_t)kb * kF8Block + 32 * s + 8 * (lane >> 4);
+          q[t][s] = (int64_t)(kb + 1) * kF8Block <= C ? *reinterpret_cast<const u32x4*>(qrow[t] + c)
+                                                      : load8h<true>(qrow[t], c, C);
         } else {
           q[t][s] = reinterpret_cast<const u32x4*>(Q)[((int64_t)(kb * 4 + s) * kTiles + t) * 64 + lane];
         }
@@ -313,13 +315,14 @@ size_t fp8_rows_scale_bytes(int64_t M, int64_t C) {
   return (size_t)(f8_pad(C) / kF8Block) * (size_t)f8_pad(M);
 }
 
-// Column ranges: about 1024 workgroups; few rows: about 32 (their projections'
-// partials are added by every workgroup of the GEMV).
+// Column ranges: about 1024 workgroups, at most 32 ranges; few rows: one block
+// per wave, at most 64 ranges (the GEMV adds their partials).
 Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few) {
   const int64_t nb = f8_pad(C) / kF8Block;
   int64_t s = few ? cdiv(nb, (int64_t)4) : cdiv((int64_t)1024, cdiv(M, (int64_t)kPrepRows));
   if (s > nb) s = nb;
-  if (s > 32) s = 32;
+  const int64_t most = few ? 64 : 32;
+  if (s > most) s = most;
   const int64_t chunk = cdiv(nb, s);
   return Fp8Prep{(int)chunk, (int)cdiv(nb, chunk)};
 }

@@ -109,16 +109,98 @@ struct GvStage {
   u32x4 xa[8];
 };
 
-// The up weight of the gated block (kPair), its low-rank factors and the
-// block's outputs (the kernel's own weight is the gate; Y receives H; G and U
-// may be NULL).
+// The gated block (kPair): X [M, K] for few tokens in operand order (xp not
+// NULL), and the projections X Ag^T, X Au^T as partials [range][2][M][r]. A
+// wave takes 128-column blocks in turn: 16 neighbouring lanes load 256 bytes of
+// a row, which pass through the wave's own LDS into the A operand of
+// v_mfma_f32_16x16x32; the workgroup's four waves are added in wave order. The
+// blocks cover whole 256-column chunks (zeros past K), as the GEMV reads them.
+template <int kRP, bool kF16>
+__global__ __launch_bounds__(256) void gemv_prep_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K, int nb,
+                                                        const uint16_t* __restrict__ Ag, const uint16_t* __restrict__ Au,
+                                                        int r, int bchunk, u32x4* __restrict__ xp,
+                                                        float* __restrict__ part) {
+  constexpr int kTiles = kRP / 16, kTA = kTiles > 0 ? kTiles : 1;
+  constexpr int kPitch = 256 + 16;
+  __shared__ __attribute__((aligned(16))) char turn[4][kTiles > 0 ? 16 * kPitch : 16];
+  __shared__ float red[4][16][kTiles > 0 ? kRP : 1];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int b0 = (int)blockIdx.x * bchunk, b1 = b0 + bchunk < nb ? b0 + bchunk : nb;
+  const int lr = lane >> 4, lc = 8 * (lane & 15);
+  f32x4 acc[2][kTA];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int t = 0; t < kTA; ++t) acc[w][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int kb = b0 + wave; kb < b1; kb += 4) {
+    u32x4 x[4], q[2][kTA][4];
+    // (whole blocks load without a test per lane, which would put each load
+    // behind a branch that waits for it)
+    const bool whole = ((int64_t)kb + 1) * 128 <= K;
+    const uint16_t* const xb = X + (int64_t)kb * 128 + lc;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t m = 4 * u + lr < M ? 4 * u + lr : M - 1;
+      x[u] = whole ? *reinterpret_cast<const u32x4*>(xb + m * K) : load8h<true>(X + m * K, (int64_t)kb * 128 + lc, K);
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int64_t j = 16 * t + (lane & 15) < r ? 16 * t + (lane & 15) : r - 1;  // (ranks past r: not stored)
+        const int64_t c = (int64_t)kb * 128 + 32 * s + 8 * (lane >> 4);
+        q[0][t][s] = whole ? *reinterpret_cast<const u32x4*>(Ag + j * K + c) : load8h<true>(Ag + j * K, c, K);
+        q[1][t][s] = whole ? *reinterpret_cast<const u32x4*>(Au + j * K + c) : load8h<true>(Au + j * K, c, K);
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int m = 4 * u + lr;
+      if (m >= M) x[u] = u32x4{0u, 0u, 0u, 0u};
+      if (xp != nullptr) {
+        const int c = (kb & 1) * 128 + lc;  // column of the 256-column chunk
+        xp[((int64_t)(kb >> 1) * 8 + ((c >> 3) & 7)) * 64 + 16 * (c >> 6) + m] = x[u];
+      }
+      if constexpr (kTiles > 0) *reinterpret_cast<u32x4*>(turn[wave] + m * kPitch + 2 * lc) = x[u];
+    }
+    // lanes read what others wrote: the LDS keeps a wave's order, the compiler must too
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int s = 0; s < (kTiles > 0 ? 4 : 0); ++s) {
+      const bf16x8 a = *reinterpret_cast<const bf16x8*>(turn[wave] + (lane & 15) * kPitch + 64 * s + 16 * (lane >> 4));
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) acc[w][t] = mfma16<kF16>(a, __builtin_bit_cast(bf16x8, q[w][t][s]), acc[w][t]);
+    }
+    asm volatile("" ::: "memory");
+  }
+  if constexpr (kTiles > 0) {
+    for (int w = 0; w < 2; ++w) {
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          red[wave][4 * (lane >> 4) + v][16 * t + (lane & 15)] = w == 0 ? acc[0][t][v] : acc[1][t][v];
+      __syncthreads();
+      for (int o = threadIdx.x; o < (int)M * r; o += 256) {
+        const int m = o / r, j = o % r;
+        part[(((int64_t)blockIdx.x * 2 + w) * M + m) * r + j] = red[0][m][j] + red[1][m][j] + red[2][m][j] + red[3][m][j];
+      }
+    }
+  }
+}
+
+// The up weight of the gated block (kPair), its low-rank factor and the
+// block's outputs (the kernel's own weight is the gate, its T holds both
+// projections [2][M][r], Y receives H; G and U may be NULL).
 struct GvSecond {
   const uint8_t* codes;
   const uint8_t* code8;
   const float* s2;
   const float* mean;
   const float* codebook;
-  const float* T;
   const uint16_t* B;
   uint16_t* G;
   uint16_t* U;
@@ -381,11 +463,10 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
       f32x4 l = f32x4{0.f, 0.f, 0.f, 0.f};
       const int m = lane & 15;
       const int64_t n = n0 + (kPair ? 0 : i * 16) + (lane & 15);
-      const float* const Ti = kPair && i == 1 ? up.T : T;
       const uint16_t* const Bi = kPair && i == 1 ? up.B : B;
       for (int j0 = 0; j0 < r; j0 += 4) {
         const int j = j0 + (lane >> 4);
-        const float a = (m < M && j < r) ? Ti[m * r + j] : 0.0f;
+        const float a = (m < M && j < r) ? T[((kPair ? i * M : 0) + m) * r + j] : 0.0f;
         const float b = (n < N && j < r) ? from16<kF16>(Bi[n * r + j]) : 0.0f;
         l = __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, l, 0, 0, 0);
       }
@@ -474,17 +555,51 @@ hipError_t launch_gemv(const Nf4View& w, const uint16_t* X, int64_t M, const flo
   return hipGetLastError();
 }
 
-hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const float* T,
-                            const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* H, uint16_t* G,
-                            uint16_t* U, void* ws, hipStream_t stream, bool f16) {
+// Column ranges of the block's projections: about one 128-column block per wave,
+// at most 16 workgroups. (A small kernel adds their partials: added in the
+// epilogue by every workgroup of the GEMV, they took 24 us at 28672 x 8192 where
+// the launch takes 3, and the LDS has no room to add them at its start.)
+struct PairPlan {
+  int nb, chunk, parts;
+};
+
+PairPlan pair_plan(int64_t k) {
+  const int nb = (int)(2 * cdiv(k, (int64_t)256));
+  const int chunk = cdiv(nb, 16) > 4 ? (int)cdiv(nb, 16) : 4;
+  return PairPlan{nb, chunk, (int)cdiv(nb, chunk)};
+}
+
+size_t gemv_pair_ws_bytes(int64_t M, int64_t k, int r) {
+  const PairPlan p = pair_plan(k);
+  return gemv_ws_bytes(k) + align256((size_t)p.parts * 2 * M * r * 4) + align256((size_t)2 * M * r * 4);
+}
+
+hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const uint16_t* Ag,
+                            const uint16_t* Bg, const uint16_t* Au, const uint16_t* Bu, int r, float scale, uint16_t* H,
+                            uint16_t* G, uint16_t* U, float* T_save, void* ws, hipStream_t stream, bool f16) {
   if (!gemv_fits(g.n, g.k)) return hipErrorInvalidValue;
   u32x4* Xp = static_cast<u32x4*>(ws);
+  const PairPlan pl = pair_plan(g.k);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + gemv_ws_bytes(g.k));
   const bool xp = M >= kXpMinM && g.n >= kXpMinN;
-  if (xp) {
-    const int64_t entries = cdiv(g.k, (int64_t)256) * 512;
-    gemv_xperm_kernel<<<(unsigned)cdiv(entries, (int64_t)256), 256, 0, stream>>>(X, M, g.k, Xp, entries);
+  if (xp || r > 0) {
+#define QLORA_GPREP2(RP, H16) \
+  gemv_prep_kernel<RP, H16><<<(unsigned)pl.parts, 256, 0, stream>>>(X, M, g.k, pl.nb, Ag, Au, r, pl.chunk, xp ? Xp : nullptr, part)
+#define QLORA_GPREP(RP) { if (f16) QLORA_GPREP2(RP, true); else QLORA_GPREP2(RP, false); }
+    if (r == 0) QLORA_GPREP(0)
+    else if (r <= 16) QLORA_GPREP(16)
+    else if (r <= 32) QLORA_GPREP(32)
+    else if (r <= 64) QLORA_GPREP(64)
+    else QLORA_GPREP(128)
+#undef QLORA_GPREP
+#undef QLORA_GPREP2
   }
-  const GvSecond up{u.codes, u.code8, u.s2, u.mean, u.codebook, T ? T + M * r : nullptr, Bu, G, U};
+  float* const T = T_save ? T_save : part + align256((size_t)pl.parts * 2 * M * r * 4) / 4;
+  if (r > 0) {
+    const hipError_t e = launch_rowdot_finalize(part, pl.parts, 2 * M, r, T, nullptr, scale, stream, f16);
+    if (e != hipSuccess) return e;
+  }
+  const GvSecond up{u.codes, u.code8, u.s2, u.mean, u.codebook, Bu, G, U};
   // four waves (two workgroups per CU) where there are at least two per CU, else eight
   const int64_t wgs = cdiv(g.n, (int64_t)16);
   const int form = g.code8 ? 0 : (g.s2_bf16 ? 2 : 1);

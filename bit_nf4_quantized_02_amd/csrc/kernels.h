@@ -200,10 +200,11 @@ hipError_t launch_gemv_dx(const Nf4View& w, const uint16_t* dY, int64_t M, const
                           float keep = 1.0f);
 
 // ---- the gated feed-forward block H = silu(G) U over two NF4 weights
-// Both T = X Ag^T, X Au^T as [2][M][r]. G and U may be NULL. ws: gemv_ws_bytes(k).
-hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const float* T,
-                            const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* H, uint16_t* G,
-                            uint16_t* U, void* ws, hipStream_t stream, bool f16);
+// Few tokens (M <= 16). G, U and T_save ([2][M][r]) may be NULL.
+size_t gemv_pair_ws_bytes(int64_t M, int64_t k, int r);
+hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const uint16_t* Ag,
+                            const uint16_t* Bg, const uint16_t* Au, const uint16_t* Bu, int r, float scale, uint16_t* H,
+                            uint16_t* G, uint16_t* U, float* T_save, void* ws, hipStream_t stream, bool f16);
 // Low-rank columns of the block's GEMMs, [hi_g | lo_g | hi_u | lo_u | 0].
 inline int gated_extra_cols(int r) { return r > 0 ? ((4 * r + 63) / 64) * 64 : 0; }
 // Both weights expanded for the forward: rows in groups of 64, 32 gate rows

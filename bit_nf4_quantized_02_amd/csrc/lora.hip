@@ -177,14 +177,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void c
         st.p[i] = *reinterpret_cast<const u32x4*>(P + ml * C + cpl);
         if constexpr (kMask) st.mk[i] = *reinterpret_cast<const uint2*>(pmask + ml * C + cpl);
       } else {
-        st.p[i] = u32x4{0u, 0u, 0u, 0u};
-        if (m < m1) {
-          uint32_t e[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) e[x] = (cp + x < C) ? (uint32_t)P[m * C + cp + x] : 0u;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) st.p[i][x] = e[2 * x] | (e[2 * x + 1] << 16);
-        }
+        st.p[i] = load8h<false>(P + (m < m1 ? m : m1 - 1) * C, cp, C);
       }
     }
 #pragma unroll
