@@ -35,14 +35,24 @@ __device__ __forceinline__ uint32_t f8_finite_abs(float x) {
   return a >= 0x7F800000u ? 0u : a;
 }
 
-// Four values times inv -> four E4M3 bytes; an infinity is stored as NaN (the
-// format has none), so it stays visible in every product it enters.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// Largest of the 16 lanes of a row (lanes 16 q .. 16 q + 15), in all of them:
+// rotations within the row by 8, 4, 2 and 1.
+__device__ __forceinline__ uint32_t row16_max(uint32_t a) {
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x128, 0xF, 0xF, true));
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x124, 0xF, 0xF, true));
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x122, 0xF, 0xF, true));
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x121, 0xF, 0xF, true));
+  return a;
+}
+
+// Four values times inv -> four E4M3 bytes. None is infinite: the callers
+// have made NaN of infinities (the format has none), so that they stay visible
+// in every product they enter.
 __device__ __forceinline__ uint32_t f8_pack4(const float* x, float inv) {
-  float v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = isinf(x[i]) ? __uint_as_float(0x7FC00000u) : x[i] * inv;
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inv, x[1] * inv, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inv, x[3] * inv, w, true);
   return (uint32_t)w;
 }
 

@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "fp8.h"
+#include "gemm_tile.h"
 #include "kernels.h"
 
 namespace qlora {
@@ -62,10 +63,14 @@ __global__ __launch_bounds__(256) void fp8_encode_kernel(const void* __restrict_
     const int64_t r = r0 + 16 * i;
     load8f<kDt, true>(W, (r < n ? r : n - 1) * k, c, k, f[i]);  // rows past n repeat the last one (not stored)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a = max(a, f8_finite_abs(f[i][e]));
+    for (int e = 0; e < 8; ++e) {
+      a = max(a, f8_finite_abs(f[i][e]));
+      f[i][e] = isinf(f[i][e]) ? __uint_as_float(0x7FC00000u) : f[i][e];
+    }
   }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) a = max(a, (uint32_t)__shfl_xor((int)a, d));
+  a = row16_max(a);
+  a = max(a, (uint32_t)__shfl_xor((int)a, 16));
+  a = max(a, (uint32_t)__shfl_xor((int)a, 32));
   if ((t & 63) == 0) wmax[t >> 6] = a;
   __syncthreads();
   a = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
@@ -115,8 +120,9 @@ __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restri
 //   kFew = false: codes [M, Cp] (zero past C) and the GEMM's scale words, one
 // per (128-column block, 128-row tile, row % 32) with the bytes of rows +0,
 // +32, +64, +96, so that a wave of the GEMM gets the scales of its four
-// 32-row operand blocks with one load. Q in operand order. A wave holds 32
-// rows; the workgroup's four walk the blocks of one column range.
+// 32-row operand blocks with one load. A wave holds 32
+// rows; the workgroup's four walk the blocks of one column range and share Q's,
+// which are copied (in operand order) into LDS one block ahead.
 //   kFew = true (M <= 16): codes in the GEMV's operand order [block][lane][32
 // bytes] (lane: row lane % 16, bytes 32 (lane / 16) ..; zeros past M), scales
 // [block][16]; Q [r, C] as it is. The four waves take the range's blocks in
@@ -132,10 +138,13 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
   constexpr int kPitch = 256 + 16;  // bytes per staged row (16 rows on distinct banks)
   typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
   __shared__ __attribute__((aligned(16))) char turn[4][kTiles > 0 ? 16 * kPitch : 16];
+  // Q of a block, [32-column step][rank tile][1 KB], two blocks in two arrays
+  // (so that the compiler can tell the one being filled)
+  __shared__ __attribute__((aligned(16))) char fac0[kTiles > 0 && !kFew ? kTiles * 4096 : 16];
+  __shared__ __attribute__((aligned(16))) char fac1[kTiles > 0 && !kFew ? kTiles * 4096 : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t m0 = kFew ? 0 : (int64_t)blockIdx.x * kPrepRows + wave * 16 * kMR;
-  if (!kFew && m0 >= M) return;
   const int nb = (int)(Cp / kF8Block);
   const int b0 = (int)blockIdx.y * bchunk, b1 = b0 + bchunk < nb ? b0 + bchunk : nb;
   constexpr int kStep = kFew ? 4 : 1;
@@ -171,24 +180,32 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
         for (int u = 0; u < 4; ++u) x[i][u] = load8h<kVec>(prow[i][u], c, C);
     }
   };
-  u32x4 x[kMR][4], nx[kMR][4];
-  const int kb0 = kFew ? b0 + wave : b0;
-  if (kb0 < b1) load(kb0, x);
-  for (int kb = kb0; kb < b1; kb += kStep) {
-    u32x4 q[kTA][4];
+  const i32x4 qrs = make_rsrc(Q, (int64_t)nb * kTiles * 4096);
+  auto copy_q = [&](int kb, char* fac) {  // this wave's share: the block's 32-column step `wave`
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
+      copy16(qrs, (uint32_t)lane * 16, (kb * 4 + wave) * kTiles * 1024 + t * 1024, fac + (wave * kTiles + t) * 1024);
+  };
+  auto block = [&](int kb, const char* fac, char* next, u32x4 (&x)[kMR][4], u32x4 (&nx)[kMR][4]) {
+    const int kn = kb + kStep < b1 ? kb + kStep : kb;
+    u32x4 q[kFew ? kTA : 1][4];
+    if constexpr (kFew) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if constexpr (kFew) {
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
           const int64_t c = (int64_t)kb * kF8Block + 32 * s + 8 * (lane >> 4);
           q[t][s] = (int64_t)(kb + 1) * kF8Block <= C ? *reinterpret_cast<const u32x4*>(qrow[t] + c)
                                                       : load8h<true>(qrow[t], c, C);
-        } else {
-          q[t][s] = reinterpret_cast<const u32x4*>(Q)[((int64_t)(kb * 4 + s) * kTiles + t) * 64 + lane];
         }
-      }
-    load(kb + kStep < b1 ? kb + kStep : kb, nx);
+    } else if constexpr (kTiles > 0) {
+      // this block's Q has landed, and every wave is done with the buffer the
+      // next goes to (the eight loads issued after it, or stores after those,
+      // may still be in flight)
+      gt::step_barrier<4>();
+      copy_q(kn, next);
+    }
+    load(kn, nx);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < kMR; ++i) {
@@ -199,18 +216,31 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
         if constexpr (kTiles > 0)
           *reinterpret_cast<u32x4*>(turn[wave] + (4 * u + lr) * kPitch + 2 * lc) = x[i][u];
         if (codes != nullptr) {
+          // the row's largest magnitude, from the 16-bit patterns (two at a
+          // time, then the 16 lanes of the row by rotations within them)
+          u16x2 top = {0, 0};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[i][u][e] & 0x7FFF7FFFu));
+          uint32_t h = max((uint32_t)top[0], (uint32_t)top[1]);
+          h = row16_max(h);
           float f[8];
-          uint32_t a = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             f[2 * e] = from16<kF16>(x[i][u][e] & 0xFFFFu);
             f[2 * e + 1] = from16<kF16>(x[i][u][e] >> 16);
           }
+          if (__builtin_expect(__ballot(h >= (kF16 ? 0x7C00u : 0x7F80u)) != 0, 0)) {
+            // a value of some row is not finite: the maximum without such values
+            uint32_t a = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) a = max(a, f8_finite_abs(f[e]));
-#pragma unroll
-          for (int d = 1; d < 16; d *= 2) a = max(a, (uint32_t)__shfl_xor((int)a, d));
-          const uint32_t b = f8_scale_byte(a);
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t v = f8_finite_abs(f[e]) != 0 ? (x[i][u][e >> 1] >> (16 * (e & 1))) & 0x7FFFu : 0u;
+              a = max(a, v);
+              if (isinf(f[e])) f[e] = __uint_as_float(0x7FC00000u);
+            }
+            h = row16_max(a);
+          }
+          const uint32_t b = f8_scale_byte(__float_as_uint(from16<kF16>(h)));
           const float inv = f8_inv_scale(b);
           const u32x2 o = {f8_pack4(f, inv), f8_pack4(f + 4, inv)};
           if constexpr (kFew) {
@@ -230,14 +260,25 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
       for (int s = 0; s < (kTiles > 0 ? 4 : 0); ++s) {
         const bf16x8 pa = *reinterpret_cast<const bf16x8*>(turn[wave] + (lane & 15) * kPitch + 64 * s + 16 * (lane >> 4));
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) acc[i][t] = mfma16<kF16>(pa, __builtin_bit_cast(bf16x8, q[t][s]), acc[i][t]);
+        for (int t = 0; t < kTiles; ++t) {
+          if constexpr (kFew)
+            acc[i][t] = mfma16<kF16>(pa, __builtin_bit_cast(bf16x8, q[t][s]), acc[i][t]);
+          else
+            acc[i][t] = mfma16<kF16>(pa, *reinterpret_cast<const bf16x8*>(fac + (s * kTiles + t) * 1024 + lane * 16), acc[i][t]);
+        }
       }
       asm volatile("" ::: "memory");
     }
-#pragma unroll
-    for (int i = 0; i < kMR; ++i)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) x[i][u] = nx[i][u];
+  };
+  u32x4 x0[kMR][4], x1[kMR][4];
+  const int kb0 = kFew ? b0 + wave : b0;
+  if (kb0 < b1) {
+    if constexpr (!kFew) copy_q(kb0, fac0);
+    load(kb0, x0);
+  }
+  for (int kb = kb0; kb < b1; kb += 2 * kStep) {
+    block(kb, fac0, fac1, x0, x1);
+    if (kb + kStep < b1) block(kb + kStep, fac1, fac0, x1, x0);
   }
   // D layout: lane -> rank lane % 16, rows 4 (lane / 16) + v
   if constexpr (kRP > 0 && kFew) {
@@ -263,6 +304,8 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
           if (m < M && j < r) part[((int64_t)blockIdx.y * M + m) * r + j] = acc[i][t][v];
         }
   }
+  // (copies of the repeated last block may still be landing: done before the workgroup's LDS is another's)
+  __builtin_amdgcn_s_waitcnt(0);
 }
 
 // Weight codes [n, kp] -> [k, np] (np: n up to a multiple of 128, zero past

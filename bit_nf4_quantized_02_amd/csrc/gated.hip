@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "gemm_tile.h"
 #include "kernels.h"
 
 namespace qlora {
@@ -141,6 +142,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&p)[parts_of<
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       p[q][w] = pack2<kF16>(rem[2 * w], rem[2 * w + 1]);
+      asm("" : "+v"(p[q][w]));  // (unpacked from here, not converted a second time)
       rem[2 * w] -= from16<kF16>(p[q][w] & 0xFFFFu);
       rem[2 * w + 1] -= from16<kF16>(p[q][w] >> 16);
     }
@@ -157,131 +159,151 @@ __device__ __forceinline__ void join8(const u32x4& g, const u32x4& u, const u32x
                from16<kF16>((dh[w] >> (16 * h)) & 0xFFFFu), dg[2 * w + h], du[2 * w + h]);
 }
 
-constexpr int kJoinMR = 2;     // 16-row tiles per wave
-constexpr int kJoinWaves = 4;  // each with rows of its own
-constexpr int kJoinRows = 16 * kJoinMR * kJoinWaves;
+constexpr int kJoinWaves = 4;                // 16 rows each
+constexpr int kJoinRows = 16 * kJoinWaves;
 
-// A wave holds 32 rows and walks its workgroup's columns 32 at a time: four
-// neighbouring lanes load 64 bytes of a row, dG and dU are formed in that
-// layout and written rounded to D, and their parts pass through the wave's own
-// LDS into the A operand of v_mfma_f32_16x16x32 (lane: row lane % 16, columns
-// 8 (lane / 16) ..) against the factors in operand order. (Loaded in operand
-// layout, neighbouring lanes lie in different rows: 55 cache accesses per load,
-// 340 us at 4096 x 22016, r = 64.) kRP: ranks padded (0: no adapters, D only).
+// A wave holds 16 rows and walks its workgroup's columns 64 at a time: eight
+// neighbouring lanes load the 128 bytes of a row's line, dG and dU are formed
+// in that layout and written rounded to D, and their parts pass one by one
+// through the wave's own LDS into the A operand of v_mfma_f32_16x16x32 (lane:
+// row lane % 16, columns 8 (lane / 16) ..). The step's factors, which the four
+// waves share, are copied into LDS one step ahead. (Loaded straight in operand
+// layout neighbouring lanes lie in different rows, 55 cache accesses per load:
+// 340 us at 4096 x 22016, r = 64; in half lines, with the factors read by each
+// wave: 276.) kRP: ranks padded (0: no adapters, D only).
 template <int kRP, bool kF16, bool kVec>
 __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
     const uint16_t* __restrict__ G, const uint16_t* __restrict__ U, const uint16_t* __restrict__ dH, int64_t M, int64_t n,
-    int64_t np, const u32x4* __restrict__ Bo, int r, int64_t cchunk, uint16_t* __restrict__ D,
+    int64_t np, const uint16_t* __restrict__ Bo, int r, int64_t cchunk, uint16_t* __restrict__ D,
     float* __restrict__ part) {
-  constexpr int kTiles = kRP / 16;
+  constexpr int kTiles = kRP / 16, kTA = kTiles > 0 ? kTiles : 1;
   constexpr int kP = parts_of<kF16>();
   typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
-  // [wave][w][part][16 rows x 64 bytes], 16-byte piece p of row i at p ^ (i / 4 % 4)
-  __shared__ __attribute__((aligned(16))) char turn[kJoinWaves][kTiles > 0 ? 2 * kP * 1024 : 16];
+  // factors of a step: [w][32-column half][rank tile][1 KB], two steps in two
+  // arrays (so that the compiler can tell the one being filled)
+  __shared__ __attribute__((aligned(16))) char fac0[kTA * 4096];
+  __shared__ __attribute__((aligned(16))) char fac1[kTA * 4096];
+  // [wave][two buffers][16 rows x 128 bytes], 16-byte piece p of row i at p ^ (i / 2)
+  __shared__ __attribute__((aligned(16))) char turn[kJoinWaves][2][kTiles > 0 ? 2048 : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m0 = (int64_t)blockIdx.x * kJoinRows + wave * 16 * kJoinMR;
-  if (m0 >= M) return;
+  const int64_t m0 = (int64_t)blockIdx.x * kJoinRows + wave * 16;
   const int64_t cbeg = (int64_t)blockIdx.y * cchunk;
   const int64_t cend = cbeg + cchunk < np ? cbeg + cchunk : np;
-  const int lr = lane >> 2, co = 8 * (lane & 3);  // loads: row lr, columns co ..
-  char* const wr = turn[wave] + lr * 64 + (((lane & 3) ^ ((lr >> 2) & 3)) << 4);
-  const char* const rd = turn[wave] + (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 2) & 3)) << 4);
-  int64_t off[kJoinMR];  // row offsets (rows past M repeat the last one; not stored)
+  const int lr = lane >> 3, co = 8 * (lane & 7);  // loads: rows lr and lr + 8, columns co ..
+  const int wr0 = lr * 128 + (((lane & 7) ^ (lr >> 1)) << 4), wr1 = (lr + 8) * 128 + (((lane & 7) ^ ((lr + 8) >> 1)) << 4);
+  const int rrow = lane & 15;
+  const int rd0 = rrow * 128 + (((lane >> 4) ^ (rrow >> 1)) << 4), rd1 = rrow * 128 + (((4 + (lane >> 4)) ^ (rrow >> 1)) << 4);
+  int64_t off[2];  // row offsets (rows past M repeat the last one; not stored)
+  bool in[2];
 #pragma unroll
-  for (int i = 0; i < kJoinMR; ++i) {
-    const int64_t m = m0 + 16 * i + lr;
-    off[i] = (m < M ? m : M - 1) * n;
+  for (int u = 0; u < 2; ++u) {
+    const int64_t m = m0 + 8 * u + lr;
+    in[u] = m < M;
+    off[u] = (m < M ? m : M - 1) * n + co;
   }
-  f32x4 acc[2][kJoinMR][kTiles > 0 ? kTiles : 1];
+  f32x4 acc[2][kTA];
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int i = 0; i < kJoinMR; ++i)
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) acc[w][i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < kTA; ++t) acc[w][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   struct Stage {
-    u32x4 g[kJoinMR], u[kJoinMR], d[kJoinMR];
+    u32x4 g[2], u[2], d[2];
   };
   // whole steps load without a test per lane (a test would put each load behind
   // a branch that waits for it)
   auto load = [&](int64_t c, Stage& s) {
-    if (c + 32 <= n) {
+    if (c + 64 <= n) {
 #pragma unroll
-      for (int i = 0; i < kJoinMR; ++i) {
-        s.g[i] = *reinterpret_cast<const Vec*>(G + off[i] + c + co);
-        s.u[i] = *reinterpret_cast<const Vec*>(U + off[i] + c + co);
-        s.d[i] = *reinterpret_cast<const Vec*>(dH + off[i] + c + co);
+      for (int u = 0; u < 2; ++u) {
+        s.g[u] = *reinterpret_cast<const Vec*>(G + c + off[u]);
+        s.u[u] = *reinterpret_cast<const Vec*>(U + c + off[u]);
+        s.d[u] = *reinterpret_cast<const Vec*>(dH + c + off[u]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kJoinMR; ++i) {
-        s.g[i] = load8h<kVec>(G + off[i], c + co, n);
-        s.u[i] = load8h<kVec>(U + off[i], c + co, n);
-        s.d[i] = load8h<kVec>(dH + off[i], c + co, n);
+      for (int u = 0; u < 2; ++u) {
+        s.g[u] = load8h<kVec>(G + off[u] - co, c + co, n);
+        s.u[u] = load8h<kVec>(U + off[u] - co, c + co, n);
+        s.d[u] = load8h<kVec>(dH + off[u] - co, c + co, n);
       }
     }
   };
-  const u32x4* const bo1 = Bo + (np / 32) * kTiles * 64;  // the up factor
-  Stage cur, nxt;
-  load(cbeg, cur);
-  for (int64_t c = cbeg; c < cend; c += 32) {
-    // the factors first: waiting for them must not wait for the next step's loads
-    u32x4 b[2][kTiles > 0 ? kTiles : 1];
+  // this wave's share of a step's factors: weight wave / 2, half wave % 2
+  const i32x4 brs = make_rsrc(Bo, np / 32 * kTiles * 2048);
+  auto copy_factors = [&](int64_t c, char* fac) {
+    const uint32_t at = (uint32_t)(((wave >> 1) * (np / 32) + (c >> 5) + (wave & 1)) * kTiles * 1024);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      b[0][t] = Bo[((c >> 5) * kTiles + t) * 64 + lane];
-      b[1][t] = bo1[((c >> 5) * kTiles + t) * 64 + lane];
-    }
-    load(c + 32 < cend ? c + 32 : c, nxt);
+    for (int t = 0; t < kTiles; ++t)
+      copy16(brs, (uint32_t)lane * 16, (int)(at + t * 1024), fac + (wave * kTiles + t) * 1024);
+  };
+  auto step = [&](int64_t c, const char* fac, char* next, Stage& cur, Stage& nxt) {
+    // the factors of this step have landed, and every wave is done with the
+    // buffer that the next ones go to (the six loads issued after them, or the
+    // stores after those, may still be in flight)
+    if constexpr (kTiles > 0) gt::step_barrier<4>();
+    const int64_t cn = c + 64 < cend ? c + 64 : c;
+    copy_factors(cn, next);
+    load(cn, nxt);
     __builtin_amdgcn_sched_barrier(0);
+    float x[2][2][8];  // [row half][w]
 #pragma unroll
-    for (int i = 0; i < kJoinMR; ++i) {
-      float dg[8], du[8];
-      join8<kF16>(cur.g[i], cur.u[i], cur.d[i], dg, du);
+    for (int u = 0; u < 2; ++u) join8<kF16>(cur.g[u], cur.u[u], cur.d[u], x[u][0], x[u][1]);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
       u32x4 p[2][kP];
-      split8<kF16>(dg, p[0]);
-      split8<kF16>(du, p[1]);
-      const int64_t m = m0 + 16 * i + lr;
-      if (D != nullptr && m < M) {
-        *reinterpret_cast<u32x4*>(D + m * 2 * np + c + co) = p[0][0];
-        *reinterpret_cast<u32x4*>(D + m * 2 * np + np + c + co) = p[1][0];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        split8<kF16>(x[u][w], p[u]);
+        if (D != nullptr && in[u])
+          *reinterpret_cast<u32x4*>(D + (m0 + 8 * u + lr) * 2 * np + w * np + c + co) = p[u][0];
       }
       if constexpr (kTiles > 0) {
+        bf16x8 b[2][kTA];
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(wr + (w * kP + q) * 1024) = p[w][q];
-        // lanes read what others wrote: the LDS keeps a wave's order, the
-        // compiler must too
-        asm volatile("" ::: "memory");
+          for (int t = 0; t < kTiles; ++t)
+            b[h][t] = *reinterpret_cast<const bf16x8*>(fac + lane * 16 + ((w * 2 + h) * kTiles + t) * 1024);
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int q = kP - 1; q >= 0; --q) {
+          char* const buf = turn[wave][(w * kP + q) & 1];
+          *reinterpret_cast<u32x4*>(buf + wr0) = p[0][q];
+          *reinterpret_cast<u32x4*>(buf + wr1) = p[1][q];
+          // lanes read what others wrote: the LDS keeps a wave's order, the
+          // compiler must too
+          asm volatile("" ::: "memory");
+          const bf16x8 a0 = *reinterpret_cast<const bf16x8*>(buf + rd0), a1 = *reinterpret_cast<const bf16x8*>(buf + rd1);
+          asm volatile("" ::: "memory");
 #pragma unroll
-          for (int q = kP - 1; q >= 0; --q) {
-            const bf16x8 a = *reinterpret_cast<const bf16x8*>(rd + (w * kP + q) * 1024);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-              acc[w][i][t] = mfma16<kF16>(a, __builtin_bit_cast(bf16x8, b[w][t]), acc[w][i][t]);
+          for (int t = 0; t < kTiles; ++t) {
+            acc[w][t] = mfma16<kF16>(a0, b[0][t], acc[w][t]);
+            acc[w][t] = mfma16<kF16>(a1, b[1][t], acc[w][t]);
           }
-        asm volatile("" ::: "memory");
+        }
       }
     }
-    cur = nxt;
+  };
+  Stage s0, s1;
+  copy_factors(cbeg, fac0);
+  load(cbeg, s0);
+  for (int64_t c = cbeg; c < cend; c += 128) {
+    step(c, fac0, fac1, s0, s1);
+    if (c + 64 < cend) step(c + 64, fac1, fac0, s1, s0);
   }
   // partials [split][w][M][r]; D layout: lane -> rank lane % 16, rows 4 (lane / 16) + v
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int i = 0; i < kJoinMR; ++i)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int64_t m = m0 + 16 * i + 4 * (lane >> 4) + v;
-          const int j = 16 * t + (lane & 15);
-          if (m < M && j < r) part[(((int64_t)blockIdx.y * 2 + w) * M + m) * r + j] = acc[w][i][t][v];
-        }
+      for (int v = 0; v < 4; ++v) {
+        const int64_t m = m0 + 4 * (lane >> 4) + v;
+        const int j = 16 * t + (lane & 15);
+        if (m < M && j < r) part[(((int64_t)blockIdx.y * 2 + w) * M + m) * r + j] = acc[w][t][v];
+      }
+  // (copies of the repeated last step may still be landing: done before the workgroup's LDS is another's)
+  __builtin_amdgcn_s_waitcnt(0);
 }
 
 // P = the partials added in split order; split row m = [hi_g | lo_g | hi_u |
@@ -394,13 +416,14 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
     u32x4 g, u, d;
   };
   const bool inside = c0 + kDbCols <= n;
+  const uint32_t lane_at = (uint32_t)(prow * n + 8 * (t & 7));
   auto load = [&](int64_t mb, Stage& s) {
     const int64_t m = mb + prow;
     const int64_t o = (m < m1 ? m : m1 - 1) * n;
-    if (inside) {
-      s.g = *reinterpret_cast<const Vec*>(G + o + pc);
-      s.u = *reinterpret_cast<const Vec*>(U + o + pc);
-      s.d = *reinterpret_cast<const Vec*>(dH + o + pc);
+    if (inside && mb + 32 <= m1) {  // (uniform base, the lane's offset in 32 bits)
+      s.g = *reinterpret_cast<const Vec*>(G + (mb * n + c0) + lane_at);
+      s.u = *reinterpret_cast<const Vec*>(U + (mb * n + c0) + lane_at);
+      s.d = *reinterpret_cast<const Vec*>(dH + (mb * n + c0) + lane_at);
     } else {
       s.g = load8h<kVec>(G + o, pc, n);
       s.u = load8h<kVec>(U + o, pc, n);
@@ -498,8 +521,8 @@ __global__ __launch_bounds__(256) void gated_db_reduce_kernel(const float* __res
   dB[i] = accumulate ? dB[i] + scale * s : scale * s;
 }
 
-// Column ranges of the join: about 1024 workgroups (each a multiple of 32
-// columns, at least 64; at most 32 ranges, whose partials are added later).
+// Column ranges of the join: about 1024 workgroups (each a multiple of 64
+// columns; at most 32 ranges, whose partials are added later).
 struct JoinPlan {
   int64_t cchunk;
   int splits;
@@ -510,7 +533,7 @@ JoinPlan join_plan(int64_t M, int64_t n) {
   int64_t s = cdiv((int64_t)1024, cdiv(M, (int64_t)kJoinRows));
   if (s > np / 64) s = np / 64;
   if (s > 32) s = 32;
-  const int64_t cchunk = cdiv(cdiv(np, s), (int64_t)32) * 32;
+  const int64_t cchunk = cdiv(cdiv(np, s), (int64_t)64) * 64;
   return {cchunk, (int)cdiv(np, cchunk)};
 }
 
@@ -593,7 +616,7 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
   }
   const dim3 grid((unsigned)cdiv(M, (int64_t)kJoinRows), (unsigned)pl.splits);
 #define QLORA_JOIN2(RP, H, V) \
-  gated_join_kernel<RP, H, V><<<grid, 64 * kJoinWaves, 0, stream>>>(G, U, dH, M, n, np, reinterpret_cast<const u32x4*>(Bo), r, pl.cchunk, D, part)
+  gated_join_kernel<RP, H, V><<<grid, 64 * kJoinWaves, 0, stream>>>(G, U, dH, M, n, np, Bo, r, pl.cchunk, D, part)
 #define QLORA_JOIN(RP)                                                              \
   {                                                                                 \
     if (n % 8 == 0) { if (f16) QLORA_JOIN2(RP, true, true); else QLORA_JOIN2(RP, false, true); } \
