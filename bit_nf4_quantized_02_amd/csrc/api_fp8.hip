@@ -90,7 +90,7 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
     o.T = cv.take<float>((size_t)M * r * 4);
     const size_t p1 = (size_t)fp8_prep_plan(M, n, false).splits * M * r * 4, p2 = rowdot_ws_bytes(M, k, r);
     o.proj = cv.take<float>(p1 > p2 ? p1 : p2);
-    const size_t g1 = coldot_ws_bytes(M, k, r), g2 = coldot_ws_bytes(M, n, r);
+    const size_t g1 = colgrad_ws_bytes(M, k, r, 1), g2 = colgrad_ws_bytes(M, n, r, 1);
     o.grad = cv.take<char>(g1 > g2 ? g1 : g2);
   }
   o.part = cv.take<float>(gemm_fp8_ws_bytes(M, n, k));
@@ -213,7 +213,6 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
   const bool f16 = dtype == QLORA_DT_FP16;
   const uint16_t *x = static_cast<const uint16_t*>(X), *dy = static_cast<const uint16_t*>(dY),
                  *a = static_cast<const uint16_t*>(A), *b = static_cast<const uint16_t*>(B);
-  float* const grad = static_cast<float*>(o.grad);
   if (dX || dA) {
     if (r > 0) e = launch_operand_order(b, nullptr, 1, n, f8_pad(n), r, o.Bo, st);
     if (e == hipSuccess)
@@ -230,14 +229,14 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
       e = launch_gemm_fp8(o.yq, o.ys, M, n, o.US, lora_extra_cols(r), o.wt, w->scale, 1, kb, (f8_pad(n) / kF8Block) * kb,
                           o.Ax, k, static_cast<uint16_t*>(dX), o.part, st, f16);
   }
-  if (e == hipSuccess && dA) e = launch_coldot(x, M, k, o.U, r, scale, dA, 1, k, accumulate, grad, st, nullptr, f16, /*fine=*/true);
+  if (e == hipSuccess && dA) e = launch_colgrad(x, M, k, o.U, 1, r, scale, dA, nullptr, true, accumulate, o.grad, st, f16);
   if (e == hipSuccess && dB) {
     const float* T = T_saved;
     if (T == nullptr) {
       e = launch_rowdot(x, M, k, a, 0, r, o.T, nullptr, scale, o.proj, st, nullptr, f16);
       T = o.T;
     }
-    if (e == hipSuccess) e = launch_coldot(dy, M, n, T, r, scale, dB, r, 1, accumulate, grad, st, nullptr, f16, /*fine=*/true);
+    if (e == hipSuccess) e = launch_colgrad(dy, M, n, T, 1, r, scale, dB, nullptr, false, accumulate, o.grad, st, f16);
   }
   return hip_status(e);
 }

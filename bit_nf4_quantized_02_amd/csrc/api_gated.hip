@@ -79,7 +79,7 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
     o.P = cv.take<float>((size_t)2 * M * r * 4);
     o.PS = cv.take<uint16_t>((size_t)M * xc * 2);
     o.proj = cv.take<char>(rowdot_ws_bytes(M, k, r));
-    o.grad = cv.take<char>(coldot_ws_bytes(M, k, r));
+    o.grad = cv.take<char>(colgrad_ws_bytes(M, k, r, 2));
     o.join = cv.take<char>(gated_join_ws_bytes(M, n, r));
     o.db = cv.take<char>(gated_db_ws_bytes(M, n, r));
   }
@@ -183,7 +183,7 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
   const int xc = gated_extra_cols(r);
   const int64_t np = gated_pad(n);
   const uint16_t* const x = u16(X);
-  float *const proj = static_cast<float*>(o.proj), *const grad = static_cast<float*>(o.grad);
+  float* const proj = static_cast<float*>(o.proj);
   if (dX || need_a)
     e = launch_gated_join(u16(G), u16(U), u16(dH), M, n, u16(B_gate), u16(B_up), r, scale, dX ? o.D : nullptr, o.P,
                           dX ? o.PS : nullptr, o.join, st, f16);
@@ -194,11 +194,8 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
       e = launch_gemm_bf16_ext(o.D, M, 2 * np, r > 0 ? o.PS : nullptr, xc, o.F, k, o.F + 2 * np * k, k, k,
                                static_cast<uint16_t*>(dX), o.part, st, nullptr, 1.0f, f16, /*nn=*/true);
   }
-  for (int w = 0; w < 2; ++w) {
-    float* const dA = w == 0 ? dA_gate : dA_up;
-    if (e == hipSuccess && dA)
-      e = launch_coldot(x, M, k, o.P + w * M * r, r, scale, dA, 1, k, accumulate, grad, st, nullptr, f16, /*fine=*/true);
-  }
+  if (e == hipSuccess && need_a)
+    e = launch_colgrad(x, M, k, o.P, 2, r, scale, dA_gate, dA_up, true, accumulate, o.grad, st, f16);
   if (e == hipSuccess && need_b) {
     const float* T = T_saved;
     if (T == nullptr) {

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "colgrad.h"
 #include "gemm_tile.h"
 #include "kernels.h"
 
@@ -119,33 +120,6 @@ __device__ __forceinline__ void join_bwd(float g, float u, float dh, float& dg, 
   const float sg = fast_sigmoid(g), si = g * sg;
   dg = dh * u * fmaf(si, 1.0f - sg, sg);
   du = dh * si;
-}
-
-// Eight fp32 values -> kParts 16-bit parts whose sum holds 24 (bf16, three)
-// or 22 (fp16, two) bits of each.
-template <bool kF16>
-constexpr int parts_of() { return kF16 ? 2 : 3; }
-
-template <bool kF16>
-__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&p)[parts_of<kF16>()]) {
-  float rem[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    rem[e] = x[e];
-    // one fp32 value from here on: folded into the operation that made x, the
-    // fp16 conversion stored and the one subtracted were rounded from
-    // different values and a step apart for one element in 10^5
-    asm("" : "+v"(rem[e]));
-  }
-#pragma unroll
-  for (int q = 0; q < parts_of<kF16>(); ++q)
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      p[q][w] = pack2<kF16>(rem[2 * w], rem[2 * w + 1]);
-      asm("" : "+v"(p[q][w]));  // (unpacked from here, not converted a second time)
-      rem[2 * w] -= from16<kF16>(p[q][w] & 0xFFFFu);
-      rem[2 * w + 1] -= from16<kF16>(p[q][w] >> 16);
-    }
 }
 
 // dG and dU of eight adjacent elements.
@@ -337,52 +311,6 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
 
 // ------------------------------------------------------ adapter gradients dB
 
-// T [2][M][r] -> Tt [32-token step][part][w][rank tile][lane][16 bytes], the A
-// operand of dB's products: lane l holds rank 16 t + l % 16, tokens 8 (l / 16)
-// .. +7 of the step, zero past M and r.
-template <bool kF16>
-__global__ __launch_bounds__(256) void gated_tt_kernel(const float* __restrict__ T, int64_t M, int r, int tiles,
-                                                       u32x4* __restrict__ out) {
-  __shared__ float tile[32][kMaxRank + 1];
-  const int w = blockIdx.y;
-  const int64_t m0 = (int64_t)blockIdx.x * 32;
-  for (int i = threadIdx.x; i < 32 * r; i += 256) {
-    const int64_t m = m0 + i / r;
-    tile[i / r][i % r] = m < M ? T[(w * M + m) * r + i % r] : 0.0f;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tiles * 64; i += 256) {
-    const int j = 16 * (i >> 6) + (i & 15);
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = j < r ? tile[8 * ((i >> 4) & 3) + e][j] : 0.0f;
-    u32x4 p[parts_of<kF16>()];
-    split8<kF16>(x, p);
-#pragma unroll
-    for (int q = 0; q < parts_of<kF16>(); ++q)
-      out[(((int64_t)blockIdx.x * parts_of<kF16>() + q) * 2 + w) * tiles * 64 + i] = p[q];
-  }
-}
-
-constexpr int kDbCols = 64;             // columns per workgroup
-constexpr int kDbTile = 32 * kDbCols * 2;  // bytes of one staged part
-
-// Staged tile [32 tokens][64 columns]: the 32-byte segment s of row i is kept
-// at s ^ f(i), f(i) = bit 1 of i + 2 (bit 3 of i), so that the eight rows that
-// one cycle of a transposing read touches lie on distinct banks.
-__device__ __forceinline__ int db_seg(int row, int s) { return row * 128 + ((s ^ (((row >> 1) & 1) | ((row >> 2) & 2))) << 5); }
-
-// B operand (8 tokens of one column per lane) of column tile s from such a tile
-__device__ __forceinline__ bf16x8 db_operand(const char* tile, int s, int lane) {
-  const int row = 8 * (lane >> 4) + ((lane & 15) >> 2);
-  const char* const p = tile + db_seg(row, s) + 8 * (lane & 3);
-  const char* const p4 = tile + db_seg(row + 4, s) + 8 * (lane & 3);
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p4));
-  const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  return __builtin_bit_cast(bf16x8, v);
-}
-
 // Partial of dB over tokens [m0, m1): rows = ranks, columns = block columns.
 // Each 32-token step every thread forms dG and dU of one row's 8 columns and
 // stages their parts as [token][column] tiles in LDS (two sets, one barrier
@@ -508,19 +436,6 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
       }
 }
 
-// dB (+)= scale * (partials added in split order)
-__global__ __launch_bounds__(256) void gated_db_reduce_kernel(const float* __restrict__ part, int splits, int64_t count,
-                                                              float scale, float* __restrict__ dBg,
-                                                              float* __restrict__ dBu, int accumulate) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int w = blockIdx.y;
-  float* const dB = w == 0 ? dBg : dBu;
-  if (i >= count || dB == nullptr) return;
-  float s = part[w * count + i];
-  for (int p = 1; p < splits; ++p) s += part[(p * 2 + w) * count + i];
-  dB[i] = accumulate ? dB[i] + scale * s : scale * s;
-}
-
 // Column ranges of the join: about 1024 workgroups (each a multiple of 64
 // columns; at most 32 ranges, whose partials are added later).
 struct JoinPlan {
@@ -550,9 +465,6 @@ DbPlan db_plan(int64_t M, int64_t n) {
   const int64_t mchunk = cdiv(cdiv(M, s), (int64_t)32) * 32;
   return {mchunk, (int)cdiv(M, mchunk)};
 }
-
-// T's parts in operand order (three at most).
-size_t db_t_bytes(int64_t M, int r) { return (size_t)cdiv(M, (int64_t)32) * 3 * 2 * rank_pad(r) * 64; }
 
 PairView pair_view(const Nf4View& w, const uint16_t* lr) {
   return PairView{reinterpret_cast<const uint32_t*>(w.codes), w.code8, w.s2, w.mean, w.codebook, lr};
@@ -642,7 +554,7 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
 
 size_t gated_db_ws_bytes(int64_t M, int64_t n, int r) {
   if (r == 0) return 0;
-  return align256(db_t_bytes(M, r)) + align256((size_t)db_plan(M, n).splits * 2 * r * (size_t)n * 4);
+  return align256(rank_parts_bytes(M, r, 2)) + align256((size_t)db_plan(M, n).splits * 2 * r * (size_t)n * 4);
 }
 
 hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
@@ -651,12 +563,9 @@ hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t*
   const DbPlan pl = db_plan(M, n);
   const int rp = rank_pad(r);
   u32x4* const Tt = static_cast<u32x4*>(ws);
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(db_t_bytes(M, r)));
-  const dim3 tg((unsigned)cdiv(M, (int64_t)32), 2);
-  if (f16)
-    gated_tt_kernel<true><<<tg, 256, 0, stream>>>(T, M, r, rp / 16, Tt);
-  else
-    gated_tt_kernel<false><<<tg, 256, 0, stream>>>(T, M, r, rp / 16, Tt);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(rank_parts_bytes(M, r, 2)));
+  const hipError_t e = launch_rank_parts(T, 2, M, r, Tt, stream, f16);
+  if (e != hipSuccess) return e;
   const dim3 grid((unsigned)cdiv(n, (int64_t)kDbCols), (unsigned)pl.splits);
 #define QLORA_DB2(RP, H, V) \
   gated_db_kernel<RP, H, V><<<grid, 256, 0, stream>>>(G, U, dH, M, n, Tt, r, pl.mchunk, part)
@@ -671,9 +580,7 @@ hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t*
   else QLORA_DB(128)
 #undef QLORA_DB
 #undef QLORA_DB2
-  gated_db_reduce_kernel<<<dim3((unsigned)cdiv(n * r, (int64_t)256), 2), 256, 0, stream>>>(part, pl.splits, n * r, scale,
-                                                                                          dBg, dBu, accumulate);
-  return hipGetLastError();
+  return launch_grad_reduce(part, pl.splits, 2, n * r, scale, dBg, dBu, accumulate, stream);
 }
 
 }  // namespace qlora

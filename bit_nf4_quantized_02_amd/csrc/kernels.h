@@ -65,11 +65,10 @@ hipError_t launch_rowdot_finalize(const float* part, int ns, int64_t M, int r, f
 // Column reduction over M in fixed order, for the adapter gradients:
 //   G[c, j] (+)= scale * sum_m P[m, c] * Q[m, j]    P bf16 [M, C], Q fp32 [M, r]
 // written at G[c * g_sc + j * g_sj]. partial (fp32, [splits, C, r]) is workspace.
-// fine (bf16, no mask): Q in three bf16 parts (24 bits) instead of two.
 size_t coldot_ws_bytes(int64_t M, int64_t C, int r);
 hipError_t launch_coldot(const uint16_t* P, int64_t M, int64_t C, const float* Q, int r, float scale,
                          float* G, int64_t g_sc, int64_t g_sj, int accumulate, float* partial,
-                         hipStream_t stream, const uint8_t* pmask = nullptr, bool f16 = false, bool fine = false);
+                         hipStream_t stream, const uint8_t* pmask = nullptr, bool f16 = false);
 // dA and dB of one layer in one launch (both with a single token split, no
 // mask): products (P0, C0, Q0 -> G0 with strides g_sc0, g_sj0) and (P1, ...),
 // the same arithmetic as two launch_coldot calls. coldot_pairable tells when
@@ -198,6 +197,18 @@ size_t gemv_dx_ws_bytes(int64_t n, int64_t k);
 hipError_t launch_gemv_dx(const Nf4View& w, const uint16_t* dY, int64_t M, const float* U, const uint16_t* A, int r,
                           float scale, uint16_t* dX, void* ws, hipStream_t stream, const uint8_t* mask = nullptr,
                           float keep = 1.0f);
+
+// ---- adapter gradients of the feed-forward operators (colgrad.hip)
+// Q fp32 [W][M][r] as 16-bit parts in operand order.
+size_t rank_parts_bytes(int64_t M, int r, int W);
+hipError_t launch_rank_parts(const float* Q, int W, int64_t M, int r, void* out, hipStream_t stream, bool f16);
+// G (+)= scale * partials [splits][W][count] added in order (G1: w = 1; NULL: left out).
+hipError_t launch_grad_reduce(const float* part, int splits, int W, int64_t count, float scale, float* G0, float* G1,
+                              int accumulate, hipStream_t stream);
+// Gw (+)= scale P^T Qw, as [r, C] (j_first; C % 8 == 0, W 1 or 2) or [C, r] (W = 1).
+size_t colgrad_ws_bytes(int64_t M, int64_t C, int r, int W);
+hipError_t launch_colgrad(const uint16_t* P, int64_t M, int64_t C, const float* Q, int W, int r, float scale, float* G0,
+                          float* G1, bool j_first, int accumulate, void* ws, hipStream_t stream, bool f16);
 
 // ---- the gated feed-forward block H = silu(G) U over two NF4 weights
 // Few tokens (M <= 16). G, U and T_save ([2][M][r]) may be NULL.

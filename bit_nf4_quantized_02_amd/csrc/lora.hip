@@ -39,14 +39,13 @@ namespace {
 // MFMAs run.
 constexpr int kColdotDepth64 = 1;  // register stages in flight at ranks 33..64 (more stages cost occupancy)
 
-template <int kRP, int kCW, bool kFine>
+template <int kRP, int kCW>
 struct ColdotSmem {
   static constexpr int kPPitch = 4 * kCW * 2 + 32;  // bytes per staged P row (+ pad)
   static constexpr int kQPitch = kRP * 2 + (kRP >= 32 ? 32 : 0);
   char p[32 * kPPitch];
   char qh[32 * kQPitch];
   char ql[32 * kQPitch];
-  char qx[kFine ? 32 * kQPitch : 16];  // third part of Q (kFine)
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -86,10 +85,7 @@ struct ColdotSecond {
   int64_t g_sc, g_sj;
 };
 
-// kFine: Q in three bf16 parts, i.e. all 24 bits (two leave 2.5e-6 of the
-// gradient's norm, three 1e-7, a third of the MFMAs more).
-template <int kRP, int kCW, bool kVec, bool kMask = false, bool kF16 = false, bool kDirect = false, bool kPair = false,
-          bool kFine = false>
+template <int kRP, int kCW, bool kVec, bool kMask = false, bool kF16 = false, bool kDirect = false, bool kPair = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void coldot_mfma_kernel(
     const uint16_t* __restrict__ P, int64_t M, int64_t C, const float* __restrict__ Q, int r, int64_t mchunk,
     float* __restrict__ partial, const uint8_t* __restrict__ pmask, float scale, float* __restrict__ G, int64_t g_sc,
@@ -107,7 +103,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void c
   constexpr int kCPR = kCW / 2;              // 16-byte chunks per staged P row (4 kCW columns)
   constexpr int kRPT = 256 / kCPR;           // P rows covered by one pass of the 256 threads
   constexpr int kPL = 32 / kRPT;             // P chunks per thread per step
-  using Smem = ColdotSmem<kRP, kCW, kFine>;
+  using Smem = ColdotSmem<kRP, kCW>;
   constexpr int kPP = Smem::kPPitch;
   constexpr int kQP = Smem::kQPitch;
   __shared__ __attribute__((aligned(16))) Smem sm;
@@ -177,7 +173,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void c
         st.p[i] = *reinterpret_cast<const u32x4*>(P + ml * C + cpl);
         if constexpr (kMask) st.mk[i] = *reinterpret_cast<const uint2*>(pmask + ml * C + cpl);
       } else {
-        st.p[i] = load8h<false>(P + (m < m1 ? m : m1 - 1) * C, cp, C);
+        st.p[i] = u32x4{0u, 0u, 0u, 0u};
+        if (m < m1) {
+          uint32_t e[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) e[x] = (cp + x < C) ? (uint32_t)P[m * C + cp + x] : 0u;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) st.p[i][x] = e[2 * x] | (e[2 * x + 1] << 16);
+        }
       }
     }
 #pragma unroll
@@ -222,12 +225,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void c
       const int idx = t + 256 * e;
       const int mm = idx / kRP, j = idx % kRP;
       const uint16_t qh = to16<kF16>(st.q[e]);
-      const float q1 = st.q[e] - from16<kF16>(qh);
-      const uint16_t ql = to16<kF16>(q1);
+      const uint16_t ql = to16<kF16>(st.q[e] - from16<kF16>(qh));
       *reinterpret_cast<uint16_t*>(sm.qh + mm * kQP + j * 2) = qh;
       *reinterpret_cast<uint16_t*>(sm.ql + mm * kQP + j * 2) = ql;
-      if constexpr (kFine)
-        *reinterpret_cast<uint16_t*>(sm.qx + mm * kQP + j * 2) = to16<kF16>(q1 - from16<kF16>(ql));
     }
     __syncthreads();
     if (mb + kDepth * 32 < m1) load(mb + kDepth * 32, st);
@@ -242,11 +242,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void c
       for (int ct = 0; ct < kCT; ++ct) {
         acc[a][ct] = mfma16<kF16>(ah, pb[ct], acc[a][ct]);
         acc[a][ct] = mfma16<kF16>(al, pb[ct], acc[a][ct]);
-      }
-      if constexpr (kFine) {
-        const bf16x8 ax = tr_operand(sm.qx, kQP, a * 16, lane);
-#pragma unroll
-        for (int ct = 0; ct < kCT; ++ct) acc[a][ct] = mfma16<kF16>(ax, pb[ct], acc[a][ct]);
       }
     }
     __syncthreads();
@@ -352,7 +347,7 @@ size_t coldot_ws_bytes(int64_t M, int64_t C, int r) {
 
 hipError_t launch_coldot(const uint16_t* P, int64_t M, int64_t C, const float* Q, int r, float scale, float* G,
                          int64_t g_sc, int64_t g_sj, int accumulate, float* partial, hipStream_t stream,
-                         const uint8_t* pmask, bool f16, bool fine) {
+                         const uint8_t* pmask, bool f16) {
   const int ns = coldot_splits(M, C);
   const int64_t mchunk = cdiv(cdiv(M, ns), 32) * 32;
   const dim3 grid((unsigned)cdiv(C, 4 * kColdotCW), (unsigned)ns);
@@ -362,16 +357,13 @@ hipError_t launch_coldot(const uint16_t* P, int64_t M, int64_t C, const float* Q
   if (pmask != nullptr && !vec) return hipErrorInvalidValue;
   if (pmask != nullptr && f16) return hipErrorInvalidValue;
   const bool direct = ns == 1;
-#define QLORA_COLDOT4(RP, CW, VEC, MASK, F16, D, X)                                                             \
-  coldot_mfma_kernel<RP, CW, VEC, MASK, F16, D, false, X><<<grid, 256, 0, stream>>>(                             \
-      P, M, C, Q, r, mchunk, partial, pmask, scale, G, g_sc, g_sj, accumulate)
-#define QLORA_COLDOT3(RP, CW, VEC, MASK, F16, D) QLORA_COLDOT4(RP, CW, VEC, MASK, F16, D, false)
+#define QLORA_COLDOT3(RP, CW, VEC, MASK, F16, D)                                                                \
+  coldot_mfma_kernel<RP, CW, VEC, MASK, F16, D><<<grid, 256, 0, stream>>>(P, M, C, Q, r, mchunk, partial, pmask, \
+                                                                           scale, G, g_sc, g_sj, accumulate)
 #define QLORA_COLDOT2(RP, CW, D)                                  \
   if (f16 && vec) QLORA_COLDOT3(RP, CW, true, false, true, D);    \
   else if (f16) QLORA_COLDOT3(RP, CW, false, false, true, D);     \
   else if (pmask != nullptr) QLORA_COLDOT3(RP, CW, true, true, false, D); \
-  else if (fine && vec) QLORA_COLDOT4(RP, CW, true, false, false, D, true);  \
-  else if (fine) QLORA_COLDOT4(RP, CW, false, false, false, D, true);        \
   else if (vec) QLORA_COLDOT3(RP, CW, true, false, false, D);     \
   else QLORA_COLDOT3(RP, CW, false, false, false, D);
 #define QLORA_COLDOT(RP)                                  \
@@ -386,7 +378,6 @@ hipError_t launch_coldot(const uint16_t* P, int64_t M, int64_t C, const float* Q
 #undef QLORA_COLDOT
 #undef QLORA_COLDOT2
 #undef QLORA_COLDOT3
-#undef QLORA_COLDOT4
   if (!direct)
     coldot_reduce_kernel<<<(unsigned)cdiv(C * r, 256), 256, 0, stream>>>(partial, C, r, ns, scale, G, g_sc, g_sj,
                                                                         accumulate);
