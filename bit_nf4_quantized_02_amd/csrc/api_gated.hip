@@ -51,7 +51,7 @@ size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
     return cv.used;
   }
   const int xc = gated_extra_cols(r);
-  if (r > 0) o.proj = cv.take<char>(rowdot_ws_bytes(M, k, r));
+  if (r > 0) o.proj = cv.take<char>(gated_project_ws_bytes(M, k, r));
   if (r > 0) o.TS = cv.take<uint16_t>((size_t)M * xc * 2);
   o.F = cv.take<uint16_t>(gated_fwd_operand_bytes(n, k, r));
   o.part = cv.take<float>(gemm_bf16_ws_bytes(M, k, xc, gated_rows(n)));
@@ -78,7 +78,7 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
     o.T = cv.take<float>((size_t)2 * M * r * 4);
     o.P = cv.take<float>((size_t)2 * M * r * 4);
     o.PS = cv.take<uint16_t>((size_t)M * xc * 2);
-    o.proj = cv.take<char>(rowdot_ws_bytes(M, k, r));
+    o.proj = cv.take<char>(gated_project_ws_bytes(M, k, r));
     o.grad = cv.take<char>(colgrad_ws_bytes(M, k, r, 2));
     o.join = cv.take<char>(gated_join_ws_bytes(M, n, r));
     o.db = cv.take<char>(gated_db_ws_bytes(M, n, r));
@@ -133,15 +133,9 @@ qlora_status qlora_gated_fwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
   if (few_tokens(M, n, k))
     return hip_status(launch_gemv_pair(g, u, x, M, u16(A_gate), u16(B_gate), u16(A_up), u16(B_up), r, scale, h, gs, us,
                                        T_save, o.few, st, f16));
-  float* const proj = static_cast<float*>(o.proj);
   hipError_t e = hipSuccess;
   const int xc = gated_extra_cols(r);
-  if (r > 0) {
-    e = launch_rowdot(x, M, k, u16(A_gate), 0, r, T_save, o.TS, scale, proj, st, nullptr, f16, 2 * r, xc);
-    if (e == hipSuccess)
-      e = launch_rowdot(x, M, k, u16(A_up), 0, r, T_save ? T_save + M * r : nullptr, o.TS + 2 * r, scale, proj, st,
-                        nullptr, f16, xc - 2 * r, xc);
-  }
+  if (r > 0) e = launch_gated_project(x, M, k, u16(A_gate), u16(A_up), r, scale, T_save, o.TS, o.proj, st, f16);
   if (e == hipSuccess) e = launch_gated_expand_fwd(g, u, u16(B_gate), u16(B_up), r, o.F, st, f16);
   if (e == hipSuccess) e = launch_gemm_gated(x, M, k, o.TS, xc, o.F, n, h, gs, us, o.part, st, f16);
   return hip_status(e);
@@ -183,7 +177,6 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
   const int xc = gated_extra_cols(r);
   const int64_t np = gated_pad(n);
   const uint16_t* const x = u16(X);
-  float* const proj = static_cast<float*>(o.proj);
   if (dX || need_a)
     e = launch_gated_join(u16(G), u16(U), u16(dH), M, n, u16(B_gate), u16(B_up), r, scale, dX ? o.D : nullptr, o.P,
                           dX ? o.PS : nullptr, o.join, st, f16);
@@ -199,9 +192,7 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
   if (e == hipSuccess && need_b) {
     const float* T = T_saved;
     if (T == nullptr) {
-      e = launch_rowdot(x, M, k, u16(A_gate), 0, r, o.T, nullptr, scale, proj, st, nullptr, f16);
-      if (e == hipSuccess)
-        e = launch_rowdot(x, M, k, u16(A_up), 0, r, o.T + M * r, nullptr, scale, proj, st, nullptr, f16);
+      e = launch_gated_project(x, M, k, u16(A_gate), u16(A_up), r, scale, o.T, nullptr, o.proj, st, f16);
       T = o.T;
     }
     if (e == hipSuccess)

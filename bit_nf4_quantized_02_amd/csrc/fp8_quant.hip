@@ -127,7 +127,8 @@ __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restri
 // bytes] (lane: row lane % 16, bytes 32 (lane / 16) ..; zeros past M), scales
 // [block][16]; Q [r, C] as it is. The four waves take the range's blocks in
 // turn and their projections are added in wave order.
-// Partials of the projection go to part [range][M][r]; codes NULL: only those.
+// Partials of the projection go to part [range][factor][M][r] (blockIdx.z: one of
+// several factors, each over all of P); codes NULL: only those.
 template <int kRP, bool kF16, bool kVec, bool kFew>
 __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restrict__ P, int64_t M, int64_t C, int64_t Cp,
                                                        const uint16_t* __restrict__ Q, int r, int bchunk,
@@ -145,6 +146,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t m0 = kFew ? 0 : (int64_t)blockIdx.x * kPrepRows + wave * 16 * kMR;
+  const int64_t range = (int64_t)blockIdx.y * gridDim.z + blockIdx.z;  // partials: column range, then factor
   const int nb = (int)(Cp / kF8Block);
   const int b0 = (int)blockIdx.y * bchunk, b1 = b0 + bchunk < nb ? b0 + bchunk : nb;
   constexpr int kStep = kFew ? 4 : 1;
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
         for (int u = 0; u < 4; ++u) x[i][u] = load8h<kVec>(prow[i][u], c, C);
     }
   };
-  const i32x4 qrs = make_rsrc(Q, (int64_t)nb * kTiles * 4096);
+  const i32x4 qrs = make_rsrc(Q + (int64_t)blockIdx.z * nb * kTiles * 2048, (int64_t)nb * kTiles * 4096);
   auto copy_q = [&](int kb, char* fac) {  // this wave's share: the block's 32-column step `wave`
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
@@ -290,7 +292,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
     __syncthreads();
     for (int o = threadIdx.x; o < (int)M * r; o += 256) {
       const int m = o / r, j = o % r;
-      part[((int64_t)blockIdx.y * M + m) * r + j] = red[0][m][j] + red[1][m][j] + red[2][m][j] + red[3][m][j];
+      part[(range * M + m) * r + j] = red[0][m][j] + red[1][m][j] + red[2][m][j] + red[3][m][j];
     }
   } else {
 #pragma unroll
@@ -301,7 +303,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
         for (int v = 0; v < 4; ++v) {
           const int64_t m = m0 + 16 * i + 4 * (lane >> 4) + v;
           const int j = 16 * t + (lane & 15);
-          if (m < M && j < r) part[((int64_t)blockIdx.y * M + m) * r + j] = acc[i][t][v];
+          if (m < M && j < r) part[(range * M + m) * r + j] = acc[i][t][v];
         }
   }
   // (copies of the repeated last block may still be landing: done before the workgroup's LDS is another's)
@@ -358,11 +360,14 @@ size_t fp8_rows_scale_bytes(int64_t M, int64_t C) {
   return (size_t)(f8_pad(C) / kF8Block) * (size_t)f8_pad(M);
 }
 
-// Column ranges: about 1024 workgroups, at most 32 ranges; few rows: one block
-// per wave, at most 64 ranges (the GEMV adds their partials).
-Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few) {
+// Column ranges: about 512 workgroups (1024 writes and reads twice the
+// partials: 4096 x 22016, r = 64 93 against 84 us with the sum after it, 256
+// 105), for two factors 512 in both together (512 each: 23 against 20 us at
+// 2048 x 4096); at most 32 ranges. Few rows: one block per wave, at most 64
+// ranges (the GEMV adds their partials).
+Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few, int W) {
   const int64_t nb = f8_pad(C) / kF8Block;
-  int64_t s = few ? cdiv(nb, (int64_t)4) : cdiv((int64_t)1024, cdiv(M, (int64_t)kPrepRows));
+  int64_t s = few ? cdiv(nb, (int64_t)4) : cdiv((int64_t)(W == 1 ? 512 : 256), W * cdiv(M, (int64_t)kPrepRows));
   if (s > nb) s = nb;
   const int64_t most = few ? 64 : 32;
   if (s > most) s = most;
@@ -371,11 +376,12 @@ Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few) {
 }
 
 hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r,
-                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16) {
-  const Fp8Prep pl = fp8_prep_plan(M, C, few);
+                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16, int W) {
+  const Fp8Prep pl = fp8_prep_plan(M, C, few, W);
   const int64_t Cp = f8_pad(C);
   if (few && (C % 8 != 0 || M > 16)) return hipErrorInvalidValue;
-  const dim3 grid(few ? 1u : (unsigned)cdiv(M, (int64_t)kPrepRows), (unsigned)pl.splits);
+  if (W > 1 && (few || codes != nullptr)) return hipErrorInvalidValue;
+  const dim3 grid(few ? 1u : (unsigned)cdiv(M, (int64_t)kPrepRows), (unsigned)pl.splits, (unsigned)W);
 #define QLORA_PREP3(RP, H, V, F) \
   fp8_prep_kernel<RP, H, V, F><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, r, pl.chunk, codes, scale, part)
 #define QLORA_PREP2(RP, H)                                                                             \

@@ -15,6 +15,7 @@
 
 #include "common.h"
 #include "colgrad.h"
+#include "fp8.h"
 #include "gemm_tile.h"
 #include "kernels.h"
 
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
   const int w = x >= r ? 1 : 0, j = x - w * r;
   float s = part[(w * M + m) * r + j];
   for (int p = 1; p < splits; ++p) s += part[(((int64_t)p * 2 + w) * M + m) * r + j];
-  P[(w * M + m) * r + j] = s;
+  if (P) P[(w * M + m) * r + j] = s;
   if (split) {
     float v = scale * s;
     asm("" : "+v"(v));  // one value for both conversions (split8)
@@ -508,6 +509,36 @@ hipError_t launch_gated_expand_dx(const Nf4View& g, const Nf4View& u, const uint
   return hipGetLastError();
 }
 
+namespace {
+
+hipError_t launch_p(const float* part, int splits, int64_t M, int r, float scale, float* P, uint16_t* split,
+                    hipStream_t stream, bool f16) {
+  const int xc = gated_extra_cols(r);
+  const unsigned grid = (unsigned)cdiv(M * (xc - 2 * r), (int64_t)256);
+  if (f16)
+    gated_p_kernel<true><<<grid, 256, 0, stream>>>(part, splits, M, r, xc, scale, P, split);
+  else
+    gated_p_kernel<false><<<grid, 256, 0, stream>>>(part, splits, M, r, xc, scale, P, split);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t gated_project_ws_bytes(int64_t M, int64_t k, int r) {
+  return align256(2 * operand_order_bytes(f8_pad(k), r)) +
+         align256((size_t)fp8_prep_plan(M, k, false, 2).splits * 2 * M * r * 4);
+}
+
+hipError_t launch_gated_project(const uint16_t* X, int64_t M, int64_t k, const uint16_t* Ag, const uint16_t* Au, int r,
+                                float scale, float* T, uint16_t* split, void* ws, hipStream_t stream, bool f16) {
+  uint16_t* const Ao = static_cast<uint16_t*>(ws);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(2 * operand_order_bytes(f8_pad(k), r)));
+  hipError_t e = launch_operand_order(Ag, Au, 0, k, f8_pad(k), r, Ao, stream);
+  if (e == hipSuccess) e = launch_fp8_prep(X, M, k, Ao, r, nullptr, nullptr, part, false, stream, f16, 2);
+  if (e == hipSuccess) e = launch_p(part, fp8_prep_plan(M, k, false, 2).splits, M, r, scale, T, split, stream, f16);
+  return e;
+}
+
 size_t gated_join_ws_bytes(int64_t M, int64_t n, int r) {
   if (r == 0) return 0;
   return align256(2 * operand_order_bytes(gated_pad(n), r)) +
@@ -541,14 +572,7 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
   else QLORA_JOIN(128)
 #undef QLORA_JOIN
 #undef QLORA_JOIN2
-  if (r > 0) {
-    const int xc = gated_extra_cols(r);
-    const unsigned pg = (unsigned)cdiv(M * (xc - 2 * r), (int64_t)256);
-    if (f16)
-      gated_p_kernel<true><<<pg, 256, 0, stream>>>(part, pl.splits, M, r, xc, scale, P, split);
-    else
-      gated_p_kernel<false><<<pg, 256, 0, stream>>>(part, pl.splits, M, r, xc, scale, P, split);
-  }
+  if (r > 0) return launch_p(part, pl.splits, M, r, scale, P, split, stream, f16);
   return hipGetLastError();
 }
 

@@ -48,15 +48,13 @@ inline int lora_extra_cols(int r) { return r > 0 ? ((2 * r + 63) / 64) * 64 : 0;
 // out[m, j] = sum_c P[m, c] Q(c, j), P bf16 [M, C]; Q bf16 [r, C] (q_layout
 // 0) or [C, r] (q_layout 1); fp32 out [M, r] (nullable). If split != NULL it
 // also receives rows [bf16(scale*out) | bf16(scale*out - hi) | 0 ...] of
-// lora_extra_cols(r) elements; with split_cols >= 2r the rows are zero-padded
-// to split_cols elements instead and lie split_ld elements apart. part:
-// workspace of rowdot_ws_bytes (may be 0).
+// lora_extra_cols(r) elements. part: workspace of rowdot_ws_bytes (may be 0).
 size_t rowdot_ws_bytes(int64_t M, int64_t C, int r);
 // pmask (uint8 [M, C], q_layout 0 and C % 8 == 0 only; NULL: none): P's
 // elements whose byte is 0 read as zero (dropout on the adapter's input).
 hipError_t launch_rowdot(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int q_layout, int r,
                          float* out, uint16_t* split, float scale, float* part, hipStream_t stream,
-                         const uint8_t* pmask = nullptr, bool f16 = false, int split_cols = 0, int split_ld = 0);
+                         const uint8_t* pmask = nullptr, bool f16 = false);
 
 // out / split (as launch_rowdot's) from partials [ns][M][r], added in order.
 hipError_t launch_rowdot_finalize(const float* part, int ns, int64_t M, int r, float* out, uint16_t* split, float scale,
@@ -218,6 +216,11 @@ hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* 
                             uint16_t* G, uint16_t* U, float* T_save, void* ws, hipStream_t stream, bool f16);
 // Low-rank columns of the block's GEMMs, [hi_g | lo_g | hi_u | lo_u | 0].
 inline int gated_extra_cols(int r) { return r > 0 ? ((4 * r + 63) / 64) * 64 : 0; }
+// X Ag^T and X Au^T: T (NULL: not written) as [2][M][r], and the scaled
+// columns in split (NULL: not written).
+size_t gated_project_ws_bytes(int64_t M, int64_t k, int r);
+hipError_t launch_gated_project(const uint16_t* X, int64_t M, int64_t k, const uint16_t* Ag, const uint16_t* Au, int r,
+                                float scale, float* T, uint16_t* split, void* ws, hipStream_t stream, bool f16);
 // Both weights expanded for the forward: rows in groups of 64, 32 gate rows
 // then the same 32 up rows, [W' | low-rank columns], pitch k + extra.
 inline int64_t gated_rows(int64_t n) { return (n + 31) / 32 * 64; }
@@ -260,15 +263,16 @@ hipError_t launch_fp8_encode(const void* W, int dt, int64_t n, int64_t k, uint8_
 hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream);
 // Activations P [M, C] -> codes and scales ([M, C up to 128] and the GEMM's
 // scale words; few, M <= 16: the GEMV's operand order, fp8_gemv_*_bytes),
-// and for r > 0 the partials [splits][M][r] of P Q^T; Q in operand order, for
-// few as it is, [r, C].
+// and for r > 0 the partials [splits][W][M][r] of P Q^T; W factors in operand
+// order one after the other, for few one as it is, [r, C]. codes NULL (W = 2):
+// the projections only.
 struct Fp8Prep {
   int chunk, splits;
 };
-Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few);
+Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few, int W = 1);
 size_t fp8_rows_scale_bytes(int64_t M, int64_t C);
 hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r,
-                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16);
+                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16, int W = 1);
 // The weight's codes as [k, n up to 128] rows for dX.
 hipError_t launch_fp8_transpose(const Fp8View& w, uint8_t* out, hipStream_t stream);
 // out = RN16([act | split] [f | fx]^T); f's scale byte of (output block,

@@ -86,7 +86,7 @@ struct RowdotCfg {
 template <int kRP, int kQL, bool kVecP, bool kVecQ, bool kDirect, bool kMask = false, bool kF16 = false, int kMR = 1>
 __global__ __launch_bounds__((rowdot_threads<kRP, kMR>())) __attribute__((amdgpu_waves_per_eu(kMR > 1 ? 2 : 1))) void rowdot_kernel(
     const uint16_t* __restrict__ P, int64_t M, int64_t C, const uint16_t* __restrict__ Q, int r, int64_t cchunk,
-    float* __restrict__ out, uint16_t* __restrict__ split, int xc, int ldx, float scale, float* __restrict__ part,
+    float* __restrict__ out, uint16_t* __restrict__ split, int xc, float scale, float* __restrict__ part,
     const uint8_t* __restrict__ pmask = nullptr) {
 #pragma clang fp contract(off)
   using Cfg = RowdotCfg<kRP, kQL, kMR>;
@@ -352,9 +352,9 @@ __global__ __launch_bounds__((rowdot_threads<kRP, kMR>())) __attribute__((amdgpu
         if (col < r && out != nullptr) out[mm * r + j] = s;
         const float ss = scale * s;
         const uint16_t hi = to16<kF16>(ss);
-        split[mm * ldx + col] = col < r ? hi : to16<kF16>(ss - from16<kF16>(hi));
+        split[mm * xc + col] = col < r ? hi : to16<kF16>(ss - from16<kF16>(hi));
       } else {
-        split[mm * ldx + col] = 0;
+        split[mm * xc + col] = 0;
       }
     }
     else {
@@ -387,8 +387,7 @@ __global__ __launch_bounds__((rowdot_threads<kRP, kMR>())) __attribute__((amdgpu
 template <bool kF16>
 __global__ __launch_bounds__(256) void rowdot_finalize_kernel(const float* __restrict__ part, int64_t M, int r,
                                                               int64_t nsplit, float* __restrict__ out,
-                                                              uint16_t* __restrict__ split, int xc, int ldx,
-                                                              float scale) {
+                                                              uint16_t* __restrict__ split, int xc, float scale) {
 #pragma clang fp contract(off)
   __shared__ float gsum[256];
   __shared__ float tot[kMaxRankPad];
@@ -426,7 +425,7 @@ __global__ __launch_bounds__(256) void rowdot_finalize_kernel(const float* __res
         const uint16_t hi = to16<kF16>(ss);
         v = col < r ? hi : to16<kF16>(ss - from16<kF16>(hi));
       }
-      split[m * ldx + col] = v;
+      split[m * xc + col] = v;
     }
   }
 }
@@ -472,22 +471,23 @@ RowdotPlan rowdot_plan(int64_t M, int64_t C, int r) {
 template <int kRP, int kQL, int kMR>
 hipError_t launch_rp(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r, float* out,
                      uint16_t* split, float scale, float* part, hipStream_t stream, const uint8_t* pmask, bool f16,
-                     int ns, int xc, int ldx) {
+                     int ns) {
   constexpr int kNW = RowdotCfg<kRP, kQL, kMR>::kNW;
   constexpr int kRows = RowdotCfg<kRP, kQL, kMR>::kRows;
   const int64_t cchunk = cdiv(cdiv(C, (int64_t)ns), (int64_t)32) * 32;
   const dim3 grid((unsigned)cdiv(M, (int64_t)kRows), (unsigned)ns);
+  const int xc = lora_extra_cols(r);
   const bool vp = C % 8 == 0;
   const bool vq = kQL == 0 ? (C % 8 == 0) : (r % 8 == 0);
 #define QLORA_RD(VP, VQ, D)                                                                                \
   rowdot_kernel<kRP, kQL, VP, VQ, D, false, false, kMR><<<grid, kNW * 64, 0, stream>>>(P, M, C, Q, r, cchunk, \
-                                                                                      out, split, xc, ldx, scale, part)
+                                                                                      out, split, xc, scale, part)
 #define QLORA_RDM(VQ, D)                                                                                   \
   rowdot_kernel<kRP, 0, true, VQ, D, true, false, kMR><<<grid, kNW * 64, 0, stream>>>(P, M, C, Q, r, cchunk, out, \
-                                                                                     split, xc, ldx, scale, part, pmask)
+                                                                                     split, xc, scale, part, pmask)
 #define QLORA_RDF(VP, VQ, D)                                                                               \
   rowdot_kernel<kRP, kQL, VP, VQ, D, false, true, kMR><<<grid, kNW * 64, 0, stream>>>(P, M, C, Q, r, cchunk, out, \
-                                                                                     split, xc, ldx, scale, part)
+                                                                                     split, xc, scale, part)
 #define QLORA_RD2(D)                                           \
   if (f16) {                                                   \
     if (pmask != nullptr) return hipErrorInvalidValue;         \
@@ -522,22 +522,21 @@ hipError_t launch_rp(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q,
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (f16)
-    rowdot_finalize_kernel<true><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, ldx, scale);
+    rowdot_finalize_kernel<true><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, scale);
   else
-    rowdot_finalize_kernel<false><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, ldx, scale);
+    rowdot_finalize_kernel<false><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, scale);
   return hipGetLastError();
 }
 
 template <int kRP, int kQL>
 hipError_t launch_rq(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r, float* out,
-                     uint16_t* split, float scale, float* part, hipStream_t stream, const uint8_t* pmask, bool f16,
-                     int xc, int ldx) {
+                     uint16_t* split, float scale, float* part, hipStream_t stream, const uint8_t* pmask, bool f16) {
   const RowdotPlan pl = rowdot_plan(M, C, r);
   if constexpr (kRP <= 64) {
     if (pl.mr > 1)
-      return launch_rp<kRP, kQL, kTallMR>(P, M, C, Q, r, out, split, scale, part, stream, pmask, f16, pl.ns, xc, ldx);
+      return launch_rp<kRP, kQL, kTallMR>(P, M, C, Q, r, out, split, scale, part, stream, pmask, f16, pl.ns);
   }
-  return launch_rp<kRP, kQL, 1>(P, M, C, Q, r, out, split, scale, part, stream, pmask, f16, pl.ns, xc, ldx);
+  return launch_rp<kRP, kQL, 1>(P, M, C, Q, r, out, split, scale, part, stream, pmask, f16, pl.ns);
 }
 
 }  // namespace
@@ -546,9 +545,9 @@ hipError_t launch_rowdot_finalize(const float* part, int ns, int64_t M, int r, f
                                   hipStream_t stream, bool f16) {
   const int xc = lora_extra_cols(r);
   if (f16)
-    rowdot_finalize_kernel<true><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, xc, scale);
+    rowdot_finalize_kernel<true><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, scale);
   else
-    rowdot_finalize_kernel<false><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, xc, scale);
+    rowdot_finalize_kernel<false><<<(unsigned)M, 256, 0, stream>>>(part, M, r, ns, out, split, xc, scale);
   return hipGetLastError();
 }
 
@@ -559,11 +558,10 @@ size_t rowdot_ws_bytes(int64_t M, int64_t C, int r) {
 
 hipError_t launch_rowdot(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int q_layout, int r,
                          float* out, uint16_t* split, float scale, float* part, hipStream_t stream,
-                         const uint8_t* pmask, bool f16, int split_cols, int split_ld) {
-  const int xc = split_cols > 0 ? split_cols : lora_extra_cols(r), ldx = split_ld > 0 ? split_ld : xc;
+                         const uint8_t* pmask, bool f16) {
 #define QLORA_RP(RP)                                                                                  \
-  return q_layout == 0 ? launch_rq<RP, 0>(P, M, C, Q, r, out, split, scale, part, stream, pmask, f16, xc, ldx) \
-                       : launch_rq<RP, 1>(P, M, C, Q, r, out, split, scale, part, stream, pmask, f16, xc, ldx);
+  return q_layout == 0 ? launch_rq<RP, 0>(P, M, C, Q, r, out, split, scale, part, stream, pmask, f16) \
+                       : launch_rq<RP, 1>(P, M, C, Q, r, out, split, scale, part, stream, pmask, f16);
   if (r <= 16) { QLORA_RP(16) }
   if (r <= 32) { QLORA_RP(32) }
   if (r <= 64) { QLORA_RP(64) }
