@@ -26,7 +26,7 @@ bool dims_ok(int64_t M, int64_t n, int64_t k, int r) {
 }
 
 bool fwd_fits(int64_t M, int64_t n, int64_t k, int r) {
-  return M <= 16 ? 32 * f8_pad(k) < ((int64_t)1 << 31) : gemm_fp8_offsets_fit(M, k, lora_extra_cols(r), n);
+  return M <= 16 ? 32 * f8_pad(k) < ((int64_t)1 << 31) : gemm_fp8_offsets_fit(M, k, lora_extra_cols(r), n, false);
 }
 
 struct FwdWs {
@@ -67,7 +67,6 @@ size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
 struct BwdWs {
   uint8_t* yq = nullptr;   // dY's codes and scale words
   uint8_t* ys = nullptr;
-  uint8_t* wt = nullptr;   // the weight's codes as [k, n]
   uint16_t* US = nullptr;
   uint16_t* Ax = nullptr;
   uint16_t* Bo = nullptr;  // B in operand order
@@ -81,7 +80,6 @@ struct BwdWs {
 size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
   o.yq = cv.take<uint8_t>((size_t)M * f8_pad(n));
   o.ys = cv.take<uint8_t>(fp8_rows_scale_bytes(M, n));
-  o.wt = cv.take<uint8_t>((size_t)k * f8_pad(n));
   if (r > 0) {
     o.US = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
     o.Ax = cv.take<uint16_t>((size_t)k * lora_extra_cols(r) * 2);
@@ -177,7 +175,7 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int6
   }
   if (e == hipSuccess)
     e = launch_gemm_fp8(o.xq, o.xs, M, k, o.TS, lora_extra_cols(r), w->codes, w->scale, nb, 1,
-                        (f8_pad(n) / kF8Block) * nb, o.Bx, n, static_cast<uint16_t*>(Y), o.part, st, f16);
+                        (f8_pad(n) / kF8Block) * nb, o.Bx, n, static_cast<uint16_t*>(Y), o.part, st, f16, false);
   return hip_status(e);
 }
 
@@ -188,7 +186,7 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
   if (s != QLORA_OK) return s;
   const int64_t n = w->n, k = w->k;
   if (!is16(dtype) || (accumulate != 0 && accumulate != 1)) return QLORA_ERR_INVALID_ARG;
-  if (!dims_ok(M, n, k, r) || (M > 0 && dX && !gemm_fp8_offsets_fit(M, n, lora_extra_cols(r), k)))
+  if (!dims_ok(M, n, k, r) || (M > 0 && dX && !gemm_fp8_offsets_fit(M, n, lora_extra_cols(r), k, true)))
     return QLORA_ERR_SHAPE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (r == 0) {
@@ -223,11 +221,10 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
   }
   if (dX) {
     if (e == hipSuccess && r > 0) e = launch_lowrank_rows_t(a, r, k, o.Ax, st);
-    if (e == hipSuccess) e = launch_fp8_transpose(view8(w), o.wt, st);
     const int64_t kb = f8_pad(k) / kF8Block;
     if (e == hipSuccess)
-      e = launch_gemm_fp8(o.yq, o.ys, M, n, o.US, lora_extra_cols(r), o.wt, w->scale, 1, kb, (f8_pad(n) / kF8Block) * kb,
-                          o.Ax, k, static_cast<uint16_t*>(dX), o.part, st, f16);
+      e = launch_gemm_fp8(o.yq, o.ys, M, n, o.US, lora_extra_cols(r), w->codes, w->scale, 1, kb,
+                          (f8_pad(n) / kF8Block) * kb, o.Ax, k, static_cast<uint16_t*>(dX), o.part, st, f16, true);
   }
   if (e == hipSuccess && dA) e = launch_colgrad(x, M, k, o.U, 1, r, scale, dA, nullptr, true, accumulate, o.grad, st, f16);
   if (e == hipSuccess && dB) {

@@ -310,31 +310,6 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
   __builtin_amdgcn_s_waitcnt(0);
 }
 
-// Weight codes [n, kp] -> [k, np] (np: n up to a multiple of 128, zero past
-// n), the operand whose rows run along dX's contraction. A thread turns 4
-// rows x 16 columns in registers; 32 lanes write 128 contiguous bytes.
-__global__ __launch_bounds__(256) void fp8_transpose_kernel(const uint8_t* __restrict__ codes, int64_t n, int64_t k,
-                                                            int64_t kp, int64_t np, uint8_t* __restrict__ out) {
-  const int64_t r0 = (int64_t)blockIdx.y * kF8Block + (threadIdx.x & 31) * 4;
-  const int64_t c0 = (int64_t)blockIdx.x * kF8Block + (threadIdx.x >> 5) * 16;
-  if (c0 >= k) return;
-  u32x4 v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = *reinterpret_cast<const u32x4*>(codes + (r0 + i < n ? r0 + i : n - 1) * kp + c0);
-    if (r0 + i >= n) v[i] = u32x4{0u, 0u, 0u, 0u};
-  }
-#pragma unroll
-  for (int w = 0; w < 4; ++w)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t sh = 8 * e;
-      const uint32_t o = ((v[0][w] >> sh) & 0xFFu) | (((v[1][w] >> sh) & 0xFFu) << 8) |
-                         (((v[2][w] >> sh) & 0xFFu) << 16) | (((v[3][w] >> sh) & 0xFFu) << 24);
-      *reinterpret_cast<uint32_t*>(out + (c0 + 4 * w + e) * np + r0) = o;
-    }
-}
-
 }  // namespace
 
 hipError_t launch_fp8_encode(const void* W, int dt, int64_t n, int64_t k, uint8_t* codes, uint8_t* scale,
@@ -399,13 +374,6 @@ hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16
 #undef QLORA_PREP
 #undef QLORA_PREP2
 #undef QLORA_PREP3
-  return hipGetLastError();
-}
-
-hipError_t launch_fp8_transpose(const Fp8View& w, uint8_t* out, hipStream_t stream) {
-  const int64_t kp = f8_pad(w.k), np = f8_pad(w.n);
-  const dim3 grid((unsigned)(kp / kF8Block), (unsigned)(np / kF8Block));
-  fp8_transpose_kernel<<<grid, 256, 0, stream>>>(w.codes, w.n, w.k, kp, np, out);
   return hipGetLastError();
 }
 

@@ -30,6 +30,7 @@ namespace {
 using namespace gt;
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 struct F8Args {
   const uint8_t* act;   // [M, lda] codes
@@ -37,7 +38,8 @@ struct F8Args {
   int64_t M, lda;
   const uint16_t* act_x;  // [M, kx] low-rank split columns
   int kx;
-  const uint8_t* f;     // [nout, lda] codes
+  const uint8_t* f;     // [nout, ldf] codes; kNN: [kc, ldf]
+  int64_t ldf, f_rows;
   const uint8_t* fs;    // scale byte of (output block, contraction block) at ob * fs_o + cb * fs_c
   int64_t fs_o, fs_c, fs_bytes;
   int64_t nout;
@@ -77,6 +79,29 @@ __device__ __forceinline__ i32x8 frag32(const char* T, int rb, int kk, int lane)
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+// The weight stored along its outputs (kNN; a forward's weight read for dX):
+// its tile is 128 contraction rows of 256 output columns, and the same 32
+// bytes of a column come back through four transposing reads of 8 rows: in
+// every 16-lane group lane i addresses row base + i / 2, bytes 8 (i % 2) .. +7
+// of the group's 16 columns, and receives column i of the 8 rows. Chunk c of
+// row r lies at c ^ 2 (r & 7), so the 8 rows of two neighbouring groups fall
+// on distinct banks. (dX of 4096 x 8192 x 22016, same box: 612 us; the weight
+// transposed first and read along its rows 622 + 84.)
+__device__ __forceinline__ int nn_key(int row) { return 2 * (row & 7); }
+
+__device__ __forceinline__ i32x8 frag32_nn(const char* T, int cb, int kk, int lane) {
+  const int i = lane & 15;
+  const int chunk = (cb >> 4) + ((lane >> 4) & 1);
+  const int row = 64 * kk + 16 * (lane >> 5) + (i >> 1);
+  const char* const p = T + row * kBN + ((chunk ^ nn_key(row)) << 4) + 8 * (i & 1);  // (rows 8 apart share the key)
+  typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+  const i32x2 v0 = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(p));
+  const i32x2 v1 = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(p + 8 * kBN));
+  const i32x2 v2 = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(p + 32 * kBN));
+  const i32x2 v3 = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(p + 40 * kBN));
+  return i32x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+}
+
 struct Scales {
   uint32_t a, b;
 };
@@ -96,15 +121,22 @@ __device__ __forceinline__ void read_a(Frags& f, const char* Ac, int wm0, int i,
   __builtin_amdgcn_sched_barrier(0);
 }
 
+template <bool kNN>
 __device__ __forceinline__ void read_b(Frags& f, const char* Bc, int wn0, int kk, int lane) {
 #pragma unroll
-  for (int j = 0; j < kTN; ++j) f.b[kk][j] = frag32(Bc, wn0 + 32 * j, kk, lane);
+  for (int j = 0; j < kTN; ++j) {
+    if constexpr (kNN)
+      f.b[kk][j] = frag32_nn(Bc, wn0 + 32 * j, kk, lane);
+    else
+      f.b[kk][j] = frag32(Bc, wn0 + 32 * j, kk, lane);
+  }
   __builtin_amdgcn_sched_barrier(0);
 }
 
 struct Rsrc {
   i32x4 act, as, f, fs;
   uint32_t as_off, as_step, fs_off, fs_step;  // scale offsets: this lane's word, bytes per step
+  uint32_t f_step;                            // weight bytes per step
 };
 
 __device__ __forceinline__ void load_scales(const Rsrc& rs, int step, Scales& s) {
@@ -121,6 +153,7 @@ __device__ __forceinline__ void load_scales(const Rsrc& rs, int step, Scales& s)
 // 1's first substep from (An, Bn1). (4096 x 8192 x 22016, same box: 625 us; one
 // block earlier 636, one later 647, two later 658.) The scales of step + 1 are
 // loaded before the copies, so the same wait covers them.
+template <bool kNN>
 __device__ __forceinline__ void f8_step(const Rsrc& rs, const Rows& p, int step, int nk, int wave,
                                         const char* __restrict__ Ac, const char* __restrict__ Bc,
                                         char* __restrict__ An, const char* __restrict__ Bn1, char* __restrict__ Bn2,
@@ -132,10 +165,10 @@ __device__ __forceinline__ void f8_step(const Rsrc& rs, const Rows& p, int step,
   load_scales(rs, s1, nxt);
   __builtin_amdgcn_sched_barrier(0);
   issue4(rs.act, p.a, s1 * 128, An + wave * kCopies * 1024);
-  issue4(rs.f, p.f, s2 * 128, Bn2 + wave * kCopies * 1024);
+  issue4(rs.f, p.f, (int)((uint32_t)s2 * rs.f_step), Bn2 + wave * kCopies * 1024);
   __builtin_amdgcn_sched_barrier(0);
   mfma_row<0>(acc, f, 0, cur);
-  read_b(f, Bc, wn0, 1, lane);
+  read_b<kNN>(f, Bc, wn0, 1, lane);
   read_a(f, Ac, wm0, 0, 1, lane);
   mfma_row<1>(acc, f, 0, cur);
   read_a(f, Ac, wm0, 1, 1, lane);
@@ -146,7 +179,7 @@ __device__ __forceinline__ void f8_step(const Rsrc& rs, const Rows& p, int step,
   mfma_row<0>(acc, f, 1, cur);
   step_barrier<kCopies>();
   __builtin_amdgcn_sched_barrier(0);
-  read_b(f, Bn1, wn0, 0, lane);
+  read_b<kNN>(f, Bn1, wn0, 0, lane);
   read_a(f, An, wm0, 0, 0, lane);
   mfma_row<1>(acc, f, 1, cur);
   read_a(f, An, wm0, 1, 0, lane);
@@ -163,12 +196,12 @@ __device__ __forceinline__ void f8_prologue(const Rsrc& rs, const Rows& p, int s
                                             Scales& s) {
   load_scales(rs, sbeg, s);
   issue4(rs.act, p.a, sbeg * 128, A0 + wave * kCopies * 1024);
-  issue4(rs.f, p.f, sbeg * 128, B0 + wave * kCopies * 1024);
-  issue4(rs.f, p.f, (sbeg + 1 < nk ? sbeg + 1 : nk - 1) * 128, B1 + wave * kCopies * 1024);
+  issue4(rs.f, p.f, (int)((uint32_t)sbeg * rs.f_step), B0 + wave * kCopies * 1024);
+  issue4(rs.f, p.f, (int)((uint32_t)(sbeg + 1 < nk ? sbeg + 1 : nk - 1) * rs.f_step), B1 + wave * kCopies * 1024);
   step_barrier<kCopies>();
 }
 
-template <bool kF16>
+template <bool kF16, bool kNN>
 __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(F8Args a) {
   __shared__ __attribute__((aligned(16))) char As0[kTileBytes];
   __shared__ __attribute__((aligned(16))) char As1[kTileBytes];
@@ -232,12 +265,20 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(F8Args a) {
       const int64_t m = m0 + row < a.M ? m0 + row : a.M - 1;  // rows past the end repeat the last (not stored)
       const int64_t n = n0 + row < a.nout ? n0 + row : a.nout - 1;
       p.a[i] = (uint32_t)(m * a.lda + 16 * lc);
-      p.f[i] = (uint32_t)(n * a.lda + 16 * lc);
+      if constexpr (kNN) {
+        // columns past nout read other data (their outputs are not stored),
+        // rows past the end zeros (range check)
+        const int r = (wave * kCopies + i) * 4 + (lane >> 4);
+        p.f[i] = (uint32_t)(r * a.ldf + n0 + 16 * ((lane & 15) ^ nn_key(r)));
+      } else {
+        p.f[i] = (uint32_t)(n * a.ldf + 16 * lc);
+      }
     }
     Rsrc rs;
     const int64_t mt128 = cdiv(a.M, (int64_t)kF8Block);
     rs.act = make_rsrc(a.act, a.M * a.lda);
-    rs.f = make_rsrc(a.f, a.nout * a.lda);
+    rs.f = make_rsrc(a.f, a.f_rows * a.ldf);
+    rs.f_step = kNN ? (uint32_t)(128 * a.ldf) : 128u;
     rs.as = make_rsrc(a.as, (int64_t)nk_all * mt128 * 128);
     rs.fs = make_rsrc(a.fs, a.fs_bytes);
     // (row tiles past M and output blocks past nout: any in-range scale, the results are not stored)
@@ -250,25 +291,25 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(F8Args a) {
     Scales s0, s1;
     Frags f;
     f8_prologue(rs, p, sbeg, nk, wave, As0, Bs0, Bs1, s0);
-    read_b(f, Bs0, wn0, 0, lane);
+    read_b<kNN>(f, Bs0, wn0, 0, lane);
 #pragma unroll
     for (int i = 0; i < kTM; ++i) read_a(f, As0, wm0, i, 0, lane);
-    f8_step(rs, p, sbeg, nk, wave, As0, Bs0, As1, Bs1, Bs2, acc, f, s0, s1);
+    f8_step<kNN>(rs, p, sbeg, nk, wave, As0, Bs0, As1, Bs1, Bs2, acc, f, s0, s1);
     int s = sbeg + 1;
     for (; s + 6 <= nk; s += 6) {
-      f8_step(rs, p, s, nk, wave, As1, Bs1, As0, Bs2, Bs0, acc, f, s1, s0);
-      f8_step(rs, p, s + 1, nk, wave, As0, Bs2, As1, Bs0, Bs1, acc, f, s0, s1);
-      f8_step(rs, p, s + 2, nk, wave, As1, Bs0, As0, Bs1, Bs2, acc, f, s1, s0);
-      f8_step(rs, p, s + 3, nk, wave, As0, Bs1, As1, Bs2, Bs0, acc, f, s0, s1);
-      f8_step(rs, p, s + 4, nk, wave, As1, Bs2, As0, Bs0, Bs1, acc, f, s1, s0);
-      f8_step(rs, p, s + 5, nk, wave, As0, Bs0, As1, Bs1, Bs2, acc, f, s0, s1);
+      f8_step<kNN>(rs, p, s, nk, wave, As1, Bs1, As0, Bs2, Bs0, acc, f, s1, s0);
+      f8_step<kNN>(rs, p, s + 1, nk, wave, As0, Bs2, As1, Bs0, Bs1, acc, f, s0, s1);
+      f8_step<kNN>(rs, p, s + 2, nk, wave, As1, Bs0, As0, Bs1, Bs2, acc, f, s1, s0);
+      f8_step<kNN>(rs, p, s + 3, nk, wave, As0, Bs1, As1, Bs2, Bs0, acc, f, s0, s1);
+      f8_step<kNN>(rs, p, s + 4, nk, wave, As1, Bs2, As0, Bs0, Bs1, acc, f, s1, s0);
+      f8_step<kNN>(rs, p, s + 5, nk, wave, As0, Bs0, As1, Bs1, Bs2, acc, f, s0, s1);
     }
     const int rem = nk - s;
-    if (rem > 0) f8_step(rs, p, s, nk, wave, As1, Bs1, As0, Bs2, Bs0, acc, f, s1, s0);
-    if (rem > 1) f8_step(rs, p, s + 1, nk, wave, As0, Bs2, As1, Bs0, Bs1, acc, f, s0, s1);
-    if (rem > 2) f8_step(rs, p, s + 2, nk, wave, As1, Bs0, As0, Bs1, Bs2, acc, f, s1, s0);
-    if (rem > 3) f8_step(rs, p, s + 3, nk, wave, As0, Bs1, As1, Bs2, Bs0, acc, f, s0, s1);
-    if (rem > 4) f8_step(rs, p, s + 4, nk, wave, As1, Bs2, As0, Bs0, Bs1, acc, f, s1, s0);
+    if (rem > 0) f8_step<kNN>(rs, p, s, nk, wave, As1, Bs1, As0, Bs2, Bs0, acc, f, s1, s0);
+    if (rem > 1) f8_step<kNN>(rs, p, s + 1, nk, wave, As0, Bs2, As1, Bs0, Bs1, acc, f, s0, s1);
+    if (rem > 2) f8_step<kNN>(rs, p, s + 2, nk, wave, As1, Bs0, As0, Bs1, Bs2, acc, f, s1, s0);
+    if (rem > 3) f8_step<kNN>(rs, p, s + 3, nk, wave, As0, Bs1, As1, Bs2, Bs0, acc, f, s0, s1);
+    if (rem > 4) f8_step<kNN>(rs, p, s + 4, nk, wave, As1, Bs2, As0, Bs0, Bs1, acc, f, s1, s0);
     __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());
     __syncthreads();
   }
@@ -296,9 +337,11 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(F8Args a) {
 
 }  // namespace
 
-bool gemm_fp8_offsets_fit(int64_t M, int64_t kc, int kx, int64_t nout) {
+// 32-bit offsets (kNN reads up to a tile's width past the operand's end, where the range check has to see it)
+bool gemm_fp8_offsets_fit(int64_t M, int64_t kc, int kx, int64_t nout, bool nn) {
   const int64_t lim = (int64_t)1 << 32;
-  return M * f8_pad(kc) < lim && nout * f8_pad(kc) < lim && M * (int64_t)kx * 2 < lim && nout * (int64_t)kx * 2 < lim;
+  const int64_t fb = nn ? f8_pad(kc) * f8_pad(nout) + kBN : nout * f8_pad(kc);
+  return M * f8_pad(kc) < lim && fb < lim && M * (int64_t)kx * 2 < lim && nout * (int64_t)kx * 2 < lim;
 }
 
 size_t gemm_fp8_ws_bytes(int64_t M, int64_t kc, int64_t nout) {
@@ -308,21 +351,25 @@ size_t gemm_fp8_ws_bytes(int64_t M, int64_t kc, int64_t nout) {
 
 hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int64_t kc, const uint16_t* split, int kx,
                            const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
-                           const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16) {
+                           const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16,
+                           bool nn) {
   F8Args a{};
   a.act = act; a.as = as; a.M = M; a.lda = f8_pad(kc);
   a.act_x = split; a.kx = kx;
   a.f = f; a.fs = fs; a.fs_o = fs_o; a.fs_c = fs_c; a.fs_bytes = fs_bytes;
+  a.ldf = nn ? f8_pad(nout) : a.lda; a.f_rows = nn ? kc : nout;
   a.nout = nout; a.fx = fx; a.out = out;
   const GemmSplit sp = gemm_split_plan(M, nout, a.lda / kF8Block);
   a.full = sp.full; a.tail = sp.tail; a.splits = sp.splits;
   a.part = part;
   if (a.splits > 1 && part == nullptr) return hipErrorInvalidValue;
   const dim3 grid((unsigned)(a.full + a.tail * a.splits));
-  if (f16)
-    gemm_fp8_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-  else
-    gemm_fp8_kernel<false><<<grid, kThreads, 0, stream>>>(a);
+#define QLORA_GEMM8(H, NN) gemm_fp8_kernel<H, NN><<<grid, kThreads, 0, stream>>>(a)
+  if (f16 && nn) QLORA_GEMM8(true, true);
+  else if (f16) QLORA_GEMM8(true, false);
+  else if (nn) QLORA_GEMM8(false, true);
+  else QLORA_GEMM8(false, false);
+#undef QLORA_GEMM8
   if (a.splits > 1) return launch_gemm_reduce(part, sp, M, nout, out, stream, f16);
   return hipGetLastError();
 }

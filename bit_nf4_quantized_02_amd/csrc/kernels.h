@@ -273,15 +273,15 @@ Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few, int W = 1);
 size_t fp8_rows_scale_bytes(int64_t M, int64_t C);
 hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r,
                            uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16, int W = 1);
-// The weight's codes as [k, n up to 128] rows for dX.
-hipError_t launch_fp8_transpose(const Fp8View& w, uint8_t* out, hipStream_t stream);
 // out = RN16([act | split] [f | fx]^T); f's scale byte of (output block,
-// contraction block) at ob * fs_o + cb * fs_c. part: gemm_fp8_ws_bytes().
-bool gemm_fp8_offsets_fit(int64_t M, int64_t kc, int kx, int64_t nout);
+// contraction block) at ob * fs_o + cb * fs_c. nn: f is [kc, nout up to 128].
+// part: gemm_fp8_ws_bytes().
+bool gemm_fp8_offsets_fit(int64_t M, int64_t kc, int kx, int64_t nout, bool nn);
 size_t gemm_fp8_ws_bytes(int64_t M, int64_t kc, int64_t nout);
 hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int64_t kc, const uint16_t* split, int kx,
                            const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
-                           const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16);
+                           const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16,
+                           bool nn);
 // M <= 16: Y = RN16(X8 W8^T + scale T B^T) from launch_fp8_prep's operands; T
 // as `parts` partials [parts][M][r] that the kernel adds in order, written to
 // T_save if it is not NULL.
