@@ -73,7 +73,10 @@ struct BwdWs {
   float* U = nullptr;
   float* T = nullptr;
   float* proj = nullptr;
-  void* grad = nullptr;
+  void* Up = nullptr;      // U's and T's parts
+  void* Tp = nullptr;
+  float* da = nullptr;     // partials of the gradients
+  float* db = nullptr;
   float* part = nullptr;
 };
 
@@ -88,8 +91,10 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
     o.T = cv.take<float>((size_t)M * r * 4);
     const size_t p1 = (size_t)fp8_prep_plan(M, n, false).splits * M * r * 4, p2 = rowdot_ws_bytes(M, k, r);
     o.proj = cv.take<float>(p1 > p2 ? p1 : p2);
-    const size_t g1 = colgrad_ws_bytes(M, k, r, 1), g2 = colgrad_ws_bytes(M, n, r, 1);
-    o.grad = cv.take<char>(g1 > g2 ? g1 : g2);
+    o.Up = cv.take<char>(rank_parts_bytes(M, r, 1));
+    o.Tp = cv.take<char>(rank_parts_bytes(M, r, 1));
+    o.da = cv.take<float>(colgrad_ws_bytes(M, k, r, 1));
+    o.db = cv.take<float>(colgrad_ws_bytes(M, n, r, 1));
   }
   o.part = cv.take<float>(gemm_fp8_ws_bytes(M, n, k));
   return cv.used;
@@ -155,7 +160,7 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int6
   const bool few = M <= 16;
   const int parts = fp8_prep_plan(M, k, few).splits;
   hipError_t e = hipSuccess;
-  if (r > 0 && !few) e = launch_operand_order(a, nullptr, 0, k, f8_pad(k), r, o.Ao, st);
+  if (r > 0 && !few) e = launch_factors(a, 0, k, f8_pad(k), r, o.Ao, b, n, o.Bx, st);
   if (e == hipSuccess) e = launch_fp8_prep(x, M, k, few ? a : o.Ao, r, o.xq, o.xs, o.proj, few, st, f16);
   if (few) {
     if (r > 0 && !gemv_adds(M, k, r)) {
@@ -169,10 +174,7 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int6
     return hip_status(e);
   }
   const int64_t nb = f8_pad(k) / kF8Block;
-  if (r > 0) {
-    if (e == hipSuccess) e = launch_rowdot_finalize(o.proj, parts, M, r, T_save, o.TS, scale, st, f16);
-    if (e == hipSuccess) e = launch_lowrank_rows(b, n, r, o.Bx, st);
-  }
+  if (r > 0 && e == hipSuccess) e = launch_rowdot_finalize(o.proj, parts, M, r, T_save, o.TS, scale, st, f16);
   if (e == hipSuccess)
     e = launch_gemm_fp8(o.xq, o.xs, M, k, o.TS, lora_extra_cols(r), w->codes, w->scale, nb, 1,
                         (f8_pad(n) / kF8Block) * nb, o.Bx, n, static_cast<uint16_t*>(Y), o.part, st, f16, false);
@@ -212,7 +214,10 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
   const uint16_t *x = static_cast<const uint16_t*>(X), *dy = static_cast<const uint16_t*>(dY),
                  *a = static_cast<const uint16_t*>(A), *b = static_cast<const uint16_t*>(B);
   if (dX || dA) {
-    if (r > 0) e = launch_operand_order(b, nullptr, 1, n, f8_pad(n), r, o.Bo, st);
+    if (r > 0 && dX)
+      e = launch_factors(b, 1, n, f8_pad(n), r, o.Bo, a, k, o.Ax, st);
+    else if (r > 0)
+      e = launch_operand_order(b, nullptr, 1, n, f8_pad(n), r, o.Bo, st);
     if (e == hipSuccess)
       e = launch_fp8_prep(dy, M, n, o.Bo, r, dX ? o.yq : nullptr, o.ys, o.proj, false, st, f16);
     if (e == hipSuccess && r > 0)
@@ -220,21 +225,24 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
                                  f16);
   }
   if (dX) {
-    if (e == hipSuccess && r > 0) e = launch_lowrank_rows_t(a, r, k, o.Ax, st);
     const int64_t kb = f8_pad(k) / kF8Block;
     if (e == hipSuccess)
       e = launch_gemm_fp8(o.yq, o.ys, M, n, o.US, lora_extra_cols(r), w->codes, w->scale, 1, kb,
                           (f8_pad(n) / kF8Block) * kb, o.Ax, k, static_cast<uint16_t*>(dX), o.part, st, f16, true);
   }
-  if (e == hipSuccess && dA) e = launch_colgrad(x, M, k, o.U, 1, r, scale, dA, nullptr, true, accumulate, o.grad, st, f16);
-  if (e == hipSuccess && dB) {
-    const float* T = T_saved;
-    if (T == nullptr) {
-      e = launch_rowdot(x, M, k, a, 0, r, o.T, nullptr, scale, o.proj, st, nullptr, f16);
-      T = o.T;
-    }
-    if (e == hipSuccess) e = launch_colgrad(dy, M, n, T, 1, r, scale, dB, nullptr, false, accumulate, o.grad, st, f16);
+  if (!dA && !dB) return hip_status(e);
+  const float* T = T_saved;
+  if (e == hipSuccess && dB && T == nullptr) {
+    e = launch_rowdot(x, M, k, a, 0, r, o.T, nullptr, scale, o.proj, st, nullptr, f16);
+    T = o.T;
   }
+  GradJob ja{}, jb{};
+  if (e == hipSuccess) e = launch_rank_parts(o.U, dA ? 1 : 0, o.Up, T, dB ? 1 : 0, o.Tp, M, r, st, f16);
+  if (e == hipSuccess && dA)
+    e = launch_colgrad(x, M, k, o.Up, 1, r, scale, dA, nullptr, true, accumulate, o.da, ja, st, f16);
+  if (e == hipSuccess && dB)
+    e = launch_colgrad(dy, M, n, o.Tp, 1, r, scale, dB, nullptr, false, accumulate, o.db, jb, st, f16);
+  if (e == hipSuccess) e = launch_grad_reduce(ja, jb, scale, accumulate, st);
   return hip_status(e);
 }
 

@@ -65,9 +65,11 @@ struct BwdWs {
   uint16_t* D = nullptr;   // [dG | dU]
   uint16_t* F = nullptr;   // both weights, contraction-major
   void* proj = nullptr;
-  void* grad = nullptr;
   void* join = nullptr;
-  void* db = nullptr;
+  void* Pp = nullptr;      // P's and T's parts
+  void* Tp = nullptr;
+  float* da = nullptr;     // partials of the gradients
+  float* db = nullptr;
   float* part = nullptr;
 };
 
@@ -79,9 +81,11 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
     o.P = cv.take<float>((size_t)2 * M * r * 4);
     o.PS = cv.take<uint16_t>((size_t)M * xc * 2);
     o.proj = cv.take<char>(gated_project_ws_bytes(M, k, r));
-    o.grad = cv.take<char>(colgrad_ws_bytes(M, k, r, 2));
     o.join = cv.take<char>(gated_join_ws_bytes(M, n, r));
-    o.db = cv.take<char>(gated_db_ws_bytes(M, n, r));
+    o.Pp = cv.take<char>(rank_parts_bytes(M, r, 2));
+    o.Tp = cv.take<char>(rank_parts_bytes(M, r, 2));
+    o.da = cv.take<float>(colgrad_ws_bytes(M, k, r, 2));
+    o.db = cv.take<float>(gated_db_ws_bytes(M, n, r));
   }
   o.D = cv.take<uint16_t>((size_t)M * 2 * np * 2);
   o.F = cv.take<uint16_t>(gated_dx_operand_bytes(n, k, r));
@@ -187,17 +191,19 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
       e = launch_gemm_bf16_ext(o.D, M, 2 * np, r > 0 ? o.PS : nullptr, xc, o.F, k, o.F + 2 * np * k, k, k,
                                static_cast<uint16_t*>(dX), o.part, st, nullptr, 1.0f, f16, /*nn=*/true);
   }
-  if (e == hipSuccess && need_a)
-    e = launch_colgrad(x, M, k, o.P, 2, r, scale, dA_gate, dA_up, true, accumulate, o.grad, st, f16);
-  if (e == hipSuccess && need_b) {
-    const float* T = T_saved;
-    if (T == nullptr) {
-      e = launch_gated_project(x, M, k, u16(A_gate), u16(A_up), r, scale, o.T, nullptr, o.proj, st, f16);
-      T = o.T;
-    }
-    if (e == hipSuccess)
-      e = launch_gated_db(u16(G), u16(U), u16(dH), M, n, T, r, scale, dB_gate, dB_up, accumulate, o.db, st, f16);
+  if (!need_a && !need_b) return hip_status(e);
+  const float* T = T_saved;
+  if (e == hipSuccess && need_b && T == nullptr) {
+    e = launch_gated_project(x, M, k, u16(A_gate), u16(A_up), r, scale, o.T, nullptr, o.proj, st, f16);
+    T = o.T;
   }
+  GradJob ja{}, jb{};
+  if (e == hipSuccess) e = launch_rank_parts(o.P, need_a ? 2 : 0, o.Pp, T, need_b ? 2 : 0, o.Tp, M, r, st, f16);
+  if (e == hipSuccess && need_a)
+    e = launch_colgrad(x, M, k, o.Pp, 2, r, scale, dA_gate, dA_up, true, accumulate, o.da, ja, st, f16);
+  if (e == hipSuccess && need_b)
+    e = launch_gated_db(u16(G), u16(U), u16(dH), M, n, o.Tp, r, dB_gate, dB_up, o.db, jb, st, f16);
+  if (e == hipSuccess) e = launch_grad_reduce(ja, jb, scale, accumulate, st);
   return hip_status(e);
 }
 

@@ -21,12 +21,17 @@ constexpr int kMaxRank = 128;
 
 // Q [W][M][r] -> [32-token step][part][w][rank tile][lane][16 bytes], the A
 // operand of the products over the tokens: lane l holds rank 16 t + l % 16, tokens 8 (l / 16)
-// .. +7 of the step, zero past M and r.
+// .. +7 of the step, zero past M and r. Two such operands (of W0 and of the
+// rest of gridDim.y) in one launch.
 template <bool kF16>
-__global__ __launch_bounds__(256) void rank_parts_kernel(const float* __restrict__ Q, int64_t M, int r, int tiles,
-                                                       u32x4* __restrict__ out) {
+__global__ __launch_bounds__(256) void rank_parts_kernel(const float* __restrict__ Q0, int W0,
+                                                         const float* __restrict__ Q1, int64_t M, int r, int tiles,
+                                                         u32x4* __restrict__ out0, u32x4* __restrict__ out1) {
   __shared__ float tile[32][kMaxRank + 1];
-  const int w = blockIdx.y;
+  const bool first = (int)blockIdx.y < W0;
+  const int w = first ? blockIdx.y : blockIdx.y - W0, W = first ? W0 : gridDim.y - W0;
+  const float* const Q = first ? Q0 : Q1;
+  u32x4* const out = first ? out0 : out1;
   const int64_t m0 = (int64_t)blockIdx.x * 32;
   // the step's 32 r values are one run (16-byte aligned): at most four loads per
   // thread, issued together
@@ -60,10 +65,9 @@ __global__ __launch_bounds__(256) void rank_parts_kernel(const float* __restrict
     split8<kF16>(x, p);
 #pragma unroll
     for (int q = 0; q < parts_of<kF16>(); ++q)
-      out[(((int64_t)blockIdx.x * parts_of<kF16>() + q) * gridDim.y + w) * tiles * 64 + i] = p[q];
+      out[(((int64_t)blockIdx.x * parts_of<kF16>() + q) * W + w) * tiles * 64 + i] = p[q];
   }
 }
-
 
 // A workgroup: 64 columns and one token range, 64 tokens per step in two sets of
 // LDS (one barrier per step): every thread stages 16 bytes of two rows, the B
@@ -183,17 +187,31 @@ __global__ __launch_bounds__(256) void colgrad_kernel(const uint16_t* __restrict
   }
 }
 
-// G (+)= scale * (partials [splits][W][count] added in order); a NULL gradient is left out.
-__global__ __launch_bounds__(256) void grad_reduce_kernel(const float* __restrict__ part, int splits, int64_t count,
-                                                          float scale, float* __restrict__ G0, float* __restrict__ G1,
-                                                          int accumulate) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int w = blockIdx.y, W = gridDim.y;
-  float* const G = w == 0 ? G0 : G1;
-  if (i >= count || G == nullptr) return;
-  float s = part[w * count + i];
-  for (int p = 1; p < splits; ++p) s += part[((int64_t)p * W + w) * count + i];
-  G[i] = accumulate ? G[i] + scale * s : scale * s;
+// G (+)= scale * (partials [splits][W][count] added in order) of two jobs in
+// one launch (blockIdx.z); a NULL gradient is left out. Four values per
+// thread, whose first (a multiple of 4) is 16-byte aligned where count is.
+__global__ __launch_bounds__(256) void grad_reduce_kernel(GradJob j0, GradJob j1, float scale, int accumulate) {
+  const GradJob j = blockIdx.z == 0 ? j0 : j1;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int w = blockIdx.y;
+  float* const G = w == 0 ? j.G0 : j.G1;
+  if (i >= j.count || w >= j.W || G == nullptr) return;
+  const float* const src = j.part + w * j.count + i;
+  const int64_t pitch = (int64_t)j.W * j.count;
+  if (j.count % 4 == 0) {
+    f32x4 s = *reinterpret_cast<const f32x4*>(src);
+#pragma unroll 4
+    for (int p = 1; p < j.splits; ++p) s += *reinterpret_cast<const f32x4*>(src + p * pitch);
+    f32x4* const o = reinterpret_cast<f32x4*>(G + i);
+    s = scale * s;
+    *o = accumulate ? *o + s : s;
+  } else {
+    for (int e = 0; e < 4 && i + e < j.count; ++e) {
+      float s = src[e];
+      for (int p = 1; p < j.splits; ++p) s += src[p * pitch + e];
+      G[i + e] = accumulate ? G[i + e] + scale * s : scale * s;
+    }
+  }
 }
 
 // Token ranges: about 512 workgroups, each at least 128 tokens, at most 16
@@ -215,36 +233,39 @@ GradPlan grad_plan(int64_t M, int64_t C) {
 
 size_t rank_parts_bytes(int64_t M, int r, int W) { return (size_t)cdiv(M, (int64_t)32) * 3 * W * rank_pad(r) * 64; }
 
-hipError_t launch_rank_parts(const float* Q, int W, int64_t M, int r, void* out, hipStream_t stream, bool f16) {
-  const dim3 grid((unsigned)cdiv(M, (int64_t)32), (unsigned)W);
+hipError_t launch_rank_parts(const float* Q0, int W0, void* out0, const float* Q1, int W1, void* out1, int64_t M, int r,
+                             hipStream_t stream, bool f16) {
+  const dim3 grid((unsigned)cdiv(M, (int64_t)32), (unsigned)(W0 + W1));
+  u32x4 *const o0 = static_cast<u32x4*>(out0), *const o1 = static_cast<u32x4*>(out1);
+  const int tiles = rank_pad(r) / 16;
   if (f16)
-    rank_parts_kernel<true><<<grid, 256, 0, stream>>>(Q, M, r, rank_pad(r) / 16, static_cast<u32x4*>(out));
+    rank_parts_kernel<true><<<grid, 256, 0, stream>>>(Q0, W0, Q1, M, r, tiles, o0, o1);
   else
-    rank_parts_kernel<false><<<grid, 256, 0, stream>>>(Q, M, r, rank_pad(r) / 16, static_cast<u32x4*>(out));
+    rank_parts_kernel<false><<<grid, 256, 0, stream>>>(Q0, W0, Q1, M, r, tiles, o0, o1);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_reduce(const float* part, int splits, int W, int64_t count, float scale, float* G0, float* G1,
-                              int accumulate, hipStream_t stream) {
-  grad_reduce_kernel<<<dim3((unsigned)cdiv(count, (int64_t)256), (unsigned)W), 256, 0, stream>>>(part, splits, count, scale,
-                                                                                                G0, G1, accumulate);
+hipError_t launch_grad_reduce(const GradJob& a, const GradJob& b, float scale, int accumulate, hipStream_t stream) {
+  if (a.W == 0 && b.W == 0) return hipSuccess;
+  const int64_t count = a.count > b.count ? a.count : b.count;
+  const dim3 grid((unsigned)cdiv(count, (int64_t)1024), (unsigned)(a.W > b.W ? a.W : b.W), 2);
+  grad_reduce_kernel<<<grid, 256, 0, stream>>>(a, b, scale, accumulate);
   return hipGetLastError();
 }
 
 size_t colgrad_ws_bytes(int64_t M, int64_t C, int r, int W) {
   const GradPlan pl = grad_plan(M, C);
-  return align256(rank_parts_bytes(M, r, W)) +
-         (pl.splits > 1 ? align256((size_t)pl.splits * W * r * (size_t)C * 4) : 0);
+  return pl.splits > 1 ? align256((size_t)pl.splits * W * r * (size_t)C * 4) : 0;
 }
 
-hipError_t launch_colgrad(const uint16_t* P, int64_t M, int64_t C, const float* Q, int W, int r, float scale, float* G0,
-                          float* G1, bool j_first, int accumulate, void* ws, hipStream_t stream, bool f16) {
-  hipError_t e = launch_rank_parts(Q, W, M, r, ws, stream, f16);
-  if (e != hipSuccess) return e;
-  const u32x4* const Qp = static_cast<const u32x4*>(ws);
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(rank_parts_bytes(M, r, W)));
+hipError_t launch_colgrad(const uint16_t* P, int64_t M, int64_t C, const void* parts, int W, int r, float scale,
+                          float* G0, float* G1, bool j_first, int accumulate, float* part, GradJob& job,
+                          hipStream_t stream, bool f16) {
+  const u32x4* const Qp = static_cast<const u32x4*>(parts);
   const GradPlan pl = grad_plan(M, C);
   const bool direct = pl.splits == 1;
+  job = GradJob{};
+  if (!direct) job = GradJob{part, C * r, pl.splits, W, G0, G1};
   const dim3 grid((unsigned)cdiv(C, (int64_t)kDbCols), (unsigned)pl.splits);
 #define QLORA_CG3(RP, H, V, NW, J) \
   colgrad_kernel<RP, H, V, NW, J><<<grid, 256, 0, stream>>>(P, M, C, Qp, r, pl.mchunk, part, direct, scale, G0, G1, accumulate)
@@ -264,7 +285,6 @@ hipError_t launch_colgrad(const uint16_t* P, int64_t M, int64_t C, const float* 
 #undef QLORA_CG
 #undef QLORA_CG2
 #undef QLORA_CG3
-  if (!direct) return launch_grad_reduce(part, pl.splits, W, C * r, scale, G0, G1, accumulate, stream);
   return hipGetLastError();
 }
 

@@ -172,10 +172,9 @@ __global__ __launch_bounds__(256) void expand_cols_kernel(const uint8_t* __restr
 // Low-rank operand rows alone, [n, xc]: row i = [B[i, :] | B[i, :] | 0 ...]
 // (the columns the row expansion appends to W'), for a GEMM whose weight
 // operand is a separate matrix. One thread per 8 output columns.
-__global__ __launch_bounds__(256) void lowrank_rows_kernel(const uint16_t* __restrict__ B, int64_t n, int r, int xc,
-                                                           u32x4* __restrict__ out) {
+__device__ __forceinline__ void lowrank_rows_part(const uint16_t* __restrict__ B, int64_t n, int r, int xc, int64_t q,
+                                                  u32x4* __restrict__ out) {
   const int cpr = xc / 8;
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (q >= n * cpr) return;
   const int64_t i = q / cpr;
   const int j0 = (int)(q % cpr) * 8;
@@ -191,6 +190,11 @@ __global__ __launch_bounds__(256) void lowrank_rows_kernel(const uint16_t* __res
     v[p] = h[0] | (h[1] << 16);
   }
   out[q] = v;
+}
+
+__global__ __launch_bounds__(256) void lowrank_rows_kernel(const uint16_t* __restrict__ B, int64_t n, int r, int xc,
+                                                           u32x4* __restrict__ out) {
+  lowrank_rows_part(B, n, r, xc, (int64_t)blockIdx.x * 256 + threadIdx.x, out);
 }
 
 // [xc, k] rows [A ; A ; 0]: row x is A's row x % r for x < 2r, zeros after.
@@ -209,11 +213,10 @@ __global__ __launch_bounds__(256) void lowrank_cols_kernel(const uint16_t* __res
 // [k, xc] rows of A^T: row c = [A[0..r-1, c] | the same | 0]. One thread per
 // (row, 8 columns): neighbouring threads take neighbouring c, so each A row
 // is read in runs.
-__global__ __launch_bounds__(256) void lowrank_rows_t_kernel(const uint16_t* __restrict__ A, int r, int xc, int64_t k,
-                                                             u32x4* __restrict__ out) {
+__device__ __forceinline__ void lowrank_rows_t_part(const uint16_t* __restrict__ A, int r, int xc, int64_t k, int64_t c,
+                                                    int piece, u32x4* __restrict__ out) {
   const int cpr = xc / 8;
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int j0 = (int)blockIdx.y * 8;
+  const int j0 = piece * 8;
   if (c >= k) return;
   uint32_t h[8];
 #pragma unroll
@@ -221,7 +224,7 @@ __global__ __launch_bounds__(256) void lowrank_rows_t_kernel(const uint16_t* __r
     const int j = j0 + e;
     h[e] = j < 2 * r ? (uint32_t)A[(int64_t)(j % r) * k + c] : 0u;
   }
-  out[c * cpr + blockIdx.y] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+  out[c * cpr + piece] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
 }
 
 // A low-rank factor in the operand order of v_mfma_f32_16x16x32: for 32
@@ -231,13 +234,10 @@ __global__ __launch_bounds__(256) void lowrank_rows_t_kernel(const uint16_t* __r
 // rows are 16 lines for the four lanes that share one. One workgroup per 32
 // columns and factor; layout 0: Q [r, C], 1: Q [C, r].
 template <int kLayout>
-__global__ __launch_bounds__(256) void operand_order_kernel(const uint16_t* __restrict__ Q0,
-                                                            const uint16_t* __restrict__ Q1, int64_t C, int r, int tiles,
-                                                            u32x4* __restrict__ out) {
+__device__ __forceinline__ void operand_order_part(const uint16_t* __restrict__ Q, int64_t C, int r, int tiles, int64_t step,
+                                                   u32x4* __restrict__ out) {
   __shared__ uint16_t tile[32][130];  // [column][rank]
-  const uint16_t* const Q = blockIdx.y == 0 ? Q0 : Q1;
-  const int64_t c0 = (int64_t)blockIdx.x * 32;
-  out += ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * tiles * 64;
+  const int64_t c0 = step * 32;
   for (int i = threadIdx.x; i < 32 * r; i += 256) {
     const int c = kLayout == 0 ? i & 31 : i / r, j = kLayout == 0 ? i >> 5 : i % r;
     tile[c][j] = c0 + c < C ? (kLayout == 0 ? Q[j * C + c0 + c] : Q[(c0 + c) * r + j]) : (uint16_t)0;
@@ -249,7 +249,33 @@ __global__ __launch_bounds__(256) void operand_order_kernel(const uint16_t* __re
     if (j < r)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = tile[c + 2 * e][j] | ((uint32_t)tile[c + 2 * e + 1][j] << 16);
-    out[i] = v;
+    out[step * tiles * 64 + i] = v;
+  }
+}
+
+template <int kLayout>
+__global__ __launch_bounds__(256) void operand_order_kernel(const uint16_t* __restrict__ Q0,
+                                                            const uint16_t* __restrict__ Q1, int64_t C, int r, int tiles,
+                                                            u32x4* __restrict__ out) {
+  operand_order_part<kLayout>(blockIdx.y == 0 ? Q0 : Q1, C, r, tiles, blockIdx.x,
+                              out + (int64_t)blockIdx.y * gridDim.x * tiles * 64);
+}
+
+// Both factors of an adapter in one launch: Q in operand order (workgroups
+// below `steps`), then the other, F over nf outputs, as low-rank operand rows:
+// layout 0 (forward) Q = A [r, C], F = B [nf, r]; 1 (dX) Q = B [C, r], F = A [r, nf].
+template <int kLayout>
+__global__ __launch_bounds__(256) void factors_kernel(const uint16_t* __restrict__ Q, int64_t C, int r, int tiles,
+                                                      int steps, u32x4* __restrict__ order,
+                                                      const uint16_t* __restrict__ F, int64_t nf, int xc,
+                                                      u32x4* __restrict__ rows) {
+  if ((int)blockIdx.x < steps) return operand_order_part<kLayout>(Q, C, r, tiles, blockIdx.x, order);
+  const int64_t b = blockIdx.x - steps;
+  if constexpr (kLayout == 0) {
+    lowrank_rows_part(F, nf, r, xc, b * 256 + threadIdx.x, rows);
+  } else {
+    const int pieces = xc / 8;
+    lowrank_rows_t_part(F, r, xc, nf, b / pieces * 256 + threadIdx.x, (int)(b % pieces), rows);
   }
 }
 
@@ -268,11 +294,16 @@ hipError_t launch_operand_order(const uint16_t* Q, const uint16_t* Q1, int layou
   return hipGetLastError();
 }
 
-hipError_t launch_lowrank_rows_t(const uint16_t* A, int r, int64_t k, uint16_t* out, hipStream_t stream) {
-  const int xc = lora_extra_cols(r);
-  if (xc == 0 || k == 0) return hipSuccess;
-  lowrank_rows_t_kernel<<<dim3((unsigned)cdiv(k, (int64_t)256), (unsigned)(xc / 8)), 256, 0, stream>>>(
-      A, r, xc, k, reinterpret_cast<u32x4*>(out));
+hipError_t launch_factors(const uint16_t* Q, int layout, int64_t C, int64_t Cp, int r, uint16_t* order,
+                          const uint16_t* F, int64_t nf, uint16_t* rows, hipStream_t stream) {
+  const int xc = lora_extra_cols(r), steps = (int)(Cp / 32), tiles = rank_pad(r) / 16;
+  const int64_t rest = layout == 0 ? cdiv(nf * (xc / 8), (int64_t)256) : cdiv(nf, (int64_t)256) * (xc / 8);
+  const unsigned grid = (unsigned)(steps + rest);
+  u32x4 *const o = reinterpret_cast<u32x4*>(order), *const x = reinterpret_cast<u32x4*>(rows);
+  if (layout == 0)
+    factors_kernel<0><<<grid, 256, 0, stream>>>(Q, C, r, tiles, steps, o, F, nf, xc, x);
+  else
+    factors_kernel<1><<<grid, 256, 0, stream>>>(Q, C, r, tiles, steps, o, F, nf, xc, x);
   return hipGetLastError();
 }
 

@@ -578,18 +578,16 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
 
 size_t gated_db_ws_bytes(int64_t M, int64_t n, int r) {
   if (r == 0) return 0;
-  return align256(rank_parts_bytes(M, r, 2)) + align256((size_t)db_plan(M, n).splits * 2 * r * (size_t)n * 4);
+  return align256((size_t)db_plan(M, n).splits * 2 * r * (size_t)n * 4);
 }
 
 hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
-                           const float* T, int r, float scale, float* dBg, float* dBu, int accumulate, void* ws,
+                           const void* parts, int r, float* dBg, float* dBu, float* part, GradJob& job,
                            hipStream_t stream, bool f16) {
   const DbPlan pl = db_plan(M, n);
   const int rp = rank_pad(r);
-  u32x4* const Tt = static_cast<u32x4*>(ws);
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(rank_parts_bytes(M, r, 2)));
-  const hipError_t e = launch_rank_parts(T, 2, M, r, Tt, stream, f16);
-  if (e != hipSuccess) return e;
+  const u32x4* const Tt = static_cast<const u32x4*>(parts);
+  job = GradJob{part, n * r, pl.splits, 2, dBg, dBu};
   const dim3 grid((unsigned)cdiv(n, (int64_t)kDbCols), (unsigned)pl.splits);
 #define QLORA_DB2(RP, H, V) \
   gated_db_kernel<RP, H, V><<<grid, 256, 0, stream>>>(G, U, dH, M, n, Tt, r, pl.mchunk, part)
@@ -604,7 +602,7 @@ hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t*
   else QLORA_DB(128)
 #undef QLORA_DB
 #undef QLORA_DB2
-  return launch_grad_reduce(part, pl.splits, 2, n * r, scale, dBg, dBu, accumulate, stream);
+  return hipGetLastError();
 }
 
 }  // namespace qlora

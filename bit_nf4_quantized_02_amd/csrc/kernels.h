@@ -157,8 +157,11 @@ size_t operand_order_bytes(int64_t Cp, int r);
 hipError_t launch_operand_order(const uint16_t* Q, const uint16_t* Q1, int layout, int64_t C, int64_t Cp, int r,
                                 uint16_t* out, hipStream_t stream);
 
-// [k, lora_extra_cols(r)] rows of A^T: row c = [A[:, c] | A[:, c] | 0].
-hipError_t launch_lowrank_rows_t(const uint16_t* A, int r, int64_t k, uint16_t* out, hipStream_t stream);
+// One factor Q in operand order as above and the other as low-rank operand rows
+// [nf, lora_extra_cols(r)]: layout 0 (forward) Q = A [r, C], F = B [nf, r], rows
+// [B | B | 0]; 1 (dX) Q = B [C, r], F = A [r, nf], row c = [A[:, c] | A[:, c] | 0].
+hipError_t launch_factors(const uint16_t* Q, int layout, int64_t C, int64_t Cp, int r, uint16_t* order,
+                          const uint16_t* F, int64_t nf, uint16_t* rows, hipStream_t stream);
 
 // [lora_extra_cols(r), k] rows [A ; A ; 0] (bf16), the low-rank operand of the
 // nn GEMM (dX over a bf16 base).
@@ -197,16 +200,25 @@ hipError_t launch_gemv_dx(const Nf4View& w, const uint16_t* dY, int64_t M, const
                           float keep = 1.0f);
 
 // ---- adapter gradients of the feed-forward operators (colgrad.hip)
-// Q fp32 [W][M][r] as 16-bit parts in operand order.
+// Q0 fp32 [W0][M][r], Q1 [W1][M][r] as 16-bit parts in operand order (W 0: none).
 size_t rank_parts_bytes(int64_t M, int r, int W);
-hipError_t launch_rank_parts(const float* Q, int W, int64_t M, int r, void* out, hipStream_t stream, bool f16);
-// G (+)= scale * partials [splits][W][count] added in order (G1: w = 1; NULL: left out).
-hipError_t launch_grad_reduce(const float* part, int splits, int W, int64_t count, float scale, float* G0, float* G1,
-                              int accumulate, hipStream_t stream);
-// Gw (+)= scale P^T Qw, as [r, C] (j_first; C % 8 == 0, W 1 or 2) or [C, r] (W = 1).
+hipError_t launch_rank_parts(const float* Q0, int W0, void* out0, const float* Q1, int W1, void* out1, int64_t M, int r,
+                             hipStream_t stream, bool f16);
+// Gradients left as partials [splits][W][count], to be added in order (G1: w =
+// 1; NULL: left out); W 0: none.
+struct GradJob {
+  const float* part;
+  int64_t count;
+  int splits, W;
+  float *G0, *G1;
+};
+hipError_t launch_grad_reduce(const GradJob& a, const GradJob& b, float scale, int accumulate, hipStream_t stream);
+// Gw (+)= scale P^T Qw from Q's parts, as [r, C] (j_first; C % 8 == 0, W 1 or
+// 2) or [C, r] (W = 1); `job` is what launch_grad_reduce has to finish.
 size_t colgrad_ws_bytes(int64_t M, int64_t C, int r, int W);
-hipError_t launch_colgrad(const uint16_t* P, int64_t M, int64_t C, const float* Q, int W, int r, float scale, float* G0,
-                          float* G1, bool j_first, int accumulate, void* ws, hipStream_t stream, bool f16);
+hipError_t launch_colgrad(const uint16_t* P, int64_t M, int64_t C, const void* parts, int W, int r, float scale,
+                          float* G0, float* G1, bool j_first, int accumulate, float* part, GradJob& job,
+                          hipStream_t stream, bool f16);
 
 // ---- the gated feed-forward block H = silu(G) U over two NF4 weights
 // Few tokens (M <= 16). G, U and T_save ([2][M][r]) may be NULL.
@@ -245,11 +257,11 @@ size_t gated_join_ws_bytes(int64_t M, int64_t n, int r);
 hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
                              const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* D, float* P,
                              uint16_t* split, void* ws, hipStream_t stream, bool f16);
-// dBg = scale dG^T T[0], dBu = scale dU^T T[1] (either may be NULL), dG and dU
-// unrounded.
+// dBg = scale dG^T T[0], dBu = scale dU^T T[1] (either may be NULL) from T's
+// parts, dG and dU unrounded; finished by launch_grad_reduce(job).
 size_t gated_db_ws_bytes(int64_t M, int64_t n, int r);
 hipError_t launch_gated_db(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
-                           const float* T, int r, float scale, float* dBg, float* dBu, int accumulate, void* ws,
+                           const void* parts, int r, float* dBg, float* dBu, float* part, GradJob& job,
                            hipStream_t stream, bool f16);
 
 // ---- the 8-bit layer (formats and layouts: fp8.h)
