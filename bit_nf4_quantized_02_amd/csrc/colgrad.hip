@@ -84,7 +84,6 @@ __global__ __launch_bounds__(256) void colgrad_kernel(const uint16_t* __restrict
                                                       float* __restrict__ part, bool direct, float scale,
                                                       float* __restrict__ G0, float* __restrict__ G1, int accumulate) {
   constexpr int kP = parts_of<kF16>();
-  typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
   constexpr int kJTall = kRP / 16;
   constexpr int kWJ = kJTall >= 4 ? 4 : kJTall;  // waves along ranks
   constexpr int kWC = 4 / kWJ;                   // waves along columns
@@ -99,7 +98,7 @@ __global__ __launch_bounds__(256) void colgrad_kernel(const uint16_t* __restrict
   const int64_t m1 = m0 + mchunk < M ? m0 + mchunk : M;
   const int prow = t >> 3;
   const int64_t pc = c0 + 8 * (t & 7);
-  const bool inside = c0 + kDbCols <= C;
+  const int64_t pcl = pc < C ? pc : C - 8;  // (columns past C repeat the last eight, their results are not stored)
   struct Stage {
     u32x4 p[2];
   };
@@ -108,7 +107,10 @@ __global__ __launch_bounds__(256) void colgrad_kernel(const uint16_t* __restrict
     for (int h = 0; h < 2; ++h) {
       const int64_t m = mb + 32 * h + prow;
       const uint16_t* const row = P + (m < m1 ? m : m1 - 1) * C;
-      s.p[h] = inside ? *reinterpret_cast<const Vec*>(row + pc) : load8h<kVec>(row, pc, C);
+      if constexpr (kVec)  // (no branch: behind one, the next wait for a part waits for this load too)
+        s.p[h] = *reinterpret_cast<const u32x4*>(row + pcl);
+      else
+        s.p[h] = c0 + kDbCols <= C ? *reinterpret_cast<const u32x4_any*>(row + pc) : load8h<false>(row, pc, C);
     }
   };
   // (tokens past the range add nothing, whatever the row read in their place holds)
@@ -150,6 +152,7 @@ __global__ __launch_bounds__(256) void colgrad_kernel(const uint16_t* __restrict
     }
     if (mb + 64 < m1) stage(set ^ 1, mb + 64, st);
     load(mb + 128 < m1 ? mb + 128 : m0, st);
+    __builtin_amdgcn_sched_barrier(0);  // (issued here, not behind the products)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll

@@ -326,7 +326,6 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
                                                        const u32x4* __restrict__ Tt, int r, int64_t mchunk,
                                                        float* __restrict__ part) {
   constexpr int kP = parts_of<kF16>();
-  typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
   constexpr int kJTall = kRP / 16;
   constexpr int kWJ = kJTall >= 4 ? 4 : kJTall;     // waves along ranks
   constexpr int kWC = 4 / kWJ;                      // waves along columns
@@ -344,19 +343,22 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
   struct Stage {
     u32x4 g, u, d;
   };
-  const bool inside = c0 + kDbCols <= n;
-  const uint32_t lane_at = (uint32_t)(prow * n + 8 * (t & 7));
+  const int64_t pcl = pc < n ? pc : n - 8;  // (columns past n repeat the last eight, their results are not stored)
   auto load = [&](int64_t mb, Stage& s) {
     const int64_t m = mb + prow;
     const int64_t o = (m < m1 ? m : m1 - 1) * n;
-    if (inside && mb + 32 <= m1) {  // (uniform base, the lane's offset in 32 bits)
-      s.g = *reinterpret_cast<const Vec*>(G + (mb * n + c0) + lane_at);
-      s.u = *reinterpret_cast<const Vec*>(U + (mb * n + c0) + lane_at);
-      s.d = *reinterpret_cast<const Vec*>(dH + (mb * n + c0) + lane_at);
+    if constexpr (kVec) {  // (no branch: behind one, the next wait for T's parts waits for these loads too)
+      s.g = *reinterpret_cast<const u32x4*>(G + o + pcl);
+      s.u = *reinterpret_cast<const u32x4*>(U + o + pcl);
+      s.d = *reinterpret_cast<const u32x4*>(dH + o + pcl);
+    } else if (c0 + kDbCols <= n) {
+      s.g = *reinterpret_cast<const u32x4_any*>(G + o + pc);
+      s.u = *reinterpret_cast<const u32x4_any*>(U + o + pc);
+      s.d = *reinterpret_cast<const u32x4_any*>(dH + o + pc);
     } else {
-      s.g = load8h<kVec>(G + o, pc, n);
-      s.u = load8h<kVec>(U + o, pc, n);
-      s.d = load8h<kVec>(dH + o, pc, n);
+      s.g = load8h<false>(G + o, pc, n);
+      s.u = load8h<false>(U + o, pc, n);
+      s.d = load8h<false>(dH + o, pc, n);
     }
   };
   // (rows past the range add nothing, whatever the row read in their place holds)
@@ -399,22 +401,25 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
           ta[w][q][a] = Tt[((((mb >> 5) * kP + q) * 2 + w) * kJTall + wj * kJT + a) * 64 + lane];
     if (mb + 32 < m1) stage(set ^ 1, mb + 32, st);
     load(mb + 64 < m1 ? mb + 64 : m0, st);
+    __builtin_amdgcn_sched_barrier(0);  // (issued here, not behind the products)
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int b = 0; b < kCT; ++b) {
+      bf16x8 pb[2][kP];
 #pragma unroll
-      for (int b = 0; b < kCT; ++b) {
-        bf16x8 pb[kP];
+      for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int q = 0; q < kP; ++q)
-          pb[q] = db_operand(sm + ((set * 2 + w) * kP + q) * kDbTile, wc * kCT + b, lane);
+          pb[w][q] = db_operand(sm + ((set * 2 + w) * kP + q) * kDbTile, wc * kCT + b, lane);
 #pragma unroll
-        for (int a = 0; a < kJT; ++a)
+      for (int order = kP - 1; order >= 0; --order)
 #pragma unroll
-          for (int order = kP - 1; order >= 0; --order)
+        for (int q = 0; q <= order; ++q)
 #pragma unroll
-            for (int q = 0; q <= order; ++q)
-              acc[w][a][b] = mfma16<kF16>(__builtin_bit_cast(bf16x8, ta[w][order - q][a]), pb[q], acc[w][a][b]);
-      }
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int a = 0; a < kJT; ++a)
+              acc[w][a][b] = mfma16<kF16>(__builtin_bit_cast(bf16x8, ta[w][order - q][a]), pb[w][q], acc[w][a][b]);
+    }
     __syncthreads();
   }
   // D[j][c]: lane -> c = lane % 16, j = 4 (lane / 16) + v; partials [split][w][n][r], as dB
