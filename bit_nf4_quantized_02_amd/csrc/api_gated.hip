@@ -47,7 +47,7 @@ struct FwdWs {
 
 size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
   if (few_tokens(M, n, k)) {
-    o.few = cv.take<char>(gemv_pair_ws_bytes(M, k, r));
+    o.few = cv.take<char>(gemv_pair_ws_bytes(M, n, k, r));
     return cv.used;
   }
   const int xc = gated_extra_cols(r);

@@ -29,16 +29,8 @@
 // low-rank term T B^T is formed with fp32 MFMAs (one 16-row tile per wave,
 // T and B exact in fp32) and added in fp32, and Y is rounded to bf16 once.
 #include "common.h"
+#include "gemv_nf4.h"
 #include "kernels.h"
-
-// The gated feed-forward block's few-token form is the same kernel with the
-// gate weight's rows as one tile and the up weight's as the other (kPair): X
-// is read and the launch paid once for both, and H = silu(G) U is formed from
-// the unrounded fp32 sums in the epilogue.
-
-#ifndef QLORA_GEMV_XP_MIN_M
-#define QLORA_GEMV_XP_MIN_M 5
-#endif
 
 namespace qlora {
 
@@ -71,35 +63,6 @@ template <int kW>
 constexpr int lut_copies() { return kW == 8 ? 32 : 16; }
 constexpr int kRingDepth = 3;  // chunks of codes per wave: one worked on, two in flight
 
-// s_waitcnt immediate that waits for LDS / scalar-memory operations only
-// (lgkmcnt <= n; vmcnt and expcnt left at their maxima)
-constexpr int lgkm_wait(int n) { return 0xC07F | (n << 8); }
-
-// Swizzle of a 128-byte code line in LDS: row r of a 16-row tile keeps its
-// 16-byte segment g at position g ^ sw(r). The 8 (or 16) lanes that read one
-// segment of 8 (16) consecutive rows in one LDS cycle then hit distinct banks
-// whether the LDS serves 128 or 256 bytes per cycle.
-__device__ __forceinline__ int code_swz(int r) { return (r ^ (r >> 3)) & 7; }
-
-// Scale fields of block blk in one of the three stored forms, without
-// branches (kForm 0: double-quantized, E4M3 code + fp32 second-level scale
-// per 256 blocks; 1: fp32 per block; 2: bf16 per block), as scale_fields.
-// c8r / s2r: descriptors of the code and scale arrays.
-template <int kForm>
-__device__ __forceinline__ void scale_fields_of(const i32x4& c8r, const i32x4& s2r, uint32_t blk, uint32_t& c8,
-                                                float& s2v) {
-  if constexpr (kForm == 0) {
-    c8 = raw_buffer_load_u8(c8r, (int)blk, 0, 0);
-    s2v = __builtin_bit_cast(float, raw_buffer_load_u32(s2r, (int)((blk / kDqBlock) * 4), 0, 0));
-  } else if constexpr (kForm == 1) {
-    c8 = kE4m3One;
-    s2v = __builtin_bit_cast(float, raw_buffer_load_u32(s2r, (int)(blk * 4), 0, 0));
-  } else {
-    c8 = kE4m3One;
-    s2v = bf16_bits_to_f32(raw_buffer_load_u16(s2r, (int)(blk * 2), 0, 0));
-  }
-}
-
 // Scale fields of one 256-column chunk for the lane's rows, and its
 // activation operand.
 template <int kT>
@@ -109,109 +72,12 @@ struct GvStage {
   u32x4 xa[8];
 };
 
-// The gated block (kPair): X [M, K] for few tokens in operand order (xp not
-// NULL), and the projections X Ag^T, X Au^T as partials [range][2][M][r]. A
-// wave takes 128-column blocks in turn: 16 neighbouring lanes load 256 bytes of
-// a row, which pass through the wave's own LDS into the A operand of
-// v_mfma_f32_16x16x32; the workgroup's four waves are added in wave order. The
-// blocks cover whole 256-column chunks (zeros past K), as the GEMV reads them.
-template <int kRP, bool kF16>
-__global__ __launch_bounds__(256) void gemv_prep_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K, int nb,
-                                                        const uint16_t* __restrict__ Ag, const uint16_t* __restrict__ Au,
-                                                        int r, int bchunk, u32x4* __restrict__ xp,
-                                                        float* __restrict__ part) {
-  constexpr int kTiles = kRP / 16, kTA = kTiles > 0 ? kTiles : 1;
-  constexpr int kPitch = 256 + 16;
-  __shared__ __attribute__((aligned(16))) char turn[4][kTiles > 0 ? 16 * kPitch : 16];
-  __shared__ float red[4][16][kTiles > 0 ? kRP : 1];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b0 = (int)blockIdx.x * bchunk, b1 = b0 + bchunk < nb ? b0 + bchunk : nb;
-  const int lr = lane >> 4, lc = 8 * (lane & 15);
-  f32x4 acc[2][kTA];
-#pragma unroll
-  for (int w = 0; w < 2; ++w)
-#pragma unroll
-    for (int t = 0; t < kTA; ++t) acc[w][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kb = b0 + wave; kb < b1; kb += 4) {
-    u32x4 x[4], q[2][kTA][4];
-    // (whole blocks load without a test per lane, which would put each load
-    // behind a branch that waits for it)
-    const bool whole = ((int64_t)kb + 1) * 128 <= K;
-    const uint16_t* const xb = X + (int64_t)kb * 128 + lc;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t m = 4 * u + lr < M ? 4 * u + lr : M - 1;
-      x[u] = whole ? *reinterpret_cast<const u32x4*>(xb + m * K) : load8h<true>(X + m * K, (int64_t)kb * 128 + lc, K);
-    }
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int64_t j = 16 * t + (lane & 15) < r ? 16 * t + (lane & 15) : r - 1;  // (ranks past r: not stored)
-        const int64_t c = (int64_t)kb * 128 + 32 * s + 8 * (lane >> 4);
-        q[0][t][s] = whole ? *reinterpret_cast<const u32x4*>(Ag + j * K + c) : load8h<true>(Ag + j * K, c, K);
-        q[1][t][s] = whole ? *reinterpret_cast<const u32x4*>(Au + j * K + c) : load8h<true>(Au + j * K, c, K);
-      }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int m = 4 * u + lr;
-      if (m >= M) x[u] = u32x4{0u, 0u, 0u, 0u};
-      if (xp != nullptr) {
-        const int c = (kb & 1) * 128 + lc;  // column of the 256-column chunk
-        xp[((int64_t)(kb >> 1) * 8 + ((c >> 3) & 7)) * 64 + 16 * (c >> 6) + m] = x[u];
-      }
-      if constexpr (kTiles > 0) *reinterpret_cast<u32x4*>(turn[wave] + m * kPitch + 2 * lc) = x[u];
-    }
-    // lanes read what others wrote: the LDS keeps a wave's order, the compiler must too
-    asm volatile("" ::: "memory");
-#pragma unroll
-    for (int s = 0; s < (kTiles > 0 ? 4 : 0); ++s) {
-      const bf16x8 a = *reinterpret_cast<const bf16x8*>(turn[wave] + (lane & 15) * kPitch + 64 * s + 16 * (lane >> 4));
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) acc[w][t] = mfma16<kF16>(a, __builtin_bit_cast(bf16x8, q[w][t][s]), acc[w][t]);
-    }
-    asm volatile("" ::: "memory");
-  }
-  if constexpr (kTiles > 0) {
-    for (int w = 0; w < 2; ++w) {
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          red[wave][4 * (lane >> 4) + v][16 * t + (lane & 15)] = w == 0 ? acc[0][t][v] : acc[1][t][v];
-      __syncthreads();
-      for (int o = threadIdx.x; o < (int)M * r; o += 256) {
-        const int m = o / r, j = o % r;
-        part[(((int64_t)blockIdx.x * 2 + w) * M + m) * r + j] = red[0][m][j] + red[1][m][j] + red[2][m][j] + red[3][m][j];
-      }
-    }
-  }
-}
-
-// The up weight of the gated block (kPair), its low-rank factor and the
-// block's outputs (the kernel's own weight is the gate, its T holds both
-// projections [2][M][r], Y receives H; G and U may be NULL).
-struct GvSecond {
-  const uint8_t* codes;
-  const uint8_t* code8;
-  const float* s2;
-  const float* mean;
-  const float* codebook;
-  const uint16_t* B;
-  uint16_t* G;
-  uint16_t* U;
-};
-
 // kT: 16-row tiles per workgroup (each wave covers all of them over its
 // share of the contraction); kW: waves. kXp: activations from the
 // operand-ordered copy Xp (else read in place from X). kF16: fp16
 // activations, weights, B and output (the compute-type ablation). kForm: the
 // block-scale form (scale_fields_of).
-template <int kT, int kW, bool kXp, bool kF16, int kForm, bool kPair = false>
+template <int kT, int kW, bool kXp, bool kF16, int kForm>
 __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ code8,
                                                        const float* __restrict__ s2,
@@ -221,14 +87,13 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
                                                        const u32x4* __restrict__ Xp, int64_t M,
                                                        const float* __restrict__ T,
                                                        const uint16_t* __restrict__ B, int r, float scale,
-                                                       uint16_t* __restrict__ Y, GvSecond up = {}) {
-  static_assert(!kPair || kT == 2, "a pair is one tile of each weight");
-  constexpr int NT = kPair ? 16 : 16 * kT;  // output columns per workgroup
+                                                       uint16_t* __restrict__ Y) {
+  constexpr int NT = 16 * kT;
   constexpr int kSlot = kT * 2048;  // one wave's codes of one chunk: kT tiles x 16 rows x 128 bytes
   // three separate ring arrays, so the compiler can tell the one being read
   // from the ones being filled by direct copies (and waits only for the copy
   // of the chunk it reads)
-  constexpr int kLutCopies = kPair ? 16 : lut_copies<kW>();
+  constexpr int kLutCopies = lut_copies<kW>();
   __shared__ __attribute__((aligned(16))) char lut[256 * kLutCopies * 8];
   __shared__ __attribute__((aligned(16))) char ring0[kW * kSlot];
   __shared__ __attribute__((aligned(16))) char ring1[kW * kSlot];
@@ -239,23 +104,12 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
   // table fill below reads LDS, not 16 rounds of global loads per thread
   float* const levels = reinterpret_cast<float*>(ring0);
   if (t < 16) levels[t] = codebook[t];
-  if constexpr (kPair) {
-    if (t < 16) levels[16 + t] = up.codebook[t];
-  }
   __syncthreads();
-  // kPair: where the two weights' levels are equal (the usual case) both read
-  // one table of 16 copies; else each has its own of 8 copies in its half.
-  bool same = true;
-  if constexpr (kPair)
-    same = __ballot(__float_as_uint(levels[lane & 15]) != __float_as_uint(levels[16 + (lane & 15)])) == 0;
   for (int i = t; i < 256 * kLutCopies; i += 64 * kW) {
-    const int e = same ? i / kLutCopies : (i >> 3) & 255;
-    const float* const lv = same || i < 2048 ? levels : levels + 16;
-    reinterpret_cast<float2*>(lut)[i] = float2{lv[e & 15], lv[e >> 4]};
+    const int e = i / kLutCopies;
+    reinterpret_cast<float2*>(lut)[i] = float2{levels[e & 15], levels[e >> 4]};
   }
-  float mean[kPair ? 2 : 1];
-  mean[0] = weight_mean(code8, mean_p);
-  if constexpr (kPair) mean[1] = weight_mean(up.code8, up.mean);
+  const float mean = weight_mean(code8, mean_p);
   const int64_t n0 = (int64_t)blockIdx.x * NT;
   // this wave's contiguous range of 256-column chunks (a multiple-of-64 tail
   // in the last one)
@@ -273,9 +127,7 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
   // N lie past the end of the codes and read as zero (their outputs are not
   // stored); columns past K in the last chunk read the next row's codes and
   // meet zero activations.
-  i32x4 crs[kPair ? 2 : 1];
-  crs[0] = make_rsrc(codes, N * (K / 2));
-  if constexpr (kPair) crs[1] = make_rsrc(up.codes, N * (K / 2));
+  const i32x4 crs = make_rsrc(codes, N * (K / 2));
   uint32_t cvoff[kT][2];
 #pragma unroll
   for (int i = 0; i < kT; ++i)
@@ -283,18 +135,16 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
     for (int h = 0; h < 2; ++h) {
       const int rr = 8 * h + (lane >> 3);
       const int g = (lane & 7) ^ code_swz(rr);
-      cvoff[i][h] = (uint32_t)((n0 + (kPair ? 0 : 16 * i) + rr) * (K / 2) + 16 * g);
+      cvoff[i][h] = (uint32_t)((n0 + 16 * i + rr) * (K / 2) + 16 * g);
     }
   // reads: row col, logical segments 2 grp and 2 grp + 1 (64 codes)
   const uint32_t rd0 = (uint32_t)(col * 128 + 16 * ((2 * grp) ^ code_swz(col)));
-  const uint32_t lane_off = same ? (uint32_t)(lane % kLutCopies) * 8 : (uint32_t)(lane % 8) * 8;
-  const uint32_t up_off = same ? lane_off : lane_off + 16384;  // kPair: the up weight's table
-  const int lut_shift = same ? 7 : 6;                          // kPair: log2 bytes per entry
+  const uint32_t lane_off = (uint32_t)(lane % kLutCopies) * 8;
   // scale rows (clamped: rows past N are computed and dropped)
   uint32_t bbase[kT];  // (blocks < 2^27: the codes stay under 4 GiB)
 #pragma unroll
   for (int i = 0; i < kT; ++i) {
-    const int64_t n = n0 + (kPair ? 0 : 16 * i) + col;
+    const int64_t n = n0 + 16 * i + col;
     bbase[i] = (uint32_t)((n < N ? n : N - 1) * kblocks);
   }
   // activations: Xp[q][s][lane] (operand order), or X[col][256 q + 64 grp +
@@ -304,14 +154,8 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
 
   // scale arrays (blocks < 2^30: 32-bit byte offsets)
   const int64_t nblk = N * kblocks;
-  const int64_t s2_bytes = kForm == 0 ? cdiv(nblk, (int64_t)kDqBlock) * 4 : nblk * (kForm == 1 ? 4 : 2);
-  i32x4 c8rs[kPair ? 2 : 1], s2rs[kPair ? 2 : 1];
-  c8rs[0] = make_rsrc(code8, kForm == 0 ? nblk : 0);
-  s2rs[0] = make_rsrc(s2, s2_bytes);
-  if constexpr (kPair) {
-    c8rs[1] = make_rsrc(up.code8, kForm == 0 ? nblk : 0);
-    s2rs[1] = make_rsrc(up.s2, s2_bytes);
-  }
+  const i32x4 c8rs = make_rsrc(code8, kForm == 0 ? nblk : 0);
+  const i32x4 s2rs = make_rsrc(s2, kForm == 0 ? cdiv(nblk, (int64_t)kDqBlock) * 4 : nblk * (kForm == 1 ? 4 : 2));
 
   auto issue = [&](int j, char* R, GvStage<kT>& st) {
     const int q = wave + kW * (j < cnt ? j : cnt - 1);  // past the range: the last chunk again
@@ -319,12 +163,11 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
 #pragma unroll
     for (int i = 0; i < kT; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) copy16(crs[kPair ? i : 0], cvoff[i][h], q * 128, dst + i * 2048 + h * 1024);
+      for (int h = 0; h < 2; ++h) copy16(crs, cvoff[i][h], q * 128, dst + i * 2048 + h * 1024);
     const int kc = q * 256 + 64 * grp;
     const uint32_t bq = (uint32_t)(kc < K ? kc / kBlock : kblocks - 1);
 #pragma unroll
-    for (int i = 0; i < kT; ++i)
-      scale_fields_of<kForm>(c8rs[kPair ? i : 0], s2rs[kPair ? i : 0], bbase[i] + bq, st.c8[i], st.s2v[i]);
+    for (int i = 0; i < kT; ++i) scale_fields_of<kForm>(c8rs, s2rs, bbase[i] + bq, st.c8[i], st.s2v[i]);
     if constexpr (kXp) {
 #pragma unroll
       for (int s = 0; s < 8; ++s) st.xa[s] = raw_buffer_load_b128(xrs, (int)xvoff, q * 8192 + s * 1024, 0);
@@ -361,7 +204,7 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
         cw[i][e] = c0[e];
         cw[i][4 + e] = c1[e];
       }
-      cp[i] = decode_block_scale(st.c8[i], st.s2v[i], mean[kPair ? i : 0]);
+      cp[i] = decode_block_scale(st.c8[i], st.s2v[i], mean);
     }
     float2 lv[2][4 * kGw];
     auto gather = [&](int g, float2 (&out)[4 * kGw]) {
@@ -371,9 +214,7 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           uint32_t addr;
-          if constexpr (kPair) {
-            addr = (((cw[i][s0 + w] >> (8 * p)) & 0xFFu) << lut_shift) | (i == 0 ? lane_off : up_off);
-          } else if constexpr (kLutCopies == 32) {
+          if constexpr (kLutCopies == 32) {
             // bytes of the result: lane_off (byte 0 of the second operand),
             // code byte p (byte p of the first), zero, zero
             addr = __builtin_amdgcn_perm(cw[i][s0 + w], lane_off, 0x0C0C0400u + ((uint32_t)p << 8));
@@ -462,12 +303,11 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
     for (int i = wave; i < kT; i += kW) {
       f32x4 l = f32x4{0.f, 0.f, 0.f, 0.f};
       const int m = lane & 15;
-      const int64_t n = n0 + (kPair ? 0 : i * 16) + (lane & 15);
-      const uint16_t* const Bi = kPair && i == 1 ? up.B : B;
+      const int64_t n = n0 + i * 16 + (lane & 15);
       for (int j0 = 0; j0 < r; j0 += 4) {
         const int j = j0 + (lane >> 4);
-        const float a = (m < M && j < r) ? T[((kPair ? i * M : 0) + m) * r + j] : 0.0f;
-        const float b = (n < N && j < r) ? from16<kF16>(Bi[n * r + j]) : 0.0f;
+        const float a = (m < M && j < r) ? T[m * r + j] : 0.0f;
+        const float b = (n < N && j < r) ? from16<kF16>(B[n * r + j]) : 0.0f;
         l = __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, l, 0, 0, 0);
       }
 #pragma unroll
@@ -480,21 +320,11 @@ __global__ __launch_bounds__(64 * kW) void gemv_nf4_kernel(const uint8_t* __rest
     const int64_t n = n0 + nl;
     if (m >= M || n >= N) continue;
     const int i = nl >> 4, nc = nl & 15;
-    auto sum = [&](int i) {
-      float y = red[0][i][m][nc];
+    float y = red[0][i][m][nc];
 #pragma unroll
-      for (int w2 = 1; w2 < kW; ++w2) y += red[w2][i][m][nc];  // in wave order
-      return r > 0 ? fmaf(scale, lred[i][m][nc], y) : y;
-    };
-    const float y = sum(i);
-    if constexpr (kPair) {
-      const float u = sum(1);
-      Y[m * N + n] = to16<kF16>(silu(y) * u);
-      if (up.G) up.G[m * N + n] = to16<kF16>(y);
-      if (up.U) up.U[m * N + n] = to16<kF16>(u);
-    } else {
-      Y[m * N + n] = to16<kF16>(y);
-    }
+    for (int w2 = 1; w2 < kW; ++w2) y += red[w2][i][m][nc];  // in wave order
+    if (r > 0) y = fmaf(scale, lred[i][m][nc], y);
+    Y[m * N + n] = to16<kF16>(y);
   }
 }
 
@@ -504,19 +334,11 @@ bool gemv_fits(int64_t n, int64_t k) { return (n + 256) * (k / 2) < ((int64_t)1 
 
 size_t gemv_ws_bytes(int64_t k) { return align256((size_t)cdiv(k, 256) * 512 * 16); }
 
-// Token counts from which the activations are first rewritten in operand
-// order: below it the few distinct rows an activation load touches cost less
-// than the extra pass (measured on the 70B-class shapes). Weights with fewer
-// than kXpMinN rows never take it: their workgroups re-read X only a few
-// times, and the extra launch costs more (a 1024 x 1024 layer at M = 16).
-constexpr int64_t kXpMinM = QLORA_GEMV_XP_MIN_M;
-constexpr int64_t kXpMinN = 4096;
-
 hipError_t launch_gemv(const Nf4View& w, const uint16_t* X, int64_t M, const float* T, const uint16_t* B, int r,
                        float scale, uint16_t* Y, void* ws, hipStream_t stream, bool f16) {
   if (!gemv_fits(w.n, w.k)) return hipErrorInvalidValue;
   u32x4* Xp = static_cast<u32x4*>(ws);
-  const bool xp = M >= kXpMinM && w.n >= kXpMinN;
+  const bool xp = gemv_orders_x(M, w.n);
   if (xp) {
     const int64_t entries = cdiv(w.k, (int64_t)256) * 512;
     gemv_xperm_kernel<<<(unsigned)cdiv(entries, (int64_t)256), 256, 0, stream>>>(X, M, w.k, Xp, entries);
@@ -552,75 +374,6 @@ hipError_t launch_gemv(const Nf4View& w, const uint16_t* X, int64_t M, const flo
 #undef QLORA_GEMV2
 #undef QLORA_GEMV3
 #undef QLORA_GEMV4
-  return hipGetLastError();
-}
-
-// Column ranges of the block's projections: about one 128-column block per wave,
-// at most 16 workgroups. (A small kernel adds their partials: added in the
-// epilogue by every workgroup of the GEMV, they took 24 us at 28672 x 8192 where
-// the launch takes 3, and the LDS has no room to add them at its start.)
-struct PairPlan {
-  int nb, chunk, parts;
-};
-
-PairPlan pair_plan(int64_t k) {
-  const int nb = (int)(2 * cdiv(k, (int64_t)256));
-  const int chunk = cdiv(nb, 16) > 4 ? (int)cdiv(nb, 16) : 4;
-  return PairPlan{nb, chunk, (int)cdiv(nb, chunk)};
-}
-
-size_t gemv_pair_ws_bytes(int64_t M, int64_t k, int r) {
-  const PairPlan p = pair_plan(k);
-  return gemv_ws_bytes(k) + align256((size_t)p.parts * 2 * M * r * 4) + align256((size_t)2 * M * r * 4);
-}
-
-hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const uint16_t* Ag,
-                            const uint16_t* Bg, const uint16_t* Au, const uint16_t* Bu, int r, float scale, uint16_t* H,
-                            uint16_t* G, uint16_t* U, float* T_save, void* ws, hipStream_t stream, bool f16) {
-  if (!gemv_fits(g.n, g.k)) return hipErrorInvalidValue;
-  u32x4* Xp = static_cast<u32x4*>(ws);
-  const PairPlan pl = pair_plan(g.k);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + gemv_ws_bytes(g.k));
-  const bool xp = M >= kXpMinM && g.n >= kXpMinN;
-  if (xp || r > 0) {
-#define QLORA_GPREP2(RP, H16) \
-  gemv_prep_kernel<RP, H16><<<(unsigned)pl.parts, 256, 0, stream>>>(X, M, g.k, pl.nb, Ag, Au, r, pl.chunk, xp ? Xp : nullptr, part)
-#define QLORA_GPREP(RP) { if (f16) QLORA_GPREP2(RP, true); else QLORA_GPREP2(RP, false); }
-    if (r == 0) QLORA_GPREP(0)
-    else if (r <= 16) QLORA_GPREP(16)
-    else if (r <= 32) QLORA_GPREP(32)
-    else if (r <= 64) QLORA_GPREP(64)
-    else QLORA_GPREP(128)
-#undef QLORA_GPREP
-#undef QLORA_GPREP2
-  }
-  float* const T = T_save ? T_save : part + align256((size_t)pl.parts * 2 * M * r * 4) / 4;
-  if (r > 0) {
-    const hipError_t e = launch_rowdot_finalize(part, pl.parts, 2 * M, r, T, nullptr, scale, stream, f16);
-    if (e != hipSuccess) return e;
-  }
-  const GvSecond up{u.codes, u.code8, u.s2, u.mean, u.codebook, Bu, G, U};
-  // four waves (two workgroups per CU) where there are at least two per CU, else eight
-  const int64_t wgs = cdiv(g.n, (int64_t)16);
-  const int form = g.code8 ? 0 : (g.s2_bf16 ? 2 : 1);
-#define QLORA_GVP3(W, XP, H16, F)                                                                               \
-  gemv_nf4_kernel<2, W, XP, H16, F, true><<<dim3((unsigned)wgs), 64 * W, 0, stream>>>(                           \
-      g.codes, g.code8, g.s2, g.mean, g.codebook, g.s2_bf16, g.n, g.k, X, Xp, M, T, Bg, r, scale, H, up)
-#define QLORA_GVP2(W, XP, H16)                   \
-  {                                              \
-    if (form == 0) QLORA_GVP3(W, XP, H16, 0);    \
-    else if (form == 1) QLORA_GVP3(W, XP, H16, 1); \
-    else QLORA_GVP3(W, XP, H16, 2);              \
-  }
-#define QLORA_GVP1(W, XP) \
-  { if (f16) QLORA_GVP2(W, XP, true) else QLORA_GVP2(W, XP, false) }
-#define QLORA_GVP(W) \
-  { if (xp) QLORA_GVP1(W, true) else QLORA_GVP1(W, false) }
-  if (wgs >= 512) QLORA_GVP(4) else QLORA_GVP(8)
-#undef QLORA_GVP
-#undef QLORA_GVP1
-#undef QLORA_GVP2
-#undef QLORA_GVP3
   return hipGetLastError();
 }
 

@@ -222,7 +222,7 @@ hipError_t launch_colgrad(const uint16_t* P, int64_t M, int64_t C, const void* p
 
 // ---- the gated feed-forward block H = silu(G) U over two NF4 weights
 // Few tokens (M <= 16). G, U and T_save ([2][M][r]) may be NULL.
-size_t gemv_pair_ws_bytes(int64_t M, int64_t k, int r);
+size_t gemv_pair_ws_bytes(int64_t M, int64_t n, int64_t k, int r);
 hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const uint16_t* Ag,
                             const uint16_t* Bg, const uint16_t* Au, const uint16_t* Bu, int r, float scale, uint16_t* H,
                             uint16_t* G, uint16_t* U, float* T_save, void* ws, hipStream_t stream, bool f16);
