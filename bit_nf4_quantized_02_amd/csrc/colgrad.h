@@ -54,4 +54,26 @@ __device__ __forceinline__ bf16x8 db_operand(const char* tile, int s, int lane) 
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// Token ranges for `groups` column groups of `steps` steps each: the number
+// (at most `most`) for which the fullest CU has least to do, every range
+// costing `extra` steps more (its first loads, its partials). The ranges of
+// one CU share its issue, so what counts is how many it gets: 344 groups in 3
+// ranges are 1032 workgroups, five of 43 steps on some of the 256 CUs, in 2
+// ranges three of 64 (dB of 4096 x 22016, r = 64: 232 -> 217 us). One alone
+// does not fill a CU and counts as two (dA of 4096 x 8192 from 256 workgroups
+// 43 us, from 512 39).
+inline int token_ranges(int64_t groups, int64_t steps, int64_t most, int64_t extra) {
+  int best = 1;
+  int64_t least = 0;
+  for (int64_t s = 1; s <= most; ++s) {
+    const int64_t share = cdiv(groups * s, (int64_t)256) > 2 ? cdiv(groups * s, (int64_t)256) : 2;
+    const int64_t cost = share * (cdiv(steps, s) + extra);
+    if (s == 1 || cost < least) {
+      least = cost;
+      best = (int)s;
+    }
+  }
+  return best;
+}
+
 }  // namespace qlora

@@ -217,18 +217,17 @@ __global__ __launch_bounds__(256) void grad_reduce_kernel(GradJob j0, GradJob j1
   }
 }
 
-// Token ranges: about 512 workgroups, each at least 128 tokens, at most 16
-// ranges (their partials are written and read again).
+// Token ranges: each at least 128 tokens, at most 16 (their partials are
+// written and read again).
 struct GradPlan {
   int64_t mchunk;
   int splits;
 };
 
 GradPlan grad_plan(int64_t M, int64_t C) {
-  int64_t s = cdiv((int64_t)512, cdiv(C, (int64_t)kDbCols));
-  if (s > cdiv(M, (int64_t)128)) s = cdiv(M, (int64_t)128);
-  if (s > 16) s = 16;
-  const int64_t mchunk = cdiv(cdiv(M, s), (int64_t)64) * 64;
+  const int64_t steps = cdiv(M, (int64_t)64), most = cdiv(M, (int64_t)128);
+  const int64_t s = token_ranges(cdiv(C, (int64_t)kDbCols), steps, most < 16 ? most : 16, 2);
+  const int64_t mchunk = cdiv(steps, s) * 64;
   return {mchunk, (int)cdiv(M, mchunk)};
 }
 

@@ -298,8 +298,18 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
     return;
   }
   const int w = x >= r ? 1 : 0, j = x - w * r;
-  float s = part[(w * M + m) * r + j];
-  for (int p = 1; p < splits; ++p) s += part[(((int64_t)p * 2 + w) * M + m) * r + j];
+  // (eight loads together: those past the last repeat it and are not added)
+  const float* const src = part + (w * M + m) * r + j;
+  const int64_t pitch = 2 * M * r;
+  float s = 0.0f;
+  for (int p0 = 0; p0 < splits; p0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) v[p] = src[(p0 + p < splits ? p0 + p : splits - 1) * pitch];
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      if (p0 + p < splits) s = p0 + p == 0 ? v[p] : s + v[p];
+  }
   if (P) P[(w * M + m) * r + j] = s;
   if (split) {
     float v = scale * s;
@@ -458,17 +468,16 @@ JoinPlan join_plan(int64_t M, int64_t n) {
   return {cchunk, (int)cdiv(np, cchunk)};
 }
 
-// Token ranges of dB: about 1024 workgroups, each at least 128 tokens.
+// Token ranges of dB: each at least 128 tokens, at most 16.
 struct DbPlan {
   int64_t mchunk;
   int splits;
 };
 
 DbPlan db_plan(int64_t M, int64_t n) {
-  int64_t s = cdiv((int64_t)1024, cdiv(n, (int64_t)kDbCols));
-  if (s > cdiv(M, (int64_t)128)) s = cdiv(M, (int64_t)128);
-  if (s > 16) s = 16;
-  const int64_t mchunk = cdiv(cdiv(M, s), (int64_t)32) * 32;
+  const int64_t steps = cdiv(M, (int64_t)32), most = cdiv(M, (int64_t)128);
+  const int64_t s = token_ranges(cdiv(n, (int64_t)kDbCols), steps, most < 16 ? most : 16, 4);
+  const int64_t mchunk = cdiv(steps, s) * 32;
   return {mchunk, (int)cdiv(M, mchunk)};
 }
 
