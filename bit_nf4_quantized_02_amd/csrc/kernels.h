@@ -276,8 +276,8 @@ hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream
 // Activations P [M, C] -> codes and scales ([M, C up to 128] and the GEMM's
 // scale words; few, M <= 16: the GEMV's operand order, fp8_gemv_*_bytes),
 // and for r > 0 the partials [splits][W][M][r] of P Q^T; W factors in operand
-// order one after the other, for few one as it is, [r, C]. codes NULL (W = 2):
-// the projections only.
+// order one after the other, for few one as it is, [r, C]. codes NULL (always
+// for W = 2): the projections only.
 struct Fp8Prep {
   int chunk, splits;
 };

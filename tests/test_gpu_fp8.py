@@ -176,3 +176,22 @@ def test_empty_batch_accumulate_and_partial_outputs(q):
     assert not z[1].any() and not z[2].any() and z[0].shape == (0, k)
     again = q.fp8_linear_bwd(w, X, T, dY, A, B, s)
     assert all(torch.equal(a, b) for a, b in zip(again, (dX, dA, dB)))
+
+
+@pytest.mark.parametrize("n,k,r", [(1030, 1088, 8), (70, 320, 0), (8192 + 9, 192, 4)])
+def test_bytes_around_the_weight_are_not_read_as_codes(q, n, k, r):
+    """The same weight inside a buffer whose other bytes are NaN codes gives the same results: the tiles of
+    the forward, of dX (whose contraction ends inside one) and of the single-token form end with the weight."""
+    w = q.quantize_fp8(_normal((n, k), 0.02, torch.float32, 38, n, k).cuda())
+    buf = torch.full((n + 512, w.codes.shape[1]), 0x7F, dtype=torch.uint8, device="cuda")
+    buf[256:256 + n] = w.codes
+    inner = q.FP8Weight(n, k, buf[256:256 + n], w.scale)
+    A = _normal((r, k), 0.05, BF, 38, 1).cuda() if r else None
+    B = _normal((n, r), 0.05, BF, 38, 2).cuda() if r else None
+    for m in (1, 16, 40, 300):
+        say(f"case: fp8 inside NaN codes M={m} N={n} K={k}")
+        X, dY = _normal((m, k), 1.0, BF, 38, m, 3).cuda(), _normal((m, n), 1.0, BF, 38, m, 4).cuda()
+        a, b = (q.fp8_linear_fwd(v, X, A, B, 0.5) for v in (w, inner))
+        assert torch.isfinite(a[0]).all() and torch.equal(a[0], b[0])
+        a, b = (q.fp8_linear_bwd(v, X, None, dY, A, B, 0.5) for v in (w, inner))
+        assert torch.isfinite(a[0]).all() and torch.equal(a[0], b[0])

@@ -130,6 +130,29 @@ def test_storage_forms(q, m, form):
     _run(q, m, 200, 320, 8, BF, **form)
 
 
+@pytest.mark.parametrize("m,n,k,r,dt,form", [
+    (1, 12307, 512, 7, BF, {}), (16, 4101, 2304, 66, HF, {}), (5, 8209, 256, 128, BF, dict(double_quant=False)),
+    (2, 4100, 4864, 12, BF, dict(double_quant=False, scale_dtype=BF)),
+    (8, 4130, 2112, 33, BF, dict(double_quant=False, scale_dtype=BF)), (4, 4112, 2304, 0, HF, {}),
+])
+def test_few_tokens_several_row_groups(q, m, n, k, r, dt, form):
+    """More than 256 groups of 16 rows (a workgroup takes several), the last one short, with whole and cut
+    256-column chunks, chunk counts that leave waves without one, ranks of every remainder."""
+    say(f"case: gated M={m} N={n} K={k} r={r} {dt} {form}")
+    _run(q, m, n, k, r, dt, **form)
+
+
+@pytest.mark.parametrize("m", [2, 16])
+def test_levels_of_each_weight_whole_chunks(q, m):
+    n, k, s = 4120, 512, 0.5
+    grid = torch.tensor(q.build_uniform4_codebook(), device="cuda")
+    wg = q.quantize_nf4(_normal((n, k), 0.03, BF, 44, 0))
+    wu = q.quantize_nf4(_normal((n, k), 0.03, BF, 44, 1), codebook=grid)
+    block = (wg, wu, None, None, None, None)
+    X = _normal((m, k), 1.0, BF, 44, 2)
+    _check_fwd(q, block, X, s, q.gated_fwd(*block[:2], X, *block[2:], s), BF)
+
+
 @pytest.mark.parametrize("m,n", [(4, 200), (16, 8200), (50, 200)])
 def test_levels_of_each_weight(q, m, n):
     """Gate in NF4, up on the uniform grid: each tile is expanded with its own levels."""
