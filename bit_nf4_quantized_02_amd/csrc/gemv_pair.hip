@@ -14,8 +14,8 @@
 // groups in turn, the table is built once and the ring runs on from one group
 // into the next, whose first chunks are in flight while the last group's sums
 // are joined. Bound by the expansion (about 3 vector operations per weight and
-// one LDS read per two) as much as by HBM. (28672 x 8192, one token: 69 us,
-// 3.5 TB/s of codes and scales; 11008 x 4096, 16 fp16 tokens: 22. A workgroup
+// one LDS read per two) as much as by HBM. (28672 x 8192, one token: 66 us,
+// 3.7 TB/s of codes and scales; 11008 x 4096, 16 fp16 tokens: 22. A workgroup
 // of four waves for each row group, two on a CU: 77 and 29.)
 #include "common.h"
 #include "gemv_nf4.h"
@@ -203,14 +203,34 @@ constexpr int kPW = 8;               // waves
 constexpr int kSlot = 2 * 2048;      // a wave's codes of one chunk: 16 rows x 128 bytes of each weight
 constexpr int64_t kPairGroups = 256;  // workgroups: one per CU
 
+// Where the activation operand comes from: X in place; the operand-ordered copy
+// Xp; up to four tokens, two loads whose 16-lane rows hold the four tokens' 32
+// columns each, turned within the row to the eight fragments (rows past the
+// fourth then repeat the others, and their results are not stored). The eight
+// loads of the other forms keep the address units busy for twice as long as the
+// codes' copies: 28672 x 8192 at 1 and 4 tokens 66 and 67 us with two loads, 69
+// and 71 in place, 78 and 79 from Xp, whose zero rows are read too.
+constexpr int kXPlace = 0, kXOrder = 1, kXFour = 2;
+
 // One 256-column chunk: the lane's scale fields of both weights, its
 // activation operand, and its share of L for the row group.
+template <int kX>
 struct PairStage {
   uint32_t c8[2];
   uint32_t s2[2];
   float l;
-  u32x4 xa[8];
+  u32x4 xa[kX == kXFour ? 2 : 8];
 };
+
+// Lane i of every 16-lane row receives lane (i + kBy) % 16's value.
+template <int kBy>
+__device__ __forceinline__ u32x4 row_turn(const u32x4& v) {
+  u32x4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    o[e] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[e], 0x120 + 16 - kBy, 0xF, 0xF, true);  // row_ror
+  return o;
+}
 
 // The scale fields of block blk = 4 q' + grp as loaded, and at their use. kWhole
 // (K % 256 == 0, so that a row's blocks come in whole fours): as the 32-bit word
@@ -239,9 +259,8 @@ __device__ __forceinline__ float pair_scale(uint32_t c8, uint32_t s2, int grp, f
   return decode_block_scale(c8, __builtin_bit_cast(float, s2), mean);
 }
 
-// kXp: activations from the operand-ordered copy Xp (else in place from X);
-// kForm: the block-scale form (scale_fields_of). G and U may be NULL; L NULL: no adapters.
-template <bool kXp, bool kF16, int kForm, bool kWhole>
+// kX: see above; kForm: the block-scale form (scale_fields_of). G and U may be NULL; L NULL: no adapters.
+template <int kX, bool kF16, int kForm, bool kWhole>
 __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, PairWeight wu, int64_t N, int64_t K,
                                                              const uint16_t* __restrict__ X,
                                                              const u32x4* __restrict__ Xp, int64_t M,
@@ -295,8 +314,10 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
   const uint32_t rd0 = (uint32_t)(col * 128 + 16 * ((2 * grp) ^ code_swz(col)));
   const uint32_t off[2] = {(uint32_t)(same ? lane & 31 : lane & 15) * 8,
                            (uint32_t)(same ? lane & 31 : 16 + (lane & 15)) * 8};
-  const i32x4 xrs = kXp ? make_rsrc(Xp, (int64_t)nq * 512 * 16) : make_rsrc(X, M * K * 2);
-  const uint32_t xvoff = kXp ? (uint32_t)lane * 16 : (uint32_t)(col * K * 2 + 128 * grp);
+  const i32x4 xrs = kX == kXOrder ? make_rsrc(Xp, (int64_t)nq * 512 * 16) : make_rsrc(X, M * K * 2);
+  const uint32_t xvoff = kX == kXOrder  ? (uint32_t)lane * 16
+                         : kX == kXFour ? (uint32_t)((col & 3) * K * 2 + 128 * grp + 16 * (col >> 2))
+                                        : (uint32_t)(col * K * 2 + 128 * grp);
   const int64_t nblk = N * kblocks;
   const int64_t s2_bytes = kForm == 0 ? cdiv(nblk, (int64_t)kDqBlock) * 4 : nblk * (kForm == 1 ? 4 : 2);
   const i32x4 c8rs[2] = {make_rsrc(wg.code8, kForm == 0 ? nblk : 0), make_rsrc(wu.code8, kForm == 0 ? nblk : 0)};
@@ -309,7 +330,7 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
   // the next chunk to be copied, and (below) the next to be worked on
   int ic = 0, left = items;
   uint32_t in0 = blockIdx.x * 16;
-  auto issue = [&](char* R, PairStage& st) {
+  auto issue = [&](char* R, PairStage<kX>& st) {
     const int q = wave + kPW * ic < nq ? wave + kPW * ic : nq - 1;  // (past the end: not worked on)
     char* const dst = R + wave * kSlot;
     const uint32_t row0 = in0 * (uint32_t)(K / 2);
@@ -324,13 +345,14 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
     for (int i = 0; i < 2; ++i) pair_scale_load<kForm, kWhole>(c8rs[i], s2rs[i], blk, st.c8[i], st.s2[i]);
     st.l = __builtin_bit_cast(
         float, raw_buffer_load_u32(lrs, (int)(lm < M && in0 + col < N ? lvoff + in0 * 4 : 0x80000000u), 0, 0));
-    if constexpr (kXp) {
+    if constexpr (kX == kXOrder) {
 #pragma unroll
       for (int s = 0; s < 8; ++s) st.xa[s] = raw_buffer_load_b128(xrs, (int)xvoff, q * 8192 + s * 1024, 0);
     } else {
       const uint32_t v = kWhole || kc < K ? xvoff : 0x80000000u;
 #pragma unroll
-      for (int s = 0; s < 8; ++s) st.xa[s] = raw_buffer_load_b128(xrs, (int)(v + 16 * s), q * 512, 0);
+      for (int s = 0; s < (kX == kXFour ? 2 : 8); ++s)
+        st.xa[s] = raw_buffer_load_b128(xrs, (int)(v + (kX == kXFour ? 64 : 16) * s), q * 512, 0);
     }
     if (--left > 0 && ++ic == per) {  // (past the last: that one again)
       ic = 0;
@@ -343,7 +365,7 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
   // group g + 1 are issued before the products of group g.
   constexpr int kGw = 2;
   constexpr int kGroups = 16 / kGw;
-  auto compute = [&](const char* R, const PairStage& st) {
+  auto compute = [&](const char* R, const PairStage<kX>& st) {
     const char* const src = R + wave * kSlot;
     uint32_t cw[2][8];
     float cp[2];
@@ -357,6 +379,15 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
         cw[i][4 + e] = c1[e];
       }
       cp[i] = pair_scale<kForm, kWhole>(st.c8[i], st.s2[i], grp, mean[i]);
+    }
+    u32x4 xa[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      if constexpr (kX == kXFour)
+        xa[s] = (s & 3) == 0 ? st.xa[s >> 2] : (s & 3) == 1 ? row_turn<4>(st.xa[s >> 2]) : (s & 3) == 2 ? row_turn<8>(st.xa[s >> 2])
+                                                                                 : row_turn<12>(st.xa[s >> 2]);
+      else
+        xa[s] = st.xa[s];
     }
     float2 lv[2][4 * kGw];
     auto gather = [&](int g, float2 (&out)[4 * kGw]) {
@@ -390,7 +421,7 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
           const float2 l = lv[g & 1][4 * w + p];
           bw[p] = pack2<kF16>(nf4_scaled(l.x, cp[i]), nf4_scaled(l.y, cp[i]));
         }
-        acc[i] = mfma16<kF16>(__builtin_bit_cast(bf16x8, st.xa[s0 + w]), __builtin_bit_cast(bf16x8, bw), acc[i]);
+        acc[i] = mfma16<kF16>(__builtin_bit_cast(bf16x8, xa[s0 + w]), __builtin_bit_cast(bf16x8, bw), acc[i]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -407,7 +438,7 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
   // there), are added in wave order.
   int cc = 0;
   int64_t n0 = (int64_t)blockIdx.x * 16;
-  auto step = [&](char* R, const PairStage& st) {
+  auto step = [&](char* R, const PairStage<kX>& st) {
     if (wave + kPW * cc < nq) compute(R, st);
     if (++cc < per) return;
     cc = 0;
@@ -442,7 +473,7 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
   };
 
   __syncthreads();  // the table (and the levels read before the copies reuse the first ring)
-  PairStage st0, st1, st2;
+  PairStage<kX> st0, st1, st2;
   issue(ring0, st0);
   issue(ring1, st1);
   // whole groups of three chunks, with no exit inside a group (a path on which
@@ -495,7 +526,7 @@ hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* 
   const PairPlan pl = pair_plan(g.k);
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + gemv_ws_bytes(g.k));
   float* const L = r > 0 ? part + align256((size_t)pl.parts * 2 * M * r * 4) / 4 : nullptr;
-  const bool xp = gemv_orders_x(M, g.n);
+  const bool xp = M > 4 && gemv_orders_x(M, g.n);
   if (xp || r > 0) {
 #define QLORA_GPREP2(RP, H16) \
   gemv_prep_kernel<RP, H16><<<(unsigned)pl.parts, 256, 0, stream>>>(X, M, g.k, pl.nb, Ag, Au, r, pl.chunk, xp ? Xp : nullptr, part)
@@ -530,7 +561,9 @@ hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* 
     else QLORA_GVP3(XP, H16, 2)              \
   }
 #define QLORA_GVP(XP) { if (f16) QLORA_GVP2(XP, true) else QLORA_GVP2(XP, false) }
-  if (xp) QLORA_GVP(true) else QLORA_GVP(false)
+  if (M <= 4) QLORA_GVP(kXFour)
+  else if (xp) QLORA_GVP(kXOrder)
+  else QLORA_GVP(kXPlace)
 #undef QLORA_GVP
 #undef QLORA_GVP2
 #undef QLORA_GVP3
