@@ -14,8 +14,8 @@
 // groups in turn, the table is built once and the ring runs on from one group
 // into the next, whose first chunks are in flight while the last group's sums
 // are joined. Bound by the expansion (about 3 vector operations per weight and
-// one LDS read per two) as much as by HBM. (28672 x 8192, one token: 66 us,
-// 3.7 TB/s of codes and scales; 11008 x 4096, 16 fp16 tokens: 22. A workgroup
+// one LDS read per two) as much as by HBM. (28672 x 8192, one token: 63 us,
+// 3.9 TB/s of codes and scales; 11008 x 4096, 16 fp16 tokens: 22. A workgroup
 // of four waves for each row group, two on a CU: 77 and 29.)
 #include "common.h"
 #include "gemv_nf4.h"
@@ -201,6 +201,7 @@ struct PairWeight {
 
 constexpr int kPW = 8;               // waves
 constexpr int kSlot = 2 * 2048;      // a wave's codes of one chunk: 16 rows x 128 bytes of each weight
+static_assert(kSlot >= 2 * 2 * 256 * 4, "the sums of two row groups fit a slot");
 constexpr int64_t kPairGroups = 256;  // workgroups: one per CU
 
 // Where the activation operand comes from: X in place; the operand-ordered copy
@@ -222,13 +223,15 @@ struct PairStage {
   u32x4 xa[kX == kXFour ? 2 : 8];
 };
 
-// Lane i of every 16-lane row receives lane (i + kBy) % 16's value.
-template <int kBy>
-__device__ __forceinline__ u32x4 row_turn(const u32x4& v) {
-  u32x4 o;
+// Lane i of every 16-lane row receives lane (i + 4 by) % 16's value.
+__device__ __forceinline__ u32x4 row_turn(const u32x4& v, int by) {
+  u32x4 o = v;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    o[e] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[e], 0x120 + 16 - kBy, 0xF, 0xF, true);  // row_ror
+    o[e] = by == 0   ? v[e]
+           : by == 1 ? (uint32_t)__builtin_amdgcn_mov_dpp((int)v[e], 0x12C, 0xF, 0xF, true)   // row_ror:12
+           : by == 2 ? (uint32_t)__builtin_amdgcn_mov_dpp((int)v[e], 0x128, 0xF, 0xF, true)   // row_ror:8
+                     : (uint32_t)__builtin_amdgcn_mov_dpp((int)v[e], 0x124, 0xF, 0xF, true);  // row_ror:4
   return o;
 }
 
@@ -361,10 +364,9 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
   };
 
   f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-  // One chunk, in groups of kGw code words per lane: the table reads of
-  // group g + 1 are issued before the products of group g.
-  constexpr int kGw = 2;
-  constexpr int kGroups = 16 / kGw;
+  // One chunk, one code word of each weight at a time: the table reads of word
+  // s + 1 are issued before the products of word s, and the two products of a
+  // word add to different sums.
   auto compute = [&](const char* R, const PairStage<kX>& st) {
     const char* const src = R + wave * kSlot;
     uint32_t cw[2][8];
@@ -380,48 +382,42 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
       }
       cp[i] = pair_scale<kForm, kWhole>(st.c8[i], st.s2[i], grp, mean[i]);
     }
-    u32x4 xa[8];
+    float2 lv[2][8];
+    auto gather = [&](int s, float2 (&out)[8]) {
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      if constexpr (kX == kXFour)
-        xa[s] = (s & 3) == 0 ? st.xa[s >> 2] : (s & 3) == 1 ? row_turn<4>(st.xa[s >> 2]) : (s & 3) == 2 ? row_turn<8>(st.xa[s >> 2])
-                                                                                 : row_turn<12>(st.xa[s >> 2]);
-      else
-        xa[s] = st.xa[s];
-    }
-    float2 lv[2][4 * kGw];
-    auto gather = [&](int g, float2 (&out)[4 * kGw]) {
-      const int i = g / (8 / kGw), s0 = (g % (8 / kGw)) * kGw;
-#pragma unroll
-      for (int w = 0; w < kGw; ++w)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int p = 0; p < 4; ++p)
-          out[4 * w + p] = *reinterpret_cast<const float2*>(
-              lut + __builtin_amdgcn_perm(cw[i][s0 + w], off[i], 0x0C0C0400u + ((uint32_t)p << 8)));
+          out[4 * i + p] = *reinterpret_cast<const float2*>(
+              lut + __builtin_amdgcn_perm(cw[i][s], off[i], 0x0C0C0400u + ((uint32_t)p << 8)));
     };
     gather(0, lv[0]);
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      // (one wait for all of group g's reads)
-      if (g + 1 < kGroups) {
-        gather(g + 1, lv[(g + 1) & 1]);
+    for (int s = 0; s < 8; ++s) {
+      // (one wait for all of word s's reads)
+      if (s + 1 < 8) {
+        gather(s + 1, lv[(s + 1) & 1]);
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(lgkm_wait(4 * kGw));
+        __builtin_amdgcn_s_waitcnt(lgkm_wait(8));
       } else {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(lgkm_wait(0));
       }
       __builtin_amdgcn_sched_barrier(0);
-      const int i = g / (8 / kGw), s0 = (g % (8 / kGw)) * kGw;
+      u32x4 xa;
+      if constexpr (kX == kXFour)
+        xa = row_turn(st.xa[s >> 2], s & 3);
+      else
+        xa = st.xa[s];
 #pragma unroll
-      for (int w = 0; w < kGw; ++w) {
+      for (int i = 0; i < 2; ++i) {
         u32x4 bw;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const float2 l = lv[g & 1][4 * w + p];
+          const float2 l = lv[s & 1][4 * i + p];
           bw[p] = pack2<kF16>(nf4_scaled(l.x, cp[i]), nf4_scaled(l.y, cp[i]));
         }
-        acc[i] = mfma16<kF16>(__builtin_bit_cast(bf16x8, xa[s0 + w]), __builtin_bit_cast(bf16x8, bw), acc[i]);
+        acc[i] = mfma16<kF16>(__builtin_bit_cast(bf16x8, xa), __builtin_bit_cast(bf16x8, bw), acc[i]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -433,11 +429,16 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  // One chunk, and after a row group's last the join: the waves' sums, each in
-  // its own slot of the ring array just read (free until the next copies go
-  // there), are added in wave order.
-  int cc = 0;
+  // One chunk, and after the last of every second row group (and of the very
+  // last) the join of both: the waves' sums, each in its own slot of the ring
+  // array just read (free until the next copies go there), are added in wave
+  // order, 256 threads per row group. (28672 x 8192, one token: 63 us; a join
+  // for every row group 66.)
+  int cc = 0, groups = items / per;
+  bool held = false;
+  f32x4 hold[2] = {acc[0], acc[1]};
   int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t nstep = 16 * (int64_t)gridDim.x;
   auto step = [&](char* R, const PairStage<kX>& st) {
     if (wave + kPW * cc < nq) compute(R, st);
     if (++cc < per) return;
@@ -446,30 +447,41 @@ __global__ __launch_bounds__(64 * kPW) void gemv_pair_kernel(PairWeight wg, Pair
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[i][v] += wave == 2 * v + i ? st.l : 0.0f;
-    float(*mine)[16][16] = reinterpret_cast<float(*)[16][16]>(R + wave * kSlot);
+    if (--groups > 0 && !held) {
+      held = true;
+      hold[0] = acc[0];
+      hold[1] = acc[1];
+    } else {
+      float(*mine)[2][16][16] = reinterpret_cast<float(*)[2][16][16]>(R + wave * kSlot);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) mine[i][4 * grp + v][col] = acc[i][v];
-    meet();
-    const int m = t >> 4, nc = t & 15;
-    if (m < M && n0 + nc < N) {
-      float y[2];
+        for (int v = 0; v < 4; ++v) {
+          mine[0][i][4 * grp + v][col] = acc[i][v];
+          mine[1][i][4 * grp + v][col] = hold[i][v];
+        }
+      meet();
+      const int m = (t >> 4) & 15, nc = t & 15;
+      const int64_t n = n0 + nc - (t >> 8) * nstep;  // the second half of the threads: the group before
+      if (m < M && n < N && (held || t < 256)) {
+        float y[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float* const s = reinterpret_cast<const float*>(R) + (i * 16 + m) * 16 + nc;
-        y[i] = s[0];
+        for (int i = 0; i < 2; ++i) {
+          const float* const s = reinterpret_cast<const float*>(R) + (((t >> 8) * 2 + i) * 16 + m) * 16 + nc;
+          y[i] = s[0];
 #pragma unroll
-        for (int w = 1; w < kPW; ++w) y[i] += s[w * (kSlot / 4)];
+          for (int w = 1; w < kPW; ++w) y[i] += s[w * (kSlot / 4)];
+        }
+        const int64_t o = m * N + n;
+        H[o] = to16<kF16>(silu(y[0]) * y[1]);
+        if (G) G[o] = to16<kF16>(y[0]);
+        if (U) U[o] = to16<kF16>(y[1]);
       }
-      const int64_t o = m * N + n0 + nc;
-      H[o] = to16<kF16>(silu(y[0]) * y[1]);
-      if (G) G[o] = to16<kF16>(y[0]);
-      if (U) U[o] = to16<kF16>(y[1]);
+      meet();
+      held = false;
     }
-    meet();
     acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    n0 += 16 * (int64_t)gridDim.x;
+    n0 += nstep;
   };
 
   __syncthreads();  // the table (and the levels read before the copies reuse the first ring)
