@@ -664,6 +664,13 @@ def fp8_linear_workspace_bytes(M: int, n: int, k: int, r: int, is_bwd: bool) -> 
     return int(_lib.qlora_fp8_linear_workspace_bytes(M, n, k, r, int(bool(is_bwd))))
 
 
+def _adapter8(w: FP8Weight, A: torch.Tensor, B: torch.Tensor | None, r: int, dt, dev) -> None:
+    if B is None:
+        raise ValueError("B: missing")
+    _given(A, dt, (r, w.k), "A", dev)
+    _given(B, dt, (w.n, r), "B", dev)
+
+
 def fp8_linear_fwd(w: FP8Weight, X: torch.Tensor, A: torch.Tensor | None, B: torch.Tensor | None, scale: float,
                    Y: torch.Tensor | None = None, T: torch.Tensor | None = None, save_T: bool = True,
                    ws: torch.Tensor | None = None, stream=None):
@@ -675,8 +682,7 @@ def fp8_linear_fwd(w: FP8Weight, X: torch.Tensor, A: torch.Tensor | None, B: tor
     _is_f16(dt)
     _given(X, dt, (M, w.k), "X", dev)
     if r:
-        _given(A, dt, (r, w.k), "A", dev)
-        _need(B, dt, (w.n, r), "B")
+        _adapter8(w, A, B, r, dt, dev)
     with _on(stream, dev):
         Y = _out(Y, True, dt, (M, w.n), "Y", dev)
         T = _out(T, save_T and r > 0, torch.float32, (M, r), "T", dev)
@@ -702,8 +708,7 @@ def fp8_linear_bwd(w: FP8Weight, X: torch.Tensor | None, T: torch.Tensor | None,
     _given(dY, dt, (M, w.n), "dY", dev)
     _given(X, dt, (M, w.k), "X", dev)
     if r:
-        _given(A, dt, (r, w.k), "A", dev)
-        _need(B, dt, (w.n, r), "B")
+        _adapter8(w, A, B, r, dt, dev)
         _given(T, torch.float32, (M, r), "T", dev)
     with _on(stream, dev):
         dX = _out(dX, need_dX, dt, (M, w.k), "dX", dev)

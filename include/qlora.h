@@ -424,8 +424,9 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight *w, const void *X, int6
  * forward: rounding X to X8 is passed through. T_saved, accumulate, M = 0 and
  * r = 0 as in qlora_linear_bwd. Reruns are bit-identical.
  * ws (device) holds qlora_fp8_linear_workspace_bytes(M, n, k, r, 1) bytes.
- * Errors: as the forward (operands of dX: M np, k np with np = n rounded up
- * to a multiple of 128).
+ * dX reads the codes as they are stored. Errors: as the forward (operands of
+ * dX: M np, and np kp with a tile's 256 bytes more, np = n rounded up to a
+ * multiple of 128).
  */
 qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight *w, const void *X, const float *T_saved, const void *dY,
                                   int64_t M, int dtype, const void *A, const void *B, int r, float scale, void *dX,

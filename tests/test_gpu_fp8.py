@@ -195,3 +195,22 @@ def test_bytes_around_the_weight_are_not_read_as_codes(q, n, k, r):
         assert torch.isfinite(a[0]).all() and torch.equal(a[0], b[0])
         a, b = (q.fp8_linear_bwd(v, X, None, dY, A, B, 0.5) for v in (w, inner))
         assert torch.isfinite(a[0]).all() and torch.equal(a[0], b[0])
+
+
+def test_binding_refuses_what_the_call_does_not_take(q):
+    m, n, k, r = 20, 64, 128, 4
+    w = q.quantize_fp8(_normal((n, k), 0.02, BF, 39, 0).cuda())
+    X, dY = _normal((m, k), 1.0, BF, 39, 1).cuda(), _normal((m, n), 1.0, BF, 39, 2).cuda()
+    A, B = _normal((r, k), 0.05, BF, 39, 3).cuda(), _normal((n, r), 0.05, BF, 39, 4).cuda()
+    for a, b in ((A, None), (A, B.cpu()), (A, B.half()), (A, B.t()), (A[:, :64], B), (A.t(), B)):
+        with pytest.raises(ValueError):
+            q.fp8_linear_fwd(w, X, a, b, 0.5)
+        with pytest.raises(ValueError):
+            q.fp8_linear_bwd(w, X, None, dY, a, b, 0.5)
+    for x, y in ((X.half(), dY), (X[:, :64], dY), (X, dY[:, :32]), (X[:3], dY)):
+        with pytest.raises(ValueError):
+            q.fp8_linear_bwd(w, x, None, y, A, B, 0.5)
+    with pytest.raises(ValueError):
+        q.fp8_linear_bwd(w, X, torch.zeros(m, r + 1, device="cuda"), dY, A, B, 0.5)
+    with pytest.raises(ValueError):
+        q.fp8_linear_fwd(w, X, A, B, 0.5, Y=torch.empty(m, n, device="cuda"))

@@ -124,6 +124,10 @@ def test_host_checks_of_the_abi():
     # operands of 4 GiB are refused (M kp here)
     long = ctypes.byref(q._Weight8(64, 1 << 20, 1 << 20, 1 << 21))
     assert lib.qlora_fp8_linear_fwd(long, p, 4096, 0, p, p, 8, 1.0, p, None, p, 1 << 62, None) == -2
+    # and the codes for dX, up to the end of the last tile (np kp + 256 bytes)
+    for n in (65536, 65535, 65409):
+        wide = ctypes.byref(q._Weight8(n, 65536, 1 << 20, 1 << 21))
+        assert lib.qlora_fp8_linear_bwd(wide, None, None, p, 40, 0, p, p, 8, 1.0, p, None, None, 0, p, 1 << 62, None) == -2
     for a in ((0, 100, 192, 8, 0), (4, 100, 100, 8, 0), (4, 100, 192, 129, 0), (4, 100, 192, 8, 2)):
         assert lib.qlora_fp8_linear_workspace_bytes(*a) == 0
     # the binding: CPU tensors, wrong types and shapes
