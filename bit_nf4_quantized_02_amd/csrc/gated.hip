@@ -34,7 +34,6 @@ struct PairView {
   const uint16_t* lr;  // B (forward) or A (dX)
 };
 
-constexpr int kMaxRank = 128;
 constexpr int kRows = 8;  // weight rows per workgroup, as the plain row expansion
 
 // One 16-byte output chunk column of 8 rows per thread; blockIdx.z picks the
