@@ -138,13 +138,13 @@ def _check(status: int, where: str) -> None:
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # (every call's argument types are declared)
 
 
 def _stream(stream=None):
     if stream is None:  # the current stream of the current device (without building its Stream object: 3 us)
-        return _vp(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return _vp(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _need(t: torch.Tensor, dtype, shape, name):
@@ -495,6 +495,9 @@ def lora_linear_bwd(W: torch.Tensor, X: torch.Tensor | None, T: torch.Tensor | N
 _DT = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32, torch.float16: DT_FP16}
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(stream, device):
     """Context of a call: the tensors' device is current, and what the call
     allocates belongs to the stream that it runs on."""
@@ -502,8 +505,8 @@ def _on(stream, device):
         if stream.device != device:
             raise ValueError(f"stream of {stream.device} for tensors on {device}")
         return torch.cuda.stream(stream)
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if device.index == torch._C._cuda_getDevice():  # (a tensor of the device exists: CUDA is initialised)
+        return _NOTHING
     return torch.cuda.device(device)
 
 
@@ -627,6 +630,9 @@ class FP8Weight:
         kb = -(-self.k // FP8_BLOCK)
         _need(self.codes, torch.uint8, (self.n, kb * FP8_BLOCK), "codes")
         _given(self.scale, torch.uint8, (-(-self.n // FP8_BLOCK), kb), "scale", self.codes.device)
+        return self._struct()
+
+    def _struct(self) -> _Weight8:
         return _Weight8(self.n, self.k, self.codes.data_ptr(), self.scale.data_ptr())
 
     def nbytes(self) -> int:
@@ -643,9 +649,11 @@ def quantize_fp8(W: torch.Tensor, out: FP8Weight | None = None, stream=None) -> 
     with _on(stream, W.device):
         if out is None:
             out = FP8Weight.empty(n, k, device=W.device)
+            st = out._struct()
         elif (out.n, out.k) != (n, k):
             raise ValueError(f"out: [{out.n}, {out.k}], expected [{n}, {k}]")
-        st = out.struct()
+        else:
+            st = out.struct()
         _check(_lib.qlora_quantize_fp8(_ptr(W), _DT[W.dtype], ctypes.byref(st), _stream(stream)), "qlora_quantize_fp8")
     return out
 
