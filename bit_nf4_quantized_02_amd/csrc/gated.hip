@@ -1,5 +1,5 @@
 // Kernels of the gated feed-forward block around its two GEMMs (gemm_bf16.hip)
-// and its few-token form (gemv_nf4.hip):
+// and its few-token form (gemv_pair.hip):
 //
 //   G = X Wg'^T + s (X Ag^T) Bg^T,  U = X Wu'^T + s (X Au^T) Bu^T,  H = silu(G) U
 //   dG = dH U sg (1 + G (1 - sg)),  dU = dH G sg,  sg = sigma(G)
@@ -144,7 +144,7 @@ constexpr int kJoinRows = 16 * kJoinWaves;
 // waves share, are copied into LDS one step ahead. (Loaded straight in operand
 // layout neighbouring lanes lie in different rows, 55 cache accesses per load:
 // 340 us at 4096 x 22016, r = 64; in half lines, with the factors read by each
-// wave: 276.) kRP: ranks padded (0: no adapters, D only).
+// wave: 276; so 208, 4.4 TB/s of the values read and written.) kRP: ranks padded (0: no adapters, D only).
 template <int kRP, bool kF16, bool kVec>
 __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
     const uint16_t* __restrict__ G, const uint16_t* __restrict__ U, const uint16_t* __restrict__ dH, int64_t M, int64_t n,
@@ -328,7 +328,10 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
 // the transposing read, the A operand (8 tokens of one rank) from Tt in runs.
 // The four waves split the ranks first and then the columns, so that no rank
 // row is loaded twice where there are at least 64. Products of parts whose
-// order is below the last bit kept are left out (mid * lo and lo * lo).
+// order is below the last bit kept are left out (mid * lo and lo * lo). Bound by
+// issue: forming and splitting dG and dU takes 54% of the cycles on the vector
+// units, the products 35% on the matrix cores (4096 x 22016, r = 64: 215 us,
+// where reading G, U and dH alone takes 108).
 template <int kRP, bool kF16, bool kVec>
 __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restrict__ G, const uint16_t* __restrict__ U,
                                                        const uint16_t* __restrict__ dH, int64_t M, int64_t n,
