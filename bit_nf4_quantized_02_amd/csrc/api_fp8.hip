@@ -237,7 +237,7 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
     T = o.T;
   }
   GradJob ja{}, jb{};
-  if (e == hipSuccess) e = launch_rank_parts(o.U, dA ? 1 : 0, o.Up, T, dB ? 1 : 0, o.Tp, M, r, st, f16);
+  if (e == hipSuccess) e = launch_rank_parts(o.U, dA ? 1 : 0, o.Up, T, dB ? 1 : 0, o.Tp, M, r, st);
   if (e == hipSuccess && dA)
     e = launch_colgrad(x, M, k, o.Up, 1, r, scale, dA, nullptr, true, accumulate, o.da, ja, st, f16);
   if (e == hipSuccess && dB)

@@ -198,7 +198,7 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
     T = o.T;
   }
   GradJob ja{}, jb{};
-  if (e == hipSuccess) e = launch_rank_parts(o.P, need_a ? 2 : 0, o.Pp, T, need_b ? 2 : 0, o.Tp, M, r, st, f16);
+  if (e == hipSuccess) e = launch_rank_parts(o.P, need_a ? 2 : 0, o.Pp, T, need_b ? 2 : 0, o.Tp, M, r, st);
   if (e == hipSuccess && need_a)
     e = launch_colgrad(x, M, k, o.Pp, 2, r, scale, dA_gate, dA_up, true, accumulate, o.da, ja, st, f16);
   if (e == hipSuccess && need_b)

@@ -1,37 +1,57 @@
-// Pieces of the gradient kernels that contract over the tokens (gated.hip's
-// dB, colgrad.hip): fp32 values in 16-bit parts, and the staged tile whose
-// columns come back as MFMA operands.
+// Pieces of the gradient kernels (gated.hip's join and dB, colgrad.hip): fp32
+// values in 16-bit parts, and the staged tile whose columns come back as MFMA
+// operands.
 #pragma once
 
 #include "common.h"
 
 namespace qlora {
 
-// Eight fp32 values -> kParts 16-bit parts whose sum holds 24 (bf16, three)
-// or 22 (fp16, two) bits of each.
-template <bool kF16>
-constexpr int parts_of() { return kF16 ? 2 : 3; }
+// Eight fp32 values -> kN bf16 parts whose sum holds 8 kN bits of each. bf16
+// for both compute types: its exponents are fp32's, so three parts hold all 24
+// bits of a gradient of any size, where the second of two fp16 parts is below
+// fp16's smallest step for values under 2^-3 (2e-3 of the sum lost at 1e-5) and
+// the first infinite above 65504. Two parts hold an fp16 value exactly (11 bits).
+constexpr int kParts = 3;
 
-template <bool kF16>
-__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&p)[parts_of<kF16>()]) {
+template <int kN>
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&p)[kN]) {
   float rem[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     rem[e] = x[e];
     // one fp32 value from here on: folded into the operation that made x, the
-    // fp16 conversion stored and the one subtracted were rounded from
-    // different values and a step apart for one element in 10^5
+    // conversion stored and the one subtracted could be rounded from different values
     asm("" : "+v"(rem[e]));
   }
 #pragma unroll
-  for (int q = 0; q < parts_of<kF16>(); ++q)
+  for (int q = 0; q < kN; ++q)
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      p[q][w] = pack2<kF16>(rem[2 * w], rem[2 * w + 1]);
+      p[q][w] = pack2<false>(rem[2 * w], rem[2 * w + 1]);
       asm("" : "+v"(p[q][w]));  // (unpacked from here, not converted a second time)
-      rem[2 * w] -= from16<kF16>(p[q][w] & 0xFFFFu);
-      rem[2 * w + 1] -= from16<kF16>(p[q][w] >> 16);
+      rem[2 * w] -= from16<false>(p[q][w] & 0xFFFFu);
+      rem[2 * w + 1] -= from16<false>(p[q][w] >> 16);
     }
+}
+
+// Eight 16-bit values -> bf16 parts: themselves, or an fp16 value's two.
+template <bool kF16>
+constexpr int parts16() { return kF16 ? 2 : 1; }
+
+template <bool kF16>
+__device__ __forceinline__ void split8h(const u32x4& v, u32x4 (&p)[parts16<kF16>()]) {
+  if constexpr (kF16) {
+    float x[8];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      x[2 * w] = from16<true>(v[w] & 0xFFFFu);
+      x[2 * w + 1] = from16<true>(v[w] >> 16);
+    }
+    split8(x, p);
+  } else {
+    p[0] = v;
+  }
 }
 
 // Columns of a workgroup, and bytes of a staged tile [32 tokens][64 columns].

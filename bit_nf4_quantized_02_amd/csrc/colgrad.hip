@@ -3,9 +3,9 @@
 //   Gw[c, j] (+)= scale * sum_m P[m, c] Qw[m, j],   w = 0 (and 1, sharing P)
 //
 // P 16 bits [M, C], Qw fp32 [M, r]: dA = s P^T X from the fp32 projections, dB
-// = s dY^T T. Q takes part with all its 24 bits (three bf16 parts; two fp16
-// parts, 22): one small kernel writes the parts in operand order, and the
-// products then read them in runs. Bound by HBM: P is read once for both Q.
+// = s dY^T T. Q takes part with all its 24 bits, as three bf16 parts (an fp16 P
+// as its two, exact): one small kernel writes Q's parts in operand order, and
+// the products then read them in runs. Bound by HBM: P is read once for both Q.
 // Against the layer calls' coldot kernel (lora.hip), which converts Q again in
 // every workgroup and meets at two barriers per 32 tokens, a step here has one.
 #include <type_traits>
@@ -23,7 +23,6 @@ constexpr int kMaxRank = 128;
 // operand of the products over the tokens: lane l holds rank 16 t + l % 16, tokens 8 (l / 16)
 // .. +7 of the step, zero past M and r. Two such operands (of W0 and of the
 // rest of gridDim.y) in one launch.
-template <bool kF16>
 __global__ __launch_bounds__(256) void rank_parts_kernel(const float* __restrict__ Q0, int W0,
                                                          const float* __restrict__ Q1, int64_t M, int r, int tiles,
                                                          u32x4* __restrict__ out0, u32x4* __restrict__ out1) {
@@ -61,11 +60,10 @@ __global__ __launch_bounds__(256) void rank_parts_kernel(const float* __restrict
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = j < r ? tile[8 * ((i >> 4) & 3) + e][j] : 0.0f;
-    u32x4 p[parts_of<kF16>()];
-    split8<kF16>(x, p);
+    u32x4 p[kParts];
+    split8(x, p);
 #pragma unroll
-    for (int q = 0; q < parts_of<kF16>(); ++q)
-      out[(((int64_t)blockIdx.x * parts_of<kF16>() + q) * W + w) * tiles * 64 + i] = p[q];
+    for (int q = 0; q < kParts; ++q) out[(((int64_t)blockIdx.x * kParts + q) * W + w) * tiles * 64 + i] = p[q];
   }
 }
 
@@ -83,13 +81,13 @@ __global__ __launch_bounds__(256) void colgrad_kernel(const uint16_t* __restrict
                                                       const u32x4* __restrict__ Qp, int r, int64_t mchunk,
                                                       float* __restrict__ part, bool direct, float scale,
                                                       float* __restrict__ G0, float* __restrict__ G1, int accumulate) {
-  constexpr int kP = parts_of<kF16>();
+  constexpr int kP = kParts, kX = parts16<kF16>();
   constexpr int kJTall = kRP / 16;
   constexpr int kWJ = kJTall >= 4 ? 4 : kJTall;  // waves along ranks
   constexpr int kWC = 4 / kWJ;                   // waves along columns
   constexpr int kJT = kJTall / kWJ;              // rank tiles per wave
   constexpr int kCT = kDbCols / 16 / kWC;        // column tiles per wave
-  __shared__ __attribute__((aligned(16))) char sm[2 * 2 * kDbTile];  // [set][32-token half]
+  __shared__ __attribute__((aligned(16))) char sm[2 * 2 * kX * kDbTile];  // [set][32-token half][part of P]
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wj = wave % kWJ, wc = wave / kWJ;
@@ -118,7 +116,11 @@ __global__ __launch_bounds__(256) void colgrad_kernel(const uint16_t* __restrict
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (mb + 64 > m1 && mb + 32 * h + prow >= m1) s.p[h] = u32x4{0u, 0u, 0u, 0u};
-      *reinterpret_cast<u32x4*>(sm + (set * 2 + h) * kDbTile + db_seg(prow, (t & 7) >> 1) + (t & 1) * 16) = s.p[h];
+      u32x4 x[kX];
+      split8h<kF16>(s.p[h], x);
+#pragma unroll
+      for (int e = 0; e < kX; ++e)
+        *reinterpret_cast<u32x4*>(sm + ((set * 2 + h) * kX + e) * kDbTile + db_seg(prow, (t & 7) >> 1) + (t & 1) * 16) = x[e];
     }
   };
   f32x4 acc[kW][kJT][kCT];
@@ -157,14 +159,19 @@ __global__ __launch_bounds__(256) void colgrad_kernel(const uint16_t* __restrict
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int b = 0; b < kCT; ++b) {
-        const bf16x8 pb = db_operand(sm + (set * 2 + h) * kDbTile, wc * kCT + b, lane);
+        bf16x8 pb[kX];
+#pragma unroll
+        for (int e = 0; e < kX; ++e) pb[e] = db_operand(sm + ((set * 2 + h) * kX + e) * kDbTile, wc * kCT + b, lane);
+        // (the smallest products first; the third part of Q times the second of P is below the last bit kept)
 #pragma unroll
         for (int p = kP - 1; p >= 0; --p)
 #pragma unroll
-          for (int w = 0; w < kW; ++w)
+          for (int e = kX - 1; e >= 0; --e)
 #pragma unroll
-            for (int a = 0; a < kJT; ++a)
-              acc[w][a][b] = mfma16<kF16>(__builtin_bit_cast(bf16x8, q[h][p][w][a]), pb, acc[w][a][b]);
+            for (int w = 0; w < (p + e < kP ? kW : 0); ++w)
+#pragma unroll
+              for (int a = 0; a < kJT; ++a)
+                acc[w][a][b] = mfma16<false>(__builtin_bit_cast(bf16x8, q[h][p][w][a]), pb[e], acc[w][a][b]);
       }
     __syncthreads();
   }
@@ -233,17 +240,14 @@ GradPlan grad_plan(int64_t M, int64_t C) {
 
 }  // namespace
 
-size_t rank_parts_bytes(int64_t M, int r, int W) { return (size_t)cdiv(M, (int64_t)32) * 3 * W * rank_pad(r) * 64; }
+size_t rank_parts_bytes(int64_t M, int r, int W) { return (size_t)cdiv(M, (int64_t)32) * kParts * W * rank_pad(r) * 64; }
 
 hipError_t launch_rank_parts(const float* Q0, int W0, void* out0, const float* Q1, int W1, void* out1, int64_t M, int r,
-                             hipStream_t stream, bool f16) {
+                             hipStream_t stream) {
   const dim3 grid((unsigned)cdiv(M, (int64_t)32), (unsigned)(W0 + W1));
   u32x4 *const o0 = static_cast<u32x4*>(out0), *const o1 = static_cast<u32x4*>(out1);
   const int tiles = rank_pad(r) / 16;
-  if (f16)
-    rank_parts_kernel<true><<<grid, 256, 0, stream>>>(Q0, W0, Q1, M, r, tiles, o0, o1);
-  else
-    rank_parts_kernel<false><<<grid, 256, 0, stream>>>(Q0, W0, Q1, M, r, tiles, o0, o1);
+  rank_parts_kernel<<<grid, 256, 0, stream>>>(Q0, W0, Q1, M, r, tiles, o0, o1);
   return hipGetLastError();
 }
 

@@ -17,6 +17,7 @@
 //                                      G[c, np + j] = A[j mod r, c] j <  2r, else 0
 // with xc = lora_extra_cols(r) and np = n rounded up to a multiple of 64.
 // Values are bit-identical to qlora_dequant's.
+#include "colgrad.h"
 #include "common.h"
 #include "kernels.h"
 
@@ -232,8 +233,9 @@ __device__ __forceinline__ void lowrank_rows_t_part(const uint16_t* __restrict__
 // l % 16, columns c0 + 8 (l / 16) .. +7 (zero past r and C). Kernels that walk
 // the columns then read it in runs of 1 KB; read in place, a wave's 16 rank
 // rows are 16 lines for the four lanes that share one. One workgroup per 32
-// columns and factor; layout 0: Q [r, C], 1: Q [C, r].
-template <int kLayout>
+// columns and factor; layout 0: Q [r, C], 1: Q [C, r]. kSplit: an fp16 factor
+// as two bf16 parts (exact), [32 columns][part][rank tile].
+template <int kLayout, bool kSplit = false>
 __device__ __forceinline__ void operand_order_part(const uint16_t* __restrict__ Q, int64_t C, int r, int tiles, int64_t step,
                                                    u32x4* __restrict__ out) {
   __shared__ uint16_t tile[32][130];  // [column][rank]
@@ -249,16 +251,19 @@ __device__ __forceinline__ void operand_order_part(const uint16_t* __restrict__ 
     if (j < r)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = tile[c + 2 * e][j] | ((uint32_t)tile[c + 2 * e + 1][j] << 16);
-    out[step * tiles * 64 + i] = v;
+    u32x4 p[parts16<kSplit>()];
+    split8h<kSplit>(v, p);
+#pragma unroll
+    for (int q = 0; q < parts16<kSplit>(); ++q) out[(step * parts16<kSplit>() + q) * tiles * 64 + i] = p[q];
   }
 }
 
-template <int kLayout>
+template <int kLayout, bool kSplit>
 __global__ __launch_bounds__(256) void operand_order_kernel(const uint16_t* __restrict__ Q0,
                                                             const uint16_t* __restrict__ Q1, int64_t C, int r, int tiles,
                                                             u32x4* __restrict__ out) {
-  operand_order_part<kLayout>(blockIdx.y == 0 ? Q0 : Q1, C, r, tiles, blockIdx.x,
-                              out + (int64_t)blockIdx.y * gridDim.x * tiles * 64);
+  operand_order_part<kLayout, kSplit>(blockIdx.y == 0 ? Q0 : Q1, C, r, tiles, blockIdx.x,
+                                      out + (int64_t)blockIdx.y * gridDim.x * parts16<kSplit>() * tiles * 64);
 }
 
 // Both factors of an adapter in one launch: Q in operand order (workgroups
@@ -284,13 +289,16 @@ __global__ __launch_bounds__(256) void factors_kernel(const uint16_t* __restrict
 size_t operand_order_bytes(int64_t Cp, int r) { return (size_t)(Cp / 32) * (rank_pad(r) / 16) * 1024; }
 
 hipError_t launch_operand_order(const uint16_t* Q, const uint16_t* Q1, int layout, int64_t C, int64_t Cp, int r,
-                                uint16_t* out, hipStream_t stream) {
+                                uint16_t* out, hipStream_t stream, bool split16) {
+  if (split16 && layout != 1) return hipErrorInvalidValue;
   const dim3 grid((unsigned)(Cp / 32), Q1 ? 2 : 1);
   u32x4* const o = reinterpret_cast<u32x4*>(out);
   if (layout == 0)
-    operand_order_kernel<0><<<grid, 256, 0, stream>>>(Q, Q1, C, r, rank_pad(r) / 16, o);
+    operand_order_kernel<0, false><<<grid, 256, 0, stream>>>(Q, Q1, C, r, rank_pad(r) / 16, o);
+  else if (split16)
+    operand_order_kernel<1, true><<<grid, 256, 0, stream>>>(Q, Q1, C, r, rank_pad(r) / 16, o);
   else
-    operand_order_kernel<1><<<grid, 256, 0, stream>>>(Q, Q1, C, r, rank_pad(r) / 16, o);
+    operand_order_kernel<1, false><<<grid, 256, 0, stream>>>(Q, Q1, C, r, rank_pad(r) / 16, o);
   return hipGetLastError();
 }
 

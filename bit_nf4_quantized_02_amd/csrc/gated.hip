@@ -7,8 +7,8 @@
 //   dAg = s Pg^T X,  dBg = s dG^T Tg,  and the same for u
 //
 // dG and dU enter dX's GEMM in 16 bits (its output has no more). The adapter
-// gradients are fp32, so their products take the unrounded fp32 dG and dU in
-// parts: three bf16 parts hold all 24 bits, two fp16 parts 22. Neither G and U
+// gradients are fp32, so their products take the unrounded fp32 dG and dU as
+// three bf16 parts, in fp16 too (colgrad.h). Neither G and U
 // nor dG and dU are kept in fp32: the two kernels that need them compute them
 // again from the 16-bit G, U and dH, which is fewer bytes than reading parts.
 #include <type_traits>
@@ -145,18 +145,20 @@ constexpr int kJoinRows = 16 * kJoinWaves;
 // layout neighbouring lanes lie in different rows, 55 cache accesses per load:
 // 340 us at 4096 x 22016, r = 64; in half lines, with the factors read by each
 // wave: 276; so 208, 4.4 TB/s of the values read and written.) kRP: ranks padded (0: no adapters, D only).
+// An fp16 B comes as its two bf16 parts; the third part of dG times the second
+// of B is below the last bit kept.
 template <int kRP, bool kF16, bool kVec>
 __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
     const uint16_t* __restrict__ G, const uint16_t* __restrict__ U, const uint16_t* __restrict__ dH, int64_t M, int64_t n,
     int64_t np, const uint16_t* __restrict__ Bo, int r, int64_t cchunk, uint16_t* __restrict__ D,
     float* __restrict__ part) {
   constexpr int kTiles = kRP / 16, kTA = kTiles > 0 ? kTiles : 1;
-  constexpr int kP = parts_of<kF16>();
+  constexpr int kP = kParts, kB = parts16<kF16>();
   typedef typename std::conditional<kVec, u32x4, u32x4_any>::type Vec;
-  // factors of a step: [w][32-column half][rank tile][1 KB], two steps in two
-  // arrays (so that the compiler can tell the one being filled)
-  __shared__ __attribute__((aligned(16))) char fac0[kTA * 4096];
-  __shared__ __attribute__((aligned(16))) char fac1[kTA * 4096];
+  // factors of a step: [w][32-column half][part][rank tile][1 KB], two steps in
+  // two arrays (so that the compiler can tell the one being filled)
+  __shared__ __attribute__((aligned(16))) char fac0[kTA * kB * 4096];
+  __shared__ __attribute__((aligned(16))) char fac1[kTA * kB * 4096];
   // [wave][two buffers][16 rows x 128 bytes], 16-byte piece p of row i at p ^ (i / 2)
   __shared__ __attribute__((aligned(16))) char turn[kJoinWaves][2][kTiles > 0 ? 2048 : 16];
   const int lane = threadIdx.x & 63;
@@ -204,12 +206,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
     }
   };
   // this wave's share of a step's factors: weight wave / 2, half wave % 2
-  const i32x4 brs = make_rsrc(Bo, np / 32 * kTiles * 2048);
+  constexpr int kFac = kB * kTiles;  // KB of 32 columns
+  const i32x4 brs = make_rsrc(Bo + (wave >> 1) * (np / 32) * kFac * 512, np / 32 * kFac * 1024);
   auto copy_factors = [&](int64_t c, char* fac) {
-    const uint32_t at = (uint32_t)(((wave >> 1) * (np / 32) + (c >> 5) + (wave & 1)) * kTiles * 1024);
+    const uint32_t at = (uint32_t)(((c >> 5) + (wave & 1)) * kFac * 1024);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-      copy16(brs, (uint32_t)lane * 16, (int)(at + t * 1024), fac + (wave * kTiles + t) * 1024);
+    for (int t = 0; t < kFac; ++t)
+      copy16(brs, (uint32_t)lane * 16, (int)(at + t * 1024), fac + (wave * kFac + t) * 1024);
   };
   auto step = [&](int64_t c, const char* fac, char* next, Stage& cur, Stage& nxt) {
     // the factors of this step have landed, and every wave is done with the
@@ -228,11 +231,40 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
       u32x4 p[2][kP];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        split8<kF16>(x[u][w], p[u]);
+        split8(x[u][w], p[u]);
+        u32x4 d = p[u][0];
+        if constexpr (kF16) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = pack2<true>(x[u][w][2 * e], x[u][w][2 * e + 1]);
+        }
         if (D != nullptr && in[u])
-          *reinterpret_cast<u32x4*>(D + (m0 + 8 * u + lr) * 2 * np + w * np + c + co) = p[u][0];
+          *reinterpret_cast<u32x4*>(D + (m0 + 8 * u + lr) * 2 * np + w * np + c + co) = d;
       }
-      if constexpr (kTiles > 0) {
+      if constexpr (kTiles > 0 && kF16) {
+        bf16x8 a[kP][2];
+#pragma unroll
+        for (int q = 0; q < kP; ++q) {
+          char* const buf = turn[wave][(w * kP + q) & 1];
+          *reinterpret_cast<u32x4*>(buf + wr0) = p[0][q];
+          *reinterpret_cast<u32x4*>(buf + wr1) = p[1][q];
+          asm volatile("" ::: "memory");  // (as below)
+          a[q][0] = *reinterpret_cast<const bf16x8*>(buf + rd0);
+          a[q][1] = *reinterpret_cast<const bf16x8*>(buf + rd1);
+          asm volatile("" ::: "memory");
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const char* const f = fac + lane * 16 + ((w * 2 + h) * kFac + t) * 1024;
+            const bf16x8 hi = *reinterpret_cast<const bf16x8*>(f), lo = *reinterpret_cast<const bf16x8*>(f + kTiles * 1024);
+#pragma unroll
+            for (int q = kP - 1; q >= 0; --q) {
+              if (q + 1 < kP) acc[w][t] = mfma16<false>(a[q][h], lo, acc[w][t]);
+              acc[w][t] = mfma16<false>(a[q][h], hi, acc[w][t]);
+            }
+          }
+      } else if constexpr (kTiles > 0) {
         bf16x8 b[2][kTA];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -251,8 +283,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
           asm volatile("" ::: "memory");
 #pragma unroll
           for (int t = 0; t < kTiles; ++t) {
-            acc[w][t] = mfma16<kF16>(a0, b[0][t], acc[w][t]);
-            acc[w][t] = mfma16<kF16>(a1, b[1][t], acc[w][t]);
+            acc[w][t] = mfma16<false>(a0, b[0][t], acc[w][t]);
+            acc[w][t] = mfma16<false>(a1, b[1][t], acc[w][t]);
           }
         }
       }
@@ -312,7 +344,7 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
   if (P) P[(w * M + m) * r + j] = s;
   if (split) {
     float v = scale * s;
-    asm("" : "+v"(v));  // one value for both conversions (split8)
+    asm("" : "+v"(v));  // one value for both conversions (as split8)
     const uint16_t hi = to16<kF16>(v);
     split[m * xc + w * 2 * r + j] = hi;
     split[m * xc + w * 2 * r + r + j] = to16<kF16>(v - from16<kF16>(hi));
@@ -337,7 +369,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
                                                        const uint16_t* __restrict__ dH, int64_t M, int64_t n,
                                                        const u32x4* __restrict__ Tt, int r, int64_t mchunk,
                                                        float* __restrict__ part) {
-  constexpr int kP = parts_of<kF16>();
+  constexpr int kP = kParts;
   constexpr int kJTall = kRP / 16;
   constexpr int kWJ = kJTall >= 4 ? 4 : kJTall;     // waves along ranks
   constexpr int kWC = 4 / kWJ;                      // waves along columns
@@ -380,10 +412,10 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
     join8<kF16>(s.g, s.u, s.d, dg, du);
     u32x4 p[kP];
     char* const at = sm + set * (2 * kP * kDbTile) + db_seg(prow, (t & 7) >> 1) + (t & 1) * 16;
-    split8<kF16>(dg, p);
+    split8(dg, p);
 #pragma unroll
     for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(at + q * kDbTile) = p[q];
-    split8<kF16>(du, p);
+    split8(du, p);
 #pragma unroll
     for (int q = 0; q < kP; ++q) *reinterpret_cast<u32x4*>(at + (kP + q) * kDbTile) = p[q];
   };
@@ -430,7 +462,7 @@ __global__ __launch_bounds__(256) void gated_db_kernel(const uint16_t* __restric
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int a = 0; a < kJT; ++a)
-              acc[w][a][b] = mfma16<kF16>(__builtin_bit_cast(bf16x8, ta[w][order - q][a]), pb[w][q], acc[w][a][b]);
+              acc[w][a][b] = mfma16<false>(__builtin_bit_cast(bf16x8, ta[w][order - q][a]), pb[w][q], acc[w][a][b]);
     }
     __syncthreads();
   }
@@ -555,9 +587,10 @@ hipError_t launch_gated_project(const uint16_t* X, int64_t M, int64_t k, const u
   return e;
 }
 
+// (B in operand order: both factors, an fp16 one in two parts)
 size_t gated_join_ws_bytes(int64_t M, int64_t n, int r) {
   if (r == 0) return 0;
-  return align256(2 * operand_order_bytes(gated_pad(n), r)) +
+  return align256(4 * operand_order_bytes(gated_pad(n), r)) +
          align256((size_t)join_plan(M, n).splits * 2 * (size_t)M * r * 4);
 }
 
@@ -568,9 +601,9 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
   const int64_t np = gated_pad(n);
   const int rp = rank_pad(r);
   uint16_t* const Bo = static_cast<uint16_t*>(ws);
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(2 * operand_order_bytes(np, r)));
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(4 * operand_order_bytes(np, r)));
   if (r > 0) {
-    const hipError_t e = launch_operand_order(Bg, Bu, 1, n, np, r, Bo, stream);
+    const hipError_t e = launch_operand_order(Bg, Bu, 1, n, np, r, Bo, stream, f16);
     if (e != hipSuccess) return e;
   }
   const dim3 grid((unsigned)cdiv(M, (int64_t)kJoinRows), (unsigned)pl.splits);

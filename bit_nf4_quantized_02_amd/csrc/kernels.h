@@ -154,8 +154,10 @@ inline int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 :
 // / 16][64 lanes][16 bytes], zero past C (Cp: a multiple of 32); Q1's (not NULL)
 // after it.
 size_t operand_order_bytes(int64_t Cp, int r);
+// split16: Q is fp16 and given as two bf16 parts, one after the other for each
+// 32 columns (twice the bytes).
 hipError_t launch_operand_order(const uint16_t* Q, const uint16_t* Q1, int layout, int64_t C, int64_t Cp, int r,
-                                uint16_t* out, hipStream_t stream);
+                                uint16_t* out, hipStream_t stream, bool split16 = false);
 
 // One factor Q in operand order as above and the other as low-rank operand rows
 // [nf, lora_extra_cols(r)]: layout 0 (forward) Q = A [r, C], F = B [nf, r], rows
@@ -200,10 +202,10 @@ hipError_t launch_gemv_dx(const Nf4View& w, const uint16_t* dY, int64_t M, const
                           float keep = 1.0f);
 
 // ---- adapter gradients of the feed-forward operators (colgrad.hip)
-// Q0 fp32 [W0][M][r], Q1 [W1][M][r] as 16-bit parts in operand order (W 0: none).
+// Q0 fp32 [W0][M][r], Q1 [W1][M][r] as bf16 parts in operand order (W 0: none).
 size_t rank_parts_bytes(int64_t M, int r, int W);
 hipError_t launch_rank_parts(const float* Q0, int W0, void* out0, const float* Q1, int W1, void* out1, int64_t M, int r,
-                             hipStream_t stream, bool f16);
+                             hipStream_t stream);
 // Gradients left as partials [splits][W][count], to be added in order (G1: w =
 // 1; NULL: left out); W 0: none.
 struct GradJob {

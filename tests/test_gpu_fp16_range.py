@@ -1,0 +1,106 @@
+"""fp16 calls of the feed-forward operators over the whole range of their
+operands: what the definitions keep in fp32 (T, P, dG, dU and the adapter
+gradients) holds fp32's accuracy where fp16 itself would have run out of bits
+(below 2^-3 its second part is a subnormal) or of range (above 65504).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from bit_nf4_quantized_02_amd import synth
+from oracle import fp8 as o8
+from oracle import mlp as omlp
+
+from gpu_util import f32, say
+
+pytestmark = pytest.mark.gpu
+
+HF = torch.float16
+
+
+@pytest.fixture(scope="module")
+def q():
+    from bit_nf4_quantized_02_amd import qlora
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return qlora
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _normal(shape, std, *seed):
+    return torch.from_numpy(synth.rng(*seed).standard_normal(shape) * std).to(HF).cuda()
+
+
+def _ranks(name, got, ref, more=0.0):
+    """Every rank's gradient by itself ([ranks, *]): 2^-20 of its norm. Each of T, P, dG, dU is an fp32 value that
+    enters with 24 bits, after a few fp32 operations, and the products are added in fp32 over at most 1088 terms of
+    either sign, whose error is a few 2^-24 of the root of their squares. more: what each rank may miss besides."""
+    g, r = np.asarray(f32(got), np.float64), np.asarray(ref)
+    assert np.isfinite(g).all(), name
+    e, n = np.linalg.norm(g - r, axis=1), np.linalg.norm(r, axis=1)
+    say(f"  {name}: worst rank 2^{np.log2((e / n).max()):.2f}")
+    assert (e <= 2.0 ** -20 * n + more).all(), name
+
+
+def _product_error(P, Q):
+    """Largest error of the fp16 product P Q over its groups of 8 contraction elements, beyond fp32 sums. The matrix
+    instruction aligns the 8 products of a group at 2^-24 of the largest (measured: 1 - 1 + 2^-24 is exact, 2^-25 is
+    lost), and there an operand below fp16's smallest normal value counts as 2^-14 (2^-20 - 2^-20 + 2^-38 is exact,
+    2^-39 lost): each of the other 7 loses less than 2^-24 of it."""
+    c = -(-P.shape[1] // 8) * 8
+    p, q = np.zeros((P.shape[0], c)), np.zeros((c, Q.shape[1]))
+    p[:, :P.shape[1]] = np.where(P == 0, 0, np.maximum(np.abs(P), 2.0 ** -14))
+    q[:P.shape[1]] = np.where(Q == 0, 0, np.maximum(np.abs(Q), 2.0 ** -14))
+    return 7 * 2.0 ** -24 * sum((p[:, i:i + 8, None] * q[None, i:i + 8]).max(1) for i in range(0, c, 8))
+
+
+# std of dH (dY), of U, of X and of B: a young adapter under no loss scaling, dG past 65504, T past 65504
+SCALES = [(1e-3, 1.0, 1.0, 1e-2), (1e-4, 1.0, 1.0, 1e-3), (1e-5, 0.1, 1e-2, 1e-3), (1e4, 100.0, 1.0, 0.05),
+          (1.0, 1.0, 1e4, 10.0)]
+
+
+@pytest.mark.parametrize("m,n,k,r", [(300, 1030, 1088, 12), (140, 264, 320, 64), (40, 200, 192, 100), (70, 129, 64, 20)])
+@pytest.mark.parametrize("dh,u,x,b", SCALES)
+def test_gated_adapter_gradients(q, m, n, k, r, dh, u, x, b):
+    say(f"case: fp16 gated gradients M={m} N={n} K={k} r={r}, dH {dh} U {u} X {x} B {b}")
+    s = 0.5
+    w = q.quantize_nf4(_normal((n, k), 0.03, 60, 0).bfloat16())
+    X, dH = _normal((m, k), x, 60, 1), _normal((m, n), dh, 60, 2)
+    G, U = _normal((m, n), 1.0, 60, 3), _normal((m, n), u, 60, 4)
+    Ag, Au = (_normal((r, k), k ** -0.5 * 30, 60, 5 + i) for i in range(2))
+    # ranks of very different size beside each other
+    sp = 2.0 ** -(torch.arange(r, device="cuda") % 8)
+    Bg, Bu = ((_normal((n, r), b, 60, 7 + i).float() * sp).half() for i in range(2))
+    T = torch.stack([X.float() @ Ag.float().T, X.float() @ Au.float().T])
+    out = q.gated_bwd(w, w, X, T, G, U, dH, Ag, Bg, Au, Bu, s, need_dX=False)
+    Z = np.zeros((n, k))
+    ref = omlp.gated_bwd(_f64(X), Z, Z, _f64(G), _f64(U), _f64(dH), _f64(Ag), _f64(Bg), _f64(Au), _f64(Bu), s)
+    # dB from the T that was passed, not from its 64-bit definition
+    dG, dU = omlp.silu_mul_bwd(_f64(G), _f64(U), _f64(dH))
+    _ranks("dAg", out[1], ref[1])
+    _ranks("dAu", out[3], ref[3])
+    _ranks("dBg", out[2].T, s * (dG.T @ _f64(T[0])).T)
+    _ranks("dBu", out[4].T, s * (dU.T @ _f64(T[1])).T)
+    if dh * u < 1e3:  # dX as well: dG and dU within fp16
+        full = q.gated_bwd(w, w, X, T, G, U, dH, Ag, Bg, Au, Bu, s)
+        assert all(torch.equal(p, t) for p, t in zip(full[1:], out[1:]))
+
+
+@pytest.mark.parametrize("m,n,k,r", [(300, 1030, 1088, 12), (140, 264, 320, 64), (40, 200, 192, 100), (70, 129, 64, 20)])
+@pytest.mark.parametrize("dy,u,x,b", SCALES)
+def test_fp8_layer_adapter_gradients(q, m, n, k, r, dy, u, x, b):
+    dy = min(dy * u, 1e4)
+    say(f"case: fp16 8-bit layer gradients M={m} N={n} K={k} r={r}, dY {dy} X {x} B {b}")
+    s = 0.5
+    w = q.quantize_fp8(_normal((n, k), 0.02, 61, 0))
+    X, dY = _normal((m, k), x, 61, 1), _normal((m, n), dy, 61, 2)
+    A = _normal((r, k), k ** -0.5 * 30, 61, 3)
+    B = (_normal((n, r), b, 61, 4).float() * 2.0 ** -(torch.arange(r, device="cuda") % 8)).half()
+    T = X.float() @ A.float().T
+    _, dA, dB = q.fp8_linear_bwd(w, X, T, dY, A, B, s, need_dX=False)
+    _, dAr, _ = o8.linear_bwd(_f64(X), np.zeros((n, k)), _f64(A), _f64(B), s, _f64(dY))
+    _ranks("dA", dA, dAr, s * np.linalg.norm(_product_error(_f64(dY), _f64(B)).T @ np.abs(_f64(X)), axis=1))
+    _ranks("dB", dB.T, s * (_f64(dY).T @ _f64(T)).T)
