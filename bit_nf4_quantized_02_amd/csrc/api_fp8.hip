@@ -35,6 +35,7 @@ struct FwdWs {
   float* proj = nullptr;   // partials of T
   float* T = nullptr;      // M <= 16: T where its partials are too many for the GEMV to add
   uint16_t* TS = nullptr;  // low-rank operand columns
+  float* rs = nullptr;     // their factor of each row (fp16)
   uint16_t* Bx = nullptr;
   uint16_t* Ao = nullptr;  // A in operand order
   float* part = nullptr;
@@ -57,6 +58,7 @@ size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
   o.xs = cv.take<uint8_t>(fp8_rows_scale_bytes(M, k));
   if (r > 0) {
     o.TS = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
+    o.rs = cv.take<float>(row_scale_bytes(M));
     o.Bx = cv.take<uint16_t>((size_t)n * lora_extra_cols(r) * 2);
     o.Ao = cv.take<uint16_t>(operand_order_bytes(f8_pad(k), r));
   }
@@ -68,6 +70,7 @@ struct BwdWs {
   uint8_t* yq = nullptr;   // dY's codes and scale words
   uint8_t* ys = nullptr;
   uint16_t* US = nullptr;
+  float* rs = nullptr;     // the factor of each row of US (fp16)
   uint16_t* Ax = nullptr;
   uint16_t* Bo = nullptr;  // B in operand order
   float* U = nullptr;
@@ -85,6 +88,7 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
   o.ys = cv.take<uint8_t>(fp8_rows_scale_bytes(M, n));
   if (r > 0) {
     o.US = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
+    o.rs = cv.take<float>(row_scale_bytes(M));
     o.Ax = cv.take<uint16_t>((size_t)k * lora_extra_cols(r) * 2);
     o.Bo = cv.take<uint16_t>(operand_order_bytes(f8_pad(n), r));
     o.U = cv.take<float>((size_t)M * r * 4);
@@ -174,9 +178,11 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int6
     return hip_status(e);
   }
   const int64_t nb = f8_pad(k) / kF8Block;
-  if (r > 0 && e == hipSuccess) e = launch_rowdot_finalize(o.proj, parts, M, r, T_save, o.TS, scale, st, f16);
+  if (r > 0 && e == hipSuccess)
+    e = f16 ? launch_scaled_columns(o.proj, parts, 1, M, r, lora_extra_cols(r), scale, T_save, o.TS, o.rs, st)
+            : launch_rowdot_finalize(o.proj, parts, M, r, T_save, o.TS, scale, st, false);
   if (e == hipSuccess)
-    e = launch_gemm_fp8(o.xq, o.xs, M, k, o.TS, lora_extra_cols(r), w->codes, w->scale, nb, 1,
+    e = launch_gemm_fp8(o.xq, o.xs, M, k, o.TS, lora_extra_cols(r), o.rs, w->codes, w->scale, nb, 1,
                         (f8_pad(n) / kF8Block) * nb, o.Bx, n, static_cast<uint16_t*>(Y), o.part, st, f16, false);
   return hip_status(e);
 }
@@ -220,14 +226,16 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, cons
       e = launch_operand_order(b, nullptr, 1, n, f8_pad(n), r, o.Bo, st);
     if (e == hipSuccess)
       e = launch_fp8_prep(dy, M, n, o.Bo, r, dX ? o.yq : nullptr, o.ys, o.proj, false, st, f16);
+    const int parts = fp8_prep_plan(M, n, false).splits;
+    uint16_t* const us = dX ? o.US : nullptr;
     if (e == hipSuccess && r > 0)
-      e = launch_rowdot_finalize(o.proj, fp8_prep_plan(M, n, false).splits, M, r, o.U, dX ? o.US : nullptr, scale, st,
-                                 f16);
+      e = f16 ? launch_scaled_columns(o.proj, parts, 1, M, r, lora_extra_cols(r), scale, o.U, us, o.rs, st)
+              : launch_rowdot_finalize(o.proj, parts, M, r, o.U, us, scale, st, false);
   }
   if (dX) {
     const int64_t kb = f8_pad(k) / kF8Block;
     if (e == hipSuccess)
-      e = launch_gemm_fp8(o.yq, o.ys, M, n, o.US, lora_extra_cols(r), w->codes, w->scale, 1, kb,
+      e = launch_gemm_fp8(o.yq, o.ys, M, n, o.US, lora_extra_cols(r), o.rs, w->codes, w->scale, 1, kb,
                           (f8_pad(n) / kF8Block) * kb, o.Ax, k, static_cast<uint16_t*>(dX), o.part, st, f16, true);
   }
   if (!dA && !dB) return hip_status(e);

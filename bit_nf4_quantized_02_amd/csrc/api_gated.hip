@@ -41,6 +41,7 @@ struct FwdWs {
   void* few = nullptr;     // few tokens: the GEMV's operands
   void* proj = nullptr;
   uint16_t* TS = nullptr;  // low-rank columns of the GEMM
+  float* rs = nullptr;     // their factor of each row (fp16)
   uint16_t* F = nullptr;   // both weights expanded
   float* part = nullptr;
 };
@@ -53,6 +54,7 @@ size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
   const int xc = gated_extra_cols(r);
   if (r > 0) o.proj = cv.take<char>(gated_project_ws_bytes(M, k, r));
   if (r > 0) o.TS = cv.take<uint16_t>((size_t)M * xc * 2);
+  if (r > 0) o.rs = cv.take<float>(row_scale_bytes(M));
   o.F = cv.take<uint16_t>(gated_fwd_operand_bytes(n, k, r));
   o.part = cv.take<float>(gemm_bf16_ws_bytes(M, k, xc, gated_rows(n)));
   return cv.used;
@@ -62,6 +64,7 @@ struct BwdWs {
   float* T = nullptr;      // [2][M][r] without T_saved
   float* P = nullptr;      // [2][M][r]
   uint16_t* PS = nullptr;  // low-rank columns of dX's GEMM
+  float* rs = nullptr;     // their factor of each row (fp16)
   uint16_t* D = nullptr;   // [dG | dU]
   uint16_t* F = nullptr;   // both weights, contraction-major
   void* proj = nullptr;
@@ -80,6 +83,7 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
     o.T = cv.take<float>((size_t)2 * M * r * 4);
     o.P = cv.take<float>((size_t)2 * M * r * 4);
     o.PS = cv.take<uint16_t>((size_t)M * xc * 2);
+    o.rs = cv.take<float>(row_scale_bytes(M));
     o.proj = cv.take<char>(gated_project_ws_bytes(M, k, r));
     o.join = cv.take<char>(gated_join_ws_bytes(M, n, r));
     o.Pp = cv.take<char>(rank_parts_bytes(M, r, 2));
@@ -139,9 +143,10 @@ qlora_status qlora_gated_fwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
                                        T_save, o.few, st, f16));
   hipError_t e = hipSuccess;
   const int xc = gated_extra_cols(r);
-  if (r > 0) e = launch_gated_project(x, M, k, u16(A_gate), u16(A_up), r, scale, T_save, o.TS, o.proj, st, f16);
+  if (r > 0) e = launch_gated_project(x, M, k, u16(A_gate), u16(A_up), r, scale, T_save, o.TS, o.rs, o.proj,
+                                    st, f16);
   if (e == hipSuccess) e = launch_gated_expand_fwd(g, u, u16(B_gate), u16(B_up), r, o.F, st, f16);
-  if (e == hipSuccess) e = launch_gemm_gated(x, M, k, o.TS, xc, o.F, n, h, gs, us, o.part, st, f16);
+  if (e == hipSuccess) e = launch_gemm_gated(x, M, k, o.TS, xc, o.rs, o.F, n, h, gs, us, o.part, st, f16);
   return hip_status(e);
 }
 
@@ -183,18 +188,20 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* w_gate, const qlora_nf4_wei
   const uint16_t* const x = u16(X);
   if (dX || need_a)
     e = launch_gated_join(u16(G), u16(U), u16(dH), M, n, u16(B_gate), u16(B_up), r, scale, dX ? o.D : nullptr, o.P,
-                          dX ? o.PS : nullptr, o.join, st, f16);
+                          dX ? o.PS : nullptr, o.rs, o.join, st, f16);
   if (dX) {
     if (e == hipSuccess)
       e = launch_gated_expand_dx(view_of(w_gate), view_of(w_up), u16(A_gate), u16(A_up), r, o.F, st, f16);
     if (e == hipSuccess)
       e = launch_gemm_bf16_ext(o.D, M, 2 * np, r > 0 ? o.PS : nullptr, xc, o.F, k, o.F + 2 * np * k, k, k,
-                               static_cast<uint16_t*>(dX), o.part, st, nullptr, 1.0f, f16, /*nn=*/true);
+                               static_cast<uint16_t*>(dX), o.part, st, nullptr, 1.0f, f16, /*nn=*/true,
+                               o.rs);
   }
   if (!need_a && !need_b) return hip_status(e);
   const float* T = T_saved;
   if (e == hipSuccess && need_b && T == nullptr) {
-    e = launch_gated_project(x, M, k, u16(A_gate), u16(A_up), r, scale, o.T, nullptr, o.proj, st, f16);
+    e = launch_gated_project(x, M, k, u16(A_gate), u16(A_up), r, scale, o.T, nullptr, nullptr, o.proj, st,
+                             f16);
     T = o.T;
   }
   GradJob ja{}, jb{};

@@ -314,7 +314,6 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
 
 // P = the partials added in split order; split row m = [hi_g | lo_g | hi_u |
 // lo_u | 0] of scale P. One thread per (m, w, j), and for the padding columns.
-template <bool kF16>
 __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ part, int splits, int64_t M, int r,
                                                       int xc, float scale, float* __restrict__ P,
                                                       uint16_t* __restrict__ split) {
@@ -345,10 +344,68 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
   if (split) {
     float v = scale * s;
     asm("" : "+v"(v));  // one value for both conversions (as split8)
-    const uint16_t hi = to16<kF16>(v);
+    const uint16_t hi = to16<false>(v);
     split[m * xc + w * 2 * r + j] = hi;
-    split[m * xc + w * 2 * r + r + j] = to16<kF16>(v - from16<kF16>(hi));
+    split[m * xc + w * 2 * r + r + j] = to16<false>(v - from16<false>(hi));
   }
+}
+
+// The fp16 form, of one or two factors (launch_scaled_columns): one row per
+// wave, up to four of its W r values per lane.
+__global__ __launch_bounds__(256) void scaled_columns_kernel(const float* __restrict__ part, int splits, int W, int64_t M,
+                                                             int r, int xc, float scale, float* __restrict__ out,
+                                                             uint16_t* __restrict__ split,
+                                                             float* __restrict__ row_scale) {
+#pragma clang fp contract(off)
+  const int lane = threadIdx.x & 63;
+  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (m >= M) return;
+  const int count = W * r;
+  const int64_t pitch = (int64_t)W * M * r;
+  float v[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = lane + 64 * e;
+    v[e] = 0.0f;
+    if (i >= count) continue;
+    const int64_t at = ((int64_t)(i / r) * M + m) * r + i % r;
+    float s = 0.0f;
+    for (int p0 = 0; p0 < splits; p0 += 8) {
+      float t[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) t[p] = part[at + (p0 + p < splits ? p0 + p : splits - 1) * pitch];
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p0 + p < splits) s = p0 + p == 0 ? t[p] : s + t[p];
+    }
+    if (out) out[at] = s;
+    v[e] = scale * s;
+    asm("" : "+v"(v[e]));  // one value for the maximum and both conversions
+    top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  }
+  if (split == nullptr) return;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+  // largest value 1.x 2^(b - 127): e = b - 141, kept where 2^e and 2^-e are normal numbers
+  // (a row with a value that is not finite, or of zeros, stays as it is)
+  int e2 = (int)(top >> 23) - 141;
+  e2 = top == 0 || top >= 0x7F800000u ? 0 : e2 < -112 ? -112 : e2;
+  const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+  if (lane == 0) row_scale[m] = __uint_as_float((uint32_t)(127 + e2) << 23);
+  uint16_t* const row = split + m * xc;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = lane + 64 * e;
+    if (i >= count) continue;
+    float x = v[e] * down;
+    asm("" : "+v"(x));
+    const uint16_t hi = to16<true>(x);
+    const int c = i / r * 2 * r + i % r;
+    row[c] = hi;
+    row[c + r] = to16<true>(x - from16<true>(hi));
+  }
+  for (int c = 2 * count + lane; c < xc; c += 64) row[c] = 0;
 }
 
 // ------------------------------------------------------ adapter gradients dB
@@ -560,17 +617,23 @@ hipError_t launch_gated_expand_dx(const Nf4View& g, const Nf4View& u, const uint
 namespace {
 
 hipError_t launch_p(const float* part, int splits, int64_t M, int r, float scale, float* P, uint16_t* split,
-                    hipStream_t stream, bool f16) {
+                    float* row_scale, hipStream_t stream, bool f16) {
   const int xc = gated_extra_cols(r);
+  if (f16) return launch_scaled_columns(part, splits, 2, M, r, xc, scale, P, split, row_scale, stream);
   const unsigned grid = (unsigned)cdiv(M * (xc - 2 * r), (int64_t)256);
-  if (f16)
-    gated_p_kernel<true><<<grid, 256, 0, stream>>>(part, splits, M, r, xc, scale, P, split);
-  else
-    gated_p_kernel<false><<<grid, 256, 0, stream>>>(part, splits, M, r, xc, scale, P, split);
+  gated_p_kernel<<<grid, 256, 0, stream>>>(part, splits, M, r, xc, scale, P, split);
   return hipGetLastError();
 }
 
 }  // namespace
+
+hipError_t launch_scaled_columns(const float* part, int splits, int W, int64_t M, int r, int xc, float scale, float* out,
+                                 uint16_t* split, float* row_scale, hipStream_t stream) {
+  if (W * r > 256 || (split != nullptr && row_scale == nullptr)) return hipErrorInvalidValue;
+  scaled_columns_kernel<<<(unsigned)cdiv(M, (int64_t)4), 256, 0, stream>>>(part, splits, W, M, r, xc, scale, out, split,
+                                                                          row_scale);
+  return hipGetLastError();
+}
 
 size_t gated_project_ws_bytes(int64_t M, int64_t k, int r) {
   return align256(2 * operand_order_bytes(f8_pad(k), r)) +
@@ -578,12 +641,13 @@ size_t gated_project_ws_bytes(int64_t M, int64_t k, int r) {
 }
 
 hipError_t launch_gated_project(const uint16_t* X, int64_t M, int64_t k, const uint16_t* Ag, const uint16_t* Au, int r,
-                                float scale, float* T, uint16_t* split, void* ws, hipStream_t stream, bool f16) {
+                                float scale, float* T, uint16_t* split, float* row_scale, void* ws, hipStream_t stream,
+                                bool f16) {
   uint16_t* const Ao = static_cast<uint16_t*>(ws);
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(2 * operand_order_bytes(f8_pad(k), r)));
   hipError_t e = launch_operand_order(Ag, Au, 0, k, f8_pad(k), r, Ao, stream);
   if (e == hipSuccess) e = launch_fp8_prep(X, M, k, Ao, r, nullptr, nullptr, part, false, stream, f16, 2);
-  if (e == hipSuccess) e = launch_p(part, fp8_prep_plan(M, k, false, 2).splits, M, r, scale, T, split, stream, f16);
+  if (e == hipSuccess) e = launch_p(part, fp8_prep_plan(M, k, false, 2).splits, M, r, scale, T, split, row_scale, stream, f16);
   return e;
 }
 
@@ -596,7 +660,7 @@ size_t gated_join_ws_bytes(int64_t M, int64_t n, int r) {
 
 hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
                              const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* D, float* P,
-                             uint16_t* split, void* ws, hipStream_t stream, bool f16) {
+                             uint16_t* split, float* row_scale, void* ws, hipStream_t stream, bool f16) {
   const JoinPlan pl = join_plan(M, n);
   const int64_t np = gated_pad(n);
   const int rp = rank_pad(r);
@@ -621,7 +685,7 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
   else QLORA_JOIN(128)
 #undef QLORA_JOIN
 #undef QLORA_JOIN2
-  if (r > 0) return launch_p(part, pl.splits, M, r, scale, P, split, stream, f16);
+  if (r > 0) return launch_p(part, pl.splits, M, r, scale, P, split, row_scale, stream, f16);
   return hipGetLastError();
 }
 

@@ -65,6 +65,8 @@ struct BfArgs {
   uint16_t* g_out;
   uint16_t* u_out;
   int64_t hn;
+  // factor of each row of the low-rank columns (kScaled; rows up to a multiple of 256)
+  const float* row_scale;
 };
 
 constexpr int kCopies = 32 / kWaves;  // 1 KB copies per wave per operand tile
@@ -427,6 +429,9 @@ __device__ __forceinline__ void mask_acc_lds(f32x16 (&acc)[kTM][kTN], const char
 // low-rank steps runs them first (unpipelined, 1-4 steps) on buffers 0 while
 // the tile's mask bytes land in buffers 1, masks and scales the accumulators
 // from there, then runs its main steps as usual.
+// kScaled (the fp16 forms of the gated block): the low-rank columns hold s T 2^-e
+// with one e per row, so that they neither leave fp16's range nor fall below its
+// steps; their steps run first in the same way and the sums take 2^e then.
 // kF16: fp16 operands and output (the compute-type ablation), else bf16.
 // kA3: the mirrored ring (bf16_step_a3; plain bf16 only).
 // kGate: the gated feed-forward block's forward. The weight operand holds 32
@@ -484,17 +489,22 @@ __global__ __launch_bounds__(kThreads) void gemm_bf16_kernel(BfArgs a) {
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
   int nk_end = nk;  // exclusive end of the pipelined range
-  if constexpr (kMask) {
+  constexpr bool kScaled = kF16 && (kNN || kGate);
+  if constexpr (kMask || kScaled) {
     if (nk > nk_main) {
-      issue_mask_lds(a, m0, n0, wave, As1, Bs1);
+      if constexpr (kMask) issue_mask_lds(a, m0, n0, wave, As1, Bs1);
       for (int step = sbeg > nk_main ? sbeg : nk_main; step < nk; ++step) {
         issue_step<kNN>(rs, plan, step, nk_main, wave, As0, Bs0, a.ldf, a.ldx);
         step_barrier<0>();  // (the first one also waits for the mask bytes)
         plain_step<kF16, kNN>(As0, Bs0, wave, acc);
         __syncthreads();  // every wave's reads done before the next copies land
       }
-      mask_acc_lds(acc, As1, Bs1, a.keep_scale, a.M, a.nout, m0, n0, wm0, wn0, lane);
-      __syncthreads();  // mask reads done before the main steps' copies reuse buffers 1
+      if constexpr (kMask) {
+        mask_acc_lds(acc, As1, Bs1, a.keep_scale, a.M, a.nout, m0, n0, wm0, wn0, lane);
+        __syncthreads();  // mask reads done before the main steps' copies reuse buffers 1
+      } else {
+        scale_rows(acc, a.row_scale, m0 + wm0, lane);
+      }
       nk_end = nk_main;
     }
   }
@@ -718,7 +728,7 @@ constexpr int64_t kActStreamBytes = 128LL << 20;
 hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, const uint16_t* split, int kx,
                                 const uint16_t* f, int64_t ldf, const uint16_t* fx, int64_t ldx, int64_t nout,
                                 uint16_t* out, float* part, hipStream_t stream, const uint8_t* mask, float keep_scale,
-                                bool f16, bool nn) {
+                                bool f16, bool nn, const float* row_scale) {
   BfArgs a{};
   a.mask = mask;
   a.keep_scale = keep_scale;
@@ -734,7 +744,8 @@ hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, cons
   const dim3 grid((unsigned)(a.full + a.tail * a.splits));
   if (nn) {
     // the weight operand stored [contraction][output] (bf16 base, dX)
-    if (mask != nullptr) return hipErrorInvalidValue;
+    if (mask != nullptr || (f16 && kx > 0 && row_scale == nullptr)) return hipErrorInvalidValue;
+    a.row_scale = row_scale;
     if (f16)
       gemm_bf16_kernel<false, true, true><<<grid, kThreads, 0, stream>>>(a);
     else if (M * kc * 2 > kActStreamBytes)
@@ -770,9 +781,11 @@ hipError_t launch_gemm_bf16(const uint16_t* act, int64_t M, int64_t kc, const ui
 }
 
 hipError_t launch_gemm_gated(const uint16_t* act, int64_t M, int64_t k, const uint16_t* split, int kx,
-                             const uint16_t* f, int64_t n, uint16_t* H, uint16_t* G, uint16_t* U, float* part,
-                             hipStream_t stream, bool f16) {
+                             const float* row_scale, const uint16_t* f, int64_t n, uint16_t* H, uint16_t* G, uint16_t* U,
+                             float* part, hipStream_t stream, bool f16) {
+  if (f16 && kx > 0 && row_scale == nullptr) return hipErrorInvalidValue;
   BfArgs a{};
+  a.row_scale = row_scale;
   a.act = act; a.M = M; a.kc = k;
   a.act_x = split; a.kx = kx;
   a.f = f; a.ldf = k + kx; a.nout = gated_rows(n);

@@ -38,6 +38,7 @@ struct F8Args {
   int64_t M, lda;
   const uint16_t* act_x;  // [M, kx] low-rank split columns
   int kx;
+  const float* row_scale;  // fp16: what the split columns of each row were divided by (rows up to a multiple of 256)
   const uint8_t* f;     // [nout, ldf] codes; kNN: [kc, ldf]
   int64_t ldf, f_rows;
   const uint8_t* fs;    // scale byte of (output block, contraction block) at ob * fs_o + cb * fs_c
@@ -254,6 +255,9 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(F8Args a) {
       }
       __syncthreads();  // every wave's reads done before the next copies land
     }
+    if constexpr (kF16) {
+      if (a.kx > 0) scale_rows(acc, a.row_scale, m0 + wm0, lane);
+    }
   }
 
   {
@@ -350,10 +354,13 @@ size_t gemm_fp8_ws_bytes(int64_t M, int64_t kc, int64_t nout) {
 }
 
 hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int64_t kc, const uint16_t* split, int kx,
+                           const float* row_scale,
                            const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
                            const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16,
                            bool nn) {
+  if (f16 && kx > 0 && row_scale == nullptr) return hipErrorInvalidValue;
   F8Args a{};
+  a.row_scale = row_scale;
   a.act = act; a.as = as; a.M = M; a.lda = f8_pad(kc);
   a.act_x = split; a.kx = kx;
   a.f = f; a.fs = fs; a.fs_o = fs_o; a.fs_c = fs_c; a.fs_bytes = fs_bytes;

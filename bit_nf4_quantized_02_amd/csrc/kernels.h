@@ -146,7 +146,8 @@ hipError_t launch_gemm_bf16(const uint16_t* act, int64_t M, int64_t kc, const ui
 hipError_t launch_gemm_bf16_ext(const uint16_t* act, int64_t M, int64_t kc, const uint16_t* split, int kx,
                                 const uint16_t* f, int64_t ldf, const uint16_t* fx, int64_t ldx, int64_t nout,
                                 uint16_t* out, float* part, hipStream_t stream, const uint8_t* mask = nullptr,
-                                float keep_scale = 1.0f, bool f16 = false, bool nn = false);
+                                float keep_scale = 1.0f, bool f16 = false, bool nn = false,
+                                const float* row_scale = nullptr);
 
 // Ranks padded to what the kernels that take factors in operand order are built for.
 inline int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
@@ -228,13 +229,23 @@ size_t gemv_pair_ws_bytes(int64_t M, int64_t n, int64_t k, int r);
 hipError_t launch_gemv_pair(const Nf4View& g, const Nf4View& u, const uint16_t* X, int64_t M, const uint16_t* Ag,
                             const uint16_t* Bg, const uint16_t* Au, const uint16_t* Bu, int r, float scale, uint16_t* H,
                             uint16_t* G, uint16_t* U, float* T_save, void* ws, hipStream_t stream, bool f16);
-// Low-rank columns of the block's GEMMs, [hi_g | lo_g | hi_u | lo_u | 0].
+// Low-rank columns of the block's GEMMs, [hi_g | lo_g | hi_u | lo_u | 0] of s T
+// or s P (fp16: times 2^-e, by row).
 inline int gated_extra_cols(int r) { return r > 0 ? ((4 * r + 63) / 64) * 64 : 0; }
+// fp16: low-rank columns from partials [splits][W][M][r] added in order. out
+// (NULL: not written) takes the sums [W][M][r]; split (NULL: not written) row m's
+// columns [hi_0 | lo_0 | hi_1 | .. | 0] (xc in all) of scale * sums times 2^-e,
+// and row_scale[m] 2^e, with e so that the row's largest value lies in [2^14, 2^15):
+// none leaves fp16's range, and lo's smallest step is 2^-39 of it.
+inline size_t row_scale_bytes(int64_t M) { return (size_t)((M + 255) / 256 * 256) * 4; }  // whole tiles of rows
+hipError_t launch_scaled_columns(const float* part, int splits, int W, int64_t M, int r, int xc, float scale, float* out,
+                                 uint16_t* split, float* row_scale, hipStream_t stream);
 // X Ag^T and X Au^T: T (NULL: not written) as [2][M][r], and the scaled
-// columns in split (NULL: not written).
+// columns in split (NULL: not written; fp16: with row_scale).
 size_t gated_project_ws_bytes(int64_t M, int64_t k, int r);
 hipError_t launch_gated_project(const uint16_t* X, int64_t M, int64_t k, const uint16_t* Ag, const uint16_t* Au, int r,
-                                float scale, float* T, uint16_t* split, void* ws, hipStream_t stream, bool f16);
+                                float scale, float* T, uint16_t* split, float* row_scale, void* ws, hipStream_t stream,
+                                bool f16);
 // Both weights expanded for the forward: rows in groups of 64, 32 gate rows
 // then the same 32 up rows, [W' | low-rank columns], pitch k + extra.
 inline int64_t gated_rows(int64_t n) { return (n + 31) / 32 * 64; }
@@ -244,8 +255,8 @@ hipError_t launch_gated_expand_fwd(const Nf4View& g, const Nf4View& u, const uin
 // The forward GEMM over it with the join in its epilogue (part as the plain
 // GEMM's for gated_rows(n) outputs).
 hipError_t launch_gemm_gated(const uint16_t* act, int64_t M, int64_t k, const uint16_t* split, int kx,
-                             const uint16_t* f, int64_t n, uint16_t* H, uint16_t* G, uint16_t* U, float* part,
-                             hipStream_t stream, bool f16);
+                             const float* row_scale, const uint16_t* f, int64_t n, uint16_t* H, uint16_t* G, uint16_t* U,
+                             float* part, hipStream_t stream, bool f16);
 // Both weights contraction-major for dX: [Wg ; 0 ; Wu ; 0 ; Ag ; Ag ; Au ; Au
 // ; 0], each weight's rows padded to a multiple of 64, pitch k.
 inline int64_t gated_pad(int64_t n) { return (n + 63) / 64 * 64; }
@@ -254,11 +265,11 @@ hipError_t launch_gated_expand_dx(const Nf4View& g, const Nf4View& u, const uint
                                   uint16_t* out, hipStream_t stream, bool f16);
 // D [M, 2 gated_pad(n)] = [dG | 0 | dU | 0] in 16 bits (D NULL: not written),
 // and (r > 0) P = [dG Bg ; dU Bu] as fp32 [2][M][r] from the unrounded dG, dU,
-// with its scaled hi / lo columns in split (NULL: not written).
+// with its scaled hi / lo columns in split (NULL: not written; fp16: with row_scale).
 size_t gated_join_ws_bytes(int64_t M, int64_t n, int r);
 hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_t* dH, int64_t M, int64_t n,
                              const uint16_t* Bg, const uint16_t* Bu, int r, float scale, uint16_t* D, float* P,
-                             uint16_t* split, void* ws, hipStream_t stream, bool f16);
+                             uint16_t* split, float* row_scale, void* ws, hipStream_t stream, bool f16);
 // dBg = scale dG^T T[0], dBu = scale dU^T T[1] (either may be NULL) from T's
 // parts, dG and dU unrounded; finished by launch_grad_reduce(job).
 size_t gated_db_ws_bytes(int64_t M, int64_t n, int r);
@@ -289,10 +300,11 @@ hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16
                            uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16, int W = 1);
 // out = RN16([act | split] [f | fx]^T); f's scale byte of (output block,
 // contraction block) at ob * fs_o + cb * fs_c. nn: f is [kc, nout up to 128].
-// part: gemm_fp8_ws_bytes().
+// part: gemm_fp8_ws_bytes(). fp16 with kx > 0: row_scale as launch_scaled_columns'.
 bool gemm_fp8_offsets_fit(int64_t M, int64_t kc, int kx, int64_t nout, bool nn);
 size_t gemm_fp8_ws_bytes(int64_t M, int64_t kc, int64_t nout);
 hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int64_t kc, const uint16_t* split, int kx,
+                           const float* row_scale,
                            const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
                            const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16,
                            bool nn);

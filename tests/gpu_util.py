@@ -83,3 +83,15 @@ def assert_grad(name, got, ref):
     """fp32 adapter gradient (or T) against the oracle: relative Frobenius
     error <= GTOL."""
     assert report(name, f32(got), ref, floor=False) <= GTOL
+
+
+def sum8_error(P, Q):
+    """Largest error of an 8-bit matrix product P Q (the values, any sign) beyond fp32 sums, element by element. The
+    matrix instruction aligns the products of 8 consecutive contraction elements at 2^-13 of the largest and cuts
+    the rest off (measured: 2^16 + 2^3 is exact, of 2^16 + 2^2 the 2^2 is lost; products of different groups of 8 add
+    in fp32), so each of the other 7 loses less than 2^-13 of it."""
+    P, Q = np.abs(np.asarray(P)), np.abs(np.asarray(Q))
+    E = np.zeros((P.shape[0], Q.shape[1]))
+    for i in range(0, P.shape[1], 8):
+        E += np.max([np.outer(P[:, c], Q[c]) for c in range(i, min(i + 8, P.shape[1]))], axis=0)
+    return 7 * 2.0 ** -13 * E

@@ -10,9 +10,11 @@ import torch
 
 from bit_nf4_quantized_02_amd import synth
 from oracle import fp8 as o8
+from oracle import linear as olin
 from oracle import mlp as omlp
 
-from gpu_util import f32, say
+from gpu_util import assert_grad, check_elementwise, f32, say, sum8_error
+from test_gpu_gated import _check_bwd, _check_fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +106,57 @@ def test_fp8_layer_adapter_gradients(q, m, n, k, r, dy, u, x, b):
     _, dAr, _ = o8.linear_bwd(_f64(X), np.zeros((n, k)), _f64(A), _f64(B), s, _f64(dY))
     _ranks("dA", dA, dAr, s * np.linalg.norm(_product_error(_f64(dY), _f64(B)).T @ np.abs(_f64(X)), axis=1))
     _ranks("dB", dB.T, s * (_f64(dY).T @ _f64(T)).T)
+
+
+# std of the weight, of A and of B: T and P far past 65504, and of a size where their low parts would be subnormal
+LOWRANK = [(0.03, 8e3, 5e-5), (0.03, 1e-4, 3e3), (1e-3, 1e-6, 3e3), (1e-3, 3e3, 1e-6)]
+
+
+@pytest.mark.parametrize("m,n,k,r", [(300, 1030, 1088, 12), (40, 200, 320, 128), (17, 64, 64, 1), (600, 96, 2048, 20)])
+@pytest.mark.parametrize("w,a,b", LOWRANK)
+def test_gated_low_rank_term(q, m, n, k, r, w, a, b):
+    """H, G, U and dX where s T or s P leaves fp16's range, or is small beside a large factor: the element-wise bounds
+    of the ordinary cases."""
+    say(f"case: fp16 gated M={m} N={n} K={k} r={r}, W {w} A {a} B {b}")
+    s = 0.5
+    wg, wu = (q.quantize_nf4(_normal((n, k), w, 62, i).bfloat16()) for i in range(2))
+    Ag, Au = (_normal((r, k), a, 62, 2 + i) for i in range(2))
+    Bg, Bu = (_normal((n, r), b, 62, 4 + i) for i in range(2))
+    X, dH = _normal((m, k), 1.0, 62, 6), _normal((m, n), 1.0, 62, 7)
+    X[0], dH[-1] = 0, 0                                # rows without a largest value
+    block = (wg, wu, Ag, Bg, Au, Bu)
+    out = q.gated_fwd(wg, wu, X, Ag, Bg, Au, Bu, s)
+    assert all(torch.isfinite(t).all() for t in out[1:])
+    if not torch.isfinite(out[0]).all():               # (G U may leave the range by itself)
+        assert float((out[1].double() * torch.sigmoid(out[1].double()) * out[2].double()).abs().max()) > 65000
+        return
+    _check_fwd(q, block, X, s, out, HF)
+    G, U = _normal((m, n), 1.0, 62, 8), _normal((m, n), 1.0, 62, 9)
+    back = q.gated_bwd(wg, wu, X, out[3], G, U, dH, Ag, Bg, Au, Bu, s)
+    assert torch.isfinite(back[0]).all()
+    _check_bwd(q, block, X, G, U, dH, s, back, HF)
+
+
+@pytest.mark.parametrize("m,n,k,r", [(300, 1030, 1088, 12), (40, 200, 320, 128), (17, 64, 64, 1), (600, 96, 2048, 20)])
+@pytest.mark.parametrize("w,a,b", LOWRANK)
+def test_fp8_layer_low_rank_term(q, m, n, k, r, w, a, b):
+    say(f"case: fp16 8-bit layer M={m} N={n} K={k} r={r}, W {w} A {a} B {b}")
+    s = 0.5
+    wt = q.quantize_fp8(_normal((n, k), w, 63, 0).float())
+    X, dY, A, B = _normal((m, k), 1.0, 63, 1), _normal((m, n), 1.0, 63, 2), _normal((r, k), a, 63, 3), _normal((n, r), b, 63, 4)
+    X[0], dY[-1] = 0, 0
+    Y, T = q.fp8_linear_fwd(wt, X, A, B, s)
+    dX, _, _ = q.fp8_linear_bwd(wt, X, T, dY, A, B, s)
+    W8 = o8.weight_values(wt.codes.cpu().numpy(), wt.scale.cpu().numpy(), n, k)
+    Xo, dYo, Ao, Bo = (_f64(t) for t in (X, dY, A, B))
+    Yr, Tr = o8.linear_fwd(Xo, W8, Ao, Bo, s)
+    dXr = o8.linear_bwd(Xo, W8, Ao, Bo, s, dYo)[0]
+    aX, aY = (np.abs(o8.rows_values(*o8.encode_rows(t), t.shape[1])) for t in (Xo, dYo))
+    ly, lx = (np.abs(Xo) @ np.abs(Ao).T) @ np.abs(Bo).T, (np.abs(dYo) @ np.abs(Bo)) @ np.abs(Ao)
+    assert torch.isfinite(Y).all() and torch.isfinite(dX).all()
+    aW = np.abs(W8)
+    bY = olin._bound(Yr, aX @ aW.T, ly, s, k, "fp16", 256) + sum8_error(aX, aW.T)
+    bX = olin._bound(dXr, aY @ aW, lx, s, n, "fp16", 256) + sum8_error(aY, aW)
+    assert check_elementwise("Y", f32(Y), Yr, bY) == 0
+    assert check_elementwise("dX", f32(dX), dXr, bX) == 0
+    assert_grad("T", T, Tr)
