@@ -115,10 +115,18 @@ __device__ __forceinline__ float fast_sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
 }
 
-// dg = dh u (sg + silu (1 - sg)), du = dh silu, silu = g sg
+// dg = dh u (sg + silu (1 - sg)), du = dh silu, silu = g sg. In fp16 a finite G
+// may have been saved as an infinity: silu is 0 at the lower one (not -inf 0),
+// its derivative 0 and 1.
+template <bool kF16>
 __device__ __forceinline__ void join_bwd(float g, float u, float dh, float& dg, float& du) {
-  const float sg = fast_sigmoid(g), si = g * sg;
-  dg = dh * u * fmaf(si, 1.0f - sg, sg);
+  const float sg = fast_sigmoid(g), rest = 1.0f - sg;
+  float si = g * sg, bend = si;
+  if constexpr (kF16) {
+    if (sg == 0.0f) si = bend = 0.0f;
+    if (rest == 0.0f) bend = 0.0f;
+  }
+  dg = dh * u * fmaf(bend, rest, sg);
   du = dh * si;
 }
 
@@ -129,7 +137,7 @@ __device__ __forceinline__ void join8(const u32x4& g, const u32x4& u, const u32x
   for (int w = 0; w < 4; ++w)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      join_bwd(from16<kF16>((g[w] >> (16 * h)) & 0xFFFFu), from16<kF16>((u[w] >> (16 * h)) & 0xFFFFu),
+      join_bwd<kF16>(from16<kF16>((g[w] >> (16 * h)) & 0xFFFFu), from16<kF16>((u[w] >> (16 * h)) & 0xFFFFu),
                from16<kF16>((dh[w] >> (16 * h)) & 0xFFFFu), dg[2 * w + h], du[2 * w + h]);
 }
 

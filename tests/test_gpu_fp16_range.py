@@ -160,3 +160,36 @@ def test_fp8_layer_low_rank_term(q, m, n, k, r, w, a, b):
     assert check_elementwise("Y", f32(Y), Yr, bY) == 0
     assert check_elementwise("dX", f32(dX), dXr, bX) == 0
     assert_grad("T", T, Tr)
+
+
+def test_gates_saved_as_infinities(q):
+    """A pre-activation below -65520 is saved as -inf in fp16 and above 65520 as inf: H comes from the fp32 value, and
+    the gradients are the definition's at the limits, silu -> 0 and silu' -> 0 or 1. Before: NaN in the whole row of
+    dX and in every adapter gradient."""
+    m, n, k, r, s = 40, 200, 192, 8, 0.5
+    w = q.quantize_nf4(_normal((n, k), 0.03, 64, 0).bfloat16())
+    X, dH = _normal((m, k), 1.0, 64, 1), _normal((m, n), 1.0, 64, 2)
+    G, U = _normal((m, n), 1.0, 64, 3), _normal((m, n), 1.0, 64, 4)
+    A, B = _normal((r, k), k ** -0.5, 64, 5), _normal((n, r), 0.05, 64, 6)
+    G[3, ::7], G[20] = -np.inf, -np.inf
+    lim = G.clone()
+    lim[G == -np.inf] = -60000                     # sigma is 0 there
+    T = torch.stack([X.float() @ A.float().T] * 2)
+    out = q.gated_bwd(w, w, X, T, G, U, dH, A, B, A, B, s)
+    want = q.gated_bwd(w, w, X, T, lim, U, dH, A, B, A, B, s)
+    assert all(torch.isfinite(t).all() and torch.equal(t, v) for t, v in zip(out, want))
+    G[5, 11] = np.inf                              # silu' = 1: dG = dH U; dU is infinite
+    lim[5, 11] = 60000                             # (sigma is 1 there)
+    out = q.gated_bwd(w, w, X, T, G, U, dH, A, B, A, B, s, need_dX=False)
+    want = q.gated_bwd(w, w, X, T, lim, U, dH, A, B, A, B, s, need_dX=False)
+    assert torch.equal(out[1], want[1]) and torch.equal(out[2], want[2])
+    # the forward that saves them
+    x = torch.zeros(20, 64, dtype=HF, device="cuda")
+    x[:, 0] = 60000.0
+    eye = q.quantize_nf4((torch.eye(64, device="cuda") * -4).bfloat16())
+    for rows in (16, 20):
+        H, Gs, Us, _ = q.gated_fwd(eye, eye, x[:rows].contiguous(), None, None, None, None, 1.0)
+        assert torch.isinf(Gs[:, 0]).all() and not H.any()
+        dX = q.gated_bwd(eye, eye, x[:rows].contiguous(), None, Gs, torch.ones_like(Us), torch.ones_like(H), None, None,
+                         None, None, 1.0)[0]
+        assert torch.isfinite(dX).all() and not dX[:, 0].any()
