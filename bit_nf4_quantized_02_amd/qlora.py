@@ -538,6 +538,8 @@ def _adapters(n, k, A_gate, B_gate, A_up, B_up, dt, dev) -> int:
     r = 0 if A_gate is None else A_gate.shape[0]
     if (A_gate is None) != (A_up is None):
         raise ValueError("both adapters or neither")
+    if A_gate is None and not (B_gate is None and B_up is None):
+        raise ValueError("A_gate and A_up: missing for the B given")
     if r:
         for t, shape, name in ((A_gate, (r, k), "A_gate"), (A_up, (r, k), "A_up"), (B_gate, (n, r), "B_gate"),
                                (B_up, (n, r), "B_up")):
@@ -672,11 +674,17 @@ def fp8_linear_workspace_bytes(M: int, n: int, k: int, r: int, is_bwd: bool) -> 
     return int(_lib.qlora_fp8_linear_workspace_bytes(M, n, k, r, int(bool(is_bwd))))
 
 
-def _adapter8(w: FP8Weight, A: torch.Tensor, B: torch.Tensor | None, r: int, dt, dev) -> None:
-    if B is None:
-        raise ValueError("B: missing")
-    _given(A, dt, (r, w.k), "A", dev)
-    _given(B, dt, (w.n, r), "B", dev)
+def _adapter8(w: FP8Weight, A: torch.Tensor | None, B: torch.Tensor | None, dt, dev) -> int:
+    """The layer's rank; both factors or neither."""
+    r = 0 if A is None else A.shape[0]
+    if A is None and B is not None:
+        raise ValueError("A: missing for the B given")
+    if r:
+        if B is None:
+            raise ValueError("B: missing")
+        _given(A, dt, (r, w.k), "A", dev)
+        _given(B, dt, (w.n, r), "B", dev)
+    return r
 
 
 def fp8_linear_fwd(w: FP8Weight, X: torch.Tensor, A: torch.Tensor | None, B: torch.Tensor | None, scale: float,
@@ -686,11 +694,9 @@ def fp8_linear_fwd(w: FP8Weight, X: torch.Tensor, A: torch.Tensor | None, B: tor
     (qlora_fp8_linear_fwd); bf16 or fp16, as X.  Returns (Y, T)."""
     st = w.struct()
     M, dt, dev = X.shape[0], X.dtype, w.codes.device
-    r = 0 if A is None else A.shape[0]
     _is_f16(dt)
     _given(X, dt, (M, w.k), "X", dev)
-    if r:
-        _adapter8(w, A, B, r, dt, dev)
+    r = _adapter8(w, A, B, dt, dev)
     with _on(stream, dev):
         Y = _out(Y, True, dt, (M, w.n), "Y", dev)
         T = _out(T, save_T and r > 0, torch.float32, (M, r), "T", dev)
@@ -711,12 +717,11 @@ def fp8_linear_bwd(w: FP8Weight, X: torch.Tensor | None, T: torch.Tensor | None,
     (qlora_fp8_linear_bwd).  Returns (dX, dA, dB)."""
     st = w.struct()
     M, dt, dev = dY.shape[0], dY.dtype, w.codes.device
-    r = 0 if A is None else A.shape[0]
     _is_f16(dt)
     _given(dY, dt, (M, w.n), "dY", dev)
     _given(X, dt, (M, w.k), "X", dev)
+    r = _adapter8(w, A, B, dt, dev)
     if r:
-        _adapter8(w, A, B, r, dt, dev)
         _given(T, torch.float32, (M, r), "T", dev)
     with _on(stream, dev):
         dX = _out(dX, need_dX, dt, (M, w.k), "dX", dev)
