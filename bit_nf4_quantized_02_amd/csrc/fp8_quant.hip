@@ -207,6 +207,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
       // may still be in flight)
       gt::step_barrier<4>();
       copy_q(kn, next);
+      __builtin_amdgcn_sched_barrier(0);  // (copies before loads: the next barrier's wait counts the operations after them)
     }
     load(kn, nx);
     __builtin_amdgcn_sched_barrier(0);
@@ -277,6 +278,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
   const int kb0 = kFew ? b0 + wave : b0;
   if (kb0 < b1) {
     if constexpr (!kFew) copy_q(kb0, fac0);
+    __builtin_amdgcn_sched_barrier(0);
     load(kb0, x0);
   }
   for (int kb = kb0; kb < b1; kb += 2 * kStep) {

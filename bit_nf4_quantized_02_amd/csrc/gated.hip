@@ -229,6 +229,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
     if constexpr (kTiles > 0) gt::step_barrier<4>();
     const int64_t cn = c + 64 < cend ? c + 64 : c;
     copy_factors(cn, next);
+    __builtin_amdgcn_sched_barrier(0);  // (copies before loads: the next barrier's wait counts the operations after them)
     load(cn, nxt);
     __builtin_amdgcn_sched_barrier(0);
     float x[2][2][8];  // [row half][w]
@@ -300,6 +301,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void gated_join_kernel(
   };
   Stage s0, s1;
   copy_factors(cbeg, fac0);
+  __builtin_amdgcn_sched_barrier(0);
   load(cbeg, s0);
   for (int64_t c = cbeg; c < cend; c += 128) {
     step(c, fac0, fac1, s0, s1);
