@@ -194,10 +194,15 @@ hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* x
 #define QLORA_GV8(KT, H)                                                                                          \
   gemv_fp8_kernel<KT, H><<<(unsigned)cdiv(w.n, (int64_t)(16 * KT)), 64 * kGvWaves, 0, stream>>>(                   \
       w.codes, w.scale, w.n, f8_pad(w.k), reinterpret_cast<const u32x4*>(xq), xs, M, T, parts, B, r, scale, Y, T_save)
-  // Two tiles per workgroup where that still gives every CU one and at most one
-  // (8192 x 28672: 45 us against 51 with one tile); more rows run one tile, two
-  // or three workgroups per CU (28672 x 8192 at 16 tokens: 62 us against 65).
-  if (w.n >= 8192 && w.n < 16384) {
+  // One tile of rows takes 57 KB of LDS (two workgroups on a CU), two tiles 106
+  // (one). Two where that gives a CU at most one workgroup and one tile would give
+  // some CUs two (4097 to 8192 rows): every CU then reads alone and to the end.
+  // One token, encode included, one against two tiles: 4200 x 28672 46 and 38 us,
+  // 8192 x 28672 55 and 50, 7168 x 4096 13.0 and 12.1, 8192 x 8192 18.3 and 18.9.
+  // Fewer rows leave CUs idle with two tiles (4096 x 28672 31 and 40 us), more
+  // start a second round of them (8200 x 8192 20 and 22, 11008 x 8192 25 and 27).
+  constexpr int64_t kCus = 256;
+  if (w.n > 16 * kCus && w.n <= 32 * kCus) {
     if (f16) QLORA_GV8(2, true); else QLORA_GV8(2, false);
   } else {
     if (f16) QLORA_GV8(1, true); else QLORA_GV8(1, false);
