@@ -15,7 +15,8 @@
 // Loaded in operand order they cost a cache access per lane: 52 us for 8192 x
 // 28672 at one token.
 // Partial sums of the waves are added in wave order through LDS, the low-rank
-// term is added in fp32, and Y is rounded once.
+// term is added in fp32, and Y is rounded once. What a sum of 8 products holds
+// inside the instruction is said in fp8.h.
 #include "fp8.h"
 #include "kernels.h"
 
