@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256) void fp8_encode_kernel(const void* __restrict_
 __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scale, int64_t n, int64_t k,
                                                          int64_t kp, uint16_t* __restrict__ out) {
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t q = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   const int64_t per = k / 16;
   if (q >= n * per) return;
   const int64_t r = q / per, c = (q % per) * 16;
@@ -329,8 +329,10 @@ hipError_t launch_fp8_encode(const void* W, int dt, int64_t n, int64_t k, uint8_
 }
 
 hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream) {
-  const int64_t q = w.n * (w.k / 16);
-  fp8_decode_kernel<<<(unsigned)cdiv(q, (int64_t)256), 256, 0, stream>>>(w.codes, w.scale, w.n, w.k, f8_pad(w.k), out);
+  // (a grid has less than 2^32 threads along one dimension: 2^36 elements at 16 each)
+  const int64_t blocks = cdiv(w.n * (w.k / 16), (int64_t)256), y = cdiv(blocks, (int64_t)1 << 23);
+  const dim3 grid((unsigned)cdiv(blocks, y), (unsigned)y);
+  fp8_decode_kernel<<<grid, 256, 0, stream>>>(w.codes, w.scale, w.n, w.k, f8_pad(w.k), out);
   return hipGetLastError();
 }
 

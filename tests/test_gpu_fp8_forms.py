@@ -76,3 +76,23 @@ def test_sums_of_one_sign(q, m, n, k, dt):
         e = sum8_error(P, Q) + olin._gamma(P.shape[1] // 8 + 16) * ref
         assert check_elementwise(name, f32(got), ref, e + u * (ref + e)) == 0
         say(f"  {name}: mean (got - ref) / ref {float((f32(got) / ref - 1).mean()):.2e}")
+
+
+def test_decode_of_more_elements_than_one_grid_dimension(q):
+    """2^36 elements (64 GiB of codes, 128 GiB of values): the last rows and the first, the rest not looked at."""
+    n, k = 1 << 22, 16384
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 210 << 30:
+        pytest.skip("needs 200 GiB of free device memory")
+    say(f"case: fp8 decode {n}x{k}")
+    w = q.FP8Weight.empty(n, k)
+    w.scale.fill_(127)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    at = torch.tensor([0, 1, 255, n // 2, n - 128, n - 1], device="cuda")
+    codes = torch.randint(0, 127, (at.numel(), k), generator=g, device="cuda", dtype=torch.uint8)
+    w.codes[at] = codes
+    v = q.dequant_fp8(w)[at].double().cpu().numpy()
+    del w
+    torch.cuda.empty_cache()
+    assert (v == o8.table()[codes.cpu().numpy()]).all()
