@@ -527,6 +527,15 @@ def _out(t: torch.Tensor | None, want: bool, dtype, shape, name, device, zeros: 
     return t
 
 
+def _workspace(ws: torch.Tensor | None, nbytes: int, device) -> torch.Tensor | None:
+    """The call's workspace: the caller's, on its device and whole (its size is the call's check), or a new one."""
+    if ws is None:
+        return _bytes(nbytes, device)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected contiguous on {device}, got contiguous={ws.is_contiguous()} on {ws.device}")
+    return ws
+
+
 # --------------------------------------------------------------------------- gated feed-forward block
 
 def gated_workspace_bytes(M: int, n: int, k: int, r: int, is_bwd: bool) -> int:
@@ -568,8 +577,7 @@ def gated_fwd(w_gate: NF4Weight, w_up: NF4Weight, X: torch.Tensor, A_gate: torch
         G = _out(G, save, dt, (M, n), "G", dev)
         U = _out(U, save, dt, (M, n), "U", dev)
         T = _out(T, save and r > 0, torch.float32, (2, M, r), "T", dev)
-        if ws is None:
-            ws = _bytes(gated_workspace_bytes(M, n, k, r, False), dev)
+        ws = _workspace(ws, gated_workspace_bytes(M, n, k, r, False) if ws is None else 0, dev)
         _check(_lib.qlora_gated_fwd(ctypes.byref(sg), ctypes.byref(su), _ptr(X), M, _DT[dt], _ptr(A_gate), _ptr(B_gate),
                                     _ptr(A_up), _ptr(B_up), r, float(scale), _ptr(H), _ptr(G), _ptr(U), _ptr(T),
                                     _ptr(ws), 0 if ws is None else ws.nbytes, _stream(stream)), "qlora_gated_fwd")
@@ -602,8 +610,7 @@ def gated_bwd(w_gate: NF4Weight, w_up: NF4Weight, X: torch.Tensor | None, T: tor
         dB_gate = _out(dB_gate, b, f32, (n, r), "dB_gate", dev, zeros=accumulate)
         dA_up = _out(dA_up, a, f32, (r, k), "dA_up", dev, zeros=accumulate)
         dB_up = _out(dB_up, b, f32, (n, r), "dB_up", dev, zeros=accumulate)
-        if ws is None:
-            ws = _bytes(gated_workspace_bytes(M, n, k, r, True), dev)
+        ws = _workspace(ws, gated_workspace_bytes(M, n, k, r, True) if ws is None else 0, dev)
         _check(_lib.qlora_gated_bwd(ctypes.byref(sg), ctypes.byref(su), _ptr(X), _ptr(T), _ptr(G), _ptr(U), _ptr(dH), M,
                                     _DT[dt], _ptr(A_gate), _ptr(B_gate), _ptr(A_up), _ptr(B_up), r, float(scale),
                                     _ptr(dX), _ptr(dA_gate), _ptr(dB_gate), _ptr(dA_up), _ptr(dB_up),
@@ -700,8 +707,7 @@ def fp8_linear_fwd(w: FP8Weight, X: torch.Tensor, A: torch.Tensor | None, B: tor
     with _on(stream, dev):
         Y = _out(Y, True, dt, (M, w.n), "Y", dev)
         T = _out(T, save_T and r > 0, torch.float32, (M, r), "T", dev)
-        if ws is None:
-            ws = _bytes(fp8_linear_workspace_bytes(M, w.n, w.k, r, False), dev)
+        ws = _workspace(ws, fp8_linear_workspace_bytes(M, w.n, w.k, r, False) if ws is None else 0, dev)
         _check(_lib.qlora_fp8_linear_fwd(ctypes.byref(st), _ptr(X), M, _DT[dt], _ptr(A), _ptr(B), r, float(scale),
                                          _ptr(Y), _ptr(T), _ptr(ws), 0 if ws is None else ws.nbytes, _stream(stream)),
                "qlora_fp8_linear_fwd")
@@ -727,8 +733,7 @@ def fp8_linear_bwd(w: FP8Weight, X: torch.Tensor | None, T: torch.Tensor | None,
         dX = _out(dX, need_dX, dt, (M, w.k), "dX", dev)
         dA = _out(dA, r > 0 and need_dA, torch.float32, (r, w.k), "dA", dev, zeros=accumulate)
         dB = _out(dB, r > 0 and need_dB, torch.float32, (w.n, r), "dB", dev, zeros=accumulate)
-        if ws is None:
-            ws = _bytes(fp8_linear_workspace_bytes(M, w.n, w.k, r, True), dev)
+        ws = _workspace(ws, fp8_linear_workspace_bytes(M, w.n, w.k, r, True) if ws is None else 0, dev)
         _check(_lib.qlora_fp8_linear_bwd(ctypes.byref(st), _ptr(X), _ptr(T), _ptr(dY), M, _DT[dt], _ptr(A), _ptr(B), r,
                                          float(scale), _ptr(dX), _ptr(dA), _ptr(dB), int(bool(accumulate)), _ptr(ws),
                                          0 if ws is None else ws.nbytes, _stream(stream)), "qlora_fp8_linear_bwd")

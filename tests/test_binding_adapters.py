@@ -40,3 +40,32 @@ def test_calls_with_half_an_adapter():
             q.gated_fwd(w4, w4, X, *lr, 1.0)
         with pytest.raises(ValueError):
             q.gated_bwd(w4, w4, X, None, dY, dY, dY, *lr, 1.0)
+
+
+def test_workspace_of_another_device():
+    cpu, meta = torch.device("cpu"), torch.device("meta")
+    ws = torch.empty(256, dtype=torch.uint8)
+    assert q._workspace(ws, 0, cpu) is ws and q._workspace(None, 0, cpu) is None
+    assert q._workspace(None, 100, cpu).nbytes == 100
+    for bad, dev in ((ws, meta), (ws[::2], cpu)):
+        with pytest.raises(ValueError, match="ws"):
+            q._workspace(bad, 0, dev)
+
+
+@pytest.mark.gpu
+def test_calls_with_a_workspace_in_host_memory():
+    m, n, k = 20, 96, 128
+    z = lambda *s: torch.zeros(s, dtype=BF, device="cuda")  # noqa: E731
+    X, dY, ws = z(m, k), z(m, n), torch.empty(1 << 24, dtype=torch.uint8)
+    w8, w4 = q.quantize_fp8(torch.ones(n, k, device="cuda")), q.quantize_nf4(torch.ones(n, k, device="cuda"))
+    with pytest.raises(ValueError, match="ws"):
+        q.fp8_linear_fwd(w8, X, None, None, 1.0, ws=ws)
+    with pytest.raises(ValueError, match="ws"):
+        q.fp8_linear_bwd(w8, X, None, dY, None, None, 1.0, ws=ws)
+    with pytest.raises(ValueError, match="ws"):
+        q.gated_fwd(w4, w4, X, None, None, None, None, 1.0, ws=ws)
+    with pytest.raises(ValueError, match="ws"):
+        q.gated_bwd(w4, w4, X, None, dY, dY, dY, None, None, None, None, 1.0, ws=ws)
+    own = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    assert torch.equal(q.fp8_linear_fwd(w8, X, None, None, 1.0, ws=own)[0], dY)
+    assert torch.equal(q.gated_fwd(w4, w4, X, None, None, None, None, 1.0, ws=own)[0], dY)
