@@ -54,7 +54,7 @@ size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
   const int xc = gated_extra_cols(r);
   if (r > 0) o.proj = cv.take<char>(gated_project_ws_bytes(M, k, r));
   if (r > 0) o.TS = cv.take<uint16_t>((size_t)M * xc * 2);
-  if (r > 0) o.rs = cv.take<float>(row_scale_bytes(M));
+  if (r > 0) o.rs = cv.take<float>(row_scale_bytes(M, 2));
   o.F = cv.take<uint16_t>(gated_fwd_operand_bytes(n, k, r));
   o.part = cv.take<float>(gemm_bf16_ws_bytes(M, k, xc, gated_rows(n)));
   return cv.used;

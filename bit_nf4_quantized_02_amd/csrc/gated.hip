@@ -365,15 +365,15 @@ __global__ __launch_bounds__(256) void gated_p_kernel(const float* __restrict__ 
 __global__ __launch_bounds__(256) void scaled_columns_kernel(const float* __restrict__ part, int splits, int W, int64_t M,
                                                              int r, int xc, float scale, float* __restrict__ out,
                                                              uint16_t* __restrict__ split,
-                                                             float* __restrict__ row_scale) {
+                                                             float* __restrict__ row_scale, bool apart) {
 #pragma clang fp contract(off)
   const int lane = threadIdx.x & 63;
   const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (m >= M) return;
   const int count = W * r;
-  const int64_t pitch = (int64_t)W * M * r;
+  const int64_t pitch = (int64_t)W * M * r, pad = (M + 255) / 256 * 256;
   float v[4];
-  uint32_t top = 0;
+  uint32_t top[2] = {0, 0};  // of each factor
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int i = lane + 64 * e;
@@ -392,23 +392,30 @@ __global__ __launch_bounds__(256) void scaled_columns_kernel(const float* __rest
     if (out) out[at] = s;
     v[e] = scale * s;
     asm("" : "+v"(v[e]));  // one value for the maximum and both conversions
-    top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    const uint32_t a = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+    top[0] = max(top[0], i < r ? a : 0u);
+    top[1] = max(top[1], i < r ? 0u : a);
   }
   if (split == nullptr) return;
+  if (!apart) top[0] = top[1] = max(top[0], top[1]);
+  float down[2];
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  // largest value 1.x 2^(b - 127): e = b - 141, kept where 2^e and 2^-e are normal numbers
-  // (a row with a value that is not finite, or of zeros, stays as it is)
-  int e2 = (int)(top >> 23) - 141;
-  e2 = top == 0 || top >= 0x7F800000u ? 0 : e2 < -112 ? -112 : e2;
-  const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-  if (lane == 0) row_scale[m] = __uint_as_float((uint32_t)(127 + e2) << 23);
+  for (int w = 0; w < 2; ++w) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) top[w] = max(top[w], (uint32_t)__shfl_xor((int)top[w], d));
+    // largest value 1.x 2^(b - 127): e = b - 141, kept where 2^e and 2^-e are normal numbers
+    // (a row with a value that is not finite, or of zeros, stays as it is)
+    int e2 = (int)(top[w] >> 23) - 141;
+    e2 = top[w] == 0 || top[w] >= 0x7F800000u ? 0 : e2 < -112 ? -112 : e2;
+    down[w] = __uint_as_float((uint32_t)(127 - e2) << 23);
+    if (lane == 0 && (w == 0 || apart)) row_scale[w * pad + m] = __uint_as_float((uint32_t)(127 + e2) << 23);
+  }
   uint16_t* const row = split + m * xc;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int i = lane + 64 * e;
     if (i >= count) continue;
-    float x = v[e] * down;
+    float x = v[e] * (i < r ? down[0] : down[1]);
     asm("" : "+v"(x));
     const uint16_t hi = to16<true>(x);
     const int c = i / r * 2 * r + i % r;
@@ -627,9 +634,9 @@ hipError_t launch_gated_expand_dx(const Nf4View& g, const Nf4View& u, const uint
 namespace {
 
 hipError_t launch_p(const float* part, int splits, int64_t M, int r, float scale, float* P, uint16_t* split,
-                    float* row_scale, hipStream_t stream, bool f16) {
+                    float* row_scale, bool apart, hipStream_t stream, bool f16) {
   const int xc = gated_extra_cols(r);
-  if (f16) return launch_scaled_columns(part, splits, 2, M, r, xc, scale, P, split, row_scale, stream);
+  if (f16) return launch_scaled_columns(part, splits, 2, M, r, xc, scale, P, split, row_scale, stream, apart);
   const unsigned grid = (unsigned)cdiv(M * (xc - 2 * r), (int64_t)256);
   gated_p_kernel<<<grid, 256, 0, stream>>>(part, splits, M, r, xc, scale, P, split);
   return hipGetLastError();
@@ -638,10 +645,10 @@ hipError_t launch_p(const float* part, int splits, int64_t M, int r, float scale
 }  // namespace
 
 hipError_t launch_scaled_columns(const float* part, int splits, int W, int64_t M, int r, int xc, float scale, float* out,
-                                 uint16_t* split, float* row_scale, hipStream_t stream) {
-  if (W * r > 256 || (split != nullptr && row_scale == nullptr)) return hipErrorInvalidValue;
+                                 uint16_t* split, float* row_scale, hipStream_t stream, bool apart) {
+  if (W < 1 || W > 2 || W * r > 256 || (split != nullptr && row_scale == nullptr)) return hipErrorInvalidValue;
   scaled_columns_kernel<<<(unsigned)cdiv(M, (int64_t)4), 256, 0, stream>>>(part, splits, W, M, r, xc, scale, out, split,
-                                                                          row_scale);
+                                                                          row_scale, apart);
   return hipGetLastError();
 }
 
@@ -657,7 +664,8 @@ hipError_t launch_gated_project(const uint16_t* X, int64_t M, int64_t k, const u
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(2 * operand_order_bytes(f8_pad(k), r)));
   hipError_t e = launch_operand_order(Ag, Au, 0, k, f8_pad(k), r, Ao, stream);
   if (e == hipSuccess) e = launch_fp8_prep(X, M, k, Ao, r, nullptr, nullptr, part, false, stream, f16, 2);
-  if (e == hipSuccess) e = launch_p(part, fp8_prep_plan(M, k, false, 2).splits, M, r, scale, T, split, row_scale, stream, f16);
+  if (e == hipSuccess) e = launch_p(part, fp8_prep_plan(M, k, false, 2).splits, M, r, scale, T, split, row_scale,
+                                    /*apart=*/true, stream, f16);
   return e;
 }
 
@@ -695,7 +703,7 @@ hipError_t launch_gated_join(const uint16_t* G, const uint16_t* U, const uint16_
   else QLORA_JOIN(128)
 #undef QLORA_JOIN
 #undef QLORA_JOIN2
-  if (r > 0) return launch_p(part, pl.splits, M, r, scale, P, split, row_scale, stream, f16);
+  if (r > 0) return launch_p(part, pl.splits, M, r, scale, P, split, row_scale, /*apart=*/false, stream, f16);
   return hipGetLastError();
 }
 

@@ -65,7 +65,8 @@ struct BfArgs {
   uint16_t* g_out;
   uint16_t* u_out;
   int64_t hn;
-  // factor of each row of the low-rank columns (kScaled; rows up to a multiple of 256)
+  // factor of each row of the low-rank columns (kScaled; rows up to a multiple
+  // of 256; kGate: of the gate's, then of the up projection's)
   const float* row_scale;
 };
 
@@ -503,7 +504,7 @@ __global__ __launch_bounds__(kThreads) void gemm_bf16_kernel(BfArgs a) {
         mask_acc_lds(acc, As1, Bs1, a.keep_scale, a.M, a.nout, m0, n0, wm0, wn0, lane);
         __syncthreads();  // mask reads done before the main steps' copies reuse buffers 1
       } else {
-        scale_rows(acc, a.row_scale, m0 + wm0, lane);
+        scale_rows(acc, a.row_scale, kGate ? mt * kBM : 0, m0 + wm0, lane);
       }
       nk_end = nk_main;
     }

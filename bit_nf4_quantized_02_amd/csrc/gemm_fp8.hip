@@ -258,7 +258,7 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_kernel(F8Args a) {
       __syncthreads();  // every wave's reads done before the next copies land
     }
     if constexpr (kF16) {
-      if (a.kx > 0) scale_rows(acc, a.row_scale, m0 + wm0, lane);
+      if (a.kx > 0) scale_rows(acc, a.row_scale, 0, m0 + wm0, lane);
     }
   }
 

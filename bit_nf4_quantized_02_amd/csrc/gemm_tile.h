@@ -188,19 +188,20 @@ __device__ __forceinline__ void store_half(uint16_t* reg, uint16_t* out, int64_t
 }
 
 // Accumulators times a factor of each row (rows past M: any value), while they
-// hold only the low-rank term of fp16 columns that were scaled by row.
-__device__ __forceinline__ void scale_rows(f32x16 (&acc)[kTM][kTN], const float* __restrict__ row_scale, int64_t m0,
-                                           int lane) {
+// hold only the low-rank term of fp16 columns that were scaled by row; column
+// block j's factors lie `pitch` after those of the one before.
+__device__ __forceinline__ void scale_rows(f32x16 (&acc)[kTM][kTN], const float* __restrict__ row_scale, int64_t pitch,
+                                           int64_t m0, int lane) {
 #pragma unroll
   for (int i = 0; i < kTM; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f32x4 s = *reinterpret_cast<const f32x4*>(row_scale + m0 + i * 32 + 8 * q + 4 * (lane >> 5));
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int j = 0; j < kTN; ++j)
+      for (int j = 0; j < kTN; ++j) {
+        const f32x4 s = *reinterpret_cast<const f32x4*>(row_scale + j * pitch + m0 + i * 32 + 8 * q + 4 * (lane >> 5));
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][j][4 * q + v] *= s[v];
-    }
+      }
 }
 
 // Dropout on the low-rank term of a tile: while the accumulators hold only

@@ -235,11 +235,14 @@ inline int gated_extra_cols(int r) { return r > 0 ? ((4 * r + 63) / 64) * 64 : 0
 // fp16: low-rank columns from partials [splits][W][M][r] added in order. out
 // (NULL: not written) takes the sums [W][M][r]; split (NULL: not written) row m's
 // columns [hi_0 | lo_0 | hi_1 | .. | 0] (xc in all) of scale * sums times 2^-e,
-// and row_scale[m] 2^e, with e so that the row's largest value lies in [2^14, 2^15):
-// none leaves fp16's range, and lo's smallest step is 2^-39 of it.
-inline size_t row_scale_bytes(int64_t M) { return (size_t)((M + 255) / 256 * 256) * 4; }  // whole tiles of rows
+// and row_scale [row_scale_rows(M)] 2^e, with e so that the row's largest value
+// lies in [2^14, 2^15): none leaves fp16's range, and lo's smallest step is 2^-39
+// of it. apart: an e for each factor (row_scale [W][row_scale_rows(M)]), where
+// their products are different outputs.
+inline int64_t row_scale_rows(int64_t M) { return (M + 255) / 256 * 256; }  // whole tiles of rows
+inline size_t row_scale_bytes(int64_t M, int W = 1) { return (size_t)row_scale_rows(M) * W * 4; }
 hipError_t launch_scaled_columns(const float* part, int splits, int W, int64_t M, int r, int xc, float scale, float* out,
-                                 uint16_t* split, float* row_scale, hipStream_t stream);
+                                 uint16_t* split, float* row_scale, hipStream_t stream, bool apart = false);
 // X Ag^T and X Au^T: T (NULL: not written) as [2][M][r], and the scaled
 // columns in split (NULL: not written; fp16: with row_scale).
 size_t gated_project_ws_bytes(int64_t M, int64_t k, int r);

@@ -137,6 +137,20 @@ def test_gated_low_rank_term(q, m, n, k, r, w, a, b):
     _check_bwd(q, block, X, G, U, dH, s, back, HF)
 
 
+@pytest.mark.parametrize("big", ["gate", "up"])
+@pytest.mark.parametrize("m,n,k,r", [(300, 1030, 1088, 12), (40, 200, 320, 128), (4, 200, 320, 8)])
+def test_gated_low_rank_terms_of_different_size(q, m, n, k, r, big):
+    """One projection's T is 10^10 times the other's: G and U are different outputs, each as exact as alone."""
+    say(f"case: fp16 gated M={m} N={n} K={k} r={r}, {big} large")
+    s = 0.5
+    wg, wu = (q.quantize_nf4(_normal((n, k), 1e-3, 65, i).bfloat16()) for i in range(2))
+    lr = {"large": (_normal((r, k), 8e3, 65, 2), _normal((n, r), 1e-6, 65, 3)),
+          "small": (_normal((r, k), 1e-6, 65, 4), _normal((n, r), 3e3, 65, 5))}
+    (Ag, Bg), (Au, Bu) = lr["large" if big == "gate" else "small"], lr["small" if big == "gate" else "large"]
+    X = _normal((m, k), 1.0, 65, 6)
+    _check_fwd(q, (wg, wu, Ag, Bg, Au, Bu), X, s, q.gated_fwd(wg, wu, X, Ag, Bg, Au, Bu, s), HF)
+
+
 @pytest.mark.parametrize("m,n,k,r", [(300, 1030, 1088, 12), (40, 200, 320, 128), (17, 64, 64, 1), (600, 96, 2048, 20)])
 @pytest.mark.parametrize("w,a,b", LOWRANK)
 def test_fp8_layer_low_rank_term(q, m, n, k, r, w, a, b):
