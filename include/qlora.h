@@ -321,7 +321,11 @@ qlora_status qlora_linear_bwd_f16(const qlora_nf4_weight *w, const void *X, cons
  * RN16(G) and U_save = RN16(U), all [M, n], in bf16 or fp16 per dtype (w' in
  * the same type). T_save (nullable): [2, M, r] fp32, Tg then Tu. For M <= 16
  * one pass over both weights' codes; above, both are expanded into ws and
- * multiplied by one GEMM whose epilogue is the join.
+ * multiplied by one GEMM whose epilogue is the join, T entering as 16-bit hi and
+ * lo parts of scale * T (16 bits of each value in bf16; in fp16 22 bits of the
+ * row's largest, scaled exactly, so that T may be of any size).
+ * In fp16 G, U and H beyond 65504 are saved as infinities, as in any fp16
+ * arithmetic; H itself is formed from the fp32 values.
  * ws (device) holds qlora_gated_workspace_bytes(M, n, k, r, 0) bytes.
  * Errors: INVALID_ARG (also dtype fp32, and weights of different storage
  * forms), SHAPE (weights of different shapes, k % 64, a size above 2^22, the
@@ -340,7 +344,13 @@ qlora_status qlora_gated_fwd(const qlora_nf4_weight *w_gate, const qlora_nf4_wei
  *   dX = RN16( RN16(dG) Wg' + RN16(dU) Wu' + scale (Pg Ag + Pu Au) )
  *   dA_gate = scale Pg^T X,  dB_gate = scale dG^T Tg, and the same for up
  * Each output may be NULL; the two halves of dX are one product with one
- * rounding. The adapter gradients (fp32) come from the unrounded dG and dU.
+ * rounding. dX's operands RN16(dG) and RN16(dU) have the range of the type (in
+ * fp16: infinite above 65504, steps of 2^-24 below 2^-14: the caller scales the
+ * loss); P enters dX as T the forward. The adapter gradients (fp32) come from
+ * the unrounded dG and dU and hold fp32's accuracy and range in both types.
+ * silu' is taken at the saved G, at its limits where that is infinite in fp16;
+ * the sigmoid there is the hardware's 2^x and reciprocal (a relative 2^-24 |G|
+ * where it is small).
  * T_saved ([2, M, r], nullable: recomputed from X), accumulate, M = 0 and r =
  * 0 as in qlora_linear_bwd; X is needed as there. Reruns are bit-identical.
  * ws (device) holds qlora_gated_workspace_bytes(M, n, k, r, 1) bytes.
@@ -424,7 +434,9 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight *w, const void *X, int6
  *   dX = RN16( dY8 W8 + scale * U A )   if dX != NULL
  *   dA = scale * U^T X, dB = scale * dY^T T   (fp32, if not NULL)
  * dY8: the values dY is encoded to, per 128 columns of a row (inside the
- * call); its products are added as the forward's. U, dA and dB use dY itself. The straight-through gradient of the
+ * call); its products are added as the forward's. U, dA and dB use dY itself,
+ * and dA and dB hold fp32's accuracy and range in both types (an fp16 factor
+ * below 2^-14 enters U and T in steps of 2^-38 of the other). The straight-through gradient of the
  * forward: rounding X to X8 is passed through. T_saved, accumulate, M = 0 and
  * r = 0 as in qlora_linear_bwd. Reruns are bit-identical.
  * ws (device) holds qlora_fp8_linear_workspace_bytes(M, n, k, r, 1) bytes.
