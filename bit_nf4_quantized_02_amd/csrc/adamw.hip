@@ -17,25 +17,10 @@
 // in place over the host link, which then bounds the step.
 #include <cmath>
 
-#include "common.h"
-#include "qlora.h"
+#include "adamw.h"
 
 namespace qlora {
 namespace {
-
-struct AdamwC {
-  float b1, b2, omb1, omb2, lr, eps, wd, bc1, bc2;
-};
-
-__device__ __forceinline__ void adamw_one(float& th, float g, float& m, float& v, const AdamwC& c) {
-#pragma clang fp contract(off)
-  m = c.b1 * m + c.omb1 * g;
-  v = c.b2 * v + c.omb2 * (g * g);
-  const float mhat = m / c.bc1;
-  const float vhat = v / c.bc2;
-  const float u = mhat / (sqrtf(vhat) + c.eps) + c.wd * th;
-  th = th - c.lr * u;
-}
 
 // Four elements per thread (16-byte accesses when every array is 16-byte
 // aligned), grid-stride; the last count % 4 elements one per thread.
@@ -73,9 +58,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(float* __restrict__ theta, u
   }
 }
 
-// Device address of an optimizer-state buffer: device memory as is, pinned
-// host memory through its device mapping; anything else (pageable host
-// memory, unknown pointers) is rejected.
+}  // namespace
+
 bool state_ptr(float* p, float** dev) {
   hipPointerAttribute_t a;
   if (hipPointerGetAttributes(&a, p) != hipSuccess) {
@@ -101,24 +85,10 @@ bool state_ptr(float* p, float** dev) {
   return false;
 }
 
-}  // namespace
-}  // namespace qlora
-
-extern "C" qlora_status qlora_adamw_step(float* theta, uint16_t* theta16, const float* grad, float* m, float* v,
-                                         int64_t count, int64_t step, float lr, float beta1, float beta2, float eps,
-                                         float weight_decay, void* stream) {
-  using namespace qlora;
-  if (count < 0 || step < 1) return QLORA_ERR_SHAPE;
-  if (count == 0) return QLORA_OK;
-  if (!theta || !grad || !m || !v) return QLORA_ERR_INVALID_ARG;
+bool adamw_constants(int64_t step, float lr, float beta1, float beta2, float eps, float weight_decay, AdamwC& c) {
   if (!(beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f && eps >= 0.0f && lr >= 0.0f &&
         weight_decay >= 0.0f))
-    return QLORA_ERR_INVALID_ARG;
-  const auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  if (!al16(theta) || !al16(grad) || !al16(m) || !al16(v) || (theta16 && !al16(theta16))) return QLORA_ERR_INVALID_ARG;
-  float *md = nullptr, *vd = nullptr;
-  if (!state_ptr(m, &md) || !state_ptr(v, &vd)) return QLORA_ERR_INVALID_ARG;
-  AdamwC c;
+    return false;
   c.b1 = beta1;
   c.b2 = beta2;
   c.omb1 = (float)(1.0 - (double)beta1);
@@ -128,7 +98,24 @@ extern "C" qlora_status qlora_adamw_step(float* theta, uint16_t* theta16, const 
   c.wd = weight_decay;
   c.bc1 = (float)(1.0 - std::pow((double)beta1, (double)step));
   c.bc2 = (float)(1.0 - std::pow((double)beta2, (double)step));
-  if (!(c.bc1 > 0.0f) || !(c.bc2 > 0.0f)) return QLORA_ERR_INVALID_ARG;
+  return c.bc1 > 0.0f && c.bc2 > 0.0f;
+}
+
+}  // namespace qlora
+
+extern "C" qlora_status qlora_adamw_step(float* theta, uint16_t* theta16, const float* grad, float* m, float* v,
+                                         int64_t count, int64_t step, float lr, float beta1, float beta2, float eps,
+                                         float weight_decay, void* stream) {
+  using namespace qlora;
+  if (count < 0 || step < 1) return QLORA_ERR_SHAPE;
+  if (count == 0) return QLORA_OK;
+  if (!theta || !grad || !m || !v) return QLORA_ERR_INVALID_ARG;
+  AdamwC c;
+  if (!adamw_constants(step, lr, beta1, beta2, eps, weight_decay, c)) return QLORA_ERR_INVALID_ARG;
+  const auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  if (!al16(theta) || !al16(grad) || !al16(m) || !al16(v) || (theta16 && !al16(theta16))) return QLORA_ERR_INVALID_ARG;
+  float *md = nullptr, *vd = nullptr;
+  if (!state_ptr(m, &md) || !state_ptr(v, &vd)) return QLORA_ERR_INVALID_ARG;
   int64_t blocks = (count / 4 + 255) / 256;
   if (blocks < 1) blocks = 1;
   if (blocks > 4096) blocks = 4096;

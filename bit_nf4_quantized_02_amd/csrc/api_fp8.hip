@@ -46,15 +46,16 @@ struct FwdWs {
 // small kernel adds them before it otherwise (a launch, about 4 us).
 bool gemv_adds(int64_t M, int64_t k, int r) { return (int64_t)fp8_prep_plan(M, k, M <= 16).splits * M * r * 4 <= 16384; }
 
-size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, FwdWs& o) {
+// rows: the activations come encoded (qlora_fp8_rows).
+size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, bool rows, Carver& cv, FwdWs& o) {
   o.proj = cv.take<float>((size_t)fp8_prep_plan(M, k, M <= 16).splits * M * r * 4);
   if (M <= 16) {
-    o.xq = cv.take<uint8_t>(fp8_gemv_codes_bytes(k));
-    o.xs = cv.take<uint8_t>(fp8_gemv_scale_bytes(k));
+    if (!rows) o.xq = cv.take<uint8_t>(fp8_gemv_codes_bytes(k));
+    if (!rows) o.xs = cv.take<uint8_t>(fp8_gemv_scale_bytes(k));
     o.T = cv.take<float>((size_t)M * r * 4);
     return cv.used;
   }
-  o.xq = cv.take<uint8_t>((size_t)M * f8_pad(k));
+  if (!rows) o.xq = cv.take<uint8_t>((size_t)M * f8_pad(k));
   o.xs = cv.take<uint8_t>(fp8_rows_scale_bytes(M, k));
   if (r > 0) {
     o.TS = cv.take<uint16_t>((size_t)M * lora_extra_cols(r) * 2);
@@ -106,6 +107,55 @@ size_t bwd_ws(int64_t M, int64_t n, int64_t k, int r, Carver& cv, BwdWs& o) {
 
 bool is16(int dtype) { return dtype == QLORA_DT_BF16 || dtype == QLORA_DT_FP16; }
 
+// The forward; x8: the activations' codes and scales, or NULL where X is encoded here.
+qlora_status fwd_impl(const qlora_fp8_weight* w, const qlora_fp8_rows* x8, const void* X, int64_t M, int dtype,
+                      const void* A, const void* B, int r, float scale, void* Y, float* T_save, void* ws, size_t ws_bytes,
+                      void* stream) {
+  const bool rows = x8 != nullptr;
+  const int64_t n = w->n, k = w->k;
+  if (!is16(dtype)) return QLORA_ERR_INVALID_ARG;
+  if (!dims_ok(M, n, k, r) || !fwd_fits(M, n, k, r)) return QLORA_ERR_SHAPE;
+  if (M == 0) return QLORA_OK;
+  if (((!rows || r > 0) && !good(X)) || !good(Y) || (r > 0 && (!good(A) || !good(B))) || (T_save && !aligned16(T_save)))
+    return QLORA_ERR_INVALID_ARG;
+  if (rows && (!good(x8->codes) || !good(x8->scale))) return QLORA_ERR_INVALID_ARG;
+  Carver size(nullptr), cv(ws);
+  FwdWs o;
+  const size_t need = fwd_ws(M, n, k, r, rows, size, o);
+  if (need > 0 && (!good(ws) || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
+  fwd_ws(M, n, k, r, rows, cv, o);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool f16 = dtype == QLORA_DT_FP16;
+  const uint16_t *x = static_cast<const uint16_t*>(X), *a = static_cast<const uint16_t*>(A),
+                 *b = static_cast<const uint16_t*>(B);
+  const bool few = M <= 16;
+  const int parts = fp8_prep_plan(M, k, few).splits;
+  hipError_t e = hipSuccess;
+  if (r > 0 && !few) e = launch_factors(a, 0, k, f8_pad(k), r, o.Ao, b, n, o.Bx, st);
+  if (e == hipSuccess && (!rows || r > 0)) e = launch_fp8_prep(x, M, k, few ? a : o.Ao, r, o.xq, o.xs, o.proj, few, st, f16);
+  const uint8_t *const xq = rows ? x8->codes : o.xq, *const xs = rows ? x8->scale : o.xs;
+  if (few) {
+    if (r > 0 && !gemv_adds(M, k, r)) {
+      float* const T = T_save ? T_save : o.T;
+      if (e == hipSuccess) e = launch_rowdot_finalize(o.proj, parts, M, r, T, nullptr, scale, st, f16);
+      if (e == hipSuccess)
+        e = launch_fp8_gemv(view8(w), xq, xs, rows, M, T, 1, b, r, scale, static_cast<uint16_t*>(Y), nullptr, st, f16);
+    } else if (e == hipSuccess) {
+      e = launch_fp8_gemv(view8(w), xq, xs, rows, M, o.proj, parts, b, r, scale, static_cast<uint16_t*>(Y), T_save, st, f16);
+    }
+    return hip_status(e);
+  }
+  const int64_t nb = f8_pad(k) / kF8Block;
+  if (rows && e == hipSuccess) e = launch_fp8_scale_words(xs, M, nb, o.xs, st);
+  if (r > 0 && e == hipSuccess)
+    e = f16 ? launch_scaled_columns(o.proj, parts, 1, M, r, lora_extra_cols(r), scale, T_save, o.TS, o.rs, st)
+            : launch_rowdot_finalize(o.proj, parts, M, r, T_save, o.TS, scale, st, false);
+  if (e == hipSuccess)
+    e = launch_gemm_fp8(xq, o.xs, M, k, o.TS, lora_extra_cols(r), o.rs, w->codes, w->scale, nb, 1,
+                        (f8_pad(n) / kF8Block) * nb, o.Bx, n, static_cast<uint16_t*>(Y), o.part, st, f16, false);
+  return hip_status(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -139,7 +189,7 @@ size_t qlora_fp8_linear_workspace_bytes(int64_t M, int64_t n, int64_t k, int r, 
     return bwd_ws(M, n, k, r, cv, o);
   }
   FwdWs o;
-  return fwd_ws(M, n, k, r, cv, o);
+  return fwd_ws(M, n, k, r, false, cv, o);
 }
 
 qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int64_t M, int dtype, const void* A,
@@ -147,44 +197,38 @@ qlora_status qlora_fp8_linear_fwd(const qlora_fp8_weight* w, const void* X, int6
                                   void* stream) {
   const qlora_status s = check_fp8(w);
   if (s != QLORA_OK) return s;
-  const int64_t n = w->n, k = w->k;
-  if (!is16(dtype)) return QLORA_ERR_INVALID_ARG;
-  if (!dims_ok(M, n, k, r) || !fwd_fits(M, n, k, r)) return QLORA_ERR_SHAPE;
-  if (M == 0) return QLORA_OK;
-  if (!good(X) || !good(Y) || (r > 0 && (!good(A) || !good(B))) || (T_save && !aligned16(T_save)))
-    return QLORA_ERR_INVALID_ARG;
-  if (!good(ws) || ws_bytes < qlora_fp8_linear_workspace_bytes(M, n, k, r, 0)) return QLORA_ERR_WORKSPACE;
-  Carver cv(ws);
+  return fwd_impl(w, nullptr, X, M, dtype, A, B, r, scale, Y, T_save, ws, ws_bytes, stream);
+}
+
+size_t qlora_fp8_rows_bytes(int64_t M, int64_t k) {
+  if (M < 1 || k < 1 || k % QLORA_BLOCK) return 0;
+  return (size_t)(M * f8_pad(k) + M * (f8_pad(k) / kF8Block));
+}
+
+qlora_status qlora_dequant_fp8_rows(const qlora_fp8_rows* x, int dtype, void* out, void* stream) {
+  if (x == nullptr || !is16(dtype)) return QLORA_ERR_INVALID_ARG;
+  if (x->M < 0 || x->M > kMaxDim || x->k < 1 || x->k > kMaxDim || x->k % QLORA_BLOCK) return QLORA_ERR_SHAPE;
+  if (x->M == 0) return QLORA_OK;
+  if (!good(x->codes) || !good(x->scale) || !good(out)) return QLORA_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_decode_rows(x->codes, x->scale, x->M, x->k, static_cast<uint16_t*>(out),
+                                           static_cast<hipStream_t>(stream), dtype == QLORA_DT_FP16));
+}
+
+size_t qlora_fp8_linear_rows_workspace_bytes(int64_t M, int64_t n, int64_t k, int r) {
+  if (M < 1 || !dims_ok(M, n, k, r)) return 0;
+  Carver cv(nullptr);
   FwdWs o;
-  fwd_ws(M, n, k, r, cv, o);
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  const bool f16 = dtype == QLORA_DT_FP16;
-  const uint16_t *x = static_cast<const uint16_t*>(X), *a = static_cast<const uint16_t*>(A),
-                 *b = static_cast<const uint16_t*>(B);
-  const bool few = M <= 16;
-  const int parts = fp8_prep_plan(M, k, few).splits;
-  hipError_t e = hipSuccess;
-  if (r > 0 && !few) e = launch_factors(a, 0, k, f8_pad(k), r, o.Ao, b, n, o.Bx, st);
-  if (e == hipSuccess) e = launch_fp8_prep(x, M, k, few ? a : o.Ao, r, o.xq, o.xs, o.proj, few, st, f16);
-  if (few) {
-    if (r > 0 && !gemv_adds(M, k, r)) {
-      float* const T = T_save ? T_save : o.T;
-      if (e == hipSuccess) e = launch_rowdot_finalize(o.proj, parts, M, r, T, nullptr, scale, st, f16);
-      if (e == hipSuccess)
-        e = launch_fp8_gemv(view8(w), o.xq, o.xs, M, T, 1, b, r, scale, static_cast<uint16_t*>(Y), nullptr, st, f16);
-    } else if (e == hipSuccess) {
-      e = launch_fp8_gemv(view8(w), o.xq, o.xs, M, o.proj, parts, b, r, scale, static_cast<uint16_t*>(Y), T_save, st, f16);
-    }
-    return hip_status(e);
-  }
-  const int64_t nb = f8_pad(k) / kF8Block;
-  if (r > 0 && e == hipSuccess)
-    e = f16 ? launch_scaled_columns(o.proj, parts, 1, M, r, lora_extra_cols(r), scale, T_save, o.TS, o.rs, st)
-            : launch_rowdot_finalize(o.proj, parts, M, r, T_save, o.TS, scale, st, false);
-  if (e == hipSuccess)
-    e = launch_gemm_fp8(o.xq, o.xs, M, k, o.TS, lora_extra_cols(r), o.rs, w->codes, w->scale, nb, 1,
-                        (f8_pad(n) / kF8Block) * nb, o.Bx, n, static_cast<uint16_t*>(Y), o.part, st, f16, false);
-  return hip_status(e);
+  return fwd_ws(M, n, k, r, true, cv, o);
+}
+
+qlora_status qlora_fp8_linear_fwd_rows(const qlora_fp8_weight* w, const qlora_fp8_rows* x8, const void* X, int dtype,
+                                       const void* A, const void* B, int r, float scale, void* Y, float* T_save,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  const qlora_status s = check_fp8(w);
+  if (s != QLORA_OK) return s;
+  if (x8 == nullptr) return QLORA_ERR_INVALID_ARG;
+  if (x8->k != w->k) return QLORA_ERR_SHAPE;
+  return fwd_impl(w, x8, X, x8->M, dtype, A, B, r, scale, Y, T_save, ws, ws_bytes, stream);
 }
 
 qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight* w, const void* X, const float* T_saved, const void* dY,

@@ -85,8 +85,10 @@ __global__ __launch_bounds__(256) void fp8_encode_kernel(const void* __restrict_
   }
 }
 
-// out = RN_bf16(value * scale): 16 codes per thread. Exact wherever bf16
-// holds the product (all but the smallest scales).
+// out = RN16(value * scale): 16 codes per thread. Exact wherever the 16 bits
+// hold the product (in bf16 all but the smallest scales). kRows: a scale for
+// each row (activations) instead of each 128.
+template <bool kRows, bool kF16>
 __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scale, int64_t n, int64_t k,
                                                          int64_t kp, uint16_t* __restrict__ out) {
@@ -95,13 +97,13 @@ __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restri
   if (q >= n * per) return;
   const int64_t r = q / per, c = (q % per) * 16;
   const u32x4 v = *reinterpret_cast<const u32x4*>(codes + r * kp + c);
-  const int e = (int)scale[(r / kF8Block) * (kp / kF8Block) + c / kF8Block] - 127;
+  const int e = (int)scale[(kRows ? r : r / kF8Block) * (kp / kF8Block) + c / kF8Block] - 127;
   u32x4 o[2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[i], true);
-    o[i >> 1][2 * (i & 1)] = pack_bf16x2(ldexpf(lo[0], e), ldexpf(lo[1], e));
-    o[i >> 1][2 * (i & 1) + 1] = pack_bf16x2(ldexpf(hi[0], e), ldexpf(hi[1], e));
+    o[i >> 1][2 * (i & 1)] = pack2<kF16>(ldexpf(lo[0], e), ldexpf(lo[1], e));
+    o[i >> 1][2 * (i & 1) + 1] = pack2<kF16>(ldexpf(hi[0], e), ldexpf(hi[1], e));
   }
   u32x4* const p = reinterpret_cast<u32x4*>(out + r * k + c);
   p[0] = o[0];
@@ -328,11 +330,48 @@ hipError_t launch_fp8_encode(const void* W, int dt, int64_t n, int64_t k, uint8_
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream) {
+namespace {
+
+template <bool kRows, bool kF16>
+hipError_t decode(const uint8_t* codes, const uint8_t* scale, int64_t n, int64_t k, uint16_t* out, hipStream_t stream) {
   // (a grid has less than 2^32 threads along one dimension: 2^36 elements at 16 each)
-  const int64_t blocks = cdiv(w.n * (w.k / 16), (int64_t)256), y = cdiv(blocks, (int64_t)1 << 23);
+  const int64_t blocks = cdiv(n * (k / 16), (int64_t)256), y = cdiv(blocks, (int64_t)1 << 23);
   const dim3 grid((unsigned)cdiv(blocks, y), (unsigned)y);
-  fp8_decode_kernel<<<grid, 256, 0, stream>>>(w.codes, w.scale, w.n, w.k, f8_pad(w.k), out);
+  fp8_decode_kernel<kRows, kF16><<<grid, 256, 0, stream>>>(codes, scale, n, k, f8_pad(k), out);
+  return hipGetLastError();
+}
+
+// One lane a word: the scale bytes of rows +0, +32, +64, +96 of a 128-row tile
+// (rows from M on: the last, what is theirs is not stored).
+__global__ __launch_bounds__(256) void fp8_scale_words_kernel(const uint8_t* __restrict__ scale, int64_t M, int64_t nb,
+                                                              uint32_t* __restrict__ words) {
+  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, mt = cdiv(M, (int64_t)kF8Block);
+  if (q >= nb * mt * 32) return;
+  const int64_t row = q / nb, kb = q % nb, tile = row / 32, r = row % 32;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = tile * kF8Block + r + 32 * i;
+    w |= (uint32_t)scale[(m < M ? m : M - 1) * nb + kb] << (8 * i);
+  }
+  words[(kb * mt + tile) * 32 + r] = w;
+}
+
+}  // namespace
+
+hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream) {
+  return decode<false, false>(w.codes, w.scale, w.n, w.k, out, stream);
+}
+
+hipError_t launch_fp8_decode_rows(const uint8_t* codes, const uint8_t* scale, int64_t M, int64_t k, uint16_t* out,
+                                  hipStream_t stream, bool f16) {
+  return f16 ? decode<true, true>(codes, scale, M, k, out, stream) : decode<true, false>(codes, scale, M, k, out, stream);
+}
+
+hipError_t launch_fp8_scale_words(const uint8_t* scale, int64_t M, int64_t nb, uint8_t* words, hipStream_t stream) {
+  const int64_t count = nb * cdiv(M, (int64_t)kF8Block) * 32;
+  fp8_scale_words_kernel<<<(unsigned)cdiv(count, (int64_t)256), 256, 0, stream>>>(scale, M, nb,
+                                                                                 reinterpret_cast<uint32_t*>(words));
   return hipGetLastError();
 }
 

@@ -42,10 +42,13 @@ struct Block {
   uint32_t xs, ws;
 };
 
-template <int kT, bool kF16>
+// kRows: the activations as codes [M, kp] and scales [M, kp / 128] of each row
+// (the lanes of a row's 128 columns read one line of it; rows from M on repeat
+// the last, their sums are not stored) instead of operand order.
+template <int kT, bool kF16, bool kRows>
 __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* __restrict__ codes,
                                                                  const uint8_t* __restrict__ wscale, int64_t N,
-                                                                 int64_t kp, const u32x4* __restrict__ Xq,
+                                                                 int64_t kp, const uint8_t* __restrict__ Xq,
                                                                  const uint8_t* __restrict__ Xs, int64_t M,
                                                                  const float* __restrict__ T, int parts,
                                                                  const uint16_t* __restrict__ B, int r, float scale,
@@ -67,8 +70,11 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
   // this workgroup's rows (those past N read as zero and are not stored)
   const i32x4 wr = make_rsrc(codes + n0 * kp, rows * kp);
   const i32x4 sr = make_rsrc(wscale + (n0 / kF8Block) * nb, nb);
-  const i32x4 xr = make_rsrc(Xq, (int64_t)nb * 2048);
-  const i32x4 xsr = make_rsrc(Xs, (int64_t)nb * 16);
+  const i32x4 xr = make_rsrc(Xq, kRows ? M * kp : (int64_t)nb * 2048);
+  const i32x4 xsr = make_rsrc(Xs, kRows ? M * nb : (int64_t)nb * 16);
+  const int xm = (lane & 15) < M ? (lane & 15) : (int)M - 1;
+  const int xoff = kRows ? (int)(xm * kp) + 32 * (lane >> 4) : lane * 32;
+  const int xsoff = kRows ? xm * nb : lane & 15;
   // copy h of tile i: lane l fills row 8 h + l / 8, position l % 8
   uint32_t woff[kT][2];
 #pragma unroll
@@ -89,8 +95,8 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
 #pragma unroll
       for (int h = 0; h < 2; ++h) copy16(wr, woff[i][h], kb * kF8Block, dst + i * 2048 + h * 1024);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) b.x[h] = raw_buffer_load_b128(xr, lane * 32 + 16 * h, kb * 2048, 0);
-    b.xs = raw_buffer_load_u8(xsr, lane & 15, kb * 16, 0);
+    for (int h = 0; h < 2; ++h) b.x[h] = raw_buffer_load_b128(xr, xoff + 16 * h, kb * (kRows ? kF8Block : 2048), 0);
+    b.xs = raw_buffer_load_u8(xsr, xsoff, kb * (kRows ? 1 : 16), 0);
     b.ws = raw_buffer_load_u8(sr, 0, kb, 0);
   };
   f32x4 acc[kT];
@@ -189,12 +195,14 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
 size_t fp8_gemv_codes_bytes(int64_t k) { return (size_t)(f8_pad(k) / kF8Block) * 2048; }
 size_t fp8_gemv_scale_bytes(int64_t k) { return (size_t)(f8_pad(k) / kF8Block) * 16; }
 
-hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* xs, int64_t M, const float* T, int parts,
-                           const uint16_t* B, int r, float scale, uint16_t* Y, float* T_save, hipStream_t stream,
-                           bool f16) {
-#define QLORA_GV8(KT, H)                                                                                          \
-  gemv_fp8_kernel<KT, H><<<(unsigned)cdiv(w.n, (int64_t)(16 * KT)), 64 * kGvWaves, 0, stream>>>(                   \
-      w.codes, w.scale, w.n, f8_pad(w.k), reinterpret_cast<const u32x4*>(xq), xs, M, T, parts, B, r, scale, Y, T_save)
+hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* xs, bool rows, int64_t M, const float* T,
+                           int parts, const uint16_t* B, int r, float scale, uint16_t* Y, float* T_save,
+                           hipStream_t stream, bool f16) {
+  if (M < 1 || M > 16) return hipErrorInvalidValue;
+#define QLORA_GV8R(KT, H, R)                                                                                      \
+  gemv_fp8_kernel<KT, H, R><<<(unsigned)cdiv(w.n, (int64_t)(16 * KT)), 64 * kGvWaves, 0, stream>>>(                \
+      w.codes, w.scale, w.n, f8_pad(w.k), xq, xs, M, T, parts, B, r, scale, Y, T_save)
+#define QLORA_GV8(KT, H) { if (rows) QLORA_GV8R(KT, H, true); else QLORA_GV8R(KT, H, false); }
   // One tile of rows takes 57 KB of LDS (two workgroups on a CU), two tiles 106
   // (one). Two where that gives a CU at most one workgroup and one tile would give
   // some CUs two (4097 to 8192 rows): every CU then reads alone and to the end.
@@ -204,11 +212,12 @@ hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* x
   // start a second round of them (8200 x 8192 20 and 22, 11008 x 8192 25 and 27).
   constexpr int64_t kCus = 256;
   if (w.n > 16 * kCus && w.n <= 32 * kCus) {
-    if (f16) QLORA_GV8(2, true); else QLORA_GV8(2, false);
+    if (f16) QLORA_GV8(2, true) else QLORA_GV8(2, false)
   } else {
-    if (f16) QLORA_GV8(1, true); else QLORA_GV8(1, false);
+    if (f16) QLORA_GV8(1, true) else QLORA_GV8(1, false)
   }
 #undef QLORA_GV8
+#undef QLORA_GV8R
   return hipGetLastError();
 }
 

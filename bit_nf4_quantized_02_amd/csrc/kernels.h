@@ -311,14 +311,31 @@ hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int
                            const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
                            const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16,
                            bool nn);
-// M <= 16: Y = RN16(X8 W8^T + scale T B^T) from launch_fp8_prep's operands; T
+// M <= 16: Y = RN16(X8 W8^T + scale T B^T) from launch_fp8_prep's operands, or
+// (rows) from codes [M, k up to 128] and scales [M, blocks] of each row; T
 // as `parts` partials [parts][M][r] that the kernel adds in order, written to
 // T_save if it is not NULL.
 size_t fp8_gemv_codes_bytes(int64_t k);
 size_t fp8_gemv_scale_bytes(int64_t k);
-hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* xs, int64_t M, const float* T, int parts,
-                           const uint16_t* B, int r, float scale, uint16_t* Y, float* T_save, hipStream_t stream,
-                           bool f16);
+hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* xs, bool rows, int64_t M, const float* T,
+                           int parts, const uint16_t* B, int r, float scale, uint16_t* Y, float* T_save,
+                           hipStream_t stream, bool f16);
+// Activations encoded by row (qlora_fp8_rows): their values in 16 bits, and
+// their scales [M, nb] as the GEMM's scale words.
+hipError_t launch_fp8_decode_rows(const uint8_t* codes, const uint8_t* scale, int64_t M, int64_t k, uint16_t* out,
+                                  hipStream_t stream, bool f16);
+hipError_t launch_fp8_scale_words(const uint8_t* scale, int64_t M, int64_t nb, uint8_t* words, hipStream_t stream);
+
+// ---- residual addition and root-mean-square norm (rmsnorm.hip)
+// R (with H) may be NULL, as may Y, rstd and codes (with scale; k % 64 == 0).
+hipError_t launch_rms_fwd(const uint16_t* X, const uint16_t* R, const void* w, bool w32, int64_t M, int64_t k, float eps,
+                          uint16_t* Y, uint16_t* H, float* rstd, uint8_t* codes, uint8_t* scale, hipStream_t stream,
+                          bool f16);
+// R, dX and dw may be NULL; part: rms_bwd_ws_bytes(M, k), for dw.
+size_t rms_bwd_ws_bytes(int64_t M, int64_t k);
+hipError_t launch_rms_bwd(const uint16_t* dY, const uint16_t* H, const float* rstd, const void* w, bool w32,
+                          const uint16_t* R, int64_t M, int64_t k, uint16_t* dX, float* dw, int accumulate, float* part,
+                          hipStream_t stream, bool f16);
 
 hipError_t launch_silu_fwd(const uint16_t* G, const uint16_t* U, uint16_t* H, int64_t count,
                            hipStream_t stream);

@@ -48,11 +48,27 @@ class _Weight8(ctypes.Structure):
     _fields_ = [("n", _i64), ("k", _i64), ("codes", _vp), ("scale", _vp)]
 
 
+class _Rows8(ctypes.Structure):
+    _fields_ = [("M", _i64), ("k", _i64), ("codes", _vp), ("scale", _vp)]
+
+
+class _Param(ctypes.Structure):
+    _fields_ = [("theta", _vp), ("theta16", _vp), ("grad", _vp), ("m", _vp), ("v", _vp), ("count", _i64),
+                ("grad_dtype", ctypes.c_int32), ("dtype16", ctypes.c_int32)]
+
+
+class _Table(ctypes.Structure):
+    _fields_ = [("chunks", _vp), ("n_chunks", _i64), ("elements", _i64), ("complete", ctypes.c_int32)]
+
+
 SCALE_FP32, SCALE_DQ, SCALE_BF16 = 0, 1, 2
 
 
 _W = ctypes.POINTER(_Weight)
 _W8 = ctypes.POINTER(_Weight8)
+_R8 = ctypes.POINTER(_Rows8)
+_P = ctypes.POINTER(_Param)
+_T = ctypes.POINTER(_Table)
 
 _SIGS = {
     "qlora_status_string": (ctypes.c_char_p, [_int]),
@@ -113,6 +129,18 @@ _SIGS = {
     "qlora_fp8_linear_fwd": (_int, [_W8, _vp, _i64, _int, _vp, _vp, _int, _f, _vp, _vp, _vp, _sz, _vp]),
     "qlora_fp8_linear_bwd": (_int, [_W8, _vp, _vp, _vp, _i64, _int, _vp, _vp, _int, _f, _vp, _vp, _vp, _int, _vp, _sz,
                                      _vp]),
+    "qlora_fp8_rows_bytes": (_sz, [_i64, _i64]),
+    "qlora_dequant_fp8_rows": (_int, [_R8, _int, _vp, _vp]),
+    "qlora_fp8_linear_rows_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "qlora_fp8_linear_fwd_rows": (_int, [_W8, _R8, _vp, _int, _vp, _vp, _int, _f, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_rms_norm_fwd": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _int, _f, _vp, _vp, _vp, _R8, _vp]),
+    "qlora_rms_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "qlora_rms_norm_bwd": (_int, [_vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _int, _vp, _vp, _int, _vp, _sz, _vp]),
+    "qlora_param_table_bytes": (_sz, [_P, _i64]),
+    "qlora_param_table_build": (_int, [_P, _i64, _vp, _sz, _T]),
+    "qlora_grad_norm_workspace_bytes": (_sz, []),
+    "qlora_grad_norm": (_int, [_T, _f, _f, _vp, _vp, _sz, _vp]),
+    "qlora_adamw_step_many": (_int, [_T, _vp, _f, _i64, _f, _f, _f, _f, _f, _vp]),
     "qlora_calib_mfma": (_int, [_int, _int, _vp, _vp]),
     "qlora_calib_stream_read": (_int, [_vp, _i64, _vp, _vp]),
 }
@@ -740,6 +768,146 @@ def fp8_linear_bwd(w: FP8Weight, X: torch.Tensor | None, T: torch.Tensor | None,
     return dX, dA, dB
 
 
+# --------------------------------------------------------------------------- 8-bit activations
+
+@dataclass
+class FP8Rows:
+    """Device buffers of activations in the 8-bit layer's format (owned by these tensors)."""
+    M: int
+    k: int
+    codes: torch.Tensor      # uint8 E4M3 patterns [M, k up to a multiple of 128]
+    scale: torch.Tensor      # uint8 exponent bytes [M, ceil(k / 128)]
+
+    @staticmethod
+    def empty(M: int, k: int, device="cuda") -> "FP8Rows":
+        kb = -(-k // FP8_BLOCK)
+        return FP8Rows(M, k, torch.empty((M, kb * FP8_BLOCK), dtype=torch.uint8, device=device),
+                       torch.empty((M, kb), dtype=torch.uint8, device=device))
+
+    def struct(self) -> _Rows8:
+        kb = -(-self.k // FP8_BLOCK)
+        _need(self.codes, torch.uint8, (self.M, kb * FP8_BLOCK), "codes")
+        _given(self.scale, torch.uint8, (self.M, kb), "scale", self.codes.device)
+        return self._struct()
+
+    def _struct(self) -> _Rows8:
+        return _Rows8(self.M, self.k, self.codes.data_ptr(), self.scale.data_ptr())
+
+    def nbytes(self) -> int:
+        return int(_lib.qlora_fp8_rows_bytes(self.M, self.k))
+
+
+def dequant_fp8_rows(x8: FP8Rows, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of encoded activations, [M, k] bf16 or fp16 (qlora_dequant_fp8_rows)."""
+    _is_f16(dtype)
+    st, dev = x8.struct(), x8.codes.device
+    with _on(stream, dev):
+        out = _out(out, True, dtype, (x8.M, x8.k), "out", dev)
+        _check(_lib.qlora_dequant_fp8_rows(ctypes.byref(st), _DT[dtype], _ptr(out), _stream(stream)),
+               "qlora_dequant_fp8_rows")
+    return out
+
+
+def fp8_linear_rows_workspace_bytes(M: int, n: int, k: int, r: int) -> int:
+    return int(_lib.qlora_fp8_linear_rows_workspace_bytes(M, n, k, r))
+
+
+def fp8_linear_fwd_rows(w: FP8Weight, x8: FP8Rows, X: torch.Tensor | None, A: torch.Tensor | None,
+                        B: torch.Tensor | None, scale: float, Y: torch.Tensor | None = None,
+                        T: torch.Tensor | None = None, save_T: bool = True, ws: torch.Tensor | None = None,
+                        stream=None, dtype=torch.bfloat16):
+    """Y = X8 W8^T + scale (X A^T) B^T on activations that are encoded already
+    (qlora_fp8_linear_fwd_rows); X is for the adapter only.  dtype: that of X,
+    A, B and Y.  Returns (Y, T)."""
+    _is_f16(dtype)
+    st, sx = w.struct(), x8.struct()
+    M, dev = x8.M, w.codes.device
+    if x8.codes.device != dev:
+        raise ValueError(f"x8: on {x8.codes.device}, expected {dev}")
+    r = _adapter8(w, A, B, dtype, dev)
+    if r and X is None:
+        raise ValueError("X: missing for the adapter given")
+    _given(X, dtype, (M, w.k), "X", dev)
+    with _on(stream, dev):
+        Y = _out(Y, True, dtype, (M, w.n), "Y", dev)
+        T = _out(T, save_T and r > 0, torch.float32, (M, r), "T", dev)
+        ws = _workspace(ws, fp8_linear_rows_workspace_bytes(M, w.n, w.k, r) if ws is None else 0, dev)
+        _check(_lib.qlora_fp8_linear_fwd_rows(ctypes.byref(st), ctypes.byref(sx), _ptr(X), _DT[dtype], _ptr(A), _ptr(B), r,
+                                              float(scale), _ptr(Y), _ptr(T), _ptr(ws), 0 if ws is None else ws.nbytes,
+                                              _stream(stream)), "qlora_fp8_linear_fwd_rows")
+    return Y, T
+
+
+# --------------------------------------------------------------------------- residual addition and norm
+
+def _gain(w: torch.Tensor, dt, k: int, dev) -> int:
+    """The gain's type: the activations' or fp32."""
+    _given(w, dt if w.dtype != torch.float32 else torch.float32, (k,), "w", dev)
+    return _DT[w.dtype]
+
+
+def rms_norm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
+                 Y: torch.Tensor | None = None, H: torch.Tensor | None = None, rstd: torch.Tensor | None = None,
+                 x8: FP8Rows | None = None, want_y: bool = True, want_x8: bool = False, save: bool = True,
+                 stream=None):
+    """h = X + residual, Y = h rstd w with rstd = (mean(h^2) + eps)^-1/2 over the
+    last of X's two dimensions (qlora_rms_norm_fwd); want_x8: Y as the 8-bit
+    layer's activations (too).  Returns (Y, h, rstd, x8): h is X itself without a
+    residual (H may be `residual`, which is then updated in place), rstd is for
+    rms_norm_bwd; Y, rstd and x8 are None unless asked for or given."""
+    if X.dim() != 2:
+        raise ValueError("X must be [M, k]")
+    (M, k), dt, dev = X.shape, X.dtype, X.device
+    _is_f16(dt)
+    _need(X, dt, (M, k), "X")
+    _given(residual, dt, (M, k), "residual", dev)
+    wt = _gain(w, dt, k, dev)
+    if residual is None and H is not None:
+        raise ValueError("H: given without a residual")
+    with _on(stream, dev):
+        Y = _out(Y, want_y, dt, (M, k), "Y", dev)
+        H = _out(H, residual is not None, dt, (M, k), "H", dev)
+        rstd = _out(rstd, save, torch.float32, (M,), "rstd", dev)
+        s8 = None
+        if x8 is None and want_x8:
+            x8 = FP8Rows.empty(M, k, device=dev)
+            s8 = ctypes.byref(x8._struct())
+        elif x8 is not None:
+            if x8.codes.device != dev:
+                raise ValueError(f"x8: on {x8.codes.device}, expected {dev}")
+            s8 = ctypes.byref(x8.struct())
+        _check(_lib.qlora_rms_norm_fwd(_ptr(X), _ptr(residual), _ptr(w), wt, M, k, _DT[dt], float(eps), _ptr(Y), _ptr(H),
+                                       _ptr(rstd), s8, _stream(stream)), "qlora_rms_norm_fwd")
+    return Y, X if H is None else H, rstd, x8
+
+
+def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, w: torch.Tensor,
+                 dres: torch.Tensor | None = None, need_dX: bool = True, need_dw: bool = True,
+                 dX: torch.Tensor | None = None, dw: torch.Tensor | None = None, accumulate: bool = False,
+                 ws: torch.Tensor | None = None, stream=None):
+    """The gradients of rms_norm_fwd from its h and rstd (qlora_rms_norm_bwd): dX
+    of X and the residual alike, with dres, what reaches h past the norm, added
+    (dX may be `dres`); dw of the gain, fp32.  Returns (dX, dw)."""
+    if dY.dim() != 2:
+        raise ValueError("dY must be [M, k]")
+    (M, k), dt, dev = dY.shape, dY.dtype, dY.device
+    _is_f16(dt)
+    _need(dY, dt, (M, k), "dY")
+    _given(H, dt, (M, k), "H", dev)
+    _given(rstd, torch.float32, (M,), "rstd", dev)
+    _given(dres, dt, (M, k), "dres", dev)
+    wt = _gain(w, dt, k, dev)
+    with _on(stream, dev):
+        dX = _out(dX, need_dX, dt, (M, k), "dX", dev)
+        dw = _out(dw, need_dw, torch.float32, (k,), "dw", dev, zeros=accumulate)
+        need = int(_lib.qlora_rms_norm_bwd_workspace_bytes(M, k)) if ws is None and dw is not None else 0
+        ws = _workspace(ws, need, dev)
+        _check(_lib.qlora_rms_norm_bwd(_ptr(dY), _ptr(H), _ptr(rstd), _ptr(w), wt, _ptr(dres), M, k, _DT[dt], _ptr(dX),
+                                       _ptr(dw), int(bool(accumulate)), _ptr(ws), 0 if ws is None else ws.nbytes,
+                                       _stream(stream)), "qlora_rms_norm_bwd")
+    return dX, dw
+
+
 # --------------------------------------------------------------------------- building blocks
 
 def lowrank_split_cols(r: int) -> int:
@@ -997,6 +1165,95 @@ def adamw_step(theta: torch.Tensor, grad: torch.Tensor, m: torch.Tensor, v: torc
                                  ctypes.c_void_p(v.data_ptr()), n, int(step), float(lr), float(betas[0]),
                                  float(betas[1]), float(eps), float(weight_decay), _stream(stream)),
            "qlora_adamw_step")
+
+
+@dataclass
+class Param:
+    """One tensor of a ParamTable: its gradient and, for the step, its fp32
+    master copy, moments (on the GPU or in pinned host memory) and 16-bit copy."""
+    grad: torch.Tensor
+    theta: torch.Tensor | None = None
+    m: torch.Tensor | None = None
+    v: torch.Tensor | None = None
+    theta16: torch.Tensor | None = None
+
+    def _struct(self, dev) -> _Param:
+        g, n = self.grad, self.grad.numel()
+        if g.dtype not in _DT:
+            raise ValueError(f"grad: expected bf16, fp16 or fp32, got {g.dtype}")
+        _given(g, g.dtype, g.shape, "grad", dev)
+        given = [t is not None for t in (self.theta, self.m, self.v)]
+        if any(given) != all(given) or (self.theta16 is not None and not all(given)):
+            raise ValueError("theta, m and v: all of them, or only the gradient")
+        _given(self.theta, torch.float32, g.shape, "theta", dev)
+        for t, name in ((self.m, "m"), (self.v, "v")):
+            if t is None:
+                continue
+            if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
+                raise ValueError(f"{name}: expected contiguous fp32 with {n} elements on the GPU or in pinned host memory")
+            if t.is_cuda and t.device != dev:
+                raise ValueError(f"{name}: on {t.device}, expected {dev}")
+        dt16 = torch.bfloat16
+        if self.theta16 is not None:
+            dt16 = self.theta16.dtype
+            _is_f16(dt16)
+            _given(self.theta16, dt16, g.shape, "theta16", dev)
+        return _Param(_ptr(self.theta), _ptr(self.theta16), _ptr(g), _ptr(self.m), _ptr(self.v), n, _DT[g.dtype],
+                      _DT[dt16])
+
+
+class ParamTable:
+    """The tensors that grad_norm and adamw_step_many work on, laid out once on
+    their device (qlora_param_table_build).  It keeps the tensors alive; they are
+    the ones that are read and written as long as it is used: a step's gradients
+    go into the same buffers as the last one's."""
+
+    def __init__(self, params: list[Param], device=None):
+        if device is None:
+            device = params[0].grad.device if params else torch.device("cuda", torch.cuda.current_device())
+        self.params = list(params)
+        self.device = torch.device(device)
+        arr = (_Param * len(params))(*(p._struct(self.device) for p in params))
+        nbytes = int(_lib.qlora_param_table_bytes(arr, len(params)))
+        image = torch.empty(nbytes, dtype=torch.uint8)
+        self._table = _Table()
+        with torch.cuda.device(self.device):
+            _check(_lib.qlora_param_table_build(arr, len(params), _ptr(image), nbytes, ctypes.byref(self._table)),
+                   "qlora_param_table_build")
+            self._chunks = image.to(self.device)
+        self._table.chunks = self._chunks.data_ptr() if nbytes else None
+        self._ref = ctypes.byref(self._table)
+
+    @property
+    def elements(self) -> int:
+        return int(self._table.elements)
+
+
+def grad_norm(table: ParamTable, max_norm: float = float("inf"), grad_scale: float = 1.0,
+              out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """[norm, factor] on the device, fp32: the norm of grad_scale times all the
+    table's gradients, and what scales them to at most max_norm (NaN where a
+    gradient is not finite) (qlora_grad_norm)."""
+    dev = table.device
+    with _on(stream, dev):
+        out = _out(out, True, torch.float32, (2,), "out", dev)
+        ws = _workspace(ws, int(_lib.qlora_grad_norm_workspace_bytes()) if ws is None else 0, dev)
+        _check(_lib.qlora_grad_norm(table._ref, float(grad_scale), float(max_norm), _ptr(out), _ptr(ws), ws.nbytes,
+                                    _stream(stream)), "qlora_grad_norm")
+    return out
+
+
+def adamw_step_many(table: ParamTable, step: int, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
+                    weight_decay: float = 0.0, clip: torch.Tensor | None = None, grad_scale: float = 1.0,
+                    stream=None) -> None:
+    """In-place AdamW step of every tensor in the table, on grad_scale * clip[1]
+    times its gradient (qlora_adamw_step_many); clip is grad_norm's result."""
+    dev = table.device
+    _given(clip, torch.float32, (2,), "clip", dev)
+    with _on(stream, dev):
+        _check(_lib.qlora_adamw_step_many(table._ref, _ptr(clip), float(grad_scale), int(step), float(lr),
+                                          float(betas[0]), float(betas[1]), float(eps), float(weight_decay),
+                                          _stream(stream)), "qlora_adamw_step_many")
 
 
 def calib_mfma(blocks: int, iters: int, sink: torch.Tensor, stream=None) -> int:

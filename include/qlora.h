@@ -448,6 +448,88 @@ qlora_status qlora_fp8_linear_bwd(const qlora_fp8_weight *w, const void *X, cons
                                   int64_t M, int dtype, const void *A, const void *B, int r, float scale, void *dX,
                                   float *dA, float *dB, int accumulate, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Activations in the 8-bit layer's format: E4M3 values with a scale for every
+ * 128 consecutive values of a row, by the rules above.
+ *   codes  [M, kp] bytes, kp = k rounded up to a multiple of 128, the columns
+ *          from k on zero
+ *   scale  [M, kp / 128] exponent bytes
+ * Both (device), owned by the caller.
+ */
+typedef struct {
+  int64_t M;
+  int64_t k;
+  uint8_t *codes;
+  uint8_t *scale;
+} qlora_fp8_rows;
+
+/* Bytes of encoded activations, codes + scale (0 if k % 64 != 0 or a size is not positive). */
+size_t qlora_fp8_rows_bytes(int64_t M, int64_t k);
+
+/*
+ * The values encoded activations stand for: out (device, [M, k], bf16 or fp16
+ * per dtype), what a backward reads as X where only the codes were kept. Exact
+ * wherever the 16 bits hold value * scale, else rounded to nearest even.
+ * Errors: INVALID_ARG, SHAPE (k % 64, sizes above 2^22), HIP.
+ */
+qlora_status qlora_dequant_fp8_rows(const qlora_fp8_rows *x, int dtype, void *out, void *stream);
+
+/*
+ * qlora_fp8_linear_fwd on activations that are encoded already, by the norm
+ * below, once for all layers that read them:
+ *   Y = RN16( X8 W8^T + scale * T B^T ),  T = X A^T
+ * X8 (M and k from it; k is the weight's) replaces the encoding of X; X (device)
+ * [M, k] in 16 bits is read for the adapter only (NULL for r = 0). Where X8 is
+ * the encoding of X, Y and T are qlora_fp8_linear_fwd's, bit for bit. dtype is
+ * X's, A's, B's and Y's. The backward is qlora_fp8_linear_bwd's.
+ * ws (device) holds qlora_fp8_linear_rows_workspace_bytes(M, n, k, r) bytes
+ * (NULL where that is 0). Errors: as qlora_fp8_linear_fwd.
+ */
+size_t qlora_fp8_linear_rows_workspace_bytes(int64_t M, int64_t n, int64_t k, int r);
+qlora_status qlora_fp8_linear_fwd_rows(const qlora_fp8_weight *w, const qlora_fp8_rows *X8, const void *X, int dtype,
+                                       const void *A, const void *B, int r, float scale, void *Y, float *T_save,
+                                       void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The residual's addition with the root-mean-square norm, between the layers:
+ *   h = RN16( RN32(x + residual) )     (residual NULL: h = x)
+ *   rstd = 1 / sqrt( mean(h^2) + eps ) (fp32, over the k columns of a row)
+ *   y = RN16( h * rstd * w )           (fp32 products)
+ * X, residual (nullable), Y and H (device) [M, k] in bf16 or fp16 per dtype, w
+ * (device) [k] in w_dtype: dtype or QLORA_DT_FP32. H receives h, the stream that
+ * goes on past the norm (given exactly where residual is; it may be residual
+ * itself). Y, rstd ([M], for the backward) and X8 are written if they are not
+ * NULL. X8 receives y, as rounded to 16 bits, in the 8-bit layer's format (k % 64
+ * == 0; its padding columns are written too): the codes that qlora_fp8_linear_fwd
+ * makes of y itself. A row that holds a NaN or an infinity, or whose squares add
+ * up to more than fp32 holds, is what these formulas give for it in fp32. No
+ * other buffers may overlap.
+ * Any M up to 2^22 and k up to 2^22, M k up to 2^36 (M = 0 launches nothing).
+ * Errors: INVALID_ARG (also eps negative or not finite, H without residual or
+ * the reverse), SHAPE (sizes, X8 of another shape, k % 64 with X8), HIP.
+ */
+qlora_status qlora_rms_norm_fwd(const void *X, const void *residual, const void *w, int w_dtype, int64_t M, int64_t k,
+                                int dtype, float eps, void *Y, void *H, float *rstd, const qlora_fp8_rows *X8,
+                                void *stream);
+
+/*
+ * Its backward, from the saved h and rstd:
+ *   g = dY * w,  hn = h * rstd
+ *   dX = RN16( rstd * (g - hn * mean(g * hn)) + dres )   if dX != NULL
+ *   dw = sum over the rows of dY * hn  (fp32, [k])        if dw != NULL
+ * dX is the gradient of x and of the residual alike; dres (device, nullable, [M,
+ * k]) is the gradient that reaches h past the norm, added before the one
+ * rounding; dX may be dres itself. Encoding y to 8 bits is passed through.
+ * accumulate = 0 overwrites dw, 1 adds to it; M = 0 with accumulate = 0 sets it
+ * to zero. Sums in a fixed order: reruns are bit-identical.
+ * ws (device) holds qlora_rms_norm_bwd_workspace_bytes(M, k) bytes where dw is
+ * asked for (else it may be NULL). Errors: as the forward, and WORKSPACE.
+ */
+size_t qlora_rms_norm_bwd_workspace_bytes(int64_t M, int64_t k);
+qlora_status qlora_rms_norm_bwd(const void *dY, const void *H, const float *rstd, const void *w, int w_dtype,
+                                const void *dres, int64_t M, int64_t k, int dtype, void *dX, float *dw, int accumulate,
+                                void *ws, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------------
  * Building blocks. qlora_linear_fwd and qlora_linear_bwd are compositions of
  * the calls below (same kernels, same order); they are exported so a caller
@@ -727,6 +809,81 @@ qlora_status qlora_adapter_unmerge(const void *merged, int64_t n, int64_t k, con
 qlora_status qlora_adamw_step(float *theta, uint16_t *theta16, const float *grad, float *m, float *v, int64_t count,
                               int64_t step, float lr, float beta1, float beta2, float eps, float weight_decay,
                               void *stream);
+
+/*
+ * What a step does to the tensors of all adapters together.
+ *
+ * A table describes the tensors to the calls below. qlora_param_table_build
+ * writes its image into host memory, once; the caller copies the image to the
+ * device, sets table->chunks to the copy, and keeps both as long as the tensors
+ * stay where they are. No call changes a table.
+ *
+ * One tensor of `count` elements: grad (device, bf16, fp32 or fp16 per
+ * grad_dtype); theta (device, fp32 master copy), m and v (fp32 states: device
+ * memory, or host memory pinned with hipHostMalloc), theta16 (device, nullable:
+ * the layer calls' copy, bf16 or fp16 per dtype16), as in qlora_adamw_step. theta,
+ * m, v and theta16 all NULL: for the norm only.
+ */
+typedef struct {
+  float *theta;
+  uint16_t *theta16;
+  const void *grad;
+  float *m;
+  float *v;
+  int64_t count;
+  int32_t grad_dtype; /* qlora_dtype */
+  int32_t dtype16;    /* QLORA_DT_BF16 or QLORA_DT_FP16 */
+} qlora_param;
+
+typedef struct {
+  const void *chunks; /* (device) the image; set by the caller */
+  int64_t n_chunks;
+  int64_t elements;
+  int32_t complete;   /* 1: every tensor has theta, m and v */
+} qlora_param_table;
+
+/* Bytes of the image for these n tensors (host; 0 for none, or on bad arguments). */
+size_t qlora_param_table_bytes(const qlora_param *params, int64_t n);
+
+/*
+ * The image of n tensors into image (host, image_bytes bytes), and the rest of
+ * *table. Pure host code, no launch. Errors: INVALID_ARG (NULL or misaligned
+ * pointers, bad types, some but not all of theta, m and v, states in pageable
+ * host memory, a buffer that the step writes and another one that overlaps it),
+ * SHAPE (a count below 0 or above 2^40, tensors or chunks of them above 2^22),
+ * WORKSPACE (image too small).
+ */
+qlora_status qlora_param_table_build(const qlora_param *params, int64_t n, void *image, size_t image_bytes,
+                                     qlora_param_table *table);
+
+/*
+ * The norm of all gradients together, and the factor that scales them to at
+ * most max_norm:
+ *   out[0] = norm = grad_scale * sqrt( sum over every element of g^2 )
+ *   out[1] = max_norm / norm if norm > max_norm, else 1
+ * out (device, 2 fp32). Squares are added in fp64 in a fixed order: no finite
+ * gradient overflows or vanishes (out[0] itself is rounded to fp32), reruns are
+ * bit-identical. If a gradient is not finite, out[1] is NaN and out[0] infinite
+ * or NaN. grad_scale (> 0, finite) undoes a loss scale; max_norm > 0 (infinity:
+ * the norm only). A table without elements has norm 0.
+ * ws (device) holds qlora_grad_norm_workspace_bytes() bytes.
+ * Errors: INVALID_ARG, WORKSPACE, HIP.
+ */
+size_t qlora_grad_norm_workspace_bytes(void);
+qlora_status qlora_grad_norm(const qlora_param_table *table, float grad_scale, float max_norm, float *out, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/*
+ * qlora_adamw_step over every tensor of a complete table in one launch, on the
+ * gradients grad_scale * clip[1] * g: the product of the two factors is rounded,
+ * then that with g, then the update is qlora_adamw_step's operation for operation.
+ * clip (device, nullable: 1) is what qlora_grad_norm left; where clip[1] is NaN
+ * (a gradient is not finite) nothing is changed. step and lr are values of the
+ * call: a captured call replays them. Errors: INVALID_ARG (also a table that is
+ * not complete, hyperparameters out of range), SHAPE (step < 1), HIP.
+ */
+qlora_status qlora_adamw_step_many(const qlora_param_table *table, const float *clip, float grad_scale, int64_t step,
+                                   float lr, float beta1, float beta2, float eps, float weight_decay, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement helpers (not part of the layer): attainable peaks on the box at

@@ -20,15 +20,18 @@ Modules
                    16-bit result.
 ``oracle.merge``   the adapter folded into a dequantized copy of the base (and
                    taken out again), exact in fp64, rounded once.
-``oracle.adamw``   the AdamW step on the adapter and its learning-rate schedule.
+``oracle.adamw``   the AdamW step on the adapter, its learning-rate schedule, and
+                   the global gradient norm with the factor that clips it.
 ``oracle.mlp``     the gated-MLP join silu(G) * U and its gradients, which chains
                    the MLP linears of the 7B block and the 65B-class stack.
 ``oracle.fp8``     the 8-bit layer: E4M3 values with a power-of-two scale per
                    block of 128, the encoding, and the layer over its values.
+``oracle.norm``    residual addition and root-mean-square norm, forward and
+                   backward, with the error bounds of an fp32 evaluation.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against facts that do
 not come from this code (values the pages print, closed forms, brute force,
 library routines for special cases). No function here is "parity unpinned".
 """
 
-from . import nf4, linear, merge, adamw, mlp, fp8  # noqa: F401
+from . import nf4, linear, merge, adamw, mlp, fp8, norm  # noqa: F401

@@ -46,3 +46,14 @@ def cosine_lr(step: int, total: int, warmup: int, peak: float, floor: float = 0.
         return peak * step / max(warmup, 1)
     p = (step - warmup) / max(total - warmup, 1)
     return floor + (peak - floor) * 0.5 * (1.0 + np.cos(np.pi * min(p, 1.0)))
+
+
+def clip_factor(grads, max_norm: float, grad_scale: float = 1.0):
+    """(norm, factor): the norm of grad_scale times all gradients together, and what scales them to at most max_norm;
+    the factor is NaN where a gradient is not finite."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        s = sum(float((np.asarray(g, dtype=np.float64).ravel() ** 2).sum()) for g in grads)
+    norm = grad_scale * float(np.sqrt(s))
+    if not np.isfinite(s):
+        return norm, float("nan")
+    return norm, max_norm / norm if norm > max_norm else 1.0

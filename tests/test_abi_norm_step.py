@@ -1,0 +1,168 @@
+"""Host-only checks of the norm, the 8-bit layer on encoded activations, the gradient norm and the step over many
+tensors: sizes, refusals of the C ABI and of the binding (no kernel launched)."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+from bit_nf4_quantized_02_amd import qlora as q
+
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+OK, ARG, SHAPE, WORK = 0, -1, -2, -4
+P, ODD = ctypes.c_void_p(1 << 24), ctypes.c_void_p((1 << 24) + 8)
+lib = q.raw()
+
+
+def _rows(M=4, k=128, codes=1 << 24, scale=1 << 25):
+    return ctypes.byref(q._Rows8(M, k, codes, scale))
+
+
+def _fwd(X=P, res=None, w=P, wt=0, M=4, k=128, dt=0, eps=1e-5, Y=P, H=None, rstd=P, x8=None):
+    return lib.qlora_rms_norm_fwd(X, res, w, wt, M, k, dt, eps, Y, H, rstd, x8, None)
+
+
+def test_norm_forward_refusals():
+    for bad in (dict(dt=1), dict(dt=7), dict(wt=2), dict(wt=0, dt=2), dict(eps=-1e-5), dict(eps=math.inf),
+                dict(eps=math.nan), dict(X=None), dict(w=None), dict(X=ODD), dict(w=ODD), dict(Y=ODD), dict(rstd=ODD),
+                dict(res=P), dict(H=P), dict(res=ODD, H=P), dict(res=P, H=ODD), dict(x8=_rows(codes=None)),
+                dict(x8=_rows(scale=None)), dict(x8=_rows(codes=(1 << 24) + 8))):
+        assert _fwd(**bad) == ARG, bad
+    for bad in (dict(M=-1), dict(k=0), dict(M=(1 << 22) + 1), dict(k=(1 << 22) + 1), dict(M=1 << 22, k=1 << 15),
+                dict(x8=_rows(M=5)), dict(x8=_rows(k=64)), dict(k=100, x8=_rows(k=100))):
+        assert _fwd(**bad) == SHAPE, bad
+    assert _fwd(M=0) == OK and _fwd(M=0, X=None, Y=None, w=None) == OK
+
+
+def _bwd(dY=P, H=P, rstd=P, w=P, wt=0, dres=None, M=4, k=128, dt=0, dX=P, dw=P, acc=0, ws=P, n=1 << 30):
+    return lib.qlora_rms_norm_bwd(dY, H, rstd, w, wt, dres, M, k, dt, dX, dw, acc, ws, n, None)
+
+
+def test_norm_backward_refusals():
+    for bad in (dict(dt=1), dict(wt=2), dict(acc=2), dict(dY=None), dict(H=None), dict(rstd=None), dict(w=None),
+                dict(dY=ODD), dict(H=ODD), dict(rstd=ODD), dict(w=ODD), dict(dres=ODD), dict(dX=ODD), dict(dw=ODD)):
+        assert _bwd(**bad) == ARG, bad
+    for bad in (dict(M=-1), dict(k=0), dict(M=1 << 22, k=1 << 15)):
+        assert _bwd(**bad) == SHAPE, bad
+    need = lib.qlora_rms_norm_bwd_workspace_bytes(4, 128)
+    assert need > 0
+    assert _bwd(n=need - 1) == WORK and _bwd(ws=None) == WORK and _bwd(ws=ODD) == WORK
+    assert _bwd(dX=None, dw=None, ws=None, n=0) == OK                     # nothing asked for
+    assert _bwd(M=0, dw=None, ws=None, n=0) == OK and _bwd(M=0, acc=1, ws=None, n=0) == OK
+    for M, k in ((0, 128), (4, 0), (-1, 128), (1 << 23, 64)):
+        assert lib.qlora_rms_norm_bwd_workspace_bytes(M, k) == 0
+
+
+def test_encoded_activations_sizes_and_refusals():
+    assert lib.qlora_fp8_rows_bytes(3, 128) == 3 * 129 and lib.qlora_fp8_rows_bytes(3, 192) == 3 * (256 + 2)
+    assert [lib.qlora_fp8_rows_bytes(M, k) for M, k in ((0, 128), (3, 100), (3, 0), (-1, 64))] == [0, 0, 0, 0]
+    deq = lambda x, dt=0, out=P: lib.qlora_dequant_fp8_rows(x, dt, out, None)  # noqa: E731
+    assert [deq(None), deq(_rows(), 1), deq(_rows(), 0, None), deq(_rows(), 0, ODD), deq(_rows(codes=None)),
+            deq(_rows(scale=8))] == [ARG] * 6
+    assert [deq(_rows(M=-1)), deq(_rows(k=100)), deq(_rows(M=(1 << 22) + 1))] == [SHAPE] * 3
+    assert deq(_rows(M=0)) == OK
+    w = ctypes.byref(q._Weight8(96, 128, 1 << 26, 1 << 27))
+
+    def lin(w=w, x=_rows(20), X=P, dt=0, A=P, B=P, r=8, Y=P, T=None, ws=P, n=1 << 30):
+        return lib.qlora_fp8_linear_fwd_rows(w, x, X, dt, A, B, r, 1.0, Y, T, ws, n, None)
+
+    for bad in (dict(w=None), dict(x=None), dict(dt=1), dict(X=None), dict(X=ODD), dict(A=None), dict(B=ODD), dict(Y=None),
+                dict(T=ODD), dict(x=_rows(20, codes=None)), dict(x=_rows(20, scale=(1 << 24) + 4))):
+        assert lin(**bad) == ARG, bad
+    for bad in (dict(x=_rows(20, 192)), dict(r=200), dict(r=-1), dict(x=_rows(-1))):
+        assert lin(**bad) == SHAPE, bad
+    for M, r in ((20, 8), (4, 8), (20, 0)):
+        need = lib.qlora_fp8_linear_rows_workspace_bytes(M, 96, 128, r)
+        assert need > 0 and lin(x=_rows(M), r=r, n=need - 1) == WORK and lin(x=_rows(M), r=r, ws=None) == WORK
+        assert need <= lib.qlora_fp8_linear_workspace_bytes(M, 96, 128, r, 0)
+    assert lib.qlora_fp8_linear_rows_workspace_bytes(4, 96, 128, 0) == 0
+    assert [lib.qlora_fp8_linear_rows_workspace_bytes(*a) for a in ((0, 96, 128, 8), (4, 96, 100, 8), (4, 96, 128, 200))] == [0] * 3
+    assert lin(x=_rows(0)) == OK
+
+
+def _table(params, size=None):
+    arr = (q._Param * len(params))(*params)
+    n = lib.qlora_param_table_bytes(arr, len(params))
+    image = ctypes.create_string_buffer(max(n, 1))
+    t = q._Table()
+    return lib.qlora_param_table_build(arr, len(params), image, n if size is None else size, ctypes.byref(t)), t, n, image
+
+
+def _grad(at, count, dt=1):
+    return q._Param(None, None, at, None, None, count, dt, 0)
+
+
+def test_table_of_gradients():
+    """Chunks of at most 4096 elements (16384 in large sets) that cover every tensor in order, none for an empty one."""
+    for counts, each in (([1, 4096, 4097, 0, 10000], 4096), ([5], 4096), ([(1 << 25) + 3, 40000], 16384)):
+        params = [_grad((1 << 30) * (i + 1), c) for i, c in enumerate(counts)]
+        s, t, n, image = _table(params)
+        chunks = sum(-(-c // each) for c in counts)
+        assert s == OK and t.complete == 0 and t.elements == sum(counts) and t.n_chunks == chunks and n == 48 * chunks
+        words = memoryview(image.raw[:n]).cast("Q")
+        halves = memoryview(image.raw[:n]).cast("I")
+        i = 0
+        for j, c in enumerate(counts):
+            for at in range(0, c, each):
+                assert list(words[6 * i:6 * i + 5]) == [0, 0, 0, (1 << 30) * (j + 1) + 4 * at, 0]
+                assert list(halves[12 * i + 10:12 * i + 12]) == [min(each, c - at), 1]
+                i += 1
+    s, t, n, _ = _table([])
+    assert s == OK and n == 0 and t.n_chunks == 0 and t.elements == 0
+
+
+def test_table_refusals():
+    g = _grad(1 << 30, 100)
+    assert _table([g], size=47)[0] == WORK
+    assert lib.qlora_param_table_build(None, 1, None, 0, ctypes.byref(q._Table())) == ARG
+    assert lib.qlora_param_table_build(ctypes.byref(g), 1, None, 48, ctypes.byref(q._Table())) == WORK
+    assert lib.qlora_param_table_build(ctypes.byref(g), 1, P, 48, None) == ARG
+    for bad in (_grad(None, 100), _grad((1 << 30) + 4, 100), _grad(1 << 30, 100, dt=3), _grad(1 << 30, 100, dt=-1),
+                q._Param(None, None, 1 << 30, 1 << 20, None, 100, 1, 0), q._Param(None, 1 << 20, 1 << 30, None, None, 100, 1, 0),
+                q._Param(1 << 20, None, 1 << 30, None, None, 100, 1, 0), q._Param(None, None, 1 << 30, None, None, 100, 1, 1)):
+        assert _table([g, bad])[0] == ARG
+    for bad in (_grad(1 << 30, -1), _grad(1 << 30, (1 << 40) + 1), _grad(1 << 30, 1 << 40)):
+        assert _table([bad])[0] == SHAPE and _table([bad])[2] == 0
+
+
+def test_gradient_norm_and_step_refusals():
+    t = q._Table(1 << 24, 3, 100, 0)
+    ref = ctypes.byref(t)
+    need = lib.qlora_grad_norm_workspace_bytes()
+    norm = lambda t=ref, s=1.0, m=1.0, out=P, ws=P, n=need: lib.qlora_grad_norm(t, s, m, out, ws, n, None)  # noqa: E731
+    bad_tables = [q._Table(None, 3, 100, 1), q._Table((1 << 24) + 8, 3, 100, 1), q._Table(1 << 24, -1, 100, 1),
+                  q._Table(1 << 24, (1 << 22) + 1, 100, 1)]
+    for kw in (dict(t=None), dict(s=0.0), dict(s=-1.0), dict(s=math.inf), dict(s=math.nan), dict(m=0.0), dict(m=-1.0),
+               dict(m=math.nan), dict(out=None), dict(out=ODD), *(dict(t=ctypes.byref(b)) for b in bad_tables)):
+        assert norm(**kw) == ARG, kw
+    assert norm(ws=None) == WORK and norm(ws=ODD) == WORK and norm(n=need - 1) == WORK
+    full = q._Table(1 << 24, 3, 100, 1)
+
+    def step(t=ctypes.byref(full), clip=None, s=1.0, at=1, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.0):
+        return lib.qlora_adamw_step_many(t, clip, s, at, lr, b1, b2, eps, wd, None)
+
+    for kw in (dict(t=None), dict(t=ref), dict(clip=ODD), dict(s=0.0), dict(s=math.inf), dict(s=math.nan), dict(lr=-1.0),
+               dict(b1=1.0), dict(b2=-0.1), dict(eps=-1.0), dict(wd=-1.0), dict(lr=math.nan),
+               *(dict(t=ctypes.byref(b)) for b in bad_tables)):
+        assert step(**kw) == ARG, kw
+    assert step(at=0) == SHAPE
+    assert step(t=ctypes.byref(q._Table(None, 0, 0, 1))) == OK
+
+
+def test_binding_refuses_on_the_host():
+    z = lambda *s, dt=BF: torch.zeros(s, dtype=dt)  # noqa: E731
+    for call in (lambda: q.rms_norm_fwd(z(4, 8), z(8), 1e-5),                              # not on the GPU
+                 lambda: q.rms_norm_fwd(z(4, 2, 8), z(8), 1e-5),                           # not [M, k]
+                 lambda: q.rms_norm_fwd(z(4, 8, dt=F32), z(8), 1e-5),                      # fp32 activations
+                 lambda: q.rms_norm_bwd(z(4, 2, 8), z(4, 8), z(4, dt=F32), z(8)),
+                 lambda: q.rms_norm_bwd(z(4, 8), z(4, 8), z(4, dt=F32), z(8)),
+                 lambda: q.dequant_fp8_rows(q.FP8Rows.empty(4, 128, device="cpu")),
+                 lambda: q.dequant_fp8_rows(q.FP8Rows.empty(4, 128, device="cpu"), dtype=F32),
+                 lambda: q.fp8_linear_fwd_rows(q.FP8Weight.empty(96, 128, device="cpu"),
+                                               q.FP8Rows.empty(4, 128, device="cpu"), None, None, None, 1.0),
+                 lambda: q.ParamTable([q.Param(z(4, dt=F32))]),
+                 lambda: q.ParamTable([q.Param(z(4, dt=torch.float64))]),
+                 lambda: q.Param(z(4, dt=F32), theta=z(4, dt=F32))._struct(torch.device("cpu"))):
+        with pytest.raises(ValueError):
+            call()

@@ -1,0 +1,292 @@
+"""GPU parity of the gradient norm and the AdamW step over many tensors (qlora_grad_norm, qlora_adamw_step_many).
+
+Bars: the norm and the factor are fp64 sums rounded once to fp32, within 2^-23 of the oracle (half a step of fp32,
+2^-24, and the fp64 sum's own error, below 2^-40 here, both with room for one more rounding); the step equals
+qlora_adamw_step on the scaled gradient bit for bit, which its own tests hold to the oracle.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import adamw as oadam
+from oracle import fp8 as o8
+from oracle import norm as onorm
+
+from gpu_util import f32, say
+
+pytestmark = pytest.mark.gpu
+
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def q():
+    from bit_nf4_quantized_02_amd import qlora
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return qlora
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def params(q, counts, gdt=F32, t16=BF, seed=0, pinned=False, std=1e-2):
+    g = torch.Generator().manual_seed(seed + sum(counts))
+    r = lambda n, s: torch.randn(n, generator=g) * s  # noqa: E731
+    out = []
+    for n in counts:
+        home = (lambda t: t.pin_memory()) if pinned else (lambda t: t.cuda())
+        th = r(n, 0.05).cuda()
+        out.append(q.Param(r(n, std).to(gdt).cuda(), th, home(r(n, 1e-3)), home(r(n, 1e-3).square()),
+                           None if t16 is None else th.to(t16)))
+    return out
+
+
+def check_clip(out, grads, max_norm, scale=1.0):
+    norm, factor = oadam.clip_factor([f64(g) for g in grads], max_norm, scale)
+    n, f = (float(x) for x in out)
+    say(f"  norm {n:.6g} (oracle {norm:.6g}), factor {f:.6g}")
+    assert abs(n - norm) <= 2.0 ** -23 * norm and abs(f - factor) <= 2.0 ** -23 * factor
+
+
+COUNTS = [[1], [3, 5], [4, 64, 4096], [4097, 1, 8191, 12288, 130], [7] * 300, [100003, 2, 65536]]
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{c[0]}")
+@pytest.mark.parametrize("gdt", [F32, BF, F16])
+def test_norm(q, counts, gdt):
+    say(f"case: grad norm {len(counts)} tensors {counts[0]}.. {gdt}")
+    ps = params(q, counts, gdt)
+    grads = [p.grad for p in ps]
+    table = q.ParamTable([q.Param(g) for g in grads])
+    assert table.elements == sum(counts)
+    for max_norm, scale in ((math.inf, 1.0), (1e-3, 1.0), (1e-3, 2.0 ** -10), (0.3, 3.0), (1e6, 1.0)):
+        out = q.grad_norm(table, max_norm, grad_scale=scale)
+        check_clip(out, grads, max_norm, scale)
+        assert torch.equal(out, q.grad_norm(table, max_norm, grad_scale=scale))
+
+
+def test_norm_of_mixed_types_and_repeated_tensors(q):
+    g = torch.Generator().manual_seed(4)
+    grads = [torch.randn(n, generator=g).to(dt).cuda() for n, dt in ((5000, F32), (77, BF), (4100, F16))]
+    check_clip(q.grad_norm(q.ParamTable([q.Param(t) for t in grads]), 1.0), grads, 1.0)
+    twice = [grads[0], grads[1], grads[0]]  # (each mention counts; only the step refuses it)
+    check_clip(q.grad_norm(q.ParamTable([q.Param(t) for t in twice]), 1.0), twice, 1.0)
+
+
+def test_norm_at_the_ends_of_fp32(q):
+    """Squares that fp32 cannot hold, large and small; the norm is right as long as it is an fp32 number itself."""
+    for v in (1e30, 3e38, 1e-30, 1e-38, 1e-44):
+        g = torch.full((1000,), v, device="cuda")
+        norm, factor = (float(x) for x in q.grad_norm(q.ParamTable([q.Param(g)]), 1.0))
+        want = float(g[0].double()) * math.sqrt(1000)
+        if want < 3.4e38:
+            assert abs(norm - want) <= 2.0 ** -23 * want + 2.0 ** -149
+        else:
+            assert math.isinf(norm)
+        assert abs(factor - min(1.0, 1 / want)) <= 2.0 ** -23 * min(1.0, 1 / want) + 2.0 ** -149
+    assert q.grad_norm(q.ParamTable([q.Param(torch.zeros(9, device="cuda"))]), 1.0).tolist() == [0.0, 1.0]
+    assert q.grad_norm(q.ParamTable([]), 1.0).tolist() == [0.0, 1.0]
+    assert q.grad_norm(q.ParamTable([q.Param(torch.zeros(0, device="cuda"))]), 1.0).tolist() == [0.0, 1.0]
+
+
+def test_norm_of_a_large_set(q):
+    """Chunks of the larger size, more of them than workgroups."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    grads = [torch.randn(n, generator=g, device="cuda") for n in (40_000_001, 16384, 3, 5_000_000)]
+    norm = math.sqrt(sum(float(t.double().square().sum()) for t in grads))
+    out = q.grad_norm(q.ParamTable([q.Param(t) for t in grads]), 1.0)
+    assert abs(float(out[0]) - norm) <= 2.0 ** -23 * norm and abs(float(out[1]) - 1 / norm) <= 2.0 ** -23 / norm
+
+
+def copies(ps):
+    return [[None if t is None else t.clone() for t in (p.theta, p.m, p.v, p.theta16)] for p in ps]
+
+
+def expect(q, ps, before, factor, step, kw):
+    """Each tensor by qlora_adamw_step on the scaled gradient."""
+    for p, (th, m, v, t16) in zip(ps, before):
+        m, v = m.cuda(), v.cuda()
+        q.adamw_step(th, p.grad.float() * factor, m, v, step, **kw)
+        assert torch.equal(p.theta, th) and torch.equal(p.m.cuda(), m) and torch.equal(p.v.cuda(), v)
+        if t16 is not None:
+            assert torch.equal(p.theta16, th.to(t16.dtype))
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{c[0]}")
+@pytest.mark.parametrize("gdt,t16,pinned", [(F32, BF, False), (F32, F16, False), (BF, None, False), (F16, F16, True)])
+def test_step(q, counts, gdt, t16, pinned):
+    say(f"case: step {len(counts)} tensors {counts[0]}.. {gdt} {t16} pinned={pinned}")
+    kw = dict(lr=3e-4, betas=(0.9, 0.995), eps=1e-8, weight_decay=0.01)
+    ps = params(q, counts, gdt, t16, pinned=pinned)
+    table = q.ParamTable(ps)
+    before = copies(ps)
+    q.adamw_step_many(table, 1, **kw)
+    torch.cuda.synchronize()
+    expect(q, ps, before, 1.0, 1, kw)
+    for step, max_norm, scale in ((2, 1e-2, 1.0), (3, 1e9, 2.0 ** -6)):
+        before = copies(ps)
+        clip = q.grad_norm(table, max_norm, grad_scale=scale)
+        q.adamw_step_many(table, step, clip=clip, grad_scale=scale, **kw)
+        torch.cuda.synchronize()
+        expect(q, ps, before, clip[1] * scale, step, kw)
+
+
+def test_step_of_a_large_set(q):
+    ps = params(q, [40_000_003, 1000], F32, BF)
+    table, before = q.ParamTable(ps), copies(ps)
+    clip = q.grad_norm(table, 0.5)
+    q.adamw_step_many(table, 4, 1e-3, clip=clip)
+    expect(q, ps, before, clip[1], 4, dict(lr=1e-3))
+
+
+def test_no_step_where_a_gradient_is_not_finite(q):
+    for dt, bad in ((F32, math.inf), (F32, math.nan), (BF, -math.inf), (F16, math.inf)):
+        ps = params(q, [5000, 77], dt)
+        ps[1].grad[76] = bad
+        table, before = q.ParamTable(ps), copies(ps)
+        clip = q.grad_norm(table, 1.0)
+        assert not math.isfinite(float(clip[0])) and math.isnan(float(clip[1]))
+        q.adamw_step_many(table, 2, 1e-3, clip=clip)
+        for p, b in zip(ps, before):
+            for t, was in zip((p.theta, p.m, p.v, p.theta16), b):
+                assert torch.equal(t, was)
+        ps[1].grad[76] = 0.5
+        clip = q.grad_norm(table, 1.0)
+        q.adamw_step_many(table, 2, 1e-3, clip=clip)
+        expect(q, ps, before, clip[1], 2, dict(lr=1e-3))
+
+
+def test_what_lies_between_the_tensors_is_left_alone(q):
+    flat = [torch.full((5000,), 3.0, device="cuda") for _ in range(4)]
+    f16 = torch.full((5000,), 3.0, dtype=BF, device="cuda")
+    cut = lambda t: [t[0:131], t[192:192 + 4097]]  # noqa: E731
+    ps = [q.Param(g, th, m, v, t) for g, th, m, v, t in zip(*(cut(t) for t in (*flat, f16)))]
+    q.adamw_step_many(q.ParamTable(ps), 1, 0.1)
+    for t in (*flat[1:], f16):
+        assert (t[131:192] == 3).all() and (t[192 + 4097:] == 3).all()
+        if t is not flat[2]:  # (m, the mean of a 3 and a gradient of 3, is 3 again)
+            assert not (t[:131] == 3).any() and not (t[192:192 + 4097] == 3).any()
+    assert (flat[0] == 3).all()
+
+
+def test_table_refusals_on_the_device(q):
+    z = lambda n=64, dt=F32: torch.zeros(n, dtype=dt, device="cuda")  # noqa: E731
+    buf = z(256)
+    ok = q.Param(z(), z(), z(), z())
+    for bad in ([ok, ok],                                                         # the same tensor twice
+                [q.Param(z(), buf[:64], z(), z()), q.Param(z(), buf[32:96], z(), z())],
+                [q.Param(buf[:64], buf[:64], z(), z())],                          # a gradient that the step overwrites
+                [q.Param(z(), z(), buf[:64], buf[60:124])],
+                [q.Param(z(), buf[:64], z(), z(), buf.view(BF)[64:128])]):
+        with pytest.raises(q.QLoraError):
+            q.ParamTable(bad)
+    with pytest.raises(q.QLoraError):
+        q.ParamTable([q.Param(buf[1:65])])                                        # not aligned
+    with pytest.raises(q.QLoraError):
+        q.adamw_step_many(q.ParamTable([q.Param(z())]), 1, 1e-3)                   # gradients only
+    for bad in (q.Param(z(), z(), torch.zeros(64), z()),                           # pageable
+                q.Param(z(), z(), z(), None), q.Param(z(), z(63), z(), z()), q.Param(z(), z(), z(63), z()),
+                q.Param(z(), z(), z(), z(), z()), q.Param(z(), z(dt=F16), z(), z()), q.Param(z(), None, None, None, z(dt=BF)),
+                q.Param(z(128)[::2])):
+        with pytest.raises(ValueError):
+            q.ParamTable([bad])
+    with pytest.raises(ValueError):
+        q.adamw_step_many(q.ParamTable([ok]), 1, 1e-3, clip=torch.zeros(3, device="cuda"))
+    shared = z()
+    assert q.ParamTable([q.Param(shared, z(), z(), z()), q.Param(shared, z(), z(), z())]).elements == 128
+
+
+def test_captured_and_on_another_stream(q):
+    ps = params(q, [4097, 300, 64], F32, BF)
+    table = q.ParamTable(ps)
+    kw = dict(lr=1e-3, weight_decay=0.01)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        q.grad_norm(table, 0.1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        clip = q.grad_norm(table, 0.1)
+        q.adamw_step_many(table, 3, clip=clip, **kw)
+    for i in range(4):
+        for p in ps:
+            p.grad.copy_(torch.randn(p.grad.shape, device="cuda") * 10.0 ** -i)
+        before = copies(ps)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_clip(clip, [p.grad for p in ps], 0.1)
+        expect(q, ps, before, clip[1].clone(), 3, kw)
+    before = copies(ps)
+    s.wait_stream(torch.cuda.current_stream())
+    clip = q.grad_norm(table, 0.1, stream=s)
+    q.adamw_step_many(table, 4, clip=clip, stream=s, **kw)
+    torch.cuda.synchronize()
+    expect(q, ps, before, clip[1], 4, kw)
+
+
+def test_a_training_step(q):
+    """The operators as a step uses them: the norm feeds two 8-bit layers with adapters, their gradients come back
+    through it, and all adapters and the gain take one clipped step. Against the formulas in fp64 on the values that the
+    calls exchange; the layers' 16-bit outputs and inputs have tests of their own."""
+    M, k, n, r, s, eps = 70, 256, 192, 8, 0.5, 1e-5
+    g = torch.Generator().manual_seed(21)
+    rnd = lambda *sh, std=1.0: (torch.randn(sh, generator=g) * std)  # noqa: E731
+    X, R = rnd(M, k).to(BF).cuda(), (3 * rnd(M, k)).to(BF).cuda()
+    dYs = [rnd(M, n, std=0.1).to(BF).cuda() for _ in range(2)]
+    dres = rnd(M, k, std=0.1).to(BF).cuda()
+    w8 = [q.quantize_fp8(rnd(n, k, std=0.05).to(BF).cuda()) for _ in range(2)]
+    masters = [t.cuda() for t in (1 + 0.1 * rnd(k), rnd(r, k, std=0.05), rnd(n, r, std=0.05), rnd(r, k, std=0.05),
+                                  rnd(n, r, std=0.05))]
+    copies16 = [t.to(BF) for t in masters]
+    grads = [torch.zeros_like(t) for t in masters]
+    moments = [[torch.zeros_like(t) for t in masters] for _ in range(2)]
+    table = q.ParamTable([q.Param(*t) for t in zip(grads, masters, *moments, copies16)])
+    gain, A0, B0, A1, B1 = copies16
+    for step in (1, 2):
+        Y, H, rstd, x8 = q.rms_norm_fwd(X, gain, eps, residual=R, want_x8=True)
+        dYn = None
+        Ts = []
+        for i, (A, B) in enumerate(((A0, B0), (A1, B1))):
+            out, T = q.fp8_linear_fwd_rows(w8[i], x8, Y, A, B, s)
+            assert out.shape == (M, n)
+            Ts.append(T)
+            dX, _, _ = q.fp8_linear_bwd(w8[i], Y, T, dYs[i], A, B, s, dA=grads[1 + 2 * i], dB=grads[2 + 2 * i])
+            dYn = dX if dYn is None else dYn + dX
+        dX, _ = q.rms_norm_bwd(dYn, H, rstd, gain, dres=dres, dw=grads[0])
+        # the gradients in fp64
+        y64, r64 = onorm.rms_fwd(f64(H), f64(gain), eps)
+        Y64 = f64(Y)
+        assert np.abs(Y64 - y64).max() <= onorm.y_bound(y64, k, 2.0 ** -8, 0).max()
+        codes, scale = o8.encode_rows(f32(Y))
+        assert np.array_equal(x8.codes.cpu().numpy(), codes) and np.array_equal(x8.scale.cpu().numpy(), scale)
+        for i, (A, B) in enumerate(((A0, B0), (A1, B1))):
+            U = f64(dYs[i]) @ f64(B)
+            dA, dB = s * U.T @ Y64, s * f64(dYs[i]).T @ (Y64 @ f64(A).T)
+            for got, want in ((grads[1 + 2 * i], dA), (grads[2 + 2 * i], dB)):
+                assert np.linalg.norm(f64(got) - want) <= 1e-5 * np.linalg.norm(want)
+        args = (f64(dYn), f64(H), f64(rstd), f64(gain), f64(dres))
+        dx, dw = onorm.rms_bwd(*args)
+        assert np.all(np.abs(f64(dX) - dx) <= onorm.dx_bound(*args, dx, 2.0 ** -8, 2.0 ** -134))
+        assert np.all(np.abs(f64(grads[0]) - dw) <= onorm.dw_bound(*args[:3]))
+        # the step
+        was = [[f64(t) for t in (th, m, v)] for th, m, v in zip(masters, *moments)]
+        clip = q.grad_norm(table, 0.3)
+        check_clip(clip, grads, 0.3)
+        q.adamw_step_many(table, step, 1e-3, clip=clip, weight_decay=0.01)
+        c = lambda x: float(np.float32(x))  # noqa: E731
+        for i, (th, m, v) in enumerate(was):
+            gc = f64(grads[i]) * float(clip[1])
+            a, b, d = oadam.adamw_step(th, gc, m, v, step, c(1e-3), b1=c(0.9), b2=c(0.999), eps=c(1e-8), wd=c(0.01))
+            # (as qlora_adamw_step's own bars, and one more rounding of the gradient, twice in v)
+            assert np.all(np.abs(f64(moments[0][i]) - b) <= 2.0 ** -20 * (0.9 * np.abs(m) + 0.1 * np.abs(gc)) + 1e-45)
+            assert np.all(np.abs(f64(moments[1][i]) - d) <= 2.0 ** -20 * (0.999 * v + 0.001 * gc * gc) + 1e-45)
+            um = np.abs(b / (1 - c(0.9) ** step)) / (np.sqrt(d / (1 - c(0.999) ** step)) + c(1e-8))
+            noise = 2.0 ** -18 * (0.9 * np.abs(m) + 0.1 * np.abs(gc)) / (1 - c(0.9) ** step) / \
+                (np.sqrt(d / (1 - c(0.999) ** step)) + c(1e-8))
+            assert np.all(np.abs(f64(masters[i]) - a) <= 2.0 ** -23 * np.maximum(np.abs(th), np.abs(a)) +
+                          1e-3 * (2.0 ** -18 * (um + 0.01 * np.abs(th)) + noise))
+            assert torch.equal(copies16[i], masters[i].to(BF))
