@@ -21,6 +21,8 @@ namespace {
 
 constexpr int64_t kInRegisters = 32768;  // columns of a row that a workgroup holds
 
+constexpr int kDwGroups = 256;  // workgroups of the backward with dw, at most: one for each compute unit
+
 // Eight 16-bit values into (row, c), nothing from n on.
 template <bool kVec>
 __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, int64_t n, const u32x4& v) {
@@ -35,39 +37,62 @@ __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, i
   }
 }
 
-// Eight gains from c on, as they are stored: 16 bits in a[0], or fp32.
-struct Gain {
-  u32x4 a[2];
+// A row of n 16-bit values, read and written in runs of eight by the kLpr lanes
+// that hold it. Where a wave has one row only, through a buffer descriptor of the
+// row: its range check replaces a branch at each run (a load behind one waits
+// for the one before it), and the addresses take no vector registers.
+template <int kLpr, bool kVec>
+struct RowOf {
+  static constexpr bool kBuffer = kVec && kLpr >= 64;
+  i32x4 rs;
+  uint16_t* p;
+  int64_t n;
+  __device__ __forceinline__ RowOf(const uint16_t* base, int64_t m, int64_t k) : p(const_cast<uint16_t*>(base) + m * k), n(k) {
+    if constexpr (kBuffer) rs = make_rsrc(p, 2 * k);
+  }
+  __device__ __forceinline__ u32x4 load(int t, int v) const {
+    if constexpr (kBuffer) return raw_buffer_load_b128(rs, 16 * t, 16 * kLpr * v, 0);
+    else return load8h<kVec>(p, 8 * (t + kLpr * v), n);
+  }
+  __device__ __forceinline__ void store(int t, int v, const u32x4& x) const {
+    if constexpr (kBuffer) raw_buffer_store_b128(x, rs, 16 * t, 16 * kLpr * v, 0);
+    else store8h<kVec>(p, 8 * (t + kLpr * v), n, x);
+  }
 };
 
-template <bool kVec>
-__device__ __forceinline__ Gain load_gain(const void* __restrict__ w, bool w32, int64_t c, int64_t n) {
-  Gain g;
-  if (!w32) {
+// Eight gains from c on, as they are stored: in 16 bits or (kW32) fp32.
+template <bool kW32>
+struct Gain {
+  u32x4 a[kW32 ? 2 : 1];
+};
+
+template <bool kW32, bool kVec>
+__device__ __forceinline__ Gain<kW32> load_gain(const void* __restrict__ w, int64_t c, int64_t n) {
+  Gain<kW32> g;
+  if constexpr (!kW32) {
     g.a[0] = load8h<kVec>(static_cast<const uint16_t*>(w), c, n);
-    g.a[1] = u32x4{0u, 0u, 0u, 0u};
-    return g;
-  }
-  const uint32_t* p = static_cast<const uint32_t*>(w);
-  if (c + 8 <= n) {
-    g.a[0] = *reinterpret_cast<const u32x4*>(p + c);
-    g.a[1] = *reinterpret_cast<const u32x4*>(p + c + 4);
   } else {
+    const uint32_t* p = static_cast<const uint32_t*>(w);
+    if (c + 8 <= n) {
+      g.a[0] = *reinterpret_cast<const u32x4*>(p + c);
+      g.a[1] = *reinterpret_cast<const u32x4*>(p + c + 4);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t e = p[c + i < n ? c + i : n - 1];
-      g.a[i >> 2][i & 3] = c + i < n ? e : 0u;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t e = p[c + i < n ? c + i : n - 1];
+        g.a[i >> 2][i & 3] = c + i < n ? e : 0u;
+      }
     }
   }
   return g;
 }
 
-template <bool kF16>
-__device__ __forceinline__ void gain8(const Gain& g, bool w32, float (&f)[8]) {
+template <bool kF16, bool kW32>
+__device__ __forceinline__ void gain8(const Gain<kW32>& g, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float s = from16<kF16>((g.a[0][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-    f[i] = w32 ? __uint_as_float(g.a[i >> 2][i & 3]) : s;
+    if constexpr (kW32) f[i] = __uint_as_float(g.a[i >> 2][i & 3]);
+    else f[i] = from16<kF16>((g.a[0][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
   }
 }
 
@@ -133,11 +158,11 @@ __device__ __forceinline__ float squares8(const u32x4& h, float s) {
 }
 
 // y of eight values, in 16 bits.
-template <bool kF16>
-__device__ __forceinline__ u32x4 normed8(const u32x4& h, float rstd, const Gain& g, bool w32) {
+template <bool kF16, bool kW32>
+__device__ __forceinline__ u32x4 normed8(const u32x4& h, float rstd, const Gain<kW32>& g) {
   float f[8], w[8];
   unpack8<kF16>(h, f);
-  gain8<kF16>(g, w32, w);
+  gain8<kF16>(g, w);
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * w[i];
   return pack8<kF16>(f);
@@ -170,10 +195,17 @@ __device__ __forceinline__ void encode8(const u32x4& y, int64_t m, int64_t c, in
   if ((c & (kF8Block - 1)) == 0) scale[m * (kp / kF8Block) + c / kF8Block] = (uint8_t)b;
 }
 
+// Which of the workgroup's rows the thread is one of (the same for a wave, where
+// it has one only).
+template <int kLpr>
+__device__ __forceinline__ int group_of() {
+  const int g = threadIdx.x / kLpr;
+  return kLpr >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
+}
+
 struct FwdArgs {
   const uint16_t *X, *R;  // R: the residual, or NULL
   const void* w;
-  int w32;
   int64_t M, k, kp;
   float inv_k, eps;
   uint16_t *Y, *H;        // Y may be NULL; H is there if R is
@@ -181,29 +213,32 @@ struct FwdArgs {
   uint8_t *codes, *scale; // may be NULL
 };
 
-template <bool kF16, int kLpr, int kV, bool kVec>
+template <bool kF16, bool kW32, int kLpr, int kV, bool kVec>
 __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArgs a) {
   constexpr int kThreads = kLpr < 256 ? 256 : kLpr;
   __shared__ float red[kThreads / 64];
   const int t = threadIdx.x & (kLpr - 1);
-  const int64_t m = (int64_t)blockIdx.x * (kThreads / kLpr) + threadIdx.x / kLpr;
+  const int64_t m = (int64_t)blockIdx.x * (kThreads / kLpr) + group_of<kLpr>();
   const bool live = m < a.M;
-  const int64_t at = (live ? m : a.M - 1) * a.k;
+  const int64_t mr = live ? m : a.M - 1;
+  const RowOf<kLpr, kVec> X(a.X, mr, a.k);
   u32x4 h[kV], r[kV];
-  Gain g[kV];
+  Gain<kW32> g[kV];
 #pragma unroll
-  for (int v = 0; v < kV; ++v) h[v] = load8h<kVec>(a.X + at, 8 * (t + kLpr * v), a.k);
+  for (int v = 0; v < kV; ++v) h[v] = X.load(t, v);
   if (a.R != nullptr) {
+    const RowOf<kLpr, kVec> R(a.R, mr, a.k);
 #pragma unroll
-    for (int v = 0; v < kV; ++v) r[v] = load8h<kVec>(a.R + at, 8 * (t + kLpr * v), a.k);
+    for (int v = 0; v < kV; ++v) r[v] = R.load(t, v);
   }
 #pragma unroll
-  for (int v = 0; v < kV; ++v) g[v] = load_gain<kVec>(a.w, a.w32, 8 * (t + kLpr * v), a.k);
+  for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
   if (a.R != nullptr) {
+    const RowOf<kLpr, kVec> H(a.H, mr, a.k);
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       h[v] = add8<kF16>(h[v], r[v]);
-      if (live) store8h<kVec>(a.H + at, 8 * (t + kLpr * v), a.k, h[v]);
+      if (live) H.store(t, v, h[v]);
     }
   }
   float s = 0.0f;
@@ -212,18 +247,19 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
   const float rstd = 1.0f / sqrtf(fmaf(row_sum<kLpr>(s, red), a.inv_k, a.eps));
   if (!live) return;
   if (t == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
+  const RowOf<kLpr, kVec> Y(a.Y, mr, a.k);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     const int64_t c = 8 * (t + kLpr * v);
-    const u32x4 y = normed8<kF16>(h[v], rstd, g[v], a.w32);
-    if (a.Y != nullptr) store8h<kVec>(a.Y + at, c, a.k, y);
+    const u32x4 y = normed8<kF16>(h[v], rstd, g[v]);
+    if (a.Y != nullptr) Y.store(t, v, y);
     if (kVec && a.codes != nullptr && c < a.kp) encode8<kF16>(y, m, c, a.kp, a.codes, a.scale);
   }
 }
 
 // Rows of any length, read twice (the second time from the caches, if they hold
 // a row of every workgroup).
-template <bool kF16, bool kVec>
+template <bool kF16, bool kW32, bool kVec>
 __global__ __launch_bounds__(1024) void rms_fwd_long_kernel(FwdArgs a) {
   __shared__ float red[16];
   const int64_t m = blockIdx.x, at = m * a.k;
@@ -240,7 +276,7 @@ __global__ __launch_bounds__(1024) void rms_fwd_long_kernel(FwdArgs a) {
   const float rstd = 1.0f / sqrtf(fmaf(row_sum<1024>(s, red), a.inv_k, a.eps));
   if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
   for (int64_t c = 8 * threadIdx.x; c < a.kp; c += 8192) {  // (each thread reads what it wrote)
-    const u32x4 y = normed8<kF16>(load8h<kVec>(in, c, a.k), rstd, load_gain<kVec>(a.w, a.w32, c, a.k), a.w32);
+    const u32x4 y = normed8<kF16>(load8h<kVec>(in, c, a.k), rstd, load_gain<kW32, kVec>(a.w, c, a.k));
     if (a.Y != nullptr) store8h<kVec>(a.Y + at, c, a.k, y);
     if (kVec && a.codes != nullptr) encode8<kF16>(y, m, c, a.kp, a.codes, a.scale);
   }
@@ -250,7 +286,6 @@ struct BwdArgs {
   const uint16_t *dY, *H, *R;  // R: the gradient that reaches h past the norm, or NULL
   const float* rstd;
   const void* w;
-  int w32;
   int64_t M, k;
   float inv_k;
   uint16_t* dX;  // may be NULL
@@ -273,105 +308,134 @@ __device__ __forceinline__ u32x4 dx8(const u32x4& dy, const u32x4& h, const u32x
   return pack8<kF16>(a);
 }
 
-// Workgroups of kThreads hold kThreads / kLpr rows at a time and walk over the
-// rows with the grid. kDw: each lane adds up dy hn of its columns over the
-// rows it meets; the rows of a workgroup are joined in LDS at the end, the
-// workgroups by rms_dw_kernel.
-template <bool kF16, int kLpr, int kV, int kThreads, bool kVec, bool kDw>
-__global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
-  constexpr int kRows = kThreads / kLpr;
-  __shared__ float red[2][kThreads / 64];
-  const int t = threadIdx.x & (kLpr - 1), group = threadIdx.x / kLpr;
-  float w[kV][8], acc[kV][8];
+// One row's share of a lane, as it was loaded.
+template <int kV>
+struct RowRegs {
+  u32x4 dy[kV], h[kV], r[kV];
+  float rstd;
+};
+
+template <int kLpr, int kV, bool kVec>
+__device__ __forceinline__ void load_row(const BwdArgs& a, int64_t m, int t, RowRegs<kV>& x) {
+  const RowOf<kLpr, kVec> dY(a.dY, m, a.k), H(a.H, m, a.k), R(a.R, m, a.R != nullptr ? a.k : 0);
+#pragma unroll
+  for (int v = 0; v < kV; ++v) x.dy[v] = dY.load(t, v);
+#pragma unroll
+  for (int v = 0; v < kV; ++v) x.h[v] = H.load(t, v);
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+    x.r[v] = RowOf<kLpr, kVec>::kBuffer || a.R != nullptr ? R.load(t, v) : u32x4{0u, 0u, 0u, 0u};  // (no R: a row of no columns)
+  x.rstd = a.rstd[m];
+}
+
+// A row's dx from its registers; kDw: dy hn added to acc. Every thread of the
+// workgroup calls (row_sum). live: the row is one of the M.
+template <bool kF16, bool kW32, int kLpr, int kV, bool kVec, bool kDw>
+__device__ __forceinline__ void do_row(const BwdArgs& a, int64_t m, bool live, int t, RowRegs<kV>& x, const Gain<kW32> (&g)[kV],
+                                       float (&acc)[kDw ? kV : 1][8], float* red) {
+  float s = 0.0f;
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    const Gain g = load_gain<kVec>(a.w, a.w32, 8 * (t + kLpr * v), a.k);
-    gain8<kF16>(g, a.w32, w[v]);
+    float dy[8], h[8], w[8];
+    unpack8<kF16>(x.dy[v], dy);
+    unpack8<kF16>(x.h[v], h);
+    gain8<kF16>(g[v], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = dy[i] * (h[i] * x.rstd);
+      s = fmaf(p, w[i], s);
+      if (kDw) acc[v][i] += live ? p : 0.0f;
+    }
+  }
+  const float dot = row_sum<kLpr>(s, red) * a.inv_k;
+  if (!live || a.dX == nullptr) return;
+  const RowOf<kLpr, kVec> dX(a.dX, m, a.k);
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    // (unpacked again: kept from above, the fp32 values take twice the registers)
+    asm volatile("" : "+v"(x.dy[v]), "+v"(x.h[v]));
+    float w[8];
+    gain8<kF16>(g[v], w);
+    dX.store(t, v, dx8<kF16>(x.dy[v], x.h[v], x.r[v], a.R != nullptr, x.rstd, dot, w));
+  }
+}
+
+// dX alone: a row for each kLpr threads.
+template <bool kF16, bool kW32, int kLpr, int kV, bool kVec>
+__global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_dx_kernel(BwdArgs a) {
+  constexpr int kThreads = kLpr < 256 ? 256 : kLpr;
+  __shared__ float red[kThreads / 64];
+  const int t = threadIdx.x & (kLpr - 1), group = group_of<kLpr>();
+  const int64_t m = (int64_t)blockIdx.x * (kThreads / kLpr) + group;
+  RowRegs<kV> x;
+  Gain<kW32> g[kV];
+  float none[1][8];
+  load_row<kLpr, kV, kVec>(a, m < a.M ? m : a.M - 1, t, x);
+#pragma unroll
+  for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
+  do_row<kF16, kW32, kLpr, kV, kVec, false>(a, m, m < a.M, t, x, g, none, red);
+}
+
+// dX and dw: kThreads threads hold kThreads / kLpr rows at a time and walk
+// over the rows with the grid, the next rows loaded before this one's sum. Each lane adds up dy hn of its columns over the rows it meets; the
+// rows of a workgroup are joined in LDS at the end, the workgroups by
+// rms_dw_kernel.
+template <bool kF16, bool kW32, int kLpr, int kV, int kThreads, bool kVec>
+__global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
+  constexpr int kRows = kThreads / kLpr, kCols = 8 * kLpr * kV;
+  __shared__ float red[2][kThreads / 64];  // in turn: one barrier a row
+  const int t = threadIdx.x & (kLpr - 1), group = group_of<kLpr>();
+  Gain<kW32> g[kV];
+  float acc[kV][8];
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[v][i] = 0.0f;
   }
-  struct Row {
-    u32x4 dy[kV], h[kV], r[kV];
-    float rstd;
-  };
   const int64_t step = (int64_t)gridDim.x * kRows;
-  auto load = [&](int64_t m0, Row& x) {
-    const int64_t m = m0 + group < a.M ? m0 + group : a.M - 1;
-    const int64_t at = m * a.k;
-    x.rstd = a.rstd[m];
-#pragma unroll
-    for (int v = 0; v < kV; ++v) x.dy[v] = load8h<kVec>(a.dY + at, 8 * (t + kLpr * v), a.k);
-#pragma unroll
-    for (int v = 0; v < kV; ++v) x.h[v] = load8h<kVec>(a.H + at, 8 * (t + kLpr * v), a.k);
+  const auto load = [&](int64_t m, RowRegs<kV>& x) { load_row<kLpr, kV, kVec>(a, m < a.M ? m : a.M - 1, t, x); };
+  const auto row = [&](int64_t m, RowRegs<kV>& x, int turn) {
+    do_row<kF16, kW32, kLpr, kV, kVec, true>(a, m, m < a.M, t, x, g, acc, red[turn]);
+  };
+  int64_t m = (int64_t)blockIdx.x * kRows + group;
+  int64_t left = (a.M - (int64_t)blockIdx.x * kRows + step - 1) / step;  // rows of the workgroup's first group
+  RowRegs<kV> x0, x1;
+  load(m, x0);
+  for (; left > 0; left -= 2, m += 2 * step) {
+    load(m + step, x1);  // (past the last row: that one again)
+    row(m, x0, 0);
+    if (left == 1) break;
+    load(m + 2 * step, x0);
+    row(m + step, x1, 1);
+  }
+  float* const out = a.part + (int64_t)blockIdx.x * a.k;
+  if constexpr (kRows == 1) {
 #pragma unroll
     for (int v = 0; v < kV; ++v)
-      x.r[v] = a.R != nullptr ? load8h<kVec>(a.R + at, 8 * (t + kLpr * v), a.k) : u32x4{0u, 0u, 0u, 0u};
-  };
-  int turn = 0;
-  auto row = [&](int64_t m0, const Row& x) {
-    const bool live = m0 + group < a.M;
-    float s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      float dy[8], h[8];
-      unpack8<kF16>(x.dy[v], dy);
-      unpack8<kF16>(x.h[v], h);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float p = dy[i] * (h[i] * x.rstd);
-        s = fmaf(p, w[v][i], s);
-        if (kDw && live) acc[v][i] += p;
+        const int64_t c = 8 * (t + kLpr * v) + i;
+        if (c < a.k) out[c] = acc[v][i];
       }
-    }
-    // (two buffers in turn: one barrier a row)
-    const float dot = row_sum<kLpr>(s, red[turn]) * a.inv_k;
-    turn ^= 1;
-    if (!live || a.dX == nullptr) return;
+  } else {
+    __shared__ float join[kRows][kCols];
 #pragma unroll
     for (int v = 0; v < kV; ++v)
-      store8h<kVec>(a.dX + (m0 + group) * a.k, 8 * (t + kLpr * v), a.k,
-                    dx8<kF16>(x.dy[v], x.h[v], x.r[v], a.R != nullptr, x.rstd, dot, w[v]));
-  };
-  Row x0, x1;
-  int64_t m0 = (int64_t)blockIdx.x * kRows;
-  load(m0, x0);
-  for (; m0 < a.M; m0 += 2 * step) {
-    if (m0 + step < a.M) load(m0 + step, x1);
-    row(m0, x0);
-    if (m0 + step >= a.M) break;
-    if (m0 + 2 * step < a.M) load(m0 + 2 * step, x0);
-    row(m0 + step, x1);
-  }
-  if constexpr (kDw) {
-    constexpr int kCols = 8 * kLpr * kV;
-    float* const out = a.part + (int64_t)blockIdx.x * a.k;
-    if constexpr (kRows == 1) {
 #pragma unroll
-      for (int v = 0; v < kV; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t c = 8 * (t + kLpr * v) + i;
-          if (c < a.k) out[c] = acc[v][i];
-        }
-    } else {
-      __shared__ float join[kRows][kCols];
-#pragma unroll
-      for (int v = 0; v < kV; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) join[group][8 * (t + kLpr * v) + i] = acc[v][i];
-      __syncthreads();
-      for (int c = threadIdx.x; c < kCols && c < a.k; c += kThreads) {
-        float s = join[0][c];
+      for (int i = 0; i < 8; ++i) join[group][8 * (t + kLpr * v) + i] = acc[v][i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < kCols && c < a.k; c += kThreads) {
+      float s = join[0][c];
 #pragma unroll 8
-        for (int g = 1; g < kRows; ++g) s += join[g][c];
-        out[c] = s;
-      }
+      for (int i = 1; i < kRows; ++i) s += join[i][c];
+      out[c] = s;
     }
   }
 }
 
 // dX for rows of any length, one workgroup a row, which is read twice.
-template <bool kF16, bool kVec>
+template <bool kF16, bool kW32, bool kVec>
 __global__ __launch_bounds__(1024) void rms_bwd_long_kernel(BwdArgs a) {
   __shared__ float red[16];
   const int64_t at = (int64_t)blockIdx.x * a.k;
@@ -381,31 +445,40 @@ __global__ __launch_bounds__(1024) void rms_bwd_long_kernel(BwdArgs a) {
     float dy[8], h[8], w[8];
     unpack8<kF16>(load8h<kVec>(a.dY + at, c, a.k), dy);
     unpack8<kF16>(load8h<kVec>(a.H + at, c, a.k), h);
-    gain8<kF16>(load_gain<kVec>(a.w, a.w32, c, a.k), a.w32, w);
+    gain8<kF16>(load_gain<kW32, kVec>(a.w, c, a.k), w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(dy[i] * (h[i] * rstd), w[i], s);
   }
   const float dot = row_sum<1024>(s, red) * a.inv_k;
   for (int64_t c = 8 * threadIdx.x; c < a.k; c += 8192) {
     float w[8];
-    gain8<kF16>(load_gain<kVec>(a.w, a.w32, c, a.k), a.w32, w);
+    gain8<kF16>(load_gain<kW32, kVec>(a.w, c, a.k), w);
     const u32x4 r = a.R != nullptr ? load8h<kVec>(a.R + at, c, a.k) : u32x4{0u, 0u, 0u, 0u};
     store8h<kVec>(a.dX + at, c, a.k,
                   dx8<kF16>(load8h<kVec>(a.dY + at, c, a.k), load8h<kVec>(a.H + at, c, a.k), r, a.R != nullptr, rstd, dot, w));
   }
 }
 
-// dw's partial sums for rows of any length: a column per lane, a range of rows
-// per workgroup row.
-template <bool kF16>
-__global__ __launch_bounds__(256) void rms_dw_long_kernel(BwdArgs a, int64_t rows) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// dw's partial sums apart from dX, for rows that leave no registers for them: 8
+// columns per lane, a range of rows per workgroup row.
+template <bool kF16, bool kVec>
+__global__ __launch_bounds__(256) void rms_dw_part_kernel(BwdArgs a, int64_t rows) {
+  const int64_t c = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   const int64_t m0 = blockIdx.y * rows, m1 = m0 + rows < a.M ? m0 + rows : a.M;
   if (c >= a.k) return;
-  float s = 0.0f;
-  for (int64_t m = m0; m < m1; ++m)
-    s = fmaf(from16<kF16>(a.dY[m * a.k + c]), from16<kF16>(a.H[m * a.k + c]) * a.rstd[m], s);
-  a.part[blockIdx.y * a.k + c] = s;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int64_t m = m0; m < m1; ++m) {
+    float dy[8], h[8];
+    unpack8<kF16>(load8h<kVec>(a.dY + m * a.k, c, a.k), dy);
+    unpack8<kF16>(load8h<kVec>(a.H + m * a.k, c, a.k), h);
+    const float r = a.rstd[m];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += dy[i] * (h[i] * r);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < a.k) a.part[blockIdx.y * a.k + c + i] = s[i];
 }
 
 // dw (+)= the partial sums [parts][k], added in order: 64 columns per workgroup,
@@ -429,72 +502,87 @@ __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* __restrict__ 
   dw[c] = accumulate ? dw[c] + s : s;
 }
 
-template <bool kF16, bool kVec>
-void fwd_of(const FwdArgs& a, hipStream_t st) {
-#define QLORA_RMS(LPR, V) \
-  rms_fwd_kernel<kF16, LPR, V, kVec><<<(unsigned)cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR, 0, st>>>(a)
-  if (a.k > kInRegisters) rms_fwd_long_kernel<kF16, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
-  else if (a.k <= 128) QLORA_RMS(16, 1);
-  else if (a.k <= 512) QLORA_RMS(64, 1);
-  else if (a.k <= 1024) QLORA_RMS(64, 2);
-  else if (a.k <= 2048) QLORA_RMS(256, 1);
-  else if (a.k <= 4096) QLORA_RMS(256, 2);
-  else if (a.k <= 8192) QLORA_RMS(256, 4);
-  else if (a.k <= 16384) QLORA_RMS(512, 4);
-  else QLORA_RMS(1024, 4);
+template <bool kF16, bool kW32, bool kVec>
+struct Forward {
+  static void launch(const FwdArgs& a, hipStream_t st) {
+#define QLORA_RMS(LPR, V)                                                                                        \
+  rms_fwd_kernel<kF16, kW32, LPR, V, kVec>                                                                       \
+      <<<(unsigned)cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR, 0, st>>>(a)
+    if (a.k > kInRegisters) rms_fwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
+    else if (a.k <= 128) QLORA_RMS(16, 1);
+    else if (a.k <= 512) QLORA_RMS(64, 1);
+    else if (a.k <= 1024) QLORA_RMS(64, 2);
+    else if (a.k <= 2048) QLORA_RMS(256, 1);
+    else if (a.k <= 4096) QLORA_RMS(256, 2);
+    else if (a.k <= 8192) QLORA_RMS(256, 4);
+    else if (a.k <= 16384) QLORA_RMS(512, 4);
+    else QLORA_RMS(1024, 4);
 #undef QLORA_RMS
-}
+  }
+};
 
-// Workgroups of the backward with dw, and their threads: what a compute unit holds
-constexpr int kDwGroups = 256, kDwThreads = 1024;
+template <bool kF16, bool kW32, bool kVec>
+struct DxOnly {
+  static void launch(const BwdArgs& a, hipStream_t st) {
+#define QLORA_RMS(LPR, V)                                                                                        \
+  rms_dx_kernel<kF16, kW32, LPR, V, kVec>                                                                        \
+      <<<(unsigned)cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR, 0, st>>>(a)
+    if (a.k > kInRegisters) rms_bwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
+    else if (a.k <= 128) QLORA_RMS(16, 1);
+    else if (a.k <= 512) QLORA_RMS(64, 1);
+    else if (a.k <= 1024) QLORA_RMS(64, 2);
+    else if (a.k <= 2048) QLORA_RMS(256, 1);
+    else if (a.k <= 4096) QLORA_RMS(256, 2);
+    else if (a.k <= 8192) QLORA_RMS(256, 4);
+    else if (a.k <= 16384) QLORA_RMS(512, 4);
+    else QLORA_RMS(1024, 4);
+#undef QLORA_RMS
+  }
+};
 
-int dw_rows(int64_t k) {
-  return kDwThreads / (k <= 128 ? 16 : k <= 1024 ? 64 : k <= 2048 ? 256 : k <= 8192 ? 512 : 1024);
-}
+// Whether a workgroup holds a row and its sums of dw in registers (rows whose
+// length is no multiple of 8 take more of them).
+bool dw_with_dx(int64_t k) { return k <= (k % 8 == 0 ? 16384 : 8192); }
+
+// Rows that a workgroup of the backward with dw holds at a time.
+int dw_rows(int64_t k) { return k <= 128 ? 64 : k <= 512 ? 16 : k <= 1024 ? 8 : k <= 2048 ? 4 : k <= 4096 ? 2 : 1; }
 
 int dw_parts(int64_t M, int64_t k) {
-  const int64_t most = k > kInRegisters ? 64 : kDwGroups, need = k > kInRegisters ? M : cdiv(M, (int64_t)dw_rows(k));
+  const int64_t most = dw_with_dx(k) ? kDwGroups : 128, need = dw_with_dx(k) ? cdiv(M, (int64_t)dw_rows(k)) : M;
   return (int)(need < most ? need : most);
 }
 
-template <bool kF16, bool kVec>
-void bwd_of(const BwdArgs& a, hipStream_t st) {
-#define QLORA_RMS(LPR, V)                                                              \
-  {                                                                                    \
-    constexpr int kT = LPR < 256 ? 256 : LPR;                                          \
-    rms_bwd_kernel<kF16, LPR, V, kT, kVec, false>                                      \
-        <<<(unsigned)cdiv(a.M, (int64_t)(kT / LPR)), kT, 0, st>>>(a);                  \
-  }
-#define QLORA_RMS_DW(LPR, V) \
-  rms_bwd_kernel<kF16, LPR, V, kDwThreads, kVec, true><<<(unsigned)dw_parts(a.M, a.k), kDwThreads, 0, st>>>(a)
-  if (a.k > kInRegisters) {
-    if (a.dX != nullptr) rms_bwd_long_kernel<kF16, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
-    if (a.part != nullptr) {
-      const int64_t parts = dw_parts(a.M, a.k);
-      const dim3 grid((unsigned)cdiv(a.k, (int64_t)256), (unsigned)parts);
-      rms_dw_long_kernel<kF16><<<grid, 256, 0, st>>>(a, cdiv(a.M, parts));
-    }
-  } else if (a.part == nullptr) {
-    if (a.k <= 128) QLORA_RMS(16, 1)
-    else if (a.k <= 512) QLORA_RMS(64, 1)
-    else if (a.k <= 1024) QLORA_RMS(64, 2)
-    else if (a.k <= 2048) QLORA_RMS(256, 1)
-    else if (a.k <= 4096) QLORA_RMS(256, 2)
-    else if (a.k <= 8192) QLORA_RMS(256, 4)
-    else if (a.k <= 16384) QLORA_RMS(512, 4)
-    else QLORA_RMS(1024, 4)
-  } else {
-    if (a.k <= 128) QLORA_RMS_DW(16, 1);
-    else if (a.k <= 512) QLORA_RMS_DW(64, 1);
-    else if (a.k <= 1024) QLORA_RMS_DW(64, 2);
-    else if (a.k <= 2048) QLORA_RMS_DW(256, 1);
-    else if (a.k <= 4096) QLORA_RMS_DW(512, 1);
-    else if (a.k <= 8192) QLORA_RMS_DW(512, 2);
-    else if (a.k <= 16384) QLORA_RMS_DW(1024, 2);
-    else QLORA_RMS_DW(1024, 4);
-  }
+template <bool kF16, bool kW32, bool kVec>
+struct Backward {
+  static void launch(const BwdArgs& a, hipStream_t st) {
+    const int64_t parts = dw_parts(a.M, a.k);
+#define QLORA_RMS(LPR, V, T) rms_bwd_kernel<kF16, kW32, LPR, V, T, kVec><<<(unsigned)parts, T, 0, st>>>(a)
+    if (!dw_with_dx(a.k)) {
+      if (a.dX != nullptr) DxOnly<kF16, kW32, kVec>::launch(a, st);
+      const dim3 grid((unsigned)cdiv(a.k, (int64_t)2048), (unsigned)parts);
+      rms_dw_part_kernel<kF16, kVec><<<grid, 256, 0, st>>>(a, cdiv(a.M, parts));
+    } else if (a.k <= 128) QLORA_RMS(16, 1, 1024);
+    else if (a.k <= 512) QLORA_RMS(64, 1, 1024);
+    else if (a.k <= 1024) QLORA_RMS(128, 1, 1024);
+    else if (a.k <= 2048) QLORA_RMS(256, 1, 1024);
+    else if (a.k <= 4096) QLORA_RMS(512, 1, 1024);
+    else if (a.k <= 8192) QLORA_RMS(1024, 1, 1024);
+    else if constexpr (kVec) QLORA_RMS(512, 4, 512);
 #undef QLORA_RMS
-#undef QLORA_RMS_DW
+  }
+};
+
+// The variant for the types and the rows' alignment.
+template <template <bool, bool, bool> class Op, typename Args>
+void launch(const Args& a, bool f16, bool w32, hipStream_t st) {
+  const bool vec = a.k % 8 == 0;
+  if (f16) {
+    if (w32) vec ? Op<true, true, true>::launch(a, st) : Op<true, true, false>::launch(a, st);
+    else vec ? Op<true, false, true>::launch(a, st) : Op<true, false, false>::launch(a, st);
+  } else {
+    if (w32) vec ? Op<false, true, true>::launch(a, st) : Op<false, true, false>::launch(a, st);
+    else vec ? Op<false, false, true>::launch(a, st) : Op<false, false, false>::launch(a, st);
+  }
 }
 
 }  // namespace
@@ -502,10 +590,8 @@ void bwd_of(const BwdArgs& a, hipStream_t st) {
 hipError_t launch_rms_fwd(const uint16_t* X, const uint16_t* R, const void* w, bool w32, int64_t M, int64_t k, float eps,
                           uint16_t* Y, uint16_t* H, float* rstd, uint8_t* codes, uint8_t* scale, hipStream_t st, bool f16) {
   if (codes != nullptr && k % 64 != 0) return hipErrorInvalidValue;
-  const FwdArgs a = {X, R, w, w32, M, k, codes != nullptr ? f8_pad(k) : k, 1.0f / (float)k, eps, Y, H, rstd, codes, scale};
-  const bool vec = k % 8 == 0;
-  if (f16) vec ? fwd_of<true, true>(a, st) : fwd_of<true, false>(a, st);
-  else vec ? fwd_of<false, true>(a, st) : fwd_of<false, false>(a, st);
+  const FwdArgs a = {X, R, w, M, k, codes != nullptr ? f8_pad(k) : k, 1.0f / (float)k, eps, Y, H, rstd, codes, scale};
+  launch<Forward>(a, f16, w32, st);
   return hipGetLastError();
 }
 
@@ -514,10 +600,9 @@ size_t rms_bwd_ws_bytes(int64_t M, int64_t k) { return (size_t)dw_parts(M, k) * 
 hipError_t launch_rms_bwd(const uint16_t* dY, const uint16_t* H, const float* rstd, const void* w, bool w32,
                           const uint16_t* R, int64_t M, int64_t k, uint16_t* dX, float* dw, int accumulate, float* part,
                           hipStream_t st, bool f16) {
-  const BwdArgs a = {dY, H, R, rstd, w, w32, M, k, 1.0f / (float)k, dX, dw != nullptr ? part : nullptr};
-  const bool vec = k % 8 == 0;
-  if (f16) vec ? bwd_of<true, true>(a, st) : bwd_of<true, false>(a, st);
-  else vec ? bwd_of<false, true>(a, st) : bwd_of<false, false>(a, st);
+  const BwdArgs a = {dY, H, R, rstd, w, M, k, 1.0f / (float)k, dX, dw != nullptr ? part : nullptr};
+  if (dw != nullptr) launch<Backward>(a, f16, w32, st);
+  else launch<DxOnly>(a, f16, w32, st);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && dw != nullptr) {
     rms_dw_kernel<<<(unsigned)cdiv(k, (int64_t)64), 1024, 0, st>>>(part, dw_parts(M, k), k, dw, accumulate);
