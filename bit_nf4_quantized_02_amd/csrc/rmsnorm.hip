@@ -37,25 +37,41 @@ __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, i
   }
 }
 
-// A row of n 16-bit values, read and written in runs of eight by the kLpr lanes
-// that hold it. Where a wave has one row only, through a buffer descriptor of the
-// row: its range check replaces a branch at each run (a load behind one waits
-// for the one before it), and the addresses take no vector registers.
+// Row m of [M, k] 16-bit values, read and written in runs of eight by the kLpr
+// lanes that hold it. Rows of a multiple of 8 go through buffer descriptors, whose
+// range check replaces a branch at each run (a load behind one waits for the one
+// before it) and whose addresses take few vector registers: a descriptor of the
+// row where a wave has one only, else of the wave's rows. A row past the last
+// reads as zeros that way; without a descriptor it reads as the last one, and is
+// not to be stored.
 template <int kLpr, bool kVec>
 struct RowOf {
-  static constexpr bool kBuffer = kVec && kLpr >= 64;
+  static_assert(kLpr == 16 || kLpr >= 64, "a wave has one row or four");
   i32x4 rs;
+  int off;
   uint16_t* p;
   int64_t n;
-  __device__ __forceinline__ RowOf(const uint16_t* base, int64_t m, int64_t k) : p(const_cast<uint16_t*>(base) + m * k), n(k) {
-    if constexpr (kBuffer) rs = make_rsrc(p, 2 * k);
+  __device__ __forceinline__ RowOf(const uint16_t* base, int64_t m, int64_t M, int64_t k, int t) {
+    uint16_t* const b = const_cast<uint16_t*>(base);
+    if constexpr (!kVec) {
+      p = b + (m < M ? m : M - 1) * k;
+      n = k;
+    } else if constexpr (kLpr >= 64) {
+      rs = make_rsrc(b + m * k, m < M ? 2 * k : 0);
+      off = 16 * t;
+    } else {
+      const int lead = (threadIdx.x & 63) / kLpr;  // the wave's rows before this one
+      const int64_t left = M - (m - lead);
+      rs = make_rsrc(b + (m - lead) * k, left > 0 ? 2 * k * (left < 4 ? left : 4) : 0);
+      off = 8 * t < k ? (int)(2 * k) * lead + 16 * t : -1;  // (past every row)
+    }
   }
   __device__ __forceinline__ u32x4 load(int t, int v) const {
-    if constexpr (kBuffer) return raw_buffer_load_b128(rs, 16 * t, 16 * kLpr * v, 0);
+    if constexpr (kVec) return raw_buffer_load_b128(rs, off, 16 * kLpr * v, 0);
     else return load8h<kVec>(p, 8 * (t + kLpr * v), n);
   }
   __device__ __forceinline__ void store(int t, int v, const u32x4& x) const {
-    if constexpr (kBuffer) raw_buffer_store_b128(x, rs, 16 * t, 16 * kLpr * v, 0);
+    if constexpr (kVec) raw_buffer_store_b128(x, rs, off, 16 * kLpr * v, 0);
     else store8h<kVec>(p, 8 * (t + kLpr * v), n, x);
   }
 };
@@ -220,21 +236,20 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
   const int t = threadIdx.x & (kLpr - 1);
   const int64_t m = (int64_t)blockIdx.x * (kThreads / kLpr) + group_of<kLpr>();
   const bool live = m < a.M;
-  const int64_t mr = live ? m : a.M - 1;
-  const RowOf<kLpr, kVec> X(a.X, mr, a.k);
+  const RowOf<kLpr, kVec> X(a.X, m, a.M, a.k, t);
   u32x4 h[kV], r[kV];
   Gain<kW32> g[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) h[v] = X.load(t, v);
   if (a.R != nullptr) {
-    const RowOf<kLpr, kVec> R(a.R, mr, a.k);
+    const RowOf<kLpr, kVec> R(a.R, m, a.M, a.k, t);
 #pragma unroll
     for (int v = 0; v < kV; ++v) r[v] = R.load(t, v);
   }
 #pragma unroll
   for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
   if (a.R != nullptr) {
-    const RowOf<kLpr, kVec> H(a.H, mr, a.k);
+    const RowOf<kLpr, kVec> H(a.H, m, a.M, a.k, t);
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       h[v] = add8<kF16>(h[v], r[v]);
@@ -247,7 +262,7 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
   const float rstd = 1.0f / sqrtf(fmaf(row_sum<kLpr>(s, red), a.inv_k, a.eps));
   if (!live) return;
   if (t == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
-  const RowOf<kLpr, kVec> Y(a.Y, mr, a.k);
+  const RowOf<kLpr, kVec> Y(a.Y, m, a.M, a.k, t);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     const int64_t c = 8 * (t + kLpr * v);
@@ -317,15 +332,20 @@ struct RowRegs {
 
 template <int kLpr, int kV, bool kVec>
 __device__ __forceinline__ void load_row(const BwdArgs& a, int64_t m, int t, RowRegs<kV>& x) {
-  const RowOf<kLpr, kVec> dY(a.dY, m, a.k), H(a.H, m, a.k), R(a.R, m, a.R != nullptr ? a.k : 0);
+  const RowOf<kLpr, kVec> dY(a.dY, m, a.M, a.k, t), H(a.H, m, a.M, a.k, t);
 #pragma unroll
   for (int v = 0; v < kV; ++v) x.dy[v] = dY.load(t, v);
 #pragma unroll
   for (int v = 0; v < kV; ++v) x.h[v] = H.load(t, v);
+  if (kVec || a.R != nullptr) {
+    const RowOf<kLpr, kVec> R(a.R, m, a.R != nullptr ? a.M : 0, a.k, t);  // (no R: rows past the last)
 #pragma unroll
-  for (int v = 0; v < kV; ++v)
-    x.r[v] = RowOf<kLpr, kVec>::kBuffer || a.R != nullptr ? R.load(t, v) : u32x4{0u, 0u, 0u, 0u};  // (no R: a row of no columns)
-  x.rstd = a.rstd[m];
+    for (int v = 0; v < kV; ++v) x.r[v] = R.load(t, v);
+  } else {
+#pragma unroll
+    for (int v = 0; v < kV; ++v) x.r[v] = u32x4{0u, 0u, 0u, 0u};
+  }
+  x.rstd = a.rstd[m < a.M ? m : a.M - 1];
 }
 
 // A row's dx from its registers; kDw: dy hn added to acc. Every thread of the
@@ -349,7 +369,7 @@ __device__ __forceinline__ void do_row(const BwdArgs& a, int64_t m, bool live, i
   }
   const float dot = row_sum<kLpr>(s, red) * a.inv_k;
   if (!live || a.dX == nullptr) return;
-  const RowOf<kLpr, kVec> dX(a.dX, m, a.k);
+  const RowOf<kLpr, kVec> dX(a.dX, m, a.M, a.k, t);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     // (unpacked again: kept from above, the fp32 values take twice the registers)
@@ -370,7 +390,7 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_dx_kernel(BwdArgs
   RowRegs<kV> x;
   Gain<kW32> g[kV];
   float none[1][8];
-  load_row<kLpr, kV, kVec>(a, m < a.M ? m : a.M - 1, t, x);
+  load_row<kLpr, kV, kVec>(a, m, t, x);
 #pragma unroll
   for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
   do_row<kF16, kW32, kLpr, kV, kVec, false>(a, m, m < a.M, t, x, g, none, red);
@@ -394,7 +414,7 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
     for (int i = 0; i < 8; ++i) acc[v][i] = 0.0f;
   }
   const int64_t step = (int64_t)gridDim.x * kRows;
-  const auto load = [&](int64_t m, RowRegs<kV>& x) { load_row<kLpr, kV, kVec>(a, m < a.M ? m : a.M - 1, t, x); };
+  const auto load = [&](int64_t m, RowRegs<kV>& x) { load_row<kLpr, kV, kVec>(a, m, t, x); };
   const auto row = [&](int64_t m, RowRegs<kV>& x, int turn) {
     do_row<kF16, kW32, kLpr, kV, kVec, true>(a, m, m < a.M, t, x, g, acc, red[turn]);
   };
@@ -403,7 +423,7 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   RowRegs<kV> x0, x1;
   load(m, x0);
   for (; left > 0; left -= 2, m += 2 * step) {
-    load(m + step, x1);  // (past the last row: that one again)
+    load(m + step, x1);
     row(m, x0, 0);
     if (left == 1) break;
     load(m + 2 * step, x0);
