@@ -37,7 +37,24 @@ __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, i
   }
 }
 
-// Row m of [M, k] 16-bit values, read and written in runs of eight by the kLpr
+// A wave's first row and, where it has four, the lane's place among them.
+struct Place {
+  int64_t first;  // (the same in all lanes)
+  int lead;
+  __device__ __forceinline__ int64_t row() const { return first + lead; }
+  __device__ __forceinline__ Place after(int64_t rows) const { return Place{first + rows, lead}; }
+};
+
+// The thread's place in a workgroup whose first row is m0.
+template <int kLpr>
+__device__ __forceinline__ Place place_of(int64_t m0) {
+  static_assert(kLpr == 16 || kLpr >= 64, "a wave has one row or four");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if constexpr (kLpr >= 64) return Place{m0 + wave / (kLpr / 64), 0};
+  else return Place{m0 + 4 * wave, (int)(threadIdx.x & 63) / 16};
+}
+
+// A row of [M, k] 16-bit values, read and written in runs of eight by the kLpr
 // lanes that hold it. Rows of a multiple of 8 go through buffer descriptors, whose
 // range check replaces a branch at each run (a load behind one waits for the one
 // before it) and whose addresses take few vector registers: a descriptor of the
@@ -46,24 +63,20 @@ __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, i
 // not to be stored.
 template <int kLpr, bool kVec>
 struct RowOf {
-  static_assert(kLpr == 16 || kLpr >= 64, "a wave has one row or four");
   i32x4 rs;
   int off;
   uint16_t* p;
   int64_t n;
-  __device__ __forceinline__ RowOf(const uint16_t* base, int64_t m, int64_t M, int64_t k, int t) {
+  __device__ __forceinline__ RowOf(const uint16_t* base, const Place& at, int64_t M, int64_t k, int t) {
     uint16_t* const b = const_cast<uint16_t*>(base);
     if constexpr (!kVec) {
-      p = b + (m < M ? m : M - 1) * k;
+      p = b + (at.row() < M ? at.row() : M - 1) * k;
       n = k;
-    } else if constexpr (kLpr >= 64) {
-      rs = make_rsrc(b + m * k, m < M ? 2 * k : 0);
-      off = 16 * t;
     } else {
-      const int lead = (threadIdx.x & 63) / kLpr;  // the wave's rows before this one
-      const int64_t left = M - (m - lead);
-      rs = make_rsrc(b + (m - lead) * k, left > 0 ? 2 * k * (left < 4 ? left : 4) : 0);
-      off = 8 * t < k ? (int)(2 * k) * lead + 16 * t : -1;  // (past every row)
+      constexpr int kRows = kLpr < 64 ? 4 : 1;
+      const int64_t left = M - at.first;
+      rs = make_rsrc(b + at.first * k, left > 0 ? 2 * k * (left < kRows ? left : kRows) : 0);
+      off = kRows == 1 ? 16 * t : 8 * t < k ? 2 * (int)k * at.lead + 16 * t : -1;  // (-1: past every row)
     }
   }
   __device__ __forceinline__ u32x4 load(int t, int v) const {
@@ -211,14 +224,6 @@ __device__ __forceinline__ void encode8(const u32x4& y, int64_t m, int64_t c, in
   if ((c & (kF8Block - 1)) == 0) scale[m * (kp / kF8Block) + c / kF8Block] = (uint8_t)b;
 }
 
-// Which of the workgroup's rows the thread is one of (the same for a wave, where
-// it has one only).
-template <int kLpr>
-__device__ __forceinline__ int group_of() {
-  const int g = threadIdx.x / kLpr;
-  return kLpr >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
-}
-
 struct FwdArgs {
   const uint16_t *X, *R;  // R: the residual, or NULL
   const void* w;
@@ -234,22 +239,23 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
   constexpr int kThreads = kLpr < 256 ? 256 : kLpr;
   __shared__ float red[kThreads / 64];
   const int t = threadIdx.x & (kLpr - 1);
-  const int64_t m = (int64_t)blockIdx.x * (kThreads / kLpr) + group_of<kLpr>();
+  const Place at = place_of<kLpr>((int64_t)blockIdx.x * (kThreads / kLpr));
+  const int64_t m = at.row();
   const bool live = m < a.M;
-  const RowOf<kLpr, kVec> X(a.X, m, a.M, a.k, t);
+  const RowOf<kLpr, kVec> X(a.X, at, a.M, a.k, t);
   u32x4 h[kV], r[kV];
   Gain<kW32> g[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) h[v] = X.load(t, v);
   if (a.R != nullptr) {
-    const RowOf<kLpr, kVec> R(a.R, m, a.M, a.k, t);
+    const RowOf<kLpr, kVec> R(a.R, at, a.M, a.k, t);
 #pragma unroll
     for (int v = 0; v < kV; ++v) r[v] = R.load(t, v);
   }
 #pragma unroll
   for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
   if (a.R != nullptr) {
-    const RowOf<kLpr, kVec> H(a.H, m, a.M, a.k, t);
+    const RowOf<kLpr, kVec> H(a.H, at, a.M, a.k, t);
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       h[v] = add8<kF16>(h[v], r[v]);
@@ -262,7 +268,7 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
   const float rstd = 1.0f / sqrtf(fmaf(row_sum<kLpr>(s, red), a.inv_k, a.eps));
   if (!live) return;
   if (t == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
-  const RowOf<kLpr, kVec> Y(a.Y, m, a.M, a.k, t);
+  const RowOf<kLpr, kVec> Y(a.Y, at, a.M, a.k, t);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     const int64_t c = 8 * (t + kLpr * v);
@@ -331,28 +337,29 @@ struct RowRegs {
 };
 
 template <int kLpr, int kV, bool kVec>
-__device__ __forceinline__ void load_row(const BwdArgs& a, int64_t m, int t, RowRegs<kV>& x) {
-  const RowOf<kLpr, kVec> dY(a.dY, m, a.M, a.k, t), H(a.H, m, a.M, a.k, t);
+__device__ __forceinline__ void load_row(const BwdArgs& a, const Place& at, int t, RowRegs<kV>& x) {
+  const RowOf<kLpr, kVec> dY(a.dY, at, a.M, a.k, t), H(a.H, at, a.M, a.k, t);
 #pragma unroll
   for (int v = 0; v < kV; ++v) x.dy[v] = dY.load(t, v);
 #pragma unroll
   for (int v = 0; v < kV; ++v) x.h[v] = H.load(t, v);
   if (kVec || a.R != nullptr) {
-    const RowOf<kLpr, kVec> R(a.R, m, a.R != nullptr ? a.M : 0, a.k, t);  // (no R: rows past the last)
+    const RowOf<kLpr, kVec> R(a.R, at, a.R != nullptr ? a.M : 0, a.k, t);  // (no R: rows past the last)
 #pragma unroll
     for (int v = 0; v < kV; ++v) x.r[v] = R.load(t, v);
   } else {
 #pragma unroll
     for (int v = 0; v < kV; ++v) x.r[v] = u32x4{0u, 0u, 0u, 0u};
   }
-  x.rstd = a.rstd[m < a.M ? m : a.M - 1];
+  x.rstd = a.rstd[at.row() < a.M ? at.row() : a.M - 1];
 }
 
 // A row's dx from its registers; kDw: dy hn added to acc. Every thread of the
-// workgroup calls (row_sum). live: the row is one of the M.
+// workgroup calls (row_sum).
 template <bool kF16, bool kW32, int kLpr, int kV, bool kVec, bool kDw>
-__device__ __forceinline__ void do_row(const BwdArgs& a, int64_t m, bool live, int t, RowRegs<kV>& x, const Gain<kW32> (&g)[kV],
+__device__ __forceinline__ void do_row(const BwdArgs& a, const Place& at, int t, RowRegs<kV>& x, const Gain<kW32> (&g)[kV],
                                        float (&acc)[kDw ? kV : 1][8], float* red) {
+  const bool live = at.row() < a.M;
   float s = 0.0f;
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
@@ -369,7 +376,7 @@ __device__ __forceinline__ void do_row(const BwdArgs& a, int64_t m, bool live, i
   }
   const float dot = row_sum<kLpr>(s, red) * a.inv_k;
   if (!live || a.dX == nullptr) return;
-  const RowOf<kLpr, kVec> dX(a.dX, m, a.M, a.k, t);
+  const RowOf<kLpr, kVec> dX(a.dX, at, a.M, a.k, t);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     // (unpacked again: kept from above, the fp32 values take twice the registers)
@@ -385,15 +392,15 @@ template <bool kF16, bool kW32, int kLpr, int kV, bool kVec>
 __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_dx_kernel(BwdArgs a) {
   constexpr int kThreads = kLpr < 256 ? 256 : kLpr;
   __shared__ float red[kThreads / 64];
-  const int t = threadIdx.x & (kLpr - 1), group = group_of<kLpr>();
-  const int64_t m = (int64_t)blockIdx.x * (kThreads / kLpr) + group;
+  const int t = threadIdx.x & (kLpr - 1);
+  const Place at = place_of<kLpr>((int64_t)blockIdx.x * (kThreads / kLpr));
   RowRegs<kV> x;
   Gain<kW32> g[kV];
   float none[1][8];
-  load_row<kLpr, kV, kVec>(a, m, t, x);
+  load_row<kLpr, kV, kVec>(a, at, t, x);
 #pragma unroll
   for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
-  do_row<kF16, kW32, kLpr, kV, kVec, false>(a, m, m < a.M, t, x, g, none, red);
+  do_row<kF16, kW32, kLpr, kV, kVec, false>(a, at, t, x, g, none, red);
 }
 
 // dX and dw: kThreads threads hold kThreads / kLpr rows at a time and walk
@@ -404,7 +411,7 @@ template <bool kF16, bool kW32, int kLpr, int kV, int kThreads, bool kVec>
 __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   constexpr int kRows = kThreads / kLpr, kCols = 8 * kLpr * kV;
   __shared__ float red[2][kThreads / 64];  // in turn: one barrier a row
-  const int t = threadIdx.x & (kLpr - 1), group = group_of<kLpr>();
+  const int t = threadIdx.x & (kLpr - 1);
   Gain<kW32> g[kV];
   float acc[kV][8];
 #pragma unroll
@@ -414,20 +421,22 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
     for (int i = 0; i < 8; ++i) acc[v][i] = 0.0f;
   }
   const int64_t step = (int64_t)gridDim.x * kRows;
-  const auto load = [&](int64_t m, RowRegs<kV>& x) { load_row<kLpr, kV, kVec>(a, m, t, x); };
-  const auto row = [&](int64_t m, RowRegs<kV>& x, int turn) {
-    do_row<kF16, kW32, kLpr, kV, kVec, true>(a, m, m < a.M, t, x, g, acc, red[turn]);
+  const auto load = [&](const Place& at, RowRegs<kV>& x) { load_row<kLpr, kV, kVec>(a, at, t, x); };
+  const auto row = [&](const Place& at, RowRegs<kV>& x, int turn) {
+    do_row<kF16, kW32, kLpr, kV, kVec, true>(a, at, t, x, g, acc, red[turn]);
   };
-  int64_t m = (int64_t)blockIdx.x * kRows + group;
-  int64_t left = (a.M - (int64_t)blockIdx.x * kRows + step - 1) / step;  // rows of the workgroup's first group
+  const int64_t m0 = (int64_t)blockIdx.x * kRows;
+  Place at = place_of<kLpr>(m0);
   RowRegs<kV> x0, x1;
-  load(m, x0);
-  for (; left > 0; left -= 2, m += 2 * step) {
-    load(m + step, x1);
-    row(m, x0, 0);
+  load(at, x0);
+  for (int64_t left = (a.M - m0 + step - 1) / step; left > 0; left -= 2) {
+    load(at.after(step), x1);
+    row(at, x0, 0);
     if (left == 1) break;
-    load(m + 2 * step, x0);
-    row(m + step, x1, 1);
+    at = at.after(step);
+    load(at.after(step), x0);
+    row(at, x1, 1);
+    at = at.after(step);
   }
   float* const out = a.part + (int64_t)blockIdx.x * a.k;
   if constexpr (kRows == 1) {
@@ -443,7 +452,7 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
 #pragma unroll
     for (int v = 0; v < kV; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) join[group][8 * (t + kLpr * v) + i] = acc[v][i];
+      for (int i = 0; i < 8; ++i) join[threadIdx.x / kLpr][8 * (t + kLpr * v) + i] = acc[v][i];
     __syncthreads();
     for (int c = threadIdx.x; c < kCols && c < a.k; c += kThreads) {
       float s = join[0][c];
@@ -511,7 +520,7 @@ __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* __restrict__ 
   const int each = (parts + 15) / 16, p1 = (range + 1) * each < parts ? (range + 1) * each : parts;
   float s = 0.0f;
   if (c < k) {
-#pragma unroll 8
+#pragma unroll 16
     for (int p = range * each; p < p1; ++p) s += part[(int64_t)p * k + c];
   }
   join[range][lane] = s;
