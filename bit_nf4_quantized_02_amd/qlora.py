@@ -865,8 +865,9 @@ def rms_norm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float, residual: torch.T
     if residual is None and H is not None:
         raise ValueError("H: given without a residual")
     with _on(stream, dev):
-        Y = _out(Y, want_y, dt, (M, k), "Y", dev)
-        H = _out(H, residual is not None, dt, (M, k), "H", dev)
+        # (empty_like is half the host's time of empty)
+        Y = torch.empty_like(X) if Y is None and want_y else _out(Y, False, dt, (M, k), "Y", dev)
+        H = torch.empty_like(X) if H is None and residual is not None else _out(H, False, dt, (M, k), "H", dev)
         rstd = _out(rstd, save, torch.float32, (M,), "rstd", dev)
         s8 = None
         if x8 is None and want_x8:
@@ -898,7 +899,7 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, w: torch
     _given(dres, dt, (M, k), "dres", dev)
     wt = _gain(w, dt, k, dev)
     with _on(stream, dev):
-        dX = _out(dX, need_dX, dt, (M, k), "dX", dev)
+        dX = torch.empty_like(dY) if dX is None and need_dX else _out(dX, False, dt, (M, k), "dX", dev)
         dw = _out(dw, need_dw, torch.float32, (k,), "dw", dev, zeros=accumulate)
         need = int(_lib.qlora_rms_norm_bwd_workspace_bytes(M, k)) if ws is None and dw is not None else 0
         ws = _workspace(ws, need, dev)

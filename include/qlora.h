@@ -850,7 +850,8 @@ size_t qlora_param_table_bytes(const qlora_param *params, int64_t n);
  * *table. Pure host code, no launch. Errors: INVALID_ARG (NULL or misaligned
  * pointers, bad types, some but not all of theta, m and v, states in pageable
  * host memory, a buffer that the step writes and another one that overlaps it),
- * SHAPE (a count below 0 or above 2^40, tensors or chunks of them above 2^22),
+ * SHAPE (a count below 0 or above 2^40, more than 2^22 tensors, or 2^23 chunks of
+ * 1024 elements),
  * WORKSPACE (image too small).
  */
 qlora_status qlora_param_table_build(const qlora_param *params, int64_t n, void *image, size_t image_bytes,

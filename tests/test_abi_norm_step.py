@@ -94,8 +94,8 @@ def _grad(at, count, dt=1):
 
 
 def test_table_of_gradients():
-    """Chunks of at most 4096 elements (16384 in large sets) that cover every tensor in order, none for an empty one."""
-    for counts, each in (([1, 4096, 4097, 0, 10000], 4096), ([5], 4096), ([(1 << 25) + 3, 40000], 16384)):
+    """Chunks of at most 1024 elements that cover every tensor in order, none for an empty one."""
+    for counts, each in (([1, 4096, 4097, 0, 10000], 1024), ([5], 1024), ([(1 << 20) + 3, 40000], 1024)):
         params = [_grad((1 << 30) * (i + 1), c) for i, c in enumerate(counts)]
         s, t, n, image = _table(params)
         chunks = sum(-(-c // each) for c in counts)
@@ -132,7 +132,7 @@ def test_gradient_norm_and_step_refusals():
     need = lib.qlora_grad_norm_workspace_bytes()
     norm = lambda t=ref, s=1.0, m=1.0, out=P, ws=P, n=need: lib.qlora_grad_norm(t, s, m, out, ws, n, None)  # noqa: E731
     bad_tables = [q._Table(None, 3, 100, 1), q._Table((1 << 24) + 8, 3, 100, 1), q._Table(1 << 24, -1, 100, 1),
-                  q._Table(1 << 24, (1 << 22) + 1, 100, 1)]
+                  q._Table(1 << 24, (1 << 23) + 1, 100, 1)]
     for kw in (dict(t=None), dict(s=0.0), dict(s=-1.0), dict(s=math.inf), dict(s=math.nan), dict(m=0.0), dict(m=-1.0),
                dict(m=math.nan), dict(out=None), dict(out=ODD), *(dict(t=ctypes.byref(b)) for b in bad_tables)):
         assert norm(**kw) == ARG, kw
