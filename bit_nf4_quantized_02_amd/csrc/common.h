@@ -268,9 +268,17 @@ __device__ __forceinline__ void copy16(const i32x4& r, uint32_t voff, int soff, 
 __device__ u32x4 raw_buffer_load_b128(i32x4 rsrc, int voffset, int soffset, int aux) __asm(
     "llvm.amdgcn.raw.buffer.load.v4i32");
 
-// 16 bytes per lane into a buffer; offsets at or past the descriptor's size are dropped.
 __device__ void raw_buffer_store_b128(u32x4 v, i32x4 rsrc, int voffset, int soffset, int aux) __asm(
     "llvm.amdgcn.raw.buffer.store.v4i32");
+
+// 16 bytes per lane into a buffer; offsets at or past the descriptor's size are
+// dropped. The whole offset is a vector register's: a store of more than 8 bytes
+// reads its data late, and where the scalar offset is a register the compiler
+// leaves no wait state before an instruction that overwrites the data (the first
+// of its words was then stored with the new value).
+__device__ __forceinline__ void buffer_store16(const i32x4& r, int voffset, const u32x4& v) {
+  raw_buffer_store_b128(v, r, voffset, 0, 0);
+}
 
 // Buffer loads of one byte / half-word / word (zero past the descriptor's
 // size). Unlike plain loads the compiler keeps them where they are issued:

@@ -84,7 +84,7 @@ struct RowOf {
     else return load8h<kVec>(p, 8 * (t + kLpr * v), n);
   }
   __device__ __forceinline__ void store(int t, int v, const u32x4& x) const {
-    if constexpr (kVec) raw_buffer_store_b128(x, rs, off, 16 * kLpr * v, 0);
+    if constexpr (kVec) buffer_store16(rs, off + 16 * kLpr * v, x);
     else store8h<kVec>(p, 8 * (t + kLpr * v), n, x);
   }
 };
