@@ -46,12 +46,18 @@ struct FwdWs {
 // small kernel adds them before it otherwise (a launch, about 4 us).
 bool gemv_adds(int64_t M, int64_t k, int r) { return (int64_t)fp8_prep_plan(M, k, M <= 16).splits * M * r * 4 <= 16384; }
 
+// Few tokens that come encoded: whether the GEMV reads them by row. For r > 0
+// the kernel before it brings them into operand order on its way (they cost the
+// GEMV more by row: 11008 x 4096 at 16 tokens 14.9 us against 10), for r = 0
+// that would be a launch of its own.
+bool gemv_of_rows(int64_t M, int r) { return r == 0 && M <= 8; }
+
 // rows: the activations come encoded (qlora_fp8_rows).
 size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, bool rows, Carver& cv, FwdWs& o) {
   o.proj = cv.take<float>((size_t)fp8_prep_plan(M, k, M <= 16).splits * M * r * 4);
   if (M <= 16) {
-    if (!rows) o.xq = cv.take<uint8_t>(fp8_gemv_codes_bytes(k));
-    if (!rows) o.xs = cv.take<uint8_t>(fp8_gemv_scale_bytes(k));
+    if (!rows || !gemv_of_rows(M, r)) o.xq = cv.take<uint8_t>(fp8_gemv_codes_bytes(k));
+    if (!rows || !gemv_of_rows(M, r)) o.xs = cv.take<uint8_t>(fp8_gemv_scale_bytes(k));
     o.T = cv.take<float>((size_t)M * r * 4);
     return cv.used;
   }
@@ -132,21 +138,24 @@ qlora_status fwd_impl(const qlora_fp8_weight* w, const qlora_fp8_rows* x8, const
   const int parts = fp8_prep_plan(M, k, few).splits;
   hipError_t e = hipSuccess;
   if (r > 0 && !few) e = launch_factors(a, 0, k, f8_pad(k), r, o.Ao, b, n, o.Bx, st);
-  if (e == hipSuccess && (!rows || r > 0)) e = launch_fp8_prep(x, M, k, few ? a : o.Ao, r, o.xq, o.xs, o.proj, few, st, f16);
-  const uint8_t *const xq = rows ? x8->codes : o.xq, *const xs = rows ? x8->scale : o.xs;
+  const bool by_row = rows && few && gemv_of_rows(M, r);
+  if (e == hipSuccess && !by_row)
+    e = launch_fp8_prep(x, M, k, few ? a : o.Ao, r, o.xq, o.xs, o.proj, few, st, f16, 1, rows ? x8->codes : nullptr,
+                        rows ? x8->scale : nullptr);
+  const uint8_t* const xq = by_row || (rows && !few) ? x8->codes : o.xq;
+  const uint8_t* const xs = by_row ? x8->scale : o.xs;
   if (few) {
     if (r > 0 && !gemv_adds(M, k, r)) {
       float* const T = T_save ? T_save : o.T;
       if (e == hipSuccess) e = launch_rowdot_finalize(o.proj, parts, M, r, T, nullptr, scale, st, f16);
       if (e == hipSuccess)
-        e = launch_fp8_gemv(view8(w), xq, xs, rows, M, T, 1, b, r, scale, static_cast<uint16_t*>(Y), nullptr, st, f16);
+        e = launch_fp8_gemv(view8(w), xq, xs, by_row, M, T, 1, b, r, scale, static_cast<uint16_t*>(Y), nullptr, st, f16);
     } else if (e == hipSuccess) {
-      e = launch_fp8_gemv(view8(w), xq, xs, rows, M, o.proj, parts, b, r, scale, static_cast<uint16_t*>(Y), T_save, st, f16);
+      e = launch_fp8_gemv(view8(w), xq, xs, by_row, M, o.proj, parts, b, r, scale, static_cast<uint16_t*>(Y), T_save, st, f16);
     }
     return hip_status(e);
   }
   const int64_t nb = f8_pad(k) / kF8Block;
-  if (rows && e == hipSuccess) e = launch_fp8_scale_words(xs, M, nb, o.xs, st);
   if (r > 0 && e == hipSuccess)
     e = f16 ? launch_scaled_columns(o.proj, parts, 1, M, r, lora_extra_cols(r), scale, T_save, o.TS, o.rs, st)
             : launch_rowdot_finalize(o.proj, parts, M, r, T_save, o.TS, scale, st, false);

@@ -132,11 +132,15 @@ __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restri
 // turn and their projections are added in wave order.
 // Partials of the projection go to part [range][factor][M][r] (blockIdx.z: one of
 // several factors, each over all of P); codes NULL: only those.
+//   gscale (not NULL): P is encoded already, with scales [M, Cp / 128] in gscale
+// and codes [M, Cp] in gcodes; the scales are rewritten into the GEMM's words, few:
+// codes and scales into the GEMV's order. With kRP = 0 P is not read then.
 template <int kRP, bool kF16, bool kVec, bool kFew>
 __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restrict__ P, int64_t M, int64_t C, int64_t Cp,
                                                        const uint16_t* __restrict__ Q, int r, int bchunk,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scale,
-                                                       float* __restrict__ part) {
+                                                       float* __restrict__ part, const uint8_t* __restrict__ gcodes,
+                                                       const uint8_t* __restrict__ gscale) {
   constexpr int kTiles = kRP / 16, kTA = kTiles > 0 ? kTiles : 1;
   constexpr int kMR = kFew ? 1 : 2;
   constexpr int kPitch = 256 + 16;  // bytes per staged row (16 rows on distinct banks)
@@ -172,6 +176,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto load = [&](int kb, u32x4 (&x)[kMR][4]) {
+    if (kRP == 0 && gscale != nullptr) return;
     const int64_t c = (int64_t)kb * kF8Block + lc;
     if ((int64_t)(kb + 1) * kF8Block <= C) {  // (uniform: no load behind a test of its own)
 #pragma unroll
@@ -211,6 +216,18 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
       copy_q(kn, next);
       __builtin_amdgcn_sched_barrier(0);  // (copies before loads: the next barrier's wait counts the operations after them)
     }
+    uint32_t gs[kMR][4];
+    u32x2 gc[kFew ? kMR : 1][4];
+    if (gscale != nullptr) {
+#pragma unroll
+      for (int i = 0; i < kMR; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int64_t m = m0 + 16 * i + 4 * u + lr, mr = m < M ? m : M - 1;
+          gs[i][u] = gscale[mr * nb + kb];
+          if constexpr (kFew) gc[i][u] = *reinterpret_cast<const u32x2*>(gcodes + mr * Cp + (int64_t)kb * kF8Block + lc);
+        }
+    }
     load(kn, nx);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -221,40 +238,47 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
         if (kFew && m >= M) x[i][u] = u32x4{0u, 0u, 0u, 0u};
         if constexpr (kTiles > 0)
           *reinterpret_cast<u32x4*>(turn[wave] + (4 * u + lr) * kPitch + 2 * lc) = x[i][u];
-        if (codes != nullptr) {
-          // the row's largest magnitude, from the 16-bit patterns (two at a
-          // time, then the 16 lanes of the row by rotations within them)
-          u16x2 top = {0, 0};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[i][u][e] & 0x7FFF7FFFu));
-          uint32_t h = max((uint32_t)top[0], (uint32_t)top[1]);
-          h = row16_max(h);
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[2 * e] = from16<kF16>(x[i][u][e] & 0xFFFFu);
-            f[2 * e + 1] = from16<kF16>(x[i][u][e] >> 16);
-          }
-          if (__builtin_expect(__ballot(h >= (kF16 ? 0x7C00u : 0x7F80u)) != 0, 0)) {
-            // a value of some row is not finite: the maximum without such values
-            uint32_t a = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t v = f8_finite_abs(f[e]) != 0 ? (x[i][u][e >> 1] >> (16 * (e & 1))) & 0x7FFFu : 0u;
-              a = max(a, v);
-              if (isinf(f[e])) f[e] = __uint_as_float(0x7FC00000u);
+        if (codes != nullptr || gscale != nullptr) {
+          uint32_t b;
+          u32x2 o;
+          if (gscale != nullptr) {
+            b = gs[i][u];
+            if constexpr (kFew) o = m < M ? gc[i][u] : u32x2{0u, 0u};
+          } else {
+            // the row's largest magnitude, from the 16-bit patterns (two at a
+            // time, then the 16 lanes of the row by rotations within them)
+            u16x2 top = {0, 0};
+  #pragma unroll
+            for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[i][u][e] & 0x7FFF7FFFu));
+            uint32_t h = max((uint32_t)top[0], (uint32_t)top[1]);
+            h = row16_max(h);
+            float f[8];
+  #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[2 * e] = from16<kF16>(x[i][u][e] & 0xFFFFu);
+              f[2 * e + 1] = from16<kF16>(x[i][u][e] >> 16);
             }
-            h = row16_max(a);
+            if (__builtin_expect(__ballot(h >= (kF16 ? 0x7C00u : 0x7F80u)) != 0, 0)) {
+              // a value of some row is not finite: the maximum without such values
+              uint32_t a = 0;
+  #pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t v = f8_finite_abs(f[e]) != 0 ? (x[i][u][e >> 1] >> (16 * (e & 1))) & 0x7FFFu : 0u;
+                a = max(a, v);
+                if (isinf(f[e])) f[e] = __uint_as_float(0x7FC00000u);
+              }
+              h = row16_max(a);
+            }
+            b = f8_scale_byte(__float_as_uint(from16<kF16>(h)));
+            const float inv = f8_inv_scale(b);
+            o = u32x2{f8_pack4(f, inv), f8_pack4(f + 4, inv)};
           }
-          const uint32_t b = f8_scale_byte(__float_as_uint(from16<kF16>(h)));
-          const float inv = f8_inv_scale(b);
-          const u32x2 o = {f8_pack4(f, inv), f8_pack4(f + 4, inv)};
           if constexpr (kFew) {
             // columns lc .. of row m: lane m + 16 (lc / 32), its bytes lc % 32 ..
             *reinterpret_cast<u32x2*>(codes + ((int64_t)kb * 64 + 16 * (lc >> 5) + 4 * u + lr) * 32 + (lc & 31)) = o;
             if ((lane & 15) == 0) scale[kb * 16 + 4 * u + lr] = (uint8_t)b;
           } else if (m < M) {
-            *reinterpret_cast<u32x2*>(codes + m * Cp + (int64_t)kb * kF8Block + lc) = o;
+            if (gscale == nullptr) *reinterpret_cast<u32x2*>(codes + m * Cp + (int64_t)kb * kF8Block + lc) = o;
             if ((lane & 15) == 0) scale[((kb * mt + m / kF8Block) * 32 + (m & 31)) * 4 + ((m >> 5) & 3)] = (uint8_t)b;
           }
         }
@@ -341,22 +365,6 @@ hipError_t decode(const uint8_t* codes, const uint8_t* scale, int64_t n, int64_t
   return hipGetLastError();
 }
 
-// One lane a word: the scale bytes of rows +0, +32, +64, +96 of a 128-row tile
-// (rows from M on: the last, what is theirs is not stored).
-__global__ __launch_bounds__(256) void fp8_scale_words_kernel(const uint8_t* __restrict__ scale, int64_t M, int64_t nb,
-                                                              uint32_t* __restrict__ words) {
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, mt = cdiv(M, (int64_t)kF8Block);
-  if (q >= nb * mt * 32) return;
-  const int64_t row = q / nb, kb = q % nb, tile = row / 32, r = row % 32;
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = tile * kF8Block + r + 32 * i;
-    w |= (uint32_t)scale[(m < M ? m : M - 1) * nb + kb] << (8 * i);
-  }
-  words[(kb * mt + tile) * 32 + r] = w;
-}
-
 }  // namespace
 
 hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream) {
@@ -366,13 +374,6 @@ hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream
 hipError_t launch_fp8_decode_rows(const uint8_t* codes, const uint8_t* scale, int64_t M, int64_t k, uint16_t* out,
                                   hipStream_t stream, bool f16) {
   return f16 ? decode<true, true>(codes, scale, M, k, out, stream) : decode<true, false>(codes, scale, M, k, out, stream);
-}
-
-hipError_t launch_fp8_scale_words(const uint8_t* scale, int64_t M, int64_t nb, uint8_t* words, hipStream_t stream) {
-  const int64_t count = nb * cdiv(M, (int64_t)kF8Block) * 32;
-  fp8_scale_words_kernel<<<(unsigned)cdiv(count, (int64_t)256), 256, 0, stream>>>(scale, M, nb,
-                                                                                 reinterpret_cast<uint32_t*>(words));
-  return hipGetLastError();
 }
 
 size_t fp8_rows_scale_bytes(int64_t M, int64_t C) {
@@ -395,14 +396,16 @@ Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few, int W) {
 }
 
 hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r,
-                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16, int W) {
+                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16, int W,
+                           const uint8_t* gcodes, const uint8_t* gscale) {
   const Fp8Prep pl = fp8_prep_plan(M, C, few, W);
   const int64_t Cp = f8_pad(C);
   if (few && (C % 8 != 0 || M > 16)) return hipErrorInvalidValue;
-  if (W > 1 && (few || codes != nullptr)) return hipErrorInvalidValue;
+  if (W > 1 && (few || codes != nullptr || gscale != nullptr)) return hipErrorInvalidValue;
+  if (gscale != nullptr && (gcodes == nullptr || (codes != nullptr) != few)) return hipErrorInvalidValue;
   const dim3 grid(few ? 1u : (unsigned)cdiv(M, (int64_t)kPrepRows), (unsigned)pl.splits, (unsigned)W);
 #define QLORA_PREP3(RP, H, V, F) \
-  fp8_prep_kernel<RP, H, V, F><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, r, pl.chunk, codes, scale, part)
+  fp8_prep_kernel<RP, H, V, F><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, r, pl.chunk, codes, scale, part, gcodes, gscale)
 #define QLORA_PREP2(RP, H)                                                                             \
   {                                                                                                    \
     if (few) QLORA_PREP3(RP, H, true, true);                                                           \

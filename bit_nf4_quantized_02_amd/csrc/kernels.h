@@ -293,14 +293,17 @@ hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream
 // scale words; few, M <= 16: the GEMV's operand order, fp8_gemv_*_bytes),
 // and for r > 0 the partials [splits][W][M][r] of P Q^T; W factors in operand
 // order one after the other, for few one as it is, [r, C]. codes NULL (always
-// for W = 2): the projections only.
+// for W = 2): the projections only. gcodes, gscale: P's codes and scales by row
+// (qlora_fp8_rows), if it has them; its scales are then rewritten instead, and for
+// few its codes into `codes` (else NULL); P is not read for r = 0.
 struct Fp8Prep {
   int chunk, splits;
 };
 Fp8Prep fp8_prep_plan(int64_t M, int64_t C, bool few, int W = 1);
 size_t fp8_rows_scale_bytes(int64_t M, int64_t C);
 hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16_t* Q, int r,
-                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16, int W = 1);
+                           uint8_t* codes, uint8_t* scale, float* part, bool few, hipStream_t stream, bool f16, int W = 1,
+                           const uint8_t* gcodes = nullptr, const uint8_t* gscale = nullptr);
 // out = RN16([act | split] [f | fx]^T); f's scale byte of (output block,
 // contraction block) at ob * fs_o + cb * fs_c. nn: f is [kc, nout up to 128].
 // part: gemm_fp8_ws_bytes(). fp16 with kx > 0: row_scale as launch_scaled_columns'.
@@ -320,11 +323,9 @@ size_t fp8_gemv_scale_bytes(int64_t k);
 hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* xs, bool rows, int64_t M, const float* T,
                            int parts, const uint16_t* B, int r, float scale, uint16_t* Y, float* T_save,
                            hipStream_t stream, bool f16);
-// Activations encoded by row (qlora_fp8_rows): their values in 16 bits, and
-// their scales [M, nb] as the GEMM's scale words.
+// The values of activations encoded by row (qlora_fp8_rows), in 16 bits.
 hipError_t launch_fp8_decode_rows(const uint8_t* codes, const uint8_t* scale, int64_t M, int64_t k, uint16_t* out,
                                   hipStream_t stream, bool f16);
-hipError_t launch_fp8_scale_words(const uint8_t* scale, int64_t M, int64_t nb, uint8_t* words, hipStream_t stream);
 
 // ---- residual addition and root-mean-square norm (rmsnorm.hip)
 // R (with H) may be NULL, as may Y, rstd and codes (with scale; k % 64 == 0).
