@@ -21,14 +21,15 @@ namespace {
 
 constexpr int64_t kInRegisters = 32768;  // columns of a row that a workgroup holds
 
+// Columns that the lanes of a row have to hold: rows of no multiple of 8 are cut
+// up to 7 columns before they begin.
+int64_t held(int64_t k) { return k % 8 == 0 ? k : k + 7; }
+
 constexpr int kDwGroups = 256;  // workgroups of the backward with dw, at most: one for each compute unit
 
-// Eight 16-bit values into (row, c), nothing from n on.
-template <bool kVec>
+// Eight 16-bit values into (row, c) of any alignment, nothing from n on.
 __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, int64_t n, const u32x4& v) {
-  if constexpr (kVec) {
-    if (c < n) *reinterpret_cast<u32x4*>(row + c) = v;
-  } else if (c + 8 <= n) {
+  if (c + 8 <= n) {
     *reinterpret_cast<u32x4_any*>(row + c) = v;
   } else {
 #pragma unroll
@@ -55,37 +56,80 @@ __device__ __forceinline__ Place place_of(int64_t m0) {
 }
 
 // A row of [M, k] 16-bit values, read and written in runs of eight by the kLpr
-// lanes that hold it. Rows of a multiple of 8 go through buffer descriptors, whose
-// range check replaces a branch at each run (a load behind one waits for the one
-// before it) and whose addresses take few vector registers: a descriptor of the
-// row where a wave has one only, else of the wave's rows. A row past the last
-// reads as zeros that way; without a descriptor it reads as the last one, and is
-// not to be stored.
+// lanes that hold it: run v of lane t begins at column 8 (t + kLpr v) - shift.
+//
+// Rows go through buffer descriptors, whose range check replaces a branch at each
+// run (a load behind one waits for the one before it) and whose addresses take few
+// vector registers: a descriptor of the row where a wave has one only, else of
+// the wave's rows. A row past the last reads as zeros. Rows whose length is no
+// multiple of 8 (kVec false) start anywhere: their runs are cut at multiples of 16
+// bytes all the same, from `shift` columns before the row, so that loads and stores
+// are aligned (5001 columns: unaligned runs 72 us for 268 MB, 3.7 TB/s). finish()
+// clears what a run holds of the row before; the last column of an odd end, of
+// whose word half is out of range, is loaded apart (tail()).
+// Four short rows in a wave with such lengths are read and written by address.
 template <int kLpr, bool kVec>
 struct RowOf {
+  static constexpr bool kShift = !kVec && kLpr >= 64, kAddress = !kVec && kLpr < 64;
   i32x4 rs;
-  int off;
+  int off, shift, end;  // end: of the row, counted as the runs' columns + shift
   uint16_t* p;
-  int64_t n;
   __device__ __forceinline__ RowOf(const uint16_t* base, const Place& at, int64_t M, int64_t k, int t) {
     uint16_t* const b = const_cast<uint16_t*>(base);
-    if constexpr (!kVec) {
+    shift = 0;
+    if constexpr (kAddress) {
       p = b + (at.row() < M ? at.row() : M - 1) * k;
-      n = k;
+    } else if constexpr (kLpr >= 64) {
+      p = b + at.first * k;
+      if constexpr (kShift) shift = shift_of(at, k);
+      rs = make_rsrc(p - shift, at.first < M ? 2 * (k + shift) : 0);
+      off = 16 * t;
     } else {
-      constexpr int kRows = kLpr < 64 ? 4 : 1;
       const int64_t left = M - at.first;
-      rs = make_rsrc(b + at.first * k, left > 0 ? 2 * k * (left < kRows ? left : kRows) : 0);
-      off = kRows == 1 ? 16 * t : 8 * t < k ? 2 * (int)k * at.lead + 16 * t : -1;  // (-1: past every row)
+      rs = make_rsrc(b + at.first * k, left > 0 ? 2 * k * (left < 4 ? left : 4) : 0);
+      off = 8 * t < k ? 2 * (int)k * at.lead + 16 * t : -1;  // (-1: past every row)
     }
+    end = (int)k + shift;
+  }
+  static __device__ __forceinline__ int shift_of(const Place& at, int64_t k) {
+    return kShift ? (int)((at.first * k) & 7) : 0;
   }
   __device__ __forceinline__ u32x4 load(int t, int v) const {
-    if constexpr (kVec) return raw_buffer_load_b128(rs, off, 16 * kLpr * v, 0);
-    else return load8h<kVec>(p, 8 * (t + kLpr * v), n);
+    if constexpr (kAddress) return load8h<false>(p, 8 * (t + kLpr * v), end);
+    else return raw_buffer_load_b128(rs, off, 16 * kLpr * v, 0);
+  }
+  __device__ __forceinline__ uint32_t tail() const {
+    if constexpr (kShift) return end & 1 ? raw_buffer_load_u16(rs, 2 * end - 2, 0, 0) : 0u;
+    else return 0u;
+  }
+  static __device__ __forceinline__ void finish(u32x4& x, uint32_t tail, int shift, int64_t k, int t, int v) {
+    if constexpr (kShift) {
+      const int e = 8 * (t + kLpr * v), last = (int)k + shift - 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (v == 0) {
+          if (e + 2 * i < shift) x[i] &= 0xFFFF0000u;
+          if (e + 2 * i + 1 < shift) x[i] = 0u;
+        }
+        if (!(last & 1) && e + 2 * i == last) x[i] = tail;
+      }
+    }
   }
   __device__ __forceinline__ void store(int t, int v, const u32x4& x) const {
-    if constexpr (kVec) buffer_store16(rs, off + 16 * kLpr * v, x);
-    else store8h<kVec>(p, 8 * (t + kLpr * v), n, x);
+    if constexpr (kAddress) {
+      store8h(p, 8 * (t + kLpr * v), end, x);
+    } else if constexpr (!kShift) {
+      buffer_store16(rs, off + 16 * kLpr * v, x);
+    } else {
+      const int e = 8 * (t + kLpr * v);
+      const bool whole = e >= shift && e + 8 <= end;
+      buffer_store16(rs, whole ? off + 16 * kLpr * v : -1, x);
+      if (!whole && e < end) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e + i >= shift && e + i < end) p[e + i - shift] = (uint16_t)(x[i >> 1] >> (16 * (i & 1)));
+      }
+    }
   }
 };
 
@@ -95,22 +139,32 @@ struct Gain {
   u32x4 a[kW32 ? 2 : 1];
 };
 
+// (Columns outside the row get any gain of it: what they are multiplied with is
+// zero or not stored.)
 template <bool kW32, bool kVec>
 __device__ __forceinline__ Gain<kW32> load_gain(const void* __restrict__ w, int64_t c, int64_t n) {
   Gain<kW32> g;
-  if constexpr (!kW32) {
-    g.a[0] = load8h<kVec>(static_cast<const uint16_t*>(w), c, n);
-  } else {
-    const uint32_t* p = static_cast<const uint32_t*>(w);
-    if (c + 8 <= n) {
-      g.a[0] = *reinterpret_cast<const u32x4*>(p + c);
-      g.a[1] = *reinterpret_cast<const u32x4*>(p + c + 4);
+  if (kVec ? c < n : c >= 0 && c + 8 <= n) {
+    if constexpr (kW32) {
+      typedef u32x4 __attribute__((aligned(4))) u32x4_4;
+      const uint32_t* const p = static_cast<const uint32_t*>(w) + c;
+      g.a[0] = *reinterpret_cast<const u32x4_4*>(p);
+      g.a[1] = *reinterpret_cast<const u32x4_4*>(p + 4);
+    } else if constexpr (kVec) {
+      g.a[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(w) + c);
     } else {
+      g.a[0] = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(w) + c);
+    }
+    return g;
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t e = p[c + i < n ? c + i : n - 1];
-        g.a[i >> 2][i & 3] = c + i < n ? e : 0u;
-      }
+  for (int i = 0; i < (kW32 ? 2 : 1); ++i) g.a[i] = u32x4{0u, 0u, 0u, 0u};
+  if (!kVec && c < n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = c + i < 0 ? 0 : c + i < n ? c + i : n - 1;
+      if constexpr (kW32) g.a[i >> 2][i & 3] = static_cast<const uint32_t*>(w)[at];
+      else g.a[0][i >> 1] |= (uint32_t)static_cast<const uint16_t*>(w)[at] << (16 * (i & 1));
     }
   }
   return g;
@@ -242,22 +296,28 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
   const Place at = place_of<kLpr>((int64_t)blockIdx.x * (kThreads / kLpr));
   const int64_t m = at.row();
   const bool live = m < a.M;
-  const RowOf<kLpr, kVec> X(a.X, at, a.M, a.k, t);
+  typedef RowOf<kLpr, kVec> Row;
+  const Row X(a.X, at, a.M, a.k, t);
   u32x4 h[kV], r[kV];
+  uint32_t xt = X.tail(), rt = 0;
   Gain<kW32> g[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) h[v] = X.load(t, v);
   if (a.R != nullptr) {
-    const RowOf<kLpr, kVec> R(a.R, at, a.M, a.k, t);
+    const Row R(a.R, at, a.M, a.k, t);
+    rt = R.tail();
 #pragma unroll
     for (int v = 0; v < kV; ++v) r[v] = R.load(t, v);
   }
 #pragma unroll
-  for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
+  for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v) - X.shift, a.k);
+#pragma unroll
+  for (int v = 0; v < kV; ++v) Row::finish(h[v], xt, X.shift, a.k, t, v);
   if (a.R != nullptr) {
-    const RowOf<kLpr, kVec> H(a.H, at, a.M, a.k, t);
+    const Row H(a.H, at, a.M, a.k, t);
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
+      Row::finish(r[v], rt, X.shift, a.k, t, v);
       h[v] = add8<kF16>(h[v], r[v]);
       if (live) H.store(t, v, h[v]);
     }
@@ -268,7 +328,7 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
   const float rstd = 1.0f / sqrtf(fmaf(row_sum<kLpr>(s, red), a.inv_k, a.eps));
   if (!live) return;
   if (t == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
-  const RowOf<kLpr, kVec> Y(a.Y, at, a.M, a.k, t);
+  const Row Y(a.Y, at, a.M, a.k, t);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     const int64_t c = 8 * (t + kLpr * v);
@@ -290,7 +350,7 @@ __global__ __launch_bounds__(1024) void rms_fwd_long_kernel(FwdArgs a) {
     u32x4 h = load8h<kVec>(a.X + at, c, a.k);
     if (a.R != nullptr) {
       h = add8<kF16>(h, load8h<kVec>(a.R + at, c, a.k));
-      store8h<kVec>(a.H + at, c, a.k, h);
+      store8h(a.H + at, c, a.k, h);
     }
     s = squares8<kF16>(h, s);
   }
@@ -298,7 +358,7 @@ __global__ __launch_bounds__(1024) void rms_fwd_long_kernel(FwdArgs a) {
   if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
   for (int64_t c = 8 * threadIdx.x; c < a.kp; c += 8192) {  // (each thread reads what it wrote)
     const u32x4 y = normed8<kF16>(load8h<kVec>(in, c, a.k), rstd, load_gain<kW32, kVec>(a.w, c, a.k));
-    if (a.Y != nullptr) store8h<kVec>(a.Y + at, c, a.k, y);
+    if (a.Y != nullptr) store8h(a.Y + at, c, a.k, y);
     if (kVec && a.codes != nullptr) encode8<kF16>(y, m, c, a.kp, a.codes, a.scale);
   }
 }
@@ -333,18 +393,23 @@ __device__ __forceinline__ u32x4 dx8(const u32x4& dy, const u32x4& h, const u32x
 template <int kV>
 struct RowRegs {
   u32x4 dy[kV], h[kV], r[kV];
+  uint32_t tail[3];
   float rstd;
 };
 
 template <int kLpr, int kV, bool kVec>
 __device__ __forceinline__ void load_row(const BwdArgs& a, const Place& at, int t, RowRegs<kV>& x) {
   const RowOf<kLpr, kVec> dY(a.dY, at, a.M, a.k, t), H(a.H, at, a.M, a.k, t);
+  x.tail[0] = dY.tail();
+  x.tail[1] = H.tail();
+  x.tail[2] = 0;
 #pragma unroll
   for (int v = 0; v < kV; ++v) x.dy[v] = dY.load(t, v);
 #pragma unroll
   for (int v = 0; v < kV; ++v) x.h[v] = H.load(t, v);
-  if (kVec || a.R != nullptr) {
+  if (!RowOf<kLpr, kVec>::kAddress || a.R != nullptr) {
     const RowOf<kLpr, kVec> R(a.R, at, a.R != nullptr ? a.M : 0, a.k, t);  // (no R: rows past the last)
+    x.tail[2] = R.tail();
 #pragma unroll
     for (int v = 0; v < kV; ++v) x.r[v] = R.load(t, v);
   } else {
@@ -360,9 +425,13 @@ template <bool kF16, bool kW32, int kLpr, int kV, bool kVec, bool kDw>
 __device__ __forceinline__ void do_row(const BwdArgs& a, const Place& at, int t, RowRegs<kV>& x, const Gain<kW32> (&g)[kV],
                                        float (&acc)[kDw ? kV : 1][8], float* red) {
   const bool live = at.row() < a.M;
+  const int shift = RowOf<kLpr, kVec>::shift_of(at, a.k);
   float s = 0.0f;
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
+    RowOf<kLpr, kVec>::finish(x.dy[v], x.tail[0], shift, a.k, t, v);
+    RowOf<kLpr, kVec>::finish(x.h[v], x.tail[1], shift, a.k, t, v);
+    RowOf<kLpr, kVec>::finish(x.r[v], x.tail[2], shift, a.k, t, v);
     float dy[8], h[8], w[8];
     unpack8<kF16>(x.dy[v], dy);
     unpack8<kF16>(x.h[v], h);
@@ -399,7 +468,8 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_dx_kernel(BwdArgs
   float none[1][8];
   load_row<kLpr, kV, kVec>(a, at, t, x);
 #pragma unroll
-  for (int v = 0; v < kV; ++v) g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
+  for (int v = 0; v < kV; ++v)
+    g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v) - RowOf<kLpr, kVec>::shift_of(at, a.k), a.k);
   do_row<kF16, kW32, kLpr, kV, kVec, false>(a, at, t, x, g, none, red);
 }
 
@@ -412,11 +482,16 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   constexpr int kRows = kThreads / kLpr, kCols = 8 * kLpr * kV;
   __shared__ float red[2][kThreads / 64];  // in turn: one barrier a row
   const int t = threadIdx.x & (kLpr - 1);
+  const int64_t m0 = (int64_t)blockIdx.x * kRows;
+  Place at = place_of<kLpr>(m0);
+  // (the same for all rows of a lane: where it has more than one, they are a
+  // multiple of 8 apart)
+  const int shift = RowOf<kLpr, kVec>::shift_of(at, a.k);
   Gain<kW32> g[kV];
   float acc[kV][8];
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v), a.k);
+    g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v) - shift, a.k);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[v][i] = 0.0f;
   }
@@ -425,8 +500,6 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   const auto row = [&](const Place& at, RowRegs<kV>& x, int turn) {
     do_row<kF16, kW32, kLpr, kV, kVec, true>(a, at, t, x, g, acc, red[turn]);
   };
-  const int64_t m0 = (int64_t)blockIdx.x * kRows;
-  Place at = place_of<kLpr>(m0);
   RowRegs<kV> x0, x1;
   load(at, x0);
   for (int64_t left = (a.M - m0 + step - 1) / step; left > 0; left -= 2) {
@@ -444,15 +517,18 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
     for (int v = 0; v < kV; ++v)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int64_t c = 8 * (t + kLpr * v) + i;
-        if (c < a.k) out[c] = acc[v][i];
+        const int64_t c = 8 * (t + kLpr * v) + i - shift;
+        if (c >= 0 && c < a.k) out[c] = acc[v][i];
       }
   } else {
     __shared__ float join[kRows][kCols];
 #pragma unroll
     for (int v = 0; v < kV; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) join[threadIdx.x / kLpr][8 * (t + kLpr * v) + i] = acc[v][i];
+      for (int i = 0; i < 8; ++i) {
+        const int c = 8 * (t + kLpr * v) + i - shift;
+        if (c >= 0) join[threadIdx.x / kLpr][c] = acc[v][i];
+      }
     __syncthreads();
     for (int c = threadIdx.x; c < kCols && c < a.k; c += kThreads) {
       float s = join[0][c];
@@ -483,7 +559,7 @@ __global__ __launch_bounds__(1024) void rms_bwd_long_kernel(BwdArgs a) {
     float w[8];
     gain8<kF16>(load_gain<kW32, kVec>(a.w, c, a.k), w);
     const u32x4 r = a.R != nullptr ? load8h<kVec>(a.R + at, c, a.k) : u32x4{0u, 0u, 0u, 0u};
-    store8h<kVec>(a.dX + at, c, a.k,
+    store8h(a.dX + at, c, a.k,
                   dx8<kF16>(load8h<kVec>(a.dY + at, c, a.k), load8h<kVec>(a.H + at, c, a.k), r, a.R != nullptr, rstd, dot, w));
   }
 }
@@ -537,14 +613,15 @@ struct Forward {
 #define QLORA_RMS(LPR, V)                                                                                        \
   rms_fwd_kernel<kF16, kW32, LPR, V, kVec>                                                                       \
       <<<(unsigned)cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR, 0, st>>>(a)
-    if (a.k > kInRegisters) rms_fwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
-    else if (a.k <= 128) QLORA_RMS(16, 1);
-    else if (a.k <= 512) QLORA_RMS(64, 1);
-    else if (a.k <= 1024) QLORA_RMS(64, 2);
-    else if (a.k <= 2048) QLORA_RMS(256, 1);
-    else if (a.k <= 4096) QLORA_RMS(256, 2);
-    else if (a.k <= 8192) QLORA_RMS(256, 4);
-    else if (a.k <= 16384) QLORA_RMS(512, 4);
+    const int64_t k = held(a.k);
+    if (k > kInRegisters) rms_fwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
+    else if (k <= 128) QLORA_RMS(16, 1);
+    else if (k <= 512) QLORA_RMS(64, 1);
+    else if (k <= 1024) QLORA_RMS(64, 2);
+    else if (k <= 2048) QLORA_RMS(256, 1);
+    else if (k <= 4096) QLORA_RMS(256, 2);
+    else if (k <= 8192) QLORA_RMS(256, 4);
+    else if (k <= 16384) QLORA_RMS(512, 4);
     else QLORA_RMS(1024, 4);
 #undef QLORA_RMS
   }
@@ -556,14 +633,15 @@ struct DxOnly {
 #define QLORA_RMS(LPR, V)                                                                                        \
   rms_dx_kernel<kF16, kW32, LPR, V, kVec>                                                                        \
       <<<(unsigned)cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR, 0, st>>>(a)
-    if (a.k > kInRegisters) rms_bwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
-    else if (a.k <= 128) QLORA_RMS(16, 1);
-    else if (a.k <= 512) QLORA_RMS(64, 1);
-    else if (a.k <= 1024) QLORA_RMS(64, 2);
-    else if (a.k <= 2048) QLORA_RMS(256, 1);
-    else if (a.k <= 4096) QLORA_RMS(256, 2);
-    else if (a.k <= 8192) QLORA_RMS(256, 4);
-    else if (a.k <= 16384) QLORA_RMS(512, 4);
+    const int64_t k = held(a.k);
+    if (k > kInRegisters) rms_bwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
+    else if (k <= 128) QLORA_RMS(16, 1);
+    else if (k <= 512) QLORA_RMS(64, 1);
+    else if (k <= 1024) QLORA_RMS(64, 2);
+    else if (k <= 2048) QLORA_RMS(256, 1);
+    else if (k <= 4096) QLORA_RMS(256, 2);
+    else if (k <= 8192) QLORA_RMS(256, 4);
+    else if (k <= 16384) QLORA_RMS(512, 4);
     else QLORA_RMS(1024, 4);
 #undef QLORA_RMS
   }
@@ -571,10 +649,13 @@ struct DxOnly {
 
 // Whether a workgroup holds a row and its sums of dw in registers (rows whose
 // length is no multiple of 8 take more of them).
-bool dw_with_dx(int64_t k) { return k <= (k % 8 == 0 ? 16384 : 8192); }
+bool dw_with_dx(int64_t k) { return held(k) <= (k % 8 == 0 ? 16384 : 8192); }
 
 // Rows that a workgroup of the backward with dw holds at a time.
-int dw_rows(int64_t k) { return k <= 128 ? 64 : k <= 512 ? 16 : k <= 1024 ? 8 : k <= 2048 ? 4 : k <= 4096 ? 2 : 1; }
+int dw_rows(int64_t k) {
+  k = held(k);
+  return k <= 128 ? 64 : k <= 512 ? 16 : k <= 1024 ? 8 : k <= 2048 ? 4 : k <= 4096 ? 2 : 1;
+}
 
 int dw_parts(int64_t M, int64_t k) {
   const int64_t most = dw_with_dx(k) ? kDwGroups : 128, need = dw_with_dx(k) ? cdiv(M, (int64_t)dw_rows(k)) : M;
@@ -584,18 +665,18 @@ int dw_parts(int64_t M, int64_t k) {
 template <bool kF16, bool kW32, bool kVec>
 struct Backward {
   static void launch(const BwdArgs& a, hipStream_t st) {
-    const int64_t parts = dw_parts(a.M, a.k);
+    const int64_t parts = dw_parts(a.M, a.k), k = held(a.k);
 #define QLORA_RMS(LPR, V, T) rms_bwd_kernel<kF16, kW32, LPR, V, T, kVec><<<(unsigned)parts, T, 0, st>>>(a)
     if (!dw_with_dx(a.k)) {
       if (a.dX != nullptr) DxOnly<kF16, kW32, kVec>::launch(a, st);
       const dim3 grid((unsigned)cdiv(a.k, (int64_t)2048), (unsigned)parts);
       rms_dw_part_kernel<kF16, kVec><<<grid, 256, 0, st>>>(a, cdiv(a.M, parts));
-    } else if (a.k <= 128) QLORA_RMS(16, 1, 1024);
-    else if (a.k <= 512) QLORA_RMS(64, 1, 1024);
-    else if (a.k <= 1024) QLORA_RMS(128, 1, 1024);
-    else if (a.k <= 2048) QLORA_RMS(256, 1, 1024);
-    else if (a.k <= 4096) QLORA_RMS(512, 1, 1024);
-    else if (a.k <= 8192) QLORA_RMS(1024, 1, 1024);
+    } else if (k <= 128) QLORA_RMS(16, 1, 1024);
+    else if (k <= 512) QLORA_RMS(64, 1, 1024);
+    else if (k <= 1024) QLORA_RMS(128, 1, 1024);
+    else if (k <= 2048) QLORA_RMS(256, 1, 1024);
+    else if (k <= 4096) QLORA_RMS(512, 1, 1024);
+    else if (k <= 8192) QLORA_RMS(1024, 1, 1024);
     else if constexpr (kVec) QLORA_RMS(512, 4, 512);
 #undef QLORA_RMS
   }
