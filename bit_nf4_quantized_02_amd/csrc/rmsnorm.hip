@@ -38,7 +38,7 @@ __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, i
   }
 }
 
-// A wave's first row and, where it has four, the lane's place among them.
+// A wave's first row and, where it has several, the lane's place among them.
 struct Place {
   int64_t first;  // (the same in all lanes)
   int lead;
@@ -49,10 +49,10 @@ struct Place {
 // The thread's place in a workgroup whose first row is m0.
 template <int kLpr>
 __device__ __forceinline__ Place place_of(int64_t m0) {
-  static_assert(kLpr == 16 || kLpr >= 64, "a wave has one row or four");
+  static_assert(kLpr == 16 || kLpr == 32 || kLpr >= 64, "a wave has four rows, two or one");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if constexpr (kLpr >= 64) return Place{m0 + wave / (kLpr / 64), 0};
-  else return Place{m0 + 4 * wave, (int)(threadIdx.x & 63) / 16};
+  else return Place{m0 + 64 / kLpr * wave, (int)(threadIdx.x & 63) / kLpr};
 }
 
 // A row of [M, k] 16-bit values, read and written in runs of eight by the kLpr
@@ -67,7 +67,7 @@ __device__ __forceinline__ Place place_of(int64_t m0) {
 // are aligned (5001 columns: unaligned runs 72 us for 268 MB, 3.7 TB/s). finish()
 // clears what a run holds of the row before; the last column of an odd end, of
 // whose word half is out of range, is loaded apart (tail()).
-// Four short rows in a wave with such lengths are read and written by address.
+// Several short rows in a wave with such lengths are read and written by address.
 template <int kLpr, bool kVec>
 struct RowOf {
   static constexpr bool kShift = !kVec && kLpr >= 64, kAddress = !kVec && kLpr < 64;
@@ -86,7 +86,7 @@ struct RowOf {
       off = 16 * t;
     } else {
       const int64_t left = M - at.first;
-      rs = make_rsrc(b + at.first * k, left > 0 ? 2 * k * (left < 4 ? left : 4) : 0);
+      rs = make_rsrc(b + at.first * k, left > 0 ? 2 * k * (left < 64 / kLpr ? left : 64 / kLpr) : 0);
       off = 8 * t < k ? 2 * (int)k * at.lead + 16 * t : -1;  // (-1: past every row)
     }
     end = (int)k + shift;
@@ -204,10 +204,8 @@ __device__ __forceinline__ float row_sum(float s, float* red) {
   s += rotated<0x124>(s);
   s += rotated<0x122>(s);
   s += rotated<0x121>(s);
-  if constexpr (kLpr >= 64) {
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-  }
+  if constexpr (kLpr >= 32) s += __shfl_xor(s, 16);
+  if constexpr (kLpr >= 64) s += __shfl_xor(s, 32);
   if constexpr (kLpr > 64) {
     constexpr int kWaves = kLpr / 64;
     const int wave = threadIdx.x >> 6;
@@ -616,6 +614,7 @@ struct Forward {
     const int64_t k = held(a.k);
     if (k > kInRegisters) rms_fwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
     else if (k <= 128) QLORA_RMS(16, 1);
+    else if (k <= 256) QLORA_RMS(32, 1);
     else if (k <= 512) QLORA_RMS(64, 1);
     else if (k <= 1024) QLORA_RMS(64, 2);
     else if (k <= 2048) QLORA_RMS(256, 1);
@@ -636,6 +635,7 @@ struct DxOnly {
     const int64_t k = held(a.k);
     if (k > kInRegisters) rms_bwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
     else if (k <= 128) QLORA_RMS(16, 1);
+    else if (k <= 256) QLORA_RMS(32, 1);
     else if (k <= 512) QLORA_RMS(64, 1);
     else if (k <= 1024) QLORA_RMS(64, 2);
     else if (k <= 2048) QLORA_RMS(256, 1);
@@ -654,7 +654,7 @@ bool dw_with_dx(int64_t k) { return held(k) <= (k % 8 == 0 ? 16384 : 8192); }
 // Rows that a workgroup of the backward with dw holds at a time.
 int dw_rows(int64_t k) {
   k = held(k);
-  return k <= 128 ? 64 : k <= 512 ? 16 : k <= 1024 ? 8 : k <= 2048 ? 4 : k <= 4096 ? 2 : 1;
+  return k <= 128 ? 64 : k <= 256 ? 32 : k <= 512 ? 16 : k <= 1024 ? 8 : k <= 2048 ? 4 : k <= 4096 ? 2 : 1;
 }
 
 int dw_parts(int64_t M, int64_t k) {
@@ -672,6 +672,7 @@ struct Backward {
       const dim3 grid((unsigned)cdiv(a.k, (int64_t)2048), (unsigned)parts);
       rms_dw_part_kernel<kF16, kVec><<<grid, 256, 0, st>>>(a, cdiv(a.M, parts));
     } else if (k <= 128) QLORA_RMS(16, 1, 1024);
+    else if (k <= 256) QLORA_RMS(32, 1, 1024);
     else if (k <= 512) QLORA_RMS(64, 1, 1024);
     else if (k <= 1024) QLORA_RMS(128, 1, 1024);
     else if (k <= 2048) QLORA_RMS(256, 1, 1024);
