@@ -651,10 +651,14 @@ struct DxOnly {
 // length is no multiple of 8 take more of them).
 bool dw_with_dx(int64_t k) { return held(k) <= (k % 8 == 0 ? 16384 : 8192); }
 
-// Rows that a workgroup of the backward with dw holds at a time.
+// Rows that a workgroup of the backward with dw holds at a time. Two of up to
+// 8192 columns, 16 values a lane, rather than one (5120: 54 us against 59, 8192: 55
+// and 56, for 268 MB); not where such a lane has no registers left for unaligned
+// ends (5001: 93 and 73).
 int dw_rows(int64_t k) {
+  const int64_t most2 = k % 8 == 0 ? 8192 : 4096;
   k = held(k);
-  return k <= 128 ? 64 : k <= 256 ? 32 : k <= 512 ? 16 : k <= 1024 ? 8 : k <= 2048 ? 4 : k <= 4096 ? 2 : 1;
+  return k <= 128 ? 64 : k <= 256 ? 32 : k <= 512 ? 16 : k <= 1024 ? 8 : k <= 2048 ? 4 : k <= most2 ? 2 : 1;
 }
 
 int dw_parts(int64_t M, int64_t k) {
@@ -677,8 +681,9 @@ struct Backward {
     else if (k <= 1024) QLORA_RMS(128, 1, 1024);
     else if (k <= 2048) QLORA_RMS(256, 1, 1024);
     else if (k <= 4096) QLORA_RMS(512, 1, 1024);
-    else if (k <= 8192) QLORA_RMS(1024, 1, 1024);
-    else if constexpr (kVec) QLORA_RMS(512, 4, 512);
+    else if constexpr (!kVec) QLORA_RMS(1024, 1, 1024);
+    else if (k <= 8192) QLORA_RMS(512, 2, 1024);
+    else QLORA_RMS(1024, 2, 1024);
 #undef QLORA_RMS
   }
 };
