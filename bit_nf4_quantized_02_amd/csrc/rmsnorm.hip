@@ -417,11 +417,15 @@ __device__ __forceinline__ void load_row(const BwdArgs& a, const Place& at, int 
   x.rstd = a.rstd[at.row() < a.M ? at.row() : a.M - 1];
 }
 
-// A row's dx from its registers; kDw: dy hn added to acc. Every thread of the
-// workgroup calls (row_sum).
-template <bool kF16, bool kW32, int kLpr, int kV, bool kVec, bool kDw>
+// Where a lane's sums of dw are: nowhere, in registers, or in LDS (f32x4 of the
+// lane's half-run h of run v at (2 v + h) kLpr + t).
+enum class Dw { kNone, kRegs, kLds };
+
+// A row's dx from its registers, and dy hn added to the sums of dw. Every thread
+// of the workgroup calls (row_sum).
+template <bool kF16, bool kW32, int kLpr, int kV, bool kVec, Dw kDw>
 __device__ __forceinline__ void do_row(const BwdArgs& a, const Place& at, int t, RowRegs<kV>& x, const Gain<kW32> (&g)[kV],
-                                       float (&acc)[kDw ? kV : 1][8], float* red) {
+                                       float (&acc)[kDw == Dw::kRegs ? kV : 1][8], f32x4* lds, float* red) {
   const bool live = at.row() < a.M;
   const int shift = RowOf<kLpr, kVec>::shift_of(at, a.k);
   float s = 0.0f;
@@ -438,7 +442,13 @@ __device__ __forceinline__ void do_row(const BwdArgs& a, const Place& at, int t,
     for (int i = 0; i < 8; ++i) {
       const float p = dy[i] * (h[i] * x.rstd);
       s = fmaf(p, w[i], s);
-      if (kDw) acc[v][i] += live ? p : 0.0f;
+      if constexpr (kDw == Dw::kRegs) acc[v][i] += live ? p : 0.0f;
+      dy[i] = p;
+    }
+    if constexpr (kDw == Dw::kLds) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        lds[(2 * v + j) * kLpr + t] += f32x4{dy[4 * j], dy[4 * j + 1], dy[4 * j + 2], dy[4 * j + 3]};
     }
   }
   const float dot = row_sum<kLpr>(s, red) * a.inv_k;
@@ -468,7 +478,7 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_dx_kernel(BwdArgs
 #pragma unroll
   for (int v = 0; v < kV; ++v)
     g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v) - RowOf<kLpr, kVec>::shift_of(at, a.k), a.k);
-  do_row<kF16, kW32, kLpr, kV, kVec, false>(a, at, t, x, g, none, red);
+  do_row<kF16, kW32, kLpr, kV, kVec, Dw::kNone>(a, at, t, x, g, none, nullptr, red);
 }
 
 // dX and dw: kThreads threads hold kThreads / kLpr rows at a time and walk
@@ -496,7 +506,7 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   const int64_t step = (int64_t)gridDim.x * kRows;
   const auto load = [&](const Place& at, RowRegs<kV>& x) { load_row<kLpr, kV, kVec>(a, at, t, x); };
   const auto row = [&](const Place& at, RowRegs<kV>& x, int turn) {
-    do_row<kF16, kW32, kLpr, kV, kVec, true>(a, at, t, x, g, acc, red[turn]);
+    do_row<kF16, kW32, kLpr, kV, kVec, Dw::kRegs>(a, at, t, x, g, acc, nullptr, red[turn]);
   };
   RowRegs<kV> x0, x1;
   load(at, x0);
@@ -537,6 +547,38 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   }
 }
 
+// dX and dw for rows that leave no registers for the sums of dw: those are in
+// LDS, 4 bytes a column, each lane's its own (a row of 28672 columns costs a
+// compute unit 0.9 us there and 11 us at its share of HBM). One row at a time.
+template <bool kF16, bool kW32, int kV, bool kVec>
+__global__ __launch_bounds__(1024) void rms_bwd_wide_kernel(BwdArgs a) {
+  __shared__ float red[2][16];
+  __shared__ f32x4 sums[2 * 1024 * kV];
+  const int t = threadIdx.x;
+  const int shift = RowOf<1024, kVec>::shift_of(Place{blockIdx.x, 0}, a.k);  // (of all its rows, a multiple of 8 apart)
+  Gain<kW32> g[kV];
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + 1024 * v) - shift, a.k);
+    sums[2 * v * 1024 + t] = sums[(2 * v + 1) * 1024 + t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  float none[1][8];
+  RowRegs<kV> x;
+  int turn = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+    load_row<1024, kV, kVec>(a, Place{m, 0}, t, x);
+    do_row<kF16, kW32, 1024, kV, kVec, Dw::kLds>(a, Place{m, 0}, t, x, g, none, sums, red[turn]);
+  }
+  float* const out = a.part + (int64_t)blockIdx.x * a.k;
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = 8 * (t + 1024 * v) + i - shift;
+      if (c >= 0 && c < a.k) out[c] = sums[(2 * v + i / 4) * 1024 + t][i & 3];
+    }
+}
+
 // dX for rows of any length, one workgroup a row, which is read twice.
 template <bool kF16, bool kW32, bool kVec>
 __global__ __launch_bounds__(1024) void rms_bwd_long_kernel(BwdArgs a) {
@@ -562,8 +604,8 @@ __global__ __launch_bounds__(1024) void rms_bwd_long_kernel(BwdArgs a) {
   }
 }
 
-// dw's partial sums apart from dX, for rows that leave no registers for them: 8
-// columns per lane, a range of rows per workgroup row.
+// dw's partial sums apart from dX, for rows that do not fit a workgroup: 8 columns
+// per lane, a range of rows per workgroup row.
 template <bool kF16, bool kVec>
 __global__ __launch_bounds__(256) void rms_dw_part_kernel(BwdArgs a, int64_t rows) {
   const int64_t c = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
@@ -647,10 +689,6 @@ struct DxOnly {
   }
 };
 
-// Whether a workgroup holds a row and its sums of dw in registers (rows whose
-// length is no multiple of 8 take more of them).
-bool dw_with_dx(int64_t k) { return held(k) <= (k % 8 == 0 ? 16384 : 8192); }
-
 // Rows that a workgroup of the backward with dw holds at a time. Two of up to
 // 8192 columns, 16 values a lane, rather than one (5120: 54 us against 59, 8192: 55
 // and 56, for 268 MB); not where such a lane has no registers left for unaligned
@@ -662,7 +700,8 @@ int dw_rows(int64_t k) {
 }
 
 int dw_parts(int64_t M, int64_t k) {
-  const int64_t most = dw_with_dx(k) ? kDwGroups : 128, need = dw_with_dx(k) ? cdiv(M, (int64_t)dw_rows(k)) : M;
+  const bool fits = held(k) <= kInRegisters;
+  const int64_t most = fits ? kDwGroups : 128, need = fits ? cdiv(M, (int64_t)dw_rows(k)) : M;
   return (int)(need < most ? need : most);
 }
 
@@ -670,8 +709,9 @@ template <bool kF16, bool kW32, bool kVec>
 struct Backward {
   static void launch(const BwdArgs& a, hipStream_t st) {
     const int64_t parts = dw_parts(a.M, a.k), k = held(a.k);
+#define QLORA_WIDE(V) rms_bwd_wide_kernel<kF16, kW32, V, kVec><<<(unsigned)parts, 1024, 0, st>>>(a)
 #define QLORA_RMS(LPR, V, T) rms_bwd_kernel<kF16, kW32, LPR, V, T, kVec><<<(unsigned)parts, T, 0, st>>>(a)
-    if (!dw_with_dx(a.k)) {
+    if (k > kInRegisters) {
       if (a.dX != nullptr) DxOnly<kF16, kW32, kVec>::launch(a, st);
       const dim3 grid((unsigned)cdiv(a.k, (int64_t)2048), (unsigned)parts);
       rms_dw_part_kernel<kF16, kVec><<<grid, 256, 0, st>>>(a, cdiv(a.M, parts));
@@ -681,10 +721,13 @@ struct Backward {
     else if (k <= 1024) QLORA_RMS(128, 1, 1024);
     else if (k <= 2048) QLORA_RMS(256, 1, 1024);
     else if (k <= 4096) QLORA_RMS(512, 1, 1024);
-    else if constexpr (!kVec) QLORA_RMS(1024, 1, 1024);
-    else if (k <= 8192) QLORA_RMS(512, 2, 1024);
-    else QLORA_RMS(1024, 2, 1024);
+    else if (k <= 8192) {
+      if constexpr (kVec) QLORA_RMS(512, 2, 1024);
+      else QLORA_RMS(1024, 1, 1024);
+    } else if (k <= 16384) QLORA_WIDE(2);
+    else QLORA_WIDE(4);
 #undef QLORA_RMS
+#undef QLORA_WIDE
   }
 };
 

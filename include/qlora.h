@@ -502,8 +502,8 @@ qlora_status qlora_fp8_linear_fwd_rows(const qlora_fp8_weight *w, const qlora_fp
  * NULL. X8 receives y, as rounded to 16 bits, in the 8-bit layer's format (k % 64
  * == 0; its padding columns are written too): the codes that qlora_fp8_linear_fwd
  * makes of y itself. A row that holds a NaN or an infinity, or whose squares add
- * up to more than fp32 holds, is what these formulas give for it in fp32. No
- * other buffers may overlap.
+ * up to more or (with eps = 0) less than fp32 holds, is what these formulas give
+ * for it in fp32; other rows do not change with it. No other buffers may overlap.
  * Any M up to 2^22 and k up to 2^22, M k up to 2^36 (M = 0 launches nothing).
  * Errors: INVALID_ARG (also eps negative or not finite, H without residual or
  * the reverse), SHAPE (sizes, X8 of another shape, k % 64 with X8), HIP.
@@ -519,7 +519,7 @@ qlora_status qlora_rms_norm_fwd(const void *X, const void *residual, const void 
  *   dw = sum over the rows of dY * hn  (fp32, [k])        if dw != NULL
  * dX is the gradient of x and of the residual alike; dres (device, nullable, [M,
  * k]) is the gradient that reaches h past the norm, added before the one
- * rounding; dX may be dres itself. Encoding y to 8 bits is passed through.
+ * rounding; dX may be dres itself, and overlaps nothing else. Encoding y to 8 bits is passed through.
  * accumulate = 0 overwrites dw, 1 adds to it; M = 0 with accumulate = 0 sets it
  * to zero. Sums in a fixed order: reruns are bit-identical.
  * ws (device) holds qlora_rms_norm_bwd_workspace_bytes(M, k) bytes where dw is
@@ -852,7 +852,8 @@ size_t qlora_param_table_bytes(const qlora_param *params, int64_t n);
  * host memory, a buffer that the step writes and another one that overlaps it),
  * SHAPE (a count below 0 or above 2^40, more than 2^22 tensors, or 2^23 chunks of
  * 1024 elements),
- * WORKSPACE (image too small).
+ * WORKSPACE (image too small), UNSUPPORTED (no host memory for the check of
+ * overlaps).
  */
 qlora_status qlora_param_table_build(const qlora_param *params, int64_t n, void *image, size_t image_bytes,
                                      qlora_param_table *table);

@@ -250,9 +250,8 @@ def test_offsets_past_32_bits(q):
     v = o8.table()[codes] * np.repeat(np.ldexp(1.0, scale.astype(int) - 127), 128, axis=1)
     assert np.array_equal(f32(back[tail]), v[:, :k])
     del back
-    dX, dw = q.rms_norm_bwd(Y, X, rstd, w, dX=Y)  # (in place: the gradient that comes in is not needed any more)
-    y = f64(q.rms_norm_fwd(X[tail], w, 1e-5)[0])
-    args = (y, f64(X[tail]), f64(rstd[tail]), f64(w), None)
+    dX, dw = q.rms_norm_bwd(Y, X, rstd, w)
+    args = (f64(Y[tail]), f64(X[tail]), f64(rstd[tail]), f64(w), None)
     dx, _ = onorm.rms_bwd(*args)
     assert np.all(np.abs(f64(dX[tail]) - dx) <= onorm.dx_bound(*args, dx, *HALF[BF]))
 
@@ -337,3 +336,73 @@ def test_another_stream_and_captured(q):
         torch.cuda.synchronize()
         for a, b in zip(outs, step()):
             assert torch.equal(a, b), i
+
+
+def test_two_calls_at_once(q):
+    """Calls that overlap on two streams, with outputs and workspaces of their own."""
+    sets = [draw(2000, k, BF, 14) for k in (1024, 1027)]
+    want = []
+    for X, R, w, dY, dR in sets:
+        Y, H, rstd, _ = q.rms_norm_fwd(X, w, 1e-5, residual=R)
+        want.append([Y, H, rstd, *q.rms_norm_bwd(dY, H, rstd, w, dres=dR)])
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, (X, R, w, dY, dR) in zip(streams, sets):
+            Y, H, rstd, _ = q.rms_norm_fwd(X, w, 1e-5, residual=R, stream=s)
+            got.append([Y, H, rstd, *q.rms_norm_bwd(dY, H, rstd, w, dres=dR, stream=s)])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, v in zip(got, want) for a, b in zip(g, v))
+
+
+def test_two_graphs_with_one_workspace(q):
+    """Replayed after one another on a stream, each leaves its own results."""
+    sets = [draw(300, k, BF, 15) for k in (512, 4096)]
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    graphs, outs, want, s = [], [], [], torch.cuda.Stream()
+    for X, R, w, dY, dR in sets:
+        Y, H, rstd, _ = q.rms_norm_fwd(X, w, 1e-5, residual=R)
+        want.append(q.rms_norm_bwd(dY, H, rstd, w, dres=dR, ws=ws))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(q.rms_norm_bwd(dY, H, rstd, w, dres=dR, ws=ws))
+        graphs.append((g, H, rstd))
+    for _ in range(3):
+        for g, _, _ in graphs:
+            g.replay()
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        for (dX, dw), (a, b) in zip(outs, want):
+            assert torch.equal(dX, a) and torch.equal(dw, b)
+            dw.zero_()
+
+
+def test_refusals_on_the_device(q):
+    X, R, w, dY, dR = draw(8, 128, BF, 16)
+    Y, H, rstd, x8 = q.rms_norm_fwd(X, w, 1e-5, residual=R, want_x8=True)
+    w8 = q.quantize_fp8(torch.ones(64, 128, device="cuda"))
+    A, B = torch.zeros(4, 128, dtype=BF, device="cuda"), torch.zeros(64, 4, dtype=BF, device="cuda")
+    half, other = X[:, ::2], torch.zeros(8, 128, dtype=F16, device="cuda")
+    for call in (lambda: q.rms_norm_fwd(half, w[:64], 1e-5), lambda: q.rms_norm_fwd(X.t(), w[:8], 1e-5),
+                 lambda: q.rms_norm_fwd(X, w[:64], 1e-5), lambda: q.rms_norm_fwd(X, w.to(F16), 1e-5),
+                 lambda: q.rms_norm_fwd(X, w, 1e-5, residual=other), lambda: q.rms_norm_fwd(X, w, 1e-5, H=H),
+                 lambda: q.rms_norm_fwd(X, w, 1e-5, Y=Y[:4]), lambda: q.rms_norm_fwd(X, w, 1e-5, rstd=rstd[:4]),
+                 lambda: q.rms_norm_fwd(X, w, 1e-5, x8=q.FP8Rows(8, 128, x8.codes[:4], x8.scale)),
+                 lambda: q.rms_norm_bwd(dY, H[:4], rstd, w), lambda: q.rms_norm_bwd(dY, H, rstd.double(), w),
+                 lambda: q.rms_norm_bwd(dY, H, rstd, w, dres=other), lambda: q.rms_norm_bwd(dY, H, rstd, w, dw=w),
+                 lambda: q.rms_norm_bwd(dY, H, rstd, w, ws=torch.empty(1 << 20, dtype=torch.uint8)),
+                 lambda: q.fp8_linear_fwd_rows(w8, x8, None, A, B, 1.0), lambda: q.fp8_linear_fwd_rows(w8, x8, other, A, B, 1.0),
+                 lambda: q.fp8_linear_fwd_rows(w8, x8, Y, None, B, 1.0),
+                 lambda: q.fp8_linear_fwd_rows(w8, q.FP8Rows(8, 128, x8.codes.cpu(), x8.scale), None, None, None, 1.0)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: q.rms_norm_fwd(X, w, -1.0), lambda: q.rms_norm_fwd(X, w, float("nan")),
+                 lambda: q.rms_norm_fwd(X[:, :100].contiguous(), w[:100], 1e-5, want_x8=True),
+                 lambda: q.rms_norm_fwd(X.view(-1)[1:1 + 128].view(1, 128), w, 1e-5),                # not aligned
+                 lambda: q.rms_norm_bwd(dY, H, rstd, w, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+                 lambda: q.fp8_linear_fwd_rows(q.quantize_fp8(torch.ones(64, 192, device="cuda")), x8, None, None, None, 1.0)):
+        with pytest.raises(q.QLoraError):
+            call()
+    assert torch.equal(q.rms_norm_fwd(X, w, 1e-5, residual=R)[0], Y)  # and is still usable
