@@ -542,6 +542,8 @@ def _given(t: torch.Tensor | None, dtype, shape, name, device) -> None:
     """_need for an operand that may be left out, on the call's device."""
     if t is None:
         return
+    if t.dtype == dtype and t.shape == shape and t.is_cuda and t.device == device and t.is_contiguous():
+        return  # (what follows says what is wrong)
     _need(t, dtype, shape, name)
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
@@ -842,8 +844,9 @@ def fp8_linear_fwd_rows(w: FP8Weight, x8: FP8Rows, X: torch.Tensor | None, A: to
 
 def _gain(w: torch.Tensor, dt, k: int, dev) -> int:
     """The gain's type: the activations' or fp32."""
-    _given(w, dt if w.dtype != torch.float32 else torch.float32, (k,), "w", dev)
-    return _DT[w.dtype]
+    wt = w.dtype
+    _given(w, dt if wt != torch.float32 else wt, (k,), "w", dev)
+    return _DT[wt]
 
 
 def rms_norm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
@@ -857,17 +860,18 @@ def rms_norm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float, residual: torch.T
     rms_norm_bwd; Y, rstd and x8 are None unless asked for or given."""
     if X.dim() != 2:
         raise ValueError("X must be [M, k]")
-    (M, k), dt, dev = X.shape, X.dtype, X.device
+    shape, dt, dev = X.shape, X.dtype, X.device
+    M, k = shape
     _is_f16(dt)
-    _need(X, dt, (M, k), "X")
-    _given(residual, dt, (M, k), "residual", dev)
+    _given(X, dt, shape, "X", dev)
+    _given(residual, dt, shape, "residual", dev)
     wt = _gain(w, dt, k, dev)
     if residual is None and H is not None:
         raise ValueError("H: given without a residual")
     with _on(stream, dev):
         # (empty_like is half the host's time of empty)
-        Y = torch.empty_like(X) if Y is None and want_y else _out(Y, False, dt, (M, k), "Y", dev)
-        H = torch.empty_like(X) if H is None and residual is not None else _out(H, False, dt, (M, k), "H", dev)
+        Y = torch.empty_like(X) if Y is None and want_y else _out(Y, False, dt, shape, "Y", dev)
+        H = torch.empty_like(X) if H is None and residual is not None else _out(H, False, dt, shape, "H", dev)
         rstd = _out(rstd, save, torch.float32, (M,), "rstd", dev)
         s8 = None
         if x8 is None and want_x8:
@@ -877,7 +881,7 @@ def rms_norm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float, residual: torch.T
             if x8.codes.device != dev:
                 raise ValueError(f"x8: on {x8.codes.device}, expected {dev}")
             s8 = ctypes.byref(x8.struct())
-        _check(_lib.qlora_rms_norm_fwd(_ptr(X), _ptr(residual), _ptr(w), wt, M, k, _DT[dt], float(eps), _ptr(Y), _ptr(H),
+        _check(_lib.qlora_rms_norm_fwd(X.data_ptr(), _ptr(residual), w.data_ptr(), wt, M, k, _DT[dt], float(eps), _ptr(Y), _ptr(H),
                                        _ptr(rstd), s8, _stream(stream)), "qlora_rms_norm_fwd")
     return Y, X if H is None else H, rstd, x8
 
@@ -891,21 +895,22 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, w: torch
     (dX may be `dres`); dw of the gain, fp32.  Returns (dX, dw)."""
     if dY.dim() != 2:
         raise ValueError("dY must be [M, k]")
-    (M, k), dt, dev = dY.shape, dY.dtype, dY.device
+    shape, dt, dev = dY.shape, dY.dtype, dY.device
+    M, k = shape
     _is_f16(dt)
-    _need(dY, dt, (M, k), "dY")
-    _given(H, dt, (M, k), "H", dev)
+    _given(dY, dt, shape, "dY", dev)
+    _given(H, dt, shape, "H", dev)
     _given(rstd, torch.float32, (M,), "rstd", dev)
-    _given(dres, dt, (M, k), "dres", dev)
+    _given(dres, dt, shape, "dres", dev)
     wt = _gain(w, dt, k, dev)
     with _on(stream, dev):
-        dX = torch.empty_like(dY) if dX is None and need_dX else _out(dX, False, dt, (M, k), "dX", dev)
+        dX = torch.empty_like(dY) if dX is None and need_dX else _out(dX, False, dt, shape, "dX", dev)
         dw = _out(dw, need_dw, torch.float32, (k,), "dw", dev, zeros=accumulate)
         need = int(_lib.qlora_rms_norm_bwd_workspace_bytes(M, k)) if ws is None and dw is not None else 0
         ws = _workspace(ws, need, dev)
-        _check(_lib.qlora_rms_norm_bwd(_ptr(dY), _ptr(H), _ptr(rstd), _ptr(w), wt, _ptr(dres), M, k, _DT[dt], _ptr(dX),
-                                       _ptr(dw), int(bool(accumulate)), _ptr(ws), 0 if ws is None else ws.nbytes,
-                                       _stream(stream)), "qlora_rms_norm_bwd")
+        _check(_lib.qlora_rms_norm_bwd(dY.data_ptr(), H.data_ptr(), rstd.data_ptr(), w.data_ptr(), wt, _ptr(dres), M, k,
+                                       _DT[dt], _ptr(dX), _ptr(dw), int(bool(accumulate)), _ptr(ws),
+                                       0 if ws is None else ws.nbytes, _stream(stream)), "qlora_rms_norm_bwd")
     return dX, dw
 
 
@@ -1230,6 +1235,9 @@ class ParamTable:
         return int(self._table.elements)
 
 
+_GRAD_NORM_WS = int(_lib.qlora_grad_norm_workspace_bytes())
+
+
 def grad_norm(table: ParamTable, max_norm: float = float("inf"), grad_scale: float = 1.0,
               out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """[norm, factor] on the device, fp32: the norm of grad_scale times all the
@@ -1238,7 +1246,7 @@ def grad_norm(table: ParamTable, max_norm: float = float("inf"), grad_scale: flo
     dev = table.device
     with _on(stream, dev):
         out = _out(out, True, torch.float32, (2,), "out", dev)
-        ws = _workspace(ws, int(_lib.qlora_grad_norm_workspace_bytes()) if ws is None else 0, dev)
+        ws = _workspace(ws, _GRAD_NORM_WS, dev)
         _check(_lib.qlora_grad_norm(table._ref, float(grad_scale), float(max_norm), _ptr(out), _ptr(ws), ws.nbytes,
                                     _stream(stream)), "qlora_grad_norm")
     return out
