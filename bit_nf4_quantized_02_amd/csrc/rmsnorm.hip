@@ -12,6 +12,11 @@
 // and its use. kLpr lanes hold a row, kV runs of 8 values each; 16 neighbouring
 // lanes hold 128 columns, a scale block of the 8-bit form. Rows of more than 32768
 // columns do not fit a workgroup's registers and are read twice.
+//
+// Measured (bf16, three sets of operands in turn, whole calls): 4096 x 8192, 268 MB,
+// forward with residual 47 us (5.7 TB/s; a copy of 1 GB runs at 5.1), dX 47, with dw
+// 55; 8-bit output instead of y 45 us (5.2 TB/s); 262144 x 128 50, 49 and 54; one row
+// of 8192 columns 3 us.
 #include "fp8.h"
 #include "kernels.h"
 
@@ -25,7 +30,10 @@ constexpr int64_t kInRegisters = 32768;  // columns of a row that a workgroup ho
 // up to 7 columns before they begin.
 int64_t held(int64_t k) { return k % 8 == 0 ? k : k + 7; }
 
-constexpr int kDwGroups = 256;  // workgroups of the backward with dw, at most: one for each compute unit
+// Workgroups of the backward with dw, at most: one of 1024 threads for each
+// compute unit (8 M values in rows of 128 to 1024: 15 - 16 us; 512 of 512 threads 16 -
+// 17, 1024 of 256 18 - 19, with more partial sums to write and read).
+constexpr int kDwGroups = 256;
 
 // Eight 16-bit values into (row, c) of any alignment, nothing from n on.
 __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, int64_t n, const u32x4& v) {
