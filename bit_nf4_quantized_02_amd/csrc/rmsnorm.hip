@@ -258,10 +258,12 @@ __device__ __forceinline__ u32x4 normed8(const u32x4& h, float rstd, const Gain<
 }
 
 // The 8-bit form of y: 16 neighbouring lanes (all of them call) hold a block of
-// 128 columns and find its scale; columns c .. of row m are this lane's.
+// 128 columns and find its scale; columns c .. of row m are this lane's. Those
+// from k on are zero, whatever the row's rstd has made of them.
 template <bool kF16>
-__device__ __forceinline__ void encode8(const u32x4& y, int64_t m, int64_t c, int64_t kp, uint8_t* __restrict__ codes,
+__device__ __forceinline__ void encode8(u32x4 y, int64_t m, int64_t c, int64_t k, int64_t kp, uint8_t* __restrict__ codes,
                                         uint8_t* __restrict__ scale) {
+  if (c >= k) y = u32x4{0u, 0u, 0u, 0u};
   u16x2 top = {0, 0};
 #pragma unroll
   for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, y[e] & 0x7FFF7FFFu));
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
     const int64_t c = 8 * (t + kLpr * v);
     const u32x4 y = normed8<kF16>(h[v], rstd, g[v]);
     if (a.Y != nullptr) Y.store(t, v, y);
-    if (kVec && a.codes != nullptr && c < a.kp) encode8<kF16>(y, m, c, a.kp, a.codes, a.scale);
+    if (kVec && a.codes != nullptr && c < a.kp) encode8<kF16>(y, m, c, a.k, a.kp, a.codes, a.scale);
   }
 }
 
@@ -365,7 +367,7 @@ __global__ __launch_bounds__(1024) void rms_fwd_long_kernel(FwdArgs a) {
   for (int64_t c = 8 * threadIdx.x; c < a.kp; c += 8192) {  // (each thread reads what it wrote)
     const u32x4 y = normed8<kF16>(load8h<kVec>(in, c, a.k), rstd, load_gain<kW32, kVec>(a.w, c, a.k));
     if (a.Y != nullptr) store8h(a.Y + at, c, a.k, y);
-    if (kVec && a.codes != nullptr) encode8<kF16>(y, m, c, a.kp, a.codes, a.scale);
+    if (kVec && a.codes != nullptr) encode8<kF16>(y, m, c, a.k, a.kp, a.codes, a.scale);
   }
 }
 

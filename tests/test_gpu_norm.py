@@ -182,6 +182,16 @@ def test_not_finite_values(q):
         assert torch.isnan(dX[11]).all() and torch.equal(dX[rest], dX0[rest])
 
 
+def test_padding_of_rows_that_are_not_finite(q):
+    """The 8-bit form's columns behind the last are zero also where rstd is NaN or infinite."""
+    for k in (64, 192, 576, 1088, 4160, 32832):
+        X = torch.ones(3, k, dtype=BF, device="cuda")
+        X[1, 5], X[2] = float("nan"), 0
+        x8 = q.rms_norm_fwd(X, torch.ones(k, dtype=BF, device="cuda"), 0.0, want_x8=True)[3]
+        assert (x8.codes[:, k:] == 0).all() and ((x8.codes[1:, :k] & 0x7F) == 0x7F).all(), k
+        assert (x8.codes[0, :k] == x8.codes[0, 0]).all()
+
+
 def test_rows_of_zeros(q):
     X, w = torch.zeros(3, 128, dtype=BF, device="cuda"), torch.ones(128, dtype=BF, device="cuda")
     Y, H, rstd, x8 = q.rms_norm_fwd(X, w, 1e-6, want_x8=True)
