@@ -557,8 +557,8 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   }
 }
 
-// dX and dw for rows that leave no registers for the sums of dw: those are in
-// LDS, 4 bytes a column, each lane's its own (a row of 28672 columns costs a
+// dX and dw for rows that leave no registers for the sums of dw, above 8192
+// columns or 4096 with unaligned ends: those are in LDS, 4 bytes a column, each lane's its own (a row of 28672 columns costs a
 // compute unit 0.9 us there and 11 us at its share of HBM). One row at a time.
 template <bool kF16, bool kW32, int kV, bool kVec>
 __global__ __launch_bounds__(1024) void rms_bwd_wide_kernel(BwdArgs a) {
@@ -657,6 +657,9 @@ __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* __restrict__ 
   dw[c] = accumulate ? dw[c] + s : s;
 }
 
+// Lanes of a row and runs of a lane: a workgroup of 256 threads as far as four
+// runs reach (8192 columns, forward: 47.3 us; 512 lanes of two runs 47.8, 1024 of one
+// 49.1; 5120: 47.2, 48.8 and 51.5), and fewer lanes than a wave's for short rows.
 template <bool kF16, bool kW32, bool kVec>
 struct Forward {
   static void launch(const FwdArgs& a, hipStream_t st) {
@@ -701,8 +704,8 @@ struct DxOnly {
 
 // Rows that a workgroup of the backward with dw holds at a time. Two of up to
 // 8192 columns, 16 values a lane, rather than one (5120: 54 us against 59, 8192: 55
-// and 56, for 268 MB); not where such a lane has no registers left for unaligned
-// ends (5001: 93 and 73).
+// and 56, for 268 MB); not with unaligned ends, which leave such a lane no registers:
+// one, and the sums of dw in LDS (5001: 71 us; in registers 74, two rows 93).
 int dw_rows(int64_t k) {
   const int64_t most2 = k % 8 == 0 ? 8192 : 4096;
   k = held(k);
@@ -733,7 +736,7 @@ struct Backward {
     else if (k <= 4096) QLORA_RMS(512, 1, 1024);
     else if (k <= 8192) {
       if constexpr (kVec) QLORA_RMS(512, 2, 1024);
-      else QLORA_RMS(1024, 1, 1024);
+      else QLORA_WIDE(1);
     } else if (k <= 16384) QLORA_WIDE(2);
     else QLORA_WIDE(4);
 #undef QLORA_RMS

@@ -66,7 +66,7 @@ def check_forward(q, X, R, w, eps, Y, H, rstd):
 
 # widths: of every form of the kernels and next to where one ends, odd ones, one column
 WIDTHS = [1, 7, 8, 64, 100, 120, 121, 122, 128, 129, 130, 132, 136, 248, 249, 250, 255, 256, 264, 505, 506, 511, 512, 520, 1000, 1018, 1024, 1026, 1027,
-          1028, 1032, 2041, 2042, 2048, 2056, 4089, 4090, 4096, 4100, 4104, 5000, 5001, 8185, 8186, 8191, 8192, 8196, 8200,
+          1028, 1032, 2041, 2042, 2048, 2056, 4089, 4090, 4096, 4097, 4100, 4104, 5000, 5001, 8185, 8186, 8191, 8192, 8196, 8200,
           16377, 16384, 16392, 20001, 32761, 32762, 32768]
 
 
@@ -118,7 +118,7 @@ def test_rows_longer_than_a_workgroup_holds(q, dt):
 
 @pytest.mark.parametrize("M,k", [(4097, 128), (1500, 64), (5000, 256), (2500, 1024), (3000, 2048), (700, 4096), (1030, 8192),
                                  (300, 12288), (9000, 100), (9001, 200), (9003, 249), (4500, 129), (4400, 506), (2300, 1022), (1200, 2043),
-                                 (1100, 3001), (600, 5001), (600, 8186), (300, 12001)])
+                                 (1100, 3001), (700, 4099), (600, 5001), (600, 8186), (300, 12001)])
 def test_many_rows(q, M, k):
     """More rows than the workgroups of the backward hold at once, the last ones not a whole group."""
     X, R, w, dY, dR = draw(M, k, BF, 3)
