@@ -858,31 +858,38 @@ def rms_norm_fwd(X: torch.Tensor, w: torch.Tensor, eps: float, residual: torch.T
     layer's activations (too).  Returns (Y, h, rstd, x8): h is X itself without a
     residual (H may be `residual`, which is then updated in place), rstd is for
     rms_norm_bwd; Y, rstd and x8 are None unless asked for or given."""
-    if X.dim() != 2:
-        raise ValueError("X must be [M, k]")
     shape, dt, dev = X.shape, X.dtype, X.device
+    if len(shape) != 2:
+        raise ValueError("X must be [M, k]")
     M, k = shape
     _is_f16(dt)
     _given(X, dt, shape, "X", dev)
-    _given(residual, dt, shape, "residual", dev)
     wt = _gain(w, dt, k, dev)
-    if residual is None and H is not None:
+    if residual is not None:
+        _given(residual, dt, shape, "residual", dev)
+    elif H is not None:
         raise ValueError("H: given without a residual")
     with _on(stream, dev):
-        # (empty_like is half the host's time of empty)
-        Y = torch.empty_like(X) if Y is None and want_y else _out(Y, False, dt, shape, "Y", dev)
-        H = torch.empty_like(X) if H is None and residual is not None else _out(H, False, dt, shape, "H", dev)
+        # (a norm of one token is a kernel of 3 us: empty_like takes half the host's time of empty)
+        if Y is not None:
+            _given(Y, dt, shape, "Y", dev)
+        elif want_y:
+            Y = torch.empty_like(X)
+        if H is not None:
+            _given(H, dt, shape, "H", dev)
+        elif residual is not None:
+            H = torch.empty_like(X)
         rstd = _out(rstd, save, torch.float32, (M,), "rstd", dev)
         s8 = None
-        if x8 is None and want_x8:
-            x8 = FP8Rows.empty(M, k, device=dev)
-            s8 = ctypes.byref(x8._struct())
-        elif x8 is not None:
+        if x8 is not None:
             if x8.codes.device != dev:
                 raise ValueError(f"x8: on {x8.codes.device}, expected {dev}")
             s8 = ctypes.byref(x8.struct())
-        _check(_lib.qlora_rms_norm_fwd(X.data_ptr(), _ptr(residual), w.data_ptr(), wt, M, k, _DT[dt], float(eps), _ptr(Y), _ptr(H),
-                                       _ptr(rstd), s8, _stream(stream)), "qlora_rms_norm_fwd")
+        elif want_x8:
+            x8 = FP8Rows.empty(M, k, device=dev)
+            s8 = ctypes.byref(x8._struct())
+        _check(_lib.qlora_rms_norm_fwd(X.data_ptr(), _ptr(residual), w.data_ptr(), wt, M, k, _DT[dt], float(eps), _ptr(Y),
+                                       _ptr(H), _ptr(rstd), s8, _stream(stream)), "qlora_rms_norm_fwd")
     return Y, X if H is None else H, rstd, x8
 
 
@@ -893,9 +900,9 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, w: torch
     """The gradients of rms_norm_fwd from its h and rstd (qlora_rms_norm_bwd): dX
     of X and the residual alike, with dres, what reaches h past the norm, added
     (dX may be `dres`); dw of the gain, fp32.  Returns (dX, dw)."""
-    if dY.dim() != 2:
-        raise ValueError("dY must be [M, k]")
     shape, dt, dev = dY.shape, dY.dtype, dY.device
+    if len(shape) != 2:
+        raise ValueError("dY must be [M, k]")
     M, k = shape
     _is_f16(dt)
     _given(dY, dt, shape, "dY", dev)
@@ -904,7 +911,10 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, w: torch
     _given(dres, dt, shape, "dres", dev)
     wt = _gain(w, dt, k, dev)
     with _on(stream, dev):
-        dX = torch.empty_like(dY) if dX is None and need_dX else _out(dX, False, dt, shape, "dX", dev)
+        if dX is not None:
+            _given(dX, dt, shape, "dX", dev)
+        elif need_dX:
+            dX = torch.empty_like(dY)
         dw = _out(dw, need_dw, torch.float32, (k,), "dw", dev, zeros=accumulate)
         need = int(_lib.qlora_rms_norm_bwd_workspace_bytes(M, k)) if ws is None and dw is not None else 0
         ws = _workspace(ws, need, dev)
