@@ -25,15 +25,28 @@ bool dims_ok(int64_t M, int64_t n, int64_t k, int r) {
          r >= 0 && r <= QLORA_MAX_RANK;
 }
 
-bool fwd_fits(int64_t M, int64_t n, int64_t k, int r) {
-  return M <= 16 ? 32 * f8_pad(k) < ((int64_t)1 << 31) : gemm_fp8_offsets_fit(M, k, lora_extra_cols(r), n, false);
+// Whether the forward is one pass over the codes (else the GEMM); rows: the
+// activations come encoded (qlora_fp8_rows), and two token tiles share a code.
+// Four would need the pass twice: for weights up to 64 MB, which are in the
+// last-level cache the second time. us, GEMM and pass, r = 64: 11008 x 4096 17 tokens
+// 42 and 27, 64 tokens 44 and 37; 4096 x 4096 36 and 18, 39 and 21; 28672 x 8192 95 and 75,
+// 99 and 113; 8192 x 28672 98 and 62, 104 and 98. The call that encodes takes the GEMM
+// from 17 tokens on.
+bool few_tokens(int64_t M, int64_t n, int64_t k, bool rows) {
+  if (!rows || M <= 16) return M <= 16;
+  return M <= 32 || (M <= kGemvMostTokens && n * f8_pad(k) <= (int64_t)64 << 20);
+}
+
+bool fwd_fits(int64_t M, int64_t n, int64_t k, int r, bool rows) {
+  return few_tokens(M, n, k, rows) ? 32 * f8_pad(k) < ((int64_t)1 << 31)
+                                   : gemm_fp8_offsets_fit(M, k, lora_extra_cols(r), n, false);
 }
 
 struct FwdWs {
   uint8_t* xq = nullptr;   // activation codes and scales
   uint8_t* xs = nullptr;
   float* proj = nullptr;   // partials of T
-  float* T = nullptr;      // M <= 16: T where its partials are too many for the GEMV to add
+  float* T = nullptr;      // few tokens: T where its partials are too many for the GEMV to add
   uint16_t* TS = nullptr;  // low-rank operand columns
   float* rs = nullptr;     // their factor of each row (fp16)
   uint16_t* Bx = nullptr;
@@ -44,7 +57,7 @@ struct FwdWs {
 // Few tokens: the GEMV adds T's partials itself while each of its workgroups
 // reads at most 16 KB of them (1 - 2 us in the shadow of its first loads); a
 // small kernel adds them before it otherwise (a launch, about 4 us).
-bool gemv_adds(int64_t M, int64_t k, int r) { return (int64_t)fp8_prep_plan(M, k, M <= 16).splits * M * r * 4 <= 16384; }
+bool gemv_adds(int64_t M, int64_t k, int r) { return (int64_t)fp8_prep_plan(M, k, true).splits * M * r * 4 <= 16384; }
 
 // Few tokens that come encoded: whether the GEMV reads them by row. For r > 0
 // the kernel before it brings them into operand order on its way (they cost the
@@ -52,12 +65,12 @@ bool gemv_adds(int64_t M, int64_t k, int r) { return (int64_t)fp8_prep_plan(M, k
 // that would be a launch of its own.
 bool gemv_of_rows(int64_t M, int r) { return r == 0 && M <= 8; }
 
-// rows: the activations come encoded (qlora_fp8_rows).
 size_t fwd_ws(int64_t M, int64_t n, int64_t k, int r, bool rows, Carver& cv, FwdWs& o) {
-  o.proj = cv.take<float>((size_t)fp8_prep_plan(M, k, M <= 16).splits * M * r * 4);
-  if (M <= 16) {
-    if (!rows || !gemv_of_rows(M, r)) o.xq = cv.take<uint8_t>(fp8_gemv_codes_bytes(k));
-    if (!rows || !gemv_of_rows(M, r)) o.xs = cv.take<uint8_t>(fp8_gemv_scale_bytes(k));
+  const bool few = few_tokens(M, n, k, rows);
+  o.proj = cv.take<float>((size_t)fp8_prep_plan(M, k, few).splits * M * r * 4);
+  if (few) {
+    if (!rows || !gemv_of_rows(M, r)) o.xq = cv.take<uint8_t>(fp8_gemv_codes_bytes(k, M));
+    if (!rows || !gemv_of_rows(M, r)) o.xs = cv.take<uint8_t>(fp8_gemv_scale_bytes(k, M));
     o.T = cv.take<float>((size_t)M * r * 4);
     return cv.used;
   }
@@ -120,7 +133,7 @@ qlora_status fwd_impl(const qlora_fp8_weight* w, const qlora_fp8_rows* x8, const
   const bool rows = x8 != nullptr;
   const int64_t n = w->n, k = w->k;
   if (!is16(dtype)) return QLORA_ERR_INVALID_ARG;
-  if (!dims_ok(M, n, k, r) || !fwd_fits(M, n, k, r)) return QLORA_ERR_SHAPE;
+  if (!dims_ok(M, n, k, r) || !fwd_fits(M, n, k, r, rows)) return QLORA_ERR_SHAPE;
   if (M == 0) return QLORA_OK;
   if (((!rows || r > 0) && !good(X)) || !good(Y) || (r > 0 && (!good(A) || !good(B))) || (T_save && !aligned16(T_save)))
     return QLORA_ERR_INVALID_ARG;
@@ -134,7 +147,7 @@ qlora_status fwd_impl(const qlora_fp8_weight* w, const qlora_fp8_rows* x8, const
   const bool f16 = dtype == QLORA_DT_FP16;
   const uint16_t *x = static_cast<const uint16_t*>(X), *a = static_cast<const uint16_t*>(A),
                  *b = static_cast<const uint16_t*>(B);
-  const bool few = M <= 16;
+  const bool few = few_tokens(M, n, k, rows);
   const int parts = fp8_prep_plan(M, k, few).splits;
   hipError_t e = hipSuccess;
   if (r > 0 && !few) e = launch_factors(a, 0, k, f8_pad(k), r, o.Ao, b, n, o.Bx, st);

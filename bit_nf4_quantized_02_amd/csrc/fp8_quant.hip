@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restri
 // 32-row operand blocks with one load. A wave holds 32
 // rows; the workgroup's four walk the blocks of one column range and share Q's,
 // which are copied (in operand order) into LDS one block ahead.
-//   kFew = true (M <= 16): codes in the GEMV's operand order [block][lane][32
+//   kFew = true: tiles of 16 rows, codes in the GEMV's operand order [tile][block][lane][32
 // bytes] (lane: row lane % 16, bytes 32 (lane / 16) ..; zeros past M), scales
 // [block][16]; Q [r, C] as it is. The four waves take the range's blocks in
 // turn and their projections are added in wave order.
@@ -152,7 +152,8 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
   __shared__ __attribute__((aligned(16))) char fac1[kTiles > 0 && !kFew ? kTiles * 4096 : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m0 = kFew ? 0 : (int64_t)blockIdx.x * kPrepRows + wave * 16 * kMR;
+  const int64_t m0 = kFew ? 16 * (int64_t)blockIdx.x : (int64_t)blockIdx.x * kPrepRows + wave * 16 * kMR;
+  const int64_t fb = kFew ? (int64_t)blockIdx.x * (Cp / kF8Block) : 0;  // blocks of the token tiles before this one
   const int64_t range = (int64_t)blockIdx.y * gridDim.z + blockIdx.z;  // partials: column range, then factor
   const int nb = (int)(Cp / kF8Block);
   const int b0 = (int)blockIdx.y * bchunk, b1 = b0 + bchunk < nb ? b0 + bchunk : nb;
@@ -275,8 +276,8 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
           }
           if constexpr (kFew) {
             // columns lc .. of row m: lane m + 16 (lc / 32), its bytes lc % 32 ..
-            *reinterpret_cast<u32x2*>(codes + ((int64_t)kb * 64 + 16 * (lc >> 5) + 4 * u + lr) * 32 + (lc & 31)) = o;
-            if ((lane & 15) == 0) scale[kb * 16 + 4 * u + lr] = (uint8_t)b;
+            *reinterpret_cast<u32x2*>(codes + ((fb + kb) * 64 + 16 * (lc >> 5) + 4 * u + lr) * 32 + (lc & 31)) = o;
+            if ((lane & 15) == 0) scale[(fb + kb) * 16 + 4 * u + lr] = (uint8_t)b;
           } else if (m < M) {
             if (gscale == nullptr) *reinterpret_cast<u32x2*>(codes + m * Cp + (int64_t)kb * kF8Block + lc) = o;
             if ((lane & 15) == 0) scale[((kb * mt + m / kF8Block) * 32 + (m & 31)) * 4 + ((m >> 5) & 3)] = (uint8_t)b;
@@ -319,9 +320,10 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
 #pragma unroll
       for (int v = 0; v < 4; ++v) red[wave][4 * (lane >> 4) + v][16 * t + (lane & 15)] = acc[0][t][v];
     __syncthreads();
-    for (int o = threadIdx.x; o < (int)M * r; o += 256) {
+    const int ml = (int)(M - m0 < 16 ? M - m0 : 16);
+    for (int o = threadIdx.x; o < ml * r; o += 256) {
       const int m = o / r, j = o % r;
-      part[(range * M + m) * r + j] = red[0][m][j] + red[1][m][j] + red[2][m][j] + red[3][m][j];
+      part[(range * M + m0 + m) * r + j] = red[0][m][j] + red[1][m][j] + red[2][m][j] + red[3][m][j];
     }
   } else {
 #pragma unroll
@@ -400,10 +402,10 @@ hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16
                            const uint8_t* gcodes, const uint8_t* gscale) {
   const Fp8Prep pl = fp8_prep_plan(M, C, few, W);
   const int64_t Cp = f8_pad(C);
-  if (few && (C % 8 != 0 || M > 16)) return hipErrorInvalidValue;
+  if (few && (C % 8 != 0 || M > kGemvMostTokens)) return hipErrorInvalidValue;
   if (W > 1 && (few || codes != nullptr || gscale != nullptr)) return hipErrorInvalidValue;
   if (gscale != nullptr && (gcodes == nullptr || (codes != nullptr) != few)) return hipErrorInvalidValue;
-  const dim3 grid(few ? 1u : (unsigned)cdiv(M, (int64_t)kPrepRows), (unsigned)pl.splits, (unsigned)W);
+  const dim3 grid((unsigned)cdiv(M, few ? (int64_t)16 : (int64_t)kPrepRows), (unsigned)pl.splits, (unsigned)W);
 #define QLORA_PREP3(RP, H, V, F) \
   fp8_prep_kernel<RP, H, V, F><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, r, pl.chunk, codes, scale, part, gcodes, gscale)
 #define QLORA_PREP2(RP, H)                                                                             \

@@ -290,7 +290,7 @@ hipError_t launch_fp8_encode(const void* W, int dt, int64_t n, int64_t k, uint8_
                              hipStream_t stream);
 hipError_t launch_fp8_decode(const Fp8View& w, uint16_t* out, hipStream_t stream);
 // Activations P [M, C] -> codes and scales ([M, C up to 128] and the GEMM's
-// scale words; few, M <= 16: the GEMV's operand order, fp8_gemv_*_bytes),
+// scale words; few: the GEMV's operand order in tiles of 16 rows, fp8_gemv_*_bytes),
 // and for r > 0 the partials [splits][W][M][r] of P Q^T; W factors in operand
 // order one after the other, for few one as it is, [r, C]. codes NULL (always
 // for W = 2): the projections only. gcodes, gscale: P's codes and scales by row
@@ -314,12 +314,14 @@ hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int
                            const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
                            const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16,
                            bool nn);
-// M <= 16: Y = RN16(X8 W8^T + scale T B^T) from launch_fp8_prep's operands, or
+// At most kGemvMostTokens tokens: Y = RN16(X8 W8^T + scale T B^T) from launch_fp8_prep's operands (few), or,
+// up to 16 tokens,
 // (rows) from codes [M, k up to 128] and scales [M, blocks] of each row; T
 // as `parts` partials [parts][M][r] that the kernel adds in order, written to
 // T_save if it is not NULL.
-size_t fp8_gemv_codes_bytes(int64_t k);
-size_t fp8_gemv_scale_bytes(int64_t k);
+constexpr int64_t kGemvMostTokens = 64;
+size_t fp8_gemv_codes_bytes(int64_t k, int64_t M);
+size_t fp8_gemv_scale_bytes(int64_t k, int64_t M);
 hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* xs, bool rows, int64_t M, const float* T,
                            int parts, const uint16_t* B, int r, float scale, uint16_t* Y, float* T_save,
                            hipStream_t stream, bool f16);

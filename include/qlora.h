@@ -479,9 +479,11 @@ qlora_status qlora_dequant_fp8_rows(const qlora_fp8_rows *x, int dtype, void *ou
  * below, once for all layers that read them:
  *   Y = RN16( X8 W8^T + scale * T B^T ),  T = X A^T
  * X8 (M and k from it; k is the weight's) replaces the encoding of X; X (device)
- * [M, k] in 16 bits is read for the adapter only (NULL for r = 0). Where X8 is
- * the encoding of X, Y and T are qlora_fp8_linear_fwd's, bit for bit. dtype is
- * X's, A's, B's and Y's. The backward is qlora_fp8_linear_bwd's.
+ * [M, k] in 16 bits is read for the adapter only (NULL for r = 0). Up to 32 tokens
+ * (64 where the weight's codes are at most 64 MB) one pass over the codes, above the
+ * GEMM. Where X8 is the encoding of X, Y and T are qlora_fp8_linear_fwd's bit for bit,
+ * except that from 17 tokens on the pass adds in another order than the GEMM there.
+ * dtype is X's, A's, B's and Y's. The backward is qlora_fp8_linear_bwd's.
  * ws (device) holds qlora_fp8_linear_rows_workspace_bytes(M, n, k, r) bytes
  * (NULL where that is 0). Errors: as qlora_fp8_linear_fwd.
  */
