@@ -3,10 +3,12 @@
 //   h = RN16(RN32(x + res)),  rstd = (mean(h^2) + eps)^-1/2,  y = RN16(h rstd w)
 //   g = dy w,  hn = h rstd,  dx = RN16(rstd (g - hn mean(g hn)) + dres),  dw = sum over rows of dy hn
 //
-// Sums and rstd are fp32. The stream h is rounded before it is normalised: the
-// backward, which reads it again, then differentiates what was computed. As 8-bit
-// activations (fp8.h) the 16-bit y is encoded, so that the layer gets the same
-// codes from here as it makes of y itself.
+// Sums are fp32; the forward joins a row's waves and takes the root in fp64, so
+// that rstd is off by little more than its own rounding (4096 columns: 3.1e-8 rms, of
+// which the rounding is 2.8e-8; all in fp32 4.5e-8, in the same time). The stream h is
+// rounded before it is normalised: the backward, which reads it again, then
+// differentiates what was computed. As 8-bit activations (fp8.h) the 16-bit y is
+// encoded, so that the layer gets the same codes from here as it makes of y itself.
 //
 // Bound by HBM: every value is read once and stays in registers between the sum
 // and its use. kLpr lanes hold a row, kV runs of 8 values each; 16 neighbouring
@@ -202,12 +204,19 @@ template <int kCtrl>
 __device__ __forceinline__ float rotated(float x) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), kCtrl, 0xF, 0xF, true));
 }
+template <int kCtrl>
+__device__ __forceinline__ double rotated(double x) {
+  return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(x), kCtrl, 0xF, 0xF, true),
+                          __builtin_amdgcn_mov_dpp(__double2loint(x), kCtrl, 0xF, 0xF, true));
+}
 
-// Sum over the kLpr lanes of a row, in all of them and in one order always.
+// Sum over the kLpr lanes of a row, in all of them and in one order always; the
+// sums of several waves are added as F. In fp64 each of 16 lanes takes one and they
+// are added in pairs (all 16 in every lane: 55.8 us against 54.6 at 22016 columns).
 // red: one float for each wave of the workgroup, used when a row has more than
 // one wave (then every thread of the workgroup calls).
-template <int kLpr>
-__device__ __forceinline__ float row_sum(float s, float* red) {
+template <int kLpr, typename F = float>
+__device__ __forceinline__ F row_sum(float s, float* red) {
   s += rotated<0x128>(s);
   s += rotated<0x124>(s);
   s += rotated<0x122>(s);
@@ -219,11 +228,20 @@ __device__ __forceinline__ float row_sum(float s, float* red) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) red[wave] = s;
     __syncthreads();
-    s = 0.0f;
+    if constexpr (sizeof(F) == sizeof(float)) {
+      s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) s += red[wave / kWaves * kWaves + i];
+      for (int i = 0; i < kWaves; ++i) s += red[wave / kWaves * kWaves + i];
+    } else {
+      F p = (F)red[wave / kWaves * kWaves + (threadIdx.x & (kWaves - 1))];
+      if constexpr (kWaves == 16) p += rotated<0x128>(p);
+      if constexpr (kWaves >= 8) p += rotated<0x124>(p);
+      if constexpr (kWaves >= 4) p += rotated<0x122>(p);
+      p += rotated<0x121>(p);
+      return p;
+    }
   }
-  return s;
+  return (F)s;
 }
 
 // h from X and the residual (16-bit patterns of eight values).
@@ -237,23 +255,36 @@ __device__ __forceinline__ u32x4 add8(const u32x4& x, const u32x4& r) {
   return pack8<kF16>(a);
 }
 
+// Sum of the squares of eight values (each exact in fp32), in pairs.
 template <bool kF16>
-__device__ __forceinline__ float squares8(const u32x4& h, float s) {
+__device__ __forceinline__ float squares8(const u32x4& h) {
   float f[8];
   unpack8<kF16>(h, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
-  return s;
+  for (int i = 0; i < 4; ++i) f[i] = fmaf(f[i], f[i], f[i + 4] * f[i + 4]);
+  return (f[0] + f[2]) + (f[1] + f[3]);
 }
 
-// y of eight values, in 16 bits.
+// x^-1/2 to within a rounding: the instruction's value (1 ulp) and one step of
+// Newton's method in fp64. Outside the range where that holds, 0 and infinity
+// among it, in fp32.
+__device__ __forceinline__ float rstd_of(double x) {
+  if (x > 1e-37 && x < 1e38) {
+    const double d = (double)__builtin_amdgcn_rsqf((float)x);
+    return (float)(d * fma(-0.5 * x * d, d, 1.5));
+  }
+  return 1.0f / sqrtf((float)x);
+}
+
+// y of eight values, in 16 bits. With w of 16 bits h w is exact in fp32, and the
+// product with rstd is the only rounding before y's own.
 template <bool kF16, bool kW32>
 __device__ __forceinline__ u32x4 normed8(const u32x4& h, float rstd, const Gain<kW32>& g) {
   float f[8], w[8];
   unpack8<kF16>(h, f);
   gain8<kF16>(g, w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * w[i];
+  for (int i = 0; i < 8; ++i) f[i] = kW32 ? f[i] * rstd * w[i] : f[i] * w[i] * rstd;
   return pack8<kF16>(f);
 }
 
@@ -290,14 +321,19 @@ struct FwdArgs {
   const uint16_t *X, *R;  // R: the residual, or NULL
   const void* w;
   int64_t M, k, kp;
-  float inv_k, eps;
+  double inv_k;
+  float eps;
   uint16_t *Y, *H;        // Y may be NULL; H is there if R is
   float* rstd;            // may be NULL
   uint8_t *codes, *scale; // may be NULL
 };
 
+// 1024 threads take 64 registers each, not 66, for two workgroups on a compute unit
+// (four values a lane in scratch: 28672 columns to 8 bits 51 us against 54, 22016 53
+// against 55; 256 and 512 threads lose 2 us of 47 by it).
 template <bool kF16, bool kW32, int kLpr, int kV, bool kVec>
-__global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArgs a) {
+__global__ __attribute__((amdgpu_waves_per_eu(kLpr == 1024 && kVec ? 8 : 1))) __launch_bounds__(
+    kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArgs a) {
   constexpr int kThreads = kLpr < 256 ? 256 : kLpr;
   __shared__ float red[kThreads / 64];
   const int t = threadIdx.x & (kLpr - 1);
@@ -332,8 +368,8 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArg
   }
   float s = 0.0f;
 #pragma unroll
-  for (int v = 0; v < kV; ++v) s = squares8<kF16>(h[v], s);
-  const float rstd = 1.0f / sqrtf(fmaf(row_sum<kLpr>(s, red), a.inv_k, a.eps));
+  for (int v = 0; v < kV; ++v) s += squares8<kF16>(h[v]);
+  const float rstd = rstd_of(fma(row_sum<kLpr, double>(s, red), a.inv_k, (double)a.eps));
   if (!live) return;
   if (t == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
   const Row Y(a.Y, at, a.M, a.k, t);
@@ -360,9 +396,9 @@ __global__ __launch_bounds__(1024) void rms_fwd_long_kernel(FwdArgs a) {
       h = add8<kF16>(h, load8h<kVec>(a.R + at, c, a.k));
       store8h(a.H + at, c, a.k, h);
     }
-    s = squares8<kF16>(h, s);
+    s += squares8<kF16>(h);
   }
-  const float rstd = 1.0f / sqrtf(fmaf(row_sum<1024>(s, red), a.inv_k, a.eps));
+  const float rstd = rstd_of(fma(row_sum<1024, double>(s, red), a.inv_k, (double)a.eps));
   if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
   for (int64_t c = 8 * threadIdx.x; c < a.kp; c += 8192) {  // (each thread reads what it wrote)
     const u32x4 y = normed8<kF16>(load8h<kVec>(in, c, a.k), rstd, load_gain<kW32, kVec>(a.w, c, a.k));
@@ -762,7 +798,7 @@ void launch(const Args& a, bool f16, bool w32, hipStream_t st) {
 hipError_t launch_rms_fwd(const uint16_t* X, const uint16_t* R, const void* w, bool w32, int64_t M, int64_t k, float eps,
                           uint16_t* Y, uint16_t* H, float* rstd, uint8_t* codes, uint8_t* scale, hipStream_t st, bool f16) {
   if (codes != nullptr && k % 64 != 0) return hipErrorInvalidValue;
-  const FwdArgs a = {X, R, w, M, k, codes != nullptr ? f8_pad(k) : k, 1.0f / (float)k, eps, Y, H, rstd, codes, scale};
+  const FwdArgs a = {X, R, w, M, k, codes != nullptr ? f8_pad(k) : k, 1.0 / (double)k, eps, Y, H, rstd, codes, scale};
   launch<Forward>(a, f16, w32, st);
   return hipGetLastError();
 }

@@ -495,7 +495,7 @@ qlora_status qlora_fp8_linear_fwd_rows(const qlora_fp8_weight *w, const qlora_fp
 /*
  * The residual's addition with the root-mean-square norm, between the layers:
  *   h = RN16( RN32(x + residual) )     (residual NULL: h = x)
- *   rstd = 1 / sqrt( mean(h^2) + eps ) (fp32, over the k columns of a row)
+ *   rstd = 1 / sqrt( mean(h^2) + eps ) (over the k columns of a row, fp32 sums of 16-bit values)
  *   y = RN16( h * rstd * w )           (fp32 products)
  * X, residual (nullable), Y and H (device) [M, k] in bf16 or fp16 per dtype, w
  * (device) [k] in w_dtype: dtype or QLORA_DT_FP32. H receives h, the stream that

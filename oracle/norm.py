@@ -36,9 +36,10 @@ def rms_bwd(dy, h, rstd, w, dres=None):
 
 
 def rstd_bound(k: int) -> float:
-    """Relative error of rstd: the chain of a row's sum (a thread's values, then the workgroup's), halved by the
-    square root, and the mean, eps, root and quotient."""
-    return (row_depth(k) / 2 + 4) * U
+    """Relative error of rstd: the chain of a row's sum (squares of 16-bit values are exact in fp32: three additions
+    of eight, a thread's eights, 4 + 2 across the wave; the waves' sums, the mean and eps are fp64), halved by the
+    square root, eps as fp32 (half a step of at most the whole) and one rounding."""
+    return ((3 + max(4, -(-k // 8192)) + 6 + 1) / 2 + 1.01) * U
 
 
 def row_depth(k: int) -> int:
