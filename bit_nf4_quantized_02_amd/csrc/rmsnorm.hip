@@ -48,6 +48,39 @@ __device__ __forceinline__ void store8h(uint16_t* __restrict__ row, int64_t c, i
   }
 }
 
+// Elements d .. of eight, zeros after them (d >= 1).
+__device__ __forceinline__ void take_from(u32x4& x, int d) {
+  if (d >= 8) x = u32x4{0u, 0u, 0u, 0u};
+  if (d & 4) x = u32x4{x[2], x[3], 0u, 0u};
+  if (d & 2) x = u32x4{x[1], x[2], x[3], 0u};
+  if (d & 1)
+    x = u32x4{(x[0] >> 16) | (x[1] << 16), (x[1] >> 16) | (x[2] << 16), (x[2] >> 16) | (x[3] << 16), x[3] >> 16};
+}
+
+// Zeros, then the first 8 - d elements of eight (1 <= d <= 7).
+__device__ __forceinline__ void put_from(u32x4& x, int d) {
+  if (d & 4) x = u32x4{0u, 0u, x[0], x[1]};
+  if (d & 2) x = u32x4{0u, x[0], x[1], x[2]};
+  if (d & 1)
+    x = u32x4{x[0] << 16, (x[0] >> 16) | (x[1] << 16), (x[1] >> 16) | (x[2] << 16), (x[2] >> 16) | (x[3] << 16)};
+}
+
+// Elements [lo, hi) of eight to p + lo .., where lo = 0 or hi = 8: a power of two of
+// them at a time. W4, W2: 8 and 4 bytes, as aligned as p is.
+template <typename W4, typename W2>
+__device__ __forceinline__ void store_some(uint16_t* p, const u32x4& x, int lo, int hi) {
+  if (lo == 0) {
+    if (hi & 4) *reinterpret_cast<W4*>(p) = u32x2{x[0], x[1]};
+    if (hi & 2) *reinterpret_cast<W2*>(p + (hi & 4)) = hi & 4 ? x[2] : x[0];
+    if (hi & 1) p[hi - 1] = (uint16_t)(hi & 4 ? (hi & 2 ? x[3] : x[2]) : (hi & 2 ? x[1] : x[0]));
+  } else {
+    const int n = 8 - lo;
+    if (n & 1) p[lo] = (uint16_t)((n & 4 ? (n & 2 ? x[0] : x[1]) : (n & 2 ? x[2] : x[3])) >> 16);
+    if (n & 2) *reinterpret_cast<W2*>(p + (n & 4 ? 2 : 6)) = n & 4 ? x[1] : x[3];
+    if (n & 4) *reinterpret_cast<W4*>(p + 4) = u32x2{x[2], x[3]};
+  }
+}
+
 // A wave's first row and, where it has several, the lane's place among them.
 struct Place {
   int64_t first;  // (the same in all lanes)
@@ -74,10 +107,13 @@ __device__ __forceinline__ Place place_of(int64_t m0) {
 // the wave's rows. A row past the last reads as zeros. Rows whose length is no
 // multiple of 8 (kVec false) start anywhere: their runs are cut at multiples of 16
 // bytes all the same, from `shift` columns before the row, so that loads and stores
-// are aligned (5001 columns: unaligned runs 72 us for 268 MB, 3.7 TB/s). finish()
+// are aligned (5001 columns: unaligned runs 72 us for 268 MB, aligned 55). finish()
 // clears what a run holds of the row before; the last column of an odd end, of
 // whose word half is out of range, is loaded apart (tail()).
-// Several short rows in a wave with such lengths are read and written by address.
+// Several short rows in a wave with such lengths are read and written by address:
+// a run that reaches past its row is read from the row's last eight values, which
+// finish() moves into place (a branch with loads of its own waits for those before
+// it: 71 columns 124 us for 268 MB).
 template <int kLpr, bool kVec>
 struct RowOf {
   static constexpr bool kShift = !kVec && kLpr >= 64, kAddress = !kVec && kLpr < 64;
@@ -105,7 +141,9 @@ struct RowOf {
     return kShift ? (int)((at.first * k) & 7) : 0;
   }
   __device__ __forceinline__ u32x4 load(int t, int v) const {
-    if constexpr (kAddress) return load8h<false>(p, 8 * (t + kLpr * v), end);
+    const int c = 8 * (t + kLpr * v);
+    if constexpr (kAddress)
+      return end < 8 ? load8h<false>(p, c, end) : *reinterpret_cast<const u32x4_any*>(p + (c + 8 <= end ? c : end - 8));
     else return raw_buffer_load_b128(rs, off, 16 * kLpr * v, 0);
   }
   __device__ __forceinline__ uint32_t tail() const {
@@ -124,21 +162,26 @@ struct RowOf {
         if (!(last & 1) && e + 2 * i == last) x[i] = tail;
       }
     }
+    if constexpr (kAddress) {
+      const int past = 8 * (t + kLpr * v) + 8 - (int)k;
+      if (k >= 8 && past > 0) take_from(x, past);
+    }
   }
   __device__ __forceinline__ void store(int t, int v, const u32x4& x) const {
     if constexpr (kAddress) {
-      store8h(p, 8 * (t + kLpr * v), end, x);
+      typedef u32x2 __attribute__((aligned(2))) W4;
+      typedef uint32_t __attribute__((aligned(2))) W2;
+      const int c = 8 * (t + kLpr * v);
+      if (c + 8 <= end) *reinterpret_cast<u32x4_any*>(p + c) = x;
+      else if (c < end) store_some<W4, W2>(p + c, x, 0, end - c);
     } else if constexpr (!kShift) {
       buffer_store16(rs, off + 16 * kLpr * v, x);
     } else {
       const int e = 8 * (t + kLpr * v);
       const bool whole = e >= shift && e + 8 <= end;
       buffer_store16(rs, whole ? off + 16 * kLpr * v : -1, x);
-      if (!whole && e < end) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (e + i >= shift && e + i < end) p[e + i - shift] = (uint16_t)(x[i >> 1] >> (16 * (i & 1)));
-      }
+      if (!whole && e < end)
+        store_some<u32x2, uint32_t>(p + (e - shift), x, e < shift ? shift - e : 0, end - e < 8 ? end - e : 8);
     }
   }
 };
@@ -149,35 +192,61 @@ struct Gain {
   u32x4 a[kW32 ? 2 : 1];
 };
 
-// (Columns outside the row get any gain of it: what they are multiplied with is
-// zero or not stored.)
+// A run that reaches past w's ends is read from its first or last eight gains;
+// settle() moves them into place and clears the others, apart from the loads, so
+// that nothing waits between these (an edge that loads its gains one by one, behind
+// a branch: 4103 columns 66 us for 268 MB).
 template <bool kW32, bool kVec>
 __device__ __forceinline__ Gain<kW32> load_gain(const void* __restrict__ w, int64_t c, int64_t n) {
   Gain<kW32> g;
-  if (kVec ? c < n : c >= 0 && c + 8 <= n) {
-    if constexpr (kW32) {
-      typedef u32x4 __attribute__((aligned(4))) u32x4_4;
-      const uint32_t* const p = static_cast<const uint32_t*>(w) + c;
-      g.a[0] = *reinterpret_cast<const u32x4_4*>(p);
-      g.a[1] = *reinterpret_cast<const u32x4_4*>(p + 4);
-    } else if constexpr (kVec) {
-      g.a[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(w) + c);
-    } else {
-      g.a[0] = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(w) + c);
+#pragma unroll
+  for (int i = 0; i < (kW32 ? 2 : 1); ++i) g.a[i] = u32x4{0u, 0u, 0u, 0u};
+  if (kVec ? c >= n : n < 8) {
+    if constexpr (!kVec) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (c + i < 0 || c + i >= n) continue;
+        if constexpr (kW32) g.a[i >> 2][i & 3] = static_cast<const uint32_t*>(w)[c + i];
+        else g.a[0][i >> 1] |= (uint32_t)static_cast<const uint16_t*>(w)[c + i] << (16 * (i & 1));
+      }
     }
     return g;
   }
-#pragma unroll
-  for (int i = 0; i < (kW32 ? 2 : 1); ++i) g.a[i] = u32x4{0u, 0u, 0u, 0u};
-  if (!kVec && c < n) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t at = c + i < 0 ? 0 : c + i < n ? c + i : n - 1;
-      if constexpr (kW32) g.a[i >> 2][i & 3] = static_cast<const uint32_t*>(w)[at];
-      else g.a[0][i >> 1] |= (uint32_t)static_cast<const uint16_t*>(w)[at] << (16 * (i & 1));
-    }
+  if constexpr (!kVec) c = c < 0 ? 0 : c + 8 <= n ? c : n - 8;
+  if constexpr (kW32) {
+    typedef u32x4 __attribute__((aligned(4))) u32x4_4;
+    const uint32_t* const p = static_cast<const uint32_t*>(w) + c;
+    g.a[0] = *reinterpret_cast<const u32x4_4*>(p);
+    g.a[1] = *reinterpret_cast<const u32x4_4*>(p + 4);
+  } else if constexpr (kVec) {
+    g.a[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(w) + c);
+  } else {
+    g.a[0] = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(w) + c);
   }
   return g;
+}
+
+template <bool kW32, bool kVec>
+__device__ __forceinline__ void settle(Gain<kW32>& g, int64_t c, int64_t n) {
+  if (kVec || n < 8) return;
+  const int past = c + 8 <= n ? 0 : c + 8 - n < 8 ? (int)(c + 8 - n) : 8, before = c < 0 ? (int)-c : 0;
+  if constexpr (!kW32) {
+    if (past > 0) take_from(g.a[0], past);
+    if (before > 0) put_from(g.a[0], before);
+  } else if (past > 0 || before > 0) {
+    uint32_t f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = past < 8 ? g.a[i >> 2][i & 3] : 0u;
+#pragma unroll
+    for (int b = 4; b > 0; b /= 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = past & b ? (i + b < 8 ? f[i + b < 8 ? i + b : 0] : 0u) : f[i];
+#pragma unroll
+      for (int i = 7; i >= 0; --i) f[i] = before & b ? (i >= b ? f[i >= b ? i - b : 0] : 0u) : f[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g.a[i >> 2][i & 3] = f[i];
+  }
 }
 
 template <bool kF16, bool kW32>
@@ -376,6 +445,7 @@ __global__ __attribute__((amdgpu_waves_per_eu(kLpr == 1024 && kVec ? 8 : 1))) __
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     const int64_t c = 8 * (t + kLpr * v);
+    settle<kW32, kVec>(g[v], c - X.shift, a.k);
     const u32x4 y = normed8<kF16>(h[v], rstd, g[v]);
     if (a.Y != nullptr) Y.store(t, v, y);
     if (kVec && a.codes != nullptr && c < a.kp) encode8<kF16>(y, m, c, a.k, a.kp, a.codes, a.scale);
@@ -401,7 +471,9 @@ __global__ __launch_bounds__(1024) void rms_fwd_long_kernel(FwdArgs a) {
   const float rstd = rstd_of(fma(row_sum<1024, double>(s, red), a.inv_k, (double)a.eps));
   if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
   for (int64_t c = 8 * threadIdx.x; c < a.kp; c += 8192) {  // (each thread reads what it wrote)
-    const u32x4 y = normed8<kF16>(load8h<kVec>(in, c, a.k), rstd, load_gain<kW32, kVec>(a.w, c, a.k));
+    Gain<kW32> g = load_gain<kW32, kVec>(a.w, c, a.k);
+    settle<kW32, kVec>(g, c, a.k);
+    const u32x4 y = normed8<kF16>(load8h<kVec>(in, c, a.k), rstd, g);
     if (a.Y != nullptr) store8h(a.Y + at, c, a.k, y);
     if (kVec && a.codes != nullptr) encode8<kF16>(y, m, c, a.k, a.kp, a.codes, a.scale);
   }
@@ -524,6 +596,9 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_dx_kernel(BwdArgs
 #pragma unroll
   for (int v = 0; v < kV; ++v)
     g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v) - RowOf<kLpr, kVec>::shift_of(at, a.k), a.k);
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+    settle<kW32, kVec>(g[v], 8 * (t + kLpr * v) - RowOf<kLpr, kVec>::shift_of(at, a.k), a.k);
   do_row<kF16, kW32, kLpr, kV, kVec, Dw::kNone>(a, at, t, x, g, none, nullptr, red);
 }
 
@@ -546,6 +621,7 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + kLpr * v) - shift, a.k);
+    settle<kW32, kVec>(g[v], 8 * (t + kLpr * v) - shift, a.k);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[v][i] = 0.0f;
   }
@@ -606,6 +682,7 @@ __global__ __launch_bounds__(1024) void rms_bwd_wide_kernel(BwdArgs a) {
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     g[v] = load_gain<kW32, kVec>(a.w, 8 * (t + 1024 * v) - shift, a.k);
+    settle<kW32, kVec>(g[v], 8 * (t + 1024 * v) - shift, a.k);
     sums[2 * v * 1024 + t] = sums[(2 * v + 1) * 1024 + t] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   float none[1][8];
@@ -636,14 +713,18 @@ __global__ __launch_bounds__(1024) void rms_bwd_long_kernel(BwdArgs a) {
     float dy[8], h[8], w[8];
     unpack8<kF16>(load8h<kVec>(a.dY + at, c, a.k), dy);
     unpack8<kF16>(load8h<kVec>(a.H + at, c, a.k), h);
-    gain8<kF16>(load_gain<kW32, kVec>(a.w, c, a.k), w);
+    Gain<kW32> g = load_gain<kW32, kVec>(a.w, c, a.k);
+    settle<kW32, kVec>(g, c, a.k);
+    gain8<kF16>(g, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(dy[i] * (h[i] * rstd), w[i], s);
   }
   const float dot = row_sum<1024>(s, red) * a.inv_k;
   for (int64_t c = 8 * threadIdx.x; c < a.k; c += 8192) {
     float w[8];
-    gain8<kF16>(load_gain<kW32, kVec>(a.w, c, a.k), w);
+    Gain<kW32> g = load_gain<kW32, kVec>(a.w, c, a.k);
+    settle<kW32, kVec>(g, c, a.k);
+    gain8<kF16>(g, w);
     const u32x4 r = a.R != nullptr ? load8h<kVec>(a.R + at, c, a.k) : u32x4{0u, 0u, 0u, 0u};
     store8h(a.dX + at, c, a.k,
                   dx8<kF16>(load8h<kVec>(a.dY + at, c, a.k), load8h<kVec>(a.H + at, c, a.k), r, a.R != nullptr, rstd, dot, w));

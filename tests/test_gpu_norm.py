@@ -98,6 +98,29 @@ def test_forward_and_backward(q, k, dt):
         assert torch.equal(alone, dw + dw)
 
 
+@pytest.mark.parametrize("k", [*range(2, 26), *range(98, 106), *range(250, 266), 515, 1021, 2045, 4093, 4101])
+def test_every_remainder(q, k):
+    """Row ends at every place of a 16-byte run, gains in 16 and 32 bits; an infinite gain reaches its own column only."""
+    for dt, w32 in ((BF, True), (BF, False), (F16, True)):
+        say(f"case: remainder k={k} {dt} w32={w32}")
+        X, R, w, dY, dR = draw(9, k, dt, 5, w32, True)
+        Y, H, rstd, _ = q.rms_norm_fwd(X, w, 1e-5, residual=R)
+        check_forward(q, X, R, w, 1e-5, Y, H, rstd)
+        args = (f64(dY), f64(H), f64(rstd), f64(w), f64(dR))
+        dx, dwx = onorm.rms_bwd(*args)
+        for need_dw in (False, True):
+            dX, dw = q.rms_norm_bwd(dY, H, rstd, w, dres=dR, need_dw=need_dw)
+            assert np.all(np.abs(f64(dX) - dx) <= onorm.dx_bound(*args, dx, *HALF[dt]))
+        assert np.all(np.abs(f64(dw) - dwx) <= onorm.dw_bound(*args[:3]))
+        for c in (0, k - 1):
+            wi = w.clone()
+            wi[c] = float("inf")
+            Yi = q.rms_norm_fwd(X, wi, 1e-5, residual=R)[0]
+            keep = torch.arange(k, device="cuda") != c
+            assert torch.equal(Yi[:, keep], Y[:, keep])
+            assert not torch.isfinite(Yi[:, c]).any()
+
+
 @pytest.mark.parametrize("dt", [BF, F16])
 def test_rows_longer_than_a_workgroup_holds(q, dt):
     for M, k in ((3, 32776), (70, 40001), (2, 100032)):
