@@ -346,14 +346,24 @@ __device__ __forceinline__ float rstd_of(double x) {
 }
 
 // y of eight values, in 16 bits. With w of 16 bits h w is exact in fp32, and the
-// product with rstd is the only rounding before y's own.
+// product with rstd is the only rounding before y's own. In bf16 the power of two in
+// rstd goes to h first (exact as well, down to 2^-126): |h w| alone may be anything
+// from 2^-266 to 2^256 where h rstd w is an ordinary number. A rstd of 0, infinity or
+// NaN stays what it is in the products. (Times as without the power, within 1%.)
 template <bool kF16, bool kW32>
 __device__ __forceinline__ u32x4 normed8(const u32x4& h, float rstd, const Gain<kW32>& g) {
   float f[8], w[8];
   unpack8<kF16>(h, f);
   gain8<kF16>(g, w);
+  const uint32_t b = __float_as_uint(rstd);
+  const float power = __uint_as_float(b & 0x7F800000u);
+  const float rest = isnan(rstd) ? rstd : __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = kW32 ? f[i] * rstd * w[i] : f[i] * w[i] * rstd;
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (kW32) f[i] = f[i] * rstd * w[i];
+    else if constexpr (kF16) f[i] = f[i] * w[i] * rstd;
+    else f[i] = f[i] * power * w[i] * rest;
+  }
   return pack8<kF16>(f);
 }
 

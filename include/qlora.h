@@ -495,8 +495,8 @@ qlora_status qlora_fp8_linear_fwd_rows(const qlora_fp8_weight *w, const qlora_fp
 /*
  * The residual's addition with the root-mean-square norm, between the layers:
  *   h = RN16( RN32(x + residual) )     (residual NULL: h = x)
- *   rstd = 1 / sqrt( mean(h^2) + eps ) (over the k columns of a row, fp32 sums of 16-bit values)
- *   y = RN16( h * rstd * w )           (fp32 products)
+ *   rstd = 1 / sqrt( mean(h^2) + eps ) (over the k columns of a row; fp32 sums, a long row's parts joined in fp64)
+ *   y = RN16( h * rstd * w )           (fp32 products, in an order in which none leaves fp32's range unless h rstd or y does)
  * X, residual (nullable), Y and H (device) [M, k] in bf16 or fp16 per dtype, w
  * (device) [k] in w_dtype: dtype or QLORA_DT_FP32. H receives h, the stream that
  * goes on past the norm (given exactly where residual is; it may be residual
