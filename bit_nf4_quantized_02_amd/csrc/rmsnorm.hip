@@ -32,6 +32,15 @@ constexpr int64_t kInRegisters = 32768;  // columns of a row that a workgroup ho
 // up to 7 columns before they begin.
 int64_t held(int64_t k) { return k % 8 == 0 ? k : k + 7; }
 
+// A workgroup for each of `groups`, over two dimensions where one would have 2^32
+// threads or more (2^22 rows of 16378 to 16383 columns); there may be more workgroups
+// than groups then. group_of(): a workgroup's place.
+dim3 grid_of(int64_t groups, int threads) {
+  const int64_t y = cdiv(groups * threads, (int64_t)1 << 31);
+  return dim3((unsigned)cdiv(groups, y), (unsigned)y);
+}
+__device__ __forceinline__ int64_t group_of() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Workgroups of the backward with dw, at most: one of 1024 threads for each
 // compute unit (8 M values in rows of 128 to 1024: 15 - 16 us; 512 of 512 threads 16 -
 // 17, 1024 of 256 18 - 19, with more partial sums to write and read).
@@ -416,7 +425,7 @@ __global__ __attribute__((amdgpu_waves_per_eu(kLpr == 1024 && kVec ? 8 : 1))) __
   constexpr int kThreads = kLpr < 256 ? 256 : kLpr;
   __shared__ float red[kThreads / 64];
   const int t = threadIdx.x & (kLpr - 1);
-  const Place at = place_of<kLpr>((int64_t)blockIdx.x * (kThreads / kLpr));
+  const Place at = place_of<kLpr>(group_of() * (kThreads / kLpr));
   const int64_t m = at.row();
   const bool live = m < a.M;
   typedef RowOf<kLpr, kVec> Row;
@@ -598,7 +607,7 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_dx_kernel(BwdArgs
   constexpr int kThreads = kLpr < 256 ? 256 : kLpr;
   __shared__ float red[kThreads / 64];
   const int t = threadIdx.x & (kLpr - 1);
-  const Place at = place_of<kLpr>((int64_t)blockIdx.x * (kThreads / kLpr));
+  const Place at = place_of<kLpr>(group_of() * (kThreads / kLpr));
   RowRegs<kV> x;
   Gain<kW32> g[kV];
   float none[1][8];
@@ -792,7 +801,7 @@ struct Forward {
   static void launch(const FwdArgs& a, hipStream_t st) {
 #define QLORA_RMS(LPR, V)                                                                                        \
   rms_fwd_kernel<kF16, kW32, LPR, V, kVec>                                                                       \
-      <<<(unsigned)cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR, 0, st>>>(a)
+      <<<grid_of(cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR), LPR < 256 ? 256 : LPR, 0, st>>>(a)
     const int64_t k = held(a.k);
     if (k > kInRegisters) rms_fwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
     else if (k <= 128) QLORA_RMS(16, 1);
@@ -813,7 +822,7 @@ struct DxOnly {
   static void launch(const BwdArgs& a, hipStream_t st) {
 #define QLORA_RMS(LPR, V)                                                                                        \
   rms_dx_kernel<kF16, kW32, LPR, V, kVec>                                                                        \
-      <<<(unsigned)cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR, 0, st>>>(a)
+      <<<grid_of(cdiv(a.M, (int64_t)(LPR < 256 ? 256 / LPR : 1)), LPR < 256 ? 256 : LPR), LPR < 256 ? 256 : LPR, 0, st>>>(a)
     const int64_t k = held(a.k);
     if (k > kInRegisters) rms_bwd_long_kernel<kF16, kW32, kVec><<<(unsigned)a.M, 1024, 0, st>>>(a);
     else if (k <= 128) QLORA_RMS(16, 1);
