@@ -132,10 +132,12 @@ __global__ __launch_bounds__(256) void fp8_decode_kernel(const uint8_t* __restri
 // turn and their projections are added in wave order.
 // Partials of the projection go to part [range][factor][M][r] (blockIdx.z: one of
 // several factors, each over all of P); codes NULL: only those.
-//   gscale (not NULL): P is encoded already, with scales [M, Cp / 128] in gscale
-// and codes [M, Cp] in gcodes; the scales are rewritten into the GEMM's words, few:
-// codes and scales into the GEMV's order. With kRP = 0 P is not read then.
-template <int kRP, bool kF16, bool kVec, bool kFew>
+//   kGiven: P is encoded already, with scales [M, Cp / 128] in gscale and codes
+// [M, Cp] in gcodes; the scales are rewritten into the GEMM's words, few: codes and
+// scales into the GEMV's order. With kRP = 0 P is not read then. (A kernel of its own:
+// with both ways in one, an encoding lane held up to 28 registers more, and the
+// backward took up to 11% longer: 28671 x 8192, 256 tokens, 108 and 120 us.)
+template <int kRP, bool kF16, bool kVec, bool kFew, bool kGiven>
 __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restrict__ P, int64_t M, int64_t C, int64_t Cp,
                                                        const uint16_t* __restrict__ Q, int r, int bchunk,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scale,
@@ -177,7 +179,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto load = [&](int kb, u32x4 (&x)[kMR][4]) {
-    if (kRP == 0 && gscale != nullptr) return;
+    if constexpr (kRP == 0 && kGiven) return;
     const int64_t c = (int64_t)kb * kF8Block + lc;
     if ((int64_t)(kb + 1) * kF8Block <= C) {  // (uniform: no load behind a test of its own)
 #pragma unroll
@@ -217,9 +219,9 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
       copy_q(kn, next);
       __builtin_amdgcn_sched_barrier(0);  // (copies before loads: the next barrier's wait counts the operations after them)
     }
-    uint32_t gs[kMR][4];
-    u32x2 gc[kFew ? kMR : 1][4];
-    if (gscale != nullptr) {
+    uint32_t gs[kGiven ? kMR : 1][4];
+    u32x2 gc[kGiven && kFew ? kMR : 1][4];
+    if constexpr (kGiven) {
 #pragma unroll
       for (int i = 0; i < kMR; ++i)
 #pragma unroll
@@ -239,22 +241,22 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
         if (kFew && m >= M) x[i][u] = u32x4{0u, 0u, 0u, 0u};
         if constexpr (kTiles > 0)
           *reinterpret_cast<u32x4*>(turn[wave] + (4 * u + lr) * kPitch + 2 * lc) = x[i][u];
-        if (codes != nullptr || gscale != nullptr) {
+        if (kGiven || codes != nullptr) {
           uint32_t b;
           u32x2 o;
-          if (gscale != nullptr) {
+          if constexpr (kGiven) {
             b = gs[i][u];
             if constexpr (kFew) o = m < M ? gc[i][u] : u32x2{0u, 0u};
           } else {
             // the row's largest magnitude, from the 16-bit patterns (two at a
             // time, then the 16 lanes of the row by rotations within them)
             u16x2 top = {0, 0};
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[i][u][e] & 0x7FFF7FFFu));
             uint32_t h = max((uint32_t)top[0], (uint32_t)top[1]);
             h = row16_max(h);
             float f[8];
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
               f[2 * e] = from16<kF16>(x[i][u][e] & 0xFFFFu);
               f[2 * e + 1] = from16<kF16>(x[i][u][e] >> 16);
@@ -262,7 +264,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
             if (__builtin_expect(__ballot(h >= (kF16 ? 0x7C00u : 0x7F80u)) != 0, 0)) {
               // a value of some row is not finite: the maximum without such values
               uint32_t a = 0;
-  #pragma unroll
+#pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const uint32_t v = f8_finite_abs(f[e]) != 0 ? (x[i][u][e >> 1] >> (16 * (e & 1))) & 0x7FFFu : 0u;
                 a = max(a, v);
@@ -279,7 +281,7 @@ __global__ __launch_bounds__(256) void fp8_prep_kernel(const uint16_t* __restric
             *reinterpret_cast<u32x2*>(codes + ((fb + kb) * 64 + 16 * (lc >> 5) + 4 * u + lr) * 32 + (lc & 31)) = o;
             if ((lane & 15) == 0) scale[(fb + kb) * 16 + 4 * u + lr] = (uint8_t)b;
           } else if (m < M) {
-            if (gscale == nullptr) *reinterpret_cast<u32x2*>(codes + m * Cp + (int64_t)kb * kF8Block + lc) = o;
+            if constexpr (!kGiven) *reinterpret_cast<u32x2*>(codes + m * Cp + (int64_t)kb * kF8Block + lc) = o;
             if ((lane & 15) == 0) scale[((kb * mt + m / kF8Block) * 32 + (m & 31)) * 4 + ((m >> 5) & 3)] = (uint8_t)b;
           }
         }
@@ -406,13 +408,16 @@ hipError_t launch_fp8_prep(const uint16_t* P, int64_t M, int64_t C, const uint16
   if (W > 1 && (few || codes != nullptr || gscale != nullptr)) return hipErrorInvalidValue;
   if (gscale != nullptr && (gcodes == nullptr || (codes != nullptr) != few)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)cdiv(M, few ? (int64_t)16 : (int64_t)kPrepRows), (unsigned)pl.splits, (unsigned)W);
-#define QLORA_PREP3(RP, H, V, F) \
-  fp8_prep_kernel<RP, H, V, F><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, r, pl.chunk, codes, scale, part, gcodes, gscale)
+  if (gscale != nullptr && C % 8 != 0) return hipErrorInvalidValue;
+#define QLORA_PREP3(RP, H, V, F, G) \
+  fp8_prep_kernel<RP, H, V, F, G><<<grid, 256, 0, stream>>>(P, M, C, Cp, Q, r, pl.chunk, codes, scale, part, gcodes, gscale)
 #define QLORA_PREP2(RP, H)                                                                             \
   {                                                                                                    \
-    if (few) QLORA_PREP3(RP, H, true, true);                                                           \
-    else if (C % 8 == 0) QLORA_PREP3(RP, H, true, false);                                              \
-    else QLORA_PREP3(RP, H, false, false);                                                             \
+    if (gscale != nullptr && few) QLORA_PREP3(RP, H, true, true, true);                                \
+    else if (gscale != nullptr) QLORA_PREP3(RP, H, true, false, true);                                 \
+    else if (few) QLORA_PREP3(RP, H, true, true, false);                                               \
+    else if (C % 8 == 0) QLORA_PREP3(RP, H, true, false, false);                                       \
+    else QLORA_PREP3(RP, H, false, false, false);                                                      \
   }
 #define QLORA_PREP(RP) { if (f16) QLORA_PREP2(RP, true) else QLORA_PREP2(RP, false) }
   if (r == 0) QLORA_PREP(0)
