@@ -416,11 +416,13 @@ struct FwdArgs {
   uint8_t *codes, *scale; // may be NULL
 };
 
-// 1024 threads take 64 registers each, not 66, for two workgroups on a compute unit
-// (four values a lane in scratch: 28672 columns to 8 bits 51 us against 54, 22016 53
-// against 55; 256 and 512 threads lose 2 us of 47 by it).
+// 1024 threads with a 16-bit gain take at most 64 registers each, for two workgroups
+// on a compute unit: bf16 64 instead of 66 (four values a lane in scratch: 28672
+// columns to 8 bits 50 us against 53, 22016 50 and 54; 256 and 512 threads lose 2 us of
+// 47 by it), fp16 62 either way. Gains of 32 bits, 82 and 75 registers, would put 39 and
+// 26 into scratch (28672 columns to 16 bits: bf16 92 us against 54, fp16 74 against 54).
 template <bool kF16, bool kW32, int kLpr, int kV, bool kVec>
-__global__ __attribute__((amdgpu_waves_per_eu(kLpr == 1024 && kVec ? 8 : 1))) __launch_bounds__(
+__global__ __attribute__((amdgpu_waves_per_eu(kLpr == 1024 && kVec && !kW32 ? 8 : 1))) __launch_bounds__(
     kLpr < 256 ? 256 : kLpr) void rms_fwd_kernel(FwdArgs a) {
   constexpr int kThreads = kLpr < 256 ? 256 : kLpr;
   __shared__ float red[kThreads / 64];
