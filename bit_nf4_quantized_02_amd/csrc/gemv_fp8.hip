@@ -139,10 +139,11 @@ __global__ __launch_bounds__(64 * kGvWaves) void gemv_fp8_kernel(const uint8_t* 
   }
   // B of the tiles' rows, all of it under way before the codes are waited for
   // (loaded rank by rank in the loop that uses it, at rank 64 the epilogue took
-  // longer than the codes: 11008 x 4096 at 16 tokens 22.5 us)
+  // longer than the codes: 11008 x 4096 at 16 tokens 22.5 us). One test for r = 0: the
+  // loop's own, a branch for each load, cost a call without an adapter 0.1 - 0.2 us of 13.
   uint32_t bq[kMaxR / 4];
   const i32x4 br = make_rsrc(B, 2 * N * r);
-  if (wave < kT) {
+  if (r > 0 && wave < kT) {
     const int64_t n = n0 + wave * 16 + (lane & 15);
     const int boff = n < N ? (int)(2 * (n * r + (lane >> 4))) : -1;  // (past every row: zero)
 #pragma unroll
