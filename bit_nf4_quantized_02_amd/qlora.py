@@ -1226,9 +1226,12 @@ class ParamTable:
 
     def __init__(self, params: list[Param], device=None):
         if device is None:
-            device = params[0].grad.device if params else torch.device("cuda", torch.cuda.current_device())
+            device = params[0].grad.device if params else "cuda"
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
         self.params = list(params)
-        self.device = torch.device(device)
+        self.device = device
         arr = (_Param * len(params))(*(p._struct(self.device) for p in params))
         nbytes = int(_lib.qlora_param_table_bytes(arr, len(params)))
         image = torch.empty(nbytes, dtype=torch.uint8)

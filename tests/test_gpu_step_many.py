@@ -200,6 +200,20 @@ def test_table_refusals_on_the_device(q):
     assert q.ParamTable([q.Param(shared, z(), z(), z()), q.Param(shared, z(), z(), z())]).elements == 128
 
 
+def test_device_without_an_index(q):
+    """device="cuda" is the current device, with and without tensors."""
+    ps = params(q, [300, 5])
+    for device in ("cuda", torch.device("cuda"), "cuda:0", torch.device("cuda", 0), None):
+        table = q.ParamTable(ps, device=device)
+        assert table.device == ps[0].grad.device and table.elements == 305
+        check_clip(q.grad_norm(table, 1e-3), [p.grad for p in ps], 1e-3)
+        before = copies(ps)
+        q.adamw_step_many(table, 1, 1e-3)
+        expect(q, ps, before, 1.0, 1, dict(lr=1e-3))
+        empty = q.ParamTable([], device=device)
+        assert empty.device == ps[0].grad.device and q.grad_norm(empty, 1.0).tolist() == [0.0, 1.0]
+
+
 def test_captured_and_on_another_stream(q):
     ps = params(q, [4097, 300, 64], F32, BF)
     table = q.ParamTable(ps)
