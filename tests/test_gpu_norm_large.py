@@ -1,5 +1,6 @@
-"""The norm's largest launches (qlora_rms_norm_fwd, qlora_rms_norm_bwd): as many rows as the calls take, at lengths that
-give each row 1024 threads, 2^32 in all.
+"""The norm's largest launches and buffers (qlora_rms_norm_fwd, qlora_rms_norm_bwd): as many rows as the calls take, at
+lengths that give each row 1024 threads, 2^32 in all; and offsets past 32 bits in rows of aligned and unaligned lengths,
+for dw too.
 
 Bars as in the norm's other tests: the oracle's bounds, which count the roundings.
 """
@@ -78,3 +79,45 @@ def test_gradient_of_most_rows(q, room):
     assert np.all(np.abs(f64(dX[rows]) - dx) <= onorm.dx_bound(*args, dx, *HALF))
     dX[rows] = 0
     assert not any(bool((part != 0).any()) for part in dX.split(M // 64))
+
+
+@pytest.mark.parametrize("M,k", [((1 << 19) + 70, 8256), ((1 << 19) + 200, 8255), (1 << 22, 1027), (1 << 22, 1017),
+                                 ((1 << 17) + 99, 32769)])
+def test_offsets_past_32_bits_in_both_directions(q, room, M, k):
+    """More than 2^32 elements (k = 1017: bytes) in a buffer. dY is zero as far as 32 bits reach, and h behind: there dw
+    is a sum of positive terms only, none of which another row has; before it dX is dres."""
+    first = (1 << (31 if k == 1017 else 32)) // k + 1
+    assert first < M
+    room(6 * 2 * M * k + (8 << 30))
+    say(f"case: norm past 32 bits M={M} k={k}")
+    g = torch.Generator(device="cuda").manual_seed(k)
+    X, R = (torch.randn((M, k), generator=g, device="cuda", dtype=BF) for _ in range(2))
+    w = (torch.rand(k, generator=g, device="cuda") + 0.5).to(BF)
+    Y, H, rstd, _ = q.rms_norm_fwd(X, w, 1e-5, residual=R)
+    for part in (slice(0, 3), slice(first - 2, first + 3), slice(M - 30, M)):
+        assert torch.equal(H[part], (X[part].float() + R[part].float()).to(BF))
+        y, r = onorm.rms_fwd(f64(H[part]), f64(w), 1e-5)
+        assert np.all(np.abs(f64(rstd[part]) - r) <= r * onorm.rstd_bound(k))
+        assert np.all(np.abs(f64(Y[part]) - y) <= onorm.y_bound(y, k, *HALF))
+    del X, Y
+    dY = torch.zeros_like(H)
+    dY[first:] = H[first:]
+    dX, dw = q.rms_norm_bwd(dY, H, rstd, w, dres=R)
+    alone, none = q.rms_norm_bwd(dY, H, rstd, w, dres=R, need_dw=False)
+    assert none is None
+    for part in (slice(first, first + 30), slice(M - 30, M)):
+        args = (f64(dY[part]), f64(H[part]), f64(rstd[part]), f64(w), f64(R[part]))
+        dx, _ = onorm.rms_bwd(*args)
+        for got in (dX, alone):
+            assert np.all(np.abs(f64(got[part]) - dx) <= onorm.dx_bound(*args, dx, *HALF))
+    step = (1 << 28) // k
+    for a in range(0, first, step):
+        part = slice(a, min(a + step, first))
+        assert torch.equal(dX[part], R[part]) and torch.equal(alone[part], R[part])
+    want = torch.zeros(k, dtype=torch.float64, device="cuda")
+    for a in range(first, M, step):
+        part = slice(a, min(a + step, M))
+        want += (H[part].double().square() * rstd[part].double()[:, None]).sum(0)
+    # (as the oracle's bound of dw, whose terms' magnitudes are the terms here)
+    depth = -(-M // 64) + 64 + 32
+    assert bool(((dw.double() - want).abs() <= (depth + 3) * onorm.U * want).all())
