@@ -277,6 +277,12 @@ hipError_t launch_fp8_gemv(const Fp8View& w, const uint8_t* xq, const uint8_t* x
   // 8192 x 28672 55 and 50, 7168 x 4096 13.0 and 12.1, 8192 x 8192 18.3 and 18.9.
   // Fewer rows leave CUs idle with two tiles (4096 x 28672 31 and 40 us), more
   // start a second round of them (8200 x 8192 20 and 22, 11008 x 8192 25 and 27).
+  // (One token that comes encoded, r = 0: 8192 x 8192 13.5 and 17.0, 8192 x 28672 41 and 43.)
+  // 17 to 32 tokens, encoded, r = 64: 4200 x 4096 19.6 and 18.1, 5120 x 13824 41.8 and
+  // 34.9, 8192 x 28672 77 and 61. From 33 on a second group of token tiles gives a CU a
+  // second workgroup either way, and neither is better throughout: 33 tokens, r = 64,
+  // 4200 x 4096 23.4 and 24.7, 7168 x 4096 26.4 and 25.3, 8192 x 4096 26.8 both, 8192 x
+  // 8192 40.2 and 44.3.
   constexpr int64_t kCus = 256;
   if (w.n > 16 * kCus && w.n <= 32 * kCus) {
     if (f16) QLORA_GV8(2, true) else QLORA_GV8(2, false)

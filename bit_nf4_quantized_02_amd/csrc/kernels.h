@@ -314,11 +314,10 @@ hipError_t launch_gemm_fp8(const uint8_t* act, const uint8_t* as, int64_t M, int
                            const uint8_t* f, const uint8_t* fs, int64_t fs_o, int64_t fs_c, int64_t fs_bytes,
                            const uint16_t* fx, int64_t nout, uint16_t* out, float* part, hipStream_t stream, bool f16,
                            bool nn);
-// At most kGemvMostTokens tokens: Y = RN16(X8 W8^T + scale T B^T) from launch_fp8_prep's operands (few), or,
-// up to 16 tokens,
-// (rows) from codes [M, k up to 128] and scales [M, blocks] of each row; T
-// as `parts` partials [parts][M][r] that the kernel adds in order, written to
-// T_save if it is not NULL.
+// At most kGemvMostTokens tokens: Y = RN16(X8 W8^T + scale T B^T) from
+// launch_fp8_prep's operands (few), or, up to 16 tokens, (rows) from codes [M, k up to
+// 128] and scales [M, blocks] of each row; T as `parts` partials [parts][M][r] that the
+// kernel adds in order, written to T_save if it is not NULL.
 constexpr int64_t kGemvMostTokens = 64;
 size_t fp8_gemv_codes_bytes(int64_t k, int64_t M);
 size_t fp8_gemv_scale_bytes(int64_t k, int64_t M);

@@ -15,10 +15,11 @@
 // lanes hold 128 columns, a scale block of the 8-bit form. Rows of more than 32768
 // columns do not fit a workgroup's registers and are read twice.
 //
-// Measured (bf16, three sets of operands in turn, whole calls): 4096 x 8192, 268 MB,
-// forward with residual 47 us (5.7 TB/s; a copy of 1 GB runs at 5.1), dX 47, with dw
-// 55; 8-bit output instead of y 45 us (5.2 TB/s); 262144 x 128 50, 49 and 54; one row
-// of 8192 columns 3 us.
+// Measured (bf16, whole calls, three sets of operands in turn; 16 sets take the same,
+// one, partly in the last-level cache, 40 us): 4096 x 8192, 268 MB, forward with
+// residual 48 us (5.6 TB/s; a copy of 1 GB runs at 5.1), dX 46, with dw 54; 8-bit output
+// instead of y 45 us (5.2 TB/s); 262144 x 128 50, 49 and 54; 838 x 40000 (rows read
+// twice) 66, 69 and 108. One row of 8192 columns: 3 us in the kernel, 11 for a call.
 #include "fp8.h"
 #include "kernels.h"
 
@@ -623,10 +624,10 @@ __global__ __launch_bounds__(kLpr < 256 ? 256 : kLpr) void rms_dx_kernel(BwdArgs
   do_row<kF16, kW32, kLpr, kV, kVec, Dw::kNone>(a, at, t, x, g, none, nullptr, red);
 }
 
-// dX and dw: kThreads threads hold kThreads / kLpr rows at a time and walk
-// over the rows with the grid, the next rows loaded before this one's sum. Each lane adds up dy hn of its columns over the rows it meets; the
-// rows of a workgroup are joined in LDS at the end, the workgroups by
-// rms_dw_kernel.
+// dX and dw: kThreads threads hold kThreads / kLpr rows at a time and walk over the
+// rows with the grid, the next rows loaded before this one's sum. Each lane adds up dy
+// hn of its columns over the rows it meets; the rows of a workgroup are joined in LDS
+// at the end, the workgroups by rms_dw_kernel.
 template <bool kF16, bool kW32, int kLpr, int kV, int kThreads, bool kVec>
 __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   constexpr int kRows = kThreads / kLpr, kCols = 8 * kLpr * kV;
@@ -690,9 +691,12 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_kernel(BwdArgs a) {
   }
 }
 
-// dX and dw for rows that leave no registers for the sums of dw, above 8192
-// columns or 4096 with unaligned ends: those are in LDS, 4 bytes a column, each lane's its own (a row of 28672 columns costs a
-// compute unit 0.9 us there and 11 us at its share of HBM). One row at a time.
+// dX and dw for rows that leave no registers for the sums of dw, above 8192 columns
+// or 4096 with unaligned ends: those are in LDS, 4 bytes a column, each lane's its own
+// (a row of 28672 columns costs a compute unit 0.9 us there and 11 us at its share of
+// HBM). One row at a time, and one workgroup on a compute unit: nothing is in flight
+// while a row is summed (28672 columns, 268 MB: 67 us with 28 MB of partial sums
+// written, and 6 to add them).
 template <bool kF16, bool kW32, int kV, bool kVec>
 __global__ __launch_bounds__(1024) void rms_bwd_wide_kernel(BwdArgs a) {
   __shared__ float red[2][16];

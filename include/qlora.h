@@ -496,7 +496,7 @@ qlora_status qlora_fp8_linear_fwd_rows(const qlora_fp8_weight *w, const qlora_fp
  * The residual's addition with the root-mean-square norm, between the layers:
  *   h = RN16( RN32(x + residual) )     (residual NULL: h = x)
  *   rstd = 1 / sqrt( mean(h^2) + eps ) (over the k columns of a row; fp32 sums, a long row's parts joined in fp64)
- *   y = RN16( h * rstd * w )           (fp32 products, in an order in which none leaves fp32's range unless h rstd or y does)
+ *   y = RN16( h * rstd * w )           (fp32 products, none out of range unless h rstd or y is)
  * X, residual (nullable), Y and H (device) [M, k] in bf16 or fp16 per dtype, w
  * (device) [k] in w_dtype: dtype or QLORA_DT_FP32. H receives h, the stream that
  * goes on past the norm (given exactly where residual is; it may be residual
@@ -521,7 +521,10 @@ qlora_status qlora_rms_norm_fwd(const void *X, const void *residual, const void 
  *   dw = sum over the rows of dY * hn  (fp32, [k])        if dw != NULL
  * dX is the gradient of x and of the residual alike; dres (device, nullable, [M,
  * k]) is the gradient that reaches h past the norm, added before the one
- * rounding; dX may be dres itself, and overlaps nothing else. Encoding y to 8 bits is passed through.
+ * rounding; dX may be dres itself, and overlaps nothing else. Encoding y to 8 bits
+ * is passed through. The mean adds dY * hn, the terms of dw, times w, in fp32; a row
+ * whose rstd is not finite, or one of whose products is more than fp32 holds, has no
+ * finite dX.
  * accumulate = 0 overwrites dw, 1 adds to it; M = 0 with accumulate = 0 sets it
  * to zero. Sums in a fixed order: reruns are bit-identical.
  * ws (device) holds qlora_rms_norm_bwd_workspace_bytes(M, k) bytes where dw is
