@@ -1,4 +1,4 @@
-"""The norm at the ends of fp32's range (qlora_rms_norm_fwd): rows whose squares overflow or vanish, gains far from one.
+"""The norm at the ends of fp32's range (qlora_rms_norm_fwd, qlora_rms_norm_bwd): rows whose squares overflow or vanish, gains far from one.
 
 y is RN16 of two fp32 products of h, rstd and w. Each rounds by 2^-24 of its value or, among the smallest numbers, by
 2^-150; a factor that is taken out of h or rstd as a power of two changes this by less than a factor of two. So with the
@@ -80,3 +80,26 @@ def test_zero_and_infinite_factors(q, k):
         want = ((X.float() * r[:, None]) * w).to(BF)
         assert torch.equal(torch.isnan(Y.cpu()), torch.isnan(want))
         assert torch.equal(Y.cpu().nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
+
+
+@pytest.mark.parametrize("k", [8, 63, 100, 192, 1027, 4096, 8192, 12288, 12001, 28672, 40001])
+@pytest.mark.parametrize("w32", [False, True])
+def test_gradient_of_rows_at_the_ends_of_the_range(q, k, w32):
+    """The forward's rstd of 0 (squares that overflow) passes dres on alone; a rstd that is not finite leaves no finite
+    dX in its row and changes no other row."""
+    g = torch.Generator().manual_seed(k)
+    H, dY, dR = ((torch.randn((40, k), generator=g)).to(BF).cuda() for _ in range(3))
+    w = (torch.rand(k, generator=g) + 0.5).to(F32 if w32 else BF).cuda()
+    plain = H.clone()
+    H[3], H[11], H[12], H[20], H[39] = 3e38, 1e-30, 0, float("inf"), float("nan")
+    rstd = q.rms_norm_fwd(H, w, 0.0)[2]
+    rstd0 = q.rms_norm_fwd(plain, w, 0.0)[2]
+    assert rstd[3] == 0 and torch.isinf(rstd[11]) and torch.isinf(rstd[12]) and rstd[20] == 0 and torch.isnan(rstd[39])
+    rest = torch.ones(40, dtype=torch.bool, device="cuda")
+    rest[[3, 11, 12, 20, 39]] = False
+    for need_dw in (False, True):
+        dX = q.rms_norm_bwd(dY, H, rstd, w, dres=dR, need_dw=need_dw)[0]
+        want = q.rms_norm_bwd(dY, plain, rstd0, w, dres=dR, need_dw=need_dw)[0]
+        assert torch.equal(dX[rest], want[rest])
+        assert torch.equal(dX[3], dR[3])
+        assert not torch.isfinite(dX[[11, 12, 20, 39]]).any()
